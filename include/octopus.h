@@ -325,6 +325,80 @@ int octo_token_logprob(octo_plan_t plan, int32_t row0, int32_t n_rows, const voi
                        float* row_lse, void* dlogits, float grad_scale, float* loss, void* ws, size_t ws_bytes,
                        void* stream);
 
+/* ---- token scoring: log-probabilities, entropy and top alternatives, with gradient ----
+ * The log-probability of octo_token_logprob without its loss, and beside it how sure each
+ * row is and what else it holds likely: for entropy bonuses and monitoring, for a serving
+ * step's log-probabilities, and as the teacher's side of octo_distill_topk.
+ * Rows [row0, row0 + n_rows) of a plan; logits, dtype, ld and vocab as in
+ * octo_token_logprob (columns past vocab are neither read nor written).  Tokens t of row r:
+ * on a pack plan the rows that continue r (pred t = r above); on a decode plan the token
+ * that cursor r takes next, t = r.  ids, logp, g_logp: device arrays over ALL rows of the
+ * plan; row_stat, entropy, g_entropy, top_ids, top_logp start at row row0.
+ * With c = inv_temp (> 0, finite: 1 / temperature), m = max_v x[r][v]:
+ *     S = sum_v exp(c (x[r][v] - m)),   row_stat[r] = (m, ln S),
+ *     logp[t] = c (x[r][ids t] - m) - ln S,   H[r] = ln S - sum_v p_v c (x[r][v] - m).
+ * Alternatives: the k largest logits, the lowest id first among equal ones (+0 and -0 are
+ * equal), with their log-probabilities.  Masked logits are -inf, or the type's lowest
+ * value; a row with every logit at -inf has row_stat (-inf, -inf), logp -inf, entropy 0
+ * and a zero gradient.  A NaN or +inf logit makes its row's ln S, entropy, log-probabilities
+ * and gradient NaN; a NaN is never an alternative, and places that are left over hold id -1
+ * and NaN. */
+
+/* Writes row_stat [n_rows][2]; entropy [n_rows] (optional); logp (with ids, both or
+ * neither) for every t whose row is in the chunk, and 0 for the chunk's path starts;
+ * top_ids int32, top_logp float [n_rows][k] if k > 0.  k <= 128, k <= vocab.  Ids outside
+ * [0, vocab) give NaN logp and OCTO_EINVAL at the next octo_sync.  OCTO_ENOTSUP if ids are
+ * given and a row of the plan has more than 64 successors.  Needs no workspace, allocates
+ * nothing, gives the same bits on every run.  Async on stream. */
+int octo_token_score(octo_plan_t plan, int32_t row0, int32_t n_rows, const void* logits, int32_t dtype,
+                     int64_t ld, int32_t vocab, float inv_temp, const int32_t* ids, float* logp,
+                     float* row_stat, float* entropy, int32_t k, int32_t* top_ids, float* top_logp,
+                     void* stream);
+
+/* Gradient of octo_token_score's logp and entropy: from row_stat (and entropy, with
+ * g_entropy) as it wrote them,
+ *     dlogits[r][v] = c (sum over t of r with ids t = v of g_logp[t] - p_v G_r
+ *                        - g_entropy[r] p_v (ln p_v + H[r])),   G_r = sum over t of r of g_logp[t].
+ * g_logp (with ids) and g_entropy (with entropy) may each be NULL: no such term.  dlogits:
+ * dtype, layout and alignment of logits; may be logits itself.  Ids outside [0, vocab) add
+ * nothing (neither to G) and give OCTO_EINVAL at the next octo_sync.  Async on stream. */
+int octo_token_score_bwd(octo_plan_t plan, int32_t row0, int32_t n_rows, const void* logits, int32_t dtype,
+                         int64_t ld, int32_t vocab, float inv_temp, const float* row_stat,
+                         const float* entropy, const int32_t* ids, const float* g_logp,
+                         const float* g_entropy, void* dlogits, void* stream);
+
+/* ---- distillation from a teacher's top logits ----
+ * Each row's divergence KL(teacher || student) from k teacher entries, with its gradient.
+ * Student q = softmax(c x[r]) over the vocabulary, c = inv_temp; teacher entries
+ * (teach_ids, teach_val) [n_rows][k] from row row0 on, an entry with a negative id or value
+ * -inf being empty.
+ *   tail = 0: values are logits, up to a constant of the row; P_i = exp(c z_i) / sum_j exp(c z_j).
+ *   tail = 1: values are log-probabilities (octo_token_score's top_logp); P_i = exp(z_i), and
+ *             P_R = max(0, 1 - sum_i P_i) is one more class, the ids not listed.
+ *     KL = sum_i P_i (ln P_i - ln q_i) + P_R (ln P_R - ln q_R),  q_R = sum of q outside the list,
+ *     dlogits[r][v] = grad_scale w_r c (q_v P - sum over i with id_i = v of P_i
+ *                     - [v not listed] P_R q_v / q_R),  P = sum_i P_i + P_R.
+ * An id may be listed more than once: its entries add up.  The rest term is dropped where no
+ * unlisted id has mass in the student.  A row whose weight is 0 (its logits are not read),
+ * whose student logits are all -inf, or, at tail = 0, whose entries are all empty, has
+ * divergence 0 and a zero gradient. */
+
+/* Workspace (bytes) for octo_distill_topk's loss over n_rows rows. */
+int octo_distill_topk_workspace_size(int32_t n_rows, size_t* bytes);
+
+/* Rows [row0, row0 + n_rows) of a pack or decode plan; logits, dtype, ld, vocab as in
+ * octo_token_logprob.  1 <= k <= 128 (k may exceed vocab).  weight (NULL: ones) and row_kl:
+ * device floats over ALL rows of the plan; row_kl[r] is written without the weight.
+ * dlogits (optional): dtype, layout and alignment of logits; may be logits itself.  loss
+ * (optional, one device float, needs ws): sum of w_r KL_r over the chunk, in a fixed order.
+ * Teacher ids >= vocab count as empty and give OCTO_EINVAL at the next octo_sync.  Async on
+ * stream. */
+int octo_distill_topk(octo_plan_t plan, int32_t row0, int32_t n_rows, const void* logits, int32_t dtype,
+                      int64_t ld, int32_t vocab, float inv_temp, int32_t k, const int32_t* teach_ids,
+                      const float* teach_val, int32_t tail, const float* weight, float* row_kl,
+                      void* dlogits, float grad_scale, float* loss, void* ws, size_t ws_bytes,
+                      void* stream);
+
 /* ---- tree-packed recurrent layer (gated delta rule), device, async on stream ----
  * ia.com.br summary, associative versus working memory: the hybrid model pairs attention
  * with linear-recurrent layers (Gated DeltaNet / Mamba-2) whose state is the branch's

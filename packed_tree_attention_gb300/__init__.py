@@ -76,7 +76,8 @@ SYMBOLS = ("octo_pool_create", "octo_pool_destroy", "octo_root", "octo_append", 
            "octo_launch_count", "octo_decode_noalloc", "octo_append_rope", "octo_rope_rows",
            "octo_rope_pool_grad", "octo_token_logprob_workspace_size", "octo_token_logprob",
            "octo_decode_plan_advance", "octo_pool_query", "octo_decode_cursors", "octo_recurrent_workspace_size",
-           "octo_recurrent_fwd", "octo_recurrent_bwd", "octo_wait_selftest", "octo_append_step")
+           "octo_recurrent_fwd", "octo_recurrent_bwd", "octo_wait_selftest", "octo_append_step", "octo_token_score",
+           "octo_token_score_bwd", "octo_distill_topk_workspace_size", "octo_distill_topk")
 
 
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
@@ -126,6 +127,10 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "octo_rope_pool_grad": [P, P, F, P],
         "octo_token_logprob_workspace_size": [I32, ctypes.POINTER(SZ)],
         "octo_token_logprob": [P, I32, I32, P, I32, ctypes.c_int64, I32, P, P, P, P, P, F, P, P, SZ, P],
+        "octo_token_score": [P, I32, I32, P, I32, ctypes.c_int64, I32, F, P, P, P, P, I32, P, P, P],
+        "octo_token_score_bwd": [P, I32, I32, P, I32, ctypes.c_int64, I32, F, P, P, P, P, P, P, P],
+        "octo_distill_topk_workspace_size": [I32, ctypes.POINTER(SZ)],
+        "octo_distill_topk": [P, I32, I32, P, I32, ctypes.c_int64, I32, F, I32, P, P, I32, P, P, P, F, P, P, SZ, P],
         "octo_decode_plan_advance": [P, P],
         "octo_pool_query": [P, ctypes.POINTER(_PoolState)],
         "octo_decode_cursors": [P, IP, I32, I32, P, P, P, P, P, F, P, SZ, P],
@@ -165,6 +170,35 @@ def _ptr(x):
     if not x.is_contiguous():
         raise ValueError("tensor arguments must be contiguous (got strides %s for shape %s)"
                          % (tuple(x.stride()), tuple(x.shape)))
+    return x.data_ptr()
+
+
+def _logits(x, n_rows, vocab, what="logits"):
+    """(address, dtype, elements between rows) of a [rows][ld] bf16 or fp32 tensor holding
+    n_rows rows of at least `vocab` entries; a column slice of a wider one is a row pitch."""
+    name = str(x.dtype)
+    if name not in ("torch.bfloat16", "torch.float32"):
+        raise ValueError("%s must be bfloat16 or float32 (got %s)" % (what, name))
+    if x.dim() != 2 or x.shape[0] < n_rows or x.shape[1] < vocab or x.stride(1) != 1:
+        raise ValueError("%s must be [rows][entries] with adjacent entries, %d rows of at least %d (got shape %s, "
+                         "strides %s)" % (what, n_rows, vocab, tuple(x.shape), tuple(x.stride())))
+    if not x.is_cuda:
+        raise ValueError("%s must be on the GPU" % what)
+    ld = x.stride(0)
+    if x.shape[0] <= 1:        # one row: any pitch will do, and the library wants 16-byte ones
+        ld = -(-max(vocab, 1) // 8) * 8
+    return x.data_ptr(), DTYPE_F32 if name == "torch.float32" else DTYPE_BF16, ld
+
+
+def _vector(x, name, count, what):
+    """Address of a contiguous tensor of at least `count` elements of torch dtype `name`."""
+    if x is None:
+        return None
+    if str(x.dtype) != "torch." + name or x.numel() < count or not x.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of at least %d elements (got %s, shape %s)"
+                         % (what, name, count, x.dtype, tuple(x.shape)))
+    if not x.is_cuda:
+        raise ValueError("%s must be on the GPU" % what)
     return x.data_ptr()
 
 
@@ -441,6 +475,64 @@ class Plan:
                                         _ptr(ids), _ptr(weight), _ptr(logp), _ptr(row_lse), _ptr(dlogits),
                                         float(grad_scale), _ptr(loss), _ptr(ws), ws.numel() * ws.element_size(),
                                         _stream(stream)), "octo_token_logprob")
+
+    def token_score(self, row0, n_rows, logits, vocab, row_stat, entropy=None, ids=None, logp=None, top_ids=None,
+                    top_logp=None, inv_temp=1.0, stream=None):
+        """octo_token_score: log-probabilities of the plan's tokens, each row's entropy and its
+        top_ids.shape[1] most likely alternatives, of the rows [row0, row0 + n_rows) whose
+        logits are `logits` [n_rows][ld] (bf16 or fp32)."""
+        x, dt, ld = _logits(logits, n_rows, vocab)
+        N, k = self.info["n_rows"], 0
+        if top_ids is not None or top_logp is not None:
+            if top_ids is None or top_logp is None or top_ids.dim() != 2 or top_ids.shape != top_logp.shape:
+                raise ValueError("top_ids and top_logp go together, both [n_rows][k]")
+            k = top_ids.shape[1]
+        _chk(self._L.octo_token_score(
+            self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, _vector(ids, "int32", N, "ids"),
+            _vector(logp, "float32", N, "logp"), _vector(row_stat, "float32", 2 * n_rows, "row_stat"),
+            _vector(entropy, "float32", n_rows, "entropy"), k, _vector(top_ids, "int32", n_rows * k, "top_ids"),
+            _vector(top_logp, "float32", n_rows * k, "top_logp"), _stream(stream)), "octo_token_score")
+
+    def token_score_bwd(self, row0, n_rows, logits, vocab, row_stat, entropy, ids, g_logp, g_entropy, dlogits,
+                        inv_temp=1.0, stream=None):
+        """octo_token_score_bwd: gradient with respect to the logits from those of logp and
+        entropy (either may be None), row_stat and entropy as token_score wrote them."""
+        x, dt, ld = _logits(logits, n_rows, vocab)
+        g = _logits(dlogits, n_rows, vocab, "dlogits")
+        if g[1:] != (dt, ld):
+            raise ValueError("dlogits must have the dtype and row pitch of logits")
+        N = self.info["n_rows"]
+        _chk(self._L.octo_token_score_bwd(
+            self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, _vector(row_stat, "float32", 2 * n_rows, "row_stat"),
+            _vector(entropy, "float32", n_rows, "entropy"), _vector(ids, "int32", N, "ids"),
+            _vector(g_logp, "float32", N, "g_logp"), _vector(g_entropy, "float32", n_rows, "g_entropy"), g[0],
+            _stream(stream)), "octo_token_score_bwd")
+
+    def distill_topk_workspace_size(self, n_rows):
+        n = ctypes.c_size_t(0)
+        _chk(self._L.octo_distill_topk_workspace_size(n_rows, ctypes.byref(n)), "octo_distill_topk_workspace_size")
+        return n.value
+
+    def distill_topk(self, row0, n_rows, logits, vocab, teach_ids, teach_val, row_kl, ws=None, weight=None, tail=False,
+                     inv_temp=1.0, dlogits=None, grad_scale=1.0, loss=None, stream=None):
+        """octo_distill_topk: KL(teacher || student) of the rows [row0, row0 + n_rows) against
+        teacher entries teach_ids, teach_val [n_rows][k] (tail: log-probabilities, the rest of
+        the mass one more class), with its gradient and weighted sum."""
+        x, dt, ld = _logits(logits, n_rows, vocab)
+        g = None
+        if dlogits is not None:
+            g, gdt, gld = _logits(dlogits, n_rows, vocab, "dlogits")
+            if (gdt, gld) != (dt, ld):
+                raise ValueError("dlogits must have the dtype and row pitch of logits")
+        if teach_ids.dim() != 2 or teach_ids.shape != teach_val.shape:
+            raise ValueError("teach_ids and teach_val must both be [n_rows][k]")
+        N, k = self.info["n_rows"], teach_ids.shape[1]
+        _chk(self._L.octo_distill_topk(
+            self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, k, _vector(teach_ids, "int32", n_rows * k, "teach_ids"),
+            _vector(teach_val, "float32", n_rows * k, "teach_val"), 1 if tail else 0,
+            _vector(weight, "float32", N, "weight"), _vector(row_kl, "float32", N, "row_kl"), g, grad_scale,
+            _vector(loss, "float32", 1, "loss"), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0,
+            _stream(stream)), "octo_distill_topk")
 
     def recurrent_workspace_size(self, n_heads, head_dim):
         return int(self._L.octo_recurrent_workspace_size(self.h, n_heads, head_dim))

@@ -177,6 +177,9 @@ int rope_validate(int32_t head_dim, float base);
 int launch_append_rope(const octo_pool_desc& d, const int32_t* d_dst_rows, const int32_t* d_pos, int32_t n,
                        const void* k, const void* v, float base, cudaStream_t s);
 
+// sum of n row losses in a fixed order (token_loss.cu)
+int launch_loss_sum(const float* part, int32_t n, float* loss, cudaStream_t s);
+
 // plan compilation (compile.cu)
 int compile_plan(octo_pool_s* pool, const int32_t* tile_segs_host, const int32_t* seg_order, int32_t n_segs,
                  bool is_decode, int32_t bm, cudaStream_t s, octo_plan_s** out);

@@ -313,6 +313,13 @@ __global__ void __launch_bounds__(1024) k_loss_sum(const float* __restrict__ par
 }
 
 }  // namespace
+
+int launch_loss_sum(const float* part, int32_t n, float* loss, cudaStream_t s) {
+  k_loss_sum<<<1, 1024, 0, s>>>(part, n, loss);
+  count_launch();
+  return cuda_status(cudaGetLastError());
+}
+
 }  // namespace octo
 
 extern "C" {
@@ -375,11 +382,8 @@ int octo_token_logprob(octo_plan_t plan, int32_t row0, int32_t n_rows, const voi
   else
     k_token_logprob<float><<<n_rows, kThreads, smem, s>>>(p);
   count_launch();
-  if (loss) {
-    k_loss_sum<<<1, 1024, 0, s>>>((const float*)ws, n_rows, loss);
-    count_launch();
-  }
-  return cuda_status(cudaGetLastError());
+  if (int st = cuda_status(cudaGetLastError())) return st;
+  return loss ? launch_loss_sum((const float*)ws, n_rows, loss, s) : OCTO_OK;
 }
 
 }  // extern "C"
