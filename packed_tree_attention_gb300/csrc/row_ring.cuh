@@ -1,0 +1,261 @@
+// Rows of logits streamed through a ring of shared-memory slots: the frame of the token
+// scoring and distillation kernels.
+//
+// A cluster of `cs` CTAs takes one row after another; each CTA has its own contiguous part of
+// the row's 16-byte vectors.  One thread copies the part, stage by stage, into the ring with
+// bulk copies (cp.async.bulk, completion on a slot's `full` barrier), running ahead over row
+// ends as far as the ring reaches; 16 consumer warps take a stage at a time, four vectors a
+// thread; 4 finisher warps do what a row needs besides, while the consumers are at the next.
+// The copies bring whole vectors: the last V % E entries are the finishers'.
+#pragma once
+
+#include "row_common.cuh"
+#include "tc_common.cuh"
+
+namespace octo {
+namespace rows {
+
+constexpr int kConsWarps = 16, kFinWarps = 4;
+constexpr int kCons = kConsWarps * 32, kFin = kFinWarps * 32;
+constexpr int kBlock = kCons + kFin + 32;   // + the copying warp
+constexpr int kPer = 4;                     // vectors of one thread in a stage
+constexpr int kMaxSlots = 24;
+constexpr int kMaxCluster = 8;
+constexpr int kFinBar = 1;                  // named barrier of the finishers
+static_assert(kFin >= kMaxTop, "a finisher thread for each teacher entry");
+
+struct RingShape {
+  int32_t cs;          // CTAs per row
+  int32_t seg;         // vectors of a CTA's part (the last ones may have fewer)
+  int32_t stage;       // vectors of a slot
+  int32_t n_stages;    // stages of a part
+  int32_t n_slots;
+};
+
+// cs CTAs per row, ring of at most `bytes`.
+inline RingShape ring_shape(int64_t nv, int cs, int bytes) {
+  RingShape s;
+  s.cs = cs;
+  s.seg = (int32_t)((nv + cs - 1) / cs);
+  s.n_stages = (s.seg + kCons * kPer - 1) / (kCons * kPer);
+  s.stage = s.n_stages ? ((s.seg + s.n_stages - 1) / s.n_stages + 31) / 32 * 32 : 32;
+  s.n_slots = bytes / (s.stage * 16);
+  if (s.n_slots > kMaxSlots) s.n_slots = kMaxSlots;
+  return s;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   tc::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void fin_sync() { asm volatile("bar.sync %0, %1;" ::"n"(kFinBar), "n"(kFin) : "memory"); }
+
+// The waits below are uniform over the warp, and fin_all over the finishers: after a wait that
+// gave up, all of them leave together and none is left at a barrier.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status, OCTO_ETIMEOUT));
+}
+__device__ __forceinline__ bool fin_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok), "n"(kFinBar), "n"(kFin)
+      : "memory");
+  return all != 0;
+}
+
+// ---- clusters ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void st_remote(uint32_t a, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_remote(uint32_t a, unsigned long long v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// mbar_wait with cluster scope (what the peers stored before arriving is visible after it)
+__device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  for (uint32_t i = 0; i < tc::kSpinLimit; i++) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  atomicExch(status, OCTO_ETIMEOUT);
+  return false;
+}
+
+// ---- two fp32 operations per instruction ----
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  static constexpr int kPairs = 4;
+  __device__ __forceinline__ static uint4 masked() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+  __device__ __forceinline__ static f2 pair(const uint4& w, int i) {
+    const uint32_t u = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+    return pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  // largest entry, NaNs left out
+  __device__ __forceinline__ static float max(const uint4& w) {
+    auto b = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(b(w.x), b(w.y)), __hmax2(b(w.z), b(w.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
+template <>
+struct Raw<float> {
+  static constexpr int kPairs = 2;
+  __device__ __forceinline__ static uint4 masked() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
+  __device__ __forceinline__ static f2 pair(const uint4& w, int i) {
+    return i == 0 ? pack2(__uint_as_float(w.x), __uint_as_float(w.y)) : pack2(__uint_as_float(w.z), __uint_as_float(w.w));
+  }
+  __device__ __forceinline__ static float max(const uint4& w) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+};
+
+// A thread's running statistics over stages.  The reference m moves once per stage at most,
+// to the largest of the thread's vectors; sums in pairs, two chains.
+template <typename T, bool kEntropy>
+struct StageStat {
+  float m;
+  f2 s[2], a[2];
+  __device__ __forceinline__ void init() { m = -FLT_MAX, s[0] = s[1] = a[0] = a[1] = 0ull; }
+  __device__ __forceinline__ void rebase(float mn, float c2) {
+    const float d = max_nan((m - mn) * c2, kCut);
+    const f2 f = pack2(ex2f(d), ex2f(d)), dd = pack2(d, d);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      if (kEntropy) a[i] = mul2(f, fma2(dd, s[i], a[i]));
+      s[i] = mul2(f, s[i]);
+    }
+    m = mn;
+  }
+  __device__ __forceinline__ void add(const uint4& w, f2 negm, f2 c2) {
+#pragma unroll
+    for (int i = 0; i < Raw<T>::kPairs; i++) {
+      float t0, t1;
+      unpack2(mul2(add2(Raw<T>::pair(w, i), negm), c2), t0, t1);
+      if (kEntropy) t0 = max_nan(t0, kCut), t1 = max_nan(t1, kCut);
+      const f2 e = pack2(ex2f(t0), ex2f(t1));
+      s[i & 1] = add2(s[i & 1], e);
+      if (kEntropy) a[i & 1] = fma2(e, pack2(t0, t1), a[i & 1]);
+    }
+  }
+  __device__ __forceinline__ Stat total() const {
+    float x, y, z, w;
+    Stat r;
+    r.m = m;
+    unpack2(add2(s[0], s[1]), x, y);
+    unpack2(add2(a[0], a[1]), z, w);
+    r.s = x + y;
+    r.a = kEntropy ? z + w : 0.f;
+    return r;
+  }
+};
+
+__device__ __forceinline__ void warp_merge(Stat& st, float c2) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    st.merge(__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
+             __shfl_xor_sync(0xffffffffu, st.a, o), c2);
+}
+
+// The barriers of a CTA.
+struct RingBars {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t part_full[2], part_empty[2];   // a row's warp sums: written, read
+  uint64_t joined[2];                     // every CTA of the cluster sent its part of a row
+  uint64_t pre_full[2], scal_full[2], p2_done[2];   // distillation
+  __device__ void init(int cs) {
+    for (int i = 0; i < kMaxSlots; i++) tc::mbar_init(&full[i], 1), tc::mbar_init(&empty[i], kConsWarps);
+    for (int i = 0; i < 2; i++) {
+      tc::mbar_init(&part_full[i], kConsWarps);
+      tc::mbar_init(&part_empty[i], kFinWarps);
+      tc::mbar_init(&joined[i], cs);
+      tc::mbar_init(&pre_full[i], kFinWarps);
+      tc::mbar_init(&scal_full[i], 1);
+      tc::mbar_init(&p2_done[i], kConsWarps);
+    }
+    tc::fence_mbar_init();
+  }
+};
+
+// A position in the ring: slot, and the parity of the slot's round.
+struct RingPos {
+  int slot = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(int n_slots) {
+    if (++slot == n_slots) slot = 0, round ^= 1;
+  }
+};
+
+constexpr int kSmemMax = 227 * 1024;
+
+// SMs of the current device
+int sm_count();
+
+// CTAs per row.  Time of a call in SM microseconds: rounds of clusters over the rows, each
+// round a part's bytes at an SM's share of the memory rate plus what a round costs besides.
+// rows_held: parts that the ring has to hold at once (0: any ring will do).
+int pick_cluster(int32_t n, int64_t nv, int ring_bytes, int rows_held);
+
+// Launches kernel(p) with n rows' clusters of cs CTAs, at most as many as the device holds.
+int launch_ring_raw(const void* kernel, const void* p, int32_t n, int cs, int smem, cudaStream_t s);
+template <typename P>
+int launch_ring(const void* kernel, const P& p, int32_t n, int cs, int smem, cudaStream_t s) {
+  return launch_ring_raw(kernel, &p, n, cs, smem, s);
+}
+
+}  // namespace rows
+}  // namespace octo

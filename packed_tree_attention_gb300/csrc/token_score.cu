@@ -9,19 +9,20 @@
 // (m, ln S) is kept rather than m c + ln S: at logits in the thousands the sum's rounding
 // would be a per-mille error of every probability that the gradient forms from it.
 
-#include "row_common.cuh"
+#include "row_ring.cuh"
 
 namespace octo {
 namespace {
 
 using namespace rows;
 
-constexpr int kThreads = 512;
+constexpr int kGroupStages = 8;      // stage classes of the group maxima
+constexpr int kMaxCand = 2048, kMaxGroups = 1024;
 
 struct ScoreParams {
   const void* logits;
   int64_t ld;
-  int32_t V, row0, k;
+  int32_t V, row0, n, k;
   float c;
   const int32_t* ids;    // [plan rows] or null
   float* logp;           // [plan rows] or null
@@ -31,71 +32,471 @@ struct ScoreParams {
   float* top_logp;       // [n][k]
   SuccTable succ;
   int32_t* status;
+  RingShape ring;
 };
 
-// One CTA per row: one pass for the statistics, then one pass per alternative for the
-// largest entry after the last one found.
+// Shared memory of the finishers; the ring's slots follow.
+struct ScoreSmem {
+  RingBars bars;
+  float part[2][kConsWarps][3];          // a row's warp sums
+  float in_stat[2][kMaxCluster][3];      // rank 0: the CTAs' sums
+  int32_t s_t[2][kMaxSucc], n_succ[2];   // successors of the row
+  uint32_t red[2][kFinWarps][2];
+  int32_t n_groups, n_cand, n_ties;
+};
+struct TopSmem {
+  unsigned long long in_list[2][kMaxCluster][kMaxTop];   // rank 0: the CTAs' alternatives, best first
+  int32_t in_count[2][kMaxCluster];
+  unsigned long long cand[kMaxCand];
+  unsigned long long sorted[kMaxTop];
+  uint16_t group[kMaxGroups];
+  float gmax[2][kGroupStages][kCons];    // largest entry of each group: a thread's vectors in a class of stages
+};
+
+template <bool kTop>
+__host__ __device__ constexpr int ring_offset() {
+  return (((int)sizeof(ScoreSmem) + 15) / 16 * 16 + (kTop ? (int)sizeof(TopSmem) : 0) + 127) / 128 * 128;
+}
+
+// An alternative: the value's key above the complement of its id, so that among equal values
+// the lowest id is the largest.
+__device__ __forceinline__ unsigned long long cand_of(uint32_t key, int32_t v) {
+  return ((unsigned long long)key << 32) | (uint32_t)~v;
+}
+
+// Reduces over the finishers; red is used alternately (buf) so that one barrier is enough.
+template <typename F>
+__device__ __forceinline__ uint32_t fin_reduce(uint32_t v, uint32_t (&red)[2][kFinWarps][2], int buf, int slot, F f) {
+  if ((threadIdx.x & 31) == 0) red[buf][((int)threadIdx.x - kCons) >> 5][slot] = v;
+  fin_sync();
+  uint32_t r = red[buf][0][slot];
+#pragma unroll
+  for (int i = 1; i < kFinWarps; i++) r = f(r, red[buf][i][slot]);
+  return r;
+}
+
+// The k largest entries of a CTA's part of a row, best first, in sm.sorted; returns how many
+// (fewer than k only where the part has no more that are not NaN).  Called by the finishers.
+//
+// The consumers leave the largest entry of each group of a thread's vectors.  The k-th largest
+// of those, tau, is a lower bound of the part's k-th largest entry, so only groups that reach
+// tau are read again (from L2): little more than k groups of 16 to 64 entries.  A bisection
+// over the keys finds tau; it stops early, at a few groups more than k.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_token_score(ScoreParams p) {
+__device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSmem& ts, int par, int v0, int nvec, int tail_n,
+                        float tail_x) {
   using VT = Vec<T>;
-  __shared__ float red[96];
-  __shared__ unsigned long long s_best;
-  const int rl = blockIdx.x;
-  const T* row = reinterpret_cast<const T*>(p.logits) + (size_t)rl * p.ld;
-  const float c2 = p.c * kLog2e;
-  Stat st;
-  st.init();
-  float mx = -INFINITY;
-  for (int v = threadIdx.x; v < p.V; v += kThreads) {
-    const float x = VT::get(row + v);
-    mx = fmaxf(mx, x);
-    if (x > st.m) st.rebase(x, c2);
-    st.add(x, c2);
+  constexpr int E = VT::E;
+  const int ft = threadIdx.x - kCons, lane = threadIdx.x & 31;
+  const int k = p.k;
+  const int n_st = (nvec + p.ring.stage - 1) / p.ring.stage;          // stages of this part
+  const int J = min(max(p.ring.n_stages, 1), kGroupStages);
+  const int nk = J * (kCons / kFin);
+  uint32_t key[kGroupStages * (kCons / kFin)];
+  uint32_t mx = 0;
+#pragma unroll
+  for (int q = 0; q < kGroupStages * (kCons / kFin); q++) {
+    key[q] = q < nk && n_st > 0 ? order_key((&ts.gmax[par][0][0])[q * kFin + ft]) : 0u;
+    mx = max(mx, key[q]);
   }
-  block_stat<kThreads>(st, c2, red);
-  const bool empty = st.s == 0.f;
-  const float m = empty ? -INFINITY : st.m, ls = empty ? -INFINITY : logf(st.s);
-  auto term = [&](float x) { return x == -INFINITY ? -INFINITY : (x - m) * p.c - ls; };
-  if (threadIdx.x == 0) {
-    p.row_stat[2 * (size_t)rl] = m;
-    p.row_stat[2 * (size_t)rl + 1] = ls;
-    if (p.entropy) p.entropy[rl] = empty ? 0.f : ls - kLn2 * (st.a / st.s);
-    if (p.ids) {
-      int32_t t[kMaxSucc];
-      bool start;
-      const int n = p.succ.find(p.row0 + rl, t, &start);
-      if (start) p.logp[p.row0 + rl] = 0.f;
-      for (int i = 0; i < n; i++) {
-        const int id = p.ids[t[i]];
-        if (id < 0 || id >= p.V) {
-          atomicExch(p.status, OCTO_EINVAL);
-          p.logp[t[i]] = __int_as_float(0x7fc00000);
+  auto umin = [](uint32_t a, uint32_t b) { return min(a, b); };
+  auto umax = [](uint32_t a, uint32_t b) { return max(a, b); };
+  auto uadd = [](uint32_t a, uint32_t b) { return a + b; };
+  const uint32_t wmin = __reduce_min_sync(0xffffffffu, mx), wmax = __reduce_max_sync(0xffffffffu, mx);
+  if (lane == 0) {
+    ss.red[0][ft >> 5][0] = wmin;
+    ss.red[0][ft >> 5][1] = wmax;
+  }
+  if (ft == 0) ss.n_groups = ss.n_cand = 0;
+  fin_sync();
+  uint32_t lo = ss.red[0][0][0], hi = ss.red[0][0][1];
+#pragma unroll
+  for (int i = 1; i < kFinWarps; i++) lo = umin(lo, ss.red[0][i][0]), hi = umax(hi, ss.red[0][i][1]);
+  lo = max(lo, 1u);   // NaN keys are 0
+  int buf = 1;
+  auto count_groups = [&](uint32_t t) {
+    uint32_t c = 0;
+#pragma unroll
+    for (int q = 0; q < kGroupStages * (kCons / kFin); q++) c += key[q] >= t;
+    c = fin_reduce(__reduce_add_sync(0xffffffffu, c), ss.red, buf, 0, uadd);
+    buf ^= 1;
+    return (int)c;
+  };
+  // invariant: at least k groups reach lo, or lo is the lowest key that all of them reach
+  auto bisect = [&](int enough) {
+    if (!enough && lo < hi && count_groups(lo + 1) < k) hi = lo;
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      const int c = count_groups(mid);
+      if (c >= k) {
+        lo = mid;
+        if (c <= enough) break;
+      } else {
+        hi = mid - 1;
+      }
+    }
+  };
+  // entries of the groups that reach `from`, at least `from` themselves, into cand
+  auto collect = [&](uint32_t from) {
+#pragma unroll
+    for (int q = 0; q < kGroupStages * (kCons / kFin); q++)
+      if (key[q] >= from) {
+        const int i = atomicAdd(&ss.n_groups, 1);
+        if (i < kMaxGroups) ts.group[i] = (uint16_t)(q * kFin + ft);
+      }
+    fin_sync();
+    const int ng = ss.n_groups;
+    if (ng > kMaxGroups) return false;
+    const int per = (p.ring.n_stages + J - 1) / J * kPer;   // most vectors of a group
+    for (int it = ft; it < ng * per; it += kFin) {
+      const int g = ts.group[it / per], sub = it % per;
+      const int jg = g / kCons, first = (jg * p.ring.n_stages + J - 1) / J, st = first + sub / kPer;
+      const int i = (sub % kPer) * kCons + g % kCons, at = st * p.ring.stage + i;
+      if (i >= p.ring.stage || at >= nvec || st * J / p.ring.n_stages != jg) continue;
+      const uint4 w = *reinterpret_cast<const uint4*>(row + (size_t)(v0 + at) * E);
+      float x[E];
+      VT::cvt(w, x);
+      uint32_t hit = 0;
+#pragma unroll
+      for (int e = 0; e < E; e++) hit |= (uint32_t)(order_key(x[e]) >= from) << e;
+      if (!hit) continue;
+      int c = atomicAdd(&ss.n_cand, __popc(hit));
+      if (c > kMaxCand) break;   // too many: all of it is done again
+#pragma unroll
+      for (int e = 0; e < E; e++)
+        if (hit >> e & 1) {
+          if (c < kMaxCand) ts.cand[c] = cand_of(order_key(x[e]), (v0 + at) * E + e);
+          c++;
+        }
+    }
+    if (ft < tail_n && order_key(tail_x) >= from) {
+      const int c = atomicAdd(&ss.n_cand, 1);
+      if (c < kMaxCand) ts.cand[c] = cand_of(order_key(tail_x), p.V - tail_n + ft);
+    }
+    fin_sync();
+    return ss.n_cand <= kMaxCand;
+  };
+  auto reset = [&] {
+    fin_sync();
+    if (ft == 0) ss.n_groups = ss.n_cand = ss.n_ties = 0;
+    fin_sync();
+  };
+  bisect(k + 8 + k / 4);
+  if (lo <= order_key(-INFINITY) || !collect(lo)) {
+    // Many entries reach tau, as with equal ones in most groups (masked rows, rounded
+    // logits).  With the exact tau fewer than k groups exceed it: take what exceeds tau, and
+    // the entries equal to it in the order of their ids.
+    bisect(0);
+    reset();
+    bool ok = lo == 0xffffffffu || collect(lo + 1);
+    if (!ok) {
+      // Those few groups alone hold more than kMaxCand entries above tau: find the part's
+      // k-th largest entry by counting over the whole part.  Rare, and slow.
+      uint32_t a = lo, b = 0xffffffffu;
+      while (a < b) {
+        const uint32_t mid = a + (b - a) / 2 + ((b - a) & 1);
+        uint32_t c = ft < tail_n && order_key(tail_x) >= mid;
+        for (int i = ft; i < nvec; i += kFin) {
+          float x[E];
+          VT::cvt(*reinterpret_cast<const uint4*>(row + (size_t)(v0 + i) * E), x);
+#pragma unroll
+          for (int e = 0; e < E; e++) c += order_key(x[e]) >= mid;
+        }
+        c = fin_reduce(__reduce_add_sync(0xffffffffu, c), ss.red, buf, 0, uadd);
+        buf ^= 1;
+        if ((int)c >= k) a = mid;
+        else b = mid - 1;
+      }
+      lo = a;   // fewer than k entries exceed it
+      reset();
+      for (int i = ft; i < nvec; i += kFin) {
+        float x[E];
+        VT::cvt(*reinterpret_cast<const uint4*>(row + (size_t)(v0 + i) * E), x);
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+          const uint32_t kx = order_key(x[e]);
+          if (kx > lo) ts.cand[atomicAdd(&ss.n_cand, 1)] = cand_of(kx, (v0 + i) * E + e);
+        }
+      }
+      if (ft < tail_n && order_key(tail_x) > lo)
+        ts.cand[atomicAdd(&ss.n_cand, 1)] = cand_of(order_key(tail_x), p.V - tail_n + ft);
+      fin_sync();
+    }
+    const int above = ss.n_cand;
+    // ties by id: 128 vectors at a time, then the last entries, until there are enough
+    int found = 0;
+    for (int base = 0; base < nvec + 1 && above + found < k; base += kFin) {
+      uint32_t hit = 0;
+      const int i = base + ft;
+      if (i < nvec) {
+        float x[E];
+        VT::cvt(*reinterpret_cast<const uint4*>(row + (size_t)(v0 + i) * E), x);
+#pragma unroll
+        for (int e = 0; e < E; e++) hit |= (uint32_t)(order_key(x[e]) == lo) << e;
+      }
+      const int mine = __popc(hit);
+      int inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) ss.red[buf][ft >> 5][0] = inc;
+      fin_sync();
+      int at = found + inc - mine, total = 0;
+#pragma unroll
+      for (int w = 0; w < kFinWarps; w++) {
+        if (w < (ft >> 5)) at += ss.red[buf][w][0];
+        total += ss.red[buf][w][0];
+      }
+      buf ^= 1;
+      for (int e = 0; e < E; e++)
+        if (hit >> e & 1) {
+          if (above + at < k) ts.cand[above + at] = cand_of(lo, (v0 + i) * E + e);
+          at++;
+        }
+      found += total;
+    }
+    if (ft < 32) {
+      const bool hit = ft < tail_n && order_key(tail_x) == lo;
+      const uint32_t who = __ballot_sync(0xffffffffu, hit);
+      const int at = above + found + __popc(who & ((1u << lane) - 1));
+      if (hit && at < k) ts.cand[at] = cand_of(lo, p.V - tail_n + ft);
+      if (ft == 0) ss.n_ties = found + __popc(who);
+    }
+    fin_sync();
+    if (above < k) {
+      if (ft == 0) ss.n_cand = min(above + ss.n_ties, k);
+      fin_sync();
+    }
+  }
+  // rank of each candidate by counting the better ones
+  const int n = ss.n_cand;
+  for (int c = ft; c < n; c += kFin) {
+    const unsigned long long mine = ts.cand[c];
+    int rank = 0;
+    for (int i = 0; i < n; i++) rank += ts.cand[i] > mine;
+    if (rank < k) ts.sorted[rank] = mine;
+  }
+  fin_sync();
+  return min(n, k);
+}
+
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant__ ScoreParams p) {
+  using VT = Vec<T>;
+  constexpr int E = VT::E;
+  extern __shared__ __align__(128) uint8_t smem[];
+  ScoreSmem& ss = *reinterpret_cast<ScoreSmem*>(smem);
+  TopSmem& ts = *reinterpret_cast<TopSmem*>(smem + (sizeof(ScoreSmem) + 15) / 16 * 16);
+  uint4* const slots = reinterpret_cast<uint4*>(smem + ring_offset<kTop>());
+  RingBars& bar = ss.bars;
+  const RingShape rs = p.ring;
+  const uint32_t rank = rs.cs > 1 ? cluster_rank() : 0;
+  const int n_clusters = gridDim.x / rs.cs, cluster = blockIdx.x / rs.cs;
+  const int nv = p.V / E;
+  const int v0 = min(nv, (int)rank * rs.seg), nvec = min(rs.seg, nv - v0);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const float c2 = p.c * kLog2e;
+  const T* const logits = reinterpret_cast<const T*>(p.logits);
+
+  if (tid == 0) bar.init(rs.cs);
+  __syncthreads();
+  if (rs.cs > 1) cluster_sync();
+
+  if (tid >= kCons + kFin) {
+    // ---- copies ----
+    if (lane == 0) {
+      RingPos pos;
+      int issued = 0;
+      bool ok = true;
+      for (int r = cluster; r < p.n && ok; r += n_clusters) {
+        const T* src = logits + (size_t)r * p.ld + (size_t)v0 * E;
+        for (int b = 0; b < nvec; b += rs.stage) {
+          if (!(ok = tc::mbar_wait(&bar.empty[pos.slot], pos.round ^ 1, p.status, OCTO_ETIMEOUT))) break;
+          const uint32_t bytes = (uint32_t)min(rs.stage, nvec - b) * 16;
+          tc::mbar_expect_tx(&bar.full[pos.slot], bytes);
+          bulk_load(slots + (size_t)pos.slot * rs.stage, src + (size_t)b * E, bytes, &bar.full[pos.slot]);
+          pos.next(rs.n_slots);
+          issued++;
+        }
+      }
+      // a copy must not outlive the CTA: the consumers have seen all of them unless a wait gave up
+      if (!ok)
+        for (int i = min(issued, rs.n_slots); i > 0; i--) {
+          if (--pos.slot < 0) pos.slot = rs.n_slots - 1, pos.round ^= 1;
+          tc::mbar_wait(&bar.full[pos.slot], pos.round, p.status, OCTO_ETIMEOUT);
+        }
+    }
+  } else if (tid < kCons) {
+    // ---- consumers: sums of the part, group maxima ----
+    RingPos pos;
+    bool ok = true;
+    const int J = min(max(rs.n_stages, 1), kGroupStages);
+    for (int r = cluster, it = 0; r < p.n && ok; r += n_clusters, it++) {
+      const int par = it & 1;
+      StageStat<T, true> st;
+      st.init();
+      float gm = -INFINITY;
+      // the finishers are done with this parity's buffers two rows ago
+      if (kTop) ok = warp_wait(&bar.part_empty[par], ((it >> 1) & 1) ^ 1, p.status);
+      for (int j = 0; j < rs.n_stages && ok; j++) {
+        const int cnt = min(rs.stage, nvec - j * rs.stage);
+        if (cnt > 0) {
+          if (!(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) break;
+          const uint4* slot = slots + (size_t)pos.slot * rs.stage;
+          uint4 w[kPer];
+          float mx = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < kPer; q++) {
+            const int i = q * kCons + tid;
+            w[q] = i < cnt ? slot[i] : Raw<T>::masked();
+            mx = fmaxf(mx, Raw<T>::max(w[q]));
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
+          if (mx > st.m) st.rebase(mx, c2);
+          gm = fmaxf(gm, mx);
+          const f2 negm = pack2(-st.m, -st.m), cc = pack2(c2, c2);
+#pragma unroll
+          for (int q = 0; q < kPer; q++)
+            if (q * kCons < cnt) st.add(w[q], negm, cc);
+          pos.next(rs.n_slots);
+        }
+        if (kTop) {
+          const int jg = j * J / rs.n_stages;
+          if (j + 1 == rs.n_stages || (j + 1) * J / rs.n_stages != jg) {
+            ts.gmax[par][jg][tid] = gm;
+            gm = -INFINITY;
+          }
+        }
+      }
+      if (!ok) break;
+      Stat tot = st.total();
+      warp_merge(tot, c2);
+      if (!kTop) ok = warp_wait(&bar.part_empty[par], ((it >> 1) & 1) ^ 1, p.status);
+      if (lane == 0) {
+        float* q = ss.part[par][tid >> 5];
+        q[0] = tot.m, q[1] = tot.s, q[2] = tot.a;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar.part_full[par]);
+    }
+  } else {
+    // ---- finishers ----
+    const int ft = tid - kCons;
+    const int tail_n = rank + 1 == (uint32_t)rs.cs ? p.V - nv * E : 0;
+    bool ok = true;
+    for (int r = cluster, it = 0; r < p.n && ok; r += n_clusters, it++) {
+      const int par = it & 1;
+      const uint32_t ph = (it >> 1) & 1;
+      const T* row = logits + (size_t)r * p.ld;
+      // what does not need the sums: successors, their logits, the row's last entries
+      if (rank == 0 && p.ids && ft == 0) {
+        bool start;
+        ss.n_succ[par] = p.succ.find(p.row0 + r, ss.s_t[par], &start);
+        if (start) p.logp[p.row0 + r] = 0.f;
+      }
+      const float tail_x = ft < tail_n ? VT::get(row + nv * E + ft) : -INFINITY;
+      fin_sync();
+      int t = -1;
+      float xt = 0.f;
+      bool bad = false;
+      if (rank == 0 && p.ids && ft < ss.n_succ[par]) {
+        t = ss.s_t[par][ft];
+        const int id = p.ids[t];
+        bad = id < 0 || id >= p.V;
+        if (bad) atomicExch(p.status, OCTO_EINVAL);
+        else xt = VT::get(row + id);
+      }
+
+      if (!(ok = fin_all(tc::mbar_wait(&bar.part_full[par], ph, p.status, OCTO_ETIMEOUT)))) break;
+      Stat st;
+      st.init();
+      if (lane < kConsWarps) {
+        const float* q = ss.part[par][lane];
+        st.m = q[0], st.s = q[1], st.a = q[2];
+      } else if (lane - kConsWarps < tail_n) {
+        const float x = VT::get(row + nv * E + lane - kConsWarps);
+        if (x > st.m) st.m = x;
+        st.add(x, c2);
+      }
+      warp_merge(st, c2);
+      int n_top = 0;
+      if (kTop) n_top = part_top<T>(row, p, ss, ts, par, v0, nvec, tail_n, tail_x);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar.part_empty[par]);
+
+      if (rs.cs > 1) {
+        // to rank 0, and an arrival to every rank: a rank sends row i + 2 only after it has
+        // all arrivals of row i + 1, so rank 0 is done with row i
+        if (kTop) {
+          const uint32_t dst = map_rank(tc::smem_u32(ts.in_list[par][rank]), 0);
+          if (ft < n_top) st_remote(dst + 8 * ft, ts.sorted[ft]);
+        }
+        if (ft == 0) {
+          const uint32_t dst = map_rank(tc::smem_u32(ss.in_stat[par][rank]), 0);
+          st_remote(dst, st.m);
+          st_remote(dst + 4, st.s);
+          st_remote(dst + 8, st.a);
+          if (kTop) st_remote(map_rank(tc::smem_u32(&ts.in_count[par][rank]), 0), __int_as_float(n_top));
+        }
+        fin_sync();
+        if (ft < rs.cs) arrive_remote(map_rank(tc::smem_u32(&bar.joined[par]), ft));
+        if (!(ok = fin_all(cluster_wait(&bar.joined[par], ph, p.status)))) break;
+        if (rank != 0) continue;
+        st.init();
+        for (int q = 0; q < rs.cs; q++) st.merge(ss.in_stat[par][q][0], ss.in_stat[par][q][1], ss.in_stat[par][q][2], c2);
+      }
+      const bool empty = st.s == 0.f;
+      const float m = empty ? -INFINITY : st.m, ls = empty ? -INFINITY : logf(st.s);
+      auto term = [&](float x) { return x == -INFINITY ? -INFINITY : (x - m) * p.c - ls; };
+      if (ft == 0) {
+        p.row_stat[2 * (size_t)r] = m;
+        p.row_stat[2 * (size_t)r + 1] = ls;
+        if (p.entropy) p.entropy[r] = empty ? 0.f : ls - kLn2 * (st.a / st.s);
+      }
+      if (t >= 0) p.logp[t] = bad ? __int_as_float(0x7fc00000) : term(xt);
+      if (kTop) {
+        const size_t o = (size_t)r * p.k;
+        auto put = [&](int rk, unsigned long long e) {
+          p.top_ids[o + rk] = (int32_t) ~(uint32_t)e;
+          p.top_logp[o + rk] = term(order_value((uint32_t)(e >> 32)));
+        };
+        int total = n_top;
+        if (rs.cs == 1) {
+          if (ft < n_top) put(ft, ts.sorted[ft]);
         } else {
-          p.logp[t[i]] = term(VT::get(row + id));
+          // an entry's rank: its place in its own list, and the better entries of the others
+          total = 0;
+          for (int q = 0; q < rs.cs; q++) total += ts.in_count[par][q];
+          for (int q = 0; q < rs.cs; q++) {
+            if (ft >= ts.in_count[par][q]) continue;
+            const unsigned long long e = ts.in_list[par][q][ft];
+            int rk = ft;
+            for (int o2 = 0; o2 < rs.cs && rk < p.k; o2++) {
+              if (o2 == q) continue;
+              int a = 0, b = ts.in_count[par][o2];   // entries [0, a) are better
+              while (a < b) {
+                const int mid = (a + b) >> 1;
+                if (ts.in_list[par][o2][mid] > e) a = mid + 1;
+                else b = mid;
+              }
+              rk += a;
+            }
+            if (rk < p.k) put(rk, e);
+          }
+        }
+        if (ft >= total && ft < p.k) {
+          p.top_ids[o + ft] = -1;
+          p.top_logp[o + ft] = __int_as_float(0x7fc00000);
         }
       }
     }
   }
-  unsigned long long last = ~0ull;
-  for (int j = 0; j < p.k; j++) {
-    if (threadIdx.x == 0) s_best = 0;
-    __syncthreads();
-    unsigned long long best = 0;
-    for (int v = threadIdx.x; v < p.V; v += kThreads) {
-      const uint32_t key = order_key(VT::get(row + v));
-      const unsigned long long e = ((unsigned long long)key << 32) | (uint32_t)~v;
-      if (key && e < last && e > best) best = e;
-    }
-    atomicMax(&s_best, best);
-    __syncthreads();
-    last = s_best;
-    if (threadIdx.x == 0) {
-      const size_t o = (size_t)rl * p.k + j;
-      p.top_ids[o] = last ? (int32_t) ~(uint32_t)last : -1;
-      p.top_logp[o] = last ? term(order_value((uint32_t)(last >> 32))) : __int_as_float(0x7fc00000);
-    }
-    __syncthreads();
-  }
+  // no CTA leaves while another may still write to its shared memory
+  __syncwarp();
+  if (rs.cs > 1) cluster_sync();
 }
 
 struct ScoreBwdParams {
@@ -111,59 +512,116 @@ struct ScoreBwdParams {
   const float* g_entropy;  // [n] or null
   SuccTable succ;
   int32_t* status;
+  int32_t parts, part_vecs;   // CTAs per row, vectors of each
 };
 
-// One CTA per row.  In log2 units, y = c2 (x - m) - log2 S and p = 2^y, an element's
-// gradient is p (A + B y) with the row's A = -c (G + g_H H), B = -c g_H ln 2, plus
-// c g_t at the successors' ids.
+// In log2 units, y = c2 (x - m) - log2 S and p = 2^y, an element's gradient is p (A + B y)
+// with the row's A = -c (G + g_H H), B = -c g_H ln 2, plus c g_t at the successors' ids.
+//
+// One pass, bound by memory: a CTA takes up to kThreads * kBwdPer vectors of a row, all of its
+// loads in flight before it looks up the row's successors.
+constexpr int kBwdThreads = 256, kBwdPer = 8;
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_token_score_bwd(ScoreBwdParams p) {
+__global__ void __launch_bounds__(kBwdThreads, 4) k_token_score_bwd(const __grid_constant__ ScoreBwdParams p) {
   using VT = Vec<T>;
-  __shared__ int32_t s_id[kMaxSucc];
+  constexpr int E = VT::E;
+  __shared__ int32_t s_t[kMaxSucc], s_id[kMaxSucc];
   __shared__ float s_g[kMaxSucc];
   __shared__ float s_G;
-  __shared__ int32_t s_n;
-  const int rl = blockIdx.x;
+  __shared__ int32_t s_n, s_lo, s_hi;
+  const int rl = blockIdx.x / p.parts, part = blockIdx.x - rl * p.parts, tid = threadIdx.x;
   const T* row = reinterpret_cast<const T*>(p.logits) + (size_t)rl * p.ld;
   T* grow = reinterpret_cast<T*>(p.dlogits) + (size_t)rl * p.ld;
-  if (threadIdx.x == 0) {
-    int n = 0;
-    float G = 0.f;
-    if (p.g_logp) {
-      int32_t t[kMaxSucc];
-      bool start;
-      const int nt = p.succ.find(p.row0 + rl, t, &start);
-      for (int i = 0; i < nt; i++) {
-        const int id = p.ids[t[i]];
-        if (id < 0 || id >= p.V) {
-          atomicExch(p.status, OCTO_EINVAL);
-          continue;
-        }
-        s_id[n] = id;
-        s_g[n] = p.g_logp[t[i]];
-        G += s_g[n++];
-      }
-    }
-    s_n = n;
-    s_G = G;
+  const int nv = p.V / E, v0 = part * p.part_vecs, v1 = min(nv, v0 + p.part_vecs);
+  uint4 w[kBwdPer];
+#pragma unroll
+  for (int q = 0; q < kBwdPer; q++) {
+    const int i = v0 + q * kBwdThreads + tid;
+    if (i < v1) w[q] = __ldcs(reinterpret_cast<const uint4*>(row) + i);
   }
-  __syncthreads();
-  const int n = s_n;
   const float m = p.row_stat[2 * (size_t)rl], ls = p.row_stat[2 * (size_t)rl + 1];
   const float gH = p.g_entropy ? p.g_entropy[rl] : 0.f, H = p.g_entropy ? p.entropy[rl] : 0.f;
-  const bool empty = m == -INFINITY;
-  const float c2 = p.c * kLog2e, l2 = ls * kLog2e;
-  const float A = -p.c * (s_G + gH * H), B = -p.c * kLn2 * gH;
-  for (int v = threadIdx.x; v < p.V; v += kThreads) {
-    float g = 0.f;
-    if (!empty) {
-      const float y = max_nan((VT::get(row + v) - m) * c2 - l2, kCut);
-      g = ex2f(y) * fmaf(B, y, A);
-      for (int i = 0; i < n; i++)
-        if (s_id[i] == v) g += p.c * s_g[i];
+  if (tid < 32) {
+    int nt = 0;
+    if (p.g_logp) {
+      if (tid == 0) {
+        bool start;
+        nt = p.succ.find(p.row0 + rl, s_t, &start);
+      }
+      nt = __shfl_sync(0xffffffffu, nt, 0);
+      __syncwarp();
+      for (int i = tid; i < nt; i += 32) {
+        const int t = s_t[i], id = p.ids[t];
+        const bool bad = id < 0 || id >= p.V;
+        if (bad) atomicExch(p.status, OCTO_EINVAL);
+        s_id[i] = bad ? -1 : id;
+        s_g[i] = bad ? 0.f : p.g_logp[t];
+      }
+      __syncwarp();
     }
-    VT::put(grow + v, g);
+    if (tid == 0) {
+      float G = 0.f;
+      int lo = p.V, hi = -1;
+      for (int i = 0; i < nt; i++) {
+        if (s_id[i] < 0) continue;
+        G += s_g[i];
+        lo = min(lo, s_id[i]);
+        hi = max(hi, s_id[i]);
+      }
+      s_n = nt, s_G = G, s_lo = lo, s_hi = hi;
+    }
   }
+  __syncthreads();
+  const int lo = s_lo, hi = s_hi;
+  const float A = -p.c * (s_G + gH * H), B = -p.c * kLn2 * gH;
+  auto onehot = [&](int v) {
+    float g = 0.f;
+    for (int i = 0; i < s_n; i++)
+      if (s_id[i] == v) g += s_g[i];
+    return p.c * g;
+  };
+  if (m == -INFINITY) {   // nothing left in the row
+    for (int i = v0 + tid; i < v1; i += kBwdThreads) __stcs(reinterpret_cast<uint4*>(grow) + i, make_uint4(0, 0, 0, 0));
+    if (v1 == nv && tid < p.V - nv * E) VT::put(grow + nv * E + tid, 0.f);
+    return;
+  }
+  const float c2 = p.c * kLog2e, l2 = ls * kLog2e;
+  const f2 negm = pack2(-m, -m), cc = pack2(c2, c2), nl = pack2(-l2, -l2), AA = pack2(A, A), BB = pack2(B, B);
+#pragma unroll
+  for (int q = 0; q < kBwdPer; q++) {
+    const int i = v0 + q * kBwdThreads + tid;
+    if (i < v1) {
+      float g[E];
+#pragma unroll
+      for (int e = 0; e < E / 2; e++) {
+        float y0, y1;
+        unpack2(fma2(add2(Raw<T>::pair(w[q], e), negm), cc, nl), y0, y1);
+        y0 = max_nan(y0, kCut);
+        y1 = max_nan(y1, kCut);
+        unpack2(mul2(pack2(ex2f(y0), ex2f(y1)), fma2(BB, pack2(y0, y1), AA)), g[2 * e], g[2 * e + 1]);
+      }
+      if (i * E <= hi && i * E + E - 1 >= lo) {
+#pragma unroll
+        for (int e = 0; e < E; e++) g[e] += onehot(i * E + e);
+      }
+      __stcs(reinterpret_cast<uint4*>(grow) + i, VT::pack(g));
+    }
+  }
+  if (v1 == nv && tid < p.V - nv * E) {
+    const int v = nv * E + tid;
+    const float y = max_nan((VT::get(row + v) - m) * c2 - l2, kCut);
+    VT::put(grow + v, ex2f(y) * fmaf(B, y, A) + onehot(v));
+  }
+}
+
+template <typename T, bool kTop>
+int launch_score(ScoreParams& p, cudaStream_t s) {
+  const int off = ring_offset<kTop>(), ring = kSmemMax - off;
+  const int64_t nv = p.V / Vec<T>::E;
+  const int cs = pick_cluster(p.n, nv, ring, 1);
+  p.ring = ring_shape(nv, cs, ring);
+  return launch_ring((const void*)k_token_score<T, kTop>, p, p.n, cs, off + p.ring.n_slots * p.ring.stage * 16, s);
 }
 
 }  // namespace
@@ -198,12 +656,10 @@ int octo_token_score(octo_plan_t plan, int32_t row0, int32_t n_rows, const void*
   cudaStream_t s = (cudaStream_t)stream;
   plan->last_stream = s;
   NvtxRange nv("octo_token_score");
-  if (dtype == OCTO_DTYPE_BF16)
-    k_token_score<__nv_bfloat16><<<n_rows, kThreads, 0, s>>>(p);
-  else
-    k_token_score<float><<<n_rows, kThreads, 0, s>>>(p);
-  count_launch();
-  return cuda_status(cudaGetLastError());
+  p.n = n_rows;
+  const bool bf = dtype == OCTO_DTYPE_BF16;
+  if (k > 0) return bf ? launch_score<__nv_bfloat16, true>(p, s) : launch_score<float, true>(p, s);
+  return bf ? launch_score<__nv_bfloat16, false>(p, s) : launch_score<float, false>(p, s);
 }
 
 int octo_token_score_bwd(octo_plan_t plan, int32_t row0, int32_t n_rows, const void* logits, int32_t dtype, int64_t ld,
@@ -232,10 +688,15 @@ int octo_token_score_bwd(octo_plan_t plan, int32_t row0, int32_t n_rows, const v
   cudaStream_t s = (cudaStream_t)stream;
   plan->last_stream = s;
   NvtxRange nv("octo_token_score_bwd");
-  if (dtype == OCTO_DTYPE_BF16)
-    k_token_score_bwd<__nv_bfloat16><<<n_rows, kThreads, 0, s>>>(p);
+  const bool bf = dtype == OCTO_DTYPE_BF16;
+  const int32_t vecs = vocab / (bf ? 8 : 4), most = kBwdThreads * kBwdPer;
+  p.parts = vecs > most ? (vecs + most - 1) / most : 1;
+  p.part_vecs = (vecs + p.parts - 1) / p.parts;
+  if ((int64_t)n_rows * p.parts > INT32_MAX) return OCTO_EINVAL;
+  if (bf)
+    k_token_score_bwd<__nv_bfloat16><<<n_rows * p.parts, kBwdThreads, 0, s>>>(p);
   else
-    k_token_score_bwd<float><<<n_rows, kThreads, 0, s>>>(p);
+    k_token_score_bwd<float><<<n_rows * p.parts, kBwdThreads, 0, s>>>(p);
   count_launch();
   return cuda_status(cudaGetLastError());
 }

@@ -127,7 +127,9 @@ def awkward_rows(V, rng):
     last[-20:] = 9.0
     return [few, one, np.full(V, -np.inf), np.full(V, 2.5), zeros, steps, np.arange(V) / V * 20, -np.arange(V) / V * 20, last,
             rng.normal(5000, 2, V), rng.normal(-5000, 2, V), np.where(np.arange(V) % 512 < 30, 8.0, -8.0) + rng.normal(0, .1, V),
-            np.where(np.arange(V) % 4096 < 8, 10.0, 0.0), rng.normal(0, 40, V), low, rng.normal(0, 3, V)]
+            np.where(np.arange(V) % 4096 < 8, 10.0, 0.0), rng.normal(0, 40, V), low, rng.normal(0, 3, V),
+            np.where((np.arange(V) % 4096 < 800) & (np.arange(V) < 16384), rng.normal(20, 1, V), 0.0),
+            np.where((np.arange(V) % 2048 < 400) & (np.arange(V) < 16384), rng.normal(20, 1, V), -np.inf)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
