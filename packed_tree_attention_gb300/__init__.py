@@ -173,33 +173,48 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_T = {}   # torch's dtypes and calls, looked up once
+
+
+def _torch():
+    import torch
+    _T.update(logits={torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}, float32=torch.float32, int32=torch.int32,
+              device=torch.cuda.current_device, stream=torch._C._cuda_getCurrentRawStream)
+    return _T
+
+
 def _logits(x, n_rows, vocab, what="logits"):
     """(address, dtype, elements between rows) of a [rows][ld] bf16 or fp32 tensor holding
     n_rows rows of at least `vocab` entries; a column slice of a wider one is a row pitch."""
-    name = str(x.dtype)
-    if name not in ("torch.bfloat16", "torch.float32"):
-        raise ValueError("%s must be bfloat16 or float32 (got %s)" % (what, name))
+    dt = (_T or _torch())["logits"].get(x.dtype)
+    if dt is None:
+        raise ValueError("%s must be bfloat16 or float32 (got %s)" % (what, x.dtype))
     if x.dim() != 2 or x.shape[0] < n_rows or x.shape[1] < vocab or x.stride(1) != 1:
         raise ValueError("%s must be [rows][entries] with adjacent entries, %d rows of at least %d (got shape %s, "
                          "strides %s)" % (what, n_rows, vocab, tuple(x.shape), tuple(x.stride())))
     if not x.is_cuda:
         raise ValueError("%s must be on the GPU" % what)
-    ld = x.stride(0)
-    if x.shape[0] <= 1:        # one row: any pitch will do, and the library wants 16-byte ones
-        ld = -(-max(vocab, 1) // 8) * 8
-    return x.data_ptr(), DTYPE_F32 if name == "torch.float32" else DTYPE_BF16, ld
+    if x.get_device() != _T["device"]():
+        raise ValueError("%s must be on the current device" % what)
+    # one row: any pitch will do, and the library wants 16-byte ones
+    return x.data_ptr(), dt, x.stride(0) if x.shape[0] > 1 else -(-max(vocab, 1) // 8) * 8
 
 
 def _vector(x, name, count, what):
     """Address of a contiguous tensor of at least `count` elements of torch dtype `name`."""
     if x is None:
         return None
-    if str(x.dtype) != "torch." + name or x.numel() < count or not x.is_contiguous():
+    if x.dtype is not (_T or _torch())[name] or x.numel() < count or not x.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of at least %d elements (got %s, shape %s)"
                          % (what, name, count, x.dtype, tuple(x.shape)))
     if not x.is_cuda:
         raise ValueError("%s must be on the GPU" % what)
     return x.data_ptr()
+
+
+def _current(s):
+    """_stream for tensors that were seen to be on the current device."""
+    return _T["stream"](_T["device"]()) if s is None else _stream(s)
 
 
 def _stream(s):
@@ -491,7 +506,7 @@ class Plan:
             self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, _vector(ids, "int32", N, "ids"),
             _vector(logp, "float32", N, "logp"), _vector(row_stat, "float32", 2 * n_rows, "row_stat"),
             _vector(entropy, "float32", n_rows, "entropy"), k, _vector(top_ids, "int32", n_rows * k, "top_ids"),
-            _vector(top_logp, "float32", n_rows * k, "top_logp"), _stream(stream)), "octo_token_score")
+            _vector(top_logp, "float32", n_rows * k, "top_logp"), _current(stream)), "octo_token_score")
 
     def token_score_bwd(self, row0, n_rows, logits, vocab, row_stat, entropy, ids, g_logp, g_entropy, dlogits,
                         inv_temp=1.0, stream=None):
@@ -506,7 +521,7 @@ class Plan:
             self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, _vector(row_stat, "float32", 2 * n_rows, "row_stat"),
             _vector(entropy, "float32", n_rows, "entropy"), _vector(ids, "int32", N, "ids"),
             _vector(g_logp, "float32", N, "g_logp"), _vector(g_entropy, "float32", n_rows, "g_entropy"), g[0],
-            _stream(stream)), "octo_token_score_bwd")
+            _current(stream)), "octo_token_score_bwd")
 
     def distill_topk_workspace_size(self, n_rows):
         n = ctypes.c_size_t(0)
@@ -532,7 +547,7 @@ class Plan:
             _vector(teach_val, "float32", n_rows * k, "teach_val"), 1 if tail else 0,
             _vector(weight, "float32", N, "weight"), _vector(row_kl, "float32", N, "row_kl"), g, grad_scale,
             _vector(loss, "float32", 1, "loss"), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0,
-            _stream(stream)), "octo_distill_topk")
+            _current(stream)), "octo_distill_topk")
 
     def recurrent_workspace_size(self, n_heads, head_dim):
         return int(self._L.octo_recurrent_workspace_size(self.h, n_heads, head_dim))

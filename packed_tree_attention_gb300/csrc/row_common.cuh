@@ -152,6 +152,49 @@ struct SuccTable {
   }
 };
 
+// SuccTable::find for rows in ascending order: keeps the segment and the place among the extra
+// successors, and searches again only past the segment's end.
+struct SuccCursor {
+  int base = 0, end = 0, pred = -1, e = -1, e_pred = -1;
+  __device__ int find(const SuccTable& s, int r, int32_t* t, bool* path_start) {
+    *path_start = false;
+    if (s.is_decode) {
+      t[0] = r;
+      return 1;
+    }
+    if (r >= end) {
+      int lo = 0, hi = s.n_segs - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s.seg_row_base[mid] <= r) lo = mid;
+        else hi = mid - 1;
+      }
+      base = s.seg_row_base[lo];
+      end = lo + 1 < s.n_segs ? s.seg_row_base[lo + 1] : s.n_rows;
+      pred = s.seg_pred[lo];
+    }
+    if (e < 0) {
+      int a = 0, b = s.n_ex;
+      while (a < b) {
+        const int mid = (a + b) >> 1;
+        if (s.ex_pred[mid] < r) a = mid + 1;
+        else b = mid;
+      }
+      e = a;
+      e_pred = e < s.n_ex ? s.ex_pred[e] : INT32_MAX;
+    }
+    while (e_pred < r) e_pred = ++e < s.n_ex ? s.ex_pred[e] : INT32_MAX;
+    *path_start = r == base && pred < 0;
+    int n = 0;
+    if (r + 1 < end) t[n++] = r + 1;
+    for (int a = e, q = e_pred; q == r && n < kMaxSucc;) {
+      t[n++] = s.ex_row[a++];
+      q = a < s.n_ex ? s.ex_pred[a] : INT32_MAX;
+    }
+    return n;
+  }
+};
+
 inline SuccTable succ_table(const octo_plan_s* p) {
   SuccTable t;
   t.seg_row_base = p->seg_row_base;

@@ -17,7 +17,7 @@ namespace rows {
 
 constexpr int kConsWarps = 16, kFinWarps = 4;
 constexpr int kCons = kConsWarps * 32, kFin = kFinWarps * 32;
-constexpr int kBlock = kCons + kFin + 32;   // + the copying warp
+constexpr int kBlock = kCons + kFin + 64;   // + the copying warp and one for look-ups
 constexpr int kPer = 4;                     // vectors of one thread in a stage
 constexpr int kMaxSlots = 24;
 constexpr int kMaxCluster = 8;
@@ -151,6 +151,15 @@ struct Raw<__nv_bfloat16> {
     const __nv_bfloat162 m = __hmax2(__hmax2(b(w.x), b(w.y)), __hmax2(b(w.z), b(w.w)));
     return fmaxf(__low2float(m), __high2float(m));
   }
+  // entries below -2^100 raised to it, NaNs kept
+  __device__ __forceinline__ static uint4 floored(const uint4& w) {
+    auto f = [](uint32_t u) {
+      uint32_t r;
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(u), "r"(0xf180f180u));
+      return r;
+    };
+    return make_uint4(f(w.x), f(w.y), f(w.z), f(w.w));
+  }
 };
 template <>
 struct Raw<float> {
@@ -162,45 +171,82 @@ struct Raw<float> {
   __device__ __forceinline__ static float max(const uint4& w) {
     return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
   }
+  __device__ __forceinline__ static uint4 floored(const uint4& w) {
+    auto f = [](uint32_t u) { return __float_as_uint(max_nan(__uint_as_float(u), -0x1p100f)); };
+    return make_uint4(f(w.x), f(w.y), f(w.z), f(w.w));
+  }
 };
 
 // A thread's running statistics over stages.  The reference m moves once per stage at most,
 // to the largest of the thread's vectors; sums in pairs, two chains.
+//
+// With a usual reference, above -2^96, the exponent of an entry is one fused multiply-add,
+// t = c2 x - r with r = c2 m rounded: relative to r the sums are exact to the exponential's
+// own error, and total() refers them back to m by the rounding error of r, which an fma gives
+// exactly.  Entries below -2^100 add nothing there and are raised to it, two at a time, so that
+// a masked one's product 2^t t is 0 and not 0 * inf.  Other references (below -2^96: nothing but
+// masked entries so far), and temperatures that take c2 2^100 out of range, take the difference
+// first and cut each exponent off.
 template <typename T, bool kEntropy>
 struct StageStat {
-  float m;
+  float m, r;
   f2 s[2], a[2];
-  __device__ __forceinline__ void init() { m = -FLT_MAX, s[0] = s[1] = a[0] = a[1] = 0ull; }
-  __device__ __forceinline__ void rebase(float mn, float c2) {
-    const float d = max_nan((m - mn) * c2, kCut);
-    const f2 f = pack2(ex2f(d), ex2f(d)), dd = pack2(d, d);
+  __device__ __forceinline__ void init() { m = -FLT_MAX, r = 0.f, s[0] = s[1] = a[0] = a[1] = 0ull; }
+  __device__ __forceinline__ static bool usual(float m, float c2) {
+    return fabsf(m) < 0x1p96f && c2 < 0x1p20f && c2 > 0x1p-80f;
+  }
+  __device__ __forceinline__ void raise(float mn, float c2) {
+    const float rn = mn * c2;
+    const float d = max_nan(usual(m, c2) ? r - rn : (m - mn) * c2, kCut);
+    const float e = ex2f(d);
+    const f2 f = pack2(e, e), dd = pack2(d, d);
 #pragma unroll
     for (int i = 0; i < 2; i++) {
       if (kEntropy) a[i] = mul2(f, fma2(dd, s[i], a[i]));
       s[i] = mul2(f, s[i]);
     }
     m = mn;
+    r = rn;
   }
-  __device__ __forceinline__ void add(const uint4& w, f2 negm, f2 c2) {
+  template <bool kUsual>
+  __device__ __forceinline__ void add_vec(const uint4& raw, float c2) {
+    const uint4 w = kEntropy && kUsual ? Raw<T>::floored(raw) : raw;
+    const f2 cc = pack2(c2, c2), neg = kUsual ? pack2(-r, -r) : pack2(-m, -m);
 #pragma unroll
     for (int i = 0; i < Raw<T>::kPairs; i++) {
+      f2 t = Raw<T>::pair(w, i);
+      t = kUsual ? fma2(t, cc, neg) : mul2(add2(t, neg), cc);
       float t0, t1;
-      unpack2(mul2(add2(Raw<T>::pair(w, i), negm), c2), t0, t1);
-      if (kEntropy) t0 = max_nan(t0, kCut), t1 = max_nan(t1, kCut);
+      unpack2(t, t0, t1);
+      if (!kUsual) t0 = max_nan(t0, kCut), t1 = max_nan(t1, kCut), t = pack2(t0, t1);
       const f2 e = pack2(ex2f(t0), ex2f(t1));
       s[i & 1] = add2(s[i & 1], e);
-      if (kEntropy) a[i & 1] = fma2(e, pack2(t0, t1), a[i & 1]);
+      if (kEntropy) a[i & 1] = fma2(e, t, a[i & 1]);
     }
   }
-  __device__ __forceinline__ Stat total() const {
+  // the vectors w[q] with q * kCons < cnt, the largest entry of all kPer being mx
+  __device__ __forceinline__ void add(const uint4 (&w)[kPer], int cnt, float mx, float c2) {
+    if (mx > m) raise(mx, c2);
+    if (usual(m, c2)) {
+#pragma unroll
+      for (int q = 0; q < kPer; q++)
+        if (q * kCons < cnt) add_vec<true>(w[q], c2);
+    } else {
+#pragma unroll
+      for (int q = 0; q < kPer; q++) add_vec<false>(w[q], c2);
+    }
+  }
+  __device__ __forceinline__ Stat total(float c2) const {
     float x, y, z, w;
-    Stat r;
-    r.m = m;
     unpack2(add2(s[0], s[1]), x, y);
     unpack2(add2(a[0], a[1]), z, w);
-    r.s = x + y;
-    r.a = kEntropy ? z + w : 0.f;
-    return r;
+    Stat t{m, x + y, kEntropy ? z + w : 0.f};
+    if (usual(m, c2)) {
+      const float d = fmaf(-m, c2, r), f = ex2f(d);
+      t.a = f * fmaf(d, t.s, t.a);
+      t.s *= f;
+    }
+    return t;
   }
 };
 
@@ -216,7 +262,8 @@ struct RingBars {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t part_full[2], part_empty[2];   // a row's warp sums: written, read
   uint64_t joined[2];                     // every CTA of the cluster sent its part of a row
-  uint64_t pre_full[2], scal_full[2], p2_done[2];   // distillation
+  uint64_t scal_full[2], scal_empty[2];   // a row's results: written, read by who needs them
+  uint64_t pre_full[2], p2_done[2];       // distillation
   __device__ void init(int cs) {
     for (int i = 0; i < kMaxSlots; i++) tc::mbar_init(&full[i], 1), tc::mbar_init(&empty[i], kConsWarps);
     for (int i = 0; i < 2; i++) {
@@ -225,6 +272,7 @@ struct RingBars {
       tc::mbar_init(&joined[i], cs);
       tc::mbar_init(&pre_full[i], kFinWarps);
       tc::mbar_init(&scal_full[i], 1);
+      tc::mbar_init(&scal_empty[i], 1);
       tc::mbar_init(&p2_done[i], kConsWarps);
     }
     tc::fence_mbar_init();

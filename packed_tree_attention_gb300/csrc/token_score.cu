@@ -16,8 +16,8 @@ namespace {
 
 using namespace rows;
 
-constexpr int kGroupStages = 8;      // stage classes of the group maxima
-constexpr int kMaxCand = 2048, kMaxGroups = 1024;
+constexpr int kGroupStages = 10;     // stage classes of the group maxima
+constexpr int kMaxCand = 2048, kMaxGroups = 1024, kMaxTrim = 512;
 
 struct ScoreParams {
   const void* logits;
@@ -40,17 +40,20 @@ struct ScoreSmem {
   RingBars bars;
   float part[2][kConsWarps][3];          // a row's warp sums
   float in_stat[2][kMaxCluster][3];      // rank 0: the CTAs' sums
-  int32_t s_t[2][kMaxSucc], n_succ[2];   // successors of the row
-  uint32_t red[2][kFinWarps][2];
-  int32_t n_groups, n_cand, n_ties;
+  float stat[2][2];                      // a row's (m, ln S), for the look-ups
+  int32_t s_t[kMaxSucc];                 // successors of the row
+  uint32_t red[2][kFinWarps];
+  int32_t n_groups, n_cand, n_ties, n_trim;
 };
 struct TopSmem {
   unsigned long long in_list[2][kMaxCluster][kMaxTop];   // rank 0: the CTAs' alternatives, best first
   int32_t in_count[2][kMaxCluster];
   unsigned long long cand[kMaxCand];
+  unsigned long long trim[kMaxTrim];
   unsigned long long sorted[kMaxTop];
   uint16_t group[kMaxGroups];
   float gmax[2][kGroupStages][kCons];    // largest entry of each group: a thread's vectors in a class of stages
+  float tmax[2][kCons];                  // and of each thread
 };
 
 template <bool kTop>
@@ -64,133 +67,147 @@ __device__ __forceinline__ unsigned long long cand_of(uint32_t key, int32_t v) {
   return ((unsigned long long)key << 32) | (uint32_t)~v;
 }
 
-// Reduces over the finishers; red is used alternately (buf) so that one barrier is enough.
-template <typename F>
-__device__ __forceinline__ uint32_t fin_reduce(uint32_t v, uint32_t (&red)[2][kFinWarps][2], int buf, int slot, F f) {
-  if ((threadIdx.x & 31) == 0) red[buf][((int)threadIdx.x - kCons) >> 5][slot] = v;
+// Sum over the finishers; red is used alternately (buf) so that one barrier is enough.
+__device__ __forceinline__ uint32_t fin_sum(uint32_t v, ScoreSmem& ss, int& buf) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  if ((threadIdx.x & 31) == 0) ss.red[buf][((int)threadIdx.x - kCons) >> 5] = v;
   fin_sync();
-  uint32_t r = red[buf][0][slot];
+  uint32_t r = 0;
 #pragma unroll
-  for (int i = 1; i < kFinWarps; i++) r = f(r, red[buf][i][slot]);
+  for (int i = 0; i < kFinWarps; i++) r += ss.red[buf][i];
+  buf ^= 1;
   return r;
 }
 
-// The k largest entries of a CTA's part of a row, best first, in sm.sorted; returns how many
+// The k largest entries of a CTA's part of a row, best first, in ts.sorted; returns how many
 // (fewer than k only where the part has no more that are not NaN).  Called by the finishers.
 //
-// The consumers leave the largest entry of each group of a thread's vectors.  The k-th largest
-// of those, tau, is a lower bound of the part's k-th largest entry, so only groups that reach
-// tau are read again (from L2): little more than k groups of 16 to 64 entries.  A bisection
-// over the keys finds tau; it stops early, at a few groups more than k.
+// The consumers leave the largest entry that each thread saw, and that of each group of its
+// vectors.  The k-th largest of the 512 threads' maxima, tau, is a lower bound of the part's
+// k-th largest entry, so only groups that reach tau are read again (from L2): for entries in
+// no order about 512 ln(512 / (512 - k)) groups, 21 for k = 20 and 147 for k = 128, of 16 to 32
+// entries.  Every warp finds tau for itself, 16 maxima a lane, by a bisection over the keys
+// that stops at a few threads more than k.
 template <typename T>
 __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSmem& ts, int par, int v0, int nvec, int tail_n,
                         float tail_x) {
   using VT = Vec<T>;
-  constexpr int E = VT::E;
+  constexpr int E = VT::E, kKeys = kCons / 32;
   const int ft = threadIdx.x - kCons, lane = threadIdx.x & 31;
   const int k = p.k;
-  const int n_st = (nvec + p.ring.stage - 1) / p.ring.stage;          // stages of this part
-  const int J = min(max(p.ring.n_stages, 1), kGroupStages);
-  const int nk = J * (kCons / kFin);
-  uint32_t key[kGroupStages * (kCons / kFin)];
-  uint32_t mx = 0;
-#pragma unroll
-  for (int q = 0; q < kGroupStages * (kCons / kFin); q++) {
-    key[q] = q < nk && n_st > 0 ? order_key((&ts.gmax[par][0][0])[q * kFin + ft]) : 0u;
-    mx = max(mx, key[q]);
-  }
-  auto umin = [](uint32_t a, uint32_t b) { return min(a, b); };
-  auto umax = [](uint32_t a, uint32_t b) { return max(a, b); };
-  auto uadd = [](uint32_t a, uint32_t b) { return a + b; };
-  const uint32_t wmin = __reduce_min_sync(0xffffffffu, mx), wmax = __reduce_max_sync(0xffffffffu, mx);
-  if (lane == 0) {
-    ss.red[0][ft >> 5][0] = wmin;
-    ss.red[0][ft >> 5][1] = wmax;
-  }
+  const int n_st = p.ring.n_stages, J = min(n_st, kGroupStages);
+  const int spc = n_st > kGroupStages ? (n_st + J - 1) / J : 1;   // most stages of a group
   if (ft == 0) ss.n_groups = ss.n_cand = 0;
-  fin_sync();
-  uint32_t lo = ss.red[0][0][0], hi = ss.red[0][0][1];
+  uint32_t lo, hi;
+  bool exact = false;
+  {
+    uint32_t key[kKeys];
+    uint32_t mn = 0xffffffffu, mx = 0;
 #pragma unroll
-  for (int i = 1; i < kFinWarps; i++) lo = umin(lo, ss.red[0][i][0]), hi = umax(hi, ss.red[0][i][1]);
-  lo = max(lo, 1u);   // NaN keys are 0
-  int buf = 1;
-  auto count_groups = [&](uint32_t t) {
-    uint32_t c = 0;
-#pragma unroll
-    for (int q = 0; q < kGroupStages * (kCons / kFin); q++) c += key[q] >= t;
-    c = fin_reduce(__reduce_add_sync(0xffffffffu, c), ss.red, buf, 0, uadd);
-    buf ^= 1;
-    return (int)c;
-  };
-  // invariant: at least k groups reach lo, or lo is the lowest key that all of them reach
-  auto bisect = [&](int enough) {
-    if (!enough && lo < hi && count_groups(lo + 1) < k) hi = lo;
+    for (int i = 0; i < kKeys; i++) {
+      key[i] = nvec > 0 ? order_key(ts.tmax[par][i * 32 + lane]) : order_key(-INFINITY);
+      mn = min(mn, key[i]);
+      mx = max(mx, key[i]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, mn);
+    hi = __reduce_max_sync(0xffffffffu, mx);
+    // at least k threads (kCons >= kMaxTop) reach lo; fewer than k reach hi + 1
+    const int enough = k + 8 + k / 4;
     while (lo < hi) {
       const uint32_t mid = lo + (hi - lo + 1) / 2;
-      const int c = count_groups(mid);
-      if (c >= k) {
+      uint32_t c = 0;
+#pragma unroll
+      for (int i = 0; i < kKeys; i++) c += key[i] >= mid;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if ((int)c >= k) {
         lo = mid;
-        if (c <= enough) break;
+        if ((int)c <= enough) break;
       } else {
         hi = mid - 1;
       }
     }
-  };
+    exact = lo == hi;
+  }
+  fin_sync();
   // entries of the groups that reach `from`, at least `from` themselves, into cand
   auto collect = [&](uint32_t from) {
-#pragma unroll
-    for (int q = 0; q < kGroupStages * (kCons / kFin); q++)
-      if (key[q] >= from) {
-        const int i = atomicAdd(&ss.n_groups, 1);
-        if (i < kMaxGroups) ts.group[i] = (uint16_t)(q * kFin + ft);
-      }
+    const float ff = order_value(from);
+    if (nvec > 0)
+      for (int t = ft; t < kCons; t += kFin)
+        if (ts.tmax[par][t] >= ff)
+          for (int j = 0; j < J; j++)
+            if (ts.gmax[par][j][t] >= ff) {
+              const int i = atomicAdd(&ss.n_groups, 1);
+              if (i < kMaxGroups) ts.group[i] = (uint16_t)(j * kCons + t);
+            }
     fin_sync();
     const int ng = ss.n_groups;
     if (ng > kMaxGroups) return false;
-    const int per = (p.ring.n_stages + J - 1) / J * kPer;   // most vectors of a group
-    for (int it = ft; it < ng * per; it += kFin) {
-      const int g = ts.group[it / per], sub = it % per;
-      const int jg = g / kCons, first = (jg * p.ring.n_stages + J - 1) / J, st = first + sub / kPer;
-      const int i = (sub % kPer) * kCons + g % kCons, at = st * p.ring.stage + i;
-      if (i >= p.ring.stage || at >= nvec || st * J / p.ring.n_stages != jg) continue;
-      const uint4 w = *reinterpret_cast<const uint4*>(row + (size_t)(v0 + at) * E);
-      float x[E];
-      VT::cvt(w, x);
-      uint32_t hit = 0;
+    constexpr int U = 4;
+    const int items = ng * kPer * spc;
+    for (int base = ft; base < items; base += U * kFin) {
+      uint4 w[U];
+      int at[U];
 #pragma unroll
-      for (int e = 0; e < E; e++) hit |= (uint32_t)(order_key(x[e]) >= from) << e;
-      if (!hit) continue;
-      int c = atomicAdd(&ss.n_cand, __popc(hit));
-      if (c > kMaxCand) break;   // too many: all of it is done again
+      for (int u = 0; u < U; u++) {
+        const int it = base + u * kFin;
+        at[u] = -1;
+        if (it >= items) continue;
+        const int gi = spc == 1 ? it / kPer : it / (kPer * spc), sub = it - gi * kPer * spc;
+        const int g = ts.group[gi], jg = g / kCons;
+        const int st = spc == 1 ? jg : (jg * n_st + J - 1) / J + sub / kPer;
+        const int i = (sub % kPer) * kCons + g % kCons;
+        if (i >= p.ring.stage || st * p.ring.stage + i >= nvec || (spc > 1 && st * J / n_st != jg)) continue;
+        at[u] = v0 + st * p.ring.stage + i;
+        w[u] = reinterpret_cast<const uint4*>(row)[at[u]];
+      }
 #pragma unroll
-      for (int e = 0; e < E; e++)
-        if (hit >> e & 1) {
-          if (c < kMaxCand) ts.cand[c] = cand_of(order_key(x[e]), (v0 + at) * E + e);
-          c++;
-        }
+      for (int u = 0; u < U; u++) {
+        if (at[u] < 0) continue;
+        float x[E];
+        VT::cvt(w[u], x);
+        uint32_t hit = 0;
+#pragma unroll
+        for (int e = 0; e < E; e++) hit |= (uint32_t)(x[e] >= ff) << e;
+        if (!hit) continue;
+        int c = atomicAdd(&ss.n_cand, __popc(hit));
+#pragma unroll
+        for (int e = 0; e < E; e++)
+          if (hit >> e & 1) {
+            if (c < kMaxCand) ts.cand[c] = cand_of(order_key(x[e]), at[u] * E + e);
+            c++;
+          }
+      }
+      if (ss.n_cand > kMaxCand) break;   // too many: all of it is done again
     }
-    if (ft < tail_n && order_key(tail_x) >= from) {
+    if (ft < tail_n && tail_x >= ff) {
       const int c = atomicAdd(&ss.n_cand, 1);
       if (c < kMaxCand) ts.cand[c] = cand_of(order_key(tail_x), p.V - tail_n + ft);
     }
     fin_sync();
     return ss.n_cand <= kMaxCand;
   };
+  int buf = 0;
   auto reset = [&] {
     fin_sync();
     if (ft == 0) ss.n_groups = ss.n_cand = ss.n_ties = 0;
     fin_sync();
   };
-  bisect(k + 8 + k / 4);
   if (lo <= order_key(-INFINITY) || !collect(lo)) {
     // Many entries reach tau, as with equal ones in most groups (masked rows, rounded
-    // logits).  With the exact tau fewer than k groups exceed it: take what exceeds tau, and
+    // logits).  With the exact tau fewer than k threads exceed it: take what exceeds tau, and
     // the entries equal to it in the order of their ids.
-    bisect(0);
+    while (!exact && lo < hi) {
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      uint32_t c = 0;
+      for (int i = 0; i < kKeys; i++) c += nvec > 0 && order_key(ts.tmax[par][i * 32 + lane]) >= mid;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if ((int)c >= k) lo = mid;
+      else hi = mid - 1;
+    }
     reset();
-    bool ok = lo == 0xffffffffu || collect(lo + 1);
-    if (!ok) {
-      // Those few groups alone hold more than kMaxCand entries above tau: find the part's
+    if (!collect(lo + 1)) {
+      // Those threads' groups alone hold more than kMaxCand entries above tau: find the part's
       // k-th largest entry by counting over the whole part.  Rare, and slow.
       uint32_t a = lo, b = 0xffffffffu;
       while (a < b) {
@@ -202,8 +219,7 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
 #pragma unroll
           for (int e = 0; e < E; e++) c += order_key(x[e]) >= mid;
         }
-        c = fin_reduce(__reduce_add_sync(0xffffffffu, c), ss.red, buf, 0, uadd);
-        buf ^= 1;
+        c = fin_sum(c, ss, buf);
         if ((int)c >= k) a = mid;
         else b = mid - 1;
       }
@@ -241,13 +257,13 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
         const int y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
       }
-      if (lane == 31) ss.red[buf][ft >> 5][0] = inc;
+      if (lane == 31) ss.red[buf][ft >> 5] = inc;
       fin_sync();
       int at = found + inc - mine, total = 0;
 #pragma unroll
       for (int w = 0; w < kFinWarps; w++) {
-        if (w < (ft >> 5)) at += ss.red[buf][w][0];
-        total += ss.red[buf][w][0];
+        if (w < (ft >> 5)) at += ss.red[buf][w];
+        total += ss.red[buf][w];
       }
       buf ^= 1;
       for (int e = 0; e < E; e++)
@@ -270,16 +286,44 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
       fin_sync();
     }
   }
-  // rank of each candidate by counting the better ones
-  const int n = ss.n_cand;
+  // rank of each candidate by counting the better ones; where there are many, first those
+  // below a lower bound of the k-th go, found by another bisection
+  int n = ss.n_cand;
+  const unsigned long long* from = ts.cand;
+  if (n > 2 * k + 64) {
+    uint32_t a = max(lo, 1u), b = 0xff800000u;   // the key of +inf
+    int left = n;
+    while (a < b && left > k + 32 + k / 4) {
+      const uint32_t mid = a + (b - a + 1) / 2;
+      uint32_t c = 0;
+      for (int i = ft; i < n; i += kFin) c += (uint32_t)(ts.cand[i] >> 32) >= mid;
+      c = fin_sum(c, ss, buf);
+      if ((int)c >= k) a = mid, left = c;
+      else b = mid - 1;
+    }
+    if (left <= kMaxTrim) {
+      if (ft == 0) ss.n_trim = 0;
+      fin_sync();
+      for (int i = ft; i < n; i += kFin)
+        if ((uint32_t)(ts.cand[i] >> 32) >= a) ts.trim[atomicAdd(&ss.n_trim, 1)] = ts.cand[i];
+      fin_sync();
+      n = left;
+      from = ts.trim;
+    }
+  }
   for (int c = ft; c < n; c += kFin) {
-    const unsigned long long mine = ts.cand[c];
+    const unsigned long long mine = from[c];
     int rank = 0;
-    for (int i = 0; i < n; i++) rank += ts.cand[i] > mine;
+#pragma unroll 4
+    for (int i = 0; i < n; i++) rank += from[i] > mine;
     if (rank < k) ts.sorted[rank] = mine;
   }
   fin_sync();
   return min(n, k);
+}
+
+__device__ __forceinline__ float log_prob(float x, float m, float ls, float c) {
+  return x == -INFINITY ? -INFINITY : (x - m) * c - ls;
 }
 
 template <typename T, bool kTop>
@@ -304,7 +348,45 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
   __syncthreads();
   if (rs.cs > 1) cluster_sync();
 
-  if (tid >= kCons + kFin) {
+  if (tid >= kCons + kFin + 32) {
+    // ---- look-ups: the tokens that the rows feed ----
+    if (rank == 0 && p.ids) {
+      SuccCursor cur;
+      for (int r = cluster, it = 0; r < p.n; r += n_clusters, it++) {
+        const int par = it & 1;
+        const T* row = logits + (size_t)r * p.ld;
+        int n = 0;
+        if (lane == 0) {
+          bool start;
+          n = cur.find(p.succ, p.row0 + r, ss.s_t, &start);
+          if (start) p.logp[p.row0 + r] = 0.f;
+        }
+        n = __shfl_sync(0xffffffffu, n, 0);
+        __syncwarp();
+        int t[kMaxSucc / 32];
+        float x[kMaxSucc / 32];
+        bool bad[kMaxSucc / 32];
+#pragma unroll
+        for (int q = 0; q < kMaxSucc / 32; q++) {
+          const int i = q * 32 + lane;
+          t[q] = -1;
+          if (i >= n) continue;
+          t[q] = ss.s_t[i];
+          const int id = p.ids[t[q]];
+          bad[q] = id < 0 || id >= p.V;
+          if (bad[q]) atomicExch(p.status, OCTO_EINVAL);
+          else x[q] = VT::get(row + id);
+        }
+        if (!warp_wait(&bar.scal_full[par], (it >> 1) & 1, p.status)) break;
+        const float m = ss.stat[par][0], ls = ss.stat[par][1];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar.scal_empty[par]);
+#pragma unroll
+        for (int q = 0; q < kMaxSucc / 32; q++)
+          if (t[q] >= 0) p.logp[t[q]] = bad[q] ? __int_as_float(0x7fc00000) : log_prob(x[q], m, ls, p.c);
+      }
+    }
+  } else if (tid >= kCons + kFin) {
     // ---- copies ----
     if (lane == 0) {
       RingPos pos;
@@ -337,7 +419,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
       const int par = it & 1;
       StageStat<T, true> st;
       st.init();
-      float gm = -INFINITY;
+      float gm = -INFINITY, tm = -INFINITY;
       // the finishers are done with this parity's buffers two rows ago
       if (kTop) ok = warp_wait(&bar.part_empty[par], ((it >> 1) & 1) ^ 1, p.status);
       for (int j = 0; j < rs.n_stages && ok; j++) {
@@ -355,24 +437,22 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
           }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
-          if (mx > st.m) st.rebase(mx, c2);
           gm = fmaxf(gm, mx);
-          const f2 negm = pack2(-st.m, -st.m), cc = pack2(c2, c2);
-#pragma unroll
-          for (int q = 0; q < kPer; q++)
-            if (q * kCons < cnt) st.add(w[q], negm, cc);
+          st.add(w, cnt, mx, c2);
           pos.next(rs.n_slots);
         }
         if (kTop) {
           const int jg = j * J / rs.n_stages;
           if (j + 1 == rs.n_stages || (j + 1) * J / rs.n_stages != jg) {
             ts.gmax[par][jg][tid] = gm;
+            tm = fmaxf(tm, gm);
             gm = -INFINITY;
           }
         }
       }
       if (!ok) break;
-      Stat tot = st.total();
+      if (kTop) ts.tmax[par][tid] = tm;
+      Stat tot = st.total(c2);
       warp_merge(tot, c2);
       if (!kTop) ok = warp_wait(&bar.part_empty[par], ((it >> 1) & 1) ^ 1, p.status);
       if (lane == 0) {
@@ -391,25 +471,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
       const int par = it & 1;
       const uint32_t ph = (it >> 1) & 1;
       const T* row = logits + (size_t)r * p.ld;
-      // what does not need the sums: successors, their logits, the row's last entries
-      if (rank == 0 && p.ids && ft == 0) {
-        bool start;
-        ss.n_succ[par] = p.succ.find(p.row0 + r, ss.s_t[par], &start);
-        if (start) p.logp[p.row0 + r] = 0.f;
-      }
       const float tail_x = ft < tail_n ? VT::get(row + nv * E + ft) : -INFINITY;
-      fin_sync();
-      int t = -1;
-      float xt = 0.f;
-      bool bad = false;
-      if (rank == 0 && p.ids && ft < ss.n_succ[par]) {
-        t = ss.s_t[par][ft];
-        const int id = p.ids[t];
-        bad = id < 0 || id >= p.V;
-        if (bad) atomicExch(p.status, OCTO_EINVAL);
-        else xt = VT::get(row + id);
-      }
-
       if (!(ok = fin_all(tc::mbar_wait(&bar.part_full[par], ph, p.status, OCTO_ETIMEOUT)))) break;
       Stat st;
       st.init();
@@ -450,18 +512,22 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
       }
       const bool empty = st.s == 0.f;
       const float m = empty ? -INFINITY : st.m, ls = empty ? -INFINITY : logf(st.s);
-      auto term = [&](float x) { return x == -INFINITY ? -INFINITY : (x - m) * p.c - ls; };
       if (ft == 0) {
         p.row_stat[2 * (size_t)r] = m;
         p.row_stat[2 * (size_t)r + 1] = ls;
         if (p.entropy) p.entropy[r] = empty ? 0.f : ls - kLn2 * (st.a / st.s);
+        if (p.ids) {
+          tc::mbar_wait(&bar.scal_empty[par], ph ^ 1, p.status, OCTO_ETIMEOUT);
+          ss.stat[par][0] = m;
+          ss.stat[par][1] = ls;
+          tc::mbar_arrive(&bar.scal_full[par]);
+        }
       }
-      if (t >= 0) p.logp[t] = bad ? __int_as_float(0x7fc00000) : term(xt);
       if (kTop) {
         const size_t o = (size_t)r * p.k;
         auto put = [&](int rk, unsigned long long e) {
           p.top_ids[o + rk] = (int32_t) ~(uint32_t)e;
-          p.top_logp[o + rk] = term(order_value((uint32_t)(e >> 32)));
+          p.top_logp[o + rk] = log_prob(order_value((uint32_t)(e >> 32)), m, ls, p.c);
         };
         int total = n_top;
         if (rs.cs == 1) {
