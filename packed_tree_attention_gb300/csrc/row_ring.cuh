@@ -5,7 +5,8 @@
 // the row's 16-byte vectors.  One thread copies the part, stage by stage, into the ring with
 // bulk copies (cp.async.bulk, completion on a slot's `full` barrier), running ahead over row
 // ends as far as the ring reaches; 16 consumer warps take a stage at a time, four vectors a
-// thread; 4 finisher warps do what a row needs besides, while the consumers are at the next.
+// thread; two teams of 4 finisher warps, one for every other row, do what a row needs besides,
+// while the consumers are at the next.
 // The copies bring whole vectors: the last V % E entries are the finishers'.
 #pragma once
 
@@ -15,13 +16,13 @@
 namespace octo {
 namespace rows {
 
-constexpr int kConsWarps = 16, kFinWarps = 4;
+constexpr int kConsWarps = 16, kFinWarps = 4, kTeams = 2;   // finisher warps of a team
 constexpr int kCons = kConsWarps * 32, kFin = kFinWarps * 32;
-constexpr int kBlock = kCons + kFin + 64;   // + the copying warp and one for look-ups
+constexpr int kBlock = kCons + kTeams * kFin + 64;   // + the copying warp and one for look-ups
 constexpr int kPer = 4;                     // vectors of one thread in a stage
 constexpr int kMaxSlots = 24;
 constexpr int kMaxCluster = 8;
-constexpr int kFinBar = 1;                  // named barrier of the finishers
+constexpr int kFinBar = 1;                  // named barriers of the finisher teams: this and the next
 static_assert(kFin >= kMaxTop, "a finisher thread for each teacher entry");
 
 struct RingShape {
@@ -38,7 +39,7 @@ inline RingShape ring_shape(int64_t nv, int cs, int bytes) {
   s.cs = cs;
   s.seg = (int32_t)((nv + cs - 1) / cs);
   s.n_stages = (s.seg + kCons * kPer - 1) / (kCons * kPer);
-  s.stage = s.n_stages ? ((s.seg + s.n_stages - 1) / s.n_stages + 31) / 32 * 32 : 32;
+  s.stage = s.n_stages > 1 ? kCons * kPer : s.n_stages ? (s.seg + 31) / 32 * 32 : 32;
   s.n_slots = bytes / (s.stage * 16);
   if (s.n_slots > kMaxSlots) s.n_slots = kMaxSlots;
   return s;
@@ -51,14 +52,45 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-__device__ __forceinline__ void fin_sync() { asm volatile("bar.sync %0, %1;" ::"n"(kFinBar), "n"(kFin) : "memory"); }
+__device__ __forceinline__ void fin_sync(int team) { asm volatile("bar.sync %0, %1;" ::"r"(kFinBar + team), "n"(kFin) : "memory"); }
 
+// Waits of these kernels: a poll suspends the thread for up to kPollNs (it wakes when the phase
+// completes), so that waiting warps leave the issue slots to the others; given up after
+// kPolls of them, several seconds.
+constexpr uint32_t kPollNs = 1000000, kPolls = 4000;
+template <bool kCluster = false>
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  const uint32_t a = tc::smem_u32(bar);
+#pragma unroll 1
+  for (uint32_t i = 0; i < kPolls; i++) {
+    uint32_t ok;
+    if (kCluster)   // what the peers stored before they arrived is visible after it
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(a), "r"(parity), "r"(kPollNs)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(a), "r"(parity), "r"(kPollNs)
+          : "memory");
+    if (ok) return true;
+  }
+  atomicExch(status, OCTO_ETIMEOUT);
+  return false;
+}
 // The waits below are uniform over the warp, and fin_all over the finishers: after a wait that
 // gave up, all of them leave together and none is left at a barrier.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status, OCTO_ETIMEOUT));
+  return __all_sync(0xffffffffu, ring_wait(bar, parity, status));
 }
-__device__ __forceinline__ bool fin_all(bool ok) {
+__device__ __forceinline__ bool fin_all(bool ok, int team) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -66,7 +98,7 @@ __device__ __forceinline__ bool fin_all(bool ok) {
       "bar.red.and.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(all)
-      : "r"((uint32_t)ok), "n"(kFinBar), "n"(kFin)
+      : "r"((uint32_t)ok), "r"(kFinBar + team), "n"(kFin)
       : "memory");
   return all != 0;
 }
@@ -94,23 +126,6 @@ __device__ __forceinline__ void st_remote(uint32_t a, unsigned long long v) {
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// mbar_wait with cluster scope (what the peers stored before arriving is visible after it)
-__device__ __forceinline__ bool cluster_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-  for (uint32_t i = 0; i < tc::kSpinLimit; i++) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(tc::smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
-  atomicExch(status, OCTO_ETIMEOUT);
-  return false;
-}
-
 // ---- two fp32 operations per instruction ----
 typedef unsigned long long f2;
 __device__ __forceinline__ f2 pack2(float a, float b) {
@@ -224,13 +239,12 @@ struct StageStat {
       if (kEntropy) a[i & 1] = fma2(e, t, a[i & 1]);
     }
   }
-  // the vectors w[q] with q * kCons < cnt, the largest entry of all kPer being mx
-  __device__ __forceinline__ void add(const uint4 (&w)[kPer], int cnt, float mx, float c2) {
+  // the vectors w, the largest entry of all kPer being mx
+  __device__ __forceinline__ void add(const uint4 (&w)[kPer], float mx, float c2) {
     if (mx > m) raise(mx, c2);
     if (usual(m, c2)) {
 #pragma unroll
-      for (int q = 0; q < kPer; q++)
-        if (q * kCons < cnt) add_vec<true>(w[q], c2);
+      for (int q = 0; q < kPer; q++) add_vec<true>(w[q], c2);
     } else {
 #pragma unroll
       for (int q = 0; q < kPer; q++) add_vec<false>(w[q], c2);
@@ -257,11 +271,31 @@ __device__ __forceinline__ void warp_merge(Stat& st, float c2) {
              __shfl_xor_sync(0xffffffffu, st.a, o), c2);
 }
 
+// A consumer thread's vectors of a slot that holds cnt of them (masked past the end), and the
+// largest entry.
+template <typename T>
+__device__ __forceinline__ float load_slot(const uint4* slot, int cnt, uint4 (&w)[kPer]) {
+  if (cnt == kPer * kCons) {
+#pragma unroll
+    for (int q = 0; q < kPer; q++) w[q] = slot[q * kCons + threadIdx.x];
+  } else {
+#pragma unroll
+    for (int q = 0; q < kPer; q++) {
+      const int i = q * kCons + threadIdx.x;
+      w[q] = i < cnt ? slot[i] : Raw<T>::masked();
+    }
+  }
+  float mx = Raw<T>::max(w[0]);
+#pragma unroll
+  for (int q = 1; q < kPer; q++) mx = fmaxf(mx, Raw<T>::max(w[q]));
+  return mx;
+}
+
 // The barriers of a CTA.
 struct RingBars {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t part_full[2], part_empty[2];   // a row's warp sums: written, read
-  uint64_t joined[2];                     // every CTA of the cluster sent its part of a row
+  uint64_t joined[2], freed[2];           // every CTA of the cluster sent its part of a row; that was read
   uint64_t scal_full[2], scal_empty[2];   // a row's results: written, read by who needs them
   uint64_t pre_full[2], p2_done[2];       // distillation
   __device__ void init(int cs) {
@@ -270,6 +304,7 @@ struct RingBars {
       tc::mbar_init(&part_full[i], kConsWarps);
       tc::mbar_init(&part_empty[i], kFinWarps);
       tc::mbar_init(&joined[i], cs);
+      tc::mbar_init(&freed[i], 1);
       tc::mbar_init(&pre_full[i], kFinWarps);
       tc::mbar_init(&scal_full[i], 1);
       tc::mbar_init(&scal_empty[i], 1);

@@ -17,7 +17,8 @@ namespace {
 using namespace rows;
 
 constexpr int kGroupStages = 10;     // stage classes of the group maxima
-constexpr int kMaxCand = 2048, kMaxGroups = 1024, kMaxTrim = 512;
+constexpr int kMaxCand = 1280, kMaxGroups = 512, kMaxTrim = 512;
+static_assert(kMaxCand >= kMaxCluster * kMaxTop, "the CTAs' alternatives are joined in cand");
 
 struct ScoreParams {
   const void* logits;
@@ -42,23 +43,24 @@ struct ScoreSmem {
   float in_stat[2][kMaxCluster][3];      // rank 0: the CTAs' sums
   float stat[2][2];                      // a row's (m, ln S), for the look-ups
   int32_t s_t[kMaxSucc];                 // successors of the row
-  uint32_t red[2][kFinWarps];
-  int32_t n_groups, n_cand, n_ties, n_trim;
 };
+// One of each for the two finisher teams.
 struct TopSmem {
-  unsigned long long in_list[2][kMaxCluster][kMaxTop];   // rank 0: the CTAs' alternatives, best first
-  int32_t in_count[2][kMaxCluster];
+  unsigned long long in_list[kMaxCluster][kMaxTop];   // rank 0: the CTAs' alternatives, best first
+  int32_t in_count[kMaxCluster];
   unsigned long long cand[kMaxCand];
   unsigned long long trim[kMaxTrim];
   unsigned long long sorted[kMaxTop];
   uint16_t group[kMaxGroups];
-  float gmax[2][kGroupStages][kCons];    // largest entry of each group: a thread's vectors in a class of stages
-  float tmax[2][kCons];                  // and of each thread
+  uint32_t red[2][kFinWarps];
+  int32_t n_groups, n_cand, n_ties, n_trim;
+  float gmax[kGroupStages][kCons];       // largest entry of each group: a thread's vectors in a class of stages
+  float tmax[kCons];                     // and of each thread
 };
 
 template <bool kTop>
 __host__ __device__ constexpr int ring_offset() {
-  return (((int)sizeof(ScoreSmem) + 15) / 16 * 16 + (kTop ? (int)sizeof(TopSmem) : 0) + 127) / 128 * 128;
+  return (((int)sizeof(ScoreSmem) + 15) / 16 * 16 + (kTop ? kTeams * (int)sizeof(TopSmem) : 0) + 127) / 128 * 128;
 }
 
 // An alternative: the value's key above the complement of its id, so that among equal values
@@ -67,16 +69,72 @@ __device__ __forceinline__ unsigned long long cand_of(uint32_t key, int32_t v) {
   return ((unsigned long long)key << 32) | (uint32_t)~v;
 }
 
+__device__ __forceinline__ int fin_thread(int team) { return (int)threadIdx.x - kCons - team * kFin; }
+
 // Sum over the finishers; red is used alternately (buf) so that one barrier is enough.
-__device__ __forceinline__ uint32_t fin_sum(uint32_t v, ScoreSmem& ss, int& buf) {
+__device__ __forceinline__ uint32_t fin_sum(uint32_t v, TopSmem& ts, int team, int& buf) {
   v = __reduce_add_sync(0xffffffffu, v);
-  if ((threadIdx.x & 31) == 0) ss.red[buf][((int)threadIdx.x - kCons) >> 5] = v;
-  fin_sync();
+  if ((threadIdx.x & 31) == 0) ts.red[buf][fin_thread(team) >> 5] = v;
+  fin_sync(team);
   uint32_t r = 0;
 #pragma unroll
-  for (int i = 0; i < kFinWarps; i++) r += ss.red[buf][i];
+  for (int i = 0; i < kFinWarps; i++) r += ts.red[buf][i];
   buf ^= 1;
   return r;
+}
+
+// The k best of the n_cand candidates into ts.sorted, best first; returns how many.  At least
+// k of them (or all) reach the key `lo`.  A candidate's rank is counted; where there are many,
+// those below a lower bound of the k-th go first, found by a bisection.
+__device__ int rank_cand(TopSmem& ts, int team, int k, uint32_t lo, int& buf) {
+  const int ft = fin_thread(team);
+  int n = ts.n_cand;
+  const unsigned long long* from = ts.cand;
+  if (n > 2 * kFin) {
+    uint32_t hi = 0;
+    for (int i = ft; i < n; i += kFin) hi = max(hi, (uint32_t)(ts.cand[i] >> 32));
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if ((ft & 31) == 0) ts.red[buf][ft >> 5] = hi;
+    if (ft == 0) ts.n_trim = 0;
+    fin_sync(team);
+#pragma unroll
+    for (int i = 0; i < kFinWarps; i++) hi = max(hi, ts.red[buf][i]);
+    buf ^= 1;
+    int left = n;
+    while (lo < hi && left > k + 32 + k / 4) {
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      uint32_t c = 0;
+      for (int i = ft; i < n; i += kFin) c += (uint32_t)(ts.cand[i] >> 32) >= mid;
+      c = fin_sum(c, ts, team, buf);
+      if ((int)c >= k) lo = mid, left = c;
+      else hi = mid - 1;
+    }
+    for (int i = ft; i < n; i += kFin)
+      if ((uint32_t)(ts.cand[i] >> 32) >= lo) {
+        const int at = atomicAdd(&ts.n_trim, 1);
+        if (at < kMaxTrim) ts.trim[at] = ts.cand[i];
+      }
+    fin_sync(team);
+    if (ts.n_trim <= kMaxTrim) {
+      n = ts.n_trim;
+      from = ts.trim;
+    }
+  }
+  for (int c = ft; c < n; c += 2 * kFin) {
+    const bool two = c + kFin < n;
+    const unsigned long long x = from[c], y = two ? from[c + kFin] : 0;
+    int rx = 0, ry = 0;
+#pragma unroll 8
+    for (int i = 0; i < n; i++) {
+      const unsigned long long o = from[i];
+      rx += o > x;
+      ry += o > y;
+    }
+    if (rx < k) ts.sorted[rx] = x;
+    if (two && ry < k) ts.sorted[ry] = y;
+  }
+  fin_sync(team);
+  return min(n, k);
 }
 
 // The k largest entries of a CTA's part of a row, best first, in ts.sorted; returns how many
@@ -89,15 +147,15 @@ __device__ __forceinline__ uint32_t fin_sum(uint32_t v, ScoreSmem& ss, int& buf)
 // entries.  Every warp finds tau for itself, 16 maxima a lane, by a bisection over the keys
 // that stops at a few threads more than k.
 template <typename T>
-__device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSmem& ts, int par, int v0, int nvec, int tail_n,
+__device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, int team, int v0, int nvec, int tail_n,
                         float tail_x) {
   using VT = Vec<T>;
   constexpr int E = VT::E, kKeys = kCons / 32;
-  const int ft = threadIdx.x - kCons, lane = threadIdx.x & 31;
+  const int ft = fin_thread(team), lane = threadIdx.x & 31;
   const int k = p.k;
   const int n_st = p.ring.n_stages, J = min(n_st, kGroupStages);
   const int spc = n_st > kGroupStages ? (n_st + J - 1) / J : 1;   // most stages of a group
-  if (ft == 0) ss.n_groups = ss.n_cand = 0;
+  if (ft == 0) ts.n_groups = ts.n_cand = 0;
   uint32_t lo, hi;
   bool exact = false;
   {
@@ -105,7 +163,7 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
     uint32_t mn = 0xffffffffu, mx = 0;
 #pragma unroll
     for (int i = 0; i < kKeys; i++) {
-      key[i] = nvec > 0 ? order_key(ts.tmax[par][i * 32 + lane]) : order_key(-INFINITY);
+      key[i] = nvec > 0 ? order_key(ts.tmax[i * 32 + lane]) : order_key(-INFINITY);
       mn = min(mn, key[i]);
       mx = max(mx, key[i]);
     }
@@ -115,10 +173,10 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
     const int enough = k + 8 + k / 4;
     while (lo < hi) {
       const uint32_t mid = lo + (hi - lo + 1) / 2;
-      uint32_t c = 0;
+      uint32_t cs[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < kKeys; i++) c += key[i] >= mid;
-      c = __reduce_add_sync(0xffffffffu, c);
+      for (int i = 0; i < kKeys; i++) cs[i & 3] += key[i] >= mid;
+      const uint32_t c = __reduce_add_sync(0xffffffffu, (cs[0] + cs[1]) + (cs[2] + cs[3]));
       if ((int)c >= k) {
         lo = mid;
         if ((int)c <= enough) break;
@@ -128,20 +186,23 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
     }
     exact = lo == hi;
   }
-  fin_sync();
+  fin_sync(team);
   // entries of the groups that reach `from`, at least `from` themselves, into cand
   auto collect = [&](uint32_t from) {
     const float ff = order_value(from);
     if (nvec > 0)
+#pragma unroll
       for (int t = ft; t < kCons; t += kFin)
-        if (ts.tmax[par][t] >= ff)
-          for (int j = 0; j < J; j++)
-            if (ts.gmax[par][j][t] >= ff) {
-              const int i = atomicAdd(&ss.n_groups, 1);
-              if (i < kMaxGroups) ts.group[i] = (uint16_t)(j * kCons + t);
-            }
-    fin_sync();
-    const int ng = ss.n_groups;
+        if (ts.tmax[t] >= ff) {
+          uint32_t hit = 0;
+#pragma unroll
+          for (int j = 0; j < kGroupStages; j++) hit |= (uint32_t)(j < J && ts.gmax[j][t] >= ff) << j;
+          int i = atomicAdd(&ts.n_groups, __popc(hit));
+          for (; hit; hit &= hit - 1, i++)
+            if (i < kMaxGroups) ts.group[i] = (uint16_t)((__ffs(hit) - 1) * kCons + t);
+        }
+    fin_sync(team);
+    const int ng = ts.n_groups;
     if (ng > kMaxGroups) return false;
     constexpr int U = 4;
     const int items = ng * kPer * spc;
@@ -170,7 +231,7 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
 #pragma unroll
         for (int e = 0; e < E; e++) hit |= (uint32_t)(x[e] >= ff) << e;
         if (!hit) continue;
-        int c = atomicAdd(&ss.n_cand, __popc(hit));
+        int c = atomicAdd(&ts.n_cand, __popc(hit));
 #pragma unroll
         for (int e = 0; e < E; e++)
           if (hit >> e & 1) {
@@ -178,20 +239,20 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
             c++;
           }
       }
-      if (ss.n_cand > kMaxCand) break;   // too many: all of it is done again
+      if (ts.n_cand > kMaxCand) break;   // too many: all of it is done again
     }
     if (ft < tail_n && tail_x >= ff) {
-      const int c = atomicAdd(&ss.n_cand, 1);
+      const int c = atomicAdd(&ts.n_cand, 1);
       if (c < kMaxCand) ts.cand[c] = cand_of(order_key(tail_x), p.V - tail_n + ft);
     }
-    fin_sync();
-    return ss.n_cand <= kMaxCand;
+    fin_sync(team);
+    return ts.n_cand <= kMaxCand;
   };
   int buf = 0;
   auto reset = [&] {
-    fin_sync();
-    if (ft == 0) ss.n_groups = ss.n_cand = ss.n_ties = 0;
-    fin_sync();
+    fin_sync(team);
+    if (ft == 0) ts.n_groups = ts.n_cand = ts.n_ties = 0;
+    fin_sync(team);
   };
   if (lo <= order_key(-INFINITY) || !collect(lo)) {
     // Many entries reach tau, as with equal ones in most groups (masked rows, rounded
@@ -200,7 +261,7 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
     while (!exact && lo < hi) {
       const uint32_t mid = lo + (hi - lo + 1) / 2;
       uint32_t c = 0;
-      for (int i = 0; i < kKeys; i++) c += nvec > 0 && order_key(ts.tmax[par][i * 32 + lane]) >= mid;
+      for (int i = 0; i < kKeys; i++) c += nvec > 0 && order_key(ts.tmax[i * 32 + lane]) >= mid;
       c = __reduce_add_sync(0xffffffffu, c);
       if ((int)c >= k) lo = mid;
       else hi = mid - 1;
@@ -219,7 +280,7 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
 #pragma unroll
           for (int e = 0; e < E; e++) c += order_key(x[e]) >= mid;
         }
-        c = fin_sum(c, ss, buf);
+        c = fin_sum(c, ts, team, buf);
         if ((int)c >= k) a = mid;
         else b = mid - 1;
       }
@@ -231,14 +292,14 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
 #pragma unroll
         for (int e = 0; e < E; e++) {
           const uint32_t kx = order_key(x[e]);
-          if (kx > lo) ts.cand[atomicAdd(&ss.n_cand, 1)] = cand_of(kx, (v0 + i) * E + e);
+          if (kx > lo) ts.cand[atomicAdd(&ts.n_cand, 1)] = cand_of(kx, (v0 + i) * E + e);
         }
       }
       if (ft < tail_n && order_key(tail_x) > lo)
-        ts.cand[atomicAdd(&ss.n_cand, 1)] = cand_of(order_key(tail_x), p.V - tail_n + ft);
-      fin_sync();
+        ts.cand[atomicAdd(&ts.n_cand, 1)] = cand_of(order_key(tail_x), p.V - tail_n + ft);
+      fin_sync(team);
     }
-    const int above = ss.n_cand;
+    const int above = ts.n_cand;
     // ties by id: 128 vectors at a time, then the last entries, until there are enough
     int found = 0;
     for (int base = 0; base < nvec + 1 && above + found < k; base += kFin) {
@@ -257,13 +318,13 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
         const int y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
       }
-      if (lane == 31) ss.red[buf][ft >> 5] = inc;
-      fin_sync();
+      if (lane == 31) ts.red[buf][ft >> 5] = inc;
+      fin_sync(team);
       int at = found + inc - mine, total = 0;
 #pragma unroll
       for (int w = 0; w < kFinWarps; w++) {
-        if (w < (ft >> 5)) at += ss.red[buf][w];
-        total += ss.red[buf][w];
+        if (w < (ft >> 5)) at += ts.red[buf][w];
+        total += ts.red[buf][w];
       }
       buf ^= 1;
       for (int e = 0; e < E; e++)
@@ -278,48 +339,15 @@ __device__ int part_top(const T* row, const ScoreParams& p, ScoreSmem& ss, TopSm
       const uint32_t who = __ballot_sync(0xffffffffu, hit);
       const int at = above + found + __popc(who & ((1u << lane) - 1));
       if (hit && at < k) ts.cand[at] = cand_of(lo, p.V - tail_n + ft);
-      if (ft == 0) ss.n_ties = found + __popc(who);
+      if (ft == 0) ts.n_ties = found + __popc(who);
     }
-    fin_sync();
+    fin_sync(team);
     if (above < k) {
-      if (ft == 0) ss.n_cand = min(above + ss.n_ties, k);
-      fin_sync();
+      if (ft == 0) ts.n_cand = min(above + ts.n_ties, k);
+      fin_sync(team);
     }
   }
-  // rank of each candidate by counting the better ones; where there are many, first those
-  // below a lower bound of the k-th go, found by another bisection
-  int n = ss.n_cand;
-  const unsigned long long* from = ts.cand;
-  if (n > 2 * k + 64) {
-    uint32_t a = max(lo, 1u), b = 0xff800000u;   // the key of +inf
-    int left = n;
-    while (a < b && left > k + 32 + k / 4) {
-      const uint32_t mid = a + (b - a + 1) / 2;
-      uint32_t c = 0;
-      for (int i = ft; i < n; i += kFin) c += (uint32_t)(ts.cand[i] >> 32) >= mid;
-      c = fin_sum(c, ss, buf);
-      if ((int)c >= k) a = mid, left = c;
-      else b = mid - 1;
-    }
-    if (left <= kMaxTrim) {
-      if (ft == 0) ss.n_trim = 0;
-      fin_sync();
-      for (int i = ft; i < n; i += kFin)
-        if ((uint32_t)(ts.cand[i] >> 32) >= a) ts.trim[atomicAdd(&ss.n_trim, 1)] = ts.cand[i];
-      fin_sync();
-      n = left;
-      from = ts.trim;
-    }
-  }
-  for (int c = ft; c < n; c += kFin) {
-    const unsigned long long mine = from[c];
-    int rank = 0;
-#pragma unroll 4
-    for (int i = 0; i < n; i++) rank += from[i] > mine;
-    if (rank < k) ts.sorted[rank] = mine;
-  }
-  fin_sync();
-  return min(n, k);
+  return rank_cand(ts, team, k, lo, buf);
 }
 
 __device__ __forceinline__ float log_prob(float x, float m, float ls, float c) {
@@ -332,7 +360,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
   constexpr int E = VT::E;
   extern __shared__ __align__(128) uint8_t smem[];
   ScoreSmem& ss = *reinterpret_cast<ScoreSmem*>(smem);
-  TopSmem& ts = *reinterpret_cast<TopSmem*>(smem + (sizeof(ScoreSmem) + 15) / 16 * 16);
+  TopSmem* const top = reinterpret_cast<TopSmem*>(smem + (sizeof(ScoreSmem) + 15) / 16 * 16);
   uint4* const slots = reinterpret_cast<uint4*>(smem + ring_offset<kTop>());
   RingBars& bar = ss.bars;
   const RingShape rs = p.ring;
@@ -348,7 +376,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
   __syncthreads();
   if (rs.cs > 1) cluster_sync();
 
-  if (tid >= kCons + kFin + 32) {
+  if (tid >= kCons + kTeams * kFin + 32) {
     // ---- look-ups: the tokens that the rows feed ----
     if (rank == 0 && p.ids) {
       SuccCursor cur;
@@ -386,7 +414,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
           if (t[q] >= 0) p.logp[t[q]] = bad[q] ? __int_as_float(0x7fc00000) : log_prob(x[q], m, ls, p.c);
       }
     }
-  } else if (tid >= kCons + kFin) {
+  } else if (tid >= kCons + kTeams * kFin) {
     // ---- copies ----
     if (lane == 0) {
       RingPos pos;
@@ -395,7 +423,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
       for (int r = cluster; r < p.n && ok; r += n_clusters) {
         const T* src = logits + (size_t)r * p.ld + (size_t)v0 * E;
         for (int b = 0; b < nvec; b += rs.stage) {
-          if (!(ok = tc::mbar_wait(&bar.empty[pos.slot], pos.round ^ 1, p.status, OCTO_ETIMEOUT))) break;
+          if (!(ok = ring_wait(&bar.empty[pos.slot], pos.round ^ 1, p.status))) break;
           const uint32_t bytes = (uint32_t)min(rs.stage, nvec - b) * 16;
           tc::mbar_expect_tx(&bar.full[pos.slot], bytes);
           bulk_load(slots + (size_t)pos.slot * rs.stage, src + (size_t)b * E, bytes, &bar.full[pos.slot]);
@@ -407,7 +435,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
       if (!ok)
         for (int i = min(issued, rs.n_slots); i > 0; i--) {
           if (--pos.slot < 0) pos.slot = rs.n_slots - 1, pos.round ^= 1;
-          tc::mbar_wait(&bar.full[pos.slot], pos.round, p.status, OCTO_ETIMEOUT);
+          ring_wait(&bar.full[pos.slot], pos.round, p.status);
         }
     }
   } else if (tid < kCons) {
@@ -428,30 +456,24 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
           if (!(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) break;
           const uint4* slot = slots + (size_t)pos.slot * rs.stage;
           uint4 w[kPer];
-          float mx = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < kPer; q++) {
-            const int i = q * kCons + tid;
-            w[q] = i < cnt ? slot[i] : Raw<T>::masked();
-            mx = fmaxf(mx, Raw<T>::max(w[q]));
-          }
+          const float mx = load_slot<T>(slot, cnt, w);
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
           gm = fmaxf(gm, mx);
-          st.add(w, cnt, mx, c2);
+          st.add(w, mx, c2);
           pos.next(rs.n_slots);
         }
         if (kTop) {
           const int jg = j * J / rs.n_stages;
           if (j + 1 == rs.n_stages || (j + 1) * J / rs.n_stages != jg) {
-            ts.gmax[par][jg][tid] = gm;
+            top[par].gmax[jg][tid] = gm;
             tm = fmaxf(tm, gm);
             gm = -INFINITY;
           }
         }
       }
       if (!ok) break;
-      if (kTop) ts.tmax[par][tid] = tm;
+      if (kTop) top[par].tmax[tid] = tm;
       Stat tot = st.total(c2);
       warp_merge(tot, c2);
       if (!kTop) ok = warp_wait(&bar.part_empty[par], ((it >> 1) & 1) ^ 1, p.status);
@@ -463,16 +485,15 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
       if (lane == 0) tc::mbar_arrive(&bar.part_full[par]);
     }
   } else {
-    // ---- finishers ----
-    const int ft = tid - kCons;
+    // ---- finishers: team `par` takes the rows of that parity ----
+    const int par = (tid - kCons) / kFin, ft = fin_thread(par);
+    TopSmem& ts = top[par];
     const int tail_n = rank + 1 == (uint32_t)rs.cs ? p.V - nv * E : 0;
-    bool ok = true;
-    for (int r = cluster, it = 0; r < p.n && ok; r += n_clusters, it++) {
-      const int par = it & 1;
+    for (int r = cluster + par * n_clusters, it = par; r < p.n; r += 2 * n_clusters, it += 2) {
       const uint32_t ph = (it >> 1) & 1;
       const T* row = logits + (size_t)r * p.ld;
       const float tail_x = ft < tail_n ? VT::get(row + nv * E + ft) : -INFINITY;
-      if (!(ok = fin_all(tc::mbar_wait(&bar.part_full[par], ph, p.status, OCTO_ETIMEOUT)))) break;
+      if (!fin_all(ring_wait(&bar.part_full[par], ph, p.status), par)) break;
       Stat st;
       st.init();
       if (lane < kConsWarps) {
@@ -485,15 +506,15 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
       }
       warp_merge(st, c2);
       int n_top = 0;
-      if (kTop) n_top = part_top<T>(row, p, ss, ts, par, v0, nvec, tail_n, tail_x);
+      if (kTop) n_top = part_top<T>(row, p, ts, par, v0, nvec, tail_n, tail_x);
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bar.part_empty[par]);
 
       if (rs.cs > 1) {
-        // to rank 0, and an arrival to every rank: a rank sends row i + 2 only after it has
-        // all arrivals of row i + 1, so rank 0 is done with row i
+        // to rank 0, once it has read what this rank sent two rows ago
+        if (!fin_all(ring_wait<true>(&bar.freed[par], ph ^ 1, p.status), par)) break;
         if (kTop) {
-          const uint32_t dst = map_rank(tc::smem_u32(ts.in_list[par][rank]), 0);
+          const uint32_t dst = map_rank(tc::smem_u32(ts.in_list[rank]), 0);
           if (ft < n_top) st_remote(dst + 8 * ft, ts.sorted[ft]);
         }
         if (ft == 0) {
@@ -501,14 +522,29 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
           st_remote(dst, st.m);
           st_remote(dst + 4, st.s);
           st_remote(dst + 8, st.a);
-          if (kTop) st_remote(map_rank(tc::smem_u32(&ts.in_count[par][rank]), 0), __int_as_float(n_top));
+          if (kTop) st_remote(map_rank(tc::smem_u32(&ts.in_count[rank]), 0), __int_as_float(n_top));
         }
-        fin_sync();
-        if (ft < rs.cs) arrive_remote(map_rank(tc::smem_u32(&bar.joined[par]), ft));
-        if (!(ok = fin_all(cluster_wait(&bar.joined[par], ph, p.status)))) break;
+        fin_sync(par);
+        if (ft == 0) arrive_remote(map_rank(tc::smem_u32(&bar.joined[par]), 0));
         if (rank != 0) continue;
+        if (!fin_all(ring_wait<true>(&bar.joined[par], ph, p.status), par)) break;
+        uint32_t bound = 1;   // the k-th best of any full list is a lower bound of the row's
         st.init();
         for (int q = 0; q < rs.cs; q++) st.merge(ss.in_stat[par][q][0], ss.in_stat[par][q][1], ss.in_stat[par][q][2], c2);
+        if (kTop) {
+          int at = ft;
+          for (int q = 0; q < rs.cs; q++) {
+            const int cnt = ts.in_count[q];
+            if (ft < cnt) ts.cand[at] = ts.in_list[q][ft];
+            if (cnt == p.k) bound = max(bound, (uint32_t)(ts.in_list[q][cnt - 1] >> 32));
+            at += cnt;
+          }
+          if (ft == 0) ts.n_cand = at;
+        }
+        fin_sync(par);
+        if (ft < rs.cs) arrive_remote(map_rank(tc::smem_u32(&bar.freed[par]), ft));
+        int buf = 0;
+        if (kTop) n_top = rank_cand(ts, par, p.k, bound, buf);
       }
       const bool empty = st.s == 0.f;
       const float m = empty ? -INFINITY : st.m, ls = empty ? -INFINITY : logf(st.s);
@@ -517,46 +553,17 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
         p.row_stat[2 * (size_t)r + 1] = ls;
         if (p.entropy) p.entropy[r] = empty ? 0.f : ls - kLn2 * (st.a / st.s);
         if (p.ids) {
-          tc::mbar_wait(&bar.scal_empty[par], ph ^ 1, p.status, OCTO_ETIMEOUT);
+          ring_wait(&bar.scal_empty[par], ph ^ 1, p.status);
           ss.stat[par][0] = m;
           ss.stat[par][1] = ls;
           tc::mbar_arrive(&bar.scal_full[par]);
         }
       }
-      if (kTop) {
-        const size_t o = (size_t)r * p.k;
-        auto put = [&](int rk, unsigned long long e) {
-          p.top_ids[o + rk] = (int32_t) ~(uint32_t)e;
-          p.top_logp[o + rk] = log_prob(order_value((uint32_t)(e >> 32)), m, ls, p.c);
-        };
-        int total = n_top;
-        if (rs.cs == 1) {
-          if (ft < n_top) put(ft, ts.sorted[ft]);
-        } else {
-          // an entry's rank: its place in its own list, and the better entries of the others
-          total = 0;
-          for (int q = 0; q < rs.cs; q++) total += ts.in_count[par][q];
-          for (int q = 0; q < rs.cs; q++) {
-            if (ft >= ts.in_count[par][q]) continue;
-            const unsigned long long e = ts.in_list[par][q][ft];
-            int rk = ft;
-            for (int o2 = 0; o2 < rs.cs && rk < p.k; o2++) {
-              if (o2 == q) continue;
-              int a = 0, b = ts.in_count[par][o2];   // entries [0, a) are better
-              while (a < b) {
-                const int mid = (a + b) >> 1;
-                if (ts.in_list[par][o2][mid] > e) a = mid + 1;
-                else b = mid;
-              }
-              rk += a;
-            }
-            if (rk < p.k) put(rk, e);
-          }
-        }
-        if (ft >= total && ft < p.k) {
-          p.top_ids[o + ft] = -1;
-          p.top_logp[o + ft] = __int_as_float(0x7fc00000);
-        }
+      if (kTop && ft < p.k) {
+        const unsigned long long e = ft < n_top ? ts.sorted[ft] : 0;
+        const size_t o = (size_t)r * p.k + ft;
+        p.top_ids[o] = ft < n_top ? (int32_t) ~(uint32_t)e : -1;
+        p.top_logp[o] = ft < n_top ? log_prob(order_value((uint32_t)(e >> 32)), m, ls, p.c) : __int_as_float(0x7fc00000);
       }
     }
   }
