@@ -239,12 +239,18 @@ struct StageStat {
       if (kEntropy) a[i & 1] = fma2(e, t, a[i & 1]);
     }
   }
-  // the vectors w, the largest entry of all kPer being mx
-  __device__ __forceinline__ void add(const uint4 (&w)[kPer], float mx, float c2) {
+  // the vectors w[q] with q * kCons < cnt, the largest entry of all kPer being mx
+  __device__ __forceinline__ void add(const uint4 (&w)[kPer], int cnt, float mx, float c2) {
     if (mx > m) raise(mx, c2);
     if (usual(m, c2)) {
+      if (cnt > (kPer - 1) * kCons) {
 #pragma unroll
-      for (int q = 0; q < kPer; q++) add_vec<true>(w[q], c2);
+        for (int q = 0; q < kPer; q++) add_vec<true>(w[q], c2);
+      } else {
+#pragma unroll
+        for (int q = 0; q < kPer - 1; q++)
+          if (q * kCons < cnt) add_vec<true>(w[q], c2);
+      }
     } else {
 #pragma unroll
       for (int q = 0; q < kPer; q++) add_vec<false>(w[q], c2);
@@ -264,11 +270,17 @@ struct StageStat {
   }
 };
 
+// Merges the lanes' statistics, every lane gets the warp's: the common reference first, so
+// that each lane moves to it once and the sums are plain additions, in a fixed order.
 __device__ __forceinline__ void warp_merge(Stat& st, float c2) {
+  float mn;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mn) : "f"(st.m));
+  st.rebase(mn, c2);
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
-    st.merge(__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-             __shfl_xor_sync(0xffffffffu, st.a, o), c2);
+  for (int o = 16; o; o >>= 1) {
+    st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
+    st.a += __shfl_xor_sync(0xffffffffu, st.a, o);
+  }
 }
 
 // A consumer thread's vectors of a slot that holds cnt of them (masked past the end), and the

@@ -145,10 +145,11 @@ __device__ int rank_cand(TopSmem& ts, int team, int k, uint32_t lo, int& buf) {
 // k-th largest entry, so only groups that reach tau are read again (from L2): for entries in
 // no order about 512 ln(512 / (512 - k)) groups, 21 for k = 20 and 147 for k = 128, of 16 to 32
 // entries.  Every warp finds tau for itself, 16 maxima a lane, by a bisection over the keys
-// that stops at a few threads more than k.
+// that stops at a few threads more than k.  Arrives on `read` when the maxima are read, well
+// before the end.
 template <typename T>
-__device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, int team, int v0, int nvec, int tail_n,
-                        float tail_x) {
+__device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, uint64_t* read, int team, int v0, int nvec,
+                        int tail_n, float tail_x) {
   using VT = Vec<T>;
   constexpr int E = VT::E, kKeys = kCons / 32;
   const int ft = fin_thread(team), lane = threadIdx.x & 31;
@@ -187,8 +188,8 @@ __device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, int tea
     exact = lo == hi;
   }
   fin_sync(team);
-  // entries of the groups that reach `from`, at least `from` themselves, into cand
-  auto collect = [&](uint32_t from) {
+  // groups that reach `from`
+  auto find_groups = [&](uint32_t from) {
     const float ff = order_value(from);
     if (nvec > 0)
 #pragma unroll
@@ -202,8 +203,16 @@ __device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, int tea
             if (i < kMaxGroups) ts.group[i] = (uint16_t)((__ffs(hit) - 1) * kCons + t);
         }
     fin_sync(team);
+    return ts.n_groups <= kMaxGroups;
+  };
+  auto release = [&] {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(read);
+  };
+  // their entries of at least `from`, into cand
+  auto collect = [&](uint32_t from) {
+    const float ff = order_value(from);
     const int ng = ts.n_groups;
-    if (ng > kMaxGroups) return false;
     constexpr int U = 4;
     const int items = ng * kPer * spc;
     for (int base = ft; base < items; base += U * kFin) {
@@ -254,8 +263,13 @@ __device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, int tea
     if (ft == 0) ts.n_groups = ts.n_cand = ts.n_ties = 0;
     fin_sync(team);
   };
-  if (lo <= order_key(-INFINITY) || !collect(lo)) {
-    // Many entries reach tau, as with equal ones in most groups (masked rows, rounded
+  bool slow;
+  if (lo > order_key(-INFINITY) && find_groups(lo)) {
+    release();
+    if (collect(lo)) return rank_cand(ts, team, k, lo, buf);
+    slow = true;
+  } else {
+    // Most groups reach tau, as with equal entries in all of them (masked rows, rounded
     // logits).  With the exact tau fewer than k threads exceed it: take what exceeds tau, and
     // the entries equal to it in the order of their ids.
     while (!exact && lo < hi) {
@@ -267,85 +281,88 @@ __device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, int tea
       else hi = mid - 1;
     }
     reset();
-    if (!collect(lo + 1)) {
-      // Those threads' groups alone hold more than kMaxCand entries above tau: find the part's
-      // k-th largest entry by counting over the whole part.  Rare, and slow.
-      uint32_t a = lo, b = 0xffffffffu;
-      while (a < b) {
-        const uint32_t mid = a + (b - a) / 2 + ((b - a) & 1);
-        uint32_t c = ft < tail_n && order_key(tail_x) >= mid;
-        for (int i = ft; i < nvec; i += kFin) {
-          float x[E];
-          VT::cvt(*reinterpret_cast<const uint4*>(row + (size_t)(v0 + i) * E), x);
-#pragma unroll
-          for (int e = 0; e < E; e++) c += order_key(x[e]) >= mid;
-        }
-        c = fin_sum(c, ts, team, buf);
-        if ((int)c >= k) a = mid;
-        else b = mid - 1;
-      }
-      lo = a;   // fewer than k entries exceed it
-      reset();
+    slow = !find_groups(lo + 1);
+    release();
+    slow = slow || !collect(lo + 1);
+  }
+  if (slow) {
+    // Few groups hold more than kMaxCand entries above tau: find the part's k-th largest
+    // entry by counting over the whole part.  Rare, and slow.
+    uint32_t a = lo, b = 0xffffffffu;
+    while (a < b) {
+      const uint32_t mid = a + (b - a) / 2 + ((b - a) & 1);
+      uint32_t c = ft < tail_n && order_key(tail_x) >= mid;
       for (int i = ft; i < nvec; i += kFin) {
         float x[E];
         VT::cvt(*reinterpret_cast<const uint4*>(row + (size_t)(v0 + i) * E), x);
 #pragma unroll
-        for (int e = 0; e < E; e++) {
-          const uint32_t kx = order_key(x[e]);
-          if (kx > lo) ts.cand[atomicAdd(&ts.n_cand, 1)] = cand_of(kx, (v0 + i) * E + e);
-        }
+        for (int e = 0; e < E; e++) c += order_key(x[e]) >= mid;
       }
-      if (ft < tail_n && order_key(tail_x) > lo)
-        ts.cand[atomicAdd(&ts.n_cand, 1)] = cand_of(order_key(tail_x), p.V - tail_n + ft);
-      fin_sync(team);
+      c = fin_sum(c, ts, team, buf);
+      if ((int)c >= k) a = mid;
+      else b = mid - 1;
     }
-    const int above = ts.n_cand;
-    // ties by id: 128 vectors at a time, then the last entries, until there are enough
-    int found = 0;
-    for (int base = 0; base < nvec + 1 && above + found < k; base += kFin) {
-      uint32_t hit = 0;
-      const int i = base + ft;
-      if (i < nvec) {
-        float x[E];
-        VT::cvt(*reinterpret_cast<const uint4*>(row + (size_t)(v0 + i) * E), x);
+    lo = a;   // fewer than k entries exceed it
+    reset();
+    for (int i = ft; i < nvec; i += kFin) {
+      float x[E];
+      VT::cvt(*reinterpret_cast<const uint4*>(row + (size_t)(v0 + i) * E), x);
 #pragma unroll
-        for (int e = 0; e < E; e++) hit |= (uint32_t)(order_key(x[e]) == lo) << e;
+      for (int e = 0; e < E; e++) {
+        const uint32_t kx = order_key(x[e]);
+        if (kx > lo) ts.cand[atomicAdd(&ts.n_cand, 1)] = cand_of(kx, (v0 + i) * E + e);
       }
-      const int mine = __popc(hit);
-      int inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) ts.red[buf][ft >> 5] = inc;
-      fin_sync(team);
-      int at = found + inc - mine, total = 0;
-#pragma unroll
-      for (int w = 0; w < kFinWarps; w++) {
-        if (w < (ft >> 5)) at += ts.red[buf][w];
-        total += ts.red[buf][w];
-      }
-      buf ^= 1;
-      for (int e = 0; e < E; e++)
-        if (hit >> e & 1) {
-          if (above + at < k) ts.cand[above + at] = cand_of(lo, (v0 + i) * E + e);
-          at++;
-        }
-      found += total;
     }
-    if (ft < 32) {
-      const bool hit = ft < tail_n && order_key(tail_x) == lo;
-      const uint32_t who = __ballot_sync(0xffffffffu, hit);
-      const int at = above + found + __popc(who & ((1u << lane) - 1));
-      if (hit && at < k) ts.cand[at] = cand_of(lo, p.V - tail_n + ft);
-      if (ft == 0) ts.n_ties = found + __popc(who);
-    }
+    if (ft < tail_n && order_key(tail_x) > lo)
+      ts.cand[atomicAdd(&ts.n_cand, 1)] = cand_of(order_key(tail_x), p.V - tail_n + ft);
     fin_sync(team);
-    if (above < k) {
-      if (ft == 0) ts.n_cand = min(above + ts.n_ties, k);
-      fin_sync(team);
+  }
+  const int above = ts.n_cand;
+  // ties by id: 128 vectors at a time, then the last entries, until there are enough
+  int found = 0;
+  for (int base = 0; base < nvec + 1 && above + found < k; base += kFin) {
+    uint32_t hit = 0;
+    const int i = base + ft;
+    if (i < nvec) {
+      float x[E];
+      VT::cvt(*reinterpret_cast<const uint4*>(row + (size_t)(v0 + i) * E), x);
+#pragma unroll
+      for (int e = 0; e < E; e++) hit |= (uint32_t)(order_key(x[e]) == lo) << e;
     }
+    const int mine = __popc(hit);
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) ts.red[buf][ft >> 5] = inc;
+    fin_sync(team);
+    int at = found + inc - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kFinWarps; w++) {
+      if (w < (ft >> 5)) at += ts.red[buf][w];
+      total += ts.red[buf][w];
+    }
+    buf ^= 1;
+    for (int e = 0; e < E; e++)
+      if (hit >> e & 1) {
+        if (above + at < k) ts.cand[above + at] = cand_of(lo, (v0 + i) * E + e);
+        at++;
+      }
+    found += total;
+  }
+  if (ft < 32) {
+    const bool hit = ft < tail_n && order_key(tail_x) == lo;
+    const uint32_t who = __ballot_sync(0xffffffffu, hit);
+    const int at = above + found + __popc(who & ((1u << lane) - 1));
+    if (hit && at < k) ts.cand[at] = cand_of(lo, p.V - tail_n + ft);
+    if (ft == 0) ts.n_ties = found + __popc(who);
+  }
+  fin_sync(team);
+  if (above < k) {
+    if (ft == 0) ts.n_cand = min(above + ts.n_ties, k);
+    fin_sync(team);
   }
   return rank_cand(ts, team, k, lo, buf);
 }
@@ -460,7 +477,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
           gm = fmaxf(gm, mx);
-          st.add(w, mx, c2);
+          st.add(w, cnt, mx, c2);
           pos.next(rs.n_slots);
         }
         if (kTop) {
@@ -506,9 +523,12 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
       }
       warp_merge(st, c2);
       int n_top = 0;
-      if (kTop) n_top = part_top<T>(row, p, ts, par, v0, nvec, tail_n, tail_x);
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bar.part_empty[par]);
+      if (kTop) {
+        n_top = part_top<T>(row, p, ts, &bar.part_empty[par], par, v0, nvec, tail_n, tail_x);
+      } else {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar.part_empty[par]);
+      }
 
       if (rs.cs > 1) {
         // to rank 0, once it has read what this rank sent two rows ago
