@@ -161,9 +161,12 @@ struct Raw<__nv_bfloat16> {
     return pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   }
   // largest entry, NaNs left out
-  __device__ __forceinline__ static float max(const uint4& w) {
+  __device__ __forceinline__ static float max(const uint4 (&w)[kPer]) {
     auto b = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
-    const __nv_bfloat162 m = __hmax2(__hmax2(b(w.x), b(w.y)), __hmax2(b(w.z), b(w.w)));
+    auto h = [&](const uint4& v) { return __hmax2(__hmax2(b(v.x), b(v.y)), __hmax2(b(v.z), b(v.w))); };
+    __nv_bfloat162 m = h(w[0]);
+#pragma unroll
+    for (int q = 1; q < kPer; q++) m = __hmax2(m, h(w[q]));
     return fmaxf(__low2float(m), __high2float(m));
   }
   // entries below -2^100 raised to it, NaNs kept
@@ -183,8 +186,13 @@ struct Raw<float> {
   __device__ __forceinline__ static f2 pair(const uint4& w, int i) {
     return i == 0 ? pack2(__uint_as_float(w.x), __uint_as_float(w.y)) : pack2(__uint_as_float(w.z), __uint_as_float(w.w));
   }
-  __device__ __forceinline__ static float max(const uint4& w) {
-    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  __device__ __forceinline__ static float max(const uint4 (&w)[kPer]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < kPer; q++)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(w[q].x), __uint_as_float(w[q].y)),
+                         fmaxf(__uint_as_float(w[q].z), __uint_as_float(w[q].w))));
+    return m;
   }
   __device__ __forceinline__ static uint4 floored(const uint4& w) {
     auto f = [](uint32_t u) { return __float_as_uint(max_nan(__uint_as_float(u), -0x1p100f)); };
@@ -192,16 +200,20 @@ struct Raw<float> {
   }
 };
 
-// A thread's running statistics over stages.  The reference m moves once per stage at most,
-// to the largest of the thread's vectors; sums in pairs, two chains.
+// A thread's running statistics over stages, sums in pairs, two chains.  The reference m follows
+// the largest entry only when that is more than 2^kSlack times as likely (with one stage's
+// largest entry as the start, hardly ever): moving it costs as much as several entries, and a
+// warp pays when one lane does.  total() refers the sums to the largest entry; the entropy's
+// sum loses 2^-24 kSlack there at most.
 //
-// With a usual reference, above -2^96, the exponent of an entry is one fused multiply-add,
-// t = c2 x - r with r = c2 m rounded: relative to r the sums are exact to the exponential's
-// own error, and total() refers them back to m by the rounding error of r, which an fma gives
-// exactly.  Entries below -2^100 add nothing there and are raised to it, two at a time, so that
-// a masked one's product 2^t t is 0 and not 0 * inf.  Other references (below -2^96: nothing but
-// masked entries so far), and temperatures that take c2 2^100 out of range, take the difference
-// first and cut each exponent off.
+// With a usual reference, of size below 2^96, the exponent of an entry is one fused
+// multiply-add, t = c2 x - r with r = c2 m rounded: relative to r the sums are exact to the
+// exponential's own error, and total() corrects by the rounding error of r, which an fma gives
+// exactly.  Entries below -2^100 add nothing there and are raised to it, so that a masked one's
+// term of the entropy is 0 and not 0 * inf.  Other references (below -2^96: nothing but masked
+// entries so far), and temperatures that take c2 2^100 out of range, take the difference first
+// and cut each exponent off.
+constexpr float kSlack = 8.f;
 template <typename T, bool kEntropy>
 struct StageStat {
   float m, r;
@@ -239,24 +251,25 @@ struct StageStat {
       if (kEntropy) a[i & 1] = fma2(e, t, a[i & 1]);
     }
   }
-  // the vectors w[q] with q * kCons < cnt, the largest entry of all kPer being mx
-  __device__ __forceinline__ void add(const uint4 (&w)[kPer], int cnt, float mx, float c2) {
-    if (mx > m) raise(mx, c2);
-    if (usual(m, c2)) {
-      if (cnt > (kPer - 1) * kCons) {
+  template <bool kUsual>
+  __device__ __forceinline__ void add_all(const uint4 (&w)[kPer], int cnt, float c2) {
+    if (cnt > (kPer - 1) * kCons) {
 #pragma unroll
-        for (int q = 0; q < kPer; q++) add_vec<true>(w[q], c2);
-      } else {
-#pragma unroll
-        for (int q = 0; q < kPer - 1; q++)
-          if (q * kCons < cnt) add_vec<true>(w[q], c2);
-      }
+      for (int q = 0; q < kPer; q++) add_vec<kUsual>(w[q], c2);
     } else {
 #pragma unroll
-      for (int q = 0; q < kPer; q++) add_vec<false>(w[q], c2);
+      for (int q = 0; q < kPer - 1; q++)
+        if (q * kCons < cnt) add_vec<kUsual>(w[q], c2);
     }
   }
-  __device__ __forceinline__ Stat total(float c2) const {
+  // the vectors w[q] with q * kCons < cnt, the largest entry of all kPer being mx
+  __device__ __forceinline__ void add(const uint4 (&w)[kPer], int cnt, float mx, float c2) {
+    if ((mx - m) * c2 > kSlack) raise(mx, c2);
+    if (usual(m, c2)) add_all<true>(w, cnt, c2);
+    else add_all<false>(w, cnt, c2);
+  }
+  // statistics relative to the largest entry mx
+  __device__ __forceinline__ Stat total(float mx, float c2) const {
     float x, y, z, w;
     unpack2(add2(s[0], s[1]), x, y);
     unpack2(add2(a[0], a[1]), z, w);
@@ -266,6 +279,7 @@ struct StageStat {
       t.a = f * fmaf(d, t.s, t.a);
       t.s *= f;
     }
+    if (mx > m) t.rebase(mx, c2);
     return t;
   }
 };
@@ -297,10 +311,7 @@ __device__ __forceinline__ float load_slot(const uint4* slot, int cnt, uint4 (&w
       w[q] = i < cnt ? slot[i] : Raw<T>::masked();
     }
   }
-  float mx = Raw<T>::max(w[0]);
-#pragma unroll
-  for (int q = 1; q < kPer; q++) mx = fmaxf(mx, Raw<T>::max(w[q]));
-  return mx;
+  return Raw<T>::max(w);
 }
 
 // The barriers of a CTA.

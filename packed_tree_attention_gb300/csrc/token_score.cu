@@ -459,12 +459,13 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
     // ---- consumers: sums of the part, group maxima ----
     RingPos pos;
     bool ok = true;
-    const int J = min(max(rs.n_stages, 1), kGroupStages);
+    const int J = min(rs.n_stages, kGroupStages);
+    StageStat<T, true> st;
     for (int r = cluster, it = 0; r < p.n && ok; r += n_clusters, it++) {
       const int par = it & 1;
-      StageStat<T, true> st;
       st.init();
       float gm = -INFINITY, tm = -INFINITY;
+      int jg = 0, frac = 0;
       // the finishers are done with this parity's buffers two rows ago
       if (kTop) ok = warp_wait(&bar.part_empty[par], ((it >> 1) & 1) ^ 1, p.status);
       for (int j = 0; j < rs.n_stages && ok; j++) {
@@ -476,22 +477,23 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
           const float mx = load_slot<T>(slot, cnt, w);
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
+          tm = fmaxf(tm, mx);
           gm = fmaxf(gm, mx);
           st.add(w, cnt, mx, c2);
           pos.next(rs.n_slots);
         }
         if (kTop) {
-          const int jg = j * J / rs.n_stages;
-          if (j + 1 == rs.n_stages || (j + 1) * J / rs.n_stages != jg) {
-            top[par].gmax[jg][tid] = gm;
-            tm = fmaxf(tm, gm);
+          // class of stage j: j J / n_stages
+          if ((frac += J) >= rs.n_stages) {
+            frac -= rs.n_stages;
+            top[par].gmax[jg++][tid] = gm;
             gm = -INFINITY;
           }
         }
       }
       if (!ok) break;
       if (kTop) top[par].tmax[tid] = tm;
-      Stat tot = st.total(c2);
+      Stat tot = st.total(tm, c2);
       warp_merge(tot, c2);
       if (!kTop) ok = warp_wait(&bar.part_empty[par], ((it >> 1) & 1) ^ 1, p.status);
       if (lane == 0) {
