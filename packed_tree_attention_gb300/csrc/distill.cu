@@ -12,20 +12,18 @@
 // q_R is summed over the entries outside the list itself: 1 - sum_i q_i would lose it
 // where the list holds nearly all of the mass.
 
-#include "row_common.cuh"
+#include "row_ring.cuh"
 
 namespace octo {
 namespace {
 
 using namespace rows;
 
-constexpr int kThreads = 512;
-
 struct DistillParams {
   const void* logits;
   void* dlogits;            // or null
   int64_t ld;
-  int32_t V, row0, k, tail;
+  int32_t V, row0, n, k, tail;
   float c, gs;
   const int32_t* t_ids;     // [n][k]
   const float* t_val;       // [n][k]
@@ -33,112 +31,456 @@ struct DistillParams {
   float* row_kl;            // [plan rows]
   float* part;              // [n] weighted row losses, or null
   int32_t* status;
+  RingShape ring;
+  int32_t words;            // words of the bitmap of a part's vectors
 };
 
-// One CTA per row: a pass for the sums inside and outside the list, a pass for the gradient.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_distill(DistillParams p) {
+// What the gradient pass needs of a row: an entry outside the list has the gradient
+// f 2^(c2 x - hi), or f 2^(c2 (x - m) - l2) where c2 m leaves the usual range.
+struct RowScale {
+  float f, hi, m, l2;
+  int32_t live, usual;
+};
+struct TeamSmem {
+  int32_t id[kMaxTop];
+  float p[kMaxTop], x[kMaxTop];
+  float red[2][kFinWarps];
+  float pre_o[kFinWarps][2], pre_in[kFinWarps][2];   // sums of the listed vectors and of the last entries
+  float in[2][kMaxCluster][4];                       // the CTAs' sums, of every other row of the team
+};
+struct DistillSmem {
+  RingBars bars;
+  float part[2][kConsWarps][2];
+  RowScale scale[2];
+  TeamSmem team[kTeams];
+};
+constexpr int kBitmapOffset = ((int)sizeof(DistillSmem) + 127) / 128 * 128;
+__host__ __device__ constexpr int slots_offset(int words) { return kBitmapOffset + (kTeams * words * 4 + 127) / 128 * 128; }
+
+__device__ __forceinline__ float fin_fold(float v, TeamSmem& t, int team, int& buf) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int w = ((int)threadIdx.x - kCons - team * kFin) >> 5;
+  if ((threadIdx.x & 31) == 0) t.red[buf][w] = v;
+  fin_sync(team);
+  float r = 0.f;
+#pragma unroll
+  for (int i = 0; i < kFinWarps; i++) r += t.red[buf][i];
+  buf ^= 1;
+  return r;
+}
+__device__ __forceinline__ float fin_max(float v, TeamSmem& t, int team, int& buf) {
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(v) : "f"(v));
+  const int w = ((int)threadIdx.x - kCons - team * kFin) >> 5;
+  if ((threadIdx.x & 31) == 0) t.red[buf][w] = v;
+  fin_sync(team);
+  float r = t.red[buf][0];
+#pragma unroll
+  for (int i = 1; i < kFinWarps; i++) r = fmaxf(r, t.red[buf][i]);
+  buf ^= 1;
+  return r;
+}
+
+// A finisher thread's entry of the teacher's list, made ready before the row's sums.
+struct Entry {
+  int id = -1;       // -1: none
+  float lp = 0.f, p = 0.f, x = 0.f;
+  float sub = 0.f;   // sum of the list's probabilities of this id
+  bool first = false;   // the id's first entry
+};
+
+// The gradient's passes.  kNone: the divergence alone.  kHeld: a part stays in the ring between
+// the two passes, and the first pass of the next row comes before the second of this one, so
+// that the join of the row's sums is never waited for: DRAM sees each logit once.  kAgain:
+// rows too long for that are streamed twice.
+enum { kNone, kHeld, kAgain };
+
+template <typename T, int kMode>
+__global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ DistillParams p) {
   using VT = Vec<T>;
-  __shared__ float red[96];
-  __shared__ int32_t s_id[kMaxTop];
-  __shared__ float s_p[kMaxTop];
-  const int rl = blockIdx.x, tid = threadIdx.x;
-  const T* row = reinterpret_cast<const T*>(p.logits) + (size_t)rl * p.ld;
-  T* grow = p.dlogits ? reinterpret_cast<T*>(p.dlogits) + (size_t)rl * p.ld : nullptr;
-  const float w = p.w ? p.w[p.row0 + rl] : 1.f;
+  constexpr int E = VT::E;
+  extern __shared__ __align__(128) uint8_t smem[];
+  DistillSmem& ss = *reinterpret_cast<DistillSmem*>(smem);
+  uint32_t* const bitmap = reinterpret_cast<uint32_t*>(smem + kBitmapOffset);
+  uint4* const slots = reinterpret_cast<uint4*>(smem + slots_offset(p.words));
+  RingBars& bar = ss.bars;
+  const RingShape rs = p.ring;
+  const uint32_t rank = rs.cs > 1 ? cluster_rank() : 0;
+  const int n_clusters = gridDim.x / rs.cs, cluster = blockIdx.x / rs.cs;
+  const int nv = p.V / E;
+  const int v0 = min(nv, (int)rank * rs.seg), nvec = min(rs.seg, nv - v0);
+  const int tid = threadIdx.x, lane = tid & 31;
   const float c2 = p.c * kLog2e;
-  bool live = w != 0.f;
-  // teacher entries
-  float z = -INFINITY;
-  int id = -1;
-  if (tid < p.k) {
-    id = p.t_ids[(size_t)rl * p.k + tid];
-    z = p.t_val[(size_t)rl * p.k + tid];
-    if (id >= p.V) atomicExch(p.status, OCTO_EINVAL);
-    if (id < 0 || id >= p.V || z == -INFINITY) id = -1, z = -INFINITY;
-    s_id[tid] = id;
-  }
-  float lp, P, pr = 0.f, zero = 0.f;
-  if (p.tail) {
-    lp = z;
-    P = expf(z);
-    float sum = P;
-    block_sum2<kThreads>(sum, zero, red);
-    pr = fmaxf(0.f, 1.f - sum);
-    if (sum != sum) pr = sum;
-  } else {
-    Stat t{z == -INFINITY ? -FLT_MAX : z, z == -INFINITY ? 0.f : 1.f, 0.f};
-    block_stat<kThreads>(t, c2, red);
-    if (t.s == 0.f) live = false;
-    lp = z == -INFINITY ? -INFINITY : (z - t.m) * p.c - logf(t.s);
-    P = expf(lp);
-  }
-  if (tid < p.k) s_p[tid] = P;
+  const T* const logits = reinterpret_cast<const T*>(p.logits);
+  T* const dlogits = reinterpret_cast<T*>(p.dlogits);
+  auto weight = [&](int r) { return !p.w ? 1.f : r < p.n ? p.w[p.row0 + r] : 0.f; };
+
+  if (tid == 0) bar.init(rs.cs);
   __syncthreads();
-  float kl = 0.f, fix = 0.f;
-  float mo = 0.f, lo = 0.f, fo = 0.f;   // reference and factor of the unlisted entries' gradient
-  if (live) {
-    // statistics of the entries that the list leaves out and of the listed ones (each id
-    // once); without the rest term the two need not be told apart
-    auto listed = [&](int v) {
-      for (int i = 0; i < p.k; i++)
-        if (s_id[i] == v) return true;
-      return false;
+  if (rs.cs > 1) cluster_sync();
+
+  if (tid >= kCons + kTeams * kFin) {
+    // ---- copies (rows of weight 0 are not read) ----
+    if (tid == kCons + kTeams * kFin) {
+      RingPos pos;
+      int issued = 0;
+      bool ok = true;
+      float w = weight(cluster);
+      for (int r = cluster; r < p.n && ok; r += n_clusters) {
+        const bool skip = w == 0.f;
+        w = weight(r + n_clusters);
+        if (skip) continue;
+        const T* src = logits + (size_t)r * p.ld + (size_t)v0 * E;
+        for (int pass = 0; pass < (kMode == kAgain ? 2 : 1) && ok; pass++)
+          for (int b = 0; b < nvec; b += rs.stage) {
+            if (!(ok = ring_wait(&bar.empty[pos.slot], pos.round ^ 1, p.status))) break;
+            const uint32_t bytes = (uint32_t)min(rs.stage, nvec - b) * 16;
+            tc::mbar_expect_tx(&bar.full[pos.slot], bytes);
+            bulk_load(slots + (size_t)pos.slot * rs.stage, src + (size_t)b * E, bytes, &bar.full[pos.slot]);
+            pos.next(rs.n_slots);
+            issued++;
+          }
+      }
+      // a copy must not outlive the CTA: the consumers have seen all of them unless a wait gave up
+      if (!ok)
+        for (int i = min(issued, rs.n_slots); i > 0; i--) {
+          if (--pos.slot < 0) pos.slot = rs.n_slots - 1, pos.round ^= 1;
+          ring_wait(&bar.full[pos.slot], pos.round, p.status);
+        }
+    }
+  } else if (tid < kCons) {
+    // ---- consumers ----
+    RingPos pos, pos2;
+    bool ok = true;
+    StageStat<T, false> st;
+    // sums over the entries outside the list
+    auto sums = [&](int it, bool live) {
+      const int par = it & 1;
+      const uint32_t ph = (it >> 1) & 1;
+      st.init();
+      float tm = -INFINITY;
+      if (p.tail && !(ok = warp_wait(&bar.pre_full[par], ph, p.status))) return;
+      if (live) {
+        const uint32_t* bits = bitmap + par * p.words;
+        for (int j = 0; j < rs.n_stages; j++) {
+          const int cnt = min(rs.stage, nvec - j * rs.stage);
+          if (cnt <= 0) break;
+          if (!(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) return;
+          uint4 w[kPer];
+          float mx = load_slot<T>(slots + (size_t)pos.slot * rs.stage, cnt, w);
+          if (kMode != kHeld) {
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
+          }
+          if (p.tail) {
+            bool any = false;
+#pragma unroll
+            for (int q = 0; q < kPer; q++) {
+              if (q * kCons >= cnt) continue;
+              const int at = (j * rs.stage + q * kCons + (tid & ~31)) >> 5;
+              const uint32_t word = at < p.words ? bits[at] : 0;
+              if (word) {
+                any = true;
+                if (word >> lane & 1) w[q] = Raw<T>::masked();
+              }
+            }
+            if (any) mx = Raw<T>::max(w);
+          }
+          tm = fmaxf(tm, mx);
+          st.add(w, cnt, mx, c2);
+          pos.next(rs.n_slots);
+        }
+      }
+      Stat tot = st.total(tm, c2);
+      warp_merge(tot, c2);
+      if (!(ok = warp_wait(&bar.part_empty[par], ph ^ 1, p.status))) return;
+      if (lane == 0) {
+        ss.part[par][tid >> 5][0] = tot.m;
+        ss.part[par][tid >> 5][1] = tot.s;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar.part_full[par]);
     };
-    Stat o, in;
-    o.init();
-    in.init();
-    for (int v = tid; v < p.V; v += kThreads) {
-      const float x = VT::get(row + v);
-      Stat& st = p.tail && listed(v) ? in : o;
-      if (x > st.m) st.rebase(x, c2);
-      st.add(x, c2);
-    }
-    block_stat<kThreads>(o, c2, red);
-    block_stat<kThreads>(in, c2, red);
-    Stat all = o;
-    all.merge(in.m, in.s, in.a, c2);
-    if (all.s == 0.f) live = false;
-    if (live) {
-      const float ls = logf(all.s);
-      float term = 0.f, sum = 0.f, lq = 0.f;
-      if (id >= 0) {
-        lq = (VT::get(row + id) - all.m) * p.c - ls;
-        if (P != 0.f) term = P * (lp - lq), sum = P;
+    // the gradient of the entries outside the list (the listed ones are overwritten later)
+    auto gradient = [&](int it, int r, bool held) {
+      const int par = it & 1;
+      if (!(ok = warp_wait(&bar.scal_full[par], (it >> 1) & 1, p.status))) return;
+      const RowScale sc = ss.scale[par];
+      uint4* out = reinterpret_cast<uint4*>(dlogits + (size_t)r * p.ld) + v0;
+      const f2 cc = pack2(c2, c2), hi = pack2(-sc.hi, -sc.hi), ff = pack2(sc.f, sc.f);
+      for (int j = 0; j < rs.n_stages; j++) {
+        const int cnt = min(rs.stage, nvec - j * rs.stage);
+        if (cnt <= 0) break;
+        if (kMode == kAgain && held && !(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) return;
+        RingPos& at = kMode == kAgain ? pos : pos2;
+        const uint4* slot = slots + (size_t)at.slot * rs.stage;
+#pragma unroll
+        for (int q = 0; q < kPer; q++) {
+          const int i = q * kCons + tid;
+          if (i >= cnt) continue;
+          uint4 o = make_uint4(0, 0, 0, 0);
+          if (sc.live) {
+            const uint4 w = slot[i];
+            float g[E];
+#pragma unroll
+            for (int e = 0; e < E / 2; e++) {
+              float y0, y1;
+              if (sc.usual) {
+                unpack2(fma2(Raw<T>::pair(w, e), cc, hi), y0, y1);
+              } else {
+                unpack2(Raw<T>::pair(w, e), y0, y1);
+                y0 = max_nan((y0 - sc.m) * c2 - sc.l2, kCut);
+                y1 = max_nan((y1 - sc.m) * c2 - sc.l2, kCut);
+              }
+              unpack2(mul2(pack2(ex2f(y0), ex2f(y1)), ff), g[2 * e], g[2 * e + 1]);
+            }
+            o = VT::pack(g);
+          }
+          __stcs(out + j * rs.stage + i, o);
+        }
+        if (held) {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bar.empty[at.slot]);
+          at.next(rs.n_slots);
+        }
       }
-      block_sum2<kThreads>(term, sum, red);
-      kl = term;
-      mo = o.m;
-      if (o.s == 0.f) {
-        pr = 0.f;   // nothing outside the list has mass
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar.p2_done[par]);
+    };
+    float w = weight(cluster);
+    bool live = w != 0.f, was = false;
+    for (int r = cluster, it = 0; ok; r += n_clusters, it++) {
+      const float wn = weight(r + n_clusters);
+      if (r < p.n) sums(it, live);
+      if (kMode == kAgain && ok && r < p.n) gradient(it, r, live);
+      if (kMode == kHeld && ok && it > 0) gradient(it - 1, r - n_clusters, was);
+      if (r >= p.n) break;
+      was = live;
+      live = wn != 0.f;
+    }
+  } else {
+    // ---- finishers: team `par` takes the rows of that parity ----
+    const int par = (tid - kCons) / kFin, ft = tid - kCons - par * kFin, wi = ft >> 5;
+    TeamSmem& ts = ss.team[par];
+    uint32_t* const bits = bitmap + par * p.words;
+    const int tail_n = rank + 1 == (uint32_t)rs.cs ? p.V - nv * E : 0;
+    int buf = 0;
+    // what does not need the row's sums: the teacher's probabilities, which vectors hold listed
+    // ids, and the sums over those vectors and the row's last entries.  A row that is not live
+    // has none of it.
+    Entry en;
+    float w = 0.f, pr = 0.f, total = 0.f, tail_x = 0.f;
+    bool live = false, tail_listed = false;
+    auto prepare = [&](int r) {
+      const T* row = logits + (size_t)r * p.ld;
+      en = Entry();
+      w = weight(r);
+      live = w != 0.f;
+      float z = -INFINITY;
+      if (live && ft < p.k) {
+        en.id = p.t_ids[(size_t)r * p.k + ft];
+        z = p.t_val[(size_t)r * p.k + ft];
+        if (en.id >= p.V) atomicExch(p.status, OCTO_EINVAL);
+        if (en.id < 0 || en.id >= p.V || z == -INFINITY) en.id = -1, z = -INFINITY;
+      }
+      if (live && en.id >= 0) en.x = VT::get(row + en.id);
+      tail_x = live && ft < tail_n ? VT::get(row + nv * E + ft) : -INFINITY;
+      if (!live) {
+        if (p.tail) {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bar.pre_full[par]);
+        }
+        return;
+      }
+      ts.id[ft] = ft < p.k ? en.id : -1;
+      if (p.tail) {
+        for (int i = ft; i < p.words; i += kFin) bits[i] = 0;
+        en.lp = z;
+        en.p = expf(z);
+        total = fin_fold(en.p, ts, par, buf);
+        pr = total != total ? total : fmaxf(0.f, 1.f - total);
       } else {
-        lo = logf(o.s);
-        const float lqr = (o.m - all.m) * p.c + lo - ls;
-        if (pr != 0.f) kl += pr * (logf(pr) - lqr);
-        fo = expf(lqr) * (sum + pr) - pr;
+        const float zm = fin_max(z, ts, par, buf);
+        const float t = z == -INFINITY ? -INFINITY : (z - zm) * p.c;
+        const float sum = fin_fold(expf(t), ts, par, buf);
+        pr = 0.f;
+        if (sum == 0.f) live = false;   // no teacher
+        en.lp = t - logf(sum);
+        en.p = en.id < 0 ? 0.f : expf(en.lp);
+        total = fin_fold(en.p, ts, par, buf);
       }
-      fix = expf(lq) * (sum + pr);
+      ts.p[ft] = en.p;
+      ts.x[ft] = en.x;   // waits for the load: a peer may overwrite the row once it has this CTA's sums
+      fin_sync(par);
+      Stat o, in;
+      o.init();
+      in.init();
+      if (en.id >= 0) {
+        const int vec = en.id / E;
+        uint32_t mask = 0;
+        bool first_vec = true;
+        en.first = true;
+        for (int i = 0; i < p.k; i++) {
+          const int other = ts.id[i];
+          if (other < 0 || other / E != vec) continue;
+          mask |= 1u << (other % E);
+          first_vec = first_vec && i >= ft;
+          if (other == en.id) en.sub += ts.p[i], en.first = en.first && i >= ft;
+        }
+        if (p.tail && vec >= v0 && vec < v0 + nvec && first_vec) {
+          const int at = vec - v0;
+          atomicOr(&bits[at >> 5], 1u << (at & 31));
+          float x[E];
+          VT::cvt(reinterpret_cast<const uint4*>(row)[vec], x);
+#pragma unroll
+          for (int e = 0; e < E; e++) {
+            Stat& s = mask >> e & 1 ? in : o;
+            if (x[e] > s.m) s.rebase(x[e], c2);
+            s.add(x[e], c2);
+          }
+        }
+      }
+      if (p.tail) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar.pre_full[par]);
+      }
+      tail_listed = false;
+      if (ft < tail_n) {
+        if (p.tail || kMode != kNone)
+          for (int i = 0; i < p.k; i++) tail_listed = tail_listed || ts.id[i] == nv * E + ft;
+        Stat& s = p.tail && tail_listed ? in : o;
+        if (tail_x > s.m) s.rebase(tail_x, c2);
+        s.add(tail_x, c2);
+      }
+      warp_merge(o, c2);
+      warp_merge(in, c2);
+      if (lane == 0) {
+        ts.pre_o[wi][0] = o.m, ts.pre_o[wi][1] = o.s;
+        ts.pre_in[wi][0] = in.m, ts.pre_in[wi][1] = in.s;
+      }
+    };
+    const int first_row = cluster + par * n_clusters;
+    if (first_row < p.n) prepare(first_row);
+    for (int r = first_row, it = par; r < p.n; r += 2 * n_clusters, it += 2) {
+      const uint32_t ph = (it >> 1) & 1;
+      if (!fin_all(ring_wait(&bar.part_full[par], ph, p.status), par)) break;
+      float kl = 0.f, fix = 0.f;
+      RowScale sc = {0.f, 0.f, 0.f, 0.f, 0, 1};
+      Stat o, in;
+      o.init();
+      in.init();
+      if (live) {
+        if (lane < kConsWarps) o.m = ss.part[par][lane][0], o.s = ss.part[par][lane][1];
+        else if (lane < kConsWarps + kFinWarps) o.m = ts.pre_o[lane - kConsWarps][0], o.s = ts.pre_o[lane - kConsWarps][1];
+        if (lane < kFinWarps) in.m = ts.pre_in[lane][0], in.s = ts.pre_in[lane][1];
+        warp_merge(o, c2);
+        warp_merge(in, c2);
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar.part_empty[par]);
+      if (rs.cs > 1) {
+        // every CTA to every CTA; in[] and the barriers by turns, so that a fast CTA's next row
+        // meets nobody who still reads or waits for this one
+        if (ft < rs.cs) {
+          const uint32_t dst = map_rank(tc::smem_u32(ts.in[ph][rank]), ft);
+          st_remote(dst, o.m);
+          st_remote(dst + 4, o.s);
+          st_remote(dst + 8, in.m);
+          st_remote(dst + 12, in.s);
+          arrive_remote(map_rank(tc::smem_u32(&bar.joined[par][ph]), ft));
+        }
+        if (!fin_all(ring_wait<true>(&bar.joined[par][ph], (it >> 2) & 1, p.status), par)) break;
+        o.init();
+        in.init();
+        if (lane < rs.cs) {
+          const float* q = ts.in[ph][lane];
+          o.m = q[0], o.s = q[1], in.m = q[2], in.s = q[3];
+        }
+        warp_merge(o, c2);
+        warp_merge(in, c2);
+      }
+      Stat all = o;
+      all.merge(in.m, in.s, 0.f, c2);
+      const bool has = live && all.s != 0.f;
+      if (has) {
+        const float ls = logf(all.s), lo = logf(o.s);
+        if (o.s == 0.f) pr = 0.f;   // nothing outside the list has mass
+        const float lqr = (o.m - all.m) * p.c + lo - ls;
+        const float sum = total + pr;
+        const float lq = en.id >= 0 ? (en.x - all.m) * p.c - ls : 0.f;
+        if (rank == 0) {
+          kl = fin_fold(en.p != 0.f ? en.p * (en.lp - lq) : 0.f, ts, par, buf);
+          if (pr != 0.f) kl += pr * (logf(pr) - lqr);
+        }
+        if (kMode != kNone) {
+          const float f = p.gs * w * p.c;
+          fix = f * (expf(lq) * sum - en.sub);
+          sc.live = 1;
+          sc.f = o.s == 0.f ? 0.f : f * (p.tail ? expf(lqr) * sum - pr : sum);
+          if (o.s != 0.f) sc.m = o.m, sc.l2 = lo * kLog2e;
+          sc.usual = StageStat<T, false>::usual(sc.m, c2);
+          // hi and what it leaves out, which goes into the factor
+          const double e = (double)sc.m * c2 + (double)sc.l2;
+          sc.hi = (float)e;
+          if (sc.usual) sc.f *= ex2f((float)(sc.hi - e));
+        }
+      }
+      if (ft == 0) {
+        if (rank == 0) {
+          p.row_kl[p.row0 + r] = kl;
+          if (p.part) p.part[r] = has ? w * kl : 0.f;
+        }
+        if (kMode != kNone) {
+          ss.scale[par] = sc;
+          tc::mbar_arrive(&bar.scal_full[par]);
+        }
+      }
+      const Entry done = en;
+      const float last_x = tail_x;
+      const bool last_listed = tail_listed;
+      if (r + 2 * n_clusters < p.n) prepare(r + 2 * n_clusters);
+      if (kMode != kNone) {
+        // after the consumers' stores: the listed entries, each id by its first, and the last ones
+        if (!fin_all(ring_wait(&bar.p2_done[par], ph, p.status), par)) break;
+        T* grow = dlogits + (size_t)r * p.ld;
+        if (has && done.id >= 0 && done.first) {
+          const int vec = done.id / E;
+          if (vec < nv ? vec >= v0 && vec < v0 + nvec : tail_n > 0) VT::put(grow + done.id, fix);
+        }
+        if (ft < tail_n && !(has && last_listed))
+          VT::put(grow + nv * E + ft, sc.live ? sc.f * ex2f(sc.usual ? fmaf(last_x, c2, -sc.hi)
+                                                                      : max_nan((last_x - sc.m) * c2 - sc.l2, kCut))
+                                              : 0.f);
+      }
     }
   }
-  const float f = p.gs * w * p.c;
-  if (tid == 0) {
-    p.row_kl[p.row0 + rl] = kl;
-    if (p.part) p.part[rl] = live ? w * kl : 0.f;
+  // no CTA leaves while another may still write to its shared memory
+  __syncwarp();
+  if (rs.cs > 1) cluster_sync();
+}
+
+template <typename T>
+int launch_distill(DistillParams& p, cudaStream_t s) {
+  const int64_t nv = p.V / Vec<T>::E;
+  const void* f = (const void*)k_distill<T, kNone>;
+  auto words = [&](int cs) { return (int)(((nv + cs - 1) / cs + 31) / 32); };
+  auto shape = [&](int cs) { return ring_shape(nv, cs, kSmemMax - slots_offset(words(cs)), true); };
+  int cs = 1;
+  if (p.dlogits) {
+    // as many CTAs as it takes for the ring to hold two rows' parts and a stage to come
+    f = (const void*)k_distill<T, kHeld>;
+    auto holds = [&](int c) { const RingShape r = shape(c); return r.n_slots >= 2 * r.n_stages + 1; };
+    while (cs < kMaxCluster && !holds(cs)) cs *= 2;
+    if (!holds(cs)) f = (const void*)k_distill<T, kAgain>, cs = 1;
   }
-  if (!grow) return;
-  __syncthreads();  // the listed entries are read before the gradient may overwrite them
-  const float l2 = lo * kLog2e;
-  for (int v = tid; v < p.V; v += kThreads)
-    VT::put(grow + v, live ? f * fo * ex2f(max_nan((VT::get(row + v) - mo) * c2 - l2, kCut)) : 0.f);
-  __syncthreads();
-  // the listed entries, each id by its first entry
-  if (live && id >= 0) {
-    float sub = 0.f;
-    bool first = true;
-    for (int i = 0; i < p.k; i++)
-      if (s_id[i] == id) sub += s_p[i], first = first && i >= tid;
-    if (first) VT::put(grow + id, f * (fix - sub));
-  }
+  int few = 1;
+  if (int st = pick_cluster(f, p.n, p.dlogits ? 2 * nv : nv, kSmemMax, [](int) { return 0.7; }, &few)) return st;
+  cs = few > cs ? few : cs;
+  while (words(cs) * 4 * kTeams > 64 * 1024 && cs < kMaxCluster) cs *= 2;
+  p.words = p.tail ? words(cs) : 0;
+  p.ring = ring_shape(nv, cs, kSmemMax - slots_offset(p.words), true);
+  if (p.ring.n_slots < 2) return OCTO_ENOTSUP;
+  return launch_ring(f, p, p.n, cs, slots_offset(p.words) + p.ring.n_slots * p.ring.stage * 16, s);
 }
 
 }  // namespace
@@ -185,12 +527,8 @@ int octo_distill_topk(octo_plan_t plan, int32_t row0, int32_t n_rows, const void
   p.status = plan->pool->d_status;
   plan->last_stream = s;
   NvtxRange nv("octo_distill_topk");
-  if (dtype == OCTO_DTYPE_BF16)
-    k_distill<__nv_bfloat16><<<n_rows, kThreads, 0, s>>>(p);
-  else
-    k_distill<float><<<n_rows, kThreads, 0, s>>>(p);
-  count_launch();
-  if (int st = cuda_status(cudaGetLastError())) return st;
+  p.n = n_rows;
+  if (int st = dtype == OCTO_DTYPE_BF16 ? launch_distill<__nv_bfloat16>(p, s) : launch_distill<float>(p, s)) return st;
   return loss ? launch_loss_sum((const float*)ws, n_rows, loss, s) : OCTO_OK;
 }
 

@@ -23,24 +23,7 @@ int sm_count() {
   return known[dev] = n;
 }
 
-int pick_cluster(int32_t n, int64_t nv, int ring_bytes, int rows_held) {
-  const int sms = std::max(1, sm_count());
-  int best = 1;
-  double best_t = 0;
-  for (int cs = 1; cs <= kMaxCluster; cs *= 2) {
-    const int slots = std::max(1, sms / cs);
-    const double rounds = (n + slots - 1) / slots;
-    const double part = (double)((nv + cs - 1) / cs) * 16e-3;   // KB
-    // an SM's share of the memory rate is 45 KB/us; alone it reaches about 80
-    const double rate = 45.0 * std::min(1.8, std::max(1.0, (double)sms / ((double)std::min(n, slots) * cs)));
-    const double t = rounds * (part / rate + 0.25 + (cs > 1 ? 0.15 : 0.0));
-    if (cs == 1 || t < 0.97 * best_t) best = cs, best_t = t;
-  }
-  return best;
-}
-
-// Clusters of this kernel, size and shared memory that the device holds at once.
-static int max_clusters(const void* kernel, int cs, int smem, int* out) {
+int max_clusters(const void* kernel, int cs, int smem, int* out) {
   int dev = 0;
   OCTO_CUDA(cudaGetDevice(&dev));
   static std::mutex mu;
@@ -70,9 +53,10 @@ static int max_clusters(const void* kernel, int cs, int smem, int* out) {
 
 int launch_ring_raw(const void* kernel, const void* p, int32_t n, int cs, int smem, cudaStream_t s) {
   if (int st = set_smem_limit(kernel, kSmemMax)) return st;
-  int clusters = 0;
-  if (cs == 1) clusters = std::max(1, sm_count());
-  else if (int st = max_clusters(kernel, cs, smem, &clusters)) return st;
+  int clusters = sm_count();
+  if (cs > 1)
+    if (int st = max_clusters(kernel, cs, smem, &clusters)) return st;
+  clusters = std::max(1, clusters);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(std::min<int64_t>(n, clusters) * cs));
   cfg.blockDim = dim3(kBlock);

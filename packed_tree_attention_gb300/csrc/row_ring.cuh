@@ -23,6 +23,7 @@ constexpr int kPer = 4;                     // vectors of one thread in a stage
 constexpr int kMaxSlots = 24;
 constexpr int kMaxCluster = 8;
 constexpr int kFinBar = 1;                  // named barriers of the finisher teams: this and the next
+static_assert(kTeams == 2, "the barriers' pairs are the teams'");
 static_assert(kFin >= kMaxTop, "a finisher thread for each teacher entry");
 
 struct RingShape {
@@ -33,13 +34,14 @@ struct RingShape {
   int32_t n_slots;
 };
 
-// cs CTAs per row, ring of at most `bytes`.
-inline RingShape ring_shape(int64_t nv, int cs, int bytes) {
+// cs CTAs per row, ring of at most `bytes`; even: stages of one size, so that the slots hold
+// the most rows, otherwise full ones and a rest.
+inline RingShape ring_shape(int64_t nv, int cs, int bytes, bool even) {
   RingShape s;
   s.cs = cs;
   s.seg = (int32_t)((nv + cs - 1) / cs);
   s.n_stages = (s.seg + kCons * kPer - 1) / (kCons * kPer);
-  s.stage = s.n_stages > 1 ? kCons * kPer : s.n_stages ? (s.seg + 31) / 32 * 32 : 32;
+  s.stage = s.n_stages > 1 && !even ? kCons * kPer : s.n_stages ? ((s.seg + s.n_stages - 1) / s.n_stages + 31) / 32 * 32 : 32;
   s.n_slots = bytes / (s.stage * 16);
   if (s.n_slots > kMaxSlots) s.n_slots = kMaxSlots;
   return s;
@@ -318,7 +320,7 @@ __device__ __forceinline__ float load_slot(const uint4* slot, int cnt, uint4 (&w
 struct RingBars {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t part_full[2], part_empty[2];   // a row's warp sums: written, read
-  uint64_t joined[2], freed[2];           // every CTA of the cluster sent its part of a row; that was read
+  uint64_t joined[kTeams][2];             // every CTA of the cluster sent its part of a row
   uint64_t scal_full[2], scal_empty[2];   // a row's results: written, read by who needs them
   uint64_t pre_full[2], p2_done[2];       // distillation
   __device__ void init(int cs) {
@@ -326,8 +328,7 @@ struct RingBars {
     for (int i = 0; i < 2; i++) {
       tc::mbar_init(&part_full[i], kConsWarps);
       tc::mbar_init(&part_empty[i], kFinWarps);
-      tc::mbar_init(&joined[i], cs);
-      tc::mbar_init(&freed[i], 1);
+      for (int j = 0; j < 2; j++) tc::mbar_init(&joined[i][j], cs);
       tc::mbar_init(&pre_full[i], kFinWarps);
       tc::mbar_init(&scal_full[i], 1);
       tc::mbar_init(&scal_empty[i], 1);
@@ -351,12 +352,29 @@ constexpr int kSmemMax = 227 * 1024;
 // SMs of the current device
 int sm_count();
 
-// CTAs per row.  Time of a call in SM microseconds: rounds of clusters over the rows, each
-// round a part's bytes at an SM's share of the memory rate plus what a round costs besides.
-// rows_held: parts that the ring has to hold at once (0: any ring will do).
-int pick_cluster(int32_t n, int64_t nv, int ring_bytes, int rows_held);
+// Clusters of cs CTAs of this kernel that the device holds at once.
+int max_clusters(const void* kernel, int cs, int smem, int* out);
 
-// Launches kernel(p) with n rows' clusters of cs CTAs, at most as many as the device holds.
+// CTAs per row for n rows of nv vectors: several only where every row has its cluster at once
+// (a cluster that takes row after row waits for its slowest CTA at each), and where the time
+// that the shorter parts save is more than joining them costs.
+//   join_us(cs): what a cluster of cs CTAs costs besides, in microseconds.
+template <typename F>
+int pick_cluster(const void* kernel, int32_t n, int64_t nv, int smem, F join_us, int* cs) {
+  *cs = 1;
+  if (int st = set_smem_limit(kernel, kSmemMax)) return st;
+  double best = (double)nv * 16e-3 / 65;   // a CTA streams a row at about 65 KB/us
+  for (int c = 2; c <= kMaxCluster && (int64_t)n * c <= sm_count(); c *= 2) {
+    const double t = (double)nv * 16e-3 / 65 / c + join_us(c);
+    if (t >= best) continue;
+    int held = 0;
+    if (int st = max_clusters(kernel, c, smem, &held)) return st;
+    if (n <= held) best = t, *cs = c;
+  }
+  return OCTO_OK;
+}
+
+// Launches kernel(p) on n rows: a cluster of cs CTAs for each, but no more than the device holds.
 int launch_ring_raw(const void* kernel, const void* p, int32_t n, int cs, int smem, cudaStream_t s);
 template <typename P>
 int launch_ring(const void* kernel, const P& p, int32_t n, int cs, int smem, cudaStream_t s) {
