@@ -41,11 +41,19 @@ struct RowScale {
   float f, hi, m, l2;
   int32_t live, usual;
 };
+// What the listed entries need: the reference and logarithm of the whole sum, the teacher's
+// rest and the logarithm of the student's.
+struct RowSums {
+  float m, ls, pr, lqr;
+  int32_t has;
+};
 struct TeamSmem {
   int32_t id[kMaxTop];
+  __align__(16) int32_t vec[kMaxTop];   // vectors of the ids
   float p[kMaxTop], x[kMaxTop];
   float red[2][kFinWarps];
   float pre_o[kFinWarps][2], pre_in[kFinWarps][2];   // sums of the listed vectors and of the last entries
+  RowSums res[2];                                    // by turns
   float in[2][kMaxCluster][4];                       // the CTAs' sums, of every other row of the team
 };
 struct DistillSmem {
@@ -166,28 +174,30 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
           const int cnt = min(rs.stage, nvec - j * rs.stage);
           if (cnt <= 0) break;
           if (!(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) return;
-          uint4 w[kPer];
-          float mx = load_slot<T>(slots + (size_t)pos.slot * rs.stage, cnt, w);
+          const uint4* slot = slots + (size_t)pos.slot * rs.stage;
+          for (int base = 0; base < cnt; base += kPer * kCons) {
+            uint4 w[kPer];
+            float mx = load_slot<T>(slot + base, cnt - base, w);
+            if (p.tail) {
+              bool any = false;
+#pragma unroll
+              for (int q = 0; q < kPer; q++) {
+                const int i = base + q * kCons + (tid & ~31);
+                const uint32_t word = i < cnt ? bits[(j * rs.stage + i) >> 5] : 0;
+                if (word) {
+                  any = true;
+                  if (word >> lane & 1) w[q] = Raw<T>::masked();
+                }
+              }
+              if (any) mx = Raw<T>::max(w);
+            }
+            tm = fmaxf(tm, mx);
+            st.add(w, cnt - base, mx, c2);
+          }
           if (kMode != kHeld) {
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
           }
-          if (p.tail) {
-            bool any = false;
-#pragma unroll
-            for (int q = 0; q < kPer; q++) {
-              if (q * kCons >= cnt) continue;
-              const int at = (j * rs.stage + q * kCons + (tid & ~31)) >> 5;
-              const uint32_t word = at < p.words ? bits[at] : 0;
-              if (word) {
-                any = true;
-                if (word >> lane & 1) w[q] = Raw<T>::masked();
-              }
-            }
-            if (any) mx = Raw<T>::max(w);
-          }
-          tm = fmaxf(tm, mx);
-          st.add(w, cnt, mx, c2);
           pos.next(rs.n_slots);
         }
       }
@@ -214,29 +224,30 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         if (kMode == kAgain && held && !(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) return;
         RingPos& at = kMode == kAgain ? pos : pos2;
         const uint4* slot = slots + (size_t)at.slot * rs.stage;
-#pragma unroll
-        for (int q = 0; q < kPer; q++) {
-          const int i = q * kCons + tid;
-          if (i >= cnt) continue;
-          uint4 o = make_uint4(0, 0, 0, 0);
-          if (sc.live) {
+        uint4* const dst = out + j * rs.stage;
+        if (!sc.live) {
+          for (int i = tid; i < cnt; i += kCons) __stcs(dst + i, make_uint4(0, 0, 0, 0));
+        } else if (sc.usual) {
+#pragma unroll kPer
+          for (int i = tid; i < cnt; i += kCons) {
             const uint4 w = slot[i];
             float g[E];
 #pragma unroll
             for (int e = 0; e < E / 2; e++) {
               float y0, y1;
-              if (sc.usual) {
-                unpack2(fma2(Raw<T>::pair(w, e), cc, hi), y0, y1);
-              } else {
-                unpack2(Raw<T>::pair(w, e), y0, y1);
-                y0 = max_nan((y0 - sc.m) * c2 - sc.l2, kCut);
-                y1 = max_nan((y1 - sc.m) * c2 - sc.l2, kCut);
-              }
+              unpack2(fma2(Raw<T>::pair(w, e), cc, hi), y0, y1);
               unpack2(mul2(pack2(ex2f(y0), ex2f(y1)), ff), g[2 * e], g[2 * e + 1]);
             }
-            o = VT::pack(g);
+            __stcs(dst + i, VT::pack(g));
           }
-          __stcs(out + j * rs.stage + i, o);
+        } else {
+          for (int i = tid; i < cnt; i += kCons) {
+            float x[E], g[E];
+            VT::cvt(slot[i], x);
+#pragma unroll
+            for (int e = 0; e < E; e++) g[e] = sc.f * ex2f(max_nan((x[e] - sc.m) * c2 - sc.l2, kCut));
+            __stcs(dst + i, VT::pack(g));
+          }
         }
         if (held) {
           __syncwarp();
@@ -292,7 +303,8 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         }
         return;
       }
-      ts.id[ft] = ft < p.k ? en.id : -1;
+      ts.id[ft] = en.id;
+      ts.vec[ft] = en.id < 0 ? -1 : en.id / E;
       if (p.tail) {
         for (int i = ft; i < p.words; i += kFin) bits[i] = 0;
         en.lp = z;
@@ -320,12 +332,20 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         uint32_t mask = 0;
         bool first_vec = true;
         en.first = true;
-        for (int i = 0; i < p.k; i++) {
+        auto same = [&](int i) {
           const int other = ts.id[i];
-          if (other < 0 || other / E != vec) continue;
           mask |= 1u << (other % E);
           first_vec = first_vec && i >= ft;
           if (other == en.id) en.sub += ts.p[i], en.first = en.first && i >= ft;
+        };
+        for (int i = 0; i < p.k; i += 4) {   // entries past k have vec -1
+          const int4 o4 = *reinterpret_cast<const int4*>(&ts.vec[i]);
+          if (o4.x == vec || o4.y == vec || o4.z == vec || o4.w == vec) {
+            if (o4.x == vec) same(i);
+            if (o4.y == vec) same(i + 1);
+            if (o4.z == vec) same(i + 2);
+            if (o4.w == vec) same(i + 3);
+          }
         }
         if (p.tail && vec >= v0 && vec < v0 + nvec && first_vec) {
           const int at = vec - v0;
@@ -352,8 +372,8 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         if (tail_x > s.m) s.rebase(tail_x, c2);
         s.add(tail_x, c2);
       }
-      warp_merge(o, c2);
-      warp_merge(in, c2);
+      if (p.tail || tail_n > 0) warp_merge(o, c2);
+      if (p.tail) warp_merge(in, c2);
       if (lane == 0) {
         ts.pre_o[wi][0] = o.m, ts.pre_o[wi][1] = o.s;
         ts.pre_in[wi][0] = in.m, ts.pre_in[wi][1] = in.s;
@@ -363,77 +383,92 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
     if (first_row < p.n) prepare(first_row);
     for (int r = first_row, it = par; r < p.n; r += 2 * n_clusters, it += 2) {
       const uint32_t ph = (it >> 1) & 1;
-      if (!fin_all(ring_wait(&bar.part_full[par], ph, p.status), par)) break;
-      float kl = 0.f, fix = 0.f;
-      RowScale sc = {0.f, 0.f, 0.f, 0.f, 0, 1};
-      Stat o, in;
-      o.init();
-      in.init();
-      if (live) {
-        if (lane < kConsWarps) o.m = ss.part[par][lane][0], o.s = ss.part[par][lane][1];
-        else if (lane < kConsWarps + kFinWarps) o.m = ts.pre_o[lane - kConsWarps][0], o.s = ts.pre_o[lane - kConsWarps][1];
-        if (lane < kFinWarps) in.m = ts.pre_in[lane][0], in.s = ts.pre_in[lane][1];
-        warp_merge(o, c2);
-        warp_merge(in, c2);
-      }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bar.part_empty[par]);
-      if (rs.cs > 1) {
-        // every CTA to every CTA; in[] and the barriers by turns, so that a fast CTA's next row
-        // meets nobody who still reads or waits for this one
-        if (ft < rs.cs) {
-          const uint32_t dst = map_rank(tc::smem_u32(ts.in[ph][rank]), ft);
-          st_remote(dst, o.m);
-          st_remote(dst + 4, o.s);
-          st_remote(dst + 8, in.m);
-          st_remote(dst + 12, in.s);
-          arrive_remote(map_rank(tc::smem_u32(&bar.joined[par][ph]), ft));
-        }
-        if (!fin_all(ring_wait<true>(&bar.joined[par][ph], (it >> 2) & 1, p.status), par)) break;
+      bool ok = true;
+      if (wi == 0) {
+        // the row's sums and what the gradient pass needs of them, by one warp: the consumers
+        // wait for it
+        ok = warp_wait(&bar.part_full[par], ph, p.status);
+        Stat o, in;
         o.init();
         in.init();
-        if (lane < rs.cs) {
-          const float* q = ts.in[ph][lane];
-          o.m = q[0], o.s = q[1], in.m = q[2], in.s = q[3];
+        if (ok && live) {
+          if (lane < kConsWarps) o.m = ss.part[par][lane][0], o.s = ss.part[par][lane][1];
+          else if (lane < kConsWarps + kFinWarps) o.m = ts.pre_o[lane - kConsWarps][0], o.s = ts.pre_o[lane - kConsWarps][1];
+          warp_merge(o, c2);
+          if (p.tail) {
+            if (lane < kFinWarps) in.m = ts.pre_in[lane][0], in.s = ts.pre_in[lane][1];
+            warp_merge(in, c2);
+          }
         }
-        warp_merge(o, c2);
-        warp_merge(in, c2);
-      }
-      Stat all = o;
-      all.merge(in.m, in.s, 0.f, c2);
-      const bool has = live && all.s != 0.f;
-      if (has) {
-        const float ls = logf(all.s), lo = logf(o.s);
-        if (o.s == 0.f) pr = 0.f;   // nothing outside the list has mass
-        const float lqr = (o.m - all.m) * p.c + lo - ls;
-        const float sum = total + pr;
-        const float lq = en.id >= 0 ? (en.x - all.m) * p.c - ls : 0.f;
-        if (rank == 0) {
-          kl = fin_fold(en.p != 0.f ? en.p * (en.lp - lq) : 0.f, ts, par, buf);
-          if (pr != 0.f) kl += pr * (logf(pr) - lqr);
+        if (ok && rs.cs > 1) {
+          // every CTA to every CTA; in[] and the barriers by turns, so that a fast CTA's next
+          // row meets nobody who still reads or waits for this one
+          if (lane < rs.cs) {
+            const uint32_t dst = map_rank(tc::smem_u32(ts.in[ph][rank]), lane);
+            st_remote(dst, o.m);
+            st_remote(dst + 4, o.s);
+            st_remote(dst + 8, in.m);
+            st_remote(dst + 12, in.s);
+            arrive_remote(map_rank(tc::smem_u32(&bar.joined[par][ph]), lane));
+          }
+          ok = __all_sync(0xffffffffu, ring_wait<true>(&bar.joined[par][ph], (it >> 2) & 1, p.status));
+          o.init();
+          in.init();
+          if (lane < rs.cs) {
+            const float* q = ts.in[ph][lane];
+            o.m = q[0], o.s = q[1], in.m = q[2], in.s = q[3];
+          }
+          warp_merge(o, c2);
+          if (p.tail) warp_merge(in, c2);
         }
-        if (kMode != kNone) {
+        Stat all = o;
+        if (p.tail) all.merge(in.m, in.s, 0.f, c2);
+        RowSums res = {all.m, 0.f, 0.f, 0.f, 0};
+        RowScale sc = {0.f, 0.f, 0.f, 0.f, 0, 1};
+        if (live && all.s != 0.f) {
+          const float lo = logf(o.s);
+          res.has = 1;
+          res.ls = logf(all.s);
+          res.pr = o.s == 0.f ? 0.f : pr;   // dropped where nothing outside the list has mass
+          res.lqr = (o.m - all.m) * p.c + lo - res.ls;
           const float f = p.gs * w * p.c;
-          fix = f * (expf(lq) * sum - en.sub);
           sc.live = 1;
-          sc.f = o.s == 0.f ? 0.f : f * (p.tail ? expf(lqr) * sum - pr : sum);
+          sc.f = o.s == 0.f ? 0.f : f * (p.tail ? expf(res.lqr) * (total + res.pr) - res.pr : total);
           if (o.s != 0.f) sc.m = o.m, sc.l2 = lo * kLog2e;
           sc.usual = StageStat<T, false>::usual(sc.m, c2);
-          // hi and what it leaves out, which goes into the factor
-          const double e = (double)sc.m * c2 + (double)sc.l2;
-          sc.hi = (float)e;
-          if (sc.usual) sc.f *= ex2f((float)(sc.hi - e));
+          // hi = c2 m + l2 rounded; what it leaves out goes into the factor
+          const float a = sc.m * c2, ae = fmaf(sc.m, c2, -a);
+          sc.hi = a + sc.l2;
+          const float b = sc.hi - a;
+          if (sc.usual) sc.f *= ex2f(-(ae + ((a - (sc.hi - b)) + (sc.l2 - b))));
+        }
+        if (lane == 0) {
+          if (kMode != kNone) {
+            ss.scale[par] = sc;
+            tc::mbar_arrive(&bar.scal_full[par]);
+          }
+          ts.res[ph] = res;
         }
       }
-      if (ft == 0) {
+      if (!fin_all(ok, par)) break;
+      if (lane == 0) tc::mbar_arrive(&bar.part_empty[par]);
+      const RowSums res = ts.res[ph];
+      const bool has = res.has;
+      float fix = 0.f;
+      if (has) {
+        const float lq = en.id >= 0 ? (en.x - res.m) * p.c - res.ls : 0.f;
         if (rank == 0) {
-          p.row_kl[p.row0 + r] = kl;
-          if (p.part) p.part[r] = has ? w * kl : 0.f;
+          float kl = fin_fold(en.p != 0.f ? en.p * (en.lp - lq) : 0.f, ts, par, buf);
+          if (res.pr != 0.f) kl += res.pr * (logf(res.pr) - res.lqr);
+          if (ft == 0) {
+            p.row_kl[p.row0 + r] = kl;
+            if (p.part) p.part[r] = w * kl;
+          }
         }
-        if (kMode != kNone) {
-          ss.scale[par] = sc;
-          tc::mbar_arrive(&bar.scal_full[par]);
-        }
+        fix = p.gs * w * p.c * (expf(lq) * (total + res.pr) - en.sub);
+      } else if (rank == 0 && ft == 0) {
+        p.row_kl[p.row0 + r] = 0.f;
+        if (p.part) p.part[r] = 0.f;
       }
       const Entry done = en;
       const float last_x = tail_x;
@@ -447,6 +482,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
           const int vec = done.id / E;
           if (vec < nv ? vec >= v0 && vec < v0 + nvec : tail_n > 0) VT::put(grow + done.id, fix);
         }
+        const RowScale& sc = ss.scale[par];   // written again after the team's next row
         if (ft < tail_n && !(has && last_listed))
           VT::put(grow + nv * E + ft, sc.live ? sc.f * ex2f(sc.usual ? fmaf(last_x, c2, -sc.hi)
                                                                       : max_nan((last_x - sc.m) * c2 - sc.l2, kCut))

@@ -34,14 +34,15 @@ struct RingShape {
   int32_t n_slots;
 };
 
-// cs CTAs per row, ring of at most `bytes`; even: stages of one size, so that the slots hold
-// the most rows, otherwise full ones and a rest.
+// cs CTAs per row, ring of at most `bytes`.  Stages of kCons * kPer vectors and a rest, or, even,
+// of one size up to twice that, so that the slots hold the most rows.
 inline RingShape ring_shape(int64_t nv, int cs, int bytes, bool even) {
   RingShape s;
   s.cs = cs;
   s.seg = (int32_t)((nv + cs - 1) / cs);
-  s.n_stages = (s.seg + kCons * kPer - 1) / (kCons * kPer);
-  s.stage = s.n_stages > 1 && !even ? kCons * kPer : s.n_stages ? ((s.seg + s.n_stages - 1) / s.n_stages + 31) / 32 * 32 : 32;
+  const int most = kCons * kPer * (even ? 2 : 1);
+  s.n_stages = (s.seg + most - 1) / most;
+  s.stage = s.n_stages > 1 && !even ? most : s.n_stages ? ((s.seg + s.n_stages - 1) / s.n_stages + 31) / 32 * 32 : 32;
   s.n_slots = bytes / (s.stage * 16);
   if (s.n_slots > kMaxSlots) s.n_slots = kMaxSlots;
   return s;
@@ -299,11 +300,11 @@ __device__ __forceinline__ void warp_merge(Stat& st, float c2) {
   }
 }
 
-// A consumer thread's vectors of a slot that holds cnt of them (masked past the end), and the
-// largest entry.
+// A consumer thread's next kPer vectors of a slot that holds cnt of them from here on (masked
+// past the end), and the largest entry.
 template <typename T>
 __device__ __forceinline__ float load_slot(const uint4* slot, int cnt, uint4 (&w)[kPer]) {
-  if (cnt == kPer * kCons) {
+  if (cnt >= kPer * kCons) {
 #pragma unroll
     for (int q = 0; q < kPer; q++) w[q] = slot[q * kCons + threadIdx.x];
   } else {
