@@ -51,6 +51,7 @@ struct TeamSmem {
   int32_t id[kMaxTop];
   __align__(16) int32_t vec[kMaxTop];   // vectors of the ids
   float p[kMaxTop], x[kMaxTop];
+  uint32_t last;                       // listed ones of the row's last entries
   float red[2][kFinWarps];
   float pre_o[kFinWarps][2], pre_in[kFinWarps][2];   // sums of the listed vectors and of the last entries
   RowSums res[2];                                    // by turns
@@ -282,29 +283,46 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
     Entry en;
     float w = 0.f, pr = 0.f, total = 0.f, tail_x = 0.f;
     bool live = false, tail_listed = false;
+    // its weight and entries are fetched a row earlier
+    int next_id = -1;
+    float next_z = 0.f, next_w = 0.f;
+    auto fetch = [&](int r) {
+      if (r >= p.n) return;
+      next_w = weight(r);
+      if (ft < p.k) {
+        next_id = p.t_ids[(size_t)r * p.k + ft];
+        next_z = p.t_val[(size_t)r * p.k + ft];
+      }
+    };
     auto prepare = [&](int r) {
       const T* row = logits + (size_t)r * p.ld;
       en = Entry();
-      w = weight(r);
+      w = next_w;
       live = w != 0.f;
       float z = -INFINITY;
       if (live && ft < p.k) {
-        en.id = p.t_ids[(size_t)r * p.k + ft];
-        z = p.t_val[(size_t)r * p.k + ft];
+        en.id = next_id;
+        z = next_z;
         if (en.id >= p.V) atomicExch(p.status, OCTO_EINVAL);
         if (en.id < 0 || en.id >= p.V || z == -INFINITY) en.id = -1, z = -INFINITY;
       }
-      if (live && en.id >= 0) en.x = VT::get(row + en.id);
+      const int vec = en.id < 0 ? -1 : en.id / E;
+      const bool own = vec >= v0 && vec < v0 + nvec;
+      uint4 wv = make_uint4(0, 0, 0, 0);
+      if (en.id >= 0) en.x = VT::get(row + en.id);
+      if (p.tail && own) wv = reinterpret_cast<const uint4*>(row)[vec];
       tail_x = live && ft < tail_n ? VT::get(row + nv * E + ft) : -INFINITY;
       if (!live) {
         if (p.tail) {
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bar.pre_full[par]);
         }
+        fin_sync(par);
         return;
       }
       ts.id[ft] = en.id;
-      ts.vec[ft] = en.id < 0 ? -1 : en.id / E;
+      ts.vec[ft] = vec;
+      if (ft == 0) ts.last = 0;
       if (p.tail) {
         for (int i = ft; i < p.words; i += kFin) bits[i] = 0;
         en.lp = z;
@@ -322,36 +340,38 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         total = fin_fold(en.p, ts, par, buf);
       }
       ts.p[ft] = en.p;
-      ts.x[ft] = en.x;   // waits for the load: a peer may overwrite the row once it has this CTA's sums
+      if (vec == nv) atomicOr(&ts.last, 1u << (en.id % E));
       fin_sync(par);
       Stat o, in;
       o.init();
       in.init();
       if (en.id >= 0) {
-        const int vec = en.id / E;
-        uint32_t mask = 0;
+        uint32_t mask = 1u << (en.id % E);
         bool first_vec = true;
+        en.sub = en.p;
         en.first = true;
-        auto same = [&](int i) {
+        auto same = [&](int i) {   // another entry in this one's vector
           const int other = ts.id[i];
           mask |= 1u << (other % E);
-          first_vec = first_vec && i >= ft;
-          if (other == en.id) en.sub += ts.p[i], en.first = en.first && i >= ft;
+          first_vec = first_vec && i > ft;
+          if (other == en.id) en.sub += ts.p[i], en.first = en.first && i > ft;
         };
         for (int i = 0; i < p.k; i += 4) {   // entries past k have vec -1
           const int4 o4 = *reinterpret_cast<const int4*>(&ts.vec[i]);
-          if (o4.x == vec || o4.y == vec || o4.z == vec || o4.w == vec) {
-            if (o4.x == vec) same(i);
-            if (o4.y == vec) same(i + 1);
-            if (o4.z == vec) same(i + 2);
-            if (o4.w == vec) same(i + 3);
+          const bool x = o4.x == vec && i != ft, y = o4.y == vec && i + 1 != ft, z4 = o4.z == vec && i + 2 != ft,
+                     w4 = o4.w == vec && i + 3 != ft;
+          if (x || y || z4 || w4) {
+            if (x) same(i);
+            if (y) same(i + 1);
+            if (z4) same(i + 2);
+            if (w4) same(i + 3);
           }
         }
-        if (p.tail && vec >= v0 && vec < v0 + nvec && first_vec) {
+        if (p.tail && own && first_vec) {
           const int at = vec - v0;
           atomicOr(&bits[at >> 5], 1u << (at & 31));
           float x[E];
-          VT::cvt(reinterpret_cast<const uint4*>(row)[vec], x);
+          VT::cvt(wv, x);
 #pragma unroll
           for (int e = 0; e < E; e++) {
             Stat& s = mask >> e & 1 ? in : o;
@@ -366,8 +386,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       }
       tail_listed = false;
       if (ft < tail_n) {
-        if (p.tail || kMode != kNone)
-          for (int i = 0; i < p.k; i++) tail_listed = tail_listed || ts.id[i] == nv * E + ft;
+        tail_listed = ts.last >> ft & 1;
         Stat& s = p.tail && tail_listed ? in : o;
         if (tail_x > s.m) s.rebase(tail_x, c2);
         s.add(tail_x, c2);
@@ -378,11 +397,15 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         ts.pre_o[wi][0] = o.m, ts.pre_o[wi][1] = o.s;
         ts.pre_in[wi][0] = in.m, ts.pre_in[wi][1] = in.s;
       }
+      ts.x[ft] = en.x;   // waits for the load: a peer may overwrite the row once it has this CTA's sums
+      fin_sync(par);
     };
     const int first_row = cluster + par * n_clusters;
+    fetch(first_row);
     if (first_row < p.n) prepare(first_row);
     for (int r = first_row, it = par; r < p.n; r += 2 * n_clusters, it += 2) {
       const uint32_t ph = (it >> 1) & 1;
+      fetch(r + 2 * n_clusters);
       bool ok = true;
       if (wi == 0) {
         // the row's sums and what the gradient pass needs of them, by one warp: the consumers
