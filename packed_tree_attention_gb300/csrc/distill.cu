@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
             const uint32_t bytes = (uint32_t)min(rs.stage, nvec - b) * 16;
             tc::mbar_expect_tx(&bar.full[pos.slot], bytes);
             bulk_load(slots + (size_t)pos.slot * rs.stage, src + (size_t)b * E, bytes, &bar.full[pos.slot]);
-            pos.next(rs.n_slots);
+            pos.skip(1, rs.n_slots);
             issued++;
           }
       }
@@ -159,7 +159,15 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
     }
   } else if (tid < kCons) {
     // ---- consumers ----
+    const int group = tid / kGroupThreads, t = tid % kGroupThreads;
+    const int n_st = (nvec + rs.stage - 1) / rs.stage, n_sub = rs.stage / kSub;
+    // the next stages of this group in the two passes' order (kAgain: of both), and which of
+    // the next row's stages those are
     RingPos pos, pos2;
+    pos.skip(group, rs.n_slots);
+    pos2.skip(group, rs.n_slots);
+    int next = group, next2 = group;
+    auto to_next_row = [&](int& next) { next = (next - n_st) & (kGroups - 1); };
     bool ok = true;
     StageStat<T, false> st;
     // sums over the entries outside the list
@@ -171,36 +179,34 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       if (p.tail && !(ok = warp_wait(&bar.pre_full[par], ph, p.status))) return;
       if (live) {
         const uint32_t* bits = bitmap + par * p.words;
-        for (int j = 0; j < rs.n_stages; j++) {
-          const int cnt = min(rs.stage, nvec - j * rs.stage);
-          if (cnt <= 0) break;
+        for (int j = next; j < n_st; j += kGroups) {
+          const int cnt = nvec - j * rs.stage;
           if (!(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) return;
           const uint4* slot = slots + (size_t)pos.slot * rs.stage;
-          for (int base = 0; base < cnt; base += kPer * kCons) {
+          for (int u = 0; u < n_sub; u++) {
+            const int left = cnt - u * kSub;
+            if (left <= 0) break;
             uint4 w[kPer];
-            float mx = load_slot<T>(slot + base, cnt - base, w);
+            load_sub<T>(slot + u * kSub, left, t, w);
+            if (kMode != kHeld && (u + 1 == n_sub || left <= kSub)) {
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
+            }
             if (p.tail) {
-              bool any = false;
 #pragma unroll
               for (int q = 0; q < kPer; q++) {
-                const int i = base + q * kCons + (tid & ~31);
-                const uint32_t word = i < cnt ? bits[(j * rs.stage + i) >> 5] : 0;
-                if (word) {
-                  any = true;
-                  if (word >> lane & 1) w[q] = Raw<T>::masked();
-                }
+                const int i = q * kGroupThreads + (t & ~31);
+                const uint32_t word = i < left ? bits[(j * rs.stage + u * kSub + i) >> 5] : 0;
+                if (word >> lane & 1) w[q] = Raw<T>::masked();
               }
-              if (any) mx = Raw<T>::max(w);
             }
+            const float mx = Raw<T>::max(w);
             tm = fmaxf(tm, mx);
-            st.add(w, cnt - base, mx, c2);
+            st.add(w, left, mx, c2);
           }
-          if (kMode != kHeld) {
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
-          }
-          pos.next(rs.n_slots);
+          pos.skip(kGroups, rs.n_slots);
         }
+        to_next_row(next);
       }
       Stat tot = st.total(tm, c2);
       warp_merge(tot, c2);
@@ -219,18 +225,18 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       const RowScale sc = ss.scale[par];
       uint4* out = reinterpret_cast<uint4*>(dlogits + (size_t)r * p.ld) + v0;
       const f2 cc = pack2(c2, c2), hi = pack2(-sc.hi, -sc.hi), ff = pack2(sc.f, sc.f);
-      for (int j = 0; j < rs.n_stages; j++) {
+      RingPos& at = kMode == kAgain ? pos : pos2;
+      int& from = kMode == kAgain ? next : next2;
+      for (int j = held ? from : group; j < n_st; j += kGroups) {
         const int cnt = min(rs.stage, nvec - j * rs.stage);
-        if (cnt <= 0) break;
-        if (kMode == kAgain && held && !(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) return;
-        RingPos& at = kMode == kAgain ? pos : pos2;
+        if (kMode == kAgain && held && !(ok = warp_wait(&bar.full[at.slot], at.round, p.status))) return;
         const uint4* slot = slots + (size_t)at.slot * rs.stage;
         uint4* const dst = out + j * rs.stage;
         if (!sc.live) {
-          for (int i = tid; i < cnt; i += kCons) __stcs(dst + i, make_uint4(0, 0, 0, 0));
+          for (int i = t; i < cnt; i += kGroupThreads) __stcs(dst + i, make_uint4(0, 0, 0, 0));
         } else if (sc.usual) {
 #pragma unroll kPer
-          for (int i = tid; i < cnt; i += kCons) {
+          for (int i = t; i < cnt; i += kGroupThreads) {
             const uint4 w = slot[i];
             float g[E];
 #pragma unroll
@@ -242,7 +248,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
             __stcs(dst + i, VT::pack(g));
           }
         } else {
-          for (int i = tid; i < cnt; i += kCons) {
+          for (int i = t; i < cnt; i += kGroupThreads) {
             float x[E], g[E];
             VT::cvt(slot[i], x);
 #pragma unroll
@@ -253,9 +259,10 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         if (held) {
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bar.empty[at.slot]);
-          at.next(rs.n_slots);
+          at.skip(kGroups, rs.n_slots);
         }
       }
+      if (held) to_next_row(from);
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bar.p2_done[par]);
     };
@@ -523,7 +530,7 @@ int launch_distill(DistillParams& p, cudaStream_t s) {
   const int64_t nv = p.V / Vec<T>::E;
   const void* f = (const void*)k_distill<T, kNone>;
   auto words = [&](int cs) { return (int)(((nv + cs - 1) / cs + 31) / 32); };
-  auto shape = [&](int cs) { return ring_shape(nv, cs, kSmemMax - slots_offset(words(cs)), true); };
+  auto shape = [&](int cs) { return ring_shape(nv, cs, kSmemMax - slots_offset(words(cs))); };
   int cs = 1;
   if (p.dlogits) {
     // as many CTAs as it takes for the ring to hold two rows' parts and a stage to come
@@ -537,8 +544,8 @@ int launch_distill(DistillParams& p, cudaStream_t s) {
   cs = few > cs ? few : cs;
   while (words(cs) * 4 * kTeams > 64 * 1024 && cs < kMaxCluster) cs *= 2;
   p.words = p.tail ? words(cs) : 0;
-  p.ring = ring_shape(nv, cs, kSmemMax - slots_offset(p.words), true);
-  if (p.ring.n_slots < 2) return OCTO_ENOTSUP;
+  p.ring = ring_shape(nv, cs, kSmemMax - slots_offset(p.words));
+  if (p.ring.n_slots < kGroups) return OCTO_ENOTSUP;
   return launch_ring(f, p, p.n, cs, slots_offset(p.words) + p.ring.n_slots * p.ring.stage * 16, s);
 }
 

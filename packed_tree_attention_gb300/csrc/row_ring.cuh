@@ -19,8 +19,11 @@ namespace rows {
 constexpr int kConsWarps = 16, kFinWarps = 4, kTeams = 2;   // finisher warps of a team
 constexpr int kCons = kConsWarps * 32, kFin = kFinWarps * 32;
 constexpr int kBlock = kCons + kTeams * kFin + 64;   // + the copying warp and one for look-ups
-constexpr int kPer = 4;                     // vectors of one thread in a stage
-constexpr int kMaxSlots = 24;
+constexpr int kGroups = 4;                  // consumer groups, a warp of each on every scheduler
+constexpr int kGroupThreads = kCons / kGroups;
+constexpr int kPer = 4;                     // vectors that a thread takes at once
+constexpr int kSub = kPer * kGroupThreads;  // and a group: stages are multiples of that
+constexpr int kMaxSlots = 28;
 constexpr int kMaxCluster = 8;
 constexpr int kFinBar = 1;                  // named barriers of the finisher teams: this and the next
 static_assert(kTeams == 2, "the barriers' pairs are the teams'");
@@ -34,17 +37,20 @@ struct RingShape {
   int32_t n_slots;
 };
 
-// cs CTAs per row, ring of at most `bytes`.  Stages of kCons * kPer vectors and a rest, or, even,
-// of one size up to twice that, so that the slots hold the most rows.
-inline RingShape ring_shape(int64_t nv, int cs, int bytes, bool even) {
+// cs CTAs per row, ring of at most `bytes`, stages of 1, 2 or 4 kSub.  Short stages give every
+// group its share of a short part, long ones cost fewer waits.  The slots are a multiple of the
+// groups, so that a slot is always the same group's: copies complete in no order, and a parity
+// wait on a slot whose last stage, another group's, had not come would take that phase's
+// predecessor for its own.
+inline RingShape ring_shape(int64_t nv, int cs, int bytes) {
   RingShape s;
   s.cs = cs;
   s.seg = (int32_t)((nv + cs - 1) / cs);
-  const int most = kCons * kPer * (even ? 2 : 1);
-  s.n_stages = (s.seg + most - 1) / most;
-  s.stage = s.n_stages > 1 && !even ? most : s.n_stages ? ((s.seg + s.n_stages - 1) / s.n_stages + 31) / 32 * 32 : 32;
+  s.stage = kSub * (s.seg <= 8 * kSub ? 1 : s.seg <= 40 * kSub ? 2 : 4);
+  s.n_stages = (s.seg + s.stage - 1) / s.stage;
   s.n_slots = bytes / (s.stage * 16);
   if (s.n_slots > kMaxSlots) s.n_slots = kMaxSlots;
+  s.n_slots -= s.n_slots % kGroups;
   return s;
 }
 
@@ -256,16 +262,16 @@ struct StageStat {
   }
   template <bool kUsual>
   __device__ __forceinline__ void add_all(const uint4 (&w)[kPer], int cnt, float c2) {
-    if (cnt > (kPer - 1) * kCons) {
+    if (cnt > (kPer - 1) * kGroupThreads) {
 #pragma unroll
       for (int q = 0; q < kPer; q++) add_vec<kUsual>(w[q], c2);
     } else {
 #pragma unroll
       for (int q = 0; q < kPer - 1; q++)
-        if (q * kCons < cnt) add_vec<kUsual>(w[q], c2);
+        if (q * kGroupThreads < cnt) add_vec<kUsual>(w[q], c2);
     }
   }
-  // the vectors w[q] with q * kCons < cnt, the largest entry of all kPer being mx
+  // the vectors w[q] with q * kGroupThreads < cnt, the largest entry of all kPer being mx
   __device__ __forceinline__ void add(const uint4 (&w)[kPer], int cnt, float mx, float c2) {
     if ((mx - m) * c2 > kSlack) raise(mx, c2);
     if (usual(m, c2)) add_all<true>(w, cnt, c2);
@@ -300,21 +306,19 @@ __device__ __forceinline__ void warp_merge(Stat& st, float c2) {
   }
 }
 
-// A consumer thread's next kPer vectors of a slot that holds cnt of them from here on (masked
-// past the end), and the largest entry.
+// Thread t of a group: its kPer vectors of the cnt ones from `slot` on (masked past the end).
 template <typename T>
-__device__ __forceinline__ float load_slot(const uint4* slot, int cnt, uint4 (&w)[kPer]) {
-  if (cnt >= kPer * kCons) {
+__device__ __forceinline__ void load_sub(const uint4* slot, int cnt, int t, uint4 (&w)[kPer]) {
+  if (cnt >= kSub) {
 #pragma unroll
-    for (int q = 0; q < kPer; q++) w[q] = slot[q * kCons + threadIdx.x];
+    for (int q = 0; q < kPer; q++) w[q] = slot[q * kGroupThreads + t];
   } else {
 #pragma unroll
     for (int q = 0; q < kPer; q++) {
-      const int i = q * kCons + threadIdx.x;
+      const int i = q * kGroupThreads + t;
       w[q] = i < cnt ? slot[i] : Raw<T>::masked();
     }
   }
-  return Raw<T>::max(w);
 }
 
 // The barriers of a CTA.
@@ -325,7 +329,7 @@ struct RingBars {
   uint64_t scal_full[2], scal_empty[2];   // a row's results: written, read by who needs them
   uint64_t pre_full[2], p2_done[2];       // distillation
   __device__ void init(int cs) {
-    for (int i = 0; i < kMaxSlots; i++) tc::mbar_init(&full[i], 1), tc::mbar_init(&empty[i], kConsWarps);
+    for (int i = 0; i < kMaxSlots; i++) tc::mbar_init(&full[i], 1), tc::mbar_init(&empty[i], kConsWarps / kGroups);
     for (int i = 0; i < 2; i++) {
       tc::mbar_init(&part_full[i], kConsWarps);
       tc::mbar_init(&part_empty[i], kFinWarps);
@@ -343,8 +347,9 @@ struct RingBars {
 struct RingPos {
   int slot = 0;
   uint32_t round = 0;
-  __device__ __forceinline__ void next(int n_slots) {
-    if (++slot == n_slots) slot = 0, round ^= 1;
+  __device__ __forceinline__ void skip(int n, int n_slots) {
+    slot += n;
+    while (slot >= n_slots) slot -= n_slots, round ^= 1;
   }
 };
 

@@ -9,6 +9,8 @@
 // (m, ln S) is kept rather than m c + ln S: at logits in the thousands the sum's rounding
 // would be a per-mille error of every probability that the gradient forms from it.
 
+#include <algorithm>
+
 #include "row_ring.cuh"
 
 namespace octo {
@@ -16,8 +18,8 @@ namespace {
 
 using namespace rows;
 
-constexpr int kGroupStages = 10;     // stage classes of the group maxima
-constexpr int kMaxCand = 1280, kMaxGroups = 512, kMaxTrim = 512;
+constexpr int kMaxBins = 10;         // bins of a thread's vectors
+constexpr int kMaxCand = 1280, kMaxHits = 512, kMaxTrim = 512;
 static_assert(kMaxCand >= kMaxCluster * kMaxTop, "the CTAs' alternatives are joined in cand");
 
 struct ScoreParams {
@@ -34,7 +36,13 @@ struct ScoreParams {
   SuccTable succ;
   int32_t* status;
   RingShape ring;
+  // A thread's vectors, kPer at a time in `subs` turns at most, fall into `bins` bins.
+  int32_t subs, bins;
 };
+
+// The first of a CTA's n_st stages of its row `it` that is the group's: the groups take the
+// stages in turn, on over row ends.
+__device__ __forceinline__ int first_stage(int group, int it, int n_st) { return (group - it * n_st) & (kGroups - 1); }
 
 // Shared memory of the finishers; the ring's slots follow.
 struct ScoreSmem {
@@ -51,10 +59,10 @@ struct TopSmem {
   unsigned long long cand[kMaxCand];
   unsigned long long trim[kMaxTrim];
   unsigned long long sorted[kMaxTop];
-  uint16_t group[kMaxGroups];
+  uint16_t hit[kMaxHits];
   uint32_t red[2][kFinWarps];
-  int32_t n_groups, n_cand, n_ties, n_trim;
-  float gmax[kGroupStages][kCons];       // largest entry of each group: a thread's vectors in a class of stages
+  int32_t n_hits, n_cand, n_ties, n_trim;
+  float bmax[kMaxBins][kCons];           // largest entry of each bin of each thread's vectors
   float tmax[kCons];                     // and of each thread
 };
 
@@ -140,23 +148,23 @@ __device__ int rank_cand(TopSmem& ts, int team, int k, uint32_t lo, int& buf) {
 // The k largest entries of a CTA's part of a row, best first, in ts.sorted; returns how many
 // (fewer than k only where the part has no more that are not NaN).  Called by the finishers.
 //
-// The consumers leave the largest entry that each thread saw, and that of each group of its
+// The consumers leave the largest entry that each thread saw, and that of each bin of its
 // vectors.  The k-th largest of the 512 threads' maxima, tau, is a lower bound of the part's
-// k-th largest entry, so only groups that reach tau are read again (from L2): for entries in
-// no order about 512 ln(512 / (512 - k)) groups, 21 for k = 20 and 147 for k = 128, of 16 to 32
+// k-th largest entry, so only bins that reach tau are read again (from L2): for entries in
+// no order about 512 ln(512 / (512 - k)) bins, 21 for k = 20 and 147 for k = 128, of 16 to 32
 // entries.  Every warp finds tau for itself, 16 maxima a lane, by a bisection over the keys
 // that stops at a few threads more than k.  Arrives on `read` when the maxima are read, well
 // before the end.
 template <typename T>
-__device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, uint64_t* read, int team, int v0, int nvec,
-                        int tail_n, float tail_x) {
+__device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, uint64_t* read, int team, int it, int v0,
+                        int nvec, int tail_n, float tail_x) {
   using VT = Vec<T>;
   constexpr int E = VT::E, kKeys = kCons / 32;
   const int ft = fin_thread(team), lane = threadIdx.x & 31;
   const int k = p.k;
-  const int n_st = p.ring.n_stages, J = min(n_st, kGroupStages);
-  const int spc = n_st > kGroupStages ? (n_st + J - 1) / J : 1;   // most stages of a group
-  if (ft == 0) ts.n_groups = ts.n_cand = 0;
+  const int n_st = (nvec + p.ring.stage - 1) / p.ring.stage, n_sub = p.ring.stage / kSub;
+  const int per_bin = (p.subs + p.bins - 1) / p.bins;   // most turns of a bin
+  if (ft == 0) ts.n_hits = ts.n_cand = 0;
   uint32_t lo, hi;
   bool exact = false;
   {
@@ -192,8 +200,8 @@ __device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, uint64_
     exact = lo == hi;
   }
   fin_sync(team);
-  // groups that reach `from`
-  auto find_groups = [&](uint32_t from) {
+  // bins that reach `from`
+  auto find_bins = [&](uint32_t from) {
     const float ff = order_value(from);
     if (nvec > 0)
 #pragma unroll
@@ -201,13 +209,13 @@ __device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, uint64_
         if (ts.tmax[t] >= ff) {
           uint32_t hit = 0;
 #pragma unroll
-          for (int j = 0; j < kGroupStages; j++) hit |= (uint32_t)(j < J && ts.gmax[j][t] >= ff) << j;
-          int i = atomicAdd(&ts.n_groups, __popc(hit));
+          for (int j = 0; j < kMaxBins; j++) hit |= (uint32_t)(j < p.bins && ts.bmax[j][t] >= ff) << j;
+          int i = atomicAdd(&ts.n_hits, __popc(hit));
           for (; hit; hit &= hit - 1, i++)
-            if (i < kMaxGroups) ts.group[i] = (uint16_t)((__ffs(hit) - 1) * kCons + t);
+            if (i < kMaxHits) ts.hit[i] = (uint16_t)((__ffs(hit) - 1) * kCons + t);
         }
     fin_sync(team);
-    return ts.n_groups <= kMaxGroups;
+    return ts.n_hits <= kMaxHits;
   };
   auto release = [&] {
     __syncwarp();
@@ -216,23 +224,28 @@ __device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, uint64_
   // their entries of at least `from`, into cand
   auto collect = [&](uint32_t from) {
     const float ff = order_value(from);
-    const int ng = ts.n_groups;
     constexpr int U = 4;
-    const int items = ng * kPer * spc;
+    const int items = ts.n_hits * kPer * per_bin;
     for (int base = ft; base < items; base += U * kFin) {
       uint4 w[U];
       int at[U];
 #pragma unroll
       for (int u = 0; u < U; u++) {
-        const int it = base + u * kFin;
+        const int item = base + u * kFin;
         at[u] = -1;
-        if (it >= items) continue;
-        const int gi = spc == 1 ? it / kPer : it / (kPer * spc), sub = it - gi * kPer * spc;
-        const int g = ts.group[gi], jg = g / kCons;
-        const int st = spc == 1 ? jg : (jg * n_st + J - 1) / J + sub / kPer;
-        const int i = (sub % kPer) * kCons + g % kCons;
-        if (i >= p.ring.stage || st * p.ring.stage + i >= nvec || (spc > 1 && st * J / n_st != jg)) continue;
-        at[u] = v0 + st * p.ring.stage + i;
+        if (item >= items) continue;
+        const int h = per_bin == 1 ? item / kPer : item / (kPer * per_bin), q = item % kPer;
+        const int bin = ts.hit[h] / kCons, t = ts.hit[h] % kCons, group = t / kGroupThreads;
+        // the bin's turns: those with turn bins / subs = bin
+        int turn = bin;
+        if (p.subs > p.bins) {
+          turn = (bin * p.subs + p.bins - 1) / p.bins + (item / kPer - h * per_bin);
+          if (turn >= p.subs || turn * p.bins / p.subs != bin) continue;
+        }
+        const int j = first_stage(group, it, n_st) + turn / n_sub * kGroups;
+        const int i = j * p.ring.stage + turn % n_sub * kSub + q * kGroupThreads + t % kGroupThreads;
+        if (j >= n_st || i >= nvec) continue;
+        at[u] = v0 + i;
         w[u] = reinterpret_cast<const uint4*>(row)[at[u]];
       }
 #pragma unroll
@@ -264,16 +277,16 @@ __device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, uint64_
   int buf = 0;
   auto reset = [&] {
     fin_sync(team);
-    if (ft == 0) ts.n_groups = ts.n_cand = ts.n_ties = 0;
+    if (ft == 0) ts.n_hits = ts.n_cand = ts.n_ties = 0;
     fin_sync(team);
   };
   bool slow;
-  if (lo > order_key(-INFINITY) && find_groups(lo)) {
+  if (lo > order_key(-INFINITY) && find_bins(lo)) {
     release();
     if (collect(lo)) return rank_cand(ts, team, k, lo, buf);
     slow = true;
   } else {
-    // Most groups reach tau, as with equal entries in all of them (masked rows, rounded
+    // Most bins reach tau, as with equal entries in all of them (masked rows, rounded
     // logits).  With the exact tau fewer than k threads exceed it: take what exceeds tau, and
     // the entries equal to it in the order of their ids.
     while (!exact && lo < hi) {
@@ -285,12 +298,12 @@ __device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, uint64_
       else hi = mid - 1;
     }
     reset();
-    slow = !find_groups(lo + 1);
+    slow = !find_bins(lo + 1);
     release();
     slow = slow || !collect(lo + 1);
   }
   if (slow) {
-    // Few groups hold more than kMaxCand entries above tau: find the part's k-th largest
+    // Few bins hold more than kMaxCand entries above tau: find the part's k-th largest
     // entry by counting over the whole part.  Rare, and slow.
     uint32_t a = lo, b = 0xffffffffu;
     while (a < b) {
@@ -448,7 +461,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
           const uint32_t bytes = (uint32_t)min(rs.stage, nvec - b) * 16;
           tc::mbar_expect_tx(&bar.full[pos.slot], bytes);
           bulk_load(slots + (size_t)pos.slot * rs.stage, src + (size_t)b * E, bytes, &bar.full[pos.slot]);
-          pos.next(rs.n_slots);
+          pos.skip(1, rs.n_slots);
           issued++;
         }
       }
@@ -460,43 +473,51 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
         }
     }
   } else if (tid < kCons) {
-    // ---- consumers: sums of the part, group maxima ----
+    // ---- consumers: sums of the part, maxima of the bins ----
+    const int group = tid / kGroupThreads, t = tid % kGroupThreads;
+    const int n_st = (nvec + rs.stage - 1) / rs.stage, n_sub = rs.stage / kSub;
     RingPos pos;
+    pos.skip(group, rs.n_slots);
     bool ok = true;
-    const int J = min(rs.n_stages, kGroupStages);
     StageStat<T, true> st;
     for (int r = cluster, it = 0; r < p.n && ok; r += n_clusters, it++) {
       const int par = it & 1;
       st.init();
-      float gm = -INFINITY, tm = -INFINITY;
-      int jg = 0, frac = 0;
+      float bm = -INFINITY, tm = -INFINITY;
+      int bin = 0, frac = 0;
       // the finishers are done with this parity's buffers two rows ago
       if (kTop) ok = warp_wait(&bar.part_empty[par], ((it >> 1) & 1) ^ 1, p.status);
-      for (int j = 0; j < rs.n_stages && ok; j++) {
-        const int cnt = min(rs.stage, nvec - j * rs.stage);
-        if (cnt > 0) {
-          if (!(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) break;
-          const uint4* slot = slots + (size_t)pos.slot * rs.stage;
-          uint4 w[kPer];
-          const float mx = load_slot<T>(slot, cnt, w);
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
-          tm = fmaxf(tm, mx);
-          gm = fmaxf(gm, mx);
-          st.add(w, cnt, mx, c2);
-          pos.next(rs.n_slots);
-        }
-        if (kTop) {
-          // class of stage j: j J / n_stages
-          if ((frac += J) >= rs.n_stages) {
-            frac -= rs.n_stages;
-            top[par].gmax[jg++][tid] = gm;
-            gm = -INFINITY;
+      for (int j = first_stage(group, it, n_st); j < n_st && ok; j += kGroups) {
+        if (!(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) break;
+        const uint4* slot = slots + (size_t)pos.slot * rs.stage;
+        const int cnt = nvec - j * rs.stage;
+        for (int u = 0; u < n_sub; u++) {
+          const int left = cnt - u * kSub;
+          if (left > 0) {
+            uint4 w[kPer];
+            load_sub<T>(slot + u * kSub, left, t, w);
+            if (u + 1 == n_sub || left <= kSub) {
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
+            }
+            const float mx = Raw<T>::max(w);
+            tm = fmaxf(tm, mx);
+            bm = fmaxf(bm, mx);
+            st.add(w, left, mx, c2);
+          }
+          if (kTop && (frac += p.bins) >= p.subs) {
+            frac -= p.subs;
+            top[par].bmax[bin++][tid] = bm;
+            bm = -INFINITY;
           }
         }
+        pos.skip(kGroups, rs.n_slots);
       }
       if (!ok) break;
-      if (kTop) top[par].tmax[tid] = tm;
+      if (kTop) {
+        for (; bin < p.bins; bin++) top[par].bmax[bin][tid] = bm, bm = -INFINITY;
+        top[par].tmax[tid] = tm;
+      }
       Stat tot = st.total(tm, c2);
       warp_merge(tot, c2);
       if (!kTop) ok = warp_wait(&bar.part_empty[par], ((it >> 1) & 1) ^ 1, p.status);
@@ -530,7 +551,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
       warp_merge(st, c2);
       int n_top = 0;
       if (kTop) {
-        n_top = part_top<T>(row, p, ts, &bar.part_empty[par], par, v0, nvec, tail_n, tail_x);
+        n_top = part_top<T>(row, p, ts, &bar.part_empty[par], par, it, v0, nvec, tail_n, tail_x);
       } else {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bar.part_empty[par]);
@@ -724,7 +745,9 @@ int launch_score(ScoreParams& p, cudaStream_t s) {
   // 13.4 / 12.5 / 11.8 / 11.8 at k = 20)
   const int k = p.k;
   if (int st = pick_cluster(f, p.n, nv, kSmemMax, [k](int c) { return k ? 1.2 + 0.015 * k + 0.15 * c : 0.7; }, &cs)) return st;
-  p.ring = ring_shape(nv, cs, ring, false);
+  p.ring = ring_shape(nv, cs, ring);
+  p.subs = std::max(1, (p.ring.n_stages + kGroups - 1) / kGroups * (p.ring.stage / kSub));
+  p.bins = std::min(p.subs, kMaxBins);
   return launch_ring(f, p, p.n, cs, off + p.ring.n_slots * p.ring.stage * 16, s);
 }
 

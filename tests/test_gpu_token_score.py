@@ -285,6 +285,46 @@ def test_score_bad_ids_and_refusals(lib):
     plan.sync()
 
 
+def test_many_rows_a_cta(lib):
+    """Dozens of rows for each CTA: slots, barriers and buffers go round many times."""
+    n, V, k = 8000, 20011, 9
+    plan = decode_plan(lib, n)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    xt = torch.empty((n, 20016), dtype=torch.bfloat16, device="cuda").normal_(0, 3, generator=g)
+    xt[:, V:] = float("nan")
+    x = xt[:, :V].double()
+    ids = torch.randint(0, V, (n,), generator=g, device="cuda")
+    lp = torch.log_softmax(x, 1)
+    H = -(lp.exp() * lp).sum(1)
+    for kk in (0, k):
+        logp, stat, ent, ti, tl = run_score(plan, xt, V, ids.cpu().numpy(), kk)
+        plan.sync()
+        close(stat.sum(1), torch.logsumexp(x, 1).cpu().numpy(), "lse")
+        close(ent, H.cpu().numpy(), "entropy")
+        close(logp, lp.gather(1, ids[:, None])[:, 0].cpu().numpy(), "logp")
+    v, i = torch.sort(x, dim=1, descending=True, stable=True)
+    assert np.array_equal(ti, i[:, :k].cpu().numpy())
+    w = torch.rand(n, generator=g, device="cuda") * (torch.rand(n, generator=g, device="cuda") < 0.8)
+    t_lp = torch.log_softmax(x + 0.3 * torch.randn(x.shape, generator=g, device="cuda"), 1)
+    val, at = torch.topk(t_lp, k, dim=1)
+    P = val.exp()
+    inside = torch.zeros_like(x, dtype=torch.bool).scatter_(1, at, True)
+    q = lp.exp()
+    for tail in (False, True):
+        lnP = val if tail else val - torch.logsumexp(val, 1, keepdim=True)
+        P = lnP.exp()
+        R = (1 - P.sum(1)) if tail else torch.zeros(n, device="cuda", dtype=torch.float64)
+        qR = q.masked_fill(inside, 0).sum(1)
+        kl = (P * (lnP - lp.gather(1, at))).sum(1) + torch.where(R > 0, R * (R.log() - qR.log()), 0.0)
+        d = q * (P.sum(1) + R)[:, None] - (R / qR)[:, None] * q.masked_fill(inside, 0)
+        d = d.scatter_add(1, at, -P) * w[:, None].double()
+        live = (w != 0).cpu().numpy()
+        got_kl, _, got = run_distill(plan, xt, V, at.cpu().numpy(), val.cpu().numpy().astype(np.float32), w.cpu().numpy(), 1.0, tail, "sep")
+        plan.sync()
+        close(got_kl, np.where(live, kl.cpu().numpy(), 0.0), "row_kl", scale=5.0)
+        close(got[:, :V], d.cpu().numpy(), "dlogits", True, scale=2.0)
+
+
 # ---- gradient ----
 
 @pytest.mark.parametrize("dtype,V,c", [("f32", 997, 1.0), ("bf16", 1037, 0.5), ("bf16", 4096, 1.0), ("f32", 4097, 1.7), ("f32", 3, 1.0)])
