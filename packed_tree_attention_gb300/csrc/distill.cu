@@ -47,7 +47,7 @@ struct RowSums {
   float m, ls, pr, lqr;
   int32_t has;
 };
-struct TeamSmem {
+struct __align__(16) TeamSmem {
   int32_t id[kMaxTop];
   __align__(16) int32_t vec[kMaxTop];   // vectors of the ids
   float p[kMaxTop], x[kMaxTop];
@@ -55,7 +55,7 @@ struct TeamSmem {
   float red[2][kFinWarps];
   float pre_o[kFinWarps][2], pre_in[kFinWarps][2];   // sums of the listed vectors and of the last entries
   RowSums res[2];                                    // by turns
-  float in[2][kMaxCluster][4];                       // the CTAs' sums, of every other row of the team
+  __align__(16) float in[2][kMaxCluster][4];                       // the CTAs' sums, of every other row of the team
 };
 struct DistillSmem {
   RingBars bars;
@@ -69,7 +69,7 @@ __host__ __device__ constexpr int slots_offset(int words) { return kBitmapOffset
 __device__ __forceinline__ float fin_fold(float v, TeamSmem& t, int team, int& buf) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int w = ((int)threadIdx.x - kCons - team * kFin) >> 5;
+  const int w = ((int)threadIdx.x - team * kFin) >> 5;
   if ((threadIdx.x & 31) == 0) t.red[buf][w] = v;
   fin_sync(team);
   float r = 0.f;
@@ -80,7 +80,7 @@ __device__ __forceinline__ float fin_fold(float v, TeamSmem& t, int team, int& b
 }
 __device__ __forceinline__ float fin_max(float v, TeamSmem& t, int team, int& buf) {
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(v) : "f"(v));
-  const int w = ((int)threadIdx.x - kCons - team * kFin) >> 5;
+  const int w = ((int)threadIdx.x - team * kFin) >> 5;
   if ((threadIdx.x & 31) == 0) t.red[buf][w] = v;
   fin_sync(team);
   float r = t.red[buf][0];
@@ -124,13 +124,13 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
   T* const dlogits = reinterpret_cast<T*>(p.dlogits);
   auto weight = [&](int r) { return !p.w ? 1.f : r < p.n ? p.w[p.row0 + r] : 0.f; };
 
-  if (tid == 0) bar.init(rs.cs);
+  if (tid == 0) bar.init();
   __syncthreads();
   if (rs.cs > 1) cluster_sync();
 
-  if (tid >= kCons + kTeams * kFin) {
+  if (tid >= kCopy && tid < kFirstCons) {
     // ---- copies (rows of weight 0 are not read) ----
-    if (tid == kCons + kTeams * kFin) {
+    if (tid == kCopy) {
       RingPos pos;
       int issued = 0;
       bool ok = true;
@@ -157,9 +157,10 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
           ring_wait(&bar.full[pos.slot], pos.round, p.status);
         }
     }
-  } else if (tid < kCons) {
+  } else if (tid >= kFirstCons) {
     // ---- consumers ----
-    const int group = tid / kGroupThreads, t = tid % kGroupThreads;
+    const int ct = tid - kFirstCons;
+    const int group = ct / kGroupThreads, t = ct % kGroupThreads;
     const int n_st = (nvec + rs.stage - 1) / rs.stage, n_sub = rs.stage / kSub;
     // the next stages of this group in the two passes' order (kAgain: of both), and which of
     // the next row's stages those are
@@ -212,8 +213,8 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       warp_merge(tot, c2);
       if (!(ok = warp_wait(&bar.part_empty[par], ph ^ 1, p.status))) return;
       if (lane == 0) {
-        ss.part[par][tid >> 5][0] = tot.m;
-        ss.part[par][tid >> 5][1] = tot.s;
+        ss.part[par][ct >> 5][0] = tot.m;
+        ss.part[par][ct >> 5][1] = tot.s;
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bar.part_full[par]);
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
     }
   } else {
     // ---- finishers: team `par` takes the rows of that parity ----
-    const int par = (tid - kCons) / kFin, ft = tid - kCons - par * kFin, wi = ft >> 5;
+    const int par = tid / kFin, ft = tid - par * kFin, wi = ft >> 5;
     TeamSmem& ts = ss.team[par];
     uint32_t* const bits = bitmap + par * p.words;
     const int tail_n = rank + 1 == (uint32_t)rs.cs ? p.V - nv * E : 0;
@@ -433,15 +434,11 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         if (ok && rs.cs > 1) {
           // every CTA to every CTA; in[] and the barriers by turns, so that a fast CTA's next
           // row meets nobody who still reads or waits for this one
-          if (lane < rs.cs) {
-            const uint32_t dst = map_rank(tc::smem_u32(ts.in[ph][rank]), lane);
-            st_remote(dst, o.m);
-            st_remote(dst + 4, o.s);
-            st_remote(dst + 8, in.m);
-            st_remote(dst + 12, in.s);
-            arrive_remote(map_rank(tc::smem_u32(&bar.joined[par][ph]), lane));
-          }
-          ok = __all_sync(0xffffffffu, ring_wait<true>(&bar.joined[par][ph], (it >> 2) & 1, p.status));
+          uint64_t* const joined = &bar.joined[par][ph];
+          if (lane == 0) tc::mbar_expect_tx(joined, rs.cs * 16);
+          if (lane < rs.cs)
+            st_async(map_rank(tc::smem_u32(ts.in[ph][rank]), lane), o.m, o.s, in.m, in.s, map_rank(tc::smem_u32(joined), lane));
+          ok = __all_sync(0xffffffffu, ring_wait<true>(joined, (it >> 2) & 1, p.status));
           o.init();
           in.init();
           if (lane < rs.cs) {

@@ -18,7 +18,9 @@ namespace rows {
 
 constexpr int kConsWarps = 16, kFinWarps = 4, kTeams = 2;   // finisher warps of a team
 constexpr int kCons = kConsWarps * 32, kFin = kFinWarps * 32;
-constexpr int kBlock = kCons + kTeams * kFin + 64;   // + the copying warp and one for look-ups
+// Warps: the finishers, the copying one, one for look-ups, the consumers.
+constexpr int kCopy = kTeams * kFin, kLook = kCopy + 32, kFirstCons = kLook + 32;
+constexpr int kBlock = kFirstCons + kCons;
 constexpr int kGroups = 4;                  // consumer groups, a warp of each on every scheduler
 constexpr int kGroupThreads = kCons / kGroups;
 constexpr int kPer = 4;                     // vectors that a thread takes at once
@@ -126,15 +128,17 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
   return a;
 }
-__device__ __forceinline__ void st_remote(uint32_t a, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+// Stores to a peer's shared memory that count their bytes on a barrier of the peer's.  (An
+// arrival with release semantics would wait for the thread's earlier global stores first.)
+__device__ __forceinline__ void st_async(uint32_t a, float x, float y, float z, float w, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a), "f"(x),
+               "f"(y), "f"(z), "f"(w), "r"(bar)
+               : "memory");
 }
-__device__ __forceinline__ void st_remote(uint32_t a, unsigned long long v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+__device__ __forceinline__ void st_async(uint32_t a, unsigned long long v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(a), "l"(v), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
+
 // ---- two fp32 operations per instruction ----
 typedef unsigned long long f2;
 __device__ __forceinline__ f2 pack2(float a, float b) {
@@ -325,15 +329,15 @@ __device__ __forceinline__ void load_sub(const uint4* slot, int cnt, int t, uint
 struct RingBars {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t part_full[2], part_empty[2];   // a row's warp sums: written, read
-  uint64_t joined[kTeams][2];             // every CTA of the cluster sent its part of a row
+  uint64_t joined[kTeams][2];             // the bytes that the cluster's CTAs send about a row
   uint64_t scal_full[2], scal_empty[2];   // a row's results: written, read by who needs them
   uint64_t pre_full[2], p2_done[2];       // distillation
-  __device__ void init(int cs) {
+  __device__ void init() {
     for (int i = 0; i < kMaxSlots; i++) tc::mbar_init(&full[i], 1), tc::mbar_init(&empty[i], kConsWarps / kGroups);
     for (int i = 0; i < 2; i++) {
       tc::mbar_init(&part_full[i], kConsWarps);
       tc::mbar_init(&part_empty[i], kFinWarps);
-      for (int j = 0; j < 2; j++) tc::mbar_init(&joined[i][j], cs);
+      for (int j = 0; j < 2; j++) tc::mbar_init(&joined[i][j], 1);
       tc::mbar_init(&pre_full[i], kFinWarps);
       tc::mbar_init(&scal_full[i], 1);
       tc::mbar_init(&scal_empty[i], 1);

@@ -48,14 +48,13 @@ __device__ __forceinline__ int first_stage(int group, int it, int n_st) { return
 struct ScoreSmem {
   RingBars bars;
   float part[2][kConsWarps][3];          // a row's warp sums
-  float in_stat[2][kMaxCluster][3];      // rank 0: the CTAs' sums
+  __align__(16) float in_stat[kMaxCluster][4];   // rank 0: the CTAs' sums
   float stat[2][2];                      // a row's (m, ln S), for the look-ups
   int32_t s_t[kMaxSucc];                 // successors of the row
 };
 // One of each for the two finisher teams.
 struct TopSmem {
   unsigned long long in_list[kMaxCluster][kMaxTop];   // rank 0: the CTAs' alternatives, best first
-  int32_t in_count[kMaxCluster];
   unsigned long long cand[kMaxCand];
   unsigned long long trim[kMaxTrim];
   unsigned long long sorted[kMaxTop];
@@ -77,7 +76,7 @@ __device__ __forceinline__ unsigned long long cand_of(uint32_t key, int32_t v) {
   return ((unsigned long long)key << 32) | (uint32_t)~v;
 }
 
-__device__ __forceinline__ int fin_thread(int team) { return (int)threadIdx.x - kCons - team * kFin; }
+__device__ __forceinline__ int fin_thread(int team) { return (int)threadIdx.x - team * kFin; }
 
 // Sum over the finishers; red is used alternately (buf) so that one barrier is enough.
 __device__ __forceinline__ uint32_t fin_sum(uint32_t v, TopSmem& ts, int team, int& buf) {
@@ -406,11 +405,11 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
   const float c2 = p.c * kLog2e;
   const T* const logits = reinterpret_cast<const T*>(p.logits);
 
-  if (tid == 0) bar.init(rs.cs);
+  if (tid == 0) bar.init();
   __syncthreads();
   if (rs.cs > 1) cluster_sync();
 
-  if (tid >= kCons + kTeams * kFin + 32) {
+  if (tid >= kLook && tid < kFirstCons) {
     // ---- look-ups: the tokens that the rows feed ----
     if (rank == 0 && p.ids) {
       SuccCursor cur;
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
           if (t[q] >= 0) p.logp[t[q]] = bad[q] ? __int_as_float(0x7fc00000) : log_prob(x[q], m, ls, p.c);
       }
     }
-  } else if (tid >= kCons + kTeams * kFin) {
+  } else if (tid >= kCopy && tid < kLook) {
     // ---- copies ----
     if (lane == 0) {
       RingPos pos;
@@ -472,9 +471,9 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
           ring_wait(&bar.full[pos.slot], pos.round, p.status);
         }
     }
-  } else if (tid < kCons) {
+  } else if (tid >= kFirstCons) {
     // ---- consumers: sums of the part, maxima of the bins ----
-    const int group = tid / kGroupThreads, t = tid % kGroupThreads;
+    const int ct = tid - kFirstCons, group = ct / kGroupThreads, t = ct % kGroupThreads;
     const int n_st = (nvec + rs.stage - 1) / rs.stage, n_sub = rs.stage / kSub;
     RingPos pos;
     pos.skip(group, rs.n_slots);
@@ -507,7 +506,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
           }
           if (kTop && (frac += p.bins) >= p.subs) {
             frac -= p.subs;
-            top[par].bmax[bin++][tid] = bm;
+            top[par].bmax[bin++][ct] = bm;
             bm = -INFINITY;
           }
         }
@@ -515,14 +514,14 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
       }
       if (!ok) break;
       if (kTop) {
-        for (; bin < p.bins; bin++) top[par].bmax[bin][tid] = bm, bm = -INFINITY;
-        top[par].tmax[tid] = tm;
+        for (; bin < p.bins; bin++) top[par].bmax[bin][ct] = bm, bm = -INFINITY;
+        top[par].tmax[ct] = tm;
       }
       Stat tot = st.total(tm, c2);
       warp_merge(tot, c2);
       if (!kTop) ok = warp_wait(&bar.part_empty[par], ((it >> 1) & 1) ^ 1, p.status);
       if (lane == 0) {
-        float* q = ss.part[par][tid >> 5];
+        float* q = ss.part[par][ct >> 5];
         q[0] = tot.m, q[1] = tot.s, q[2] = tot.a;
       }
       __syncwarp();
@@ -530,7 +529,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
     }
   } else {
     // ---- finishers: team `par` takes the rows of that parity ----
-    const int par = (tid - kCons) / kFin, ft = fin_thread(par);
+    const int par = tid / kFin, ft = fin_thread(par);
     TopSmem& ts = top[par];
     const int tail_n = rank + 1 == (uint32_t)rs.cs ? p.V - nv * E : 0;
     for (int r = cluster + par * n_clusters, it = par; r < p.n; r += 2 * n_clusters, it += 2) {
@@ -559,33 +558,24 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
 
       if (rs.cs > 1) {
         // to rank 0 (a cluster of several CTAs has a single row: nothing is sent twice)
-        if (kTop) {
-          const uint32_t dst = map_rank(tc::smem_u32(ts.in_list[rank]), 0);
-          if (ft < n_top) st_remote(dst + 8 * ft, ts.sorted[ft]);
-        }
-        if (ft == 0) {
-          const uint32_t dst = map_rank(tc::smem_u32(ss.in_stat[par][rank]), 0);
-          st_remote(dst, st.m);
-          st_remote(dst + 4, st.s);
-          st_remote(dst + 8, st.a);
-          if (kTop) st_remote(map_rank(tc::smem_u32(&ts.in_count[rank]), 0), __int_as_float(n_top));
-        }
-        fin_sync(par);
-        if (ft == 0) arrive_remote(map_rank(tc::smem_u32(&bar.joined[par][0]), 0));
+        uint64_t* const joined = &bar.joined[par][0];
+        const uint32_t far = map_rank(tc::smem_u32(joined), 0);
+        if (rank == 0 && ft == 0) tc::mbar_expect_tx(joined, rs.cs * (16 + 8 * p.k));
+        if (kTop && ft < p.k)   // places that are left over are 0
+          st_async(map_rank(tc::smem_u32(&ts.in_list[rank][ft]), 0), ft < n_top ? ts.sorted[ft] : 0ull, far);
+        if (ft == 0) st_async(map_rank(tc::smem_u32(ss.in_stat[rank]), 0), st.m, st.s, st.a, 0.f, far);
         if (rank != 0) continue;
-        if (!fin_all(ring_wait<true>(&bar.joined[par][0], ph, p.status), par)) break;
+        if (!fin_all(ring_wait<true>(joined, ph, p.status), par)) break;
         uint32_t bound = 1;   // the k-th best of any full list is a lower bound of the row's
         st.init();
-        for (int q = 0; q < rs.cs; q++) st.merge(ss.in_stat[par][q][0], ss.in_stat[par][q][1], ss.in_stat[par][q][2], c2);
+        for (int q = 0; q < rs.cs; q++) st.merge(ss.in_stat[q][0], ss.in_stat[q][1], ss.in_stat[q][2], c2);
         if (kTop) {
-          int at = ft;
           for (int q = 0; q < rs.cs; q++) {
-            const int cnt = ts.in_count[q];
-            if (ft < cnt) ts.cand[at] = ts.in_list[q][ft];
-            if (cnt == p.k) bound = max(bound, (uint32_t)(ts.in_list[q][cnt - 1] >> 32));
-            at += cnt;
+            if (ft < p.k) ts.cand[q * p.k + ft] = ts.in_list[q][ft];
+            bound = max(bound, (uint32_t)(ts.in_list[q][p.k - 1] >> 32));
           }
-          if (ft == 0) ts.n_cand = at;
+          if (ft < p.k) ts.sorted[ft] = 0;
+          if (ft == 0) ts.n_cand = rs.cs * p.k;
         }
         fin_sync(par);
         int buf = 0;
@@ -607,8 +597,8 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
       if (kTop && ft < p.k) {
         const unsigned long long e = ft < n_top ? ts.sorted[ft] : 0;
         const size_t o = (size_t)r * p.k + ft;
-        p.top_ids[o] = ft < n_top ? (int32_t) ~(uint32_t)e : -1;
-        p.top_logp[o] = ft < n_top ? log_prob(order_value((uint32_t)(e >> 32)), m, ls, p.c) : __int_as_float(0x7fc00000);
+        p.top_ids[o] = e ? (int32_t) ~(uint32_t)e : -1;
+        p.top_logp[o] = e ? log_prob(order_value((uint32_t)(e >> 32)), m, ls, p.c) : __int_as_float(0x7fc00000);
       }
     }
   }
