@@ -98,13 +98,10 @@ struct Entry {
   bool first = false;   // the id's first entry
 };
 
-// The gradient's passes.  kNone: the divergence alone.  kHeld: a part stays in the ring between
-// the two passes, and the first pass of the next row comes before the second of this one, so
-// that the join of the row's sums is never waited for: DRAM sees each logit once.  kAgain:
-// rows too long for that are streamed twice.
-enum { kNone, kHeld, kAgain };
-
-template <typename T, int kMode>
+// With a gradient every row is streamed twice, the first pass of the next row before the second
+// of this one, so that the join of the row's sums is not waited for.  The second time a row
+// comes from L2 (two rows for each cluster in flight).
+template <typename T, bool kGrad>
 __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ DistillParams p) {
   using VT = Vec<T>;
   constexpr int E = VT::E;
@@ -134,21 +131,24 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       RingPos pos;
       int issued = 0;
       bool ok = true;
-      float w = weight(cluster);
-      for (int r = cluster; r < p.n && ok; r += n_clusters) {
-        const bool skip = w == 0.f;
-        w = weight(r + n_clusters);
-        if (skip) continue;
+      auto stream = [&](int r) {
         const T* src = logits + (size_t)r * p.ld + (size_t)v0 * E;
-        for (int pass = 0; pass < (kMode == kAgain ? 2 : 1) && ok; pass++)
-          for (int b = 0; b < nvec; b += rs.stage) {
-            if (!(ok = ring_wait(&bar.empty[pos.slot], pos.round ^ 1, p.status))) break;
-            const uint32_t bytes = (uint32_t)min(rs.stage, nvec - b) * 16;
-            tc::mbar_expect_tx(&bar.full[pos.slot], bytes);
-            bulk_load(slots + (size_t)pos.slot * rs.stage, src + (size_t)b * E, bytes, &bar.full[pos.slot]);
-            pos.skip(1, rs.n_slots);
-            issued++;
-          }
+        for (int b = 0; b < nvec && ok; b += rs.stage) {
+          if (!(ok = ring_wait(&bar.empty[pos.slot], pos.round ^ 1, p.status))) return;
+          const uint32_t bytes = (uint32_t)min(rs.stage, nvec - b) * 16;
+          tc::mbar_expect_tx(&bar.full[pos.slot], bytes);
+          bulk_load(slots + (size_t)pos.slot * rs.stage, src + (size_t)b * E, bytes, &bar.full[pos.slot]);
+          pos.skip(1, rs.n_slots);
+          issued++;
+        }
+      };
+      float w = weight(cluster), was = 0.f;
+      for (int r = cluster; r - n_clusters < p.n && ok; r += n_clusters) {
+        const float wn = weight(r + n_clusters);
+        if (r < p.n && w != 0.f) stream(r);
+        if (kGrad && was != 0.f) stream(r - n_clusters);
+        was = w;
+        w = wn;
       }
       // a copy must not outlive the CTA: the consumers have seen all of them unless a wait gave up
       if (!ok)
@@ -162,13 +162,11 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
     const int ct = tid - kFirstCons;
     const int group = ct / kGroupThreads, t = ct % kGroupThreads;
     const int n_st = (nvec + rs.stage - 1) / rs.stage, n_sub = rs.stage / kSub;
-    // the next stages of this group in the two passes' order (kAgain: of both), and which of
-    // the next row's stages those are
-    RingPos pos, pos2;
+    // this group's next stage: its slot, and which of the next row's stages it is
+    RingPos pos;
     pos.skip(group, rs.n_slots);
-    pos2.skip(group, rs.n_slots);
-    int next = group, next2 = group;
-    auto to_next_row = [&](int& next) { next = (next - n_st) & (kGroups - 1); };
+    int next = group;
+    auto to_next_row = [&] { next = (next - n_st) & (kGroups - 1); };
     bool ok = true;
     StageStat<T, false> st;
     // sums over the entries outside the list
@@ -189,7 +187,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
             if (left <= 0) break;
             uint4 w[kPer];
             load_sub<T>(slot + u * kSub, left, t, w);
-            if (kMode != kHeld && (u + 1 == n_sub || left <= kSub)) {
+            if (u + 1 == n_sub || left <= kSub) {
               __syncwarp();
               if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
             }
@@ -207,7 +205,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
           }
           pos.skip(kGroups, rs.n_slots);
         }
-        to_next_row(next);
+        to_next_row();
       }
       Stat tot = st.total(tm, c2);
       warp_merge(tot, c2);
@@ -220,18 +218,16 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       if (lane == 0) tc::mbar_arrive(&bar.part_full[par]);
     };
     // the gradient of the entries outside the list (the listed ones are overwritten later)
-    auto gradient = [&](int it, int r, bool held) {
+    auto gradient = [&](int it, int r, bool live) {
       const int par = it & 1;
       if (!(ok = warp_wait(&bar.scal_full[par], (it >> 1) & 1, p.status))) return;
       const RowScale sc = ss.scale[par];
       uint4* out = reinterpret_cast<uint4*>(dlogits + (size_t)r * p.ld) + v0;
       const f2 cc = pack2(c2, c2), hi = pack2(-sc.hi, -sc.hi), ff = pack2(sc.f, sc.f);
-      RingPos& at = kMode == kAgain ? pos : pos2;
-      int& from = kMode == kAgain ? next : next2;
-      for (int j = held ? from : group; j < n_st; j += kGroups) {
+      for (int j = live ? next : group; j < n_st; j += kGroups) {
         const int cnt = min(rs.stage, nvec - j * rs.stage);
-        if (kMode == kAgain && held && !(ok = warp_wait(&bar.full[at.slot], at.round, p.status))) return;
-        const uint4* slot = slots + (size_t)at.slot * rs.stage;
+        if (live && !(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) return;
+        const uint4* slot = slots + (size_t)pos.slot * rs.stage;
         uint4* const dst = out + j * rs.stage;
         if (!sc.live) {
           for (int i = t; i < cnt; i += kGroupThreads) __stcs(dst + i, make_uint4(0, 0, 0, 0));
@@ -257,13 +253,13 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
             __stcs(dst + i, VT::pack(g));
           }
         }
-        if (held) {
+        if (live) {
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar.empty[at.slot]);
-          at.skip(kGroups, rs.n_slots);
+          if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
+          pos.skip(kGroups, rs.n_slots);
         }
       }
-      if (held) to_next_row(from);
+      if (live) to_next_row();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bar.p2_done[par]);
     };
@@ -272,8 +268,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
     for (int r = cluster, it = 0; ok; r += n_clusters, it++) {
       const float wn = weight(r + n_clusters);
       if (r < p.n) sums(it, live);
-      if (kMode == kAgain && ok && r < p.n) gradient(it, r, live);
-      if (kMode == kHeld && ok && it > 0) gradient(it - 1, r - n_clusters, was);
+      if (kGrad && ok && it > 0) gradient(it - 1, r - n_clusters, was);
       if (r >= p.n) break;
       was = live;
       live = wn != 0.f;
@@ -470,7 +465,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
           if (sc.usual) sc.f *= ex2f(-(ae + ((a - (sc.hi - b)) + (sc.l2 - b))));
         }
         if (lane == 0) {
-          if (kMode != kNone) {
+          if (kGrad) {
             ss.scale[par] = sc;
             tc::mbar_arrive(&bar.scal_full[par]);
           }
@@ -501,7 +496,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       const float last_x = tail_x;
       const bool last_listed = tail_listed;
       if (r + 2 * n_clusters < p.n) prepare(r + 2 * n_clusters);
-      if (kMode != kNone) {
+      if (kGrad) {
         // after the consumers' stores: the listed entries, each id by its first, and the last ones
         if (!fin_all(ring_wait(&bar.p2_done[par], ph, p.status), par)) break;
         T* grow = dlogits + (size_t)r * p.ld;
@@ -525,20 +520,10 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
 template <typename T>
 int launch_distill(DistillParams& p, cudaStream_t s) {
   const int64_t nv = p.V / Vec<T>::E;
-  const void* f = (const void*)k_distill<T, kNone>;
+  const void* f = p.dlogits ? (const void*)k_distill<T, true> : (const void*)k_distill<T, false>;
   auto words = [&](int cs) { return (int)(((nv + cs - 1) / cs + 31) / 32); };
-  auto shape = [&](int cs) { return ring_shape(nv, cs, kSmemMax - slots_offset(words(cs))); };
   int cs = 1;
-  if (p.dlogits) {
-    // as many CTAs as it takes for the ring to hold two rows' parts and a stage to come
-    f = (const void*)k_distill<T, kHeld>;
-    auto holds = [&](int c) { const RingShape r = shape(c); return r.n_slots >= 2 * r.n_stages + 1; };
-    while (cs < kMaxCluster && !holds(cs)) cs *= 2;
-    if (!holds(cs)) f = (const void*)k_distill<T, kAgain>, cs = 1;
-  }
-  int few = 1;
-  if (int st = pick_cluster(f, p.n, p.dlogits ? 2 * nv : nv, kSmemMax, [](int) { return 0.7; }, &few)) return st;
-  cs = few > cs ? few : cs;
+  if (int st = pick_cluster(f, p.n, p.dlogits ? 2 * nv : nv, kSmemMax, [](int) { return 0.7; }, &cs)) return st;
   while (words(cs) * 4 * kTeams > 64 * 1024 && cs < kMaxCluster) cs *= 2;
   p.words = p.tail ? words(cs) : 0;
   p.ring = ring_shape(nv, cs, kSmemMax - slots_offset(p.words));
