@@ -33,6 +33,7 @@ struct DistillParams {
   int32_t* status;
   RingShape ring;
   int32_t words;            // words of the bitmap of a part's vectors
+  int32_t ahead;            // rows between the two passes
 };
 
 // What the gradient pass needs of a row: an entry outside the list has the gradient
@@ -41,66 +42,34 @@ struct RowScale {
   float f, hi, m, l2;
   int32_t live, usual;
 };
-// What the listed entries need: the reference and logarithm of the whole sum, the teacher's
-// rest and the logarithm of the student's.
-struct RowSums {
-  float m, ls, pr, lqr;
-  int32_t has;
-};
-struct __align__(16) TeamSmem {
-  int32_t id[kMaxTop];
-  __align__(16) int32_t vec[kMaxTop];   // vectors of the ids
+// Of each finisher warp: the entries of its row, and the CTAs' sums, of every other of its rows.
+struct __align__(16) WarpSmem {
+  int32_t id[kMaxTop];   // -1: none
   float p[kMaxTop], x[kMaxTop];
-  uint32_t last;                       // listed ones of the row's last entries
-  float red[2][kFinWarps];
-  float pre_o[kFinWarps][2], pre_in[kFinWarps][2];   // sums of the listed vectors and of the last entries
-  RowSums res[2];                                    // by turns
-  __align__(16) float in[2][kMaxCluster][4];                       // the CTAs' sums, of every other row of the team
+  float in[2][kMaxCluster][4];
 };
 struct DistillSmem {
   RingBars bars;
-  float part[2][kConsWarps][2];
-  RowScale scale[2];
-  TeamSmem team[kTeams];
+  float part[kMaxRows][kConsWarps][2];
+  RowScale scale[kMaxRows];
+  WarpSmem warp[kFinishers];
 };
 constexpr int kBitmapOffset = ((int)sizeof(DistillSmem) + 127) / 128 * 128;
-__host__ __device__ constexpr int slots_offset(int words) { return kBitmapOffset + (kTeams * words * 4 + 127) / 128 * 128; }
+__host__ __device__ constexpr int slots_offset(int words) { return kBitmapOffset + (kMaxRows * words * 4 + 127) / 128 * 128; }
+constexpr int kEntries = kMaxTop / 32;   // of a lane
 
-__device__ __forceinline__ float fin_fold(float v, TeamSmem& t, int team, int& buf) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int w = ((int)threadIdx.x - team * kFin) >> 5;
-  if ((threadIdx.x & 31) == 0) t.red[buf][w] = v;
-  fin_sync(team);
-  float r = 0.f;
-#pragma unroll
-  for (int i = 0; i < kFinWarps; i++) r += t.red[buf][i];
-  buf ^= 1;
-  return r;
+  return v;
 }
-__device__ __forceinline__ float fin_max(float v, TeamSmem& t, int team, int& buf) {
+__device__ __forceinline__ float warp_max(float v) {
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(v) : "f"(v));
-  const int w = ((int)threadIdx.x - team * kFin) >> 5;
-  if ((threadIdx.x & 31) == 0) t.red[buf][w] = v;
-  fin_sync(team);
-  float r = t.red[buf][0];
-#pragma unroll
-  for (int i = 1; i < kFinWarps; i++) r = fmaxf(r, t.red[buf][i]);
-  buf ^= 1;
-  return r;
+  return v;
 }
 
-// A finisher thread's entry of the teacher's list, made ready before the row's sums.
-struct Entry {
-  int id = -1;       // -1: none
-  float lp = 0.f, p = 0.f, x = 0.f;
-  float sub = 0.f;   // sum of the list's probabilities of this id
-  bool first = false;   // the id's first entry
-};
-
-// With a gradient every row is streamed twice, the first pass of the next row before the second
-// of this one, so that the join of the row's sums is not waited for.  The second time a row
-// comes from L2 (two rows for each cluster in flight).
+// With a gradient every row is streamed twice, the first pass `ahead` rows ahead of the second,
+// so that the join of a row's sums is not waited for.  The second time a row comes from L2.
 template <typename T, bool kGrad>
 __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ DistillParams p) {
   using VT = Vec<T>;
@@ -121,7 +90,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
   T* const dlogits = reinterpret_cast<T*>(p.dlogits);
   auto weight = [&](int r) { return !p.w ? 1.f : r < p.n ? p.w[p.row0 + r] : 0.f; };
 
-  if (tid == 0) bar.init();
+  if (tid == 0) bar.init(1);
   __syncthreads();
   if (rs.cs > 1) cluster_sync();
 
@@ -131,23 +100,26 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       RingPos pos;
       int issued = 0;
       bool ok = true;
-      auto stream = [&](int r) {
+      auto stream = [&](int r, bool last) {
         const T* src = logits + (size_t)r * p.ld + (size_t)v0 * E;
         for (int b = 0; b < nvec && ok; b += rs.stage) {
           if (!(ok = ring_wait(&bar.empty[pos.slot], pos.round ^ 1, p.status))) return;
           const uint32_t bytes = (uint32_t)min(rs.stage, nvec - b) * 16;
           tc::mbar_expect_tx(&bar.full[pos.slot], bytes);
-          bulk_load(slots + (size_t)pos.slot * rs.stage, src + (size_t)b * E, bytes, &bar.full[pos.slot]);
+          bulk_load(slots + (size_t)pos.slot * rs.stage, src + (size_t)b * E, bytes, &bar.full[pos.slot], last);
           pos.skip(1, rs.n_slots);
           issued++;
         }
       };
-      float w = weight(cluster), was = 0.f;
-      for (int r = cluster; r - n_clusters < p.n && ok; r += n_clusters) {
+      float w = weight(cluster);
+      uint32_t live = 0;   // bit i: the row i rows back
+      for (int r = cluster, it = 0; ok; r += n_clusters, it++) {
+        const int r2 = r - p.ahead * n_clusters;
+        if (kGrad ? r2 >= p.n : r >= p.n) break;
         const float wn = weight(r + n_clusters);
-        if (r < p.n && w != 0.f) stream(r);
-        if (kGrad && was != 0.f) stream(r - n_clusters);
-        was = w;
+        live = live << 1 | (uint32_t)(r < p.n && w != 0.f);
+        if (live & 1) stream(r, !kGrad);
+        if (kGrad && it >= p.ahead && (live >> p.ahead & 1)) stream(r2, true);
         w = wn;
       }
       // a copy must not outlive the CTA: the consumers have seen all of them unless a wait gave up
@@ -171,13 +143,13 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
     StageStat<T, false> st;
     // sums over the entries outside the list
     auto sums = [&](int it, bool live) {
-      const int par = it & 1;
-      const uint32_t ph = (it >> 1) & 1;
+      const int b = it % kMaxRows;
+      const uint32_t ph = it / kMaxRows & 1;
       st.init();
       float tm = -INFINITY;
-      if (p.tail && !(ok = warp_wait(&bar.pre_full[par], ph, p.status))) return;
+      if (p.tail && !(ok = warp_wait(&bar.pre_full[b], ph, p.status))) return;
       if (live) {
-        const uint32_t* bits = bitmap + par * p.words;
+        const uint32_t* bits = bitmap + b * p.words;
         for (int j = next; j < n_st; j += kGroups) {
           const int cnt = nvec - j * rs.stage;
           if (!(ok = warp_wait(&bar.full[pos.slot], pos.round, p.status))) return;
@@ -209,19 +181,19 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       }
       Stat tot = st.total(tm, c2);
       warp_merge(tot, c2);
-      if (!(ok = warp_wait(&bar.part_empty[par], ph ^ 1, p.status))) return;
+      if (!(ok = warp_wait(&bar.part_empty[b], ph ^ 1, p.status))) return;
       if (lane == 0) {
-        ss.part[par][ct >> 5][0] = tot.m;
-        ss.part[par][ct >> 5][1] = tot.s;
+        ss.part[b][ct >> 5][0] = tot.m;
+        ss.part[b][ct >> 5][1] = tot.s;
       }
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bar.part_full[par]);
+      if (lane == 0) tc::mbar_arrive(&bar.part_full[b]);
     };
     // the gradient of the entries outside the list (the listed ones are overwritten later)
     auto gradient = [&](int it, int r, bool live) {
-      const int par = it & 1;
-      if (!(ok = warp_wait(&bar.scal_full[par], (it >> 1) & 1, p.status))) return;
-      const RowScale sc = ss.scale[par];
+      const int b = it % kMaxRows;
+      if (!(ok = warp_wait(&bar.scal_full[b], it / kMaxRows & 1, p.status))) return;
+      const RowScale sc = ss.scale[b];
       uint4* out = reinterpret_cast<uint4*>(dlogits + (size_t)r * p.ld) + v0;
       const f2 cc = pack2(c2, c2), hi = pack2(-sc.hi, -sc.hi), ff = pack2(sc.f, sc.f);
       for (int j = live ? next : group; j < n_st; j += kGroups) {
@@ -261,254 +233,279 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       }
       if (live) to_next_row();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bar.p2_done[par]);
+      if (lane == 0) tc::mbar_arrive(&bar.p2_done[b]);
     };
     float w = weight(cluster);
-    bool live = w != 0.f, was = false;
+    uint32_t live = 0;   // bit i: the row i rows back
     for (int r = cluster, it = 0; ok; r += n_clusters, it++) {
+      const int r2 = r - p.ahead * n_clusters;
+      if (kGrad ? r2 >= p.n : r >= p.n) break;
       const float wn = weight(r + n_clusters);
-      if (r < p.n) sums(it, live);
-      if (kGrad && ok && it > 0) gradient(it - 1, r - n_clusters, was);
-      if (r >= p.n) break;
-      was = live;
-      live = wn != 0.f;
+      live = live << 1 | (uint32_t)(r < p.n && w != 0.f);
+      if (r < p.n) sums(it, live & 1);
+      if (kGrad && ok && it >= p.ahead) gradient(it - p.ahead, r2, live >> p.ahead & 1);
+      w = wn;
     }
   } else {
-    // ---- finishers: team `par` takes the rows of that parity ----
-    const int par = tid / kFin, ft = tid - par * kFin, wi = ft >> 5;
-    TeamSmem& ts = ss.team[par];
-    uint32_t* const bits = bitmap + par * p.words;
+    // ---- finishers: the warps take the rows in turn ----
+    const int b = tid >> 5;
+    WarpSmem& ws = ss.warp[b];
+    uint32_t* const bits = bitmap + b * p.words;
     const int tail_n = rank + 1 == (uint32_t)rs.cs ? p.V - nv * E : 0;
-    int buf = 0;
-    // what does not need the row's sums: the teacher's probabilities, which vectors hold listed
-    // ids, and the sums over those vectors and the row's last entries.  A row that is not live
-    // has none of it.
-    Entry en;
-    float w = 0.f, pr = 0.f, total = 0.f, tail_x = 0.f;
-    bool live = false, tail_listed = false;
-    // its weight and entries are fetched a row earlier
-    int next_id = -1;
-    float next_z = 0.f, next_w = 0.f;
+    const int step = kFinishers * n_clusters;
+    // The lane's entries of the teacher's list (those from p.k on have no id), their
+    // probabilities and logarithms, the sum of the list's probabilities of the same id, and
+    // which entries are their id's first.
+    int id[kEntries];
+    float lp[kEntries], pe[kEntries], sub[kEntries];
+    uint32_t first = 0;
+    float w = 0.f, pr = 0.f, total = 0.f, last_x = 0.f;
+    bool live = false, last_listed = false;
+    Stat pre_o, pre_in;   // sums of the listed vectors and of the row's last entries
+    int next_id[kEntries];
+    float next_z[kEntries], next_w = 0.f;
     auto fetch = [&](int r) {
       if (r >= p.n) return;
       next_w = weight(r);
-      if (ft < p.k) {
-        next_id = p.t_ids[(size_t)r * p.k + ft];
-        next_z = p.t_val[(size_t)r * p.k + ft];
+#pragma unroll
+      for (int q = 0; q < kEntries; q++) {
+        const int i = q * 32 + lane;
+        next_id[q] = -1;
+        if (i >= p.k) continue;
+        next_id[q] = p.t_ids[(size_t)r * p.k + i];
+        next_z[q] = p.t_val[(size_t)r * p.k + i];
       }
     };
+    // What does not need the row's sums: the teacher's probabilities, which vectors hold listed
+    // ids, and the sums over those vectors.  Its weight and entries were fetched a row earlier.
     auto prepare = [&](int r) {
       const T* row = logits + (size_t)r * p.ld;
-      en = Entry();
       w = next_w;
       live = w != 0.f;
-      float z = -INFINITY;
-      if (live && ft < p.k) {
-        en.id = next_id;
-        z = next_z;
-        if (en.id >= p.V) atomicExch(p.status, OCTO_EINVAL);
-        if (en.id < 0 || en.id >= p.V || z == -INFINITY) en.id = -1, z = -INFINITY;
-      }
-      const int vec = en.id < 0 ? -1 : en.id / E;
-      const bool own = vec >= v0 && vec < v0 + nvec;
-      uint4 wv = make_uint4(0, 0, 0, 0);
-      if (en.id >= 0) en.x = VT::get(row + en.id);
-      if (p.tail && own) wv = reinterpret_cast<const uint4*>(row)[vec];
-      tail_x = live && ft < tail_n ? VT::get(row + nv * E + ft) : -INFINITY;
+      first = 0;
+      pre_o.init();
+      pre_in.init();
       if (!live) {
-        if (p.tail) {
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar.pre_full[par]);
-        }
-        fin_sync(par);
+        if (p.tail && lane == 0) tc::mbar_arrive(&bar.pre_full[b]);
         return;
       }
-      ts.id[ft] = en.id;
-      ts.vec[ft] = vec;
-      if (ft == 0) ts.last = 0;
-      if (p.tail) {
-        for (int i = ft; i < p.words; i += kFin) bits[i] = 0;
-        en.lp = z;
-        en.p = expf(z);
-        total = fin_fold(en.p, ts, par, buf);
-        pr = total != total ? total : fmaxf(0.f, 1.f - total);
-      } else {
-        const float zm = fin_max(z, ts, par, buf);
-        const float t = z == -INFINITY ? -INFINITY : (z - zm) * p.c;
-        const float sum = fin_fold(expf(t), ts, par, buf);
-        pr = 0.f;
-        if (sum == 0.f) live = false;   // no teacher
-        en.lp = t - logf(sum);
-        en.p = en.id < 0 ? 0.f : expf(en.lp);
-        total = fin_fold(en.p, ts, par, buf);
+      float z[kEntries], x[kEntries];
+#pragma unroll
+      for (int q = 0; q < kEntries; q++) {
+        id[q] = next_id[q];
+        z[q] = next_z[q];
+        if (id[q] >= p.V) atomicExch(p.status, OCTO_EINVAL);
+        if (id[q] < 0 || id[q] >= p.V || z[q] == -INFINITY) id[q] = -1, z[q] = -INFINITY;
+        x[q] = id[q] < 0 ? 0.f : VT::get(row + id[q]);
       }
-      ts.p[ft] = en.p;
-      if (vec == nv) atomicOr(&ts.last, 1u << (en.id % E));
-      fin_sync(par);
-      Stat o, in;
-      o.init();
-      in.init();
-      if (en.id >= 0) {
-        uint32_t mask = 1u << (en.id % E);
-        bool first_vec = true;
-        en.sub = en.p;
-        en.first = true;
-        auto same = [&](int i) {   // another entry in this one's vector
-          const int other = ts.id[i];
-          mask |= 1u << (other % E);
-          first_vec = first_vec && i > ft;
-          if (other == en.id) en.sub += ts.p[i], en.first = en.first && i > ft;
-        };
-        for (int i = 0; i < p.k; i += 4) {   // entries past k have vec -1
-          const int4 o4 = *reinterpret_cast<const int4*>(&ts.vec[i]);
-          const bool x = o4.x == vec && i != ft, y = o4.y == vec && i + 1 != ft, z4 = o4.z == vec && i + 2 != ft,
-                     w4 = o4.w == vec && i + 3 != ft;
-          if (x || y || z4 || w4) {
-            if (x) same(i);
-            if (y) same(i + 1);
-            if (z4) same(i + 2);
-            if (w4) same(i + 3);
+      last_x = lane < tail_n ? VT::get(row + nv * E + lane) : -INFINITY;
+      if (p.tail)
+        for (int i = lane; i < p.words; i += 32) bits[i] = 0;
+      float zm = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int q = 0; q < kEntries; q++) zm = fmaxf(zm, z[q]);
+      zm = p.tail ? 0.f : warp_max(zm);
+      total = 0.f;
+#pragma unroll
+      for (int q = 0; q < kEntries; q++) {
+        lp[q] = z[q] == -INFINITY ? -INFINITY : p.tail ? z[q] : (z[q] - zm) * p.c;
+        sum += expf(lp[q]);
+      }
+      sum = warp_sum(sum);
+      const float ls = p.tail ? 0.f : logf(sum);
+      if (!p.tail && sum == 0.f) live = false;   // no teacher
+#pragma unroll
+      for (int q = 0; q < kEntries; q++) {
+        lp[q] -= ls;
+        pe[q] = id[q] < 0 ? 0.f : expf(lp[q]);
+        total += pe[q];
+        ws.id[q * 32 + lane] = id[q];
+        ws.p[q * 32 + lane] = pe[q];
+      }
+      total = p.tail ? sum : warp_sum(total);
+      pr = !p.tail ? 0.f : total != total ? total : fmaxf(0.f, 1.f - total);
+      __syncwarp();
+      // other entries of the same id or vector
+      uint32_t mask[kEntries];
+      uint32_t first_vec = 0;
+#pragma unroll
+      for (int q = 0; q < kEntries; q++) {
+        sub[q] = pe[q];
+        mask[q] = id[q] < 0 ? 0u : 1u << (id[q] % E);
+        first |= (uint32_t)(id[q] >= 0) << q;
+        first_vec |= (uint32_t)(id[q] >= 0) << q;
+      }
+      uint32_t seen[kEntries] = {};   // entries in the vector of this one, itself among them
+      for (int i = 0; i < p.k; i += 4) {
+        const uint4 o4 = *reinterpret_cast<const uint4*>(&ws.id[i]);
+        const uint32_t v4[4] = {o4.x / E, o4.y / E, o4.z / E, o4.w / E};   // no id: no vector
+#pragma unroll
+        for (int q = 0; q < kEntries; q++) {
+          if (q * 32 >= p.k) continue;
+          const uint32_t vec = (uint32_t)id[q] / E;
+#pragma unroll
+          for (int j = 0; j < 4; j++) seen[q] += v4[j] == vec;
+        }
+      }
+      bool shared = false;
+#pragma unroll
+      for (int q = 0; q < kEntries; q++) shared = shared || (id[q] >= 0 && seen[q] > 1);
+      if (__any_sync(0xffffffffu, shared)) {
+        for (int i = 0; i < p.k; i++) {
+          const int other = ws.id[i];
+          if (other < 0) continue;
+#pragma unroll
+          for (int q = 0; q < kEntries; q++) {
+            const int own = q * 32 + lane;
+            if (id[q] < 0 || other / E != id[q] / E || i == own) continue;
+            mask[q] |= 1u << (other % E);
+            if (i < own) first_vec &= ~(1u << q);
+            if (other != id[q]) continue;
+            sub[q] += ws.p[i];
+            if (i < own) first &= ~(1u << q);
           }
         }
-        if (p.tail && own && first_vec) {
-          const int at = vec - v0;
+      }
+      uint32_t listed = 0;   // of the last entries
+      if (tail_n > 0) {
+#pragma unroll
+        for (int q = 0; q < kEntries; q++)
+          if (id[q] >= nv * E) listed |= 1u << (id[q] - nv * E);
+        listed = __reduce_or_sync(0xffffffffu, listed);
+      }
+      last_listed = listed >> lane & 1;
+      if (p.tail) {
+#pragma unroll
+        for (int q = 0; q < kEntries; q++) {
+          const int vec = id[q] / E, at = vec - v0;
+          if (!(first_vec >> q & 1) || vec < v0 || at >= nvec) continue;
           atomicOr(&bits[at >> 5], 1u << (at & 31));
-          float x[E];
-          VT::cvt(wv, x);
+          float y[E];
+          VT::cvt(reinterpret_cast<const uint4*>(row)[vec], y);
 #pragma unroll
           for (int e = 0; e < E; e++) {
-            Stat& s = mask >> e & 1 ? in : o;
-            if (x[e] > s.m) s.rebase(x[e], c2);
-            s.add(x[e], c2);
+            const bool in = mask[q] >> e & 1;
+            if (in) {
+              if (y[e] > pre_in.m) pre_in.rebase(y[e], c2);
+              pre_in.add(y[e], c2);
+            } else {
+              if (y[e] > pre_o.m) pre_o.rebase(y[e], c2);
+              pre_o.add(y[e], c2);
+            }
           }
         }
-      }
-      if (p.tail) {
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar.pre_full[par]);
+        if (lane == 0) tc::mbar_arrive(&bar.pre_full[b]);
       }
-      tail_listed = false;
-      if (ft < tail_n) {
-        tail_listed = ts.last >> ft & 1;
-        Stat& s = p.tail && tail_listed ? in : o;
-        if (tail_x > s.m) s.rebase(tail_x, c2);
-        s.add(tail_x, c2);
+      if (lane < tail_n) {
+        Stat s{fmaxf(last_x, -FLT_MAX), 0.f, 0.f};
+        s.add(last_x, c2);
+        if (p.tail && last_listed) pre_in.merge(s.m, s.s, 0.f, c2);
+        else pre_o.merge(s.m, s.s, 0.f, c2);
       }
-      if (p.tail || tail_n > 0) warp_merge(o, c2);
-      if (p.tail) warp_merge(in, c2);
-      if (lane == 0) {
-        ts.pre_o[wi][0] = o.m, ts.pre_o[wi][1] = o.s;
-        ts.pre_in[wi][0] = in.m, ts.pre_in[wi][1] = in.s;
-      }
-      ts.x[ft] = en.x;   // waits for the load: a peer may overwrite the row once it has this CTA's sums
-      fin_sync(par);
+      if (p.tail || tail_n > 0) warp_merge(pre_o, c2);
+      if (p.tail) warp_merge(pre_in, c2);
+      // waits for the loads: a peer may overwrite the row once it has this CTA's sums
+#pragma unroll
+      for (int q = 0; q < kEntries; q++) ws.x[q * 32 + lane] = x[q];
     };
-    const int first_row = cluster + par * n_clusters;
+    const int first_row = cluster + b * n_clusters;
     fetch(first_row);
     if (first_row < p.n) prepare(first_row);
-    for (int r = first_row, it = par; r < p.n; r += 2 * n_clusters, it += 2) {
-      const uint32_t ph = (it >> 1) & 1;
-      fetch(r + 2 * n_clusters);
-      bool ok = true;
-      if (wi == 0) {
-        // the row's sums and what the gradient pass needs of them, by one warp: the consumers
-        // wait for it
-        ok = warp_wait(&bar.part_full[par], ph, p.status);
-        Stat o, in;
+    for (int r = first_row, turn = 0; r < p.n; r += step, turn++) {
+      const uint32_t ph = turn & 1;
+      fetch(r + step);
+      if (!warp_wait(&bar.part_full[b], ph, p.status)) break;
+      Stat o = pre_o, in = pre_in;
+      if (live) {
+        Stat s;
+        s.init();
+        if (lane < kConsWarps) s.m = ss.part[b][lane][0], s.s = ss.part[b][lane][1];
+        warp_merge(s, c2);
+        o.merge(s.m, s.s, 0.f, c2);
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar.part_empty[b]);
+      if (rs.cs > 1) {
+        // every CTA to every CTA; in[] and the barriers by turns, so that a fast CTA's next row
+        // meets nobody who still reads or waits for this one
+        uint64_t* const joined = &bar.joined[b][ph];
+        if (lane == 0) tc::mbar_expect_tx(joined, rs.cs * 16);
+        if (lane < rs.cs)
+          st_async(map_rank(tc::smem_u32(ws.in[ph][rank]), lane), o.m, o.s, in.m, in.s, map_rank(tc::smem_u32(joined), lane));
+        if (!__all_sync(0xffffffffu, ring_wait<true>(joined, turn >> 1 & 1, p.status))) break;
         o.init();
         in.init();
-        if (ok && live) {
-          if (lane < kConsWarps) o.m = ss.part[par][lane][0], o.s = ss.part[par][lane][1];
-          else if (lane < kConsWarps + kFinWarps) o.m = ts.pre_o[lane - kConsWarps][0], o.s = ts.pre_o[lane - kConsWarps][1];
-          warp_merge(o, c2);
-          if (p.tail) {
-            if (lane < kFinWarps) in.m = ts.pre_in[lane][0], in.s = ts.pre_in[lane][1];
-            warp_merge(in, c2);
-          }
+        if (lane < rs.cs) {
+          const float* q = ws.in[ph][lane];
+          o.m = q[0], o.s = q[1], in.m = q[2], in.s = q[3];
         }
-        if (ok && rs.cs > 1) {
-          // every CTA to every CTA; in[] and the barriers by turns, so that a fast CTA's next
-          // row meets nobody who still reads or waits for this one
-          uint64_t* const joined = &bar.joined[par][ph];
-          if (lane == 0) tc::mbar_expect_tx(joined, rs.cs * 16);
-          if (lane < rs.cs)
-            st_async(map_rank(tc::smem_u32(ts.in[ph][rank]), lane), o.m, o.s, in.m, in.s, map_rank(tc::smem_u32(joined), lane));
-          ok = __all_sync(0xffffffffu, ring_wait<true>(joined, (it >> 2) & 1, p.status));
-          o.init();
-          in.init();
-          if (lane < rs.cs) {
-            const float* q = ts.in[ph][lane];
-            o.m = q[0], o.s = q[1], in.m = q[2], in.s = q[3];
-          }
-          warp_merge(o, c2);
-          if (p.tail) warp_merge(in, c2);
-        }
-        Stat all = o;
-        if (p.tail) all.merge(in.m, in.s, 0.f, c2);
-        RowSums res = {all.m, 0.f, 0.f, 0.f, 0};
-        RowScale sc = {0.f, 0.f, 0.f, 0.f, 0, 1};
-        if (live && all.s != 0.f) {
-          const float lo = logf(o.s);
-          res.has = 1;
-          res.ls = logf(all.s);
-          res.pr = o.s == 0.f ? 0.f : pr;   // dropped where nothing outside the list has mass
-          res.lqr = (o.m - all.m) * p.c + lo - res.ls;
-          const float f = p.gs * w * p.c;
-          sc.live = 1;
-          sc.f = o.s == 0.f ? 0.f : f * (p.tail ? expf(res.lqr) * (total + res.pr) - res.pr : total);
-          if (o.s != 0.f) sc.m = o.m, sc.l2 = lo * kLog2e;
-          sc.usual = StageStat<T, false>::usual(sc.m, c2);
-          // hi = c2 m + l2 rounded; what it leaves out goes into the factor
-          const float a = sc.m * c2, ae = fmaf(sc.m, c2, -a);
-          sc.hi = a + sc.l2;
-          const float b = sc.hi - a;
-          if (sc.usual) sc.f *= ex2f(-(ae + ((a - (sc.hi - b)) + (sc.l2 - b))));
-        }
-        if (lane == 0) {
-          if (kGrad) {
-            ss.scale[par] = sc;
-            tc::mbar_arrive(&bar.scal_full[par]);
-          }
-          ts.res[ph] = res;
-        }
+        warp_merge(o, c2);
+        if (p.tail) warp_merge(in, c2);
       }
-      if (!fin_all(ok, par)) break;
-      if (lane == 0) tc::mbar_arrive(&bar.part_empty[par]);
-      const RowSums res = ts.res[ph];
-      const bool has = res.has;
-      float fix = 0.f;
+      Stat all = o;
+      if (p.tail) all.merge(in.m, in.s, 0.f, c2);
+      const bool has = live && all.s != 0.f;
+      const float f = p.gs * w * p.c;
+      float ls = 0.f, lqr = 0.f;
+      RowScale sc = {0.f, 0.f, 0.f, 0.f, 0, 1};
       if (has) {
-        const float lq = en.id >= 0 ? (en.x - res.m) * p.c - res.ls : 0.f;
-        if (rank == 0) {
-          float kl = fin_fold(en.p != 0.f ? en.p * (en.lp - lq) : 0.f, ts, par, buf);
-          if (res.pr != 0.f) kl += res.pr * (logf(res.pr) - res.lqr);
-          if (ft == 0) {
-            p.row_kl[p.row0 + r] = kl;
-            if (p.part) p.part[r] = w * kl;
-          }
-        }
-        fix = p.gs * w * p.c * (expf(lq) * (total + res.pr) - en.sub);
-      } else if (rank == 0 && ft == 0) {
-        p.row_kl[p.row0 + r] = 0.f;
-        if (p.part) p.part[r] = 0.f;
+        const float lo = logf(o.s);
+        ls = logf(all.s);
+        if (o.s == 0.f) pr = 0.f;   // nothing outside the list has mass
+        lqr = (o.m - all.m) * p.c + lo - ls;
+        sc.live = 1;
+        sc.f = o.s == 0.f ? 0.f : f * (p.tail ? expf(lqr) * (total + pr) - pr : total);
+        if (o.s != 0.f) sc.m = o.m, sc.l2 = lo * kLog2e;
+        sc.usual = StageStat<T, false>::usual(sc.m, c2);
+        // hi = c2 m + l2 rounded; what it leaves out goes into the factor
+        const float a = sc.m * c2, ae = fmaf(sc.m, c2, -a);
+        sc.hi = a + sc.l2;
+        const float d = sc.hi - a;
+        if (sc.usual) sc.f *= ex2f(-(ae + ((a - (sc.hi - d)) + (sc.l2 - d))));
       }
-      const Entry done = en;
-      const float last_x = tail_x;
-      const bool last_listed = tail_listed;
-      if (r + 2 * n_clusters < p.n) prepare(r + 2 * n_clusters);
+      if (kGrad && lane == 0) {
+        ss.scale[b] = sc;
+        tc::mbar_arrive(&bar.scal_full[b]);
+      }
+      float kl = 0.f, fix[kEntries];
+#pragma unroll
+      for (int q = 0; q < kEntries; q++) {
+        fix[q] = 0.f;
+        if (!has || id[q] < 0) continue;
+        const float lq = (ws.x[q * 32 + lane] - all.m) * p.c - ls;
+        if (pe[q] != 0.f) kl += pe[q] * (lp[q] - lq);
+        if (kGrad) fix[q] = f * (expf(lq) * (total + pr) - sub[q]);
+      }
+      if (rank == 0) {
+        kl = warp_sum(kl);
+        if (has && pr != 0.f) kl += pr * (logf(pr) - lqr);
+        if (lane == 0) {
+          p.row_kl[p.row0 + r] = kl;
+          if (p.part) p.part[r] = has ? w * kl : 0.f;
+        }
+      }
+      int fixed[kEntries];   // the ids that this lane writes: firsts, in this CTA's part
+#pragma unroll
+      for (int q = 0; q < kEntries; q++) {
+        const int vec = id[q] / E;
+        const bool own = vec < nv ? vec >= v0 && vec < v0 + nvec : tail_n > 0;
+        fixed[q] = has && (first >> q & 1) && own ? id[q] : -1;
+      }
+      const float done_x = last_x;
+      const bool done_listed = has && last_listed;
+      if (r + step < p.n) prepare(r + step);
       if (kGrad) {
         // after the consumers' stores: the listed entries, each id by its first, and the last ones
-        if (!fin_all(ring_wait(&bar.p2_done[par], ph, p.status), par)) break;
+        if (!warp_wait(&bar.p2_done[b], ph, p.status)) break;
         T* grow = dlogits + (size_t)r * p.ld;
-        if (has && done.id >= 0 && done.first) {
-          const int vec = done.id / E;
-          if (vec < nv ? vec >= v0 && vec < v0 + nvec : tail_n > 0) VT::put(grow + done.id, fix);
-        }
-        const RowScale& sc = ss.scale[par];   // written again after the team's next row
-        if (ft < tail_n && !(has && last_listed))
-          VT::put(grow + nv * E + ft, sc.live ? sc.f * ex2f(sc.usual ? fmaf(last_x, c2, -sc.hi)
-                                                                      : max_nan((last_x - sc.m) * c2 - sc.l2, kCut))
-                                              : 0.f);
+#pragma unroll
+        for (int q = 0; q < kEntries; q++)
+          if (fixed[q] >= 0) VT::put(grow + fixed[q], fix[q]);
+        if (lane < tail_n && !done_listed)
+          VT::put(grow + nv * E + lane, sc.live ? sc.f * ex2f(sc.usual ? fmaf(done_x, c2, -sc.hi)
+                                                                         : max_nan((done_x - sc.m) * c2 - sc.l2, kCut))
+                                                 : 0.f);
       }
     }
   }
@@ -524,8 +521,9 @@ int launch_distill(DistillParams& p, cudaStream_t s) {
   auto words = [&](int cs) { return (int)(((nv + cs - 1) / cs + 31) / 32); };
   int cs = 1;
   if (int st = pick_cluster(f, p.n, p.dlogits ? 2 * nv : nv, kSmemMax, [](int) { return 0.7; }, &cs)) return st;
-  while (words(cs) * 4 * kTeams > 64 * 1024 && cs < kMaxCluster) cs *= 2;
+  while (words(cs) * 4 * kMaxRows > 64 * 1024 && cs < kMaxCluster) cs *= 2;
   p.words = p.tail ? words(cs) : 0;
+  p.ahead = 1;
   p.ring = ring_shape(nv, cs, kSmemMax - slots_offset(p.words));
   if (p.ring.n_slots < kGroups) return OCTO_ENOTSUP;
   return launch_ring(f, p, p.n, cs, slots_offset(p.words) + p.ring.n_slots * p.ring.stage * 16, s);

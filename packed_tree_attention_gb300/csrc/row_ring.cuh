@@ -16,10 +16,10 @@
 namespace octo {
 namespace rows {
 
-constexpr int kConsWarps = 16, kFinWarps = 4, kTeams = 2;   // finisher warps of a team
-constexpr int kCons = kConsWarps * 32, kFin = kFinWarps * 32;
+constexpr int kConsWarps = 16, kCons = kConsWarps * 32;
+constexpr int kFinishers = 8;               // warps; teams of 4 (scoring) or of 1 (distillation)
 // Warps: the finishers, the copying one, one for look-ups, the consumers.
-constexpr int kCopy = kTeams * kFin, kLook = kCopy + 32, kFirstCons = kLook + 32;
+constexpr int kCopy = kFinishers * 32, kLook = kCopy + 32, kFirstCons = kLook + 32;
 constexpr int kBlock = kFirstCons + kCons;
 constexpr int kGroups = 4;                  // consumer groups, a warp of each on every scheduler
 constexpr int kGroupThreads = kCons / kGroups;
@@ -27,9 +27,7 @@ constexpr int kPer = 4;                     // vectors that a thread takes at on
 constexpr int kSub = kPer * kGroupThreads;  // and a group: stages are multiples of that
 constexpr int kMaxSlots = 28;
 constexpr int kMaxCluster = 8;
-constexpr int kFinBar = 1;                  // named barriers of the finisher teams: this and the next
-static_assert(kTeams == 2, "the barriers' pairs are the teams'");
-static_assert(kFin >= kMaxTop, "a finisher thread for each teacher entry");
+constexpr int kMaxRows = kFinishers;        // rows that a CTA works on at once
 
 struct RingShape {
   int32_t cs;          // CTAs per row
@@ -56,14 +54,22 @@ inline RingShape ring_shape(int64_t nv, int cs, int bytes) {
   return s;
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+// last: nothing reads the bytes again, L2 may drop them first.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, bool last = false) {
+  if (last) {
+    uint64_t policy;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+                     tc::smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(tc::smem_u32(bar)), "l"(policy)
+                 : "memory");
+    return;
+  }
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    tc::smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
                : "memory");
 }
-
-__device__ __forceinline__ void fin_sync(int team) { asm volatile("bar.sync %0, %1;" ::"r"(kFinBar + team), "n"(kFin) : "memory"); }
 
 // Waits of these kernels: a poll suspends the thread for up to kPollNs (it wakes when the phase
 // completes), so that waiting warps leave the issue slots to the others; given up after
@@ -96,22 +102,9 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, int32_
   atomicExch(status, OCTO_ETIMEOUT);
   return false;
 }
-// The waits below are uniform over the warp, and fin_all over the finishers: after a wait that
-// gave up, all of them leave together and none is left at a barrier.
+// Uniform over the warp: after a wait that gave up, its lanes leave together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
   return __all_sync(0xffffffffu, ring_wait(bar, parity, status));
-}
-__device__ __forceinline__ bool fin_all(bool ok, int team) {
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"((uint32_t)ok), "r"(kFinBar + team), "n"(kFin)
-      : "memory");
-  return all != 0;
 }
 
 // ---- clusters ----
@@ -325,22 +318,22 @@ __device__ __forceinline__ void load_sub(const uint4* slot, int cnt, int t, uint
   }
 }
 
-// The barriers of a CTA.
+// The barriers of a CTA; those of a row by its turn among the rows in work.
 struct RingBars {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t part_full[2], part_empty[2];   // a row's warp sums: written, read
-  uint64_t joined[kTeams][2];             // the bytes that the cluster's CTAs send about a row
-  uint64_t scal_full[2], scal_empty[2];   // a row's results: written, read by who needs them
-  uint64_t pre_full[2], p2_done[2];       // distillation
-  __device__ void init() {
+  uint64_t part_full[kMaxRows], part_empty[kMaxRows];   // warp sums: written, read
+  uint64_t joined[kMaxRows][2];                         // the bytes that the cluster's CTAs send
+  uint64_t scal_full[kMaxRows], scal_empty[kMaxRows];   // results: written, read by who needs them
+  uint64_t pre_full[kMaxRows], p2_done[kMaxRows];       // distillation
+  __device__ void init(int team_warps) {
     for (int i = 0; i < kMaxSlots; i++) tc::mbar_init(&full[i], 1), tc::mbar_init(&empty[i], kConsWarps / kGroups);
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < kMaxRows; i++) {
       tc::mbar_init(&part_full[i], kConsWarps);
-      tc::mbar_init(&part_empty[i], kFinWarps);
+      tc::mbar_init(&part_empty[i], team_warps);
       for (int j = 0; j < 2; j++) tc::mbar_init(&joined[i][j], 1);
-      tc::mbar_init(&pre_full[i], kFinWarps);
       tc::mbar_init(&scal_full[i], 1);
       tc::mbar_init(&scal_empty[i], 1);
+      tc::mbar_init(&pre_full[i], team_warps);
       tc::mbar_init(&p2_done[i], kConsWarps);
     }
     tc::fence_mbar_init();

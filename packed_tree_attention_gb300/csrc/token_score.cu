@@ -18,6 +18,11 @@ namespace {
 
 using namespace rows;
 
+constexpr int kFinWarps = 4, kFin = kFinWarps * 32;   // a team of finishers
+constexpr int kTeams = kFinishers / kFinWarps;
+constexpr int kFinBar = 1;           // named barriers of the teams: this and the next
+static_assert(kTeams == 2, "team = parity of the row");
+static_assert(kFin >= kMaxTop, "a thread for each alternative");
 constexpr int kMaxBins = 10;         // bins of a thread's vectors
 constexpr int kMaxCand = 1280, kMaxHits = 512, kMaxTrim = 512;
 static_assert(kMaxCand >= kMaxCluster * kMaxTop, "the CTAs' alternatives are joined in cand");
@@ -76,6 +81,21 @@ __device__ __forceinline__ unsigned long long cand_of(uint32_t key, int32_t v) {
   return ((unsigned long long)key << 32) | (uint32_t)~v;
 }
 
+__device__ __forceinline__ void fin_sync(int team) { asm volatile("bar.sync %0, %1;" ::"r"(kFinBar + team), "n"(kFin) : "memory"); }
+// Uniform over the team: after a wait that gave up, all of it leaves together and none is left at
+// a barrier.
+__device__ __forceinline__ bool fin_all(bool ok, int team) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok), "r"(kFinBar + team), "n"(kFin)
+      : "memory");
+  return all != 0;
+}
 __device__ __forceinline__ int fin_thread(int team) { return (int)threadIdx.x - team * kFin; }
 
 // Sum over the finishers; red is used alternately (buf) so that one barrier is enough.
@@ -405,7 +425,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
   const float c2 = p.c * kLog2e;
   const T* const logits = reinterpret_cast<const T*>(p.logits);
 
-  if (tid == 0) bar.init();
+  if (tid == 0) bar.init(kFinWarps);
   __syncthreads();
   if (rs.cs > 1) cluster_sync();
 
