@@ -42,10 +42,12 @@ struct RowScale {
   float f, hi, m, l2;
   int32_t live, usual;
 };
+constexpr int kHashWords = 64;   // of the test for entries in one vector
+
 // Of each finisher warp: the entries of its row, and the CTAs' sums, of every other of its rows.
 struct __align__(16) WarpSmem {
-  int32_t id[kMaxTop];   // -1: none
-  float p[kMaxTop], x[kMaxTop];
+  uint32_t hash[kHashWords];
+  float x[kMaxTop];
   float in[2][kMaxCluster][4];
 };
 struct DistillSmem {
@@ -56,7 +58,6 @@ struct DistillSmem {
 };
 constexpr int kBitmapOffset = ((int)sizeof(DistillSmem) + 127) / 128 * 128;
 __host__ __device__ constexpr int slots_offset(int words) { return kBitmapOffset + (kMaxRows * words * 4 + 127) / 128 * 128; }
-constexpr int kEntries = kMaxTop / 32;   // of a lane
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -70,7 +71,8 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // With a gradient every row is streamed twice, the first pass `ahead` rows ahead of the second,
 // so that the join of a row's sums is not waited for.  The second time a row comes from L2.
-template <typename T, bool kGrad>
+// kEntries: entries of a lane, at least k / 32.
+template <typename T, bool kGrad, int kEntries>
 __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ DistillParams p) {
   using VT = Vec<T>;
   constexpr int E = VT::E;
@@ -319,53 +321,57 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         lp[q] -= ls;
         pe[q] = id[q] < 0 ? 0.f : expf(lp[q]);
         total += pe[q];
-        ws.id[q * 32 + lane] = id[q];
-        ws.p[q * 32 + lane] = pe[q];
       }
       total = p.tail ? sum : warp_sum(total);
       pr = !p.tail ? 0.f : total != total ? total : fmaxf(0.f, 1.f - total);
-      __syncwarp();
-      // other entries of the same id or vector
-      uint32_t mask[kEntries];
+      // Entries that share a vector, or an id, are few in general: a table of bits finds out
+      // which may, and only those are compared with all the others.
+      uint32_t mask[kEntries];   // listed ids in the entry's vector
       uint32_t first_vec = 0;
+      uint32_t meets[kEntries];
+#pragma unroll
+      for (int i = 0; i < kHashWords; i += 32) ws.hash[i + lane] = 0;
+      __syncwarp();
 #pragma unroll
       for (int q = 0; q < kEntries; q++) {
+        const uint32_t vec = (uint32_t)id[q] / E, h = (vec * 0x9e3779b1u) >> 21;
+        const bool has_id = id[q] >= 0;
         sub[q] = pe[q];
-        mask[q] = id[q] < 0 ? 0u : 1u << (id[q] % E);
-        first |= (uint32_t)(id[q] >= 0) << q;
-        first_vec |= (uint32_t)(id[q] >= 0) << q;
+        mask[q] = has_id ? 1u << ((uint32_t)id[q] % E) : 0u;
+        first |= (uint32_t)has_id << q;
+        first_vec |= (uint32_t)has_id << q;
+        const bool hit = has_id && (atomicOr(&ws.hash[h / 32], 1u << h % 32) >> h % 32 & 1);
+        meets[q] = __ballot_sync(0xffffffffu, hit);
       }
-      uint32_t seen[kEntries] = {};   // entries in the vector of this one, itself among them
-      for (int i = 0; i < p.k; i += 4) {
-        const uint4 o4 = *reinterpret_cast<const uint4*>(&ws.id[i]);
-        const uint32_t v4[4] = {o4.x / E, o4.y / E, o4.z / E, o4.w / E};   // no id: no vector
+      uint32_t shares = 0;       // bit q: another entry is in this one's vector
 #pragma unroll
-        for (int q = 0; q < kEntries; q++) {
-          if (q * 32 >= p.k) continue;
-          const uint32_t vec = (uint32_t)id[q] / E;
+      for (int q = 0; q < kEntries; q++)
+        for (uint32_t left = meets[q]; left; left &= left - 1) {
+          const int l = __ffs(left) - 1;
+          const uint32_t vec = (uint32_t)__shfl_sync(0xffffffffu, id[q], l) / E;
+          uint32_t with = 0;
 #pragma unroll
-          for (int j = 0; j < 4; j++) seen[q] += v4[j] == vec;
+          for (int q2 = 0; q2 < kEntries; q2++)
+            with |= (uint32_t)((uint32_t)id[q2] / E == vec && !(q2 == q && l == lane)) << q2;
+          shares |= with;
+          if (__any_sync(0xffffffffu, with != 0) && l == lane) shares |= 1u << q;
         }
-      }
-      bool shared = false;
 #pragma unroll
-      for (int q = 0; q < kEntries; q++) shared = shared || (id[q] >= 0 && seen[q] > 1);
-      if (__any_sync(0xffffffffu, shared)) {
-        for (int i = 0; i < p.k; i++) {
-          const int other = ws.id[i];
-          if (other < 0) continue;
+      for (int q = 0; q < kEntries; q++)   // in the entries' order, so that the sums are always the same
+        for (uint32_t left = __ballot_sync(0xffffffffu, shares >> q & 1); left; left &= left - 1) {
+          const int l = __ffs(left) - 1;
+          const uint32_t other = __shfl_sync(0xffffffffu, id[q], l);
+          const float po = __shfl_sync(0xffffffffu, pe[q], l);
 #pragma unroll
-          for (int q = 0; q < kEntries; q++) {
-            const int own = q * 32 + lane;
-            if (id[q] < 0 || other / E != id[q] / E || i == own) continue;
-            mask[q] |= 1u << (other % E);
-            if (i < own) first_vec &= ~(1u << q);
-            if (other != id[q]) continue;
-            sub[q] += ws.p[i];
-            if (i < own) first &= ~(1u << q);
+          for (int q2 = 0; q2 < kEntries; q2++) {
+            const bool self = q2 == q && l == lane, before = q < q2 || (q == q2 && l < lane);
+            const bool same_vec = other / E == (uint32_t)id[q2] / E && !self, same_id = other == (uint32_t)id[q2] && !self;
+            if (same_vec) mask[q2] |= 1u << (other % E);
+            if (same_id) sub[q2] += po;
+            if (same_vec && before) first_vec &= ~(1u << q2);
+            if (same_id && before) first &= ~(1u << q2);
           }
         }
-      }
       uint32_t listed = 0;   // of the last entries
       if (tail_n > 0) {
 #pragma unroll
@@ -382,16 +388,16 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
           atomicOr(&bits[at >> 5], 1u << (at & 31));
           float y[E];
           VT::cvt(reinterpret_cast<const uint4*>(row)[vec], y);
+          float mo = pre_o.m, mi = pre_in.m;
+#pragma unroll
+          for (int e = 0; e < E; e++) (mask[q] >> e & 1 ? mi : mo) = fmaxf(mask[q] >> e & 1 ? mi : mo, y[e]);
+          pre_o.rebase(mo, c2);
+          pre_in.rebase(mi, c2);
 #pragma unroll
           for (int e = 0; e < E; e++) {
             const bool in = mask[q] >> e & 1;
-            if (in) {
-              if (y[e] > pre_in.m) pre_in.rebase(y[e], c2);
-              pre_in.add(y[e], c2);
-            } else {
-              if (y[e] > pre_o.m) pre_o.rebase(y[e], c2);
-              pre_o.add(y[e], c2);
-            }
+            const float x2 = ex2f(max_nan((y[e] - (in ? mi : mo)) * c2, kCut));
+            (in ? pre_in.s : pre_o.s) += x2;
           }
         }
         __syncwarp();
@@ -517,7 +523,12 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
 template <typename T>
 int launch_distill(DistillParams& p, cudaStream_t s) {
   const int64_t nv = p.V / Vec<T>::E;
-  const void* f = p.dlogits ? (const void*)k_distill<T, true> : (const void*)k_distill<T, false>;
+  const void* f = p.dlogits ? (p.k <= 32   ? (const void*)k_distill<T, true, 1>
+                               : p.k <= 64 ? (const void*)k_distill<T, true, 2>
+                                           : (const void*)k_distill<T, true, 4>)
+                            : (p.k <= 32   ? (const void*)k_distill<T, false, 1>
+                               : p.k <= 64 ? (const void*)k_distill<T, false, 2>
+                                           : (const void*)k_distill<T, false, 4>);
   auto words = [&](int cs) { return (int)(((nv + cs - 1) / cs + 31) / 32); };
   int cs = 1;
   if (int st = pick_cluster(f, p.n, p.dlogits ? 2 * nv : nv, kSmemMax, [](int) { return 0.7; }, &cs)) return st;
