@@ -33,7 +33,6 @@ struct DistillParams {
   int32_t* status;
   RingShape ring;
   int32_t words;            // words of the bitmap of a part's vectors
-  int32_t ahead;            // rows between the two passes
 };
 
 // What the gradient pass needs of a row: an entry outside the list has the gradient
@@ -69,8 +68,9 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// With a gradient every row is streamed twice, the first pass `ahead` rows ahead of the second,
-// so that the join of a row's sums is not waited for.  The second time a row comes from L2.
+// With a gradient every row is streamed twice, the first pass of the next row before the second
+// of this one, so that the join of a row's sums is not waited for.  The second time a row comes
+// from L2.
 // kEntries: entries of a lane, at least k / 32.
 template <typename T, bool kGrad, int kEntries>
 __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ DistillParams p) {
@@ -114,14 +114,15 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         }
       };
       float w = weight(cluster);
-      uint32_t live = 0;   // bit i: the row i rows back
-      for (int r = cluster, it = 0; ok; r += n_clusters, it++) {
-        const int r2 = r - p.ahead * n_clusters;
-        if (kGrad ? r2 >= p.n : r >= p.n) break;
+      bool live = false;
+      for (int r = cluster; ok; r += n_clusters) {
+        const int prev = r - n_clusters;
+        if (kGrad ? prev >= p.n : r >= p.n) break;
         const float wn = weight(r + n_clusters);
-        live = live << 1 | (uint32_t)(r < p.n && w != 0.f);
-        if (live & 1) stream(r, !kGrad);
-        if (kGrad && it >= p.ahead && (live >> p.ahead & 1)) stream(r2, true);
+        const bool was = live;
+        live = r < p.n && w != 0.f;
+        if (live) stream(r, !kGrad);
+        if (kGrad && was) stream(prev, true);
         w = wn;
       }
       // a copy must not outlive the CTA: the consumers have seen all of them unless a wait gave up
@@ -238,14 +239,15 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       if (lane == 0) tc::mbar_arrive(&bar.p2_done[b]);
     };
     float w = weight(cluster);
-    uint32_t live = 0;   // bit i: the row i rows back
+    bool live = false;
     for (int r = cluster, it = 0; ok; r += n_clusters, it++) {
-      const int r2 = r - p.ahead * n_clusters;
-      if (kGrad ? r2 >= p.n : r >= p.n) break;
+      const int prev = r - n_clusters;
+      if (kGrad ? prev >= p.n : r >= p.n) break;
       const float wn = weight(r + n_clusters);
-      live = live << 1 | (uint32_t)(r < p.n && w != 0.f);
-      if (r < p.n) sums(it, live & 1);
-      if (kGrad && ok && it >= p.ahead) gradient(it - p.ahead, r2, live >> p.ahead & 1);
+      const bool was = live;
+      live = r < p.n && w != 0.f;
+      if (r < p.n) sums(it, live);
+      if (kGrad && ok && it > 0) gradient(it - 1, prev, was);
       w = wn;
     }
   } else {
@@ -532,9 +534,20 @@ int launch_distill(DistillParams& p, cudaStream_t s) {
   auto words = [&](int cs) { return (int)(((nv + cs - 1) / cs + 31) / 32); };
   int cs = 1;
   if (int st = pick_cluster(f, p.n, p.dlogits ? 2 * nv : nv, kSmemMax, [](int) { return 0.7; }, &cs)) return st;
+  if (p.dlogits && cs == 1) {
+    // Two rows for each cluster wait in L2 for their second pass, and their gradients pass
+    // through it: past about a third of it they are read from memory again.  More CTAs a row
+    // mean fewer rows in flight, at the price of joining the CTAs at every row, and want rows
+    // for several rounds.  4,000 rows, microseconds at 1 / 2 / 4 CTAs: of 128 KB
+    // 179 / 195 / 270, of 200 KB 294 / 257 / 351, of 304 KB 502 / 413 / 373; 2,000 of 608 KB
+    // 520 / 506 / 386.
+    const int sms = sm_count();
+    auto in_flight = [&](int c) { return (int64_t)nv * 16 * 2 * (sms / c); };
+    const int64_t room = l2_bytes() / 100 * 35;
+    while (cs < 4 && in_flight(cs) > room && (int64_t)p.n * 2 * cs > 5 * sms) cs *= 2;
+  }
   while (words(cs) * 4 * kMaxRows > 64 * 1024 && cs < kMaxCluster) cs *= 2;
   p.words = p.tail ? words(cs) : 0;
-  p.ahead = 1;
   p.ring = ring_shape(nv, cs, kSmemMax - slots_offset(p.words));
   if (p.ring.n_slots < kGroups) return OCTO_ENOTSUP;
   return launch_ring(f, p, p.n, cs, slots_offset(p.words) + p.ring.n_slots * p.ring.stage * 16, s);

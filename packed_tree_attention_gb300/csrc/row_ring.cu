@@ -3,6 +3,7 @@
 #include "row_ring.cuh"
 
 #include <algorithm>
+#include <atomic>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -10,18 +11,22 @@
 namespace octo {
 namespace rows {
 
-int sm_count() {
-  static std::mutex mu;
-  static std::map<int, int> known;
+// An attribute of the current device, asked for once.
+template <cudaDeviceAttr kAttr>
+static int attribute() {
+  static std::atomic<int> known[64];   // + 1; devices past that are asked every time
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = known.find(dev);
-  if (it != known.end()) return it->second;
+  if (dev < 64)
+    if (const int v = known[dev].load(std::memory_order_relaxed)) return v - 1;
   int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return known[dev] = n;
+  if (cudaDeviceGetAttribute(&n, kAttr, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n + 1, std::memory_order_relaxed);
+  return n;
 }
+
+int sm_count() { return attribute<cudaDevAttrMultiProcessorCount>(); }
+int64_t l2_bytes() { return attribute<cudaDevAttrL2CacheSize>(); }
 
 int max_clusters(const void* kernel, int cs, int smem, int* out) {
   int dev = 0;

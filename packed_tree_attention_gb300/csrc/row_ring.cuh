@@ -352,8 +352,9 @@ struct RingPos {
 
 constexpr int kSmemMax = 227 * 1024;
 
-// SMs of the current device
+// SMs and bytes of L2 of the current device
 int sm_count();
+int64_t l2_bytes();
 
 // Clusters of cs CTAs of this kernel that the device holds at once.
 int max_clusters(const void* kernel, int cs, int smem, int* out);
