@@ -178,43 +178,53 @@ _T = {}   # torch's dtypes and calls, looked up once
 
 def _torch():
     import torch
+    gpu = torch.cuda.is_available()
     _T.update(logits={torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}, float32=torch.float32, int32=torch.int32,
-              device=torch.cuda.current_device, stream=torch._C._cuda_getCurrentRawStream)
+              device=torch._C._cuda_getDevice if gpu else lambda: -2,
+              stream=torch._C._cuda_getCurrentRawStream if gpu else lambda dev: None)
     return _T
 
 
-def _logits(x, n_rows, vocab, what="logits"):
+def _device():
+    """The current device, on which the tensors of a call have to be (-2: no GPU)."""
+    return (_T or _torch())["device"]()
+
+
+def _elsewhere(x, what):
+    return ValueError("%s must be on the current CUDA device (is on %s)" % (what, x.device))
+
+
+def _logits(x, n_rows, vocab, dev, what="logits"):
     """(address, dtype, elements between rows) of a [rows][ld] bf16 or fp32 tensor holding
     n_rows rows of at least `vocab` entries; a column slice of a wider one is a row pitch."""
-    dt = (_T or _torch())["logits"].get(x.dtype)
+    dt = _T["logits"].get(x.dtype)
+    shape, stride = x.shape, x.stride()
     if dt is None:
         raise ValueError("%s must be bfloat16 or float32 (got %s)" % (what, x.dtype))
-    if x.dim() != 2 or x.shape[0] < n_rows or x.shape[1] < vocab or x.stride(1) != 1:
+    if len(shape) != 2 or shape[0] < n_rows or shape[1] < vocab or stride[1] != 1:
         raise ValueError("%s must be [rows][entries] with adjacent entries, %d rows of at least %d (got shape %s, "
-                         "strides %s)" % (what, n_rows, vocab, tuple(x.shape), tuple(x.stride())))
-    if not x.is_cuda:
-        raise ValueError("%s must be on the GPU" % what)
-    if x.get_device() != _T["device"]():
-        raise ValueError("%s must be on the current device" % what)
+                         "strides %s)" % (what, n_rows, vocab, tuple(shape), stride))
+    if x.get_device() != dev:
+        raise _elsewhere(x, what)
     # one row: any pitch will do, and the library wants 16-byte ones
-    return x.data_ptr(), dt, x.stride(0) if x.shape[0] > 1 else -(-max(vocab, 1) // 8) * 8
+    return x.data_ptr(), dt, stride[0] if shape[0] > 1 else -(-max(vocab, 1) // 8) * 8
 
 
-def _vector(x, name, count, what):
+def _vector(x, name, count, dev, what):
     """Address of a contiguous tensor of at least `count` elements of torch dtype `name`."""
     if x is None:
         return None
-    if x.dtype is not (_T or _torch())[name] or x.numel() < count or not x.is_contiguous():
+    if x.dtype is not _T[name] or x.numel() < count or not x.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of at least %d elements (got %s, shape %s)"
                          % (what, name, count, x.dtype, tuple(x.shape)))
-    if not x.is_cuda:
-        raise ValueError("%s must be on the GPU" % what)
+    if x.get_device() != dev:
+        raise _elsewhere(x, what)
     return x.data_ptr()
 
 
-def _current(s):
+def _current(s, dev):
     """_stream for tensors that were seen to be on the current device."""
-    return _T["stream"](_T["device"]()) if s is None else _stream(s)
+    return _T["stream"](dev) if s is None else _stream(s)
 
 
 def _stream(s):
@@ -496,32 +506,34 @@ class Plan:
         """octo_token_score: log-probabilities of the plan's tokens, each row's entropy and its
         top_ids.shape[1] most likely alternatives, of the rows [row0, row0 + n_rows) whose
         logits are `logits` [n_rows][ld] (bf16 or fp32)."""
-        x, dt, ld = _logits(logits, n_rows, vocab)
+        dev = _device()
+        x, dt, ld = _logits(logits, n_rows, vocab, dev)
         N, k = self.info["n_rows"], 0
         if top_ids is not None or top_logp is not None:
             if top_ids is None or top_logp is None or top_ids.dim() != 2 or top_ids.shape != top_logp.shape:
                 raise ValueError("top_ids and top_logp go together, both [n_rows][k]")
             k = top_ids.shape[1]
         _chk(self._L.octo_token_score(
-            self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, _vector(ids, "int32", N, "ids"),
-            _vector(logp, "float32", N, "logp"), _vector(row_stat, "float32", 2 * n_rows, "row_stat"),
-            _vector(entropy, "float32", n_rows, "entropy"), k, _vector(top_ids, "int32", n_rows * k, "top_ids"),
-            _vector(top_logp, "float32", n_rows * k, "top_logp"), _current(stream)), "octo_token_score")
+            self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, _vector(ids, "int32", N, dev, "ids"),
+            _vector(logp, "float32", N, dev, "logp"), _vector(row_stat, "float32", 2 * n_rows, dev, "row_stat"),
+            _vector(entropy, "float32", n_rows, dev, "entropy"), k, _vector(top_ids, "int32", n_rows * k, dev, "top_ids"),
+            _vector(top_logp, "float32", n_rows * k, dev, "top_logp"), _current(stream, dev)), "octo_token_score")
 
     def token_score_bwd(self, row0, n_rows, logits, vocab, row_stat, entropy, ids, g_logp, g_entropy, dlogits,
                         inv_temp=1.0, stream=None):
         """octo_token_score_bwd: gradient with respect to the logits from those of logp and
         entropy (either may be None), row_stat and entropy as token_score wrote them."""
-        x, dt, ld = _logits(logits, n_rows, vocab)
-        g = _logits(dlogits, n_rows, vocab, "dlogits")
+        dev = _device()
+        x, dt, ld = _logits(logits, n_rows, vocab, dev)
+        g = _logits(dlogits, n_rows, vocab, dev, "dlogits")
         if g[1:] != (dt, ld):
             raise ValueError("dlogits must have the dtype and row pitch of logits")
         N = self.info["n_rows"]
         _chk(self._L.octo_token_score_bwd(
-            self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, _vector(row_stat, "float32", 2 * n_rows, "row_stat"),
-            _vector(entropy, "float32", n_rows, "entropy"), _vector(ids, "int32", N, "ids"),
-            _vector(g_logp, "float32", N, "g_logp"), _vector(g_entropy, "float32", n_rows, "g_entropy"), g[0],
-            _current(stream)), "octo_token_score_bwd")
+            self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, _vector(row_stat, "float32", 2 * n_rows, dev, "row_stat"),
+            _vector(entropy, "float32", n_rows, dev, "entropy"), _vector(ids, "int32", N, dev, "ids"),
+            _vector(g_logp, "float32", N, dev, "g_logp"), _vector(g_entropy, "float32", n_rows, dev, "g_entropy"), g[0],
+            _current(stream, dev)), "octo_token_score_bwd")
 
     def distill_topk_workspace_size(self, n_rows):
         n = ctypes.c_size_t(0)
@@ -533,21 +545,28 @@ class Plan:
         """octo_distill_topk: KL(teacher || student) of the rows [row0, row0 + n_rows) against
         teacher entries teach_ids, teach_val [n_rows][k] (tail: log-probabilities, the rest of
         the mass one more class), with its gradient and weighted sum."""
-        x, dt, ld = _logits(logits, n_rows, vocab)
+        dev = _device()
+        x, dt, ld = _logits(logits, n_rows, vocab, dev)
         g = None
         if dlogits is not None:
-            g, gdt, gld = _logits(dlogits, n_rows, vocab, "dlogits")
+            g, gdt, gld = _logits(dlogits, n_rows, vocab, dev, "dlogits")
             if (gdt, gld) != (dt, ld):
                 raise ValueError("dlogits must have the dtype and row pitch of logits")
-        if teach_ids.dim() != 2 or teach_ids.shape != teach_val.shape:
+        shape = teach_ids.shape
+        if len(shape) != 2 or shape != teach_val.shape:
             raise ValueError("teach_ids and teach_val must both be [n_rows][k]")
-        N, k = self.info["n_rows"], teach_ids.shape[1]
+        N, k = self.info["n_rows"], shape[1]
+        ws_bytes = 0
+        if ws is not None:
+            ws_bytes = ws.numel() * ws.element_size()
+            if ws.get_device() != dev:
+                raise _elsewhere(ws, "ws")
         _chk(self._L.octo_distill_topk(
-            self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, k, _vector(teach_ids, "int32", n_rows * k, "teach_ids"),
-            _vector(teach_val, "float32", n_rows * k, "teach_val"), 1 if tail else 0,
-            _vector(weight, "float32", N, "weight"), _vector(row_kl, "float32", N, "row_kl"), g, grad_scale,
-            _vector(loss, "float32", 1, "loss"), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0,
-            _current(stream)), "octo_distill_topk")
+            self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, k, _vector(teach_ids, "int32", n_rows * k, dev, "teach_ids"),
+            _vector(teach_val, "float32", n_rows * k, dev, "teach_val"), 1 if tail else 0,
+            _vector(weight, "float32", N, dev, "weight"), _vector(row_kl, "float32", N, dev, "row_kl"), g, grad_scale,
+            _vector(loss, "float32", 1, dev, "loss"), _ptr(ws), ws_bytes,
+            _current(stream, dev)), "octo_distill_topk")
 
     def recurrent_workspace_size(self, n_heads, head_dim):
         return int(self._L.octo_recurrent_workspace_size(self.h, n_heads, head_dim))

@@ -64,7 +64,7 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 __device__ __forceinline__ float warp_max(float v) {
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(v) : "f"(v));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(v) : "f"(v));
   return v;
 }
 
@@ -162,10 +162,6 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
             if (left <= 0) break;
             uint4 w[kPer];
             load_sub<T>(slot + u * kSub, left, t, w);
-            if (u + 1 == n_sub || left <= kSub) {
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
-            }
             if (p.tail) {
 #pragma unroll
               for (int q = 0; q < kPer; q++) {
@@ -175,6 +171,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
               }
             }
             const float mx = Raw<T>::max(w);
+            if (u + 1 == n_sub || left <= kSub) give_back(&bar.empty[pos.slot], mx);
             tm = fmaxf(tm, mx);
             st.add(w, left, mx, c2);
           }

@@ -294,7 +294,7 @@ struct StageStat {
 // that each lane moves to it once and the sums are plain additions, in a fixed order.
 __device__ __forceinline__ void warp_merge(Stat& st, float c2) {
   float mn;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mn) : "f"(st.m));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mn) : "f"(st.m));
   st.rebase(mn, c2);
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
@@ -316,6 +316,23 @@ __device__ __forceinline__ void load_sub(const uint4* slot, int cnt, int t, uint
       w[q] = i < cnt ? slot[i] : Raw<T>::masked();
     }
   }
+}
+
+// Gives a slot back once the warp's loads of it have returned, mx being a value made of them.
+// An arrival right after the loads overtakes them: they queue behind other warps' misses
+// (scattered loads at a kernel's start take microseconds), and the next copy came into the slot
+// before they were served, 128 bytes here and there.  So the arrival is made to need mx: both
+// of its forms do the same.
+__device__ __forceinline__ void give_back(uint64_t* empty, float mx) {
+  const uint32_t v = __ballot_sync(0xffffffffu, __float_as_uint(mx) != 0x7fedcba9u);
+  if ((threadIdx.x & 31) == 0)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t"
+        "@!p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(tc::smem_u32(empty)),
+        "r"(v)
+        : "memory");
 }
 
 // The barriers of a CTA; those of a row by its turn among the rows in work.

@@ -460,11 +460,11 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
         }
         if (!warp_wait(&bar.scal_full[par], (it >> 1) & 1, p.status)) break;
         const float m = ss.stat[par][0], ls = ss.stat[par][1];
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar.scal_empty[par]);
 #pragma unroll
         for (int q = 0; q < kMaxSucc / 32; q++)
           if (t[q] >= 0) p.logp[t[q]] = bad[q] ? __int_as_float(0x7fc00000) : log_prob(x[q], m, ls, p.c);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar.scal_empty[par]);   // after what used them
       }
     }
   } else if (tid >= kCopy && tid < kLook) {
@@ -515,11 +515,8 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
           if (left > 0) {
             uint4 w[kPer];
             load_sub<T>(slot + u * kSub, left, t, w);
-            if (u + 1 == n_sub || left <= kSub) {
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive(&bar.empty[pos.slot]);
-            }
             const float mx = Raw<T>::max(w);
+            if (u + 1 == n_sub || left <= kSub) give_back(&bar.empty[pos.slot], mx);
             tm = fmaxf(tm, mx);
             bm = fmaxf(bm, mx);
             st.add(w, left, mx, c2);

@@ -95,9 +95,8 @@ def test_binding_refuses_bad_tensors():
             p.distill_topk(0, 4, bad, 10, i.view(4, 2), f.view(4, 2), f)
     with pytest.raises(ValueError):                  # host memory
         p.token_score(0, 4, x, 10, f)
-    with pytest.raises(ValueError):
-        pta._vector(i, "float32", 4, "logp")
-    with pytest.raises(ValueError):
-        pta._vector(f[::2], "float32", 4, "logp")
-    with pytest.raises(ValueError):
-        pta._vector(f, "float32", 9, "logp")
+    dev = f.get_device()
+    assert pta._vector(f, "float32", 8, dev, "logp") == f.data_ptr()
+    for bad, n, where in ((i, 4, dev), (f[::2], 4, dev), (f, 9, dev), (f, 4, dev + 1)):
+        with pytest.raises(ValueError):
+            pta._vector(bad, "float32", n, where, "logp")
