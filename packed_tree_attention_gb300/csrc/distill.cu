@@ -68,6 +68,17 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// ln s = hi + lo, hi exact: a divergence is the small difference of large logarithms, and s
+// rounded to one float would be felt in it.
+__device__ __forceinline__ void split_log(float s, float* hi, float* lo) {
+  const int e = (__float_as_int(s) >> 23) - 127;
+  const float f = __int_as_float((__float_as_int(s) & 0x7fffff) | 0x3f800000);
+  const bool normal = s >= FLT_MIN && s <= FLT_MAX;
+  // ln 2 in two parts, the first of 10 bits: e times it is exact
+  *hi = normal ? (float)e * 0.693359375f : logf(s);
+  *lo = normal ? fmaf((float)e, -2.12194440e-4f, logf(f)) : 0.f;
+}
+
 // With a gradient every row is streamed twice, the first pass of the next row before the second
 // of this one, so that the join of a row's sums is not waited for.  The second time a row comes
 // from L2.
@@ -452,13 +463,16 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       if (p.tail) all.merge(in.m, in.s, 0.f, c2);
       const bool has = live && all.s != 0.f;
       const float f = p.gs * w * p.c;
-      float ls = 0.f, lqr = 0.f;
+      float ls = 0.f, ls_lo = 0.f, lqr = 0.f;
       RowScale sc = {0.f, 0.f, 0.f, 0.f, 0, 1};
       if (has) {
         const float lo = logf(o.s);
-        ls = logf(all.s);
+        split_log(all.s, &ls, &ls_lo);
         if (o.s == 0.f) pr = 0.f;   // nothing outside the list has mass
-        lqr = (o.m - all.m) * p.c + lo - ls;
+        // ln q_R: by the ratio of the sums, unless one's reference is too far below the other's
+        Stat far = o;
+        far.rebase(all.m, c2);
+        lqr = far.s > 1e-30f ? logf(far.s / all.s) : (o.m - all.m) * p.c + lo - ls - ls_lo;
         sc.live = 1;
         sc.f = o.s == 0.f ? 0.f : f * (p.tail ? expf(lqr) * (total + pr) - pr : total);
         if (o.s != 0.f) sc.m = o.m, sc.l2 = lo * kLog2e;
@@ -478,7 +492,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       for (int q = 0; q < kEntries; q++) {
         fix[q] = 0.f;
         if (!has || id[q] < 0) continue;
-        const float lq = (ws.x[q * 32 + lane] - all.m) * p.c - ls;
+        const float lq = fmaf(ws.x[q * 32 + lane] - all.m, p.c, -ls) - ls_lo;
         if (pe[q] != 0.f) kl += pe[q] * (lp[q] - lq);
         if (kGrad) fix[q] = f * (expf(lq) * (total + pr) - sub[q]);
       }
