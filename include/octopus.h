@@ -391,8 +391,9 @@ int octo_distill_topk_workspace_size(int32_t n_rows, size_t* bytes);
  * device floats over ALL rows of the plan; row_kl[r] is written without the weight.
  * dlogits (optional): dtype, layout and alignment of logits; may be logits itself.  loss
  * (optional, one device float, needs ws): sum of w_r KL_r over the chunk, in a fixed order.
- * Teacher ids >= vocab count as empty and give OCTO_EINVAL at the next octo_sync.  Async on
- * stream. */
+ * Teacher ids >= vocab count as empty and give OCTO_EINVAL at the next octo_sync.
+ * OCTO_ENOTSUP at tail = 1 for vocabularies past some 2 million entries (fp32) or 4 (bf16).
+ * Deterministic.  Async on stream. */
 int octo_distill_topk(octo_plan_t plan, int32_t row0, int32_t n_rows, const void* logits, int32_t dtype,
                       int64_t ld, int32_t vocab, float inv_temp, int32_t k, const int32_t* teach_ids,
                       const float* teach_val, int32_t tail, const float* weight, float* row_kl,

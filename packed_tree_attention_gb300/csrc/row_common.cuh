@@ -123,75 +123,73 @@ struct SuccTable {
   const int32_t* ex_row;
   int32_t n_segs, n_rows, n_ex, is_decode;
 
-  __device__ int find(int r, int32_t* t, bool* path_start) const {
-    *path_start = false;
-    if (is_decode) {
-      t[0] = r;
-      return 1;
-    }
-    // the packed segment of r: the last one whose first row is <= r (empty segments
-    // before it share its first row, empty ones after it start past r)
-    int lo = 0, hi = n_segs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (seg_row_base[mid] <= r) lo = mid;
-      else hi = mid - 1;
-    }
-    const int end = lo + 1 < n_segs ? seg_row_base[lo + 1] : n_rows;
-    *path_start = r == seg_row_base[lo] && seg_pred[lo] < 0;
-    int n = 0;
-    if (r + 1 < end) t[n++] = r + 1;
-    int a = 0, b = n_ex;  // first extra with predecessor >= r
-    while (a < b) {
-      const int mid = (a + b) >> 1;
-      if (ex_pred[mid] < r) a = mid + 1;
-      else b = mid;
-    }
-    for (; a < n_ex && ex_pred[a] == r && n < kMaxSucc; a++) t[n++] = ex_row[a];
-    return n;
-  }
-};
-
-// SuccTable::find for rows in ascending order: keeps the segment and the place among the extra
-// successors, and searches again only past the segment's end.
-struct SuccCursor {
-  int base = 0, end = 0, pred = -1, e = -1, e_pred = -1;
-  __device__ int find(const SuccTable& s, int r, int32_t* t, bool* path_start) {
-    *path_start = false;
-    if (s.is_decode) {
-      t[0] = r;
-      return 1;
-    }
-    if (r >= end) {
-      int lo = 0, hi = s.n_segs - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s.seg_row_base[mid] <= r) lo = mid;
+  // One thread, a row of a pack plan: its segment's end, whether it starts a path, and its extra
+  // successors ex_row[e0, e0 + n).  The row's segment is the last one whose first row is <= r
+  // (empty segments before it share its first row, empty ones after it start past r).
+  __device__ void locate(int r, int* end, bool* path_start, int* e0, int* n) const {
+    int lo = 0, hi = n_segs - 1, a = 0, b = n_ex;
+    while (lo < hi || a < b) {
+      const int mid = (lo + hi + 1) >> 1, em = (a + b) >> 1;
+      const bool seg = lo < hi, ex = a < b;
+      const int base = seg ? seg_row_base[mid] : 0, pred = ex ? ex_pred[em] : 0;
+      if (seg) {
+        if (base <= r) lo = mid;
         else hi = mid - 1;
       }
-      base = s.seg_row_base[lo];
-      end = lo + 1 < s.n_segs ? s.seg_row_base[lo + 1] : s.n_rows;
-      pred = s.seg_pred[lo];
-    }
-    if (e < 0) {
-      int a = 0, b = s.n_ex;
-      while (a < b) {
-        const int mid = (a + b) >> 1;
-        if (s.ex_pred[mid] < r) a = mid + 1;
-        else b = mid;
+      if (ex) {
+        if (pred < r) a = em + 1;
+        else b = em;
       }
-      e = a;
-      e_pred = e < s.n_ex ? s.ex_pred[e] : INT32_MAX;
     }
-    while (e_pred < r) e_pred = ++e < s.n_ex ? s.ex_pred[e] : INT32_MAX;
-    *path_start = r == base && pred < 0;
-    int n = 0;
-    if (r + 1 < end) t[n++] = r + 1;
-    for (int a = e, q = e_pred; q == r && n < kMaxSucc;) {
-      t[n++] = s.ex_row[a++];
-      q = a < s.n_ex ? s.ex_pred[a] : INT32_MAX;
+    *end = lo + 1 < n_segs ? seg_row_base[lo + 1] : n_rows;
+    *path_start = r == seg_row_base[lo] && seg_pred[lo] < 0;
+    *e0 = a;
+    *n = 0;
+    while (*n < kMaxSucc && a + *n < n_ex && ex_pred[a + *n] == r) ++*n;
+  }
+
+  // One warp: row r's successors into t; returns how many.  Each step narrows a search to a
+  // 32nd, so that a call waits for one or two loads in a row and not for a binary search of them.
+  __device__ int find(int r, int32_t* t) const {
+    const int lane = threadIdx.x & 31;
+    if (is_decode) {
+      if (lane == 0) t[0] = r;
+      return 1;
     }
-    return n;
+    int lo = 0, hi = n_segs, a = 0, b = n_ex;   // the segment is in [lo, hi), the first extra in [a, b]
+    for (;;) {
+      const int s1 = (hi - lo + 31) / 32, s2 = max(1, (b - a + 31) / 32);
+      const int i = lo + lane * s1, e = a + lane * s2;
+      const int base = i < n_segs ? seg_row_base[i] : INT32_MAX, pred = e < n_ex ? ex_pred[e] : INT32_MAX;
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, base <= r && i < hi));
+      const uint32_t below = __ballot_sync(0xffffffffu, pred < r && e < b);
+      if (s1 == 1 && s2 == 1) {
+        const int after = __shfl_down_sync(0xffffffffu, base, 1);
+        int end = __shfl_sync(0xffffffffu, after, k);
+        if (k == 31) end = lo + 32 < n_segs ? seg_row_base[lo + 32] : n_rows;
+        if (end == INT32_MAX) end = n_rows;
+        int n = 0;
+        if (r + 1 < end) {
+          if (lane == 0) t[0] = r + 1;
+          n = 1;
+        }
+        for (int at = a + __popc(below); n < kMaxSucc; at += 32) {
+          const bool mine = at + lane < n_ex && ex_pred[at + lane] == r;
+          if (mine && n + lane < kMaxSucc) t[n + lane] = ex_row[at + lane];
+          const int more = __popc(__ballot_sync(0xffffffffu, mine));
+          n = min(n + more, kMaxSucc);
+          if (more < 32) break;
+        }
+        return n;
+      }
+      const int nlo = lo + k * s1;
+      hi = min(hi, nlo + s1);
+      lo = nlo;
+      const int c = __popc(below);   // the first extra is past entry c - 1 and not past entry c
+      b = min(b, a + c * s2);
+      a = c ? a + (c - 1) * s2 + 1 : a;
+      if (a > b) a = b;
+    }
   }
 };
 

@@ -47,7 +47,9 @@ struct ScoreParams {
 
 // The first of a CTA's n_st stages of its row `it` that is the group's: the groups take the
 // stages in turn, on over row ends.
-__device__ __forceinline__ int first_stage(int group, int it, int n_st) { return (group - it * n_st) & (kGroups - 1); }
+__device__ __forceinline__ int first_stage(int group, int it, int n_st) {
+  return (int)((uint32_t)group - (uint32_t)it * (uint32_t)n_st) & (kGroups - 1);
+}
 
 // Shared memory of the finishers; the ring's slots follow.
 struct ScoreSmem {
@@ -55,7 +57,6 @@ struct ScoreSmem {
   float part[2][kConsWarps][3];          // a row's warp sums
   __align__(16) float in_stat[kMaxCluster][4];   // rank 0: the CTAs' sums
   float stat[2][2];                      // a row's (m, ln S), for the look-ups
-  int32_t s_t[kMaxSucc];                 // successors of the row
 };
 // One of each for the two finisher teams.
 struct TopSmem {
@@ -430,41 +431,49 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
   if (rs.cs > 1) cluster_sync();
 
   if (tid >= kLook && tid < kFirstCons) {
-    // ---- look-ups: the tokens that the rows feed ----
+    // ---- look-ups: the tokens that the rows feed, 32 rows at a time, a lane for each ----
     if (rank == 0 && p.ids) {
-      SuccCursor cur;
-      for (int r = cluster, it = 0; r < p.n; r += n_clusters, it++) {
-        const int par = it & 1;
-        const T* row = logits + (size_t)r * p.ld;
-        int n = 0;
-        if (lane == 0) {
-          bool start;
-          n = cur.find(p.succ, p.row0 + r, ss.s_t, &start);
-          if (start) p.logp[p.row0 + r] = 0.f;
+      auto token = [&](const T* row, int t, float* x) {   // whether its id is one
+        const int id = p.ids[t];
+        const bool good = id >= 0 && id < p.V;
+        if (good) *x = VT::get(row + id);
+        else atomicExch(p.status, OCTO_EINVAL);
+        return good;
+      };
+      bool ok = true;
+      for (int first = 0; ok && cluster + first * n_clusters < p.n; first += 32) {
+        const int mine = cluster + (first + lane) * n_clusters, r = p.row0 + mine;
+        int t = -1, e0 = 0, n = 0;
+        float x = 0.f;
+        bool good = false;
+        if (mine < p.n) {
+          if (p.succ.is_decode) {
+            t = r;
+          } else {
+            int end;
+            bool start;
+            p.succ.locate(r, &end, &start, &e0, &n);
+            if (r + 1 < end) t = r + 1;
+            if (start) p.logp[r] = 0.f;
+          }
+          if (t >= 0) good = token(logits + (size_t)mine * p.ld, t, &x);
         }
-        n = __shfl_sync(0xffffffffu, n, 0);
-        __syncwarp();
-        int t[kMaxSucc / 32];
-        float x[kMaxSucc / 32];
-        bool bad[kMaxSucc / 32];
-#pragma unroll
-        for (int q = 0; q < kMaxSucc / 32; q++) {
-          const int i = q * 32 + lane;
-          t[q] = -1;
-          if (i >= n) continue;
-          t[q] = ss.s_t[i];
-          const int id = p.ids[t[q]];
-          bad[q] = id < 0 || id >= p.V;
-          if (bad[q]) atomicExch(p.status, OCTO_EINVAL);
-          else x[q] = VT::get(row + id);
+        for (int j = 0; j < 32; j++) {
+          const int it = first + j, rl = cluster + it * n_clusters, par = it & 1;
+          if (rl >= p.n) break;
+          if (!(ok = warp_wait(&bar.scal_full[par], (it >> 1) & 1, p.status))) break;
+          const float m = ss.stat[par][0], ls = ss.stat[par][1];
+          if (lane == j && t >= 0) p.logp[t] = good ? log_prob(x, m, ls, p.c) : __int_as_float(0x7fc00000);
+          const int more = __shfl_sync(0xffffffffu, n, j), at = __shfl_sync(0xffffffffu, e0, j);
+          for (int i = lane; i < more; i += 32) {   // a fork's or a rewind's
+            const int t2 = p.succ.ex_row[at + i];
+            float x2 = 0.f;
+            const bool good2 = token(logits + (size_t)rl * p.ld, t2, &x2);
+            p.logp[t2] = good2 ? log_prob(x2, m, ls, p.c) : __int_as_float(0x7fc00000);
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bar.scal_empty[par]);   // after what used them
         }
-        if (!warp_wait(&bar.scal_full[par], (it >> 1) & 1, p.status)) break;
-        const float m = ss.stat[par][0], ls = ss.stat[par][1];
-#pragma unroll
-        for (int q = 0; q < kMaxSucc / 32; q++)
-          if (t[q] >= 0) p.logp[t[q]] = bad[q] ? __int_as_float(0x7fc00000) : log_prob(x[q], m, ls, p.c);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar.scal_empty[par]);   // after what used them
       }
     }
   } else if (tid >= kCopy && tid < kLook) {
@@ -644,11 +653,13 @@ struct ScoreBwdParams {
 // with the row's A = -c (G + g_H H), B = -c g_H ln 2, plus c g_t at the successors' ids.
 //
 // One pass, bound by memory: a CTA takes up to kThreads * kBwdPer vectors of a row, all of its
-// loads in flight before it looks up the row's successors.
-constexpr int kBwdThreads = 256, kBwdPer = 8;
+// loads in flight before it looks up the row's successors.  6,144 rows of 151,936 bf16, with
+// 2 / 3 / 4 / 6 / 8 vectors a thread and as many CTAs as their registers leave: 698 / 567 /
+// 542 / 554 / 570 us (6.9 TB/s).
+constexpr int kBwdPer = 4;
 
-template <typename T>
-__global__ void __launch_bounds__(kBwdThreads, 4) k_token_score_bwd(const __grid_constant__ ScoreBwdParams p) {
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1536 / kThreads) k_token_score_bwd(const __grid_constant__ ScoreBwdParams p) {
   using VT = Vec<T>;
   constexpr int E = VT::E;
   __shared__ int32_t s_t[kMaxSucc], s_id[kMaxSucc];
@@ -662,7 +673,7 @@ __global__ void __launch_bounds__(kBwdThreads, 4) k_token_score_bwd(const __grid
   uint4 w[kBwdPer];
 #pragma unroll
   for (int q = 0; q < kBwdPer; q++) {
-    const int i = v0 + q * kBwdThreads + tid;
+    const int i = v0 + q * kThreads + tid;
     if (i < v1) w[q] = __ldcs(reinterpret_cast<const uint4*>(row) + i);
   }
   const float m = p.row_stat[2 * (size_t)rl], ls = p.row_stat[2 * (size_t)rl + 1];
@@ -670,11 +681,7 @@ __global__ void __launch_bounds__(kBwdThreads, 4) k_token_score_bwd(const __grid
   if (tid < 32) {
     int nt = 0;
     if (p.g_logp) {
-      if (tid == 0) {
-        bool start;
-        nt = p.succ.find(p.row0 + rl, s_t, &start);
-      }
-      nt = __shfl_sync(0xffffffffu, nt, 0);
+      nt = p.succ.find(p.row0 + rl, s_t);
       __syncwarp();
       for (int i = tid; i < nt; i += 32) {
         const int t = s_t[i], id = p.ids[t];
@@ -707,7 +714,7 @@ __global__ void __launch_bounds__(kBwdThreads, 4) k_token_score_bwd(const __grid
     return p.c * g;
   };
   if (m == -INFINITY) {   // nothing left in the row
-    for (int i = v0 + tid; i < v1; i += kBwdThreads) __stcs(reinterpret_cast<uint4*>(grow) + i, make_uint4(0, 0, 0, 0));
+    for (int i = v0 + tid; i < v1; i += kThreads) __stcs(reinterpret_cast<uint4*>(grow) + i, make_uint4(0, 0, 0, 0));
     if (v1 == nv && tid < p.V - nv * E) VT::put(grow + nv * E + tid, 0.f);
     return;
   }
@@ -715,7 +722,7 @@ __global__ void __launch_bounds__(kBwdThreads, 4) k_token_score_bwd(const __grid
   const f2 negm = pack2(-m, -m), cc = pack2(c2, c2), nl = pack2(-l2, -l2), AA = pack2(A, A), BB = pack2(B, B);
 #pragma unroll
   for (int q = 0; q < kBwdPer; q++) {
-    const int i = v0 + q * kBwdThreads + tid;
+    const int i = v0 + q * kThreads + tid;
     if (i < v1) {
       float g[E];
 #pragma unroll
@@ -823,14 +830,21 @@ int octo_token_score_bwd(octo_plan_t plan, int32_t row0, int32_t n_rows, const v
   plan->last_stream = s;
   NvtxRange nv("octo_token_score_bwd");
   const bool bf = dtype == OCTO_DTYPE_BF16;
-  const int32_t vecs = vocab / (bf ? 8 : 4), most = kBwdThreads * kBwdPer;
+  const int32_t vecs = vocab / (bf ? 8 : 4);
+  // Short rows: a CTA is mostly waiting for its look-ups, so many small ones (1,360 rows of
+  // 256 / 1,500 entries: 11 -> 5 / 12 -> 10 us); with few rows 256 threads are no slower.
+  const int threads = vecs <= 64 * kBwdPer && n_rows > 4 * sm_count() ? 64 : 256, most = threads * kBwdPer;
   p.parts = vecs > most ? (vecs + most - 1) / most : 1;
   p.part_vecs = (vecs + p.parts - 1) / p.parts;
   if ((int64_t)n_rows * p.parts > INT32_MAX) return OCTO_EINVAL;
-  if (bf)
-    k_token_score_bwd<__nv_bfloat16><<<n_rows * p.parts, kBwdThreads, 0, s>>>(p);
-  else
-    k_token_score_bwd<float><<<n_rows * p.parts, kBwdThreads, 0, s>>>(p);
+  const int grid = n_rows * p.parts;
+  if (threads == 64) {
+    if (bf) k_token_score_bwd<__nv_bfloat16, 64><<<grid, 64, 0, s>>>(p);
+    else k_token_score_bwd<float, 64><<<grid, 64, 0, s>>>(p);
+  } else {
+    if (bf) k_token_score_bwd<__nv_bfloat16, 256><<<grid, 256, 0, s>>>(p);
+    else k_token_score_bwd<float, 256><<<grid, 256, 0, s>>>(p);
+  }
   count_launch();
   return cuda_status(cudaGetLastError());
 }

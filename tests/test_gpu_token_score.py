@@ -552,6 +552,83 @@ def test_distill_bad_ids_and_refusals(lib):
     plan.sync()
 
 
+def test_many_successors(lib):
+    """A row that 40 branches continue, one that is rewound to again and again; more than 64
+    successors are refused where tokens are asked for, and not otherwise."""
+    def tree(children):
+        pool = lib.Pool(256, 16, 1, 64, lib.DTYPE_BF16)
+        r = pool.root()
+        pool.append(r, 50)
+        for c in pool.fork(r, children):
+            pool.append(c, 2)
+        a = r
+        pool.append(a, 3)
+        for _ in range(20):
+            a = pool.rewind(a, 1) if pool.seg_info(a)["len"] > 1 else a
+            pool.append(a, 2)
+        plan = pool.pack_tree([r], 64)
+        out = plan.copy_out()
+        pred = np.full(plan.info["n_rows"], -1)
+        base = {int(s): int(b) for s, b in zip(out["seg_order"], out["seg_row_base"])}
+        for s, b in base.items():
+            i = pool.seg_info(s)
+            pred[b + 1:b + i["len"]] = np.arange(b, b + i["len"] - 1)
+            if i["parent"] >= 0 and i["len"]:
+                pred[b] = base[i["parent"]] + i["fork"] - 1
+        return pool, plan, pred
+
+    pool, plan, pred = tree(40)
+    N, V = plan.info["n_rows"], 601
+    assert 32 < np.bincount(pred[pred >= 0]).max() <= 64
+    rng = np.random.default_rng(6)
+    ids = rng.integers(0, V, N)
+    bad = ids.copy()
+    bad[int(np.nonzero(pred == 49)[0][35])] = V       # one of the fork's
+    xt, xr, stat, H = check_score(plan, pred, rng.normal(0, 3, (N, V)), "f32", ids, 4)
+    g = rng.uniform(-1, 1, N).astype(np.float32)
+    d = torch.zeros_like(xt)
+    plan.token_score_bwd(0, N, xt, V, gpu(stat), None, gpu(ids, torch.int32), gpu(g), None, d)
+    # up to 41 terms of size 1 in a row
+    close(d[:, :V].cpu().numpy(), ts.score_bwd(xr, ids, pred, g, None), "dlogits", scale=40.0)
+    run_score(plan, xt, V, bad)
+    with pytest.raises(lib.OctoError):
+        plan.sync()
+    pool, plan, pred = tree(64)
+    N = plan.info["n_rows"]
+    xt, xr = rows_on_gpu(rng.normal(0, 3, (N, V)), "f32")
+    with pytest.raises(lib.OctoError) as e:
+        run_score(plan, xt, V, rng.integers(0, V, N))
+    assert e.value.code == lib.ENOTSUP
+    _, stat, H, _, _ = run_score(plan, xt, V)
+    close(H, ts.score(xr, np.zeros(N, int), np.full(N, -1))[2], "entropy")
+    plan.sync()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_huge_vocabularies(lib, dtype):
+    """A million entries, and a refusal past what the table of listed vectors holds."""
+    V, k = 1000003, 20
+    rng = np.random.default_rng(12)
+    plan = decode_plan(lib, 2)
+    x = rng.normal(0, 3, (2, V))
+    check_score(plan, np.arange(2), x, dtype, rng.integers(0, V, 2), k)
+    ids, val = teacher(rng, 2, V, k, True)
+    check_distill(plan, x, dtype, ids, val, None, 1.0, True)
+    check_distill(plan, x, dtype, ids, val, None, 1.0, False)
+    big = torch.zeros((1, 40000000), dtype=DT[dtype], device="cuda")
+    one = decode_plan(lib, 1)
+    kl = torch.zeros(1, device="cuda")
+    with pytest.raises(lib.OctoError) as e:
+        one.distill_topk(0, 1, big, 40000000, gpu(ids[:1], torch.int32), gpu(val[:1]), kl, tail=True)
+    assert e.value.code == lib.ENOTSUP
+    one.distill_topk(0, 1, big, 40000000, gpu(ids[:1], torch.int32), gpu(val[:1]), kl)
+    one.sync()
+    # a flat student: ln V plus the teacher's negative entropy
+    _, z = ids[0] >= 0, val[0].astype(np.float64)[(ids[0] >= 0) & np.isfinite(val[0])]
+    P = np.exp(z - z.max()) / np.exp(z - z.max()).sum()
+    close(kl.cpu().numpy(), [np.log(4e7) + (P * np.log(P)).sum()], "row_kl", scale=5.0)
+
+
 def kl_loss(f):
     return torch.full_like(f[:1], 3.0)
 
