@@ -547,14 +547,14 @@ int launch_distill(DistillParams& p, cudaStream_t s) {
   if (int st = pick_cluster(f, p.n, p.dlogits ? 2 * nv : nv, kSmemMax, [](int) { return 0.7; }, &cs)) return st;
   if (p.dlogits && cs == 1) {
     // Two rows for each cluster wait in L2 for their second pass, and their gradients pass
-    // through it: past about a third of it they are read from memory again.  More CTAs a row
+    // through it: past three tenths of it they are read from memory again.  More CTAs a row
     // mean fewer rows in flight, at the price of joining the CTAs at every row, and want rows
     // for several rounds.  4,000 rows, microseconds at 1 / 2 / 4 CTAs: of 128 KB
     // 179 / 195 / 270, of 200 KB 294 / 257 / 351, of 304 KB 502 / 413 / 373; 2,000 of 608 KB
     // 520 / 506 / 386.
     const int sms = sm_count();
     auto in_flight = [&](int c) { return (int64_t)nv * 16 * 2 * (sms / c); };
-    const int64_t room = l2_bytes() / 100 * 35;
+    const int64_t room = l2_bytes() / 100 * 30;
     while (cs < 4 && in_flight(cs) > room && (int64_t)p.n * 2 * cs > 5 * sms) cs *= 2;
   }
   while (words(cs) * 4 * kMaxRows > 64 * 1024 && cs < kMaxCluster) cs *= 2;
