@@ -219,36 +219,5 @@ inline int check_rows(const octo_plan_s* plan, int32_t row0, int32_t n_rows, con
   return OCTO_OK;
 }
 
-// Sums a, b over the block's threads in a fixed shape; red: 2 * 32 floats of shared memory.
-template <int kThreads>
-__device__ __forceinline__ void block_sum2(float& a, float& b, float* red) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  const int w = threadIdx.x >> 5;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[2 * w] = a, red[2 * w + 1] = b;
-  __syncthreads();
-  a = b = 0.f;
-  for (int i = 0; i < kThreads / 32; i++) a += red[2 * i], b += red[2 * i + 1];
-}
-
-// Merges the threads' statistics; every thread gets the block's.  red: 3 * 32 floats.
-template <int kThreads>
-__device__ __forceinline__ void block_stat(Stat& st, float c2, float* red) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-    st.merge(__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-             __shfl_xor_sync(0xffffffffu, st.a, o), c2);
-  const int w = threadIdx.x >> 5;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[3 * w] = st.m, red[3 * w + 1] = st.s, red[3 * w + 2] = st.a;
-  __syncthreads();
-  st.init();
-  for (int i = 0; i < kThreads / 32; i++) st.merge(red[3 * i], red[3 * i + 1], red[3 * i + 2], c2);
-}
-
 }  // namespace rows
 }  // namespace octo

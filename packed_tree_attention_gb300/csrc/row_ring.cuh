@@ -4,9 +4,10 @@
 // A cluster of `cs` CTAs takes one row after another; each CTA has its own contiguous part of
 // the row's 16-byte vectors.  One thread copies the part, stage by stage, into the ring with
 // bulk copies (cp.async.bulk, completion on a slot's `full` barrier), running ahead over row
-// ends as far as the ring reaches; 16 consumer warps take a stage at a time, four vectors a
-// thread; two teams of 4 finisher warps, one for every other row, do what a row needs besides,
-// while the consumers are at the next.
+// ends as far as the ring reaches; four groups of 4 consumer warps take the stages in turn, so
+// that the waits of one fall into the arithmetic of another; 8 finisher warps, in teams that
+// take the rows in turn, do what a row needs besides, while the consumers are at the next ones.
+// One CTA per SM, the grid as many clusters as the device holds.
 // The copies bring whole vectors: the last V % E entries are the finishers'.
 #pragma once
 

@@ -8,6 +8,13 @@
 //   dx_v = c (sum over t with id t = v of g_t - p_v G - g_H p_v (ln p_v + H)),  G = sum_t g_t
 // (m, ln S) is kept rather than m c + ln S: at logits in the thousands the sum's rounding
 // would be a per-mille error of every probability that the gradient forms from it.
+//
+// Bound by memory: scoring reads V entries, the gradient reads and writes V.  Measured (one
+// GB300, 6.78 TB/s copied): 10,240 rows of 151,936 bf16 scored in 430 us (7.2 TB/s), 2,048 rows
+// with their top 64 in 119 us (5.2 TB/s: 13.5 rows an SM take 14 rounds, and the last row's
+// alternatives follow its sums), 256 rows with their top 20 in 23 us (two rounds), one row in
+// 11 us, most of it the chain from the launch over the copies, the threshold and the candidates
+// to the join of the cluster.  The gradient of 6,144 such rows takes 545 us (6.8 TB/s).
 
 #include <algorithm>
 
