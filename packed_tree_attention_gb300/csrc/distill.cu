@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
   if (tid == 0) bar.init(1);
   __syncthreads();
   if (rs.cs > 1) cluster_sync();
+  wait_for_predecessor();
 
   if (tid >= kCopy && tid < kFirstCons) {
     // ---- copies (rows of weight 0 are not read) ----

@@ -56,27 +56,32 @@ int max_clusters(const void* kernel, int cs, int smem, int* out) {
   return OCTO_OK;
 }
 
+int launch_overlapped(const void* kernel, const void* p, int grid, int block, int cs, int smem, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cs;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cs > 1 ? 2 : 1;
+  void* args[1] = {const_cast<void*>(p)};
+  OCTO_CUDA(cudaLaunchKernelExC(&cfg, kernel, args));
+  count_launch();
+  return OCTO_OK;
+}
+
 int launch_ring_raw(const void* kernel, const void* p, int32_t n, int cs, int smem, cudaStream_t s) {
   if (int st = set_smem_limit(kernel, kSmemMax)) return st;
   int clusters = sm_count();
   if (cs > 1)
     if (int st = max_clusters(kernel, cs, smem, &clusters)) return st;
-  clusters = std::max(1, clusters);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(n, clusters) * cs));
-  cfg.blockDim = dim3(kBlock);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cs;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
-  void* args[1] = {const_cast<void*>(p)};
-  OCTO_CUDA(cudaLaunchKernelExC(&cfg, kernel, args));
-  count_launch();
-  return OCTO_OK;
+  return launch_overlapped(kernel, p, (int)(std::min<int64_t>(n, std::max(1, clusters)) * cs), kBlock, cs, smem, s);
 }
 
 }  // namespace rows

@@ -108,6 +108,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_
   return __all_sync(0xffffffffu, ring_wait(bar, parity, status));
 }
 
+// Launched so that its start overlaps the end of the kernel before it, a kernel waits here before
+// it touches global memory.
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- clusters ----
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -395,6 +399,9 @@ int pick_cluster(const void* kernel, int32_t n, int64_t nv, int smem, F join_us,
   }
   return OCTO_OK;
 }
+
+// Launches kernel(p), which calls wait_for_predecessor, with `grid` CTAs in clusters of cs.
+int launch_overlapped(const void* kernel, const void* p, int grid, int block, int cs, int smem, cudaStream_t s);
 
 // Launches kernel(p) on n rows: a cluster of cs CTAs for each, but no more than the device holds.
 int launch_ring_raw(const void* kernel, const void* p, int32_t n, int cs, int smem, cudaStream_t s);

@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprob(LpParams p) {
 
 __global__ void __launch_bounds__(1024) k_loss_sum(const float* __restrict__ part, int32_t n, float* __restrict__ loss) {
   __shared__ float red[32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernel before has written part
   float s = 0.f;
   for (int i = threadIdx.x; i < n; i += blockDim.x) s += part[i];
 #pragma unroll
@@ -315,9 +316,19 @@ __global__ void __launch_bounds__(1024) k_loss_sum(const float* __restrict__ par
 }  // namespace
 
 int launch_loss_sum(const float* part, int32_t n, float* loss, cudaStream_t s) {
-  k_loss_sum<<<1, 1024, 0, s>>>(part, n, loss);
+  // placed on an SM while the kernel before drains, and waiting there for its end
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  OCTO_CUDA(cudaLaunchKernelEx(&cfg, k_loss_sum, part, n, loss));
   count_launch();
-  return cuda_status(cudaGetLastError());
+  return OCTO_OK;
 }
 
 }  // namespace octo

@@ -436,6 +436,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_token_score(const __grid_constant
   if (tid == 0) bar.init(kFinWarps);
   __syncthreads();
   if (rs.cs > 1) cluster_sync();
+  wait_for_predecessor();
 
   if (tid >= kLook && tid < kFirstCons) {
     // ---- look-ups: the tokens that the rows feed, 32 rows at a time, a lane for each ----
@@ -677,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) k_token_score_bwd(c
   const T* row = reinterpret_cast<const T*>(p.logits) + (size_t)rl * p.ld;
   T* grow = reinterpret_cast<T*>(p.dlogits) + (size_t)rl * p.ld;
   const int nv = p.V / E, v0 = part * p.part_vecs, v1 = min(nv, v0 + p.part_vecs);
+  wait_for_predecessor();
   uint4 w[kBwdPer];
 #pragma unroll
   for (int q = 0; q < kBwdPer; q++) {
@@ -845,15 +847,9 @@ int octo_token_score_bwd(octo_plan_t plan, int32_t row0, int32_t n_rows, const v
   p.part_vecs = (vecs + p.parts - 1) / p.parts;
   if ((int64_t)n_rows * p.parts > INT32_MAX) return OCTO_EINVAL;
   const int grid = n_rows * p.parts;
-  if (threads == 64) {
-    if (bf) k_token_score_bwd<__nv_bfloat16, 64><<<grid, 64, 0, s>>>(p);
-    else k_token_score_bwd<float, 64><<<grid, 64, 0, s>>>(p);
-  } else {
-    if (bf) k_token_score_bwd<__nv_bfloat16, 256><<<grid, 256, 0, s>>>(p);
-    else k_token_score_bwd<float, 256><<<grid, 256, 0, s>>>(p);
-  }
-  count_launch();
-  return cuda_status(cudaGetLastError());
+  const void* f = threads == 64 ? (bf ? (const void*)k_token_score_bwd<__nv_bfloat16, 64> : (const void*)k_token_score_bwd<float, 64>)
+                                : (bf ? (const void*)k_token_score_bwd<__nv_bfloat16, 256> : (const void*)k_token_score_bwd<float, 256>);
+  return launch_overlapped(f, &p, grid, threads, 1, 0, s);
 }
 
 }  // extern "C"
