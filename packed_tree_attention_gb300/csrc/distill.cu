@@ -562,10 +562,12 @@ int launch_distill(DistillParams& p, cudaStream_t s) {
     // mean fewer rows in flight, at the price of joining the CTAs at every row, and want rows
     // for several rounds.  4,000 rows, microseconds at 1 / 2 / 4 CTAs: of 128 KB
     // 179 / 195 / 270, of 200 KB 294 / 257 / 351, of 304 KB 502 / 413 / 373; 2,000 of 608 KB
-    // 520 / 506 / 386.
+    // 520 / 506 / 386.  A cluster's joins at a row cost more with the rest class, whose CTAs each
+    // clear and fill a bitmap: four tenths there (8,192 rows of 304 KB at 2 / 4 CTAs: 790 / 828
+    // us with it, 803 / 761 without it).
     const int sms = sm_count();
     auto in_flight = [&](int c) { return (int64_t)nv * 16 * 2 * (sms / c); };
-    const int64_t room = l2_bytes() / 100 * 30;
+    const int64_t room = l2_bytes() / 100 * (p.tail ? 40 : 30);
     while (cs < 4 && in_flight(cs) > room && (int64_t)p.n * 2 * cs > 5 * sms) cs *= 2;
   }
   while (words(cs) * 4 * kMaxRows > 64 * 1024 && cs < kMaxCluster) cs *= 2;
