@@ -329,8 +329,9 @@ int octo_token_logprob(octo_plan_t plan, int32_t row0, int32_t n_rows, const voi
  * The log-probability of octo_token_logprob without its loss, and beside it how sure each
  * row is and what else it holds likely: for entropy bonuses and monitoring, for a serving
  * step's log-probabilities, and as the teacher's side of octo_distill_topk.
- * Rows [row0, row0 + n_rows) of a plan; logits, dtype, ld and vocab as in
- * octo_token_logprob (columns past vocab are neither read nor written).  Tokens t of row r:
+ * Rows [row0, row0 + n_rows) of a plan built on the current device (OCTO_EINVAL on another);
+ * logits, dtype, ld and vocab as in octo_token_logprob (columns past vocab are neither read
+ * nor written).  Tokens t of row r:
  * on a pack plan the rows that continue r (pred t = r above); on a decode plan the token
  * that cursor r takes next, t = r.  ids, logp, g_logp: device arrays over ALL rows of the
  * plan; row_stat, entropy, g_entropy, top_ids, top_logp start at row row0.
@@ -390,7 +391,8 @@ int octo_distill_topk_workspace_size(int32_t n_rows, size_t* bytes);
  * octo_token_logprob.  1 <= k <= 128 (k may exceed vocab).  weight (NULL: ones) and row_kl:
  * device floats over ALL rows of the plan; row_kl[r] is written without the weight.
  * dlogits (optional): dtype, layout and alignment of logits; may be logits itself.  loss
- * (optional, one device float, needs ws): sum of w_r KL_r over the chunk, in a fixed order.
+ * (optional, one device float, needs ws, 4-byte aligned): sum of w_r KL_r over the chunk, in a
+ * fixed order.
  * Teacher ids >= vocab count as empty and give OCTO_EINVAL at the next octo_sync.
  * OCTO_ENOTSUP at tail = 1 for vocabularies past some 2 million entries (fp32) or 4 (bf16).
  * Deterministic.  Async on stream. */

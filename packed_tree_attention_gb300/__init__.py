@@ -561,6 +561,8 @@ class Plan:
             ws_bytes = ws.numel() * ws.element_size()
             if ws.get_device() != dev:
                 raise _elsewhere(ws, "ws")
+            if not ws.is_contiguous():
+                raise ValueError("ws must be contiguous")
         _chk(self._L.octo_distill_topk(
             self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, k, _vector(teach_ids, "int32", n_rows * k, dev, "teach_ids"),
             _vector(teach_val, "float32", n_rows * k, dev, "teach_val"), 1 if tail else 0,

@@ -853,7 +853,10 @@ int compile_plan(octo_pool_s* pool, const int32_t* tile_segs_host, const int32_t
     OCTO_CUDA(cudaMalloc(&pool->d_status, sizeof(int32_t) * 4));
     OCTO_CUDA(cudaMemset(pool->d_status, 0, sizeof(int32_t) * 4));
   }
+  int device = 0;
+  OCTO_CUDA(cudaGetDevice(&device));
   octo_plan_s* pl = new octo_plan_s();
+  pl->device = device;
   pl->pool = pool;
   pl->last_stream = s;
   pl->num_pages = pool->desc.num_pages;

@@ -602,7 +602,7 @@ int octo_distill_topk(octo_plan_t plan, int32_t row0, int32_t n_rows, const void
   }
   size_t need = 0;
   octo_distill_topk_workspace_size(n_rows, &need);
-  if (!teach_ids || !teach_val || !row_kl || (loss && (!ws || ws_bytes < need))) return OCTO_EINVAL;
+  if (!teach_ids || !teach_val || !row_kl || (loss && (!ws || ws_bytes < need || ((uintptr_t)ws & 3)))) return OCTO_EINVAL;
   DistillParams p;
   p.logits = logits;
   p.dlogits = dlogits;

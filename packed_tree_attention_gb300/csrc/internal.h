@@ -144,6 +144,7 @@ struct octo_plan_s {
   size_t entries_cap = 0, csc_cap = 0, poff_cap = 0, touched_cap = 0, buf_cap = 0;   // current arrays
   cudaEvent_t order_ev = nullptr;    // orders an advance after work on another stream
   cudaStream_t last_stream = nullptr;  // stream of the last call that used the plan
+  int device = 0;                    // that the plan's arrays are on
 };
 
 namespace octo {

@@ -216,7 +216,9 @@ inline int check_rows(const octo_plan_s* plan, int32_t row0, int32_t n_rows, con
   const size_t es = dtype == OCTO_DTYPE_BF16 ? 2 : 4;
   if (((uintptr_t)logits & 15) || ((size_t)ld * es) % 16) return OCTO_EINVAL;
   if (n_rows > 0 && !logits) return OCTO_EINVAL;
-  return OCTO_OK;
+  int dev = 0;
+  OCTO_CUDA(cudaGetDevice(&dev));
+  return dev == plan->device ? OCTO_OK : OCTO_EINVAL;
 }
 
 }  // namespace rows

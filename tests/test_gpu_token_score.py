@@ -508,6 +508,27 @@ def test_distill_masks(lib, dtype, tail):
     check_distill(decode_plan(lib, n), x, dtype, ids, val, None, 1.0, tail)
 
 
+def test_distill_refuses_unfit_workspaces(lib):
+    """A workspace that its floats cannot be stored in: off a 4-byte boundary, or expanded from
+    fewer bytes than it seems to have."""
+    N, V, k = 30, 300, 5
+    plan = chain_plan(lib, N)
+    rng = np.random.default_rng(3)
+    xt, _ = rows_on_gpu(rng.normal(0, 3, (N, V)), "f32")
+    ids, val = teacher(rng, N, V, k, False)
+    ti, tv, f, loss = gpu(ids, torch.int32), gpu(val), torch.zeros(N, device="cuda"), torch.zeros(1, device="cuda")
+    need = plan.distill_topk_workspace_size(N)
+    big = torch.zeros(need + 16, dtype=torch.uint8, device="cuda")
+    for ws in (big[1:], big[2:], big[:1].expand(need), big.repeat(2)[::2]):
+        with pytest.raises((lib.OctoError, ValueError)):
+            plan.distill_topk(0, N, xt, V, ti, tv, f, ws=ws, loss=loss)
+    plan.distill_topk(0, N, xt, V, ti, tv, f, ws=big[4:], loss=loss)
+    plan.sync()
+    torch.cuda.synchronize()
+    assert abs(loss.item() - f.double().sum().item()) <= 1e-5 * (1 + abs(loss.item()))
+
+
+
 def test_distill_bad_ids_and_refusals(lib):
     N, V, k = 30, 300, 5
     plan = chain_plan(lib, N)
