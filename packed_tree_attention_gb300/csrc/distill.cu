@@ -12,7 +12,9 @@
 // q_R is summed over the entries outside the list itself: 1 - sum_i q_i would lose it
 // where the list holds nearly all of the mass.  For that, the consumers leave out every
 // 16-byte vector that holds a listed id (a bit each in a table of the row's vectors), and a
-// finisher adds what those hold besides.  The gradient pass writes every entry as an unlisted
+// finisher adds what those hold besides.  With the rest class the divergence is summed as
+// sum of (P d - P + q), d = ln P - ln q, whose terms are never negative (share below): 180 rows of
+// 30,000 fp32 entries at a divergence of 2e-5 come out 3e-5 of it off, and 2e-3 by the plain sum.  The gradient pass writes every entry as an unlisted
 // one, and the finisher then writes the listed ones.
 //
 // Bound by memory: V entries read and, for the gradient, V written; the second reading comes
@@ -87,6 +89,24 @@ __device__ __forceinline__ void split_log(float s, float* hi, float* lo) {
   // ln 2 = 355 / 512 + a rest (Cody and Waite's reduction): e * 355 / 512 is exact
   *hi = normal ? (float)e * (355.f / 512.f) : logf(s);
   *lo = normal ? fmaf((float)e, (float)(0.69314718055994531 - 355.0 / 512.0), logf(f)) : 0.f;
+}
+
+// A class's share of a divergence whose classes hold all of both masses: P d + (q - P), d = ln P - ln q.
+// The terms added are 0 in sum, and each share is P (d + e^-d - 1) >= 0, of second order in d:
+// an error of d is felt times d only.  Near a student that has learnt its teacher the plain sum
+// of P d is the small rest of terms of both signs.
+__device__ __forceinline__ float share(float P, float d, float q) {
+  if (!(fabsf(d) < 0.5f)) return P == 0.f ? q : P * d + (q - P);
+  // the power series from d^2 / 2 on; what is left out is below 3e-9 of it
+  float h = -1.f / 362880;
+  h = fmaf(h, d, 1.f / 40320);
+  h = fmaf(h, d, -1.f / 5040);
+  h = fmaf(h, d, 1.f / 720);
+  h = fmaf(h, d, -1.f / 120);
+  h = fmaf(h, d, 1.f / 24);
+  h = fmaf(h, d, -1.f / 6);
+  h = fmaf(h, d, 0.5f);
+  return P * d * d * h;
 }
 
 // With a gradient every row is streamed twice, the first pass of the next row before the second
@@ -504,12 +524,18 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         fix[q] = 0.f;
         if (!has || id[q] < 0) continue;
         const float lq = fmaf(ws.x[q * 32 + lane] - all.m, p.c, -ls) - ls_lo;
-        if (pe[q] != 0.f) kl += pe[q] * (lp[q] - lq);
+        if (p.tail) {   // an id's q goes to its first entry
+          const float d = lp[q] - lq;
+          kl += first >> q & 1 ? share(pe[q], d, expf(lq)) : pe[q] == 0.f ? 0.f : pe[q] * d - pe[q];
+        } else if (pe[q] != 0.f) {
+          kl += pe[q] * (lp[q] - lq);
+        }
         if (kGrad) fix[q] = f * (expf(lq) * (total + pr) - sub[q]);
       }
       if (rank == 0) {
         kl = warp_sum(kl);
-        if (has && pr != 0.f) kl += pr * (logf(pr) - lqr);
+        if (has && p.tail)   // without a rest in the teacher its masses need not be 1 in sum
+          kl += pr != 0.f ? share(pr, logf(pr) - lqr, expf(lqr)) : (o.s == 0.f ? 0.f : expf(lqr)) + (total - 1.f);
         if (lane == 0) {
           p.row_kl[p.row0 + r] = kl;
           if (p.part) p.part[r] = has ? w * kl : 0.f;

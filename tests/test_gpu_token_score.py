@@ -508,6 +508,39 @@ def test_distill_masks(lib, dtype, tail):
     check_distill(decode_plan(lib, n), x, dtype, ids, val, None, 1.0, tail)
 
 
+@pytest.mark.parametrize("noise", [0.0, 1e-5, 1e-3, 0.1, 0.7])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_distill_of_a_student_near_its_teacher(lib, dt, noise):
+    """With the rest class the error of a divergence falls with the divergence: an error e of a
+    class's d = ln P - ln q is felt as P |d| e + P e^2.  e: two roundings (2^-24) of ln P, of ln q and
+    of the numbers up to 2 that they are made of."""
+    N, V, k = 48, 3001, 20
+    plan = chain_plan(lib, N)
+    rng = np.random.default_rng(7)
+    xt, xr = rows_on_gpu(rng.normal(0, 3, (N, V)), dt)
+    z = xr + noise * rng.normal(size=(N, V))
+    z = z - np.log(np.exp(z - z.max(1, keepdims=True)).sum(1, keepdims=True)) - z.max(1, keepdims=True)
+    ids = np.argsort(-z, axis=1)[:, :k].copy()
+    ids[3, 1] = ids[3, 0] = -1                                      # empty entries: their mass is the rest's
+    val = np.take_along_axis(z, np.maximum(ids, 0), 1).astype(np.float32)
+    kl, _, _ = run_distill(plan, xt, V, ids, val, None, 1.0, True, None)
+    plan.sync()
+    rkl = ts.distill(xr, ids, val, tail=True)[0]
+    lq = xr - xr.max(1, keepdims=True)
+    lq = lq - np.log(np.exp(lq).sum(1, keepdims=True))
+    lqi = np.take_along_axis(lq, np.maximum(ids, 0), 1)
+    P = np.where(ids < 0, 0.0, np.exp(val.astype(np.float64)))
+    q = np.where(ids < 0, 0.0, np.exp(lqi))
+    pr, qr = 1 - P.sum(1), 1 - q.sum(1)
+    d, dr = np.abs(val - lqi), np.abs(np.log(pr / qr))
+    eps = 2.0 ** -24
+    # P_R and q_R are sums of 1 and of exponentials, each good to 4 roundings
+    bound = (P * d * 2 * eps * (np.abs(val) + np.abs(lqi) + 2)).sum(1) + dr * 8 * eps + pr * dr * 2 * eps * (np.abs(np.log(qr)) + 4)
+    bound = bound + ((2 * eps * (np.abs(val) + np.abs(lqi) + 2)) ** 2 * P).sum(1) + (16 * eps) ** 2 / pr + 16 * eps * rkl
+    assert (kl >= 0).all()
+    assert (np.abs(kl - rkl) <= bound).all(), np.max(np.abs(kl - rkl) / bound)
+
+
 def test_distill_refuses_unfit_workspaces(lib):
     """A workspace that its floats cannot be stored in: off a 4-byte boundary, or expanded from
     fewer bytes than it seems to have."""
