@@ -380,9 +380,10 @@ int octo_token_score_bwd(octo_plan_t plan, int32_t row0, int32_t n_rows, const v
  *     dlogits[r][v] = grad_scale w_r c (q_v P - sum over i with id_i = v of P_i
  *                     - [v not listed] P_R q_v / q_R),  P = sum_i P_i + P_R.
  * An id may be listed more than once: its entries add up.  The rest term is dropped where no
- * unlisted id has mass in the student.  A row whose weight is 0 (its logits are not read),
- * whose student logits are all -inf, or, at tail = 0, whose entries are all empty, has
- * divergence 0 and a zero gradient. */
+ * unlisted id has mass in the student: where ln q_v < -745 for all of them, less than 64 bits
+ * hold, as for logits masked with -inf, the type's lowest value or another far one.  A row
+ * whose weight is 0 (its logits are not read), whose student logits are all -inf, or, at
+ * tail = 0, whose entries are all empty, has divergence 0 and a zero gradient. */
 
 /* Workspace (bytes) for octo_distill_topk's loss over n_rows rows. */
 int octo_distill_topk_workspace_size(int32_t n_rows, size_t* bytes);

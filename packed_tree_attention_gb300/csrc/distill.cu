@@ -54,6 +54,9 @@ struct RowScale {
   float f, hi, m, l2;
   int32_t live, usual;
 };
+// ln of the least probability that 64 bits hold.  Where every id outside the list is below it
+// (masked with -inf, the type's lowest value or another far one), the rest class is dropped.
+constexpr float kNoMass = -745.13f;
 constexpr int kHashWords = 64;   // of the test for entries in one vector
 
 // Of each finisher warp: the entries of its row, and the CTAs' sums, of every other of its rows.
@@ -495,18 +498,21 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       if (p.tail) all.merge(in.m, in.s, 0.f, c2);
       const bool has = live && all.s != 0.f;
       const float f = p.gs * w * p.c;
-      float ls = 0.f, ls_lo = 0.f, lqr = 0.f;
+      float ls = 0.f, ls_lo = 0.f, lqr = 0.f, qr = 0.f;
       RowScale sc = {0.f, 0.f, 0.f, 0.f, 0, 1};
       if (has) {
         const float lo = logf(o.s);
         split_log(all.s, &ls, &ls_lo);
-        if (o.s == 0.f) pr = 0.f;   // nothing outside the list has mass
+        // o's sum is relative to its own largest entry, and 0 only where all are -inf
+        const bool rest = o.s != 0.f && !((o.m - all.m) * p.c - ls < kNoMass);
+        if (!rest) pr = 0.f;   // nothing outside the list has mass
         // ln q_R: by the ratio of the sums, unless one's reference is too far below the other's
         Stat far = o;
         far.rebase(all.m, c2);
         lqr = far.s > 1e-30f ? logf(far.s / all.s) : (o.m - all.m) * p.c + lo - ls - ls_lo;
+        if (rest) qr = expf(lqr);
         sc.live = 1;
-        sc.f = o.s == 0.f ? 0.f : f * (p.tail ? expf(lqr) * (total + pr) - pr : total);
+        sc.f = !p.tail ? f * total : rest ? f * (qr * (total + pr) - pr) : 0.f;
         if (o.s != 0.f) sc.m = o.m, sc.l2 = lo * kLog2e;
         sc.usual = StageStat<T, false>::usual(sc.m, c2);
         // hi = c2 m + l2 rounded; what it leaves out goes into the factor
@@ -536,7 +542,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       if (rank == 0) {
         kl = warp_sum(kl);
         if (has && p.tail)   // without a rest in the teacher its masses need not be 1 in sum
-          kl += pr != 0.f ? share(pr, logf(pr) - lqr, expf(lqr)) : (o.s == 0.f ? 0.f : expf(lqr)) + (total - 1.f);
+          kl += pr != 0.f ? share(pr, logf(pr) - lqr, qr) : qr + (total - 1.f);
         if (lane == 0) {
           p.row_kl[p.row0 + r] = kl;
           if (p.part) p.part[r] = has ? w * kl : 0.f;

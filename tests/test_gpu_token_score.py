@@ -767,3 +767,33 @@ def test_score_after_a_decode_step(lib):
         check_score(plan, np.arange(n), rng.normal(0, 3, (n, 4001)), "bf16", rng.integers(0, 4001, n), 10)
         pool.append_step(cur)
         plan.advance()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,c", [(2003, 1.0), (2003, 0.5), (50, 1.0), (70001, 1.0)])
+def test_distill_rest_outside_64_bits(lib, dtype, V, c):
+    """The rest class drops out where no unlisted id has a probability that 64 bits can hold:
+    masked with the type's lowest value, a far one, -inf, or several of them; it stays where one
+    has, however small."""
+    k, n = 8, 9
+    low = -3.3895313892515355e38 if dtype == "bf16" else np.finfo(np.float32).min
+    rng = np.random.default_rng(V)
+    x = rng.normal(0, 1, (n, V))
+    ids = np.stack([rng.choice(V, k, replace=False) for _ in range(n)]).astype(np.int32)
+    val = np.log(rng.dirichlet(np.ones(k + 1), n)[:, :k]).astype(np.float32)
+    out = np.ones((n, V), bool)
+    np.put_along_axis(out, ids, False, 1)
+    for r, far in enumerate([low, -1e30, -9984.0, low, -700.0 / c, -800.0 / c, low, low]):
+        x[r, out[r]] = far
+    at = np.flatnonzero(out[3])[V // 3]
+    x[3, at] = 0.5                                     # one of them lives
+    x[6, out[6] & (np.arange(V) % 3 == 0)] = -np.inf
+    x[7, ~out[7]] += 5000.0                            # far from zero
+    check_distill(decode_plan(lib, n), x, dtype, ids, val, None, c, True)
+    # the row masked with the lowest value is the row masked with -inf
+    y = x.copy()
+    y[x < -1e29] = -np.inf
+    a, b = (run_distill(decode_plan(lib, n), rows_on_gpu(z, dtype)[0], V, ids, val, None, c, True, "sep") for z in (x, y))
+    for r in (0, 1, 6, 7):
+        close(a[0][r], b[0][r], "row_kl", scale=5.0)
+        close(a[2][r, :V], b[2][r, :V], "dlogits", dtype == "bf16", scale=2.0)
