@@ -956,10 +956,13 @@ int compile_plan(octo_pool_s* pool, const int32_t* tile_segs_host, const int32_t
       }
     }
     std::sort(ex.begin(), ex.end());
+    std::vector<char> last((size_t)acc, 0);  // rows that end their segment: no next row of its own
+    for (int32_t k = 0; k < n_segs; k++)
+      if (const int32_t len = pool->segs[seg_order_host[k]].len) last[rbase[k] + len - 1] = 1;
     int32_t run = 0;
     for (size_t i = 0; i < ex.size(); i++) {
       run = (i > 0 && ex[i].first == ex[i - 1].first) ? run + 1 : 1;
-      pl->max_succ = std::max(pl->max_succ, run + 1);  // + the next own row
+      pl->max_succ = std::max(pl->max_succ, run + (last[ex[i].first] ? 0 : 1));
     }
     pl->max_succ = std::max(pl->max_succ, 1);
     ep.resize(ex.size());

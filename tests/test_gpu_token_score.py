@@ -797,3 +797,50 @@ def test_distill_rest_outside_64_bits(lib, dtype, V, c):
     for r in (0, 1, 6, 7):
         close(a[0][r], b[0][r], "row_kl", scale=5.0)
         close(a[2][r, :V], b[2][r, :V], "dlogits", dtype == "bf16", scale=2.0)
+
+
+@pytest.mark.parametrize("branches,goes_on,fits", [(64, False, True), (63, True, True), (65, False, False), (64, True, False)])
+def test_most_successors(lib, branches, goes_on, fits):
+    """64 successors are taken, whether one of them is the row's own next or all are branches."""
+    pool = lib.Pool(256, 16, 1, 64, lib.DTYPE_BF16)
+    r = pool.root()
+    P = 20
+    pool.append(r, P)
+    kids = pool.fork(r, branches)
+    for c in kids:
+        pool.append(c, 2)
+    if goes_on:
+        pool.append(r, 3)
+    plan = pool.pack_tree([r], 64)
+    out = plan.copy_out()
+    N, V = plan.info["n_rows"], 601
+    pred = np.arange(-1, N - 1)
+    base = {int(s): int(b) for s, b in zip(out["seg_order"], out["seg_row_base"])}
+    pred[base[r]] = -1
+    for c in kids:
+        pred[base[c]] = base[r] + P - 1
+    assert (np.bincount(pred[pred >= 0]).max() <= 64) == fits
+    rng = np.random.default_rng(branches)
+    ids = rng.integers(0, V, N)
+    g = rng.uniform(-1, 1, N).astype(np.float32)
+    x = rng.normal(0, 3, (N, V))
+    if not fits:
+        xt, _ = rows_on_gpu(x, "f32")
+        d, st = torch.zeros_like(xt), torch.zeros((N, 2), device="cuda")
+        for call in (lambda: run_score(plan, xt, V, ids),
+                     lambda: plan.token_score_bwd(0, N, xt, V, st, None, gpu(ids, torch.int32), gpu(g), None, d)):
+            with pytest.raises(lib.OctoError) as e:
+                call()
+            assert e.value.code == lib.ENOTSUP
+        return
+    xt, xr, stat, _ = check_score(plan, pred, x, "f32", ids, 3)
+    d = torch.zeros_like(xt)
+    plan.token_score_bwd(0, N, xt, V, gpu(stat), None, gpu(ids, torch.int32), gpu(g), None, d)
+    plan.sync()
+    # up to 64 terms of size 1 in a row
+    close(d[:, :V].cpu().numpy(), ts.score_bwd(xr, ids, pred, g, None), "dlogits", scale=64.0)
+    logp = torch.zeros(N, device="cuda")
+    ws = torch.empty(plan.token_logprob_workspace_size(N), dtype=torch.uint8, device="cuda")
+    plan.token_logprob(0, N, xt, V, gpu(ids, torch.int32), None, logp, ws)
+    plan.sync()
+    close(logp.cpu().numpy(), ts.score(xr, ids, pred)[0], "token_logprob's")
