@@ -411,8 +411,10 @@ __device__ int part_top(const T* row, const ScoreParams& p, TopSmem& ts, uint64_
   return rank_cand(ts, team, k, lo, buf);
 }
 
+// Of a masked entry -inf, also where all of the row are (ls = -inf), but NaN in a row of a NaN or
+// +inf logit (ls NaN).
 __device__ __forceinline__ float log_prob(float x, float m, float ls, float c) {
-  return x == -INFINITY ? -INFINITY : (x - m) * c - ls;
+  return x == -INFINITY && ls == ls ? -INFINITY : (x - m) * c - ls;
 }
 
 template <typename T, bool kTop>

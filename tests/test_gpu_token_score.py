@@ -844,3 +844,35 @@ def test_most_successors(lib, branches, goes_on, fits):
     plan.token_logprob(0, N, xt, V, gpu(ids, torch.int32), None, logp, ws)
     plan.sync()
     close(logp.cpu().numpy(), ts.score(xr, ids, pred)[0], "token_logprob's")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [3001, 12])
+def test_score_masked_entries_of_bad_rows(lib, dtype, V):
+    """A NaN or +inf logit makes every log-probability of its row NaN, those of entries masked at
+    -inf too."""
+    k = 8
+    rng = np.random.default_rng(V)
+    x = np.where(rng.random((7, V)) < 0.6, -np.inf, rng.normal(0, 3, (7, V)))
+    x[0, 2] = np.nan
+    x[1, 2] = np.inf
+    x[2] = -np.inf
+    x[2, 5] = np.nan                                   # nothing else: the alternatives are masked ones
+    x[3] = -np.inf
+    x[3, 5] = np.inf
+    x[4] = -np.inf                                     # an empty row is no bad one
+    ids = np.zeros(7, int)
+    x[:, 0] = -np.inf                                  # every row's token is masked
+    plan = decode_plan(lib, 7)
+    xt, xr = rows_on_gpu(x, dtype)
+    logp, stat, H, ti, tl = run_score(plan, xt, V, ids, k)
+    plan.sync()
+    assert np.isnan(logp[:4]).all() and np.isnan(tl[:4]).all() and np.isnan(stat[:4, 1]).all() and np.isnan(H[:4]).all()
+    assert ti[1, 0] == 2 and ti[3, 0] == 5
+    assert np.array_equal(ti[2], [0, 1, 2, 3, 4, 6, 7, 8])
+    good = slice(4, 7)
+    rl, rs, rH, rti, rtl = ts.score(xr[good], ids[good], np.arange(3), 1.0, k)
+    close(logp[good], rl, "logp")
+    close(H[good], rH, "entropy")
+    assert np.array_equal(ti[good], rti)
+    close(tl[good], rtl, "top logp")
