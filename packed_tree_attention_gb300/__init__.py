@@ -207,7 +207,7 @@ def _logits(x, n_rows, vocab, dev, what="logits"):
     if x.get_device() != dev:
         raise _elsewhere(x, what)
     # one row: any pitch will do, and the library wants 16-byte ones
-    return x.data_ptr(), dt, stride[0] if shape[0] > 1 else -(-max(vocab, 1) // 8) * 8
+    return x.data_ptr(), dt, stride[0] if n_rows > 1 else -(-max(vocab, 1) // 8) * 8
 
 
 def _vector(x, name, count, dev, what):

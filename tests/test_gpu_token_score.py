@@ -876,3 +876,36 @@ def test_score_masked_entries_of_bad_rows(lib, dtype, V):
     close(H[good], rH, "entropy")
     assert np.array_equal(ti[good], rti)
     close(tl[good], rtl, "top logp")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_row_against_a_buffer_of_several(lib, dtype):
+    """A last chunk of one row: the pitch of a single row matters to nobody."""
+    V, k, N = 1001, 6, 5
+    plan = chain_plan(lib, N)
+    rng = np.random.default_rng(4)
+    x = np.full((N, 1104), np.nan)
+    x[:, :V] = rng.normal(0, 3, (N, V))
+    xt = torch.from_numpy(x.astype(np.float32)).to(DT[dtype]).cuda()
+    xr = xt[:, :V].double().cpu().numpy()
+    ids, val = teacher(rng, N, V, k, False)
+    tok = rng.integers(0, V, N)
+    g = rng.uniform(-1, 1, N).astype(np.float32)
+    stat = gpu(ts.score(xr, tok, np.arange(-1, N - 1))[1])
+    want = ts.score_bwd(xr, tok, np.arange(-1, N - 1), g, None)
+    _, _, want_d = ts.distill(xr, ids, val)
+    kl = torch.zeros(N, device="cuda")
+    last = slice(N - 2, N - 1)
+    for logits, grad in ((xt[N - 2:], torch.full((1, 1104), -7.0, device="cuda", dtype=DT[dtype])),
+                         (xt[last], torch.full((N, 1104), -7.0, device="cuda", dtype=DT[dtype])),
+                         (xt[last], torch.full((N, 1208), -7.0, device="cuda", dtype=DT[dtype])),
+                         (xt[last].clone(), torch.full((3, 1008), -7.0, device="cuda", dtype=DT[dtype]))):
+        plan.token_score_bwd(N - 2, 1, logits, V, stat[last], None, gpu(tok, torch.int32), gpu(g), None, grad)
+        close(grad[0, :V].float().cpu().numpy(), want[N - 2], "dlogits", dtype == "bf16", scale=4.0)
+        plan.distill_topk(N - 2, 1, logits, V, gpu(ids[last], torch.int32), gpu(val[last]), kl, dlogits=grad)
+        close(grad[0, :V].float().cpu().numpy(), want_d[N - 2], "distillation's", dtype == "bf16", scale=2.0)
+        assert (grad[0, V:] == -7.0).all() and (grad[1:] == -7.0).all()
+    for n in (2, 3):
+        with pytest.raises(ValueError):
+            plan.token_score_bwd(0, n, xt, V, stat, None, gpu(tok, torch.int32), gpu(g), None, torch.zeros((N, 1208), device="cuda", dtype=DT[dtype]))
+    plan.sync()

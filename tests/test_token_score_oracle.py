@@ -100,3 +100,38 @@ def test_binding_refuses_bad_tensors():
     for bad, n, where in ((i, 4, dev), (f[::2], 4, dev), (f, 9, dev), (f, 4, dev + 1)):
         with pytest.raises(ValueError):
             pta._vector(bad, "float32", n, where, "logp")
+
+
+def test_binding_takes_one_row_of_any_pitch(monkeypatch):
+    """Logits and gradient of one row need no common pitch, in tensors of one row or of several; of
+    two rows they do."""
+    torch = pytest.importorskip("torch")
+    import packed_tree_attention_gb300 as pta
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: calls.append((name, a)) or 0
+
+    pta._torch()
+    monkeypatch.setattr(pta, "_device", lambda: -1)
+    p = pta.Plan.__new__(pta.Plan)
+    p.info, p.h, p._L = {"n_rows": 4}, None, Lib()
+    f, i = torch.zeros(8), torch.zeros(8, dtype=torch.int32)
+    wide, narrow, one, odd = torch.zeros((4, 64)), torch.zeros((3, 56)), torch.zeros((1, 72)), torch.zeros((4, 51))
+
+    def both(logits, grad, n):
+        p.token_score_bwd(0, n, logits, 50, f, None, i, f, None, grad, stream=0)
+        p.distill_topk(0, n, logits, 50, i.view(4, 2), f.view(4, 2), f, dlogits=grad, stream=0)
+
+    for logits in (wide, narrow, one, odd):
+        for grad in (wide, narrow, one, odd):
+            both(logits, grad, 1)
+            for name, a in calls[-2:]:
+                assert a[3] == logits.data_ptr() and a[5] >= 50 and a[5] % 8 == 0
+            assert grad.data_ptr() in calls[-2][1] and grad.data_ptr() in calls[-1][1]
+    both(wide, torch.zeros((2, 64)), 2)
+    assert [a[5] for _, a in calls[-2:]] == [64, 64]
+    for logits, grad in ((wide, narrow), (narrow, wide), (wide, one)):
+        with pytest.raises(ValueError):
+            both(logits, grad, 2)
