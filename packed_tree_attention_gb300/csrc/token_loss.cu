@@ -296,11 +296,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_token_logprob(LpParams p) {
   }
 }
 
-__global__ void __launch_bounds__(1024) k_loss_sum(const float* __restrict__ part, int32_t n, float* __restrict__ loss) {
+// part is written by the kernel before, which may still run when this one starts: no promise to
+// the compiler that its bytes stay the same (const __restrict__), and loads that go to L2.
+__global__ void __launch_bounds__(1024) k_loss_sum(const float* part, int32_t n, float* loss) {
   __shared__ float red[32];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernel before has written part
   float s = 0.f;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) s += part[i];
+  for (int i = threadIdx.x; i < n; i += blockDim.x) s += __ldcg(part + i);
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;

@@ -909,3 +909,48 @@ def test_one_row_against_a_buffer_of_several(lib, dtype):
         with pytest.raises(ValueError):
             plan.token_score_bwd(0, n, xt, V, stat, None, gpu(tok, torch.int32), gpu(g), None, torch.zeros((N, 1208), device="cuda", dtype=DT[dtype]))
     plan.sync()
+
+
+@pytest.mark.parametrize("n", [1, 900, 5000])
+def test_losses_of_calls_in_a_row(lib, n):
+    """Calls that follow one another on one workspace, each sum of row losses started while the rows
+    are still in work: every loss is that of its own call's rows, launched and replayed."""
+    V, k, calls = 640, 3, 24
+    plan = chain_plan(lib, n)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    xt = torch.randn((n, V), generator=g, device="cuda")
+    ids = torch.stack([torch.randperm(V, generator=g, device="cuda")[:k] for _ in range(n)]).to(torch.int32)
+    val = torch.randn((n, k), generator=g, device="cuda")
+    tok = torch.randint(0, V, (n,), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand((calls, n), generator=g, device="cuda") * torch.arange(1, calls + 1, device="cuda")[:, None]
+    kl, logp = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    ws = torch.empty(plan.distill_topk_workspace_size(n), dtype=torch.uint8, device="cuda")
+    ws2 = torch.empty(plan.token_logprob_workspace_size(n), dtype=torch.uint8, device="cuda")
+    loss, loss2 = torch.zeros((calls, 1), device="cuda"), torch.zeros((calls, 1), device="cuda")
+
+    def run(stream=None):
+        for i in range(calls):
+            plan.distill_topk(0, n, xt, V, ids, val, kl, ws, weight=w[i], loss=loss[i], stream=stream)
+            plan.token_logprob(0, n, xt, V, tok, w[i], logp, ws2, loss=loss2[i], stream=stream)
+
+    def check():
+        torch.cuda.synchronize()
+        # n / 1024 + 10 fp32 additions of a sum, and the roundings of a row's loss
+        for got, row in ((loss, kl.double()), (loss2, -logp.double())):
+            want = (w.double() * row).sum(1)
+            bound = (n / 1024 + 14) * 2.0 ** -24 * (w.double() * row.abs()).sum(1)
+            assert ((got[:, 0].double() - want).abs() <= bound + 1e-30).all()
+
+    run()
+    check()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run(side)
+    for s in (2.0, 0.5):
+        w.mul_(s)
+        xt.mul_(0.9)
+        graph.replay()
+        check()
+    plan.sync()
