@@ -515,11 +515,12 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         sc.f = !p.tail ? f * total : rest ? f * (qr * (total + pr) - pr) : 0.f;
         if (o.s != 0.f) sc.m = o.m, sc.l2 = lo * kLog2e;
         sc.usual = StageStat<T, false>::usual(sc.m, c2);
-        // hi = c2 m + l2 rounded; what it leaves out goes into the factor
-        const float a = sc.m * c2, ae = fmaf(sc.m, c2, -a);
-        sc.hi = a + sc.l2;
-        const float d = sc.hi - a;
-        if (sc.usual) sc.f *= ex2f(-(ae + ((a - (sc.hi - d)) + (sc.l2 - d))));
+        // hi = c2 m + l2 rounded; what it leaves out goes into the factor.  Each operation rounded
+        // by itself: a product fused into the difference after it would count its error twice.
+        const float a = __fmul_rn(sc.m, c2), ae = fmaf(sc.m, c2, -a);
+        sc.hi = __fadd_rn(a, sc.l2);
+        const float d = __fsub_rn(sc.hi, a);
+        if (sc.usual) sc.f *= ex2f(-(ae + (__fsub_rn(a, __fsub_rn(sc.hi, d)) + __fsub_rn(sc.l2, d))));
       }
       if (kGrad && lane == 0) {
         ss.scale[b] = sc;

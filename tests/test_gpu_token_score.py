@@ -954,3 +954,16 @@ def test_losses_of_calls_in_a_row(lib, n):
         graph.replay()
         check()
     plan.sync()
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("c", [1.0, 0.7])
+def test_distill_gradient_of_far_logits(lib, c, tail):
+    """Logits of 20,000 to 60,000: their exponents in base 2 are rounded by up to 2^-8, which the
+    gradient takes out again to the last bit; counted twice it would be 2e-3 of every entry."""
+    n, V, k = 40, 70, 4
+    rng = np.random.default_rng(11)
+    x = rng.normal(0, 2, (n, V)) + rng.uniform(20000, 60000, (n, 1))
+    ids = np.stack([rng.choice(V, k, replace=False) for _ in range(n)]).astype(np.int32)
+    val = (np.log(rng.dirichlet(np.ones(k + 1), n)[:, :k]) if tail else rng.normal(0, 2, (n, k))).astype(np.float32)
+    check_distill(decode_plan(lib, n), x, "f32", ids, val, None, c, tail)
