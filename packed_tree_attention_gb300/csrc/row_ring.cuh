@@ -234,8 +234,9 @@ struct StageStat {
     return fabsf(m) < 0x1p96f && c2 < 0x1p20f && c2 > 0x1p-80f;
   }
   __device__ __forceinline__ void raise(float mn, float c2) {
-    const float rn = mn * c2;
-    const float d = max_nan(usual(m, c2) ? r - rn : (m - mn) * c2, kCut);
+    // r is the rounded product: the difference of two of them, the new one not fused into it
+    const float rn = __fmul_rn(mn, c2);
+    const float d = max_nan(usual(m, c2) ? __fsub_rn(r, rn) : (m - mn) * c2, kCut);
     const float e = ex2f(d);
     const f2 f = pack2(e, e), dd = pack2(d, d);
 #pragma unroll

@@ -967,3 +967,14 @@ def test_distill_gradient_of_far_logits(lib, c, tail):
     ids = np.stack([rng.choice(V, k, replace=False) for _ in range(n)]).astype(np.int32)
     val = (np.log(rng.dirichlet(np.ones(k + 1), n)[:, :k]) if tail else rng.normal(0, 2, (n, k))).astype(np.float32)
     check_distill(decode_plan(lib, n), x, "f32", ids, val, None, c, tail)
+
+
+@pytest.mark.parametrize("c", [1.0, 0.7])
+@pytest.mark.parametrize("V,k", [(20001, 0), (20001, 9), (300007, 0)])
+def test_score_rising_far_logits(lib, V, k, c):
+    """Rows that rise to the end, far from zero: every thread's reference moves again and again,
+    by differences of rounded products."""
+    n = 24
+    rng = np.random.default_rng(V)
+    x = np.linspace(0, 200, V)[None] + rng.uniform(20000, 60000, (n, 1)) + rng.normal(0, 0.1, (n, V))
+    check_score(decode_plan(lib, n), np.arange(n), x, "f32", rng.integers(V - 100, V, n), k, c)
