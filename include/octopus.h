@@ -376,11 +376,12 @@ int octo_token_score_bwd(octo_plan_t plan, int32_t row0, int32_t n_rows, const v
  *   tail = 0: values are logits, up to a constant of the row; P_i = exp(c z_i) / sum_j exp(c z_j).
  *   tail = 1: values are log-probabilities (octo_token_score's top_logp); P_i = exp(z_i), and
  *             P_R = max(0, 1 - sum_i P_i) is one more class, the ids not listed.
- *     KL = sum_i P_i (ln P_i - ln q_i) + P_R (ln P_R - ln q_R),  q_R = sum of q outside the list,
- *     dlogits[r][v] = grad_scale w_r c (q_v P - sum over i with id_i = v of P_i
- *                     - [v not listed] P_R q_v / q_R),  P = sum_i P_i + P_R.
- * An id may be listed more than once: its entries add up.  The rest term is dropped where no
- * unlisted id has mass in the student: where ln q_v < -745 for all of them, less than 64 bits
+ *     T_v = sum over i with id_i = v of P_i: the entries of an id are one class,
+ *     KL = sum over listed v of T_v (ln T_v - ln q_v) + P_R (ln P_R - ln q_R),
+ *          q_R = sum of q outside the list,
+ *     dlogits[r][v] = grad_scale w_r c (q_v P - T_v - [v not listed] P_R q_v / q_R),
+ *          P = sum_i P_i + P_R.
+ * The rest term is dropped where no unlisted id has mass in the student: where ln q_v < -745 for all of them, less than 64 bits
  * hold, as for logits masked with -inf, the type's lowest value or another far one.  A row
  * whose weight is 0 (its logits are not read), whose student logits are all -inf, or, at
  * tail = 0, whose entries are all empty, has divergence 0 and a zero gradient. */

@@ -5,8 +5,9 @@ Definitions (x a row of logits, c = 1 / temperature, m = max x, S = sum_v exp(c 
     logp_v  = c (x_v - m) - ln S           entropy = - sum_v p_v logp_v, p_v = exp(logp_v)
     top k   = the k largest x, the lowest id first among equal ones; NaN never
     d logp_i / dx_v = c ([v = i] - p_v)    d entropy / dx_v = - c p_v (logp_v + entropy)
-    KL      = sum_i P_i (ln P_i - logp_{id i}) + P_R (ln P_R - ln q_R), q_R = sum of p outside the ids
-    dKL/dx_v = c (p_v P - sum over i with id_i = v of P_i - [v not listed] P_R p_v / q_R), P = sum_i P_i + P_R
+    KL      = sum over listed v of T_v (ln T_v - logp_v) + P_R (ln P_R - ln q_R), T_v = sum over i with
+              id_i = v of P_i (an id's entries are one class), q_R = sum of p outside the ids
+    dKL/dx_v = c (p_v P - T_v - [v not listed] P_R p_v / q_R), P = sum_i P_i + P_R
 A row with every logit at -inf: logp -inf, entropy 0, divergence 0, zero gradients."""
 from __future__ import annotations
 
@@ -75,6 +76,8 @@ def distill(x, t_ids, t_val, w=None, c=1.0, tail=False, grad_scale=1.0):
         at, z = t_ids[r][live], t_val[r][live].astype(np.float64)
         lnP = z if tail else log_softmax(z[None], c)[0][0]
         P = np.exp(lnP)
+        at, cls = np.unique(at, return_inverse=True)
+        P = np.bincount(cls, weights=P, minlength=len(at))
         rest = max(0.0, 1.0 - P.sum()) if tail else 0.0
         out = np.ones(V, dtype=bool)
         out[at] = False
@@ -82,9 +85,9 @@ def distill(x, t_ids, t_val, w=None, c=1.0, tail=False, grad_scale=1.0):
         if qR == 0:
             rest = 0.0
         with np.errstate(invalid="ignore"):
-            kl[r] = np.where(P > 0, P * (lnP - lp[r, at]), 0.0).sum()
+            kl[r] = np.where(P > 0, P * (np.log(np.where(P > 0, P, 1.0)) - lp[r, at]), 0.0).sum()
         d[r] = q[r] * (P.sum() + rest)
-        np.subtract.at(d[r], at, P)
+        d[r, at] -= P
         if rest > 0:
             kl[r] += rest * (np.log(rest) - np.log(qR))
             d[r][out] -= rest * q[r][out] / qR

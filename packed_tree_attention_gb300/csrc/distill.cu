@@ -5,10 +5,10 @@
 // (id_i, z_i), i < k, with id_i < 0 or z_i = -inf an empty one.
 //   renormalised: P_i = exp(c z_i) / sum_j exp(c z_j)
 //   with the rest: P_i = exp(z_i), P_R = max(0, 1 - sum_i P_i)
-//   KL = sum_i P_i (ln P_i - ln q_{id i}) + P_R (ln P_R - ln q_R),  q_R = sum of q outside
-//        the listed ids
-//   dKL/dx_v = c (q_v P - sum over i with id_i = v of P_i - [v not listed] P_R q_v / q_R),
-//        P = sum_i P_i + P_R
+//   T_v = sum over i with id_i = v of P_i
+//   KL = sum over listed v of T_v (ln T_v - ln q_v) + P_R (ln P_R - ln q_R),  q_R = sum of q
+//        outside the listed ids
+//   dKL/dx_v = c (q_v P - T_v - [v not listed] P_R q_v / q_R),  P = sum_i P_i + P_R
 // q_R is summed over the entries outside the list itself: 1 - sum_i q_i would lose it
 // where the list holds nearly all of the mass.  For that, the consumers leave out every
 // 16-byte vector that holds a listed id (a bit each in a table of the row's vectors), and a
@@ -532,11 +532,10 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
         fix[q] = 0.f;
         if (!has || id[q] < 0) continue;
         const float lq = fmaf(ws.x[q * 32 + lane] - all.m, p.c, -ls) - ls_lo;
-        if (p.tail) {   // an id's q goes to its first entry
-          const float d = lp[q] - lq;
-          kl += first >> q & 1 ? share(pe[q], d, expf(lq)) : pe[q] == 0.f ? 0.f : pe[q] * d - pe[q];
-        } else if (pe[q] != 0.f) {
-          kl += pe[q] * (lp[q] - lq);
+        if (first >> q & 1) {   // an id's entries are one class, its first one's
+          const float P = sub[q], d = (P == pe[q] ? lp[q] : logf(P)) - lq;
+          if (p.tail) kl += share(P, d, expf(lq));
+          else if (P != 0.f) kl += P * d;
         }
         if (kGrad) fix[q] = f * (expf(lq) * (total + pr) - sub[q]);
       }

@@ -978,3 +978,45 @@ def test_score_rising_far_logits(lib, V, k, c):
     rng = np.random.default_rng(V)
     x = np.linspace(0, 200, V)[None] + rng.uniform(20000, 60000, (n, 1)) + rng.normal(0, 0.1, (n, V))
     check_score(decode_plan(lib, n), np.arange(n), x, "f32", rng.integers(V - 100, V, n), k, c)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_distill_repeated_ids_are_one_class(lib, dtype, tail):
+    """A list with ids repeated equals the list with their probabilities added up by hand, and the
+    divergence from a student that has learnt it is 0."""
+    N, V, m, c = 40, 1203, 6, 0.8
+    plan = chain_plan(lib, N)
+    rng = np.random.default_rng(21)
+    x = rng.normal(0, 3, (N, V))
+    one = np.stack([rng.choice(V, m, replace=False) for _ in range(N)]).astype(np.int32)
+    parts = rng.dirichlet(np.ones(4 * m + 1), N)[:, :4 * m].reshape(N, m, 4)   # four shares of each id
+    parts[:, 0, 1:] = 0.0                              # an id listed once
+    parts[:, 1, 2] = 0.0                               # an entry that is empty
+    q = np.repeat(one, 4, 1)
+    with np.errstate(divide="ignore"):
+        val = np.log(parts).reshape(N, 4 * m) / (1.0 if tail else c)
+        whole = np.log(parts.sum(2)) / (1.0 if tail else c)
+    mix = np.stack([rng.permutation(4 * m) for _ in range(N)])
+    q, val = np.take_along_axis(q, mix, 1), np.take_along_axis(val, mix, 1).astype(np.float32)
+    x[0] = -200.0                                      # the student is the teacher
+    x[0, one[0]] = whole[0] / (c if tail else 1.0)
+    if tail:
+        rest = 1 - np.exp(whole[0]).sum()
+        x[0, np.setdiff1d(np.arange(V), one[0])] = np.log(rest / (V - m)) / c
+    xt, xr = rows_on_gpu(x, dtype)
+    kl, _, d = run_distill(plan, xt, V, q, val, None, c, tail, "sep")
+    kl1, _, d1 = run_distill(plan, xt, V, one, whole.astype(np.float32), None, c, tail, "sep")
+    plan.sync()
+    close(kl, kl1, "row_kl", scale=5.0)
+    close(d[:, :V], d1[:, :V], "dlogits", dtype == "bf16", scale=2.0)
+    assert (kl >= -5e-5).all() and (dtype == "bf16" or abs(kl[0]) < 5e-5)
+    # by the formula, without the reference
+    lp = xr * c - (xr * c).max(1, keepdims=True)
+    lp = lp - np.log(np.exp(lp).sum(1, keepdims=True))
+    P = parts.sum(2) if tail else parts.sum(2) / parts.sum((1, 2))[:, None]
+    want = (P * (np.log(P) - np.take_along_axis(lp, one, 1))).sum(1)
+    if tail:
+        R, qR = 1 - P.sum(1), 1 - np.exp(np.take_along_axis(lp, one, 1)).sum(1)
+        want = want + R * np.log(R / qR)
+    close(kl, want, "row_kl by the formula", scale=5.0)

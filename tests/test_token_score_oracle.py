@@ -135,3 +135,28 @@ def test_binding_takes_one_row_of_any_pitch(monkeypatch):
     for logits, grad in ((wide, narrow), (narrow, wide), (wide, one)):
         with pytest.raises(ValueError):
             both(logits, grad, 2)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+def test_repeated_ids_are_one_class(tail):
+    """A list with an id repeated is the list with its probabilities added up: a divergence of
+    distributions, 0 where the student is the teacher."""
+    x = np.log([[0.4, 0.3, 0.2, 0.1], [0.1, 0.1, 0.1, 0.7]])
+    ids, val = np.array([[0, 0, 1]] * 2), np.log([[0.15, 0.25, 0.3]] * 2)
+    kl, loss, d = ts.distill(x, ids, val, tail=tail)
+    one = ts.distill(x, np.array([[0, 1]] * 2), np.log([[0.4, 0.3]] * 2), tail=tail)
+    assert np.allclose(kl, one[0], atol=1e-14) and np.allclose(d, one[2], atol=1e-14) and abs(loss - one[1]) < 1e-14
+    if tail:                                            # P = (0.4, 0.3, rest 0.3) against the same and against (0.1, 0.1, 0.8)
+        assert abs(kl[0]) < 1e-14
+        assert abs(kl[1] - (0.4 * np.log(4) + 0.3 * np.log(3) + 0.3 * np.log(0.3 / 0.8))) < 1e-14
+    else:                                               # (4/7, 3/7) against shares 0.4 and 0.3 of the whole
+        assert abs(kl[0] - np.log(1 / 0.7)) < 1e-14
+    rng = np.random.default_rng(1)
+    ids = rng.integers(0, 4, (500, 9))
+    val = np.log(rng.dirichlet(np.ones(10), 500)[:, :9])
+    # by the log sum inequality at least T ln T, T the teacher's mass: 1, or what is listed where every
+    # id is, so that the rest drops out
+    T = np.exp(val).sum(1) if tail else np.ones(500)
+    T[[len(set(i)) < 4 for i in ids]] = 1.0
+    assert (T < 1).any() == tail
+    assert (ts.distill(rng.normal(0, 1, (500, 4)), ids, val, tail=tail)[0] >= T * np.log(T) - 1e-14).all()
