@@ -177,12 +177,20 @@ _T = {}   # torch's dtypes and calls, looked up once
 
 
 def _torch():
+    """Fills _T.  The device and stream come from the calls below torch.cuda.current_device and
+    current_stream, which take 3 us more of a call that has 10.  That there is no GPU is not
+    kept: the next call asks again."""
     import torch
     gpu = torch.cuda.is_available()
     _T.update(logits={torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}, float32=torch.float32, int32=torch.int32,
-              device=torch._C._cuda_getDevice if gpu else lambda: -2,
+              device=torch._C._cuda_getDevice if gpu else _no_device,
               stream=torch._C._cuda_getCurrentRawStream if gpu else lambda dev: None)
     return _T
+
+
+def _no_device():
+    import torch
+    return _torch()["device"]() if torch.cuda.is_available() else -2
 
 
 def _device():

@@ -160,3 +160,16 @@ def test_repeated_ids_are_one_class(tail):
     T[[len(set(i)) < 4 for i in ids]] = 1.0
     assert (T < 1).any() == tail
     assert (ts.distill(rng.normal(0, 1, (500, 4)), ids, val, tail=tail)[0] >= T * np.log(T) - 1e-14).all()
+
+
+def test_binding_asks_again_for_a_gpu(monkeypatch):
+    """A first call without a GPU says so and does not settle it."""
+    torch = pytest.importorskip("torch")
+    import packed_tree_attention_gb300 as pta
+    monkeypatch.setattr(pta, "_T", {})
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: False)
+    assert pta._device() == pta._device() == -2
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 40 + dev, raising=False)
+    assert pta._device() == 3 and pta._current(None, 3) == 43
