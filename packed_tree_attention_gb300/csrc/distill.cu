@@ -593,15 +593,24 @@ int launch_distill(DistillParams& p, cudaStream_t s) {
     // Two rows for each cluster wait in L2 for their second pass, and their gradients pass
     // through it: past three tenths of it they are read from memory again.  More CTAs a row
     // mean fewer rows in flight, at the price of joining the CTAs at every row, and want rows
-    // for several rounds.  4,000 rows, microseconds at 1 / 2 / 4 CTAs: of 128 KB
-    // 179 / 195 / 270, of 200 KB 294 / 257 / 351, of 304 KB 502 / 413 / 373; 2,000 of 608 KB
-    // 520 / 506 / 386.  A cluster's joins at a row cost more with the rest class, whose CTAs each
-    // clear and fill a bitmap: four tenths there (8,192 rows of 304 KB at 2 / 4 CTAs: 790 / 828
-    // us with it, 803 / 761 without it).
+    // for several rounds.  Microseconds at 1 / 2 / 4 CTAs, bf16 rows of 64 entries, 4,000 of
+    // them (3,000 from 350 KB on, 2,000 of 608 KB), without and with the rest class:
+    //   128 KB (29 % of L2 at 1 CTA)  176 / 198 / 287   174 / 210 / 343
+    //   160 KB (37 %)                 226 / 205 / 302   229 / 219 / 343
+    //   200 KB (46 %)                 293 / 253 / 358   299 / 262 / 383
+    //   250 KB (58 %)                 395 / 320 / 398   402 / 318 / 430
+    //   304 KB (70 %)                 501 / 407 / 382   512 / 401 / 430
+    //   350 KB (81 %)                 440 / 370 / 335   448 / 374 / 368
+    //   400 KB (92 %)                 504 / 440 / 370   513 / 446 / 394
+    //   608 KB (140 %)                520 / 501 / 380   531 / 510 / 387
+    // fp32 rows, with half the entries, like four CTAs earlier: 160 KB 226 / 209 / 261 and
+    // 228 / 208 / 280, 240 KB 366 / 312 / 364 and 376 / 309 / 379, 304 KB 493 / 415 / 366 and
+    // 500 / 411 / 375.  So a row gets two CTAs, and four, past three tenths, but bf16 rows with
+    // the rest class, whose CTAs each clear and fill a bitmap, get four past four tenths.
     const int sms = sm_count();
     auto in_flight = [&](int c) { return (int64_t)nv * 16 * 2 * (sms / c); };
-    const int64_t room = l2_bytes() / 100 * (p.tail ? 40 : 30);
-    while (cs < 4 && in_flight(cs) > room && (int64_t)p.n * 2 * cs > 5 * sms) cs *= 2;
+    auto room = [&](int c) { return l2_bytes() / 100 * (c == 2 && p.tail && Vec<T>::E == 8 ? 40 : 30); };
+    while (cs < 4 && in_flight(cs) > room(cs) && (int64_t)p.n * 2 * cs > 5 * sms) cs *= 2;
   }
   while (words(cs) * 4 * kMaxRows > 64 * 1024 && cs < kMaxCluster) cs *= 2;
   p.words = p.tail ? words(cs) : 0;
