@@ -396,7 +396,7 @@ int octo_distill_topk_workspace_size(int32_t n_rows, size_t* bytes);
  * (optional, one device float, needs ws, 4-byte aligned): sum of w_r KL_r over the chunk, in a
  * fixed order.
  * Teacher ids >= vocab count as empty and give OCTO_EINVAL at the next octo_sync.
- * OCTO_ENOTSUP at tail = 1 for vocabularies past some 2 million entries (fp32) or 4 (bf16).
+ * OCTO_ENOTSUP at tail = 1 for vocabularies past some 2.9 million entries (fp32) or 5.8 (bf16).
  * Deterministic.  Async on stream. */
 int octo_distill_topk(octo_plan_t plan, int32_t row0, int32_t n_rows, const void* logits, int32_t dtype,
                       int64_t ld, int32_t vocab, float inv_temp, int32_t k, const int32_t* teach_ids,

@@ -1020,3 +1020,19 @@ def test_distill_repeated_ids_are_one_class(lib, dtype, tail):
         R, qR = 1 - P.sum(1), 1 - np.exp(np.take_along_axis(lp, one, 1)).sum(1)
         want = want + R * np.log(R / qR)
     close(kl, want, "row_kl by the formula", scale=5.0)
+
+
+@pytest.mark.parametrize("dtype,fits,past", [("f32", 2900000, 2930000), ("bf16", 5800000, 5840000)])
+def test_distill_rest_up_to_the_largest_vocabulary(lib, dtype, fits, past):
+    """The rest class at the sizes that the header gives: the last that are taken, the first refused."""
+    rng = np.random.default_rng(14)
+    x = rng.normal(0, 3, (1, fits))
+    ids, val = teacher(rng, 1, fits, 40, True)
+    ids[0, :3] = [fits - 1, fits - 9, 0]
+    plan = decode_plan(lib, 1)
+    check_distill(plan, x, dtype, ids, val, None, 1.0, True)
+    big, kl = torch.zeros((1, past), dtype=DT[dtype], device="cuda"), torch.zeros(1, device="cuda")
+    with pytest.raises(lib.OctoError) as e:
+        plan.distill_topk(0, 1, big, past, gpu(ids, torch.int32), gpu(val), kl, tail=True)
+    assert e.value.code == lib.ENOTSUP
+    plan.sync()
