@@ -503,16 +503,19 @@ __global__ void __launch_bounds__(kBlock, 1) k_distill(const __grid_constant__ D
       if (has) {
         const float lo = logf(o.s);
         split_log(all.s, &ls, &ls_lo);
-        // o's sum is relative to its own largest entry, and 0 only where all are -inf
-        const bool rest = o.s != 0.f && !((o.m - all.m) * p.c - ls < kNoMass);
-        if (!rest) pr = 0.f;   // nothing outside the list has mass
-        // ln q_R: by the ratio of the sums, unless one's reference is too far below the other's
-        Stat far = o;
-        far.rebase(all.m, c2);
-        lqr = far.s > 1e-30f ? logf(far.s / all.s) : (o.m - all.m) * p.c + lo - ls - ls_lo;
-        if (rest) qr = expf(lqr);
         sc.live = 1;
-        sc.f = !p.tail ? f * total : rest ? f * (qr * (total + pr) - pr) : 0.f;
+        if (!p.tail) {
+          sc.f = f * total;
+        } else if (o.s == 0.f || (o.m - all.m) * p.c - ls < kNoMass) {
+          pr = 0.f;   // nothing outside the list has mass (o's sum is relative to its own largest entry)
+        } else {
+          // ln q_R: by the ratio of the sums, unless one's reference is too far below the other's
+          Stat far = o;
+          far.rebase(all.m, c2);
+          lqr = far.s > 1e-30f ? logf(far.s / all.s) : (o.m - all.m) * p.c + lo - ls - ls_lo;
+          qr = expf(lqr);
+          sc.f = f * (qr * (total + pr) - pr);
+        }
         if (o.s != 0.f) sc.m = o.m, sc.l2 = lo * kLog2e;
         sc.usual = StageStat<T, false>::usual(sc.m, c2);
         // hi = c2 m + l2 rounded; what it leaves out goes into the factor.  Each operation rounded
