@@ -20,9 +20,9 @@
 //
 // Bound by memory: V entries read and, for the gradient, V written; the second reading comes
 // from L2.  Measured (16,384-byte stages, one GB300, 6.78 TB/s copied): 8,192 rows of 151,936
-// bf16 against 64 entries 761 us with the gradient (6.55 TB/s of those bytes), 1,024 rows and 32
-// entries without it 56 us (5.6 TB/s), 500 rows of 50,001 fp32 with the rest class 39 us
-// (5.1 TB/s).  Parts held in shared memory between the passes, which spares L2 the second
+// bf16 against 64 entries 768 us with the gradient (6.5 TB/s of those bytes; 816 us with the rest
+// class), 1,024 rows and 32 entries without it 56 us (5.6 TB/s), 500 rows of 50,001 fp32 with the
+// rest class 40 us (5.0 TB/s).  Parts held in shared memory between the passes, which spares L2 the second
 // reading, took 876 us: they leave too little of the ring for the copies to run ahead.
 
 #include "row_ring.cuh"
