@@ -106,7 +106,7 @@ typedef struct {
   int32_t max_tile_entries;
   int32_t max_page_entries;
   int32_t n_touched_pages; /* pages some entry reads */
-  int32_t is_decode;
+  int32_t is_decode;       /* 0 pack plan, 1 decode plan, 2 chunk plan */
   int32_t n_rec_runs;      /* pack plans: runs of the recurrent layer (rows with one path predecessor chain) */
   int32_t n_rec_chunks;    /* pack plans: their chunks of up to 64 rows */
 } octo_plan_info_t;
@@ -526,6 +526,78 @@ int octo_decode_cursors(octo_pool_t pool, const octo_cursor_t* cursors, int32_t 
 #define OCTO_NOALLOC_SCRATCH_BYTES (32u << 20)
 int octo_decode_noalloc(octo_plan_t plan, int32_t n_q_heads, const void* q, const void* k_pool,
                         const void* v_pool, void* out, float* lse, float scale, void* stream);
+
+/* ---- chunks of new tokens over the paged cache ----
+ * Octopus project page, "Architecture & Co-Design" item 01 (Runtime): each turn extends a
+ * cursor over the shared pages it holds already; item 02: mounted spans are read in place.
+ * A turn brings more than one token when its prompt is read in (prefill, in parts) and when
+ * drafted tokens are checked (octo_verify_drafts): then several rows of each cursor attend to
+ * its context at once, and the context's K/V are read once for all of them. */
+
+/* Chunk plan: the last n_new[i] tokens of each cursor i (0 <= n_new[i] <= tokens of its
+ * segment; a cursor may be listed more than once), packed in cursor order; each row's context
+ * is the one octo_pack_tree gives it.  With window > 0 a row at position p sees of that only
+ * the keys at positions above p - window, and those at positions below n_sink, which stay
+ * visible from far (attention sinks); window = 0: everything (n_sink must be 0).  Single
+ * tokens under a window are chunks of one.  n_q_heads: query heads of the calls to come
+ * (OCTO_ENOTSUP past 128 a kv head).  The K/V of the new tokens must be in the pool arrays
+ * when the plan is used, not when it is built.  The plan holds as long as its pages do: later
+ * appends do not change it, a release of its segments ends it.  For chunk plans
+ * octo_plan_info counts cursors as n_segments, has no entries (max_tile_entries is the most
+ * blocks of up to 64 keys that a tile reads) and a tile's most tokens as bm; octo_plan_copy_out gives
+ * the cursors, their first rows, positions and tiles.  octo_rope_rows, octo_token_score and
+ * octo_distill_topk take them (row t leads to the token that follows it, as on a decode plan), the
+ * other calls on plans refuse them.  Synchronises `stream` once. */
+int octo_chunk_plan(octo_pool_t pool, const octo_cursor_t* cursors, const int32_t* n_new, int32_t n,
+                    int32_t n_q_heads, int32_t window, int32_t n_sink, void* stream, octo_plan_t* out);
+
+/* Workspace bytes octo_chunk_attn needs for this plan (0 on a bad plan). */
+size_t octo_chunk_attn_workspace_size(octo_plan_t plan);
+
+/* Attention of a chunk plan's rows: out = softmax(scale q k^T) v over what each row sees; kv
+ * head of query head h as in octo_attn_fwd.  q, out: [n_rows][n_q_heads][head_dim] of the pool
+ * dtype; lse: fp32 [n_rows][n_q_heads], natural log (may be NULL).  k_pool / v_pool NULL = the
+ * pool's arrays; every array 16-byte aligned.  ws: device workspace of the size above.  Long
+ * contexts of few rows are split among CTAs and joined in a fixed order: the same bits on
+ * every run.  Async on stream. */
+int octo_chunk_attn(octo_plan_t plan, const void* q, const void* k_pool, const void* v_pool, void* out,
+                    float* lse, float scale, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- verification of drafted tokens ----
+ * Speculative sampling over a chunk plan's rows: of each cursor, the first row holds the token
+ * agreed on last, the others (ids[r]) were drafted, row r from the draft's distribution
+ * q_{r-1}.  With p_r = softmax(inv_temp x[r]), x the target's logits:
+ *     a_r = min(1, p_{r-1}(ids r) / q_{r-1}(ids r)), 0 where p is 0;  accepted iff u[r] < a_r,
+ * up to the first rejected draft.  The token after the last accepted one is drawn from
+ *     max(0, p - q)   where a draft was rejected (p itself if that is 0 everywhere),
+ *     p               where all were accepted,
+ * of the last accepted row r as argmax_v w_v / noise[i][v] (lowest v first): for noise of
+ * independent Exp(1) variates that has the distribution w / sum w, and the emitted tokens have
+ * the target's own.  draft_logits NULL: the drafts are certain (q = 1 at the drafted token), the
+ * rejected one is left out.  u and noise NULL: greedy, a draft is accepted iff it is the
+ * largest logit's lowest id, which is the next token too (inv_temp then only enters next_logp;
+ * draft_logits must be NULL).  Masked logits are -inf.  A NaN in a row that is needed makes its draft
+ * rejected and is never drawn. */
+
+/* Workspace (bytes) for octo_verify_drafts over cursors [cur0, cur0 + n_cur). */
+int octo_verify_drafts_workspace_size(octo_plan_t plan, int32_t cur0, int32_t n_cur, size_t* bytes);
+
+/* Cursors [cur0, cur0 + n_cur) of a chunk plan built on the current device.  logits, dtype, ld,
+ * vocab as in octo_token_logprob, one row for each row of these cursors; draft_logits the
+ * same way with draft_ld and draft_inv_temp (row r: the distribution that row r + 1's token was drawn from; a
+ * cursor's last row is not read).  ids int32, u float: over ALL rows of the plan (a cursor's
+ * first ones are not read).  noise float [n_cur][noise_ld] > 0, 16-byte aligned, noise_ld a
+ * multiple of 4 and >= vocab.  Writes n_accept, next_id int32 [n_cur], next_logp float [n_cur]
+ * (optional: ln p of next_id), accept_p float over all rows of the plan (optional: a_r of the
+ * drafts up to and including the first rejected one, 0 in these cursors' other rows).  A cursor
+ * without rows has n_accept 0, next_id -1 and next_logp -inf, and so has one with no token
+ * left to draw, besides its accepted ones.  Ids outside [0, vocab) are rejected and give OCTO_EINVAL at the
+ * next octo_sync.  The same results on every run.  Async on stream. */
+int octo_verify_drafts(octo_plan_t plan, int32_t cur0, int32_t n_cur, const void* logits, int32_t dtype,
+                       int64_t ld, int32_t vocab, float inv_temp, const int32_t* ids,
+                       const void* draft_logits, int64_t draft_ld, float draft_inv_temp, const float* u,
+                       const float* noise, int64_t noise_ld, int32_t* n_accept, int32_t* next_id,
+                       float* next_logp, float* accept_p, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- diagnostics ---- */
 const char* octo_strerror(int status);

@@ -77,7 +77,8 @@ SYMBOLS = ("octo_pool_create", "octo_pool_destroy", "octo_root", "octo_append", 
            "octo_rope_pool_grad", "octo_token_logprob_workspace_size", "octo_token_logprob",
            "octo_decode_plan_advance", "octo_pool_query", "octo_decode_cursors", "octo_recurrent_workspace_size",
            "octo_recurrent_fwd", "octo_recurrent_bwd", "octo_wait_selftest", "octo_append_step", "octo_token_score",
-           "octo_token_score_bwd", "octo_distill_topk_workspace_size", "octo_distill_topk")
+           "octo_token_score_bwd", "octo_distill_topk_workspace_size", "octo_distill_topk", "octo_chunk_plan",
+           "octo_chunk_attn_workspace_size", "octo_chunk_attn", "octo_verify_drafts_workspace_size", "octo_verify_drafts")
 
 
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
@@ -137,6 +138,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "octo_recurrent_workspace_size": [P, I32, I32],
         "octo_wait_selftest": [P, ctypes.c_uint32, P],
         "octo_append_step": [P, IP, I32, P, P, F, P, IP],
+        "octo_chunk_plan": [P, IP, IP, I32, I32, I32, I32, P, ctypes.POINTER(P)],
+        "octo_chunk_attn_workspace_size": [P],
+        "octo_chunk_attn": [P, P, P, P, P, P, F, P, SZ, P],
+        "octo_verify_drafts_workspace_size": [P, I32, I32, ctypes.POINTER(SZ)],
+        "octo_verify_drafts": [P, I32, I32, P, I32, ctypes.c_int64, I32, F, P, P, ctypes.c_int64, F, P, P, ctypes.c_int64, P, P, P, P,
+                               P, SZ, P],
         "octo_recurrent_fwd": [P, I32, I32, P, P, P, P, P, P, P, SZ, P],
         "octo_recurrent_bwd": [P, I32, I32, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P],
     }
@@ -147,6 +154,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     L.octo_strerror.restype = ctypes.c_char_p
     L.octo_attn_bwd_workspace_size.restype = SZ
     L.octo_decode_workspace_size.restype = SZ
+    L.octo_chunk_attn_workspace_size.restype = SZ
     L.octo_recurrent_workspace_size.restype = SZ
     L.octo_launch_count.argtypes = []
     L.octo_launch_count.restype = ctypes.c_int64
@@ -183,6 +191,7 @@ def _torch():
     import torch
     gpu = torch.cuda.is_available()
     _T.update(logits={torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}, float32=torch.float32, int32=torch.int32,
+              pool={DTYPE_F32: "float32", DTYPE_BF16: "bfloat16"}, bfloat16=torch.bfloat16,
               device=torch._C._cuda_getDevice if gpu else _no_device,
               stream=torch._C._cuda_getCurrentRawStream if gpu else lambda dev: None)
     return _T
@@ -228,6 +237,17 @@ def _vector(x, name, count, dev, what):
     if x.get_device() != dev:
         raise _elsewhere(x, what)
     return x.data_ptr()
+
+
+def _workspace(ws, dev):
+    """(address, bytes) of a workspace tensor."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev:
+        raise _elsewhere(ws, "ws")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _current(s, dev):
@@ -407,6 +427,20 @@ class Pool:
         _chk(self._L.octo_decode_plan(self.h, _ip(c), len(c), _stream(stream), ctypes.byref(h)), "octo_decode_plan")
         return Plan(self, h)
 
+    def chunk_plan(self, cursors, n_new, n_q_heads, window=0, n_sink=0, stream=None):
+        """octo_chunk_plan: the last n_new[i] tokens of each cursor against their contexts, or
+        against their last `window` positions and the first n_sink."""
+        c = np.ascontiguousarray(cursors, dtype=np.int32)
+        m = np.ascontiguousarray(n_new, dtype=np.int32)
+        if c.ndim != 1 or c.shape != m.shape:
+            raise ValueError("cursors and n_new must be one-dimensional and of equal length")
+        h = ctypes.c_void_p()
+        _chk(self._L.octo_chunk_plan(self.h, _ip(c), _ip(m), len(c), n_q_heads, window, n_sink, _stream(stream),
+                                     ctypes.byref(h)), "octo_chunk_plan")
+        plan = Plan(self, h)
+        plan.n_q_heads, plan.cursor_rows = n_q_heads, m.copy()
+        return plan
+
 
 class Plan:
     """A compiled block-sparse schedule (octo_pack_tree / octo_decode_plan)."""
@@ -474,6 +508,53 @@ class Plan:
         cannot allocate device memory (its partials use the library's static scratch)."""
         _chk(self._L.octo_decode_noalloc(self.h, n_q_heads, _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(out),
                                          _ptr(lse), float(scale), _stream(stream)), "octo_decode_noalloc")
+
+    def chunk_attn_workspace_size(self):
+        return int(self._L.octo_chunk_attn_workspace_size(self.h))
+
+    def chunk_attn(self, q, out, lse, scale, ws=None, k_pool=None, v_pool=None, stream=None):
+        """octo_chunk_attn: attention of a chunk plan's rows over their contexts (lse may be None)."""
+        dev = _device()
+        p = self.pool
+        dt = _T["pool"][p.dtype]
+        n = self.info["n_rows"] * getattr(self, "n_q_heads", 0)
+        kv = p.num_pages * p.n_kv_heads * p.page_size * p.head_dim
+        _chk(self._L.octo_chunk_attn(
+            self.h, _vector(q, dt, n * p.head_dim, dev, "q"), _vector(k_pool, dt, kv, dev, "k_pool"),
+            _vector(v_pool, dt, kv, dev, "v_pool"), _vector(out, dt, n * p.head_dim, dev, "out"),
+            _vector(lse, "float32", n, dev, "lse"), scale, *_workspace(ws, dev), _current(stream, dev)), "octo_chunk_attn")
+
+    def verify_drafts_workspace_size(self, cur0, n_cur):
+        n = ctypes.c_size_t(0)
+        _chk(self._L.octo_verify_drafts_workspace_size(self.h, cur0, n_cur, ctypes.byref(n)),
+             "octo_verify_drafts_workspace_size")
+        return n.value
+
+    def verify_drafts(self, cur0, n_cur, logits, vocab, ids, n_accept, next_id, ws, u=None, noise=None, draft_logits=None,
+                      accept_p=None, next_logp=None, inv_temp=1.0, draft_inv_temp=1.0, stream=None):
+        """octo_verify_drafts: how many drafted tokens of the cursors [cur0, cur0 + n_cur) of a chunk
+        plan the target accepts, and each one's next token; sampled with u over the plan's rows and
+        noise [n_cur][ld] of Exp(1) variates, greedy without them."""
+        dev = _device()
+        rows = getattr(self, "cursor_rows", ())
+        n = int(rows[cur0:cur0 + n_cur].sum()) if 0 <= cur0 and n_cur >= 0 and cur0 + n_cur <= len(rows) else 0
+        x, dt, ld = _logits(logits, n, vocab, dev)
+        y, yld = None, ld
+        if draft_logits is not None:
+            y, ydt, yld = _logits(draft_logits, n, vocab, dev, "draft_logits")
+            if ydt != dt:
+                raise ValueError("draft_logits must have the dtype of logits")
+        e, eld = None, 0
+        if noise is not None:
+            e, edt, eld = _logits(noise, n_cur, vocab, dev, "noise")
+            if edt != DTYPE_F32:
+                raise ValueError("noise must be float32")
+        N = self.info["n_rows"]
+        _chk(self._L.octo_verify_drafts(
+            self.h, cur0, n_cur, x, dt, ld, vocab, inv_temp, _vector(ids, "int32", N, dev, "ids"), y, yld, draft_inv_temp,
+            _vector(u, "float32", N, dev, "u"), e, eld, _vector(n_accept, "int32", n_cur, dev, "n_accept"),
+            _vector(next_id, "int32", n_cur, dev, "next_id"), _vector(next_logp, "float32", n_cur, dev, "next_logp"),
+            _vector(accept_p, "float32", N, dev, "accept_p"), *_workspace(ws, dev), _current(stream, dev)), "octo_verify_drafts")
 
     def rope_rows(self, n_heads, x, base, inverse=False, stream=None):
         """octo_rope_rows: rotate the plan's packed rows of x (bf16 or fp32) in place."""
@@ -564,18 +645,11 @@ class Plan:
         if len(shape) != 2 or shape != teach_val.shape:
             raise ValueError("teach_ids and teach_val must both be [n_rows][k]")
         N, k = self.info["n_rows"], shape[1]
-        ws_bytes = 0
-        if ws is not None:
-            ws_bytes = ws.numel() * ws.element_size()
-            if ws.get_device() != dev:
-                raise _elsewhere(ws, "ws")
-            if not ws.is_contiguous():
-                raise ValueError("ws must be contiguous")
         _chk(self._L.octo_distill_topk(
             self.h, row0, n_rows, x, dt, ld, vocab, inv_temp, k, _vector(teach_ids, "int32", n_rows * k, dev, "teach_ids"),
             _vector(teach_val, "float32", n_rows * k, dev, "teach_val"), 1 if tail else 0,
             _vector(weight, "float32", N, dev, "weight"), _vector(row_kl, "float32", N, dev, "row_kl"), g, grad_scale,
-            _vector(loss, "float32", 1, dev, "loss"), _ptr(ws), ws_bytes,
+            _vector(loss, "float32", 1, dev, "loss"), *_workspace(ws, dev),
             _current(stream, dev)), "octo_distill_topk")
 
     def recurrent_workspace_size(self, n_heads, head_dim):

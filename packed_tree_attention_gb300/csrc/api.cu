@@ -123,7 +123,7 @@ size_t octo_decode_workspace_size(octo_plan_t plan, int32_t Hq) {
 
 int octo_decode(octo_plan_t plan, int32_t Hq, const void* q, const void* k_pool, const void* v_pool, void* out,
                 float* lse, float scale, void* ws, size_t ws_bytes, void* stream) {
-  if (!plan || !plan->info.is_decode) return OCTO_EINVAL;
+  if (!plan || plan->info.is_decode != 1) return OCTO_EINVAL;
   if (int st = check_heads(plan, Hq)) return st;
   if (plan->info.n_rows > 0 && (!q || !out)) return OCTO_EINVAL;
   if (ws_bytes < octo_decode_workspace_size(plan, Hq)) return OCTO_EINVAL;

@@ -1,0 +1,91 @@
+// Chunk plans: what octo_chunk_plan lays out and the chunk attention kernels read.
+#pragma once
+
+#include <vector>
+
+#include "internal.h"
+
+namespace octo {
+
+// Keys of one segment's tokens [c W, c W + W), W the plan's block width, at the positions and
+// visibility that these 32 bytes give.  Slot j is token c W + j.  The row with own index i at
+// position p sees it iff
+//     lo <= j < hi  &&  own0 + j <= i  &&  kpos + j > p - window.
+// own0 is kFarOwn where every row of the tiles that list the block sees it (an ancestor's or a
+// mounted token); kpos is kSinkPos where the tokens are sinks.  A run of tokens whose positions
+// jump, and one that the sinks end in, makes two blocks.
+struct ChunkBlock {
+  int32_t page[4];   // pages of slots [0, s), [s, 2 s) ..., s = min(page_size, W)
+  int32_t own0, kpos;
+  uint16_t lo, hi;
+  int32_t slot0;     // slot 0's place in its page (page 128: 0 or 64)
+};
+
+constexpr int32_t kFarOwn = -(1 << 30);
+constexpr int32_t kSinkPos = 1 << 30;
+constexpr int32_t kMaxPos = 1 << 29;   // positions of a chunk plan: their differences and the above fit 32 bits
+
+// Rows [row0, row0 + rows) of the plan: tokens of one cursor from own index t0 on, at positions
+// own index + shift, no mount among them; the blocks that some of them sees.
+struct ChunkTile {
+  int32_t row0, rows, t0, shift;
+  int32_t blk0, n_blk;
+  int32_t pad[2];
+};
+
+// Work of one CTA (and kv head): blocks [b0, b1) of a tile.  part < 0: all of the tile's, the
+// result is written; else partial results from row `part` on (rows * G of each kv head).
+struct ChunkItem {
+  int32_t tile, b0, b1;
+  int32_t part;
+};
+
+// A tile whose items are joined: n_parts of them, the first one's rows from `part` on.
+struct ChunkJoin {
+  int32_t tile, part, n_parts, pad;
+};
+
+struct ChunkPlan {
+  int32_t Hq = 0, G = 0, width = 0;   // width: keys per block
+  int32_t tokens = 0;                 // tokens of 128 rows (of G heads each); a tile has up to twice as many
+  int32_t window = 0;                 // 0: none
+  bool tc = false;                    // tcgen05 kernels
+  int32_t n_items = 0, n_joins = 0;
+  int32_t max_rows = 0;               // rows of the longest tile
+  int32_t max_join_rows = 0;          // and of the longest joined one
+  int64_t part_rows = 0;              // rows of all partial results (of one kv head)
+  ChunkBlock* blocks = nullptr;       // device arrays, the plan's
+  ChunkTile* tiles = nullptr;
+  ChunkItem* items = nullptr;         // largest first
+  ChunkJoin* joins = nullptr;
+  std::vector<int32_t> row0;          // [cursors + 1] first row of each (host)
+};
+
+struct ChunkArgs {
+  const void *q, *k, *v;
+  void* out;
+  float* lse;        // may be NULL
+  float scale;
+  float* part;       // partial results: [row][kv head of it] -> chunk_part()
+  float* part_ml;
+};
+
+int chunk_simt(const octo_plan_s* p, const ChunkArgs& a, cudaStream_t s);
+int chunk_join(const octo_plan_s* p, const ChunkArgs& a, cudaStream_t s);
+
+#ifdef __CUDACC__
+// Row rr (token of the tile * G + head) of kv head g of a partial result of R rows that starts
+// at row `part`: index among all partial rows.
+__device__ __forceinline__ int64_t chunk_part(int32_t part, int32_t Hkv, int32_t g, int32_t R, int32_t rr) {
+  return (int64_t)part * Hkv + (int64_t)g * R + rr;
+}
+// Slots [lo, hi) of a block that the row at own index i sees; w0: its first visible position
+// (INT32_MIN: no window).
+__device__ __forceinline__ void chunk_range(const ChunkBlock& b, int32_t i, int32_t w0, bool windowed, int& lo, int& hi) {
+  lo = b.lo;
+  if (windowed) lo = max(lo, w0 - b.kpos);
+  hi = min((int)b.hi, i - b.own0 + 1);
+}
+#endif
+
+}  // namespace octo

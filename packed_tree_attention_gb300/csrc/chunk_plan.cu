@@ -1,0 +1,389 @@
+// Chunk plans, and the entry points of the chunk attention.
+//
+// Octopus project page, "Architecture & Co-Design" item 01 (Runtime): a turn extends a cursor
+// over the pages it shares; item 02: mounted spans are read in place.  A chunk plan is to
+// several new tokens of a cursor what a decode plan is to one.  It lists, per cursor, the
+// context in blocks of 64 keys, once for all of the cursor's tiles (without a window a tile's
+// blocks are a prefix of them; under one, each tile lists the few that it sees), and cuts the
+// tiles' block lists into items of about equal length.  It is built on the host: a step's plan
+// serves every layer of a model, and its size is that of the contexts' page lists.
+
+#include <algorithm>
+#include <cstring>
+#include <memory>
+#include <new>
+#include <queue>
+
+#include "chunk.h"
+#include "row_ring.cuh"
+
+namespace octo {
+namespace {
+
+// Keys per block: 64 where pages make up 64 keys or are made up of them, so that a block is 64
+// rows of a tensor-core tile; else a page.
+int32_t block_width(int32_t P) { return (P % 64 == 0 || (P >= 16 && 64 % P == 0)) ? 64 : P; }
+
+struct Builder {
+  const octo_pool_s* pool;
+  int32_t P, W, n_sink;
+  std::vector<ChunkBlock> out;
+
+  // tokens [a, b) of segment s; own: they are the cursor's own
+  void span(int32_t s, int32_t a, int32_t b, bool own) {
+    const Segment& g = pool->segs[s];
+    for (int32_t c = a / W * W; c < b; c += W) {
+      const int32_t end = std::min(b, c + W);
+      for (int32_t t = std::max(a, c); t < end;) {
+        // the run from t on: positions rise by one, sinks or not
+        const bool sink = g.pos[t] < n_sink;
+        int32_t e = end;
+        if (g.pos[end - 1] - g.pos[t] != end - 1 - t || (sink && g.pos[end - 1] >= n_sink))
+          for (e = t + 1; e < end && g.pos[e] == g.pos[e - 1] + 1 && (g.pos[e] < n_sink) == sink;) e++;
+        ChunkBlock k;
+        const int32_t p0 = c / P;
+        for (int i = 0; i < 4; i++) k.page[i] = g.pages[std::min<size_t>(p0 + i, g.pages.size() - 1)];
+        k.slot0 = c % P;
+        k.own0 = own ? c : kFarOwn;
+        k.kpos = sink ? kSinkPos : g.pos[t] - (t - c);
+        k.lo = (uint16_t)(t - c);
+        k.hi = (uint16_t)(e - c);
+        out.push_back(k);
+        t = e;
+      }
+    }
+  }
+
+  // What a child of segment s sees of it: its first tokens, and the mounts it held by then.
+  void ancestor(int32_t s, const Segment& child) {
+    for (int32_t id : pool->segs[s].mounts) {
+      const MountRec& m = pool->mounts[id];
+      if (m.m <= child.fork && m.created < child.created) span(m.producer, m.a, m.b, false);
+    }
+    span(s, 0, child.fork, false);
+  }
+};
+
+// Visible (row, key) pairs of a tile's block.
+int64_t block_pairs(const ChunkBlock& k, const ChunkTile& t, int32_t window) {
+  const int32_t last = t.t0 + t.rows - 1;
+  auto lo = [&](int32_t i) { return window ? std::max<int32_t>(k.lo, i + t.shift - window + 1 - k.kpos) : (int32_t)k.lo; };
+  auto hi = [&](int32_t i) { return std::min<int32_t>(k.hi, i - k.own0 + 1); };
+  if (hi(t.t0) == k.hi && lo(last) == k.lo) return (int64_t)t.rows * (k.hi - k.lo);
+  int64_t n = 0;
+  for (int32_t i = t.t0; i <= last; i++) n += std::max(0, hi(i) - lo(i));
+  return n;
+}
+
+// Time of the longest-loaded of `sms` workers that take items of these lengths in turn.
+int64_t makespan(const std::vector<int32_t>& lens, int heads, int sms) {
+  std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> q;
+  for (int i = 0; i < sms; i++) q.push(0);
+  int64_t end = 0;
+  for (int32_t n : lens)
+    for (int h = 0; h < heads; h++) {
+      const int64_t t = q.top() + n;
+      q.pop();
+      q.push(t);
+      end = std::max(end, t);
+    }
+  return end;
+}
+
+// Blocks per item, an item costing its blocks and kItemCost more (its start, its query tile, its
+// epilogue), and a plan with joined tiles kJoinCost: the length with the shortest makespan among
+// those that fill the SMs 1, 2, ... times.
+constexpr int kItemCost = 5, kJoinCost = 4;
+int32_t pick_length(const std::vector<ChunkTile>& tiles, int heads, int sms) {
+  int32_t most = 1;
+  int64_t total = 0;
+  for (const ChunkTile& t : tiles) most = std::max(most, t.n_blk), total += t.n_blk;
+  int32_t best = most;
+  int64_t best_t = INT64_MAX;
+  std::vector<int32_t> lens;
+  auto pieces = [&](int32_t len) {
+    int64_t n = 0;
+    for (const ChunkTile& t : tiles) n += (t.n_blk + len - 1) / len;
+    return n;
+  };
+  auto consider = [&](int32_t len) {
+    lens.clear();
+    bool join = false;
+    for (const ChunkTile& t : tiles) {
+      const int32_t k = (t.n_blk + len - 1) / len;
+      join |= k > 1;
+      for (int32_t i = 0; i < k; i++) lens.push_back((t.n_blk - i + k - 1) / k + kItemCost);
+    }
+    std::sort(lens.begin(), lens.end(), std::greater<int32_t>());
+    const int64_t t = makespan(lens, heads, sms) + (join ? kJoinCost : 0);
+    if (t < best_t) best_t = t, best = len;
+  };
+  if ((int64_t)tiles.size() * heads > 24LL * sms) return most;   // many waves: nothing to gain
+  consider(most);
+  for (int w = 1; w <= 6; w++) {
+    // the shortest items of which w waves are enough
+    int32_t lo = 1, hi = most;
+    while (lo < hi) {
+      const int32_t mid = lo + (hi - lo) / 2;
+      if (pieces(mid) * heads <= (int64_t)w * sms) hi = mid;
+      else lo = mid + 1;
+    }
+    if (pieces(lo) * heads <= (int64_t)w * sms) consider(lo);
+  }
+  return best;
+}
+
+template <typename T>
+size_t place(size_t* at, const std::vector<T>& v) {
+  const size_t o = *at;
+  *at = align_up(o + v.size() * sizeof(T), 256);
+  return o;
+}
+
+// the pool's device status word, made on first use
+int ensure_status(octo_pool_s* pool) {
+  if (!pool->d_status) {
+    OCTO_CUDA(cudaMalloc(&pool->d_status, sizeof(int32_t) * 4));
+    OCTO_CUDA(cudaMemset(pool->d_status, 0, sizeof(int32_t) * 4));
+  }
+  return OCTO_OK;
+}
+
+int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new, int32_t n, int32_t Hq,
+          int32_t window, int32_t n_sink, cudaStream_t s, octo_plan_t* out) {
+  const octo_pool_desc& d = pool->desc;
+  std::unique_ptr<octo_plan_s> pl(new octo_plan_s());
+  std::unique_ptr<ChunkPlan> cp(new ChunkPlan());
+  cp->Hq = Hq;
+  cp->G = Hq / d.n_kv_heads;
+  cp->width = block_width(d.page_size);
+  cp->tokens = std::max(1, 128 / cp->G);
+  cp->row0.resize((size_t)n + 1, 0);
+  int64_t rows = 0;
+  int32_t top = 0;   // the largest position of a row
+  for (int32_t i = 0; i < n; i++) {
+    rows += n_new[i];
+    if (rows > INT32_MAX / 2) return OCTO_EINVAL;
+    cp->row0[i + 1] = (int32_t)rows;
+    if (n_new[i]) top = std::max(top, pool->segs[cursors[i]].pos.back());
+  }
+  if (top >= kMaxPos) return OCTO_ENOTSUP;
+  cp->window = window > top ? 0 : window;   // sees everything
+
+  Builder b{pool, d.page_size, cp->width, cp->window ? n_sink : 0, {}};
+  std::vector<ChunkBlock> blocks;
+  std::vector<ChunkTile> tiles;
+  std::vector<int32_t> row_pos((size_t)rows), chain;
+  int64_t pairs = 0;
+  for (int32_t c = 0; c < n; c++) {
+    if (!n_new[c]) continue;
+    const Segment& g = pool->segs[cursors[c]];
+    const int32_t first = g.len - n_new[c];
+    std::copy(g.pos.begin() + first, g.pos.end(), row_pos.begin() + cp->row0[c]);
+    // the cursor's context, in the order in which its rows come to see it
+    b.out.clear();
+    chain.clear();
+    for (int32_t x = cursors[c]; x >= 0; x = pool->segs[x].parent) chain.push_back(x);
+    for (size_t l = chain.size(); l-- > 1;) b.ancestor(chain[l], pool->segs[chain[l - 1]]);
+    // how many of the blocks a row sees (from which of its segment's tokens on)
+    const size_t far = b.out.size();
+    std::vector<int32_t> from(far, 0);
+    int32_t next = 0;
+    std::vector<int32_t> cut;
+    for (int32_t id : g.mounts) {
+      const MountRec& m = pool->mounts[id];
+      if (m.m > g.len - 1) continue;
+      // own blocks are cut at a mount, as their positions mostly are: what comes to be seen later
+      // is then listed later
+      if (m.m > next) {
+        b.span(cursors[c], next, m.m, true);
+        next = m.m;
+      }
+      while (from.size() < b.out.size()) from.push_back(b.out[from.size()].own0 + b.out[from.size()].lo);
+      b.span(m.producer, m.a, m.b, false);
+      from.resize(b.out.size(), m.m);
+      if (m.m > first) cut.push_back(m.m);
+    }
+    if (next < g.len) b.span(cursors[c], next, g.len, true);
+    while (from.size() < b.out.size()) from.push_back(b.out[from.size()].own0 + b.out[from.size()].lo);
+    cut.push_back(g.len);
+    const int32_t base = (int32_t)blocks.size();
+    if (!cp->window) blocks.insert(blocks.end(), b.out.begin(), b.out.end());
+    // tiles: pieces without a mount inside
+    size_t seen = 0;
+    for (int32_t t = first, k = 0; t < g.len;) {
+      while (cut[k] <= t) k++;
+      ChunkTile tile = {};
+      tile.row0 = cp->row0[c] + t - first;
+      tile.t0 = t;
+      tile.rows = std::min(2 * cp->tokens, cut[k] - t);
+      tile.shift = g.pos[t] - t;
+      const int32_t last = t + tile.rows - 1;
+      while (seen < b.out.size() && from[seen] <= last) seen++;
+      if (cp->window) {
+        tile.blk0 = (int32_t)blocks.size();
+        for (size_t i = 0; i < seen; i++) {
+          const ChunkBlock& x = b.out[i];
+          if (x.kpos + x.hi - 1 > g.pos[t] - cp->window) blocks.push_back(x);
+        }
+        tile.n_blk = (int32_t)blocks.size() - tile.blk0;
+      } else {
+        tile.blk0 = base;
+        tile.n_blk = (int32_t)seen;
+      }
+      for (int32_t i = 0; i < tile.n_blk; i++) pairs += block_pairs(blocks[tile.blk0 + i], tile, cp->window);
+      tiles.push_back(tile);
+      t += tile.rows;
+    }
+    if (blocks.size() > (size_t)INT32_MAX / 2) return OCTO_EINVAL;
+  }
+
+  // items
+  const int sms = std::max(1, rows::sm_count());
+  const int32_t len = pick_length(tiles, d.n_kv_heads, sms);
+  std::vector<ChunkItem> items;
+  std::vector<ChunkJoin> joins;
+  int32_t longest = 0;
+  for (int32_t i = 0; i < (int32_t)tiles.size(); i++) {
+    const ChunkTile& t = tiles[i];
+    longest = std::max(longest, t.n_blk);
+    cp->max_rows = std::max(cp->max_rows, t.rows);
+    const int32_t k = std::max(1, (t.n_blk + len - 1) / len);
+    if (k > 1) {
+      joins.push_back({i, (int32_t)cp->part_rows, k, 0});
+      cp->max_join_rows = std::max(cp->max_join_rows, t.rows);
+    }
+    for (int32_t j = 0, at = 0; j < k; j++) {
+      const int32_t e = at + (t.n_blk - at) / (k - j);
+      items.push_back({i, at, e, k > 1 ? (int32_t)cp->part_rows : -1});
+      at = e;
+      if (k > 1) cp->part_rows += (int64_t)t.rows * cp->G;
+      if (cp->part_rows > INT32_MAX) return OCTO_EINVAL;
+    }
+  }
+  std::stable_sort(items.begin(), items.end(), [](const ChunkItem& x, const ChunkItem& y) { return x.b1 - x.b0 > y.b1 - y.b0; });
+  cp->n_items = (int32_t)items.size();
+  cp->n_joins = (int32_t)joins.size();
+
+  // what octo_plan_copy_out gives of a chunk plan: its cursors, rows, positions and tiles
+  std::vector<int32_t> order(cursors, cursors + n), t_seg, t_t0, t_rows, none(std::max((size_t)d.num_pages, tiles.size()) + 1, 0);
+  for (int32_t c = 0, i = 0; i < (int32_t)tiles.size(); i++) {
+    while (tiles[i].row0 >= cp->row0[c + 1]) c++;
+    t_seg.push_back(cursors[c]), t_t0.push_back(tiles[i].t0), t_rows.push_back(tiles[i].rows);
+  }
+
+  // device arrays: one allocation, one copy
+  size_t at = 0;
+  const size_t o_blk = place(&at, blocks), o_tile = place(&at, tiles), o_item = place(&at, items), o_join = place(&at, joins),
+               o_pos = place(&at, row_pos), o_row0 = place(&at, cp->row0),
+               o_order = place(&at, order), o_seg = place(&at, t_seg), o_t0 = place(&at, t_t0), o_rows = place(&at, t_rows),
+               o_none = place(&at, none);
+  std::vector<char> stage(std::max<size_t>(at, 256));
+  auto put = [&](size_t o, const auto& v) {
+    if (!v.empty()) std::memcpy(stage.data() + o, v.data(), v.size() * sizeof(v[0]));
+  };
+  put(o_blk, blocks), put(o_tile, tiles), put(o_item, items), put(o_join, joins), put(o_pos, row_pos), put(o_row0, cp->row0);
+  put(o_order, order), put(o_seg, t_seg), put(o_t0, t_t0), put(o_rows, t_rows), put(o_none, none);
+  if (int st = ensure_status(pool)) return st;
+  OCTO_CUDA(cudaGetDevice(&pl->device));
+  pl->pool = pool;
+  pl->last_stream = s;
+  pl->num_pages = d.num_pages;
+  void* buf = nullptr;
+  OCTO_CUDA(cudaMallocAsync(&buf, stage.size(), s));
+  pl->allocs.push_back(buf);
+  char* base = static_cast<char*>(buf);
+  cp->blocks = reinterpret_cast<ChunkBlock*>(base + o_blk);
+  cp->tiles = reinterpret_cast<ChunkTile*>(base + o_tile);
+  cp->items = reinterpret_cast<ChunkItem*>(base + o_item);
+  cp->joins = reinterpret_cast<ChunkJoin*>(base + o_join);
+  pl->row_pos = reinterpret_cast<int32_t*>(base + o_pos);
+  pl->seg_row_base = reinterpret_cast<int32_t*>(base + o_row0);
+  pl->seg_order = reinterpret_cast<int32_t*>(base + o_order);
+  pl->tile_seg = reinterpret_cast<int32_t*>(base + o_seg);
+  pl->tile_t0 = reinterpret_cast<int32_t*>(base + o_t0);
+  pl->tile_rows = reinterpret_cast<int32_t*>(base + o_rows);
+  pl->tile_off = pl->page_off = reinterpret_cast<int32_t*>(base + o_none);   // no entries
+  std::memset(&pl->info, 0, sizeof(pl->info));
+  pl->info.n_rows = rows;
+  pl->info.n_tiles = (int64_t)tiles.size();
+  pl->info.n_segments = n;
+  pl->info.pairs = pairs;
+  pl->info.bm = 2 * cp->tokens;
+  pl->info.page_size = d.page_size;
+  pl->info.max_tile_entries = longest;
+  pl->info.is_decode = 2;
+  pl->max_succ = 1;
+  pl->chunk = std::move(cp);
+  int st = cuda_status(cudaMemcpyAsync(buf, stage.data(), stage.size(), cudaMemcpyHostToDevice, s));
+  if (st == OCTO_OK) st = cuda_status(cudaStreamSynchronize(s));   // the staging buffer goes, other streams may use the plan
+  if (st != OCTO_OK) {
+    octo_plan_destroy(pl.release());
+    return st;
+  }
+  *out = pl.release();
+  return OCTO_OK;
+}
+
+size_t part_floats(const octo_plan_s* p) {
+  return (size_t)p->chunk->part_rows * p->pool->desc.n_kv_heads * p->pool->desc.head_dim;
+}
+
+}  // namespace
+}  // namespace octo
+
+extern "C" {
+
+int octo_chunk_plan(octo_pool_t pool, const octo_cursor_t* cursors, const int32_t* n_new, int32_t n, int32_t Hq,
+                    int32_t window, int32_t n_sink, void* stream, octo_plan_t* out) {
+  octo::NvtxRange nv("octo_chunk_plan");
+  if (!pool || !out || n < 0 || (n > 0 && (!cursors || !n_new))) return OCTO_EINVAL;
+  if (Hq <= 0 || Hq % pool->desc.n_kv_heads || Hq > 65535) return OCTO_EINVAL;
+  if (window < 0 || n_sink < 0 || (!window && n_sink)) return OCTO_EINVAL;
+  if (Hq / pool->desc.n_kv_heads > 128) return OCTO_ENOTSUP;
+  for (int32_t i = 0; i < n; i++) {
+    const int32_t c = cursors[i];
+    if (c < 0 || c >= (int32_t)pool->segs.size() || pool->segs[c].freed) return OCTO_EINVAL;
+    if (n_new[i] < 0 || n_new[i] > pool->segs[c].len) return OCTO_EINVAL;
+  }
+  try {
+    return octo::build(pool, cursors, n_new, n, Hq, window, n_sink, (cudaStream_t)stream, out);
+  } catch (const std::bad_alloc&) {
+    return OCTO_ENOMEM;
+  }
+}
+
+size_t octo_chunk_attn_workspace_size(octo_plan_t plan) {
+  if (!plan || !plan->chunk) return 0;
+  const size_t rows = (size_t)plan->chunk->part_rows * plan->pool->desc.n_kv_heads;
+  return rows ? octo::align_up(octo::part_floats(plan) * sizeof(float), 256) + rows * 2 * sizeof(float) : 0;
+}
+
+int octo_chunk_attn(octo_plan_t plan, const void* q, const void* k_pool, const void* v_pool, void* out, float* lse,
+                    float scale, void* ws, size_t ws_bytes, void* stream) {
+  octo::NvtxRange nv("octo_chunk_attn");
+  if (!plan || !plan->chunk) return OCTO_EINVAL;
+  int dev = 0;
+  OCTO_CUDA(cudaGetDevice(&dev));
+  if (dev != plan->device) return OCTO_EINVAL;
+  if (plan->info.n_rows == 0) return OCTO_OK;
+  octo::ChunkArgs a;
+  a.q = q;
+  a.k = k_pool ? k_pool : plan->pool->desc.k_pool;
+  a.v = v_pool ? v_pool : plan->pool->desc.v_pool;
+  a.out = out;
+  a.lse = lse;
+  a.scale = scale;
+  if (!q || !out || !a.k || !a.v) return OCTO_EINVAL;
+  if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)lse) & 15) return OCTO_EINVAL;
+  const size_t need = octo_chunk_attn_workspace_size(plan);
+  if (need && (!ws || ws_bytes < need || ((uintptr_t)ws & 15))) return OCTO_EINVAL;
+  a.part = static_cast<float*>(ws);
+  a.part_ml = need ? reinterpret_cast<float*>(static_cast<char*>(ws) + octo::align_up(octo::part_floats(plan) * sizeof(float), 256)) : nullptr;
+  cudaStream_t s = (cudaStream_t)stream;
+  plan->last_stream = s;
+  if (int st = octo::chunk_simt(plan, a, s)) return st;
+  return plan->chunk->n_joins ? octo::chunk_join(plan, a, s) : OCTO_OK;
+}
+
+}  // extern "C"

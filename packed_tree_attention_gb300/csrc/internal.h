@@ -5,6 +5,7 @@
 #include <nvtx3/nvToolsExt.h>
 #include <stdint.h>
 
+#include <memory>
 #include <set>
 #include <vector>
 
@@ -55,6 +56,8 @@ struct PairItem {
   int16_t causal;         // bit h: half h is causal
   int32_t diag[2];        // causal: row r sees slot j iff j <= r + diag
 };
+
+struct ChunkPlan;   // chunk.h
 
 }  // namespace octo
 
@@ -145,6 +148,7 @@ struct octo_plan_s {
   cudaEvent_t order_ev = nullptr;    // orders an advance after work on another stream
   cudaStream_t last_stream = nullptr;  // stream of the last call that used the plan
   int device = 0;                    // that the plan's arrays are on
+  std::shared_ptr<octo::ChunkPlan> chunk;   // chunk plans: their own arrays; row_pos and seg_row_base ([cursors + 1]) besides
 };
 
 namespace octo {

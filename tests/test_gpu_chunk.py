@@ -1,0 +1,326 @@
+"""GPU parity of octo_chunk_attn (whole contexts, sliding windows with sinks) against the oracle's
+row contexts and a softmax in fp64, and a speculative step of the chunk calls together.
+
+Tolerances, with A = sum p |v| of the row in fp64.  fp32: scores are inner products of at most 128
+terms and exponents of at most ~40 (2^-24 each, relative), sums of at most some thousand positive
+terms: below 2^-16 of A together, 2^-15 allowed.  bf16: besides, the probabilities are rounded before the product with V
+(2^-8 of A) and the output once (2^-8 of it).  lse: an exponent's error, 2^-16 (1 + |lse|)."""
+import math
+
+import numpy as np
+import pytest
+
+import synth
+from helpers import pool_pages_needed, replay_device
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import packed_tree_attention_gb300 as pta
+    pta.load()
+    return pta
+
+
+class Case:
+    """An episode in the library's pool and in the oracle, and the rows of a chunk plan."""
+
+    def __init__(self, lib, oracle_mod, ep, G, Hkv, d, dtype, seed=0, scale=1.0):
+        self.lib, self.ep, self.G, self.Hkv, self.d, self.dtype = lib, ep, G, Hkv, d, dtype
+        t = synth.make_tensors(ep, G * Hkv, Hkv, d, dtype, scale, seed, with_do=False)
+        self.t, P = t, ep.page_size
+        npages = pool_pages_needed(ep)
+        self.kp = torch.zeros((npages, Hkv, P, d), dtype=DT[dtype], device="cuda")
+        self.vp = torch.zeros_like(self.kp)
+        self.pool = lib.Pool(npages, P, Hkv, d, lib.DTYPE_BF16 if dtype == "bf16" else lib.DTYPE_F32, self.kp, self.vp)
+        replay_device(self.pool, ep, torch.from_numpy(t.K).cuda().to(DT[dtype]), torch.from_numpy(t.V).cuda().to(DT[dtype]))
+        self.orc = oracle_mod.Oracle(P, npages, Hkv, d)
+        self.orc.replay(ep, t.K.astype(np.float64), t.V.astype(np.float64))
+        self.K, self.V = t.K.astype(np.float64), t.V.astype(np.float64)
+        self.plan = self.orc.pack(ep.roots, 32)
+        self.base = {int(s): int(b) for s, b in zip(self.plan.seg_order, self.plan.seg_row_base)}
+        seg, idx = self.orc.token_owner()
+        pos = {s: self.orc.seg_pos(s) for s in range(ep.n_segments)}
+        self.tok_pos = np.array([pos[s][i] for s, i in zip(seg, idx)])
+
+    def queries(self, cursors, n_new, seed):
+        n = int(sum(n_new))
+        q = np.random.default_rng(seed).standard_normal((n, self.G * self.Hkv, self.d)).astype(np.float32)
+        return torch.from_numpy(q).cuda().to(DT[self.dtype])
+
+    def reference(self, cursors, n_new, q, scale, window, sink):
+        """out, lse and sum p |v| in fp64."""
+        q = q.float().cpu().numpy().astype(np.float64)
+        o, a, lse = np.zeros_like(q), np.zeros_like(q), np.zeros(q.shape[:2])
+        r = 0
+        for c, n in zip(cursors, n_new):
+            for i in range(self.ep.length[c] - n, self.ep.length[c]):
+                row = self.base[c] + i
+                tok, _ = self.plan.row_context(row)
+                if window:
+                    p = self.tok_pos[tok]
+                    tok = tok[(p > self.plan.row_pos[row] - window) | (p < sink)]
+                for h in range(self.G * self.Hkv):
+                    g = h // self.G
+                    s = scale * (self.K[tok, g] @ q[r, h])
+                    lse[r, h] = np.logaddexp.reduce(s)
+                    p = np.exp(s - lse[r, h])
+                    o[r, h], a[r, h] = p @ self.V[tok, g], p @ np.abs(self.V[tok, g])
+                r += 1
+        return o, lse, a
+
+    def run(self, plan, q, scale, **kw):
+        out = torch.full_like(q, float("nan"))
+        lse = torch.full(q.shape[:2], float("nan"), device="cuda")
+        ws = torch.full((max(1, plan.chunk_attn_workspace_size()),), 255, dtype=torch.uint8, device="cuda")
+        plan.chunk_attn(q, out, lse, scale, ws, **kw)
+        plan.sync()
+        return out, lse
+
+    def check(self, cursors, n_new, window=0, sink=0, seed=1):
+        scale = 1 / math.sqrt(self.d)
+        q = self.queries(cursors, n_new, seed)
+        plan = self.pool.chunk_plan(cursors, n_new, self.G * self.Hkv, window=window, n_sink=sink)
+        assert plan.info["n_rows"] == sum(n_new) and plan.info["n_segments"] == len(cursors) and plan.info["is_decode"] == 2
+        out, lse = self.run(plan, q, scale)
+        o, L, a = self.reference(cursors, n_new, q, scale, window, sink)
+        close(out, lse, o, L, a, self.dtype)
+        return plan, q, out, lse
+
+
+def close(out, lse, o, L, a, dtype):
+    out, lse = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    tol = 2.0 ** -15 * a + 1e-7
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (a + np.abs(o))
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    assert np.all(np.abs(out - o) <= tol), "out: %g over" % (np.abs(out - o) - tol).max()
+    assert np.all(np.abs(lse - L) <= 2.0 ** -16 * (1 + np.abs(L))), "lse: %g" % np.abs(lse - L).max()
+
+
+def live(case):
+    return [s for s in range(case.ep.n_segments) if case.ep.length[s] > 0 and not case.orc.seg_info(s)["flags"] & 16]
+
+
+SHAPES = [  # group, kv heads, head_dim, page, type
+    (4, 4, 128, 64, "bf16"), (1, 2, 128, 64, "bf16"), (8, 1, 64, 32, "bf16"), (3, 2, 128, 16, "bf16"), (5, 1, 64, 128, "bf16"),
+    (2, 2, 64, 24, "bf16"), (3, 2, 64, 16, "f32"), (4, 1, 128, 64, "f32"), (1, 1, 64, 128, "f32"), (2, 1, 128, 48, "f32"),
+    (16, 1, 64, 8, "f32"),
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("window,sink", [(0, 0), (1, 0), (37, 0), (90, 70), (64, 5), (100000, 3)])
+def test_random_trees(lib, oracle_mod, shape, window, sink):
+    G, Hkv, d, P, dtype = shape
+    seed = 100 * SHAPES.index(shape) + window % 97
+    ep = synth.random_dag(seed, page_size=P, max_segments=12, max_len=220, n_roots=2)
+    c = Case(lib, oracle_mod, ep, G, Hkv, d, dtype, seed)
+    rng = np.random.default_rng(seed)
+    cur = live(c)
+    n_new = [int(rng.integers(0, min(ep.length[s], 150) + 1)) for s in cur]
+    n_new[0] = ep.length[cur[0]]
+    c.check(cur, n_new, window, sink, seed)
+
+
+def chain(P, *lens):
+    ep = synth.Episode(P)
+    c = ep.root()
+    for n in lens[:-1]:
+        ep.append(c, n)
+        c = ep.fork(c, 1)[0]
+    ep.append(c, lens[-1])
+    return ep, c
+
+
+@pytest.mark.parametrize("dtype,P", [("bf16", 64), ("f32", 16)])
+@pytest.mark.parametrize("n", [1, 2, 5, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200])
+def test_chunk_lengths(lib, oracle_mod, dtype, P, n):
+    """Around the ends of tiles, query groups and blocks; the first token of a root alone."""
+    ep, c = chain(P, n)
+    Case(lib, oracle_mod, ep, 4, 2, 128, dtype).check([c], [n])
+    ep, c = chain(P, 130, n)
+    Case(lib, oracle_mod, ep, 4, 2, 128, dtype).check([c], [n], window=70, sink=3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_context_is_split_and_joined(lib, oracle_mod, dtype):
+    ep, c = chain(64, 5000, 1100, 7)
+    case = Case(lib, oracle_mod, ep, 4, 1, 128, dtype)
+    plan, q, out, lse = case.check([c], [7])
+    assert plan.chunk_attn_workspace_size() > 0
+    again, lse2 = case.run(plan, q, 1 / math.sqrt(128))      # a workspace of other content: the same bits
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_mounts_inside_a_chunk(lib, oracle_mod, dtype):
+    """Spans mounted between the chunk's own rows, also twice in one block, one at a longer position."""
+    ep = synth.Episode(64)
+    r = ep.root()
+    ep.append(r, 50)
+    a, b, e = ep.fork(r, 3)
+    ep.append(a, 300)
+    ep.append(e, 90)
+    ep.append(b, 10)
+    ep.mount(b, a, 3, 70)
+    ep.append(b, 7)
+    ep.mount(b, e, 0, 90)
+    ep.append(b, 100)
+    case = Case(lib, oracle_mod, ep, 4, 2, 128, dtype)
+    for n in (117, 110, 107, 101, 100, 1):
+        case.check([b], [n])
+        case.check([b], [n], window=80, sink=20)
+        case.check([b], [n], window=12)
+
+
+def test_same_cursor_twice_and_empty_plans(lib, oracle_mod):
+    ep, c = chain(64, 100, 40)
+    case = Case(lib, oracle_mod, ep, 2, 2, 128, "bf16")
+    case.check([c, c, 0], [40, 3, 100])
+    for cur, n_new in (([], []), ([c], [0])):
+        plan = case.pool.chunk_plan(cur, n_new, 4)
+        assert plan.info["n_rows"] == 0 and plan.chunk_attn_workspace_size() == 0
+        q = torch.zeros((0, 4, 128), dtype=torch.bfloat16, device="cuda")
+        plan.chunk_attn(q, q.clone(), None, 1.0)
+        plan.sync()
+
+
+def test_large_scores_and_hidden_values(lib, oracle_mod):
+    """Scores of some hundred, a row's maximum moving from block to block; slots that no row may see hold the type's largest values."""
+    ep, c = chain(64, 700, 30)
+    case = Case(lib, oracle_mod, ep, 4, 1, 128, "bf16")
+    case.kp[:, :, :, :] *= 8
+    case.K *= 8
+    pages = case.pool.seg_pages(c)
+    case.kp[pages[-1], :, 30:] = 3e38
+    case.vp[pages[-1], :, 30:] = 3e38
+    scale = 1 / math.sqrt(128)
+    q = case.queries([c], [30], 5) * 4
+    plan = case.pool.chunk_plan([c], [30], 4)
+    out, lse = case.run(plan, q, scale)
+    o, L, a = case.reference([c], [30], q, scale, 0, 0)
+    out, lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    # an exponent of size E = |s| + max |s| carries 2^-24 E per rounding, some eight of them
+    s = np.abs(L).max()
+    rel = 2.0 ** -20 * s + 2.0 ** -8
+    assert np.all(np.abs(out - o) <= rel * (a + np.abs(o)) + 1e-6) and np.all(np.abs(lse - L) <= 2.0 ** -20 * s + 1e-5)
+
+
+def test_other_stream_other_arrays_and_capture(lib, oracle_mod):
+    """A plan used on another stream than it was built on, with arrays of another layer, and from a graph replayed on new queries;
+    rows behind the plan's stay as they are."""
+    ep, c = chain(64, 900, 12)
+    case = Case(lib, oracle_mod, ep, 4, 2, 128, "bf16")
+    scale = 1 / math.sqrt(128)
+    plan = case.pool.chunk_plan([c], [12], 8)
+    q = case.queries([c], [12], 3)
+    want, lse_want = case.run(plan, q, scale)
+    kp, vp = case.kp.clone(), case.vp.clone()
+    case.kp.zero_()
+    ws = torch.empty(plan.chunk_attn_workspace_size(), dtype=torch.uint8, device="cuda")
+    out, lse = torch.full((14, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((14, 8), 7.0, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plan.chunk_attn(q, out, lse, scale, ws, k_pool=kp, v_pool=vp, stream=side)
+    side.synchronize()
+    assert torch.equal(out[:12], want) and torch.equal(lse[:12], lse_want) and (out[12:] == 7).all() and (lse[12:] == 7).all()
+    static = q.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan.chunk_attn(static, out, lse, scale, ws, k_pool=kp, v_pool=vp)
+    q2 = case.queries([c], [12], 4)
+    static.copy_(q2)
+    g.replay()
+    torch.cuda.synchronize()
+    first = out[:12].clone()
+    plan.chunk_attn(q2, out, lse, scale, ws, k_pool=kp, v_pool=vp)
+    plan.sync()
+    assert torch.equal(first, out[:12]) and not torch.equal(first, want)
+
+
+def test_refusals(lib, oracle_mod):
+    ep, c = chain(64, 300, 12)
+    case = Case(lib, oracle_mod, ep, 2, 2, 128, "bf16")
+    plan = case.pool.chunk_plan([c], [12], 4)
+    q = case.queries([c], [12], 3)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    need = plan.chunk_attn_workspace_size()
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+    for bad in (None, ws[:need - 1].contiguous(), ws[1:]):
+        with pytest.raises(lib.OctoError):
+            plan.chunk_attn(q, out, lse, 1.0, bad)
+    with pytest.raises(ValueError):
+        plan.chunk_attn(q.float(), out, lse, 1.0, ws)
+    with pytest.raises(ValueError):
+        plan.chunk_attn(q[:11], out, lse, 1.0, ws)
+    with pytest.raises(ValueError):
+        plan.chunk_attn(q.transpose(0, 1), out, lse, 1.0, ws)
+    with pytest.raises(ValueError):
+        plan.chunk_attn(q, out, lse.half(), 1.0, ws)
+    with pytest.raises(ValueError):
+        plan.chunk_attn(q.cpu(), out, lse, 1.0, ws)
+    with pytest.raises(ValueError):
+        plan.chunk_attn(q, out, lse, 1.0, ws, k_pool=case.kp[:1])
+    shifted = torch.empty(q.numel() + 1, dtype=q.dtype, device="cuda")[1:].view(q.shape)
+    with pytest.raises(lib.OctoError):
+        plan.chunk_attn(shifted, out, lse, 1.0, ws)
+    # other plans and calls
+    pack, dec = case.pool.pack_tree(ep.roots, 128), case.pool.decode_plan([c])
+    assert pack.chunk_attn_workspace_size() == dec.chunk_attn_workspace_size() == 0
+    for other in (pack, dec):
+        with pytest.raises(lib.OctoError):
+            other.chunk_attn(q, out, lse, 1.0, ws)
+        with pytest.raises(lib.OctoError):
+            other.verify_drafts_workspace_size(0, 1)
+    lse_t = torch.empty((4, 12), device="cuda")
+    for call in (lambda: plan.attn_fwd(4, q, out, lse_t, 1.0), lambda: plan.decode(4, q, out, lse, 1.0, ws),
+                 lambda: plan.decode_noalloc(4, q, out, lse, 1.0), lambda: plan.advance(),
+                 lambda: plan.rope_pool_grad(case.kp.float(), 1e4),
+                 lambda: plan.recurrent_fwd(1, 128, *[torch.zeros(12 * 128, device="cuda")] * 6, ws)):
+        with pytest.raises(lib.OctoError):
+            call()
+    got = plan.copy_out()
+    assert got["seg_order"].tolist() == [c] and got["seg_row_base"].tolist() == [0] and len(got["entries"]) == 0
+    assert np.array_equal(got["row_pos"], case.pool.seg_pos(c)) and got["tile_seg"].tolist() == [c] and got["tile_rows"].tolist() == [12]
+    assert plan.recurrent_workspace_size(1, 128) == 0
+    plan.sync()
+
+
+def test_one_chunk_is_its_tokens_one_by_one(lib):
+    """The rows of a chunk against octo_decode of the same tokens, each the newest of its cursor; rotary positions too."""
+    Hq, Hkv, d, P, n = 8, 2, 128, 64, 9
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    kp = torch.zeros((40, Hkv, P, d), dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    pool = lib.Pool(40, P, Hkv, d, lib.DTYPE_BF16, kp, vp)
+    root = pool.root()
+    pool.append_rope(root, 500, rnd(500, Hkv, d), rnd(500, Hkv, d), 1e4)
+    a, b = pool.fork(root, 2)
+    pool.append_rope(a, 77, rnd(77, Hkv, d), rnd(77, Hkv, d), 1e4)
+    pool.mount(b, a, 5, 70)
+    k, v, q = rnd(n, Hkv, d), rnd(n, Hkv, d), rnd(n, Hq, d)
+    scale = 1 / math.sqrt(d)
+    one = torch.empty_like(q)
+    for t in range(n):
+        pool.append_rope(b, 1, k[t:t + 1], v[t:t + 1], 1e4)
+        plan = pool.decode_plan([b])
+        qt, o = q[t:t + 1].clone(), one[t:t + 1]
+        plan.rope_rows(Hq, qt, 1e4)
+        ws = torch.empty(plan.decode_workspace_size(Hq), dtype=torch.uint8, device="cuda")
+        plan.decode(Hq, qt, o, None, scale, ws)
+        plan.sync()
+    plan = pool.chunk_plan([b], [n], Hq)
+    q_rot, out = q.clone(), torch.empty_like(q)
+    plan.rope_rows(Hq, q_rot, 1e4)
+    ws = torch.empty(max(1, plan.chunk_attn_workspace_size()), dtype=torch.uint8, device="cuda")
+    plan.chunk_attn(q_rot, out, None, scale, ws)
+    plan.sync()
+    # both round P to at most bf16 and the output once: 2^-8 (|o| + A) each, A < 1 for means of randn
+    assert torch.all((out.float() - one.float()).abs() <= 2.0 ** -7 * (one.float().abs() + 1))

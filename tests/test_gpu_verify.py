@@ -1,0 +1,280 @@
+"""GPU parity of octo_verify_drafts against the fp64 reference in oracle/verify.py.
+
+Ids and counts are equal: the inputs' draws and thresholds are random reals, a decision that 1e-5 of a
+probability's relative error could turn is told apart beforehand and not compared.  accept_p and
+next_logp: exponents of at most ~60 with two fp32 roundings, 1e-5 (1 + |ref|)."""
+import numpy as np
+import pytest
+
+from oracle import verify as ov
+from oracle.token_score import log_softmax
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import packed_tree_attention_gb300 as pta
+    pta.load()
+    return pta
+
+
+def chunk_plan(lib, rows, before=0):
+    pool = lib.Pool(sum(-(-max(r, 1) // 16) for r in rows) + 1, 16, 1, 64, lib.DTYPE_BF16)
+    cur = [pool.root() for _ in rows]
+    for c, r in zip(cur, rows):
+        pool.append(c, max(r, 1))
+    return pool.chunk_plan(cur, rows, 1)
+
+
+def on_gpu(x, dtype, pad=8):
+    ld = -(-x.shape[1] // 8) * 8 + pad
+    full = np.full((x.shape[0], ld), np.nan, dtype=np.float32)
+    full[:, :x.shape[1]] = x
+    t = torch.from_numpy(full).to(DT[dtype]).cuda()
+    return t, t[:, :x.shape[1]].float().cpu().numpy().astype(np.float64)
+
+
+def run(plan, rows, V, x, ids, y=None, u=None, noise=None, c=1.0, cq=1.0, cur0=0, n_cur=None):
+    n_cur = len(rows) if n_cur is None else n_cur
+    i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+    N = plan.info["n_rows"]
+    acc, nxt = (torch.full((n_cur,), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+    logp, ap = torch.full((n_cur,), -7.0, device="cuda"), torch.full((N,), -7.0, device="cuda")
+    ws = torch.full((max(1, plan.verify_drafts_workspace_size(cur0, n_cur)),), 255, dtype=torch.uint8, device="cuda")
+    plan.verify_drafts(cur0, n_cur, x, V, i32(ids), acc, nxt, ws, u=None if u is None else torch.tensor(u, dtype=torch.float32, device="cuda"),
+                       noise=noise, draft_logits=y, accept_p=ap, next_logp=logp, inv_temp=c, draft_inv_temp=cq)
+    return [a.cpu().numpy() for a in (acc, nxt, logp, ap)]
+
+
+def close(got, ref, what):
+    ref, got = np.asarray(ref, dtype=np.float64), np.asarray(got, dtype=np.float64)
+    fin = np.isfinite(ref)
+    assert np.array_equal(got[~fin], ref[~fin]), what
+    assert np.all(np.abs(got[fin] - ref[fin]) <= 1e-5 * (1 + np.abs(ref[fin]))), "%s: %g" % (what, np.abs(got[fin] - ref[fin]).max())
+
+
+def inputs(rng, rows, V, masked, draft, near=1.0):
+    n = sum(rows)
+    x = rng.standard_normal((n, V)) * 3
+    if masked:
+        x[rng.random((n, V)) < masked] = -np.inf
+    y = x + near * rng.standard_normal((n, V)) if draft else None
+    ids = np.zeros(n, dtype=np.int32)
+    for r in range(n - 1):
+        row = np.where(np.isfinite(y[r] if draft else x[r]), y[r] if draft else x[r], -1e9)
+        ids[r + 1] = np.argmax(row - np.log(rng.exponential(size=V))) if draft or rng.random() < 0.3 else np.argmax(row)
+    return x, y, ids, rng.random(n).astype(np.float32), rng.exponential(size=(len(rows), V)).astype(np.float32)
+
+
+def clear(x, rows, ids, y, u, noise, c, cq):
+    """Cursors whose decisions 1e-5 of relative error does not turn: no u within that of a_r, and the same winner when each weight's
+    share of p and q moves by as much."""
+    acc, nxt, _, ap = ov.verify(x, rows, ids, y, u, noise, c, cq)
+    keep, r0 = [], 0
+    lp = log_softmax(x, c)[0]
+    lq = None if y is None else log_softmax(y, cq)[0]
+    for i, n in enumerate(rows):
+        ok = all(ap[r] == 0 or abs(u[r] - ap[r]) > 1e-5 * ap[r] for r in range(r0 + 1, min(r0 + n, r0 + 2 + acc[i])))
+        if n and nxt[i] >= 0:
+            r = r0 + acc[i]
+            p = np.exp(lp[r])
+            w = p.copy()
+            if acc[i] + 1 < n:
+                if lq is not None:
+                    w = np.maximum(p - np.exp(lq[r]), 0)
+                elif 0 <= ids[r + 1] < len(w):
+                    w[ids[r + 1]] = 0
+                if not w.max() > 0:
+                    w = p
+            err = 1e-5 * (p + (np.exp(lq[r]) if lq is not None else 0))
+            hi = (w + err) / noise[i]
+            hi[nxt[i]] = 0
+            ok &= bool(hi.max() < (w[nxt[i]] - err[nxt[i]]) / noise[i, nxt[i]])
+        keep.append(ok)
+        r0 += n
+    return np.array(keep)
+
+
+def check(lib, rows, V, dtype, masked=0.0, draft=True, c=1.0, cq=1.0, seed=0, near=1.0):
+    rng = np.random.default_rng(seed)
+    x, y, ids, u, noise = inputs(rng, rows, V, masked, draft, near)
+    xt, xr = on_gpu(x, dtype)
+    yt, yr = (None, None) if y is None else on_gpu(y, dtype, 16)
+    nt, nr = on_gpu(noise, "f32", 4 if V % 8 else 8)
+    plan = chunk_plan(lib, rows)
+    got = run(plan, rows, V, xt, ids, yt, u, nt, c, cq)
+    plan.sync()
+    ref = ov.verify(xr, rows, ids, yr, u, nr, c, cq)
+    keep = clear(xr, rows, ids, yr, u, nr, c, cq)
+    assert keep.mean() > 0.9
+    assert np.array_equal(got[0][keep], ref[0][keep]) and np.array_equal(got[1][keep], ref[1][keep])
+    close(got[2][keep], ref[2][keep], "next_logp")
+    rk = np.repeat(keep, rows)
+    close(got[3][rk], ref[3][rk], "accept_p")
+    again = run(plan, rows, V, xt, ids, yt, u, nt, c, cq)
+    assert all(np.array_equal(a, b) for a, b in zip(got, again))
+    return ref
+
+
+ROWS = [1, 5, 0, 2, 9, 1, 17, 3, 0, 4]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 31, 257, 1000, 4099, 50001])
+@pytest.mark.parametrize("draft", [True, False])
+def test_sampled(lib, dtype, V, draft):
+    check(lib, ROWS, V, dtype, draft=draft, c=1.25, cq=0.8, seed=V)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_vocabulary_of_the_benchmarks(lib, dtype):
+    ref = check(lib, [5, 3, 1, 4], 151936, dtype, seed=3)
+    assert ref[0].max() > 0
+
+
+@pytest.mark.parametrize("draft", [True, False])
+def test_masked(lib, draft):
+    check(lib, ROWS, 999, "bf16", masked=0.95, draft=draft, seed=4)
+
+
+def test_many_cursors(lib):
+    check(lib, [4] * 400, 300, "bf16", seed=5)
+    check(lib, [1] * 700, 64, "f32", seed=6)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_greedy(lib, dtype):
+    rng = np.random.default_rng(7)
+    for V in (1, 3, 33, 5000, 151936):
+        rows = ROWS if V < 10000 else [5, 2]
+        x, _, ids, _, _ = inputs(rng, rows, V, 0.3 if V > 3 else 0, False)
+        x = np.round(x)                                  # ties: the lowest id
+        x[min(3, len(x) - 1)] = -np.inf
+        xt, xr = on_gpu(x, dtype)
+        for r in range(1, len(ids)):
+            if rng.random() < 0.8:
+                ids[r] = np.argmax(xr[r - 1])
+        plan = chunk_plan(lib, rows)
+        got = run(plan, rows, V, xt, ids, c=0.7)
+        plan.sync()
+        ref = ov.verify(xr, rows, ids, c=0.7)
+        assert np.array_equal(got[0], ref[0]) and np.array_equal(got[1], ref[1]) and np.array_equal(got[3], ref[3])
+        close(got[2], ref[2], "next_logp")
+
+
+def test_certain_and_impossible_drafts(lib):
+    """Equal distributions are always accepted; a draft that the target cannot say never is; one that the draft could not say is
+    taken where the target can; certain targets leave nothing but themselves; a target without tokens draws none."""
+    V, inf = 40, float("inf")
+    rng = np.random.default_rng(8)
+    x = rng.standard_normal((12, V))
+    y = x.copy()
+    x[3, 5] = -inf                     # impossible for the target
+    y[5, 6] = -inf                     # impossible for the draft, not for the target
+    x[7], y[7] = -inf, -inf
+    x[7, 9] = y[7, 9] = 0.0            # certain
+    x[9] = -inf                        # no token left
+    rows = [3, 2, 2, 2, 3]
+    ids = np.array([0, 1, 2, 0, 5, 0, 6, 0, 9, 0, 4, 4])
+    u = np.full(12, 0.999999, dtype=np.float32)
+    noise = rng.exponential(size=(5, V)).astype(np.float32)
+    xt, xr = on_gpu(x, "f32")
+    yt, yr = on_gpu(y, "f32")
+    nt, nr = on_gpu(noise, "f32")
+    plan = chunk_plan(lib, rows)
+    acc, nxt, logp, ap = run(plan, rows, V, xt, ids, yt, u, nt)
+    plan.sync()
+    ref = ov.verify(xr, rows, ids, yr, u, nr)
+    assert acc.tolist() == [2, 0, 1, 1, 0] == ref[0].tolist()
+    assert nxt.tolist() == ref[1].tolist() and nxt[4] == -1 and nxt[1] != 5
+    close(logp, ref[2], "next_logp")
+    close(ap, ref[3], "accept_p")
+    # drafts of certain distributions, the target certain of another token and of the same one
+    acc, nxt, logp, ap = run(chunk_plan(lib, [2, 2]), [2, 2], V, xt[[7, 0, 7, 0]], [0, 3, 0, 9], None, u[:4], nt[:2].contiguous())
+    assert acc.tolist() == [0, 1] and nxt[0] == 9 and ap.tolist() == [0, 0, 0, 1]
+
+
+def test_nan_and_ids_out_of_range(lib):
+    V, rows = 64, [3, 3, 2]
+    rng = np.random.default_rng(9)
+    x, y, ids, u, noise = inputs(rng, rows, V, 0, True)
+    u[:] = 0
+    ids[1], ids[4] = V, -3
+    x[6, 3] = np.nan
+    xt, xr = on_gpu(x, "f32")
+    yt, yr = on_gpu(y, "f32")
+    nt, nr = on_gpu(noise, "f32")
+    plan = chunk_plan(lib, rows)
+    acc, nxt, logp, ap = run(plan, rows, V, xt, ids, yt, u, nt)
+    with pytest.raises(lib.OctoError):
+        plan.sync()
+    assert acc.tolist() == [0, 0, 0] and nxt[2] == -1 and logp[2] == -np.inf
+    ref = ov.verify(xr[:6], rows[:2], ids, yr[:6], u, nr[:2])
+    assert nxt[:2].tolist() == ref[1].tolist() and ap[:6].tolist() == ref[3].tolist()
+
+
+def test_some_of_the_cursors(lib):
+    """A range of the plan's cursors: their logits, the plan's ids and u; other rows of accept_p stay."""
+    rng = np.random.default_rng(10)
+    rows, V = [4, 3, 5, 2], 500
+    x, y, ids, u, noise = inputs(rng, rows, V, 0, True)
+    xt, xr = on_gpu(x, "bf16")
+    yt, yr = on_gpu(y, "bf16")
+    nt, nr = on_gpu(noise, "f32")
+    plan = chunk_plan(lib, rows)
+    whole = run(plan, rows, V, xt, ids, yt, u, nt)
+    part = run(plan, rows, V, xt[4:12], ids, yt[4:12], u, nt[1:3], cur0=1, n_cur=2)
+    plan.sync()
+    assert all(np.array_equal(a[1:3], b) for a, b in zip(whole[:3], part[:3]))
+    assert np.array_equal(whole[3][4:12], part[3][4:12]) and (part[3][:4] == -7).all() and (part[3][12:] == -7).all()
+
+
+def test_distribution_of_the_emitted_token(lib):
+    """Over many draws the first emitted token has the target's own distribution, whatever the draft's: frequencies of 40,000 within
+    five standard deviations."""
+    n, V = 40000, 8
+    rng = np.random.default_rng(11)
+    x0, y0 = rng.standard_normal(V), 2 * rng.standard_normal(V)
+    p, q = (np.exp(z - np.logaddexp.reduce(z)) for z in (x0, y0))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = np.zeros(2 * n, dtype=np.int32)
+    ids[1::2] = rng.choice(V, size=n, p=q)
+    xt = torch.tensor(x0, dtype=torch.float32, device="cuda").repeat(2 * n, 1)
+    yt = torch.tensor(y0, dtype=torch.float32, device="cuda").repeat(2 * n, 1)
+    noise = torch.empty((n, V), device="cuda").exponential_(generator=g)
+    rows = [2] * n
+    plan = chunk_plan(lib, rows)
+    acc, nxt, _, _ = run(plan, rows, V, xt, ids, yt, rng.random(2 * n).astype(np.float32), noise)
+    plan.sync()
+    first = np.where(acc > 0, ids[1::2], nxt)
+    freq = np.bincount(first, minlength=V) / n
+    assert np.all(np.abs(freq - p) <= 5 * np.sqrt(p * (1 - p) / n))
+
+
+def test_refusals(lib):
+    rows, V = [3, 2], 64
+    rng = np.random.default_rng(12)
+    x, y, ids, u, noise = inputs(rng, rows, V, 0, True)
+    xt, yt, nt = on_gpu(x, "bf16")[0], on_gpu(y, "bf16")[0], on_gpu(noise, "f32")[0]
+    plan = chunk_plan(lib, rows)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    ut, it, ws = torch.tensor(u, device="cuda"), torch.tensor(ids, device="cuda"), torch.empty(4096, dtype=torch.uint8, device="cuda")
+    call = lambda cur0=0, n_cur=2, x=xt, V=V, ids=it, a=i32(2), b=i32(2), ws=ws, **kw: plan.verify_drafts(cur0, n_cur, x, V, ids, a, b, ws, **kw)
+    for kw in (dict(cur0=1), dict(n_cur=3), dict(cur0=-1), dict(ws=None), dict(ws=ws[:64].contiguous()), dict(ws=ws[4:]), dict(u=ut), dict(noise=nt),
+               dict(draft_logits=yt), dict(inv_temp=0.0), dict(inv_temp=float("nan")), dict(u=ut, noise=nt, draft_logits=yt, draft_inv_temp=-1.0),
+               dict(V=0), dict(ids=None), dict(a=None), dict(x=xt[:, 1:])):
+        with pytest.raises((lib.OctoError, ValueError)):
+            call(**kw)
+    for kw in (dict(x=xt[:4]), dict(x=xt.half()), dict(x=xt.cpu()), dict(u=ut, noise=nt[:1]), dict(u=ut, noise=nt.bfloat16()), dict(u=ut[:4], noise=nt),
+               dict(u=ut, noise=nt, draft_logits=yt.float()), dict(u=ut, noise=nt, draft_logits=yt[:4]), dict(ids=it.long()), dict(a=i32(1)),
+               dict(accept_p=torch.zeros(4, device="cuda"))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    call(n_cur=0, x=xt[:0])
+    call()
+    plan.sync()

@@ -239,3 +239,26 @@ def test_append_step_matches_oracle(lib, oracle_mod, seed):
     for key in ("n_segments", "free_pages", "n_mounts"):
         assert before[key] == after[key]
     assert np.array_equal(before["page_owner"], after["page_owner"])
+
+
+def test_chunk_plan_refusals(lib):
+    """octo_chunk_plan's checks come before any device work."""
+    pool = lib.Pool(8, 16, 2, 64, lib.DTYPE_F32)
+    r = pool.root()
+    pool.append(r, 20)
+    a = pool.fork(r, 1)[0]
+    pool.append(a, 5)
+    gone = pool.fork(r, 1)[0]
+    pool.release(gone)
+    for cur, n_new, kw in (([a], [6], {}), ([a], [-1], {}), ([9], [1], {}), ([-1], [1], {}), ([gone], [0], {}), ([a], [1], dict(window=-1)),
+                           ([a], [1], dict(n_sink=4)), ([a], [1], dict(window=4, n_sink=-1)), ([a], [1], dict(n_q_heads=3)),
+                           ([a], [1], dict(n_q_heads=0)), ([a], [1], dict(n_q_heads=-2)), ([a], [1], dict(n_q_heads=65536))):
+        with pytest.raises(lib.OctoError) as e:
+            pool.chunk_plan(cur, n_new, **{"n_q_heads": 4, **kw})
+        assert e.value.code == lib.EINVAL
+    with pytest.raises(lib.OctoError) as e:
+        pool.chunk_plan([a], [1], 258)       # 129 query heads a kv head
+    assert e.value.code == lib.ENOTSUP
+    for cur, n_new in (([a, r], [1]), ([[a]], [[1]])):
+        with pytest.raises(ValueError):
+            pool.chunk_plan(cur, n_new, 4)
