@@ -70,6 +70,8 @@ struct ChunkArgs {
   float* part_ml;
 };
 
+bool chunk_tc_supported(const octo_pool_desc& d, int32_t width);
+int chunk_tc(const octo_plan_s* p, const ChunkArgs& a, cudaStream_t s);
 int chunk_simt(const octo_plan_s* p, const ChunkArgs& a, cudaStream_t s);
 int chunk_join(const octo_plan_s* p, const ChunkArgs& a, cudaStream_t s);
 

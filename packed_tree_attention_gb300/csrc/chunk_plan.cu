@@ -158,6 +158,7 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
   cp->G = Hq / d.n_kv_heads;
   cp->width = block_width(d.page_size);
   cp->tokens = std::max(1, 128 / cp->G);
+  cp->tc = chunk_tc_supported(d, cp->width);
   cp->row0.resize((size_t)n + 1, 0);
   int64_t rows = 0;
   int32_t top = 0;   // the largest position of a row
@@ -382,7 +383,7 @@ int octo_chunk_attn(octo_plan_t plan, const void* q, const void* k_pool, const v
   a.part_ml = need ? reinterpret_cast<float*>(static_cast<char*>(ws) + octo::align_up(octo::part_floats(plan) * sizeof(float), 256)) : nullptr;
   cudaStream_t s = (cudaStream_t)stream;
   plan->last_stream = s;
-  if (int st = octo::chunk_simt(plan, a, s)) return st;
+  if (int st = plan->chunk->tc ? octo::chunk_tc(plan, a, s) : octo::chunk_simt(plan, a, s)) return st;
   return plan->chunk->n_joins ? octo::chunk_join(plan, a, s) : OCTO_OK;
 }
 

@@ -1,0 +1,439 @@
+// Chunk attention on the 5th-generation tensor cores (tcgen05, sm_103a): bf16 pools, blocks of
+// 64 keys.
+//
+// Octopus project page, "Architecture & Co-Design" item 01 (Runtime): a turn's new tokens read
+// the cursor's shared pages.  The query heads of a kv head read the same K and V, so a tile's
+// 128 rows are T = 128 / G tokens times their G heads (row t G + h): a chunk of five tokens of
+// four heads fills 20 of them and reads its context once, a prefill chunk fills all.  One CTA
+// runs one item (a piece of a tile's blocks) of one kv head with kSlots tiles of 128 rows:
+//   two  (plans with chunks of more than T tokens): consecutive tokens' tiles share each block
+//        of K and V, one CTA an SM.  Bound by the tensor cores and the exponentials.
+//   one  (short chunks, single tokens): two CTAs an SM, so that one's start, first loads and
+//        epilogue fall into the other's streaming.  Bound by HBM.
+// Warps: 0 copies (TMA: Q, then blocks through a ring), 1 and 3 issue the MMAs of slots 0 and 1
+// (S = Q K^T into two buffers each, two blocks ahead; O += P V with P read from TMEM), 2
+// allocates TMEM, 4-7 and 8-11 are the slots' softmax, a row a thread: the running maximum stays
+// until a block's probabilities relative to it sum past 2^16, the sum is kept in fp32 of the
+// unrounded probabilities, P is rounded to bf16 (half a step, as the inputs' type has it) over
+// the S that it came from.  Warps whose rows the tile does not have take no part.
+// Partial results of split tiles are joined by k_chunk_join.
+
+#include <cuda_bf16.h>
+
+#include "chunk.h"
+#include "row_ring.cuh"
+#include "tc_common.cuh"
+
+namespace octo {
+namespace {
+
+using namespace tc;
+
+template <int D, int kSlots>
+struct Shape {
+  static constexpr int kThreads = 128 + 128 * kSlots;
+  static constexpr int kChunks = D / 64;                          // 128-byte columns of a row
+  static constexpr uint32_t kQSlot = kChunks * 128 * 128;
+  static constexpr uint32_t kTile = kChunks * 64 * 128;           // K or V of a block
+  static constexpr uint32_t kStage = 2 * kTile;
+  // stages: what is left of the SM's shared memory, or of half of it
+  static constexpr int kStages = kSlots == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 2 : 4);
+  static constexpr uint32_t kOffKV = kSlots * kQSlot;
+  static constexpr uint32_t kOffBar = kOffKV + kStages * kStage;
+  static constexpr uint32_t kSmem = kOffBar + 512 + 1024;
+  static constexpr uint32_t kColO = 0, kColS = kSlots * 128;      // TMEM columns
+  static constexpr uint32_t kCols = 256 * kSlots;
+  static constexpr uint32_t kIdS = idesc_bf16(128, 64, 0, 0);
+  static constexpr uint32_t kIdO = idesc_bf16(128, D, 0, 1);
+};
+
+struct TcParams {
+  const ChunkBlock* blocks;
+  const ChunkTile* tiles;
+  const ChunkItem* items;
+  __nv_bfloat16* out;
+  float *lse, *part, *part_ml;
+  int32_t Hq, Hkv, G, P, T, box, loads, window;   // box: tokens of a query load; loads: of 64 keys
+  float scale_log2;
+  int32_t* status;
+};
+
+template <int kStages>
+struct Bars {
+  uint64_t q_full;
+  uint64_t kv_full[kStages];
+  uint64_t kv_empty[kStages];
+  uint64_t s_full[2][2];   // [slot][buffer]
+  uint64_t p_full[2][2];
+  uint64_t o_done[2][2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  volatile int32_t abort;
+};
+
+template <class B>
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, B* b, int32_t* status) {
+  if (mbar_test(bar, parity)) return true;
+  for (uint32_t i = 0; i < kSpinLimit; i++) {
+    if (mbar_try(bar, parity)) return true;
+    if ((i & 1023) == 1023 && b->abort) return false;
+  }
+  b->abort = 1;
+  atomicExch(status, OCTO_ETIMEOUT);
+  return false;
+}
+// warp-uniform: the tcgen05 .sync.aligned accesses that follow need the whole warp
+template <class B>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, B* b, int32_t* status) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, b, status));
+}
+
+template <int D, int kSlots>
+__global__ void __launch_bounds__(Shape<D, kSlots>::kThreads, kSlots == 2 ? 1 : 2)
+    k_chunk_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcParams p) {
+  using S = Shape<D, kSlots>;
+  constexpr int kNS = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  auto* B = reinterpret_cast<Bars<kNS>*>(smem + S::kOffBar);
+  static_assert(sizeof(Bars<kNS>) <= 512, "barriers");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int g = blockIdx.x % p.Hkv;
+  const ChunkItem it = p.items[blockIdx.x / p.Hkv];
+  const ChunkTile t = p.tiles[it.tile];
+  const int n = it.b1 - it.b0;                       // at least 1
+  const ChunkBlock* blk = p.blocks + t.blk0 + it.b0;
+  const int n_slots = kSlots == 2 && t.rows > p.T ? 2 : 1;
+  auto slot_rows = [&](int s) { return min(t.rows - s * p.T, p.T) * p.G; };
+
+  if (threadIdx.x == 0) {
+    mbar_init(&B->q_full, 1);
+    for (int s = 0; s < kNS; s++) {
+      mbar_init(&B->kv_full[s], 1);
+      mbar_init(&B->kv_empty[s], n_slots);   // released by the slots' P V
+    }
+    for (int h = 0; h < n_slots; h++)
+      for (int b = 0; b < 2; b++) {
+        mbar_init(&B->s_full[h][b], 1);
+        mbar_init(&B->p_full[h][b], (slot_rows(h) + 31) / 32 * 32);
+        mbar_init(&B->o_done[h][b], 1);
+      }
+    mbar_init(&B->drain, n_slots);
+    B->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(&B->tmem_base, S::kCols);
+    tmem_relinquish();
+  }
+  // rows of the tile that no query load writes: finite, for the warps that have rows besides
+  {
+    const int q_rows = p.box * p.G;
+    for (int s = 0; s < n_slots; s++)
+      for (int c = 0; c < S::kChunks; c++)
+        for (int i = q_rows * 8 + threadIdx.x; i < 128 * 8; i += S::kThreads)
+          *reinterpret_cast<uint4*>(smem + s * S::kQSlot + c * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = B->tmem_base;
+  const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + S::kOffKV);
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    if (lane == 0) {
+      prefetch_map(&tmQ);
+      prefetch_map(&tmK);
+      prefetch_map(&tmV);
+      rows::wait_for_predecessor();
+      mbar_expect_tx(&B->q_full, (uint32_t)(n_slots * S::kChunks * p.box * p.G * 128));
+      for (int s = 0; s < n_slots; s++)
+        for (int c = 0; c < S::kChunks; c++)
+          tma_load_3d(smem + s * S::kQSlot + c * 16384, &tmQ, &B->q_full, c * 64, g * p.G, t.row0 + s * p.T);
+      int issued = 0;
+      const uint32_t part = 8192u / p.loads;   // bytes of a load
+      ChunkBlock next = blk[0];
+      for (int j = 0; j < n; j++) {
+        const int st = j % kNS;
+        const ChunkBlock k = next;
+        if (j + 1 < n) next = blk[j + 1];      // off the critical path
+        if (j >= kNS && !wait_or_abort(&B->kv_empty[st], ((j / kNS) - 1) & 1, B, p.status)) break;
+        uint8_t* dst = smem + S::kOffKV + st * S::kStage;
+        mbar_expect_tx(&B->kv_full[st], S::kStage);
+#pragma unroll
+        for (int l = 0; l < 4; l++) {
+          if (l >= p.loads) break;
+          const int row = (k.page[l] * p.Hkv + g) * p.P + k.slot0;
+#pragma unroll
+          for (int c = 0; c < S::kChunks; c++) {
+            tma_load_2d(dst + c * 8192 + l * part, &tmK, &B->kv_full[st], c * 64, row);
+            tma_load_2d(dst + S::kTile + c * 8192 + l * part, &tmV, &B->kv_full[st], c * 64, row);
+          }
+        }
+        issued = j + 1;
+      }
+      // every copy this thread started has landed before the CTA may exit
+      mbar_wait(&B->q_full, 0, p.status, OCTO_ETIMEOUT);
+      for (int j = max(0, issued - kNS); j < issued; j++)
+        mbar_wait(&B->kv_full[j % kNS], (j / kNS) & 1, p.status, OCTO_ETIMEOUT);
+    }
+  } else if (warp == 1 || (warp == 3 && n_slots == 2)) {
+    // ---------------- MMAs ----------------
+    const int hh = warp == 1 ? 0 : 1;
+    if (lane == 0) {
+      const uint64_t dq0 = desc_sw128(sQ + hh * S::kQSlot, 16, 1024);
+      const uint64_t dk0 = desc_sw128(sKV, 16, 1024);
+      const uint64_t dv0 = desc_sw128(sKV + S::kTile, 8192, 1024);
+      const uint32_t dO = tbase + S::kColO + hh * 128, dS = tbase + S::kColS + hh * 128;
+      auto issue_S = [&](int st, int b) {
+        const uint64_t kb = dk0 + (uint64_t)(st * (S::kStage >> 4));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; kk++) {
+          const uint32_t qo = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+          const uint32_t ko = ((kk >> 2) * 8192 + (kk & 3) * 32) >> 4;
+          mma_f16_ss(dS + b * 64, dq0 + qo, kb + ko, S::kIdS, kk > 0);
+        }
+        mma_commit(&B->s_full[hh][b]);
+      };
+      auto issue_PV = [&](int st, int b, bool first) {
+        const uint64_t vb = dv0 + (uint64_t)(st * (S::kStage >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 4; kk++)
+          mma_f16_ts(dO, dS + b * 64 + kk * 8, vb + (uint64_t)(kk * (2048 >> 4)), S::kIdO, (!first || kk > 0) ? 1u : 0u);
+        mma_commit(&B->o_done[hh][b]);
+      };
+      bool ok = wait_or_abort(&B->q_full, 0, B, p.status);
+      for (int j = 0; ok && j < min(n, 2); j++) {
+        if (!(ok = wait_or_abort(&B->kv_full[j], 0, B, p.status))) break;
+        tc_fence_after();
+        issue_S(j, j);
+      }
+      for (int j = 0; ok && j < n; j++) {
+        const int st = j % kNS, b = j & 1, j2 = j + 2;
+        if (!(ok = wait_or_abort(&B->p_full[hh][b], (j >> 1) & 1, B, p.status))) break;
+        tc_fence_after();
+        issue_PV(st, b, j == 0);
+        mma_commit(&B->kv_empty[st]);
+        if (j2 < n) {
+          // buffer b held P of block j, which P V above reads first (MMAs of a thread run in order)
+          if (!(ok = wait_or_abort(&B->kv_full[j2 % kNS], (j2 / kNS) & 1, B, p.status))) break;
+          tc_fence_after();
+          issue_S(j2 % kNS, b);
+        }
+      }
+      // all MMAs of this thread are complete before TMEM is released
+      mma_commit(&B->drain);
+      mbar_wait(&B->drain, 0, p.status, OCTO_ETIMEOUT);
+    }
+  } else if (warp >= 4 && ((warp - 4) >> 2) < n_slots && (warp & 3) * 32 < slot_rows((warp - 4) >> 2)) {
+    // ---------------- softmax ----------------
+    const int hh = (warp - 4) >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane, R = slot_rows(hh);
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS0 = tbase + lane_off + S::kColS + hh * 128;
+    const uint32_t tO = tbase + lane_off + S::kColO + hh * 128;
+    // own index of this thread's row, and of the warp's first and last one
+    const int base = t.t0 + hh * p.T;
+    const int own = base + min(r, R - 1) / p.G;
+    const int own_first = base + wq * 32 / p.G, own_last = base + min(wq * 32 + 31, R - 1) / p.G;
+    const bool windowed = p.window > 0;
+    const int w_shift = t.shift - p.window + 1;
+    float m_used = -INFINITY, l = 0.f;
+    bool ok = true;
+    auto fields = [&](int j) { return *reinterpret_cast<const int4*>(&blk[j].own0); };   // own0, kpos, lo | hi << 16, slot0
+    int4 next = fields(0);
+    for (int j = 0; j < n; j++) {
+      const int4 e = next;
+      if (j + 1 < n) next = fields(j + 1);
+      const int b = j & 1;
+      int lo = e.z & 0xffff, hi = (uint32_t)e.z >> 16;
+      const bool full = lo == 0 && hi == 64 && e.x + 63 <= own_first && (!windowed || own_last + w_shift <= e.y);
+      if (!(ok = warp_wait(&B->s_full[hh][b], (j >> 1) & 1, B, p.status))) break;
+      tc_fence_after();
+      uint32_t s0[32], s1[32];
+      tmem_ld32(tS0 + b * 64, s0);
+      tmem_ld32(tS0 + b * 64 + 32, s1);
+      tmem_wait_ld();
+      float x[64];   // raw scores; the scale is folded into the exponent
+#pragma unroll
+      for (int i = 0; i < 32; i++) {
+        x[i] = __uint_as_float(s0[i]);
+        x[32 + i] = __uint_as_float(s1[i]);
+      }
+      if (!full) {
+        if (windowed) lo = max(lo, own + w_shift - e.y);
+        hi = min(hi, own - e.x + 1);
+#pragma unroll
+        for (int i = 0; i < 64; i++)
+          if (i < lo || i >= hi) x[i] = -INFINITY;
+      }
+      bool need = false;
+      float factor = 1.f;
+      // nothing visible to this row yet: start from the block's exact maximum
+      if (m_used == -INFINITY) m_used = max64(x) * p.scale_log2;
+      float msub = (m_used == -INFINITY) ? 0.f : m_used;
+      uint32_t pk[32];
+      auto pass = [&]() -> float {
+        float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; i++) {
+          float a, c;
+          fma2(a, c, x[2 * i], x[2 * i + 1], p.scale_log2, -msub);
+          a = ex2(a);
+          c = ex2(c);
+          add2(ps[2 * (i & 3)], ps[2 * (i & 3) + 1], ps[2 * (i & 3)], ps[2 * (i & 3) + 1], a, c);
+          pk[i] = pack_bf16(a, c);
+        }
+        return ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+      };
+      float le = pass();
+      const bool over = !(le <= 65536.f);
+      if (__any_sync(0xffffffffu, over)) {
+        if (over) {
+          const float mc = max64(x) * p.scale_log2;
+          factor = ex2(m_used - mc);
+          l *= factor;
+          m_used = mc;
+          msub = mc;
+          need = true;
+        }
+        le = pass();
+      }
+      l += le;
+      if (j > 0 && __any_sync(0xffffffffu, need)) {
+        // O must hold every P V so far before it is rescaled
+        if (!(ok = warp_wait(&B->o_done[hh][(j - 1) & 1], ((j - 1) >> 1) & 1, B, p.status))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 32; c++) {
+          uint32_t ov[32];
+          tmem_ld32(tO + c * 32, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; i++) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * factor);
+          tmem_st32(tO + c * 32, ov);
+        }
+        tmem_wait_st();
+      }
+      tmem_st32(tS0 + b * 64, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&B->p_full[hh][b]);
+    }
+    // ---------------- results ----------------
+    if (ok && warp_wait(&B->o_done[hh][(n - 1) & 1], ((n - 1) >> 1) & 1, B, p.status)) {
+      tc_fence_after();
+      const int tok = hh * p.T + min(r, R - 1) / p.G, h = min(r, R - 1) % p.G;
+      const bool partial = it.part >= 0;
+      const size_t row = (size_t)(t.row0 + tok) * p.Hq + g * p.G + h;
+      const int64_t at = partial ? chunk_part(it.part, p.Hkv, g, t.rows * p.G, tok * p.G + h) : 0;
+      const float inv = partial ? 1.f : 1.f / l;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; c++) {
+        uint32_t ov[32];
+        tmem_ld32(tO + c * 32, ov);
+        tmem_wait_ld();
+        if (r < R) {
+          if (partial) {
+            float* dst = p.part + at * D + c * 32;
+#pragma unroll
+            for (int q4 = 0; q4 < 8; q4++) st_global_v4(dst + 4 * q4, ov[4 * q4], ov[4 * q4 + 1], ov[4 * q4 + 2], ov[4 * q4 + 3]);
+          } else {
+            __nv_bfloat16* dst = p.out + row * D + c * 32;
+#pragma unroll
+            for (int q4 = 0; q4 < 4; q4++) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; i++)
+                w[i] = pack_bf16(__uint_as_float(ov[q4 * 8 + 2 * i]) * inv, __uint_as_float(ov[q4 * 8 + 2 * i + 1]) * inv);
+              st_global_v4(dst + q4 * 8, w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+      if (r < R) {
+        if (partial) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m_used, l);
+        else if (p.lse) p.lse[row] = (m_used + log2f(l)) * 0.69314718055994531f;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tbase, S::kCols);
+}
+
+template <int D, int kSlots>
+int launch(const octo_plan_s* plan, const ChunkArgs& a, cudaStream_t s) {
+  using S = Shape<D, kSlots>;
+  const octo_pool_desc& d = plan->pool->desc;
+  const ChunkPlan& c = *plan->chunk;
+  TcParams p;
+  p.blocks = c.blocks, p.tiles = c.tiles, p.items = c.items;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse, p.part = a.part, p.part_ml = a.part_ml;
+  p.Hq = c.Hq, p.Hkv = d.n_kv_heads, p.G = c.G, p.P = d.page_size, p.T = c.tokens;
+  p.box = c.max_rows < c.tokens ? c.max_rows : c.tokens;
+  const int span = d.page_size < 64 ? d.page_size : 64;
+  p.loads = 64 / span;
+  p.window = c.window;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.status = plan->pool->d_status;
+  CUtensorMap mq, mk, mv;
+  {
+    uint64_t dims[3] = {(uint64_t)D, (uint64_t)c.Hq, (uint64_t)plan->info.n_rows};
+    uint64_t str[2] = {D * 2, (uint64_t)c.Hq * D * 2};
+    uint32_t box[3] = {64, (uint32_t)c.G, (uint32_t)p.box};
+    if (int st = encode_tmap(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, str, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B))
+      return st;
+  }
+  {
+    uint64_t dims[2] = {(uint64_t)D, (uint64_t)d.num_pages * d.n_kv_heads * d.page_size};
+    uint64_t str[1] = {D * 2};
+    uint32_t box[2] = {64, (uint32_t)span};
+    if (int st = encode_tmap(&mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.k), dims, str, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B))
+      return st;
+    if (int st = encode_tmap(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.v), dims, str, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B))
+      return st;
+  }
+  const int64_t grid = (int64_t)c.n_items * d.n_kv_heads;
+  if (grid > INT32_MAX) return OCTO_EINVAL;
+  const void* kernel = (const void*)k_chunk_tc<D, kSlots>;
+  if (int st = set_smem_limit(kernel, (int)S::kSmem)) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  void* args[4] = {&mq, &mk, &mv, &p};
+  OCTO_CUDA(cudaLaunchKernelExC(&cfg, kernel, args));
+  count_launch();
+  return OCTO_OK;
+}
+
+}  // namespace
+
+bool chunk_tc_supported(const octo_pool_desc& d, int32_t width) {
+  // rows of the pool arrays are a coordinate of the copies, 32 bits with a sign
+  return d.dtype == OCTO_DTYPE_BF16 && width == 64 && (int64_t)d.num_pages * d.n_kv_heads * d.page_size <= INT32_MAX;
+}
+
+int chunk_tc(const octo_plan_s* plan, const ChunkArgs& a, cudaStream_t s) {
+  const bool two = plan->chunk->max_rows > plan->chunk->tokens;
+  if (plan->pool->desc.head_dim == 64) return two ? launch<64, 2>(plan, a, s) : launch<64, 1>(plan, a, s);
+  return two ? launch<128, 2>(plan, a, s) : launch<128, 1>(plan, a, s);
+}
+
+}  // namespace octo
