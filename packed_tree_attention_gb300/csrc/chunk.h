@@ -25,24 +25,30 @@ constexpr int32_t kFarOwn = -(1 << 30);
 constexpr int32_t kSinkPos = 1 << 30;
 constexpr int32_t kMaxPos = 1 << 29;   // positions of a chunk plan: their differences and the above fit 32 bits
 
-// Rows [row0, row0 + rows) of the plan: tokens of one cursor from own index t0 on, at positions
-// own index + shift, no mount among them; the blocks that some of them sees.
+// Rows [row0, row0 + rows) of the plan, and blocks that some of them sees.  Of one cursor: tokens
+// from own index t0 on, at positions own index + shift, no mount among them.  Or of several
+// cursors next to each other, with blocks of common ancestors, which all of them see (t0 = 0).
 struct ChunkTile {
   int32_t row0, rows, t0, shift;
   int32_t blk0, n_blk;
   int32_t pad[2];
 };
 
-// Work of one CTA (and kv head): blocks [b0, b1) of a tile.  part < 0: all of the tile's, the
-// result is written; else partial results from row `part` on (rows * G of each kv head).
+// Work of one CTA (and kv head): blocks [b0, b1) of a tile.  part < 0: all that its rows see,
+// the result is written; else partial results from row `part` on (rows * G of each kv head).
 struct ChunkItem {
   int32_t tile, b0, b1;
   int32_t part;
 };
 
-// A tile whose items are joined: n_parts of them, the first one's rows from `part` on.
+// Partial results of an item that a joined tile takes part in: from row `part` on, R of each kv
+// head, the tile's from the off-th on.
+struct ChunkRef {
+  int32_t part, R, off, pad;
+};
+// A tile whose rows have several partial results: refs [ref0, ref0 + n_refs).
 struct ChunkJoin {
-  int32_t tile, part, n_parts, pad;
+  int32_t tile, ref0, n_refs, pad;
 };
 
 struct ChunkPlan {
@@ -53,11 +59,13 @@ struct ChunkPlan {
   int32_t n_items = 0, n_joins = 0;
   int32_t max_rows = 0;               // rows of the longest tile
   int32_t max_join_rows = 0;          // and of the longest joined one
+  int32_t max_refs = 0;
   int64_t part_rows = 0;              // rows of all partial results (of one kv head)
   ChunkBlock* blocks = nullptr;       // device arrays, the plan's
   ChunkTile* tiles = nullptr;
   ChunkItem* items = nullptr;         // largest first
   ChunkJoin* joins = nullptr;
+  ChunkRef* refs = nullptr;
   std::vector<int32_t> row0;          // [cursors + 1] first row of each (host)
 };
 

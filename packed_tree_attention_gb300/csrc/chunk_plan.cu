@@ -4,9 +4,12 @@
 // over the pages it shares; item 02: mounted spans are read in place.  A chunk plan is to
 // several new tokens of a cursor what a decode plan is to one.  It lists, per cursor, the
 // context in blocks of 64 keys, once for all of the cursor's tiles (without a window a tile's
-// blocks are a prefix of them; under one, each tile lists the few that it sees), and cuts the
-// tiles' block lists into items of about equal length.  It is built on the host: a step's plan
-// serves every layer of a model, and its size is that of the contexts' page lists.
+// blocks are a prefix of them; under one, each tile lists the few that it sees).  What several
+// cursors next to each other share, common ancestors up to the same point, is listed once for
+// all of them: their rows, next to each other too, make tiles of their own for it, so that the
+// prefix of a tree's branches is read once and not once a branch.  The tiles' block lists are
+// cut into items of about equal length.  The plan is built on the host: a step's plan serves
+// every layer of a model, and its size is that of the contexts' page lists.
 
 #include <algorithm>
 #include <cstring>
@@ -23,6 +26,12 @@ namespace {
 // Keys per block: 64 where pages make up 64 keys or are made up of them, so that a block is 64
 // rows of a tensor-core tile; else a page.
 int32_t block_width(int32_t P) { return (P % 64 == 0 || (P >= 16 && 64 % P == 0)) ? 64 : P; }
+
+// The first `fork` tokens of segment seg, and its mounts among the first n_mounts up to there.
+struct Level {
+  int32_t seg, fork, n_mounts;
+  bool operator==(const Level& o) const { return seg == o.seg && fork == o.fork && n_mounts == o.n_mounts; }
+};
 
 struct Builder {
   const octo_pool_s* pool;
@@ -54,15 +63,71 @@ struct Builder {
     }
   }
 
-  // What a child of segment s sees of it: its first tokens, and the mounts it held by then.
-  void ancestor(int32_t s, const Segment& child) {
-    for (int32_t id : pool->segs[s].mounts) {
-      const MountRec& m = pool->mounts[id];
-      if (m.m <= child.fork && m.created < child.created) span(m.producer, m.a, m.b, false);
+  // what a child sees of its parent: the mounts it held by then, and its first tokens
+  void ancestor(const Level& l) {
+    const std::vector<int32_t>& mounts = pool->segs[l.seg].mounts;
+    for (int32_t i = 0; i < l.n_mounts; i++) {
+      const MountRec& m = pool->mounts[mounts[i]];
+      if (m.m <= l.fork) span(m.producer, m.a, m.b, false);
     }
-    span(s, 0, child.fork, false);
+    span(l.seg, 0, l.fork, false);
   }
 };
+
+Level level_of(const octo_pool_s* pool, int32_t child) {
+  const Segment& c = pool->segs[child];
+  Level l{c.parent, c.fork, 0};
+  for (int32_t id : pool->segs[c.parent].mounts) l.n_mounts += pool->mounts[id].created < c.created;   // in order of creation
+  return l;
+}
+
+// A cursor with rows and what it sees besides its own segment, from the root on.
+struct Path {
+  int32_t cursor;
+  std::vector<Level> levels;
+  size_t first;                  // the levels before it are in shared tiles
+  std::vector<int32_t> shared;   // those tiles
+};
+
+// Finds the runs of cursors with common levels.  share(from, to, l0, l1): makes tiles of the paths
+// [from, to) with their common levels [l0, l1) and notes it in each path that got one.
+template <typename F>
+struct Sharing {
+  const octo_pool_s* pool;
+  std::vector<Path>& paths;
+  F share;
+  void range(size_t from, size_t to, size_t l0, size_t depth) {
+    if (to - from < 2) return;
+    size_t l1 = depth;
+    auto same = [&](size_t i, size_t l) {
+      return l < paths[i].levels.size() && l < paths[from].levels.size() && paths[i].levels[l] == paths[from].levels[l];
+    };
+    auto all_same = [&] {
+      for (size_t i = from; i < to; i++)
+        if (!same(i, l1)) return false;
+      return true;
+    };
+    while (all_same()) l1++;
+    if (l1 > l0) share(from, to, l0, l1);
+    // runs whose next level, and what is left to share before it, are the same
+    for (size_t i = from; i < to;) {
+      size_t e = i + 1;
+      auto alike = [&](size_t k) {
+        return paths[k].first == paths[i].first && l1 < paths[i].levels.size() && l1 < paths[k].levels.size() &&
+               paths[k].levels[l1] == paths[i].levels[l1];
+      };
+      while (e < to && alike(e)) e++;
+      range(i, e, std::max(l0, paths[i].first), l1);
+      i = e;
+    }
+  }
+};
+template <typename F>
+Sharing(const octo_pool_s*, std::vector<Path>&, F) -> Sharing<F>;
+
+// Shared blocks that are worth tiles of their own: with fewer, the items and the partial results
+// that these cost take longer than reading the blocks again (from L2 mostly).
+constexpr int32_t kShareBlocks = 8;
 
 // Visible (row, key) pairs of a tile's block.
 int64_t block_pairs(const ChunkBlock& k, const ChunkTile& t, int32_t window) {
@@ -90,11 +155,11 @@ int64_t makespan(const std::vector<int32_t>& lens, int heads, int sms) {
   return end;
 }
 
-// Blocks per item, an item costing its blocks and kItemCost more (its start, its query tile, its
+// Blocks per item, an item costing its blocks and item_cost more (its start, its query tile, its
 // epilogue), and a plan with joined tiles kJoinCost: the length with the shortest makespan among
-// those that fill the SMs 1, 2, ... times.
-constexpr int kItemCost = 5, kJoinCost = 4;
-int32_t pick_length(const std::vector<ChunkTile>& tiles, int heads, int sms) {
+// those that fill the `sms` places 1, 2, ... times.
+constexpr int kJoinCost = 4;
+int32_t pick_length(const std::vector<ChunkTile>& tiles, int heads, int sms, int item_cost) {
   int32_t most = 1;
   int64_t total = 0;
   for (const ChunkTile& t : tiles) most = std::max(most, t.n_blk), total += t.n_blk;
@@ -112,7 +177,7 @@ int32_t pick_length(const std::vector<ChunkTile>& tiles, int heads, int sms) {
     for (const ChunkTile& t : tiles) {
       const int32_t k = (t.n_blk + len - 1) / len;
       join |= k > 1;
-      for (int32_t i = 0; i < k; i++) lens.push_back((t.n_blk - i + k - 1) / k + kItemCost);
+      for (int32_t i = 0; i < k; i++) lens.push_back((t.n_blk - i + k - 1) / k + item_cost);
     }
     std::sort(lens.begin(), lens.end(), std::greater<int32_t>());
     const int64_t t = makespan(lens, heads, sms) + (join ? kJoinCost : 0);
@@ -171,26 +236,81 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
   if (top >= kMaxPos) return OCTO_ENOTSUP;
   cp->window = window > top ? 0 : window;   // sees everything
 
+  // tiles have the rows of one 128-row tile, of two where a chunk is longer
+  int32_t most_new = 0;
+  for (int32_t c = 0; c < n; c++) most_new = std::max(most_new, n_new[c]);
+  const int32_t cap = most_new > cp->tokens ? 2 * cp->tokens : cp->tokens;
   Builder b{pool, d.page_size, cp->width, cp->window ? n_sink : 0, {}};
   std::vector<ChunkBlock> blocks;
   std::vector<ChunkTile> tiles;
-  std::vector<int32_t> row_pos((size_t)rows), chain;
+  std::vector<int32_t> row_pos((size_t)rows);
   int64_t pairs = 0;
+  auto add_pairs = [&](const ChunkTile& t) {
+    for (int32_t i = 0; i < t.n_blk; i++) pairs += block_pairs(blocks[t.blk0 + i], t, cp->window);
+  };
+
+  // tiles of several cursors
+  std::vector<Path> paths;
   for (int32_t c = 0; c < n; c++) {
     if (!n_new[c]) continue;
+    paths.push_back({c, {}, 0, {}});
+    for (int32_t x = cursors[c]; pool->segs[x].parent >= 0; x = pool->segs[x].parent)
+      paths.back().levels.push_back(level_of(pool, x));
+    std::reverse(paths.back().levels.begin(), paths.back().levels.end());
+  }
+  if (!cp->window) {
+    Sharing sh{pool, paths, [&](size_t from, size_t to, size_t l0, size_t l1) {
+      // cursors [from, to) of `paths` and their common levels [l0, l1)
+      b.out.clear();
+      for (size_t l = l0; l < l1; l++) b.ancestor(paths[from].levels[l]);
+      if ((int32_t)b.out.size() < kShareBlocks) return false;
+      const int32_t blk0 = (int32_t)blocks.size();
+      bool any = false;
+      for (size_t i = from; i < to;) {
+        size_t e = i;
+        int32_t tokens = 0;
+        while (e < to && tokens + n_new[paths[e].cursor] <= cap) tokens += n_new[paths[e++].cursor];
+        if (e - i < 2) {
+          i = std::max(e, i + 1);
+          continue;
+        }
+        if (!any) blocks.insert(blocks.end(), b.out.begin(), b.out.end());
+        any = true;
+        ChunkTile t = {};
+        t.row0 = cp->row0[paths[i].cursor];
+        t.rows = tokens;
+        t.blk0 = blk0;
+        t.n_blk = (int32_t)b.out.size();
+        add_pairs(t);
+        for (; i < e; i++) {
+          paths[i].shared.push_back((int32_t)tiles.size());
+          paths[i].first = l1;
+        }
+        tiles.push_back(t);
+      }
+      return any;
+    }};
+    sh.range(0, paths.size(), 0, 0);
+  }
+  const size_t n_shared = tiles.size();
+  std::vector<const Path*> path_of;   // of the tiles from n_shared on
+
+  std::vector<int32_t> from, cut;
+  for (const Path& path : paths) {
+    const int32_t c = path.cursor;
     const Segment& g = pool->segs[cursors[c]];
     const int32_t first = g.len - n_new[c];
     std::copy(g.pos.begin() + first, g.pos.end(), row_pos.begin() + cp->row0[c]);
-    // the cursor's context, in the order in which its rows come to see it
+    // the rest of the cursor's context, in the order in which its rows come to see it, and from
+    // which of its segment's tokens on they do
     b.out.clear();
-    chain.clear();
-    for (int32_t x = cursors[c]; x >= 0; x = pool->segs[x].parent) chain.push_back(x);
-    for (size_t l = chain.size(); l-- > 1;) b.ancestor(chain[l], pool->segs[chain[l - 1]]);
-    // how many of the blocks a row sees (from which of its segment's tokens on)
-    const size_t far = b.out.size();
-    std::vector<int32_t> from(far, 0);
+    for (size_t l = path.first; l < path.levels.size(); l++) b.ancestor(path.levels[l]);
+    from.assign(b.out.size(), 0);
+    cut.clear();
     int32_t next = 0;
-    std::vector<int32_t> cut;
+    auto own_from = [&] {
+      while (from.size() < b.out.size()) from.push_back(b.out[from.size()].own0 + b.out[from.size()].lo);
+    };
     for (int32_t id : g.mounts) {
       const MountRec& m = pool->mounts[id];
       if (m.m > g.len - 1) continue;
@@ -200,13 +320,13 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
         b.span(cursors[c], next, m.m, true);
         next = m.m;
       }
-      while (from.size() < b.out.size()) from.push_back(b.out[from.size()].own0 + b.out[from.size()].lo);
+      own_from();
       b.span(m.producer, m.a, m.b, false);
       from.resize(b.out.size(), m.m);
       if (m.m > first) cut.push_back(m.m);
     }
     if (next < g.len) b.span(cursors[c], next, g.len, true);
-    while (from.size() < b.out.size()) from.push_back(b.out[from.size()].own0 + b.out[from.size()].lo);
+    own_from();
     cut.push_back(g.len);
     const int32_t base = (int32_t)blocks.size();
     if (!cp->window) blocks.insert(blocks.end(), b.out.begin(), b.out.end());
@@ -217,7 +337,7 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
       ChunkTile tile = {};
       tile.row0 = cp->row0[c] + t - first;
       tile.t0 = t;
-      tile.rows = std::min(2 * cp->tokens, cut[k] - t);
+      tile.rows = std::min(cap, cut[k] - t);
       tile.shift = g.pos[t] - t;
       const int32_t last = t + tile.rows - 1;
       while (seen < b.out.size() && from[seen] <= last) seen++;
@@ -232,35 +352,50 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
         tile.blk0 = base;
         tile.n_blk = (int32_t)seen;
       }
-      for (int32_t i = 0; i < tile.n_blk; i++) pairs += block_pairs(blocks[tile.blk0 + i], tile, cp->window);
+      add_pairs(tile);
       tiles.push_back(tile);
+      path_of.push_back(&path);
       t += tile.rows;
     }
     if (blocks.size() > (size_t)INT32_MAX / 2) return OCTO_EINVAL;
   }
 
-  // items
+  // items, in pieces of the tiles' blocks; the joins of what has several
   const int sms = std::max(1, rows::sm_count());
-  const int32_t len = pick_length(tiles, d.n_kv_heads, sms);
+  for (const ChunkTile& t : tiles) cp->max_rows = std::max(cp->max_rows, t.rows);
+  const bool paired = cp->tc && cp->max_rows <= cp->tokens;   // two CTAs an SM
+  const int32_t len = pick_length(tiles, d.n_kv_heads, paired ? 2 * sms : sms, paired ? 3 : 5);
   std::vector<ChunkItem> items;
   std::vector<ChunkJoin> joins;
+  std::vector<ChunkRef> refs;
+  std::vector<std::pair<size_t, size_t>> items_of(tiles.size());   // [first, end) of each tile's
   int32_t longest = 0;
-  for (int32_t i = 0; i < (int32_t)tiles.size(); i++) {
+  for (size_t i = 0; i < tiles.size(); i++) {
     const ChunkTile& t = tiles[i];
     longest = std::max(longest, t.n_blk);
-    cp->max_rows = std::max(cp->max_rows, t.rows);
     const int32_t k = std::max(1, (t.n_blk + len - 1) / len);
-    if (k > 1) {
-      joins.push_back({i, (int32_t)cp->part_rows, k, 0});
-      cp->max_join_rows = std::max(cp->max_join_rows, t.rows);
-    }
+    const bool partial = k > 1 || i < n_shared || !path_of[i - n_shared]->shared.empty();
+    items_of[i].first = items.size();
     for (int32_t j = 0, at = 0; j < k; j++) {
       const int32_t e = at + (t.n_blk - at) / (k - j);
-      items.push_back({i, at, e, k > 1 ? (int32_t)cp->part_rows : -1});
+      items.push_back({(int32_t)i, at, e, partial ? (int32_t)cp->part_rows : -1});
       at = e;
-      if (k > 1) cp->part_rows += (int64_t)t.rows * cp->G;
+      if (partial) cp->part_rows += (int64_t)t.rows * cp->G;
       if (cp->part_rows > INT32_MAX) return OCTO_EINVAL;
     }
+    items_of[i].second = items.size();
+    if (i < n_shared || !partial) continue;
+    const int32_t ref0 = (int32_t)refs.size();
+    auto add = [&](size_t tile) {
+      for (size_t x = items_of[tile].first; x < items_of[tile].second; x++)
+        refs.push_back({items[x].part, tiles[tile].rows * cp->G, (t.row0 - tiles[tile].row0) * cp->G, 0});
+    };
+    for (int32_t x : path_of[i - n_shared]->shared) add(x);
+    add(i);
+    const int32_t n_refs = (int32_t)refs.size() - ref0;
+    joins.push_back({(int32_t)i, ref0, n_refs, 0});
+    cp->max_join_rows = std::max(cp->max_join_rows, t.rows);
+    cp->max_refs = std::max(cp->max_refs, n_refs);
   }
   std::stable_sort(items.begin(), items.end(), [](const ChunkItem& x, const ChunkItem& y) { return x.b1 - x.b0 > y.b1 - y.b0; });
   cp->n_items = (int32_t)items.size();
@@ -268,14 +403,14 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
 
   // what octo_plan_copy_out gives of a chunk plan: its cursors, rows, positions and tiles
   std::vector<int32_t> order(cursors, cursors + n), t_seg, t_t0, t_rows, none(std::max((size_t)d.num_pages, tiles.size()) + 1, 0);
-  for (int32_t c = 0, i = 0; i < (int32_t)tiles.size(); i++) {
-    while (tiles[i].row0 >= cp->row0[c + 1]) c++;
-    t_seg.push_back(cursors[c]), t_t0.push_back(tiles[i].t0), t_rows.push_back(tiles[i].rows);
+  for (size_t i = n_shared; i < tiles.size(); i++) {
+    t_seg.push_back(cursors[path_of[i - n_shared]->cursor]);
+    t_t0.push_back(tiles[i].t0), t_rows.push_back(tiles[i].rows);
   }
 
   // device arrays: one allocation, one copy
   size_t at = 0;
-  const size_t o_blk = place(&at, blocks), o_tile = place(&at, tiles), o_item = place(&at, items), o_join = place(&at, joins),
+  const size_t o_blk = place(&at, blocks), o_tile = place(&at, tiles), o_item = place(&at, items), o_join = place(&at, joins), o_ref = place(&at, refs),
                o_pos = place(&at, row_pos), o_row0 = place(&at, cp->row0),
                o_order = place(&at, order), o_seg = place(&at, t_seg), o_t0 = place(&at, t_t0), o_rows = place(&at, t_rows),
                o_none = place(&at, none);
@@ -283,7 +418,7 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
   auto put = [&](size_t o, const auto& v) {
     if (!v.empty()) std::memcpy(stage.data() + o, v.data(), v.size() * sizeof(v[0]));
   };
-  put(o_blk, blocks), put(o_tile, tiles), put(o_item, items), put(o_join, joins), put(o_pos, row_pos), put(o_row0, cp->row0);
+  put(o_blk, blocks), put(o_tile, tiles), put(o_item, items), put(o_join, joins), put(o_ref, refs), put(o_pos, row_pos), put(o_row0, cp->row0);
   put(o_order, order), put(o_seg, t_seg), put(o_t0, t_t0), put(o_rows, t_rows), put(o_none, none);
   if (int st = ensure_status(pool)) return st;
   OCTO_CUDA(cudaGetDevice(&pl->device));
@@ -298,6 +433,7 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
   cp->tiles = reinterpret_cast<ChunkTile*>(base + o_tile);
   cp->items = reinterpret_cast<ChunkItem*>(base + o_item);
   cp->joins = reinterpret_cast<ChunkJoin*>(base + o_join);
+  cp->refs = reinterpret_cast<ChunkRef*>(base + o_ref);
   pl->row_pos = reinterpret_cast<int32_t*>(base + o_pos);
   pl->seg_row_base = reinterpret_cast<int32_t*>(base + o_row0);
   pl->seg_order = reinterpret_cast<int32_t*>(base + o_order);
@@ -307,10 +443,10 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
   pl->tile_off = pl->page_off = reinterpret_cast<int32_t*>(base + o_none);   // no entries
   std::memset(&pl->info, 0, sizeof(pl->info));
   pl->info.n_rows = rows;
-  pl->info.n_tiles = (int64_t)tiles.size();
+  pl->info.n_tiles = (int64_t)path_of.size();
   pl->info.n_segments = n;
   pl->info.pairs = pairs;
-  pl->info.bm = 2 * cp->tokens;
+  pl->info.bm = cap;
   pl->info.page_size = d.page_size;
   pl->info.max_tile_entries = longest;
   pl->info.is_decode = 2;

@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 
 #include "chunk.h"
+#include "row_ring.cuh"
 
 namespace octo {
 namespace {
@@ -200,43 +201,68 @@ __global__ void __launch_bounds__(256) k_chunk_simt(const __grid_constant__ Simt
   }
 }
 
-// One warp per row of a joined tile: the parts' sums and outputs relative to the common maximum,
-// in the parts' order.
+// Joined rows: the partial sums and outputs relative to the common maximum, in the refs' order.
+// `team` warps of a CTA's eight take a row: each the partial results i = w mod team, whose sums
+// the first of them adds up.  Bound by the latency of the partial results' loads.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) k_chunk_join(const ChunkJoin* joins, const ChunkTile* tiles, const float* part,
-                                                   const float* part_ml, T* out, float* lse, int Hq, int Hkv, int G) {
+__global__ void __launch_bounds__(256) k_chunk_join(const ChunkJoin* joins, const ChunkRef* refs, const ChunkTile* tiles,
+                                                   const float* part, const float* part_ml, T* out, float* lse, int Hq,
+                                                   int Hkv, int G, int team) {
   constexpr int E = D / 32;
+  __shared__ float s_o[8][D];
+  __shared__ float s_l[8];
   const ChunkJoin jn = joins[blockIdx.x / Hkv];
-  const int g = blockIdx.x % Hkv, lane = threadIdx.x & 31;
+  const int g = blockIdx.x % Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % team;
   const ChunkTile t = tiles[jn.tile];
-  const int R = t.rows * G, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (r >= R) return;
-  const int64_t at = chunk_part(jn.part, Hkv, g, R, r), step = (int64_t)R * Hkv;
-  float m = -INFINITY;
-  for (int i = lane; i < jn.n_parts; i += 32) m = fmaxf(m, part_ml[2 * (at + i * step)]);
-#pragma unroll
-  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[E];
+  const int R = t.rows * G, r = blockIdx.y * (8 / team) + warp / team;
+  const bool live = r < R;
+  rows::wait_for_predecessor();
+  auto place = [&](int i) {
+    const ChunkRef f = refs[jn.ref0 + i];
+    return chunk_part(f.part, Hkv, g, f.R, f.off + r);
+  };
+  float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; e++) o[e] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < jn.n_parts; i++) {
-    const float2 ml = *reinterpret_cast<const float2*>(part_ml + 2 * (at + i * step));
-    const float f = ex2f(ml.x - base);
-    l = fmaf(ml.y, f, l);
-    const float* src = part + (at + i * step) * D + lane * E;
-    float x[E];
-    if (E == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      x[0] = v.x, x[1] = v.y, x[E - 2] = v.z, x[E - 1] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      x[0] = v.x, x[1] = v.y;
-    }
+  if (live) {
+    for (int i = lane; i < jn.n_refs; i += 32) m = fmaxf(m, part_ml[2 * place(i)]);
 #pragma unroll
-    for (int e = 0; e < E; e++) o[e] = fmaf(x[e], f, o[e]);
+    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+    for (int i = w; i < jn.n_refs; i += team) {
+      const int64_t at = place(i);
+      const float2 ml = *reinterpret_cast<const float2*>(part_ml + 2 * at);
+      const float f = ex2f(ml.x - base);
+      l = fmaf(ml.y, f, l);
+      const float* src = part + at * D + lane * E;
+      float x[E];
+      if (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        x[0] = v.x, x[1] = v.y, x[E - 2] = v.z, x[E - 1] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        x[0] = v.x, x[1] = v.y;
+      }
+#pragma unroll
+      for (int e = 0; e < E; e++) o[e] = fmaf(x[e], f, o[e]);
+    }
   }
+  if (team > 1) {
+    if (w) {
+#pragma unroll
+      for (int e = 0; e < E; e++) s_o[warp][lane * E + e] = o[e];
+      if (lane == 0) s_l[warp] = l;
+    }
+    __syncthreads();
+    if (w) return;
+    for (int k = 1; k < team; k++) {
+      l += s_l[warp + k];
+#pragma unroll
+      for (int e = 0; e < E; e++) o[e] += s_o[warp + k][lane * E + e];
+    }
+  }
+  if (!live) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const size_t row = (size_t)(t.row0 + r / G) * Hq + g * G + r % G;
 #pragma unroll
@@ -298,19 +324,29 @@ int chunk_join(const octo_plan_s* plan, const ChunkArgs& a, cudaStream_t s) {
   const ChunkPlan& c = *plan->chunk;
   const int64_t x = (int64_t)c.n_joins * d.n_kv_heads;
   if (x > INT32_MAX) return OCTO_EINVAL;
-  const dim3 grid((unsigned)x, (unsigned)((c.max_join_rows * c.G + 7) / 8));
+  // up to four partial results are one round of loads for a warp
+  const int team = c.max_refs <= 4 ? 1 : c.max_refs <= 8 ? 2 : c.max_refs <= 16 ? 4 : 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)x, (unsigned)((c.max_join_rows * c.G * team + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   auto go = [&](auto kernel, auto* out) {
-    kernel<<<grid, 256, 0, s>>>(c.joins, c.tiles, a.part, a.part_ml, out, a.lse, c.Hq, d.n_kv_heads, c.G);
+    return cudaLaunchKernelEx(&cfg, kernel, (const ChunkJoin*)c.joins, (const ChunkRef*)c.refs, (const ChunkTile*)c.tiles, (const float*)a.part,
+                              (const float*)a.part_ml, out, a.lse, (int)c.Hq, (int)d.n_kv_heads, (int)c.G, team);
   };
-  if (d.dtype == OCTO_DTYPE_F32) {
-    if (d.head_dim == 64) go(k_chunk_join<float, 64>, static_cast<float*>(a.out));
-    else go(k_chunk_join<float, 128>, static_cast<float*>(a.out));
-  } else {
-    if (d.head_dim == 64) go(k_chunk_join<__nv_bfloat16, 64>, static_cast<__nv_bfloat16*>(a.out));
-    else go(k_chunk_join<__nv_bfloat16, 128>, static_cast<__nv_bfloat16*>(a.out));
-  }
+  cudaError_t e;
+  if (d.dtype == OCTO_DTYPE_F32)
+    e = d.head_dim == 64 ? go(k_chunk_join<float, 64>, static_cast<float*>(a.out)) : go(k_chunk_join<float, 128>, static_cast<float*>(a.out));
+  else
+    e = d.head_dim == 64 ? go(k_chunk_join<__nv_bfloat16, 64>, static_cast<__nv_bfloat16*>(a.out))
+                         : go(k_chunk_join<__nv_bfloat16, 128>, static_cast<__nv_bfloat16*>(a.out));
   count_launch();
-  return cuda_status(cudaGetLastError());
+  return cuda_status(e);
 }
 
 }  // namespace octo

@@ -179,6 +179,48 @@ def test_mounts_inside_a_chunk(lib, oracle_mod, dtype):
         case.check([b], [n], window=12)
 
 
+def forest(P):
+    """Two prompts; forks of forks, one before its parent went on and one after, a rewound one, a parent with a mount that only its
+    later children see."""
+    ep = synth.Episode(P)
+    leaves = []
+    for n in (600, 1300):
+        r = ep.root()
+        ep.append(r, n)
+        kids = ep.fork(r, 3)
+        for i, k in enumerate(kids):
+            ep.append(k, 610 + 100 * i)
+        early = ep.fork(kids[0], 2)
+        ep.append(kids[0], 30)
+        ep.mount(kids[0], kids[2], 20, 640)
+        ep.append(kids[0], 9)
+        late = ep.fork(kids[0], 3)
+        for k in early + late + ep.fork(kids[1], 9):
+            ep.append(k, 3 + k % 5)
+            leaves.append(k)
+        cont = ep.rewind(kids[2], 600)
+        ep.append(cont, 4)
+        leaves.append(cont)
+    return ep, leaves
+
+
+@pytest.mark.parametrize("dtype,P,G", [("bf16", 64, 4), ("f32", 16, 2), ("bf16", 16, 16)])
+def test_shared_prefixes(lib, oracle_mod, dtype, P, G):
+    """What neighbouring cursors share is read for all of them: every order of the cursors, chunks that fill a tile among short ones."""
+    ep, leaves = forest(P)
+    case = Case(lib, oracle_mod, ep, G, 1, 64, dtype)
+    scale = 1 / 8
+    rng = np.random.default_rng(1)
+    for cursors in (leaves, leaves[::-1], [int(x) for x in rng.permutation(leaves)], leaves + leaves[:3] + [1, 1, 2, 0]):
+        n_new = [min(ep.length[c], 1 + c % 4) if c > 2 else (200, 3, 90)[c] for c in cursors]
+        n_new[3] = 0
+        plan, _, _, _ = case.check(cursors, n_new)
+        want = sum(len(case.plan.row_context(case.base[c] + i)[0]) for c, n in zip(cursors, n_new)
+                   for i in range(ep.length[c] - n, ep.length[c]))
+        assert plan.info["pairs"] == want
+        case.check(cursors, n_new, window=700, sink=9)
+
+
 def test_same_cursor_twice_and_empty_plans(lib, oracle_mod):
     ep, c = chain(64, 100, 40)
     case = Case(lib, oracle_mod, ep, 2, 2, 128, "bf16")
