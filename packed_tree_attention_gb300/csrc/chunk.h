@@ -34,21 +34,17 @@ struct ChunkTile {
   int32_t pad[2];
 };
 
-// Work of one CTA (and kv head): blocks [b0, b1) of a tile.  part < 0: all that its rows see,
-// the result is written; else partial results from row `part` on (rows * G of each kv head).
-struct ChunkItem {
-  int32_t tile, b0, b1;
-  int32_t part;
+// A piece of work: blocks [blk, blk + n) of kv head g for rows [row0, row0 + rows), which are as
+// the tile's that it is cut from.  part < 0: all that its rows see, the result is written; else
+// partial results from the part-th on (rows * G of them).
+struct ChunkWork {
+  int32_t row0, rows, t0, shift;
+  int32_t blk, n, g, part;
 };
 
-// Partial results of an item that a joined tile takes part in: from row `part` on, R of each kv
-// head, the tile's from the off-th on.
-struct ChunkRef {
-  int32_t part, R, off, pad;
-};
-// A tile whose rows have several partial results: refs [ref0, ref0 + n_refs).
+// A joined piece of rows of kv head g: partial results refs[ref0 .. + n_refs), the first row's.
 struct ChunkJoin {
-  int32_t tile, ref0, n_refs, pad;
+  int32_t row0, rows, g, ref0, n_refs;
 };
 
 struct ChunkPlan {
@@ -56,16 +52,17 @@ struct ChunkPlan {
   int32_t tokens = 0;                 // tokens of 128 rows (of G heads each); a tile has up to twice as many
   int32_t window = 0;                 // 0: none
   bool tc = false;                    // tcgen05 kernels
-  int32_t n_items = 0, n_joins = 0;
+  int32_t n_work = 0, n_joins = 0;
+  int32_t n_ctas = 0;                 // tcgen05 kernels: CTAs, each with a run of the work
   int32_t max_rows = 0;               // rows of the longest tile
   int32_t max_join_rows = 0;          // and of the longest joined one
   int32_t max_refs = 0;
-  int64_t part_rows = 0;              // rows of all partial results (of one kv head)
+  int64_t n_part = 0;                 // partial results
   ChunkBlock* blocks = nullptr;       // device arrays, the plan's
-  ChunkTile* tiles = nullptr;
-  ChunkItem* items = nullptr;         // largest first
+  ChunkWork* work = nullptr;          // CUDA-core kernels: longest first
+  int32_t* cta_work = nullptr;        // [n_ctas + 1]
   ChunkJoin* joins = nullptr;
-  ChunkRef* refs = nullptr;
+  int32_t* refs = nullptr;
   std::vector<int32_t> row0;          // [cursors + 1] first row of each (host)
 };
 
@@ -74,8 +71,8 @@ struct ChunkArgs {
   void* out;
   float* lse;        // may be NULL
   float scale;
-  float* part;       // partial results: [row][kv head of it] -> chunk_part()
-  float* part_ml;
+  float* part;       // partial results: O [n_part][head_dim]
+  float* part_ml;    // and (maximum, sum), in the log2 domain
 };
 
 bool chunk_tc_supported(const octo_pool_desc& d, int32_t width);
@@ -84,11 +81,6 @@ int chunk_simt(const octo_plan_s* p, const ChunkArgs& a, cudaStream_t s);
 int chunk_join(const octo_plan_s* p, const ChunkArgs& a, cudaStream_t s);
 
 #ifdef __CUDACC__
-// Row rr (token of the tile * G + head) of kv head g of a partial result of R rows that starts
-// at row `part`: index among all partial rows.
-__device__ __forceinline__ int64_t chunk_part(int32_t part, int32_t Hkv, int32_t g, int32_t R, int32_t rr) {
-  return (int64_t)part * Hkv + (int64_t)g * R + rr;
-}
 // Slots [lo, hi) of a block that the row at own index i sees; w0: its first visible position
 // (INT32_MIN: no window).
 __device__ __forceinline__ void chunk_range(const ChunkBlock& b, int32_t i, int32_t w0, bool windowed, int& lo, int& hi) {

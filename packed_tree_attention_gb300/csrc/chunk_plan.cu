@@ -8,7 +8,7 @@
 // cursors next to each other share, common ancestors up to the same point, is listed once for
 // all of them: their rows, next to each other too, make tiles of their own for it, so that the
 // prefix of a tree's branches is read once and not once a branch.  The tiles' block lists are
-// cut into items of about equal length.  The plan is built on the host: a step's plan serves
+// cut into pieces for the CTAs.  The plan is built on the host: a step's plan serves
 // every layer of a model, and its size is that of the contexts' page lists.
 
 #include <algorithm>
@@ -22,6 +22,14 @@
 
 namespace octo {
 namespace {
+
+// Rows [row0, row0 + rows) of the plan, and blocks that some of them sees.  Of one cursor: tokens
+// from own index t0 on, at positions own index + shift, no mount among them.  Or of several
+// cursors next to each other, with blocks of common ancestors, which all of them see (t0 = 0).
+struct ChunkTile {
+  int32_t row0, rows, t0, shift;
+  int32_t blk0, n_blk;
+};
 
 // Keys per block: 64 where pages make up 64 keys or are made up of them, so that a block is 64
 // rows of a tensor-core tile; else a page.
@@ -140,62 +148,157 @@ int64_t block_pairs(const ChunkBlock& k, const ChunkTile& t, int32_t window) {
   return n;
 }
 
-// Time of the longest-loaded of `sms` workers that take items of these lengths in turn.
-int64_t makespan(const std::vector<int32_t>& lens, int heads, int sms) {
-  std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> q;
-  for (int i = 0; i < sms; i++) q.push(0);
-  int64_t end = 0;
-  for (int32_t n : lens)
-    for (int h = 0; h < heads; h++) {
-      const int64_t t = q.top() + n;
-      q.pop();
-      q.push(t);
-      end = std::max(end, t);
-    }
-  return end;
-}
+// The cuts of a plan's tiles into work, in the order of the tiles and of the kv heads: of each
+// (tile, kv head) the pieces, in blocks, and who takes them.
+struct Cut {
+  int32_t n, cta;
+};
+using Cuts = std::vector<std::vector<Cut>>;
 
-// Blocks per item, an item costing its blocks and item_cost more (its start, its query tile, its
-// epilogue), and a plan with joined tiles kJoinCost: the length with the shortest makespan among
-// those that fill the `sms` places 1, 2, ... times.
-constexpr int kJoinCost = 4;
-int32_t pick_length(const std::vector<ChunkTile>& tiles, int heads, int sms, int item_cost) {
+// For the CUDA-core kernels, which give a piece a CTA: pieces of about `len` blocks, the length
+// with the shortest makespan among those that fill the SMs 1, 2, ... times; a piece costs
+// kPieceCost blocks more (its start, its queries, its results), a join kJoinCost once.
+constexpr int kPieceCost = 5, kJoinCost = 4;
+Cuts cut_evenly(const std::vector<ChunkTile>& tiles, int heads, int sms) {
   int32_t most = 1;
-  int64_t total = 0;
-  for (const ChunkTile& t : tiles) most = std::max(most, t.n_blk), total += t.n_blk;
-  int32_t best = most;
-  int64_t best_t = INT64_MAX;
-  std::vector<int32_t> lens;
+  for (const ChunkTile& t : tiles) most = std::max(most, t.n_blk);
   auto pieces = [&](int32_t len) {
     int64_t n = 0;
     for (const ChunkTile& t : tiles) n += (t.n_blk + len - 1) / len;
-    return n;
+    return n * heads;
   };
+  int32_t best = most;
+  int64_t best_t = INT64_MAX;
   auto consider = [&](int32_t len) {
-    lens.clear();
-    bool join = false;
-    for (const ChunkTile& t : tiles) {
-      const int32_t k = (t.n_blk + len - 1) / len;
-      join |= k > 1;
-      for (int32_t i = 0; i < k; i++) lens.push_back((t.n_blk - i + k - 1) / k + item_cost);
-    }
+    // longest first, each to the SM that is free first
+    std::vector<int32_t> lens;
+    for (const ChunkTile& t : tiles)
+      for (int32_t k = (t.n_blk + len - 1) / len, i = 0; i < k; i++) lens.push_back((t.n_blk - i + k - 1) / k + kPieceCost);
     std::sort(lens.begin(), lens.end(), std::greater<int32_t>());
-    const int64_t t = makespan(lens, heads, sms) + (join ? kJoinCost : 0);
-    if (t < best_t) best_t = t, best = len;
+    std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> q;
+    for (int i = 0; i < sms; i++) q.push(0);
+    int64_t end = 0;
+    for (int32_t l : lens)
+      for (int h = 0; h < heads; h++) {
+        const int64_t t = q.top() + l;
+        q.pop(), q.push(t);
+        end = std::max(end, t);
+      }
+    end += lens.size() > tiles.size() ? kJoinCost : 0;
+    if (end < best_t) best_t = end, best = len;
   };
-  if ((int64_t)tiles.size() * heads > 24LL * sms) return most;   // many waves: nothing to gain
-  consider(most);
-  for (int w = 1; w <= 6; w++) {
-    // the shortest items of which w waves are enough
-    int32_t lo = 1, hi = most;
-    while (lo < hi) {
-      const int32_t mid = lo + (hi - lo) / 2;
-      if (pieces(mid) * heads <= (int64_t)w * sms) hi = mid;
-      else lo = mid + 1;
+  if (pieces(most) <= 24LL * sms) {   // else many waves: nothing to gain
+    consider(most);
+    for (int w = 1; w <= 6; w++) {
+      // the shortest pieces of which w waves are enough
+      int32_t lo = 1, hi = most;
+      while (lo < hi) {
+        const int32_t mid = lo + (hi - lo) / 2;
+        if (pieces(mid) <= (int64_t)w * sms) hi = mid;
+        else lo = mid + 1;
+      }
+      if (pieces(lo) <= (int64_t)w * sms) consider(lo);
     }
-    if (pieces(lo) * heads <= (int64_t)w * sms) consider(lo);
   }
-  return best;
+  Cuts cuts;
+  for (const ChunkTile& t : tiles) {
+    const int32_t k = std::max(1, (t.n_blk + best - 1) / best);
+    std::vector<Cut> c;
+    for (int32_t i = 0; i < k; i++) c.push_back({(t.n_blk + i) / k, 0});
+    cuts.insert(cuts.end(), heads, c);
+  }
+  return cuts;
+}
+
+// CTAs of a tensor-core kernel, each of which takes several pieces: one an SM, but no more than
+// have kLeast blocks each (joining shorter pieces takes longer than they save).  A piece costs
+// `change` blocks more.
+constexpr int kLeast = 3;
+int cta_count(const std::vector<ChunkTile>& tiles, int heads, int sms, double change, double* total) {
+  *total = 0;
+  for (const ChunkTile& t : tiles) *total += heads * (t.n_blk + change);
+  return (int)std::max(1.0, std::min((double)sms, *total / (kLeast + change)));
+}
+
+// One slot: all work in a row, cut into runs of equal cost, so that all CTAs end together.
+constexpr double kStreamChange = 1.0;
+Cuts cut_into_runs(const std::vector<ChunkTile>& tiles, int heads, int sms) {
+  double total = 0;
+  const int ctas = cta_count(tiles, heads, sms, kStreamChange, &total);
+  const double budget = (total + (ctas - 1) * kStreamChange) / ctas;   // a run's end cuts a tile: a piece more
+  Cuts cuts;
+  double at = 0;   // cost so far
+  int32_t cta = 0, pieces = 0;
+  for (const ChunkTile& t : tiles)
+    for (int h = 0; h < heads; h++) {
+      cuts.emplace_back();
+      for (int32_t left = t.n_blk; left > 0;) {
+        // what the CTA at hand has room for; a remainder of a block or two stays with it
+        const double room = (cta + 1) * budget - at - kStreamChange;
+        const bool last = cta + 1 == ctas;
+        if (!last && room < 0.5 && pieces > 0) {
+          cta++, pieces = 0;
+          continue;
+        }
+        const int32_t take = last || room >= left - 2 ? left : std::max(1, (int32_t)(room + 0.5));
+        cuts.back().push_back({take, cta});
+        left -= take;
+        pieces++;
+        at += take + kStreamChange;
+      }
+    }
+  return cuts;
+}
+
+// Two slots: a tile's partial result is up to 128 KB, so tiles go whole, longest first, to the
+// CTA with the least work, as long as that does not pass the average; what is left is cut to
+// fill the CTAs up.  (512 tiles of 35 blocks on 152 CTAs: three whole ones each, 56 cut.)
+constexpr double kPairChange = 7.0, kPartChange = 9.0;   // pieces cost 6 us more than their blocks of 0.83 us
+Cuts cut_what_is_left(const std::vector<ChunkTile>& tiles, int heads, int sms) {
+  double total = 0;
+  const int ctas = cta_count(tiles, heads, sms, kPairChange, &total);
+  Cuts cuts(tiles.size() * heads);
+  std::vector<int32_t> order(cuts.size()), left;
+  for (size_t i = 0; i < order.size(); i++) order[i] = (int32_t)i;
+  auto blocks = [&](int32_t i) { return tiles[i / heads].n_blk; };
+  std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return blocks(x) > blocks(y); });
+  std::vector<double> load(ctas, 0);
+  using Item = std::pair<double, int32_t>;
+  std::priority_queue<Item, std::vector<Item>, std::greater<Item>> q;
+  for (int32_t c = 0; c < ctas; c++) q.push({0.0, c});
+  for (int32_t i : order) {
+    const Item c = q.top();
+    const double t = c.first + blocks(i) + kPairChange;
+    if (t > total / ctas + 1) {
+      left.push_back(i);
+      continue;
+    }
+    q.pop(), q.push({t, c.second});
+    load[c.second] = t;
+    cuts[i].push_back({blocks(i), c.second});
+  }
+  if (left.empty()) return cuts;
+  // the level up to which the CTAs are filled: each takes a piece, and one more where a tile ends in it
+  double rest = 0;
+  for (int32_t i : left) rest += blocks(i) + kPartChange;
+  double lo = 0, hi = total + kPartChange;
+  for (int k = 0; k < 40; k++) {
+    const double mid = (lo + hi) / 2;
+    double room = 0;
+    for (double l : load) room += std::max(0.0, mid - l - kPartChange);
+    (room >= rest ? hi : lo) = mid;
+  }
+  int32_t c = 0;
+  for (int32_t i : left)
+    for (int32_t n = blocks(i); n > 0;) {
+      while (c + 1 < ctas && hi - load[c] - kPartChange < 1.0) c++;
+      const double room = hi - load[c] - kPartChange;
+      const int32_t take = c + 1 == ctas || room >= n - 2 ? n : std::max(1, (int32_t)(room + 0.5));
+      cuts[i].push_back({take, c});
+      n -= take;
+      load[c] += take + kPartChange;
+    }
+  return cuts;
 }
 
 template <typename T>
@@ -360,46 +463,63 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
     if (blocks.size() > (size_t)INT32_MAX / 2) return OCTO_EINVAL;
   }
 
-  // items, in pieces of the tiles' blocks; the joins of what has several
-  const int sms = std::max(1, rows::sm_count());
+  // the work, in pieces of the tiles' blocks, and the joins of what has several
+  const int sms = std::max(1, rows::sm_count()), heads = d.n_kv_heads;
   for (const ChunkTile& t : tiles) cp->max_rows = std::max(cp->max_rows, t.rows);
-  const bool paired = cp->tc && cp->max_rows <= cp->tokens;   // two CTAs an SM
-  const int32_t len = pick_length(tiles, d.n_kv_heads, paired ? 2 * sms : sms, paired ? 3 : 5);
-  std::vector<ChunkItem> items;
+  std::vector<int32_t> cta_work, refs;
+  const Cuts cuts = !cp->tc ? cut_evenly(tiles, heads, sms)
+                    : cp->max_rows > cp->tokens ? cut_what_is_left(tiles, heads, sms) : cut_into_runs(tiles, heads, sms);
+  std::vector<ChunkWork> work;
+  std::vector<int32_t> cta_of;   // of each piece
   std::vector<ChunkJoin> joins;
-  std::vector<ChunkRef> refs;
-  std::vector<std::pair<size_t, size_t>> items_of(tiles.size());   // [first, end) of each tile's
+  std::vector<std::pair<size_t, size_t>> work_of(cuts.size());   // [first, end) of each (tile, kv head)'s
   int32_t longest = 0;
   for (size_t i = 0; i < tiles.size(); i++) {
     const ChunkTile& t = tiles[i];
     longest = std::max(longest, t.n_blk);
-    const int32_t k = std::max(1, (t.n_blk + len - 1) / len);
-    const bool partial = k > 1 || i < n_shared || !path_of[i - n_shared]->shared.empty();
-    items_of[i].first = items.size();
-    for (int32_t j = 0, at = 0; j < k; j++) {
-      const int32_t e = at + (t.n_blk - at) / (k - j);
-      items.push_back({(int32_t)i, at, e, partial ? (int32_t)cp->part_rows : -1});
-      at = e;
-      if (partial) cp->part_rows += (int64_t)t.rows * cp->G;
-      if (cp->part_rows > INT32_MAX) return OCTO_EINVAL;
+    for (int32_t g = 0; g < heads; g++) {
+      const std::vector<Cut>& cut = cuts[i * heads + g];
+      const bool partial = cut.size() > 1 || i < n_shared || !path_of[i - n_shared]->shared.empty();
+      work_of[i * heads + g] = {work.size(), work.size() + cut.size()};
+      for (int32_t at = t.blk0, k = 0; k < (int32_t)cut.size(); at += cut[k++].n) {
+        work.push_back({t.row0, t.rows, t.t0, t.shift, at, cut[k].n, g, partial ? (int32_t)cp->n_part : -1});
+        cta_of.push_back(cut[k].cta);
+        if (partial) cp->n_part += (int64_t)t.rows * cp->G;
+        if (cp->n_part > INT32_MAX) return OCTO_EINVAL;
+      }
+      if (i < n_shared || !partial) continue;
+      const int32_t ref0 = (int32_t)refs.size();
+      auto add = [&](size_t tile) {
+        const auto& w = work_of[tile * heads + g];
+        for (size_t x = w.first; x < w.second; x++) refs.push_back(work[x].part + (t.row0 - tiles[tile].row0) * cp->G);
+      };
+      for (int32_t x : path_of[i - n_shared]->shared) add(x);
+      add(i);
+      const int32_t n_refs = (int32_t)refs.size() - ref0;
+      joins.push_back({t.row0, t.rows, g, ref0, n_refs});
+      cp->max_join_rows = std::max(cp->max_join_rows, t.rows);
+      cp->max_refs = std::max(cp->max_refs, n_refs);
     }
-    items_of[i].second = items.size();
-    if (i < n_shared || !partial) continue;
-    const int32_t ref0 = (int32_t)refs.size();
-    auto add = [&](size_t tile) {
-      for (size_t x = items_of[tile].first; x < items_of[tile].second; x++)
-        refs.push_back({items[x].part, tiles[tile].rows * cp->G, (t.row0 - tiles[tile].row0) * cp->G, 0});
-    };
-    for (int32_t x : path_of[i - n_shared]->shared) add(x);
-    add(i);
-    const int32_t n_refs = (int32_t)refs.size() - ref0;
-    joins.push_back({(int32_t)i, ref0, n_refs, 0});
-    cp->max_join_rows = std::max(cp->max_join_rows, t.rows);
-    cp->max_refs = std::max(cp->max_refs, n_refs);
   }
-  std::stable_sort(items.begin(), items.end(), [](const ChunkItem& x, const ChunkItem& y) { return x.b1 - x.b0 > y.b1 - y.b0; });
-  cp->n_items = (int32_t)items.size();
+  if (cp->tc) {
+    // by CTA
+    cta_work.assign(1, 0);
+    for (int32_t c : cta_of) {
+      if ((size_t)c + 2 > cta_work.size()) cta_work.resize(c + 2, 0);
+      cta_work[c + 1]++;
+    }
+    for (size_t c = 1; c < cta_work.size(); c++) cta_work[c] += cta_work[c - 1];
+    std::vector<ChunkWork> sorted(work.size());
+    std::vector<int32_t> next(cta_work);
+    for (size_t i = 0; i < work.size(); i++) sorted[next[cta_of[i]]++] = work[i];
+    work.swap(sorted);
+  } else {
+    std::stable_sort(work.begin(), work.end(), [](const ChunkWork& x, const ChunkWork& y) { return x.n > y.n; });
+  }
+  if (work.size() > (size_t)INT32_MAX || joins.size() > (size_t)INT32_MAX) return OCTO_EINVAL;
+  cp->n_work = (int32_t)work.size();
   cp->n_joins = (int32_t)joins.size();
+  cp->n_ctas = cp->tc ? (int32_t)cta_work.size() - 1 : 0;
 
   // what octo_plan_copy_out gives of a chunk plan: its cursors, rows, positions and tiles
   std::vector<int32_t> order(cursors, cursors + n), t_seg, t_t0, t_rows, none(std::max((size_t)d.num_pages, tiles.size()) + 1, 0);
@@ -410,7 +530,7 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
 
   // device arrays: one allocation, one copy
   size_t at = 0;
-  const size_t o_blk = place(&at, blocks), o_tile = place(&at, tiles), o_item = place(&at, items), o_join = place(&at, joins), o_ref = place(&at, refs),
+  const size_t o_blk = place(&at, blocks), o_work = place(&at, work), o_cta = place(&at, cta_work), o_join = place(&at, joins), o_ref = place(&at, refs),
                o_pos = place(&at, row_pos), o_row0 = place(&at, cp->row0),
                o_order = place(&at, order), o_seg = place(&at, t_seg), o_t0 = place(&at, t_t0), o_rows = place(&at, t_rows),
                o_none = place(&at, none);
@@ -418,7 +538,7 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
   auto put = [&](size_t o, const auto& v) {
     if (!v.empty()) std::memcpy(stage.data() + o, v.data(), v.size() * sizeof(v[0]));
   };
-  put(o_blk, blocks), put(o_tile, tiles), put(o_item, items), put(o_join, joins), put(o_ref, refs), put(o_pos, row_pos), put(o_row0, cp->row0);
+  put(o_blk, blocks), put(o_work, work), put(o_cta, cta_work), put(o_join, joins), put(o_ref, refs), put(o_pos, row_pos), put(o_row0, cp->row0);
   put(o_order, order), put(o_seg, t_seg), put(o_t0, t_t0), put(o_rows, t_rows), put(o_none, none);
   if (int st = ensure_status(pool)) return st;
   OCTO_CUDA(cudaGetDevice(&pl->device));
@@ -430,10 +550,10 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
   pl->allocs.push_back(buf);
   char* base = static_cast<char*>(buf);
   cp->blocks = reinterpret_cast<ChunkBlock*>(base + o_blk);
-  cp->tiles = reinterpret_cast<ChunkTile*>(base + o_tile);
-  cp->items = reinterpret_cast<ChunkItem*>(base + o_item);
+  cp->work = reinterpret_cast<ChunkWork*>(base + o_work);
+  cp->cta_work = reinterpret_cast<int32_t*>(base + o_cta);
   cp->joins = reinterpret_cast<ChunkJoin*>(base + o_join);
-  cp->refs = reinterpret_cast<ChunkRef*>(base + o_ref);
+  cp->refs = reinterpret_cast<int32_t*>(base + o_ref);
   pl->row_pos = reinterpret_cast<int32_t*>(base + o_pos);
   pl->seg_row_base = reinterpret_cast<int32_t*>(base + o_row0);
   pl->seg_order = reinterpret_cast<int32_t*>(base + o_order);
@@ -463,7 +583,7 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
 }
 
 size_t part_floats(const octo_plan_s* p) {
-  return (size_t)p->chunk->part_rows * p->pool->desc.n_kv_heads * p->pool->desc.head_dim;
+  return (size_t)p->chunk->n_part * p->pool->desc.head_dim;
 }
 
 }  // namespace
@@ -492,7 +612,7 @@ int octo_chunk_plan(octo_pool_t pool, const octo_cursor_t* cursors, const int32_
 
 size_t octo_chunk_attn_workspace_size(octo_plan_t plan) {
   if (!plan || !plan->chunk) return 0;
-  const size_t rows = (size_t)plan->chunk->part_rows * plan->pool->desc.n_kv_heads;
+  const size_t rows = (size_t)plan->chunk->n_part;
   return rows ? octo::align_up(octo::part_floats(plan) * sizeof(float), 256) + rows * 2 * sizeof(float) : 0;
 }
 

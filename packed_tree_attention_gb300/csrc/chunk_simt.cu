@@ -26,8 +26,7 @@ __device__ __forceinline__ float ex2f(float x) {
 
 struct SimtParams {
   const ChunkBlock* blocks;
-  const ChunkTile* tiles;
-  const ChunkItem* items;
+  const ChunkWork* work;
   const void *q, *k, *v;
   void* out;
   float *lse, *part, *part_ml;
@@ -63,9 +62,8 @@ __global__ void __launch_bounds__(256) k_chunk_simt(const __grid_constant__ Simt
   float* sp = sv + kKeys * D;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int sub = blockIdx.x % p.n_sub;
-  const int g = blockIdx.x / p.n_sub % p.Hkv;
-  const ChunkItem it = p.items[blockIdx.x / p.n_sub / p.Hkv];
-  const ChunkTile t = p.tiles[it.tile];
+  const ChunkWork t = p.work[blockIdx.x / p.n_sub];
+  const int g = t.g;
   const int R = t.rows * p.G, r0 = sub * M;
   if (r0 >= R) return;
   const T* q = static_cast<const T*>(p.q);
@@ -89,8 +87,8 @@ __global__ void __launch_bounds__(256) k_chunk_simt(const __grid_constant__ Simt
     for (int c = 0; c < C; c++) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const int first = t.t0 + r0 / p.G, last = t.t0 + (min(r0 + M, R) - 1) / p.G;
-  for (int b = it.b0; b < it.b1; b++) {
-    const ChunkBlock k = p.blocks[t.blk0 + b];
+  for (int b = 0; b < t.n; b++) {
+    const ChunkBlock k = p.blocks[t.blk + b];
     int lo, hi, unused;   // what some row of the CTA sees
     chunk_range(k, first, first + t.shift - p.window + 1, p.window > 0, lo, unused);
     chunk_range(k, last, 0, false, unused, hi);
@@ -184,8 +182,8 @@ __global__ void __launch_bounds__(256) k_chunk_simt(const __grid_constant__ Simt
 #pragma unroll
     for (int w = 8; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
     if (r >= R) continue;
-    if (it.part >= 0) {
-      const int64_t at = chunk_part(it.part, p.Hkv, g, R, r);
+    if (t.part >= 0) {
+      const int64_t at = (int64_t)t.part + r;
 #pragma unroll
       for (int c = 0; c < C; c++) *reinterpret_cast<float4*>(p.part + at * D + 64 * c + 4 * tx) = o[i][c];
       if (tx == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m[i], sum);
@@ -205,22 +203,18 @@ __global__ void __launch_bounds__(256) k_chunk_simt(const __grid_constant__ Simt
 // `team` warps of a CTA's eight take a row: each the partial results i = w mod team, whose sums
 // the first of them adds up.  Bound by the latency of the partial results' loads.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) k_chunk_join(const ChunkJoin* joins, const ChunkRef* refs, const ChunkTile* tiles,
-                                                   const float* part, const float* part_ml, T* out, float* lse, int Hq,
-                                                   int Hkv, int G, int team) {
+__global__ void __launch_bounds__(256) k_chunk_join(const ChunkJoin* joins, const int32_t* refs, const float* part,
+                                                   const float* part_ml, T* out, float* lse, int Hq, int G, int team) {
   constexpr int E = D / 32;
   __shared__ float s_o[8][D];
   __shared__ float s_l[8];
-  const ChunkJoin jn = joins[blockIdx.x / Hkv];
-  const int g = blockIdx.x % Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % team;
-  const ChunkTile t = tiles[jn.tile];
-  const int R = t.rows * G, r = blockIdx.y * (8 / team) + warp / team;
+  const ChunkJoin jn = joins[blockIdx.x];
+  const int g = jn.g, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % team;
+  const int R = jn.rows * G, r = blockIdx.y * (8 / team) + warp / team;
   const bool live = r < R;
+  rows::launch_dependents();
   rows::wait_for_predecessor();
-  auto place = [&](int i) {
-    const ChunkRef f = refs[jn.ref0 + i];
-    return chunk_part(f.part, Hkv, g, f.R, f.off + r);
-  };
+  auto place = [&](int i) { return (int64_t)refs[jn.ref0 + i] + r; };
   float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; e++) o[e] = 0.f;
@@ -264,7 +258,7 @@ __global__ void __launch_bounds__(256) k_chunk_join(const ChunkJoin* joins, cons
   }
   if (!live) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  const size_t row = (size_t)(t.row0 + r / G) * Hq + g * G + r % G;
+  const size_t row = (size_t)(jn.row0 + r / G) * Hq + g * G + r % G;
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
     T* dst = out + row * D + lane * E + e;
@@ -291,7 +285,7 @@ int run(SimtParams p, const octo_plan_s* plan, cudaStream_t s) {
   const int R = plan->chunk->max_rows * p.G;
   const int rm = R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8;
   p.n_sub = (R + 16 * rm - 1) / (16 * rm);
-  const int64_t ctas = (int64_t)plan->chunk->n_items * p.Hkv * p.n_sub;
+  const int64_t ctas = (int64_t)plan->chunk->n_work * p.n_sub;
   if (ctas > INT32_MAX) return OCTO_EINVAL;
   switch (rm) {
     case 1: return launch<T, D, 1>(p, ctas, s);
@@ -307,7 +301,7 @@ int chunk_simt(const octo_plan_s* plan, const ChunkArgs& a, cudaStream_t s) {
   const octo_pool_desc& d = plan->pool->desc;
   const ChunkPlan& c = *plan->chunk;
   SimtParams p;
-  p.blocks = c.blocks, p.tiles = c.tiles, p.items = c.items;
+  p.blocks = c.blocks, p.work = c.work;
   p.q = a.q, p.k = a.k, p.v = a.v, p.out = a.out, p.lse = a.lse, p.part = a.part, p.part_ml = a.part_ml;
   p.Hq = c.Hq, p.Hkv = d.n_kv_heads, p.G = c.G, p.P = d.page_size, p.width = c.width;
   p.span = d.page_size < c.width ? d.page_size : c.width;
@@ -322,12 +316,10 @@ int chunk_simt(const octo_plan_s* plan, const ChunkArgs& a, cudaStream_t s) {
 int chunk_join(const octo_plan_s* plan, const ChunkArgs& a, cudaStream_t s) {
   const octo_pool_desc& d = plan->pool->desc;
   const ChunkPlan& c = *plan->chunk;
-  const int64_t x = (int64_t)c.n_joins * d.n_kv_heads;
-  if (x > INT32_MAX) return OCTO_EINVAL;
   // up to four partial results are one round of loads for a warp
   const int team = c.max_refs <= 4 ? 1 : c.max_refs <= 8 ? 2 : c.max_refs <= 16 ? 4 : 8;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)x, (unsigned)((c.max_join_rows * c.G * team + 7) / 8));
+  cfg.gridDim = dim3((unsigned)c.n_joins, (unsigned)((c.max_join_rows * c.G * team + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -336,8 +328,8 @@ int chunk_join(const octo_plan_s* plan, const ChunkArgs& a, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   auto go = [&](auto kernel, auto* out) {
-    return cudaLaunchKernelEx(&cfg, kernel, (const ChunkJoin*)c.joins, (const ChunkRef*)c.refs, (const ChunkTile*)c.tiles, (const float*)a.part,
-                              (const float*)a.part_ml, out, a.lse, (int)c.Hq, (int)d.n_kv_heads, (int)c.G, team);
+    return cudaLaunchKernelEx(&cfg, kernel, (const ChunkJoin*)c.joins, (const int32_t*)c.refs, (const float*)a.part,
+                              (const float*)a.part_ml, out, a.lse, (int)c.Hq, (int)c.G, team);
   };
   cudaError_t e;
   if (d.dtype == OCTO_DTYPE_F32)

@@ -111,6 +111,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_
 // Launched so that its start overlaps the end of the kernel before it, a kernel waits here before
 // it touches global memory.
 __device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the kernel after it, if that waits so, be launched once every CTA has come here.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---- clusters ----
 __device__ __forceinline__ uint32_t cluster_rank() {
