@@ -591,8 +591,8 @@ int octo_verify_drafts_workspace_size(octo_plan_t plan, int32_t cur0, int32_t n_
  * (optional: ln p of next_id), accept_p float over all rows of the plan (optional: a_r of the
  * drafts up to and including the first rejected one, 0 in these cursors' other rows).  A cursor
  * without rows has n_accept 0, next_id -1 and next_logp -inf, and so has one with no token
- * left to draw, besides its accepted ones.  Ids outside [0, vocab) are rejected and give OCTO_EINVAL at the
- * next octo_sync.  The same results on every run.  Async on stream. */
+ * left to draw, besides its accepted ones.  An id outside [0, vocab) is rejected and, as
+ * the first rejected one, gives OCTO_EINVAL at the next octo_sync.  The same results on every run.  Async on stream. */
 int octo_verify_drafts(octo_plan_t plan, int32_t cur0, int32_t n_cur, const void* logits, int32_t dtype,
                        int64_t ld, int32_t vocab, float inv_temp, const int32_t* ids,
                        const void* draft_logits, int64_t draft_ld, float draft_inv_temp, const float* u,

@@ -438,7 +438,7 @@ class Pool:
         _chk(self._L.octo_chunk_plan(self.h, _ip(c), _ip(m), len(c), n_q_heads, window, n_sink, _stream(stream),
                                      ctypes.byref(h)), "octo_chunk_plan")
         plan = Plan(self, h)
-        plan.n_q_heads, plan.cursor_rows = n_q_heads, m.copy()
+        plan.n_q_heads, plan.cursor_row0 = n_q_heads, [0] + np.cumsum(m, dtype=np.int64).tolist()
         return plan
 
 
@@ -536,8 +536,8 @@ class Plan:
         plan the target accepts, and each one's next token; sampled with u over the plan's rows and
         noise [n_cur][ld] of Exp(1) variates, greedy without them."""
         dev = _device()
-        rows = getattr(self, "cursor_rows", ())
-        n = int(rows[cur0:cur0 + n_cur].sum()) if 0 <= cur0 and n_cur >= 0 and cur0 + n_cur <= len(rows) else 0
+        row0 = getattr(self, "cursor_row0", ())
+        n = row0[cur0 + n_cur] - row0[cur0] if 0 <= cur0 <= cur0 + n_cur < len(row0) else 0
         x, dt, ld = _logits(logits, n, vocab, dev)
         y, yld = None, ld
         if draft_logits is not None:

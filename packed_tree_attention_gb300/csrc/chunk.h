@@ -63,7 +63,9 @@ struct ChunkPlan {
   int32_t* cta_work = nullptr;        // [n_ctas + 1]
   ChunkJoin* joins = nullptr;
   int32_t* refs = nullptr;
-  std::vector<int32_t> row0;          // [cursors + 1] first row of each (host)
+  int32_t* drafted = nullptr;         // rows but the cursors' last ones
+  int32_t* d_live = nullptr;          // [cursors + 1] cursors with rows before each
+  std::vector<int32_t> row0, live;    // [cursors + 1] first row of each, d_live (host)
 };
 
 struct ChunkArgs {

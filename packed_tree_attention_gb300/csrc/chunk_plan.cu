@@ -528,18 +528,26 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
     t_t0.push_back(tiles[i].t0), t_rows.push_back(tiles[i].rows);
   }
 
+  // what the verification of drafted tokens goes by
+  std::vector<int32_t> drafted;
+  cp->live.assign((size_t)n + 1, 0);
+  for (int32_t c = 0; c < n; c++) {
+    cp->live[c + 1] = cp->live[c] + (n_new[c] > 0);
+    for (int32_t r = cp->row0[c]; r + 1 < cp->row0[c + 1]; r++) drafted.push_back(r);
+  }
+
   // device arrays: one allocation, one copy
   size_t at = 0;
   const size_t o_blk = place(&at, blocks), o_work = place(&at, work), o_cta = place(&at, cta_work), o_join = place(&at, joins), o_ref = place(&at, refs),
                o_pos = place(&at, row_pos), o_row0 = place(&at, cp->row0),
                o_order = place(&at, order), o_seg = place(&at, t_seg), o_t0 = place(&at, t_t0), o_rows = place(&at, t_rows),
-               o_none = place(&at, none);
+               o_none = place(&at, none), o_drafted = place(&at, drafted), o_live = place(&at, cp->live);
   std::vector<char> stage(std::max<size_t>(at, 256));
   auto put = [&](size_t o, const auto& v) {
     if (!v.empty()) std::memcpy(stage.data() + o, v.data(), v.size() * sizeof(v[0]));
   };
   put(o_blk, blocks), put(o_work, work), put(o_cta, cta_work), put(o_join, joins), put(o_ref, refs), put(o_pos, row_pos), put(o_row0, cp->row0);
-  put(o_order, order), put(o_seg, t_seg), put(o_t0, t_t0), put(o_rows, t_rows), put(o_none, none);
+  put(o_order, order), put(o_seg, t_seg), put(o_t0, t_t0), put(o_rows, t_rows), put(o_none, none), put(o_drafted, drafted), put(o_live, cp->live);
   if (int st = ensure_status(pool)) return st;
   OCTO_CUDA(cudaGetDevice(&pl->device));
   pl->pool = pool;
@@ -554,6 +562,8 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
   cp->cta_work = reinterpret_cast<int32_t*>(base + o_cta);
   cp->joins = reinterpret_cast<ChunkJoin*>(base + o_join);
   cp->refs = reinterpret_cast<int32_t*>(base + o_ref);
+  cp->drafted = reinterpret_cast<int32_t*>(base + o_drafted);
+  cp->d_live = reinterpret_cast<int32_t*>(base + o_live);
   pl->row_pos = reinterpret_cast<int32_t*>(base + o_pos);
   pl->seg_row_base = reinterpret_cast<int32_t*>(base + o_row0);
   pl->seg_order = reinterpret_cast<int32_t*>(base + o_order);

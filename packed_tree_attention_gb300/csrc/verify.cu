@@ -17,170 +17,491 @@ namespace {
 
 using namespace rows;
 
-constexpr int kStatThreads = 512;
-constexpr int kPickThreads = 1024;
+constexpr int kThreads = 512;
+constexpr int kHeld = 2;              // CTAs of 512 threads that an SM holds
+constexpr int kChunk = kPer * kThreads;   // vectors that a CTA takes at once, at most
+constexpr int kDecide = 256;          // threads of a cursor's decision
+
+// What is decided about a cursor: accepted drafts, the row (of the logits given) of the next
+// token's distribution with its statistics, and what a rejected draft takes off it: the draft's
+// distribution of that row (y_row >= 0) or one id (out >= 0).
+struct Decision {
+  int32_t acc, row, y_row, out;
+  float2 st, y_st;
+};
 
 struct VerifyParams {
   const void *x, *y;          // target's and draft's logits
   int64_t ld, yld, eld;
   int32_t V;
   float c, cy;                // inverse temperatures
+  float hi[2], lo[2];         // c log2 e and cy log2 e in two parts
   const int32_t* row0;        // [cursors + 1] first row of the plan's cursors, from cur0 on
-  int32_t first;              // row0[0]
+  const int32_t* live;        // [cursors + 1] cursors with rows before each, from cur0 on
+  const int32_t* drafted;     // rows of the plan that lead to a draft, from the first of these on
+  int32_t first, live0;       // row0[0], live[0]
   const int32_t* ids;
   const float *u, *noise;
   int32_t *n_accept, *next_id;
   float *next_logp, *accept_p;
-  float2* stat;               // [2][rows] (m, ln S) of the target's and the draft's rows
-  unsigned long long* best;   // [rows] greedy: order_key of the largest logit, ~id
-  int32_t n_rows;
+  float2* stat;               // [n_rows + n_drafted][slots] (m, S) of the target's and the draft's rows
+  unsigned long long* best;   // [n_rows][slots] greedy: order_key of the largest logit, ~id
+  Decision* decision;         // [n_cur]
+  unsigned long long* drawn;  // [n_cur] best score
+  int32_t* done;              // [n_cur] CTAs that are through with the cursor's draw
+  int32_t n_rows, n_drafted, n_cur;
+  int32_t per_row, per_chunk, slots, ctas;   // chunks of a row, vectors of a chunk
+  int32_t draw_chunk, draw_per_row, draw_ctas;   // vectors of a chunk of the draw, chunks of a row
   int32_t* status;
+
+  // CTA b of the statistics takes chunks [b C / ctas, (b + 1) C / ctas) of all rows' C; the one
+  // that has chunk x:
+  __host__ __device__ int64_t chunks() const { return (int64_t)(n_rows + n_drafted) * per_row; }
+  __device__ int64_t start(int b) const { return b * chunks() / ctas; }
+  __device__ int owner(int64_t x) const {
+    const int64_t a = (x + 1) * ctas - 1, c = chunks();
+    return a >> 32 ? (int)(a / c) : (int)((uint32_t)a / (uint32_t)c);   // a 64-bit division takes ten times as long
+  }
 };
 
 __device__ __forceinline__ unsigned long long lowest_first(uint32_t key, int v) {
   return (unsigned long long)key << 32 | (0xffffffffu - (uint32_t)v);
 }
 __device__ __forceinline__ int id_of(unsigned long long k) { return (int)(0xffffffffu - (uint32_t)k); }
-
-template <typename T, bool kGreedy>
-__global__ void __launch_bounds__(kStatThreads) k_verify_stats(const __grid_constant__ VerifyParams p) {
-  constexpr int E = Vec<T>::E;
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool draft = blockIdx.y;
-  const T* x = draft ? static_cast<const T*>(p.y) + r * p.yld : static_cast<const T*>(p.x) + r * p.ld;
-  const float c2 = (draft ? p.cy : p.c) * kLog2e;
-  Stat st;
-  st.init();
-  unsigned long long best = 0;
-  auto one = [&](float v, int i) {
-    st.add(v, c2);
-    if (kGreedy) {
-      const uint32_t k = order_key(v);
-      if (k > (uint32_t)(best >> 32)) best = lowest_first(k, i);
-    }
-  };
-  for (int i = tid; i < p.V / E; i += kStatThreads) {
-    float v[E];
-    Vec<T>::cvt(reinterpret_cast<const uint4*>(x)[i], v);
-    float mx = v[0];
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 #pragma unroll
-    for (int e = 1; e < E; e++) mx = fmaxf(mx, v[e]);
-    if (mx > st.m) st.rebase(mx, c2);
-#pragma unroll
-    for (int e = 0; e < E; e++) one(v[e], i * E + e);
-  }
-  for (int i = p.V / E * E + tid; i < p.V; i += kStatThreads) {
-    const float v = Vec<T>::get(x + i);
-    if (v > st.m) st.rebase(v, c2);
-    one(v, i);
-  }
-  __shared__ Stat part[kStatThreads / 32];
-  __shared__ unsigned long long top[kStatThreads / 32];
-  warp_merge(st, c2);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-  if (lane == 0) part[warp] = st, top[warp] = best;
-  __syncthreads();
-  if (tid) return;
-  for (int w = 1; w < kStatThreads / 32; w++) st.merge(part[w].m, part[w].s, part[w].a, c2), best = max(best, top[w]);
-  // every logit -inf: the largest stayed at the start's reference, far below, and nothing summed
-  const bool none = st.s == 0.f;
-  p.stat[draft * p.n_rows + r] = make_float2(none ? -INFINITY : st.m, none ? -INFINITY : logf(st.s));
-  if (kGreedy) p.best[r] = best;
+  for (int o = 16; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
+// largest entry of a vector, NaNs left out
+__device__ __forceinline__ float vec_max(const uint4& w, __nv_bfloat16) {
+  auto b = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
+  const __nv_bfloat162 m = __hmax2(__hmax2(b(w.x), b(w.y)), __hmax2(b(w.z), b(w.w)));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float vec_max(const uint4& w, float) {
+  return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+
+// Softmax statistics (greedy: and the largest logits) of all rows that are needed: each CTA takes
+// an equal run of chunks of up to 32 KB, over the rows' ends, and writes what it has of a row.
+// The next chunk's loads are under way while one is summed or a row's sums are joined: 64 to 128
+// KB an SM.  Bound by HBM.
+template <typename T, bool kGreedy>
+__global__ void __launch_bounds__(kThreads, kHeld) k_verify_stats(const __grid_constant__ VerifyParams p) {
+  constexpr int E = Vec<T>::E;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ Stat part_st[2][kThreads / 32];
+  __shared__ unsigned long long part_top[2][kThreads / 32];
+  launch_dependents();
+  const int nv = p.V / E;
+  const int64_t x0 = p.start(blockIdx.x), x1 = p.start(blockIdx.x + 1);
+  if (x0 >= x1) return;
+  int row = (int)(x0 / p.per_row), chunk = (int)(x0 - (int64_t)row * p.per_row);
+  auto data = [&](int r) -> const T* {
+    if (r < p.n_rows) return static_cast<const T*>(p.x) + r * p.ld;
+    return static_cast<const T*>(p.y) + (int64_t)(p.drafted[r - p.n_rows] - p.first) * p.yld;
+  };
+  const T* x = data(row);
+  wait_for_predecessor();
+  uint4 w[kPer], ahead[kPer];
+  auto fetch = [&](const T* from, int ch) {
+    const int v = ch * p.per_chunk + tid, end = min((ch + 1) * p.per_chunk, nv);
+#pragma unroll
+    for (int q = 0; q < kPer; q++)
+      ahead[q] = v + q * kThreads < end ? __ldcs(reinterpret_cast<const uint4*>(from) + v + q * kThreads) : Raw<T>::masked();
+  };
+  fetch(x, chunk);
+  int turn = 0;
+  for (int64_t at = x0; at < x1; turn ^= 1) {
+    // the chunks of this row that are this CTA's
+    const int end = (int)min((int64_t)p.per_row, chunk + (x1 - at));
+    const float c2 = (row < p.n_rows ? p.c : p.cy) * kLog2e;
+    const T* next_x = at + (end - chunk) < x1 ? data(row + 1) : x;
+    StageStat<T, false> ss;
+    ss.init();
+    float top = -INFINITY;     // largest logit so far, and (greedy) the first vector that has it
+    int top_vec = -1, top_id = -1;
+    for (int ch = chunk; ch < end; ch++) {
+#pragma unroll
+      for (int q = 0; q < kPer; q++) w[q] = ahead[q];
+      if (ch + 1 < end) fetch(x, ch + 1);
+      else if (at + (end - chunk) < x1) fetch(next_x, 0);
+      const float mx = Raw<T>::max(w);
+      if (kGreedy && mx > top) {
+#pragma unroll
+        for (int q = 0; q < kPer; q++) {
+          const float m = vec_max(w[q], T());
+          if (m > top) top = m, top_vec = ch * p.per_chunk + tid + q * kThreads;
+        }
+      }
+      top = fmaxf(top, mx);
+      ss.add(w, INT_MAX, mx, c2);
+    }
+    if (kGreedy && top_vec >= 0) {
+      float v[E];
+      Vec<T>::cvt(reinterpret_cast<const uint4*>(x)[top_vec], v);
+#pragma unroll
+      for (int e = E - 1; e >= 0; e--)
+        if (v[e] == top) top_id = top_vec * E + e;
+    }
+    Stat st = ss.total(top, c2);
+    if (end == p.per_row && tid < p.V - nv * E) {   // the entries past the last whole vector
+      const int i = nv * E + tid;
+      const float v = Vec<T>::get(x + i);
+      if (v > st.m) st.rebase(v, c2);
+      st.add(v, c2);
+      if (kGreedy && v > top) top = v, top_id = i;
+    }
+    warp_merge(st, c2);
+    unsigned long long best = 0;
+    if (kGreedy) best = warp_max(top_id >= 0 ? lowest_first(order_key(top), top_id) : 0);
+    if (lane == 0) part_st[turn][warp] = st, part_top[turn][warp] = best;
+    __syncthreads();   // the arrays of the turn before are read by then
+    if (warp == 0) {
+      st.init();
+      if (lane < kThreads / 32) st = part_st[turn][lane];
+      warp_merge(st, c2);
+      if (kGreedy) best = warp_max(lane < kThreads / 32 ? part_top[turn][lane] : 0);
+      if (lane == 0) {
+        const int64_t o = (int64_t)row * p.slots + (int)blockIdx.x - p.owner((int64_t)row * p.per_row);
+        p.stat[o] = make_float2(st.m, st.s);
+        if (kGreedy) p.best[o] = best;
+      }
+    }
+    at += end - chunk;
+    row++, chunk = 0, x = next_x;
+  }
+}
+
+// ln p of a logit of a row with largest logit st.x and ln S = st.y (-inf, -inf: no logit above -inf)
 __device__ __forceinline__ float log_p(float x, float2 st, float c) { return st.x == -INFINITY ? -INFINITY : (x - st.x) * c - st.y; }
 
-// One CTA per cursor: which drafts are accepted, then the draw.
+// One warp: (m, ln S) of row t of the statistics.
+__device__ __forceinline__ float2 row_stat(const VerifyParams& p, int t, float c) {
+  const int lane = threadIdx.x & 31, n = p.owner((int64_t)(t + 1) * p.per_row - 1) - p.owner((int64_t)t * p.per_row) + 1;
+  const float c2 = c * kLog2e;
+  Stat st;
+  st.init();
+  for (int i = lane; i < n; i += 32) {
+    const float2 s = p.stat[(int64_t)t * p.slots + i];
+    st.merge(s.x, s.y, 0.f, c2);
+  }
+  warp_merge(st, c2);
+  return st.s == 0.f ? make_float2(-INFINITY, -INFINITY) : make_float2(st.m, logf(st.s));
+}
+// One warp: the largest logit of a target's row.
+__device__ __forceinline__ unsigned long long row_best(const VerifyParams& p, int t) {
+  const int lane = threadIdx.x & 31, n = p.owner((int64_t)(t + 1) * p.per_row - 1) - p.owner((int64_t)t * p.per_row) + 1;
+  unsigned long long b = 0;
+  for (int i = lane; i < n; i += 32) b = max(b, p.best[(int64_t)t * p.slots + i]);
+  return warp_max(b);
+}
+
+// p = softmax of logits: 2^(d hi + (d lo - log2 S)), d = x - m, hi + lo = c log2 e to 48 bits: the
+// race compares probabilities of tokens, and one rounding of d c log2 e would be 2^-24 of it.
+struct Prob {
+  float m, hi, lo, l2;
+  __device__ __forceinline__ void set(float2 st, float h, float l) { m = st.x, l2 = st.y * kLog2e, hi = h, lo = l; }
+  __device__ __forceinline__ float operator()(float x) const {
+    const float d = max_nan(x - m, -1e30f);
+    return m == -INFINITY ? 0.f : ex2f(fmaf(d, hi, fmaf(d, lo, -l2)));
+  }
+};
+
+// The race of one row: the largest w / e of this thread's entries and the lowest id that has it.
+// Two exponentials and a reciprocal an entry for the 8 to 12 bytes that it takes.
+template <typename T>
+struct Race {
+  static constexpr int E = Vec<T>::E;
+  Prob pp, pq;
+  int out;          // id left out, or -1
+  float top;
+  int id;
+  __device__ __forceinline__ void start(const Decision& d, const VerifyParams& p) {
+    pp.set(d.st, p.hi[0], p.lo[0]);
+    pq.set(d.y_st, p.hi[1], p.lo[1]);
+    out = d.out, top = 0.f, id = 0;
+  }
+  __device__ __forceinline__ void one(float w, float e, int v) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(e));
+    if (v == out) w = 0.f;
+    const float s = w * inv;
+    if (s > top) top = s, id = v;
+  }
+  template <bool kSub>
+  __device__ __forceinline__ void vec(const uint4& xr, const uint4& yr, const float4 (&er)[E / 4], int v) {
+    float x[E], y[E];
+    Vec<T>::cvt(xr, x);
+    if (kSub) Vec<T>::cvt(yr, y);
+#pragma unroll
+    for (int q = 0; q < E / 4; q++) {
+      const float e[4] = {er[q].x, er[q].y, er[q].z, er[q].w};
+#pragma unroll
+      for (int k = 0; k < 4; k++) one(kSub ? pp(x[4 * q + k]) - pq(y[4 * q + k]) : pp(x[4 * q + k]), e[k], v + 4 * q + k);
+    }
+  }
+  // entry v of the row, past the last whole vector
+  __device__ __forceinline__ void tail(const T* x, const T* y, const float* e, int v) {
+    one(y ? pp(Vec<T>::get(x + v)) - pq(Vec<T>::get(y + v)) : pp(Vec<T>::get(x + v)), e[v], v);
+  }
+  __device__ __forceinline__ unsigned long long key() const { return top > 0.f ? lowest_first(__float_as_uint(top), id) : 0; }
+};
+
+// Which drafts of a cursor are accepted, a warp a draft (and one for the last row); greedy: the
+// next token too.  A chain of dependent loads: bound by latency.
 template <typename T, bool kGreedy>
-__global__ void __launch_bounds__(kPickThreads) k_verify_pick(const __grid_constant__ VerifyParams p) {
-  const int i = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(kDecide) k_verify_decide(const __grid_constant__ VerifyParams p) {
+  constexpr int kWarps = kDecide / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = blockIdx.x;
+  launch_dependents();
   const int r0 = p.row0[i] - p.first, n = p.row0[i + 1] - p.row0[i];
-  const T *x = static_cast<const T*>(p.x), *y = static_cast<const T*>(p.y);
-  __shared__ int s_acc;
-  __shared__ unsigned long long s_best;
+  const int y0 = p.n_rows - (p.live[i] - p.live0);   // statistics of the draft's row r: y0 + r
+  wait_for_predecessor();
   if (n == 0) {
     if (tid == 0) {
       p.n_accept[i] = 0, p.next_id[i] = -1;
       if (p.next_logp) p.next_logp[i] = -INFINITY;
+      p.decision[i].row = -1;
     }
     return;
   }
-  if (tid == 0) {
-    int acc = 0;
-    bool on = true;
-    if (p.accept_p) p.accept_p[p.first + r0] = 0.f;
-    for (int j = 0; j + 1 < n; j++) {
-      const int r = r0 + j, row = p.first + r + 1;   // row: of the plan, the draft's
-      float a = 0.f;
-      bool taken = false;
-      if (on) {
-        const int id = p.ids[row];
-        if (id < 0 || id >= p.V) {
-          atomicExch(p.status, OCTO_EINVAL);
-        } else if (kGreedy) {
-          const unsigned long long b = p.best[r];
-          taken = b >> 32 && p.stat[r].x != -INFINITY && id_of(b) == id;
-          a = taken;
-        } else {
-          const float lp = log_p(Vec<T>::get(x + r * p.ld + id), p.stat[r], p.c);
-          const float lq = y ? log_p(Vec<T>::get(y + r * p.yld + id), p.stat[p.n_rows + r], p.cy) : 0.f;
-          a = lp == -INFINITY ? 0.f : lp >= lq ? 1.f : expf(lp - lq);
-          if (!(lp == lp) || !(lq == lq)) a = 0.f;
-          taken = p.u[row] < a;
-        }
-      }
-      if (p.accept_p) p.accept_p[row] = a;
-      on = taken;
-      acc += taken;
+  const T *x = static_cast<const T*>(p.x), *y = static_cast<const T*>(p.y);
+  __shared__ int s_acc;
+  __shared__ Decision s_dec[kWarps];   // what each warp would decide for the last row that it looked at
+  if (tid == 0) s_acc = n - 1;
+  __syncthreads();
+  for (int j = warp; j < n && j <= *(volatile int*)&s_acc; j += kWarps) {
+    const int r = r0 + j, row = p.first + r + 1;   // row: of the plan, the draft's (j < n - 1)
+    const bool draft = j + 1 < n;
+    const int id = draft ? p.ids[row] : -1;
+    const bool known = id >= 0 && id < p.V;
+    Decision d;
+    d.acc = j, d.row = r, d.y_row = draft && y ? r : -1, d.out = draft && !y ? id : -1;
+    float a = 0.f;
+    bool taken = false;
+    if (kGreedy) {
+      const unsigned long long b = row_best(p, r);
+      d.out = b ? id_of(b) : -1;
+      taken = b && known && id_of(b) == id;
+      a = taken;
+      d.st = row_stat(p, r, p.c);
+    } else {
+      const float lx = known ? Vec<T>::get(x + r * p.ld + id) : 0.f, ly = known && y ? Vec<T>::get(y + r * p.yld + id) : 0.f;
+      const float u = draft ? p.u[row] : 0.f;
+      d.st = row_stat(p, r, p.c);
+      d.y_st = draft && y ? row_stat(p, y0 + r, p.cy) : make_float2(0.f, 0.f);
+      const float lp = log_p(lx, d.st, p.c), lq = y ? log_p(ly, d.y_st, p.cy) : 0.f;
+      if (known && lp == lp && lq == lq && lp != -INFINITY) a = lp >= lq ? 1.f : expf(lp - lq);
+      taken = u < a;
     }
-    s_acc = acc;
-    s_best = 0;
+    if (lane == 0) {
+      s_dec[warp] = d;
+      if (draft && p.accept_p) p.accept_p[row] = a;
+    }
+    if (draft && !taken) {
+      if (lane == 0) atomicMin(&s_acc, j);
+      break;   // what comes after it does not count
+    }
   }
   __syncthreads();
   const int acc = s_acc, r = r0 + acc;
-  const bool rejected = acc + 1 < n;
-  const float2 st = p.stat[r];
-  unsigned long long best = 0;
-  if (kGreedy) {
-    best = st.x == -INFINITY ? 0 : p.best[r];
-  } else {
-    const float2 sq = rejected && y ? p.stat[p.n_rows + r] : make_float2(0.f, 0.f);
-    const int out = rejected && !y ? p.ids[p.first + r + 1] : -1;
-    const float* e = p.noise + i * p.eld;
-    for (int pass = 0; pass < 2 && best == 0; pass++) {
-      for (int v = tid; v < p.V; v += kPickThreads) {
-        float w = expf(log_p(Vec<T>::get(x + r * p.ld + v), st, p.c));
-        if (pass == 0) {
-          if (rejected && y) w -= expf(log_p(Vec<T>::get(y + r * p.yld + v), sq, p.cy));
-          if (v == out) w = 0.f;
-        }
-        const float s = w / e[v];
-        if (s > 0.f && __float_as_uint(s) > (uint32_t)(best >> 32)) best = lowest_first(__float_as_uint(s), v);
-      }
-      atomicMax(&s_best, best);
-      __syncthreads();
-      best = s_best;
-    }
+  if (p.accept_p) {   // 0 in the first row and behind the first rejected draft
+    if (tid == 0) p.accept_p[p.first + r0] = 0.f;
+    for (int j = acc + 2 + tid; j < n; j += kDecide) p.accept_p[p.first + r0 + j] = 0.f;
   }
   if (tid) return;
-  const int id = best ? id_of(best) : -1;
-  p.n_accept[i] = acc;
-  p.next_id[i] = id;
-  if (p.next_logp) p.next_logp[i] = id < 0 ? -INFINITY : log_p(Vec<T>::get(x + r * p.ld + id), st, p.c);
+  // row acc was the last that its warp looked at
+  const Decision d = s_dec[acc % kWarps];
+  if (acc + 1 < n) {
+    const int id = p.ids[p.first + r + 1];
+    if (id < 0 || id >= p.V) atomicExch(p.status, OCTO_EINVAL);
+  }
+  if (kGreedy) {
+    p.n_accept[i] = acc, p.next_id[i] = d.out;
+    if (p.next_logp) p.next_logp[i] = d.out < 0 ? -INFINITY : log_p(Vec<T>::get(x + r * p.ld + d.out), d.st, p.c);
+  } else {
+    p.decision[i] = d, p.drawn[i] = 0, p.done[i] = 0;
+  }
 }
 
-size_t stat_bytes(int64_t rows) { return align_up((size_t)rows * 2 * sizeof(float2), 256); }
+// The draw of the cursors' next tokens: one CTA an SM, each with an equal run of chunks over the
+// cursors' ends.  One thread copies the chunks of logits, the draft's and the noise into a ring
+// (bulk copies, 190 KB under way); 16 warps race over them, a vector a thread, and take what they
+// have of a cursor to its best score; the last CTA of a cursor writes its results.  Bound by HBM.
+template <typename T>
+struct DrawShape {
+  static constexpr int E = Vec<T>::E;
+  static constexpr int kVec = 512;                               // vectors of a chunk, at most
+  static constexpr int kStage = kVec * (32 + 4 * E);             // logits, draft, noise
+  static constexpr int kStages = 192 * 1024 / kStage;
+  static constexpr int kConsumers = 512, kBlock = kConsumers + 32;
+  static constexpr int kSmem = kStages * kStage + 256;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(DrawShape<T>::kBlock, 1) k_verify_draw(const __grid_constant__ VerifyParams p) {
+  using S = DrawShape<T>;
+  constexpr int E = S::E;
+  extern __shared__ __align__(128) uint8_t sm[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::kStages * S::kStage);
+  uint64_t* empty = full + S::kStages;
+  __shared__ unsigned long long s_best[2], s_all, s_own;
+  __shared__ bool s_last;
+  const int tid = threadIdx.x, lane = tid & 31;
+  launch_dependents();
+  if (tid == 0) {
+    for (int k = 0; k < S::kStages; k++) tc::mbar_init(&full[k], 1), tc::mbar_init(&empty[k], S::kConsumers / 32);
+    tc::fence_mbar_init();
+    s_best[0] = s_best[1] = 0;
+  }
+  __syncthreads();
+  wait_for_predecessor();
+  const int nv = p.V / E;
+  const int64_t C = (int64_t)p.n_cur * p.draw_per_row;
+  const int64_t x0 = blockIdx.x * C / p.draw_ctas, x1 = (blockIdx.x + 1) * C / p.draw_ctas;
+  auto owner = [&](int64_t x) { return (int)(((x + 1) * p.draw_ctas - 1) / C); };
+  int i = (int)(x0 / p.draw_per_row), ch = (int)(x0 - (int64_t)i * p.draw_per_row);
+  if (tid >= S::kConsumers) {
+    if (lane) return;
+    int st = 0, issued = 0;
+    uint32_t round = 0;
+    bool ok = true;
+    Decision d = p.decision[i];
+    for (int64_t at = x0; ok && at < x1; at++) {
+      const int v0 = ch * p.draw_chunk, cnt = min(p.draw_chunk, nv - v0);
+      if (d.row >= 0 && cnt > 0) {
+        if (issued >= S::kStages && !(ok = ring_wait(&empty[st], round ^ 1, p.status))) break;
+        uint8_t* dst = sm + st * S::kStage;
+        const T* x = static_cast<const T*>(p.x) + d.row * p.ld;
+        tc::mbar_expect_tx(&full[st], (uint32_t)cnt * (d.y_row >= 0 ? 32 + 4 * E : 16 + 4 * E));
+        bulk_load(dst, x + (int64_t)v0 * E, cnt * 16, &full[st], true);
+        if (d.y_row >= 0) bulk_load(dst + S::kVec * 16, static_cast<const T*>(p.y) + d.y_row * p.yld + (int64_t)v0 * E, cnt * 16, &full[st], true);
+        bulk_load(dst + S::kVec * 32, p.noise + i * p.eld + (int64_t)v0 * E, cnt * 4 * E, &full[st], true);
+        issued++;
+        if (++st == S::kStages) st = 0, round ^= 1;
+      }
+      if (++ch == p.draw_per_row) {
+        ch = 0, i++;
+        if (at + 1 < x1) d = p.decision[i];
+      }
+    }
+    // what was started has landed before the CTA ends
+    for (int k = max(0, issued - S::kStages); k < issued; k++) ring_wait(&full[k % S::kStages], (k / S::kStages) & 1, p.status);
+    return;
+  }
+  auto sync = [] { tc::named_bar_sync(1, S::kConsumers); };
+  int st = 0, turn = 0;
+  uint32_t round = 0;
+  bool ok = true;
+  for (int64_t at = x0; at < x1; i++, ch = 0) {
+    const int end = (int)min((int64_t)p.draw_per_row, ch + (x1 - at));
+    at += end - ch;
+    const Decision d = p.decision[i];
+    if (d.row < 0) continue;
+    const T* x = static_cast<const T*>(p.x) + d.row * p.ld;
+    const T* y = d.y_row >= 0 ? static_cast<const T*>(p.y) + d.y_row * p.yld : nullptr;
+    const float* e = p.noise + i * p.eld;
+    Race<T> race;
+    race.start(d, p);
+    for (int k = ch; k < end; k++) {
+      const int v0 = k * p.draw_chunk, cnt = min(p.draw_chunk, nv - v0);
+      if (cnt <= 0) break;
+      if (ok) ok = warp_wait(&full[st], round, p.status);
+      if (ok && tid < cnt) {
+        const uint8_t* src = sm + st * S::kStage;
+        const uint4 xr = reinterpret_cast<const uint4*>(src)[tid];
+        float4 er[E / 4];
+#pragma unroll
+        for (int q = 0; q < E / 4; q++) er[q] = reinterpret_cast<const float4*>(src + S::kVec * 32)[tid * (E / 4) + q];
+        if (y) race.template vec<true>(xr, reinterpret_cast<const uint4*>(src + S::kVec * 16)[tid], er, (v0 + tid) * E);
+        else race.template vec<false>(xr, xr, er, (v0 + tid) * E);
+      }
+      give_back(&empty[st], race.top);
+      if (++st == S::kStages) st = 0, round ^= 1;
+    }
+    if (end == p.draw_per_row && tid < p.V - nv * E) race.tail(x, y, e, nv * E + tid);
+    unsigned long long best = warp_max(race.key());
+    if (lane == 0 && best) atomicMax(&s_best[turn], best);
+    sync();
+    turn ^= 1;
+    if (tid == 0) {
+      best = s_best[turn ^ 1];
+      s_best[turn] = 0;   // of the cursor before, read by then
+      if (best) atomicMax(&p.drawn[i], best);
+      const int n = owner((int64_t)(i + 1) * p.draw_per_row - 1) - owner((int64_t)i * p.draw_per_row) + 1;
+      __threadfence();
+      s_last = atomicAdd(&p.done[i], 1) == n - 1;
+      __threadfence();
+      s_all = atomicMax(&p.drawn[i], 0ull), s_own = 0;
+    }
+    sync();
+    if (!s_last) continue;
+    best = s_all;
+    if (best == 0 && (d.y_row >= 0 || d.out >= 0)) {
+      // nothing left of p: the target's own
+      race.start(d, p);
+      race.out = -1;
+      for (int v = tid; v < nv; v += S::kConsumers) {
+        const uint4 xr = reinterpret_cast<const uint4*>(x)[v];
+        float4 er[E / 4];
+#pragma unroll
+        for (int q = 0; q < E / 4; q++) er[q] = reinterpret_cast<const float4*>(e)[(int64_t)v * (E / 4) + q];
+        race.template vec<false>(xr, xr, er, v * E);
+      }
+      if (tid < p.V - nv * E) race.tail(x, nullptr, e, nv * E + tid);
+      best = warp_max(race.key());
+      if (lane == 0 && best) atomicMax(&s_own, best);
+      sync();
+      best = s_own;
+    }
+    if (tid == 0) {
+      const int id = best ? id_of(best) : -1;
+      p.n_accept[i] = d.acc;
+      p.next_id[i] = id;
+      if (p.next_logp) p.next_logp[i] = id < 0 ? -INFINITY : log_p(Vec<T>::get(x + id), d.st, p.c);
+    }
+    sync();   // the shared results are read before the next cursor's
+  }
+}
+
+int held_ctas() { return kHeld * std::max(1, sm_count()); }
+// (row, slot) pairs of the statistics: rows (ctas / rows + 2) at most
+size_t stat_count(int64_t rows) { return (size_t)(held_ctas() + 4 * rows); }
+
+struct Layout {   // of the workspace
+  size_t best, decision, drawn, done, bytes;
+  Layout(int64_t rows, int64_t n_cur) {
+    best = align_up(stat_count(rows) * sizeof(float2), 256);
+    decision = best + align_up(stat_count(rows) * 8, 256);
+    drawn = decision + align_up((size_t)n_cur * sizeof(Decision), 256);
+    done = drawn + align_up((size_t)n_cur * 8, 256);
+    bytes = done + (size_t)n_cur * 4;
+  }
+};
 
 template <typename T, bool kGreedy>
-int run(const VerifyParams& p, int32_t n_cur, cudaStream_t s) {
-  if (p.n_rows > 0) {
-    k_verify_stats<T, kGreedy><<<dim3(p.n_rows, p.y ? 2 : 1), kStatThreads, 0, s>>>(p);
-    count_launch();
+int run(VerifyParams& p, cudaStream_t s) {
+  const int nv = p.V / Vec<T>::E;
+  p.per_row = std::max(1, (nv + kChunk - 1) / kChunk);
+  p.per_chunk = (nv + p.per_row - 1) / p.per_row;
+  const int64_t rows = (int64_t)p.n_rows + p.n_drafted;
+  if (rows > INT32_MAX / 4) return OCTO_EINVAL;
+  if (rows > 0) {
+    p.ctas = (int)std::min<int64_t>(held_ctas(), p.chunks());
+    p.slots = (int)(p.ctas / rows + 2);
+    if (int st = launch_overlapped((const void*)k_verify_stats<T, kGreedy>, &p, p.ctas, kThreads, 1, 0, s)) return st;
   }
-  k_verify_pick<T, kGreedy><<<n_cur, kPickThreads, 0, s>>>(p);
-  count_launch();
-  return cuda_status(cudaGetLastError());
+  if (int st = launch_overlapped((const void*)k_verify_decide<T, kGreedy>, &p, p.n_cur, kDecide, 1, 0, s)) return st;
+  if (kGreedy || rows == 0) return OCTO_OK;
+  using S = DrawShape<T>;
+  p.draw_per_row = std::max(1, (nv + S::kVec - 1) / S::kVec);
+  p.draw_chunk = (nv + p.draw_per_row - 1) / p.draw_per_row;
+  p.draw_ctas = (int)std::min<int64_t>(std::max(1, sm_count()), (int64_t)p.n_cur * p.draw_per_row);
+  if (int st = set_smem_limit((const void*)k_verify_draw<T>, S::kSmem)) return st;
+  return launch_overlapped((const void*)k_verify_draw<T>, &p, p.draw_ctas, S::kBlock, 1, S::kSmem, s);
 }
 
 }  // namespace
@@ -191,7 +512,7 @@ extern "C" {
 int octo_verify_drafts_workspace_size(octo_plan_t plan, int32_t cur0, int32_t n_cur, size_t* bytes) {
   if (!plan || !plan->chunk || !bytes || cur0 < 0 || n_cur < 0 || (int64_t)cur0 + n_cur > plan->info.n_segments) return OCTO_EINVAL;
   const int64_t rows = plan->chunk->row0[cur0 + n_cur] - plan->chunk->row0[cur0];
-  *bytes = octo::stat_bytes(rows) + octo::align_up((size_t)rows * 8, 256);
+  *bytes = octo::Layout(rows, n_cur).bytes;
   return OCTO_OK;
 }
 
@@ -212,26 +533,41 @@ int octo_verify_drafts(octo_plan_t plan, int32_t cur0, int32_t n_cur, const void
   }
   if (noise && (noise_ld < vocab || noise_ld % 4 || ((uintptr_t)noise & 15))) return OCTO_EINVAL;
   if (n_cur > 0 && (!n_accept || !next_id)) return OCTO_EINVAL;
-  if (n > 0 && (!ids || !ws || ws_bytes < need || ((uintptr_t)ws & 15))) return OCTO_EINVAL;
+  if (n_cur > 0 && (!ws || ws_bytes < need || ((uintptr_t)ws & 15))) return OCTO_EINVAL;
+  if (n > 0 && !ids) return OCTO_EINVAL;
   if (n_cur == 0) return OCTO_OK;
   octo::VerifyParams p;
   p.x = logits, p.y = draft_logits;
   p.ld = ld, p.yld = draft_ld, p.eld = noise_ld;
   p.V = vocab;
   p.c = inv_temp, p.cy = draft_inv_temp;
+  for (int k = 0; k < 2; k++) {
+    const double c2 = (double)(k ? draft_inv_temp : inv_temp) * 1.4426950408889634074;
+    p.hi[k] = (float)c2;
+    p.lo[k] = c2 < 1e6 ? (float)(c2 - p.hi[k]) : 0.f;   // larger ones times far logits would be inf - inf
+  }
   p.row0 = plan->seg_row_base + cur0;
   p.first = first;
   p.ids = ids, p.u = u, p.noise = noise;
   p.n_accept = n_accept, p.next_id = next_id, p.next_logp = next_logp, p.accept_p = accept_p;
-  p.stat = static_cast<float2*>(ws);
-  p.best = reinterpret_cast<unsigned long long*>(static_cast<char*>(ws) + octo::stat_bytes(n));
-  p.n_rows = n;
+  const octo::Layout at(n, n_cur);
+  char* w = static_cast<char*>(ws);
+  p.stat = reinterpret_cast<float2*>(w);
+  p.best = reinterpret_cast<unsigned long long*>(w + at.best);
+  p.decision = reinterpret_cast<octo::Decision*>(w + at.decision);
+  p.drawn = reinterpret_cast<unsigned long long*>(w + at.drawn);
+  p.done = reinterpret_cast<int32_t*>(w + at.done);
+  const std::vector<int32_t>& live = plan->chunk->live;
+  p.live = plan->chunk->d_live + cur0, p.live0 = live[cur0];
+  p.drafted = plan->chunk->drafted + (first - live[cur0]);
+  p.n_drafted = draft_logits ? n - (live[cur0 + n_cur] - live[cur0]) : 0;
+  p.n_rows = n, p.n_cur = n_cur;
   p.status = plan->pool->d_status;
   cudaStream_t s = (cudaStream_t)stream;
   plan->last_stream = s;
   if (dtype == OCTO_DTYPE_BF16)
-    return greedy ? octo::run<__nv_bfloat16, true>(p, n_cur, s) : octo::run<__nv_bfloat16, false>(p, n_cur, s);
-  return greedy ? octo::run<float, true>(p, n_cur, s) : octo::run<float, false>(p, n_cur, s);
+    return greedy ? octo::run<__nv_bfloat16, true>(p, s) : octo::run<__nv_bfloat16, false>(p, s);
+  return greedy ? octo::run<float, true>(p, s) : octo::run<float, false>(p, s);
 }
 
 }  // extern "C"

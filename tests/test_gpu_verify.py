@@ -263,9 +263,10 @@ def test_refusals(lib):
     xt, yt, nt = on_gpu(x, "bf16")[0], on_gpu(y, "bf16")[0], on_gpu(noise, "f32")[0]
     plan = chunk_plan(lib, rows)
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
-    ut, it, ws = torch.tensor(u, device="cuda"), torch.tensor(ids, device="cuda"), torch.empty(4096, dtype=torch.uint8, device="cuda")
+    need = plan.verify_drafts_workspace_size(0, 2)
+    ut, it, ws = torch.tensor(u, device="cuda"), torch.tensor(ids, device="cuda"), torch.empty(need + 16, dtype=torch.uint8, device="cuda")
     call = lambda cur0=0, n_cur=2, x=xt, V=V, ids=it, a=i32(2), b=i32(2), ws=ws, **kw: plan.verify_drafts(cur0, n_cur, x, V, ids, a, b, ws, **kw)
-    for kw in (dict(cur0=1), dict(n_cur=3), dict(cur0=-1), dict(ws=None), dict(ws=ws[:64].contiguous()), dict(ws=ws[4:]), dict(u=ut), dict(noise=nt),
+    for kw in (dict(cur0=1), dict(n_cur=3), dict(cur0=-1), dict(ws=None), dict(ws=ws[:need - 1].contiguous()), dict(ws=ws[4:]), dict(u=ut), dict(noise=nt),
                dict(draft_logits=yt), dict(inv_temp=0.0), dict(inv_temp=float("nan")), dict(u=ut, noise=nt, draft_logits=yt, draft_inv_temp=-1.0),
                dict(V=0), dict(ids=None), dict(a=None), dict(x=xt[:, 1:])):
         with pytest.raises((lib.OctoError, ValueError)):
