@@ -58,6 +58,7 @@ struct ChunkPlan {
   int32_t max_join_rows = 0;          // and of the longest joined one
   int32_t max_refs = 0;
   int64_t n_part = 0;                 // partial results
+  int64_t simt_ctas[9] = {};          // CUDA-core kernels: CTAs with work if each has 16 x rows
   ChunkBlock* blocks = nullptr;       // device arrays, the plan's
   ChunkWork* work = nullptr;          // CUDA-core kernels: longest first
   int32_t* cta_work = nullptr;        // [n_ctas + 1]
@@ -81,15 +82,5 @@ bool chunk_tc_supported(const octo_pool_desc& d, int32_t width);
 int chunk_tc(const octo_plan_s* p, const ChunkArgs& a, cudaStream_t s);
 int chunk_simt(const octo_plan_s* p, const ChunkArgs& a, cudaStream_t s);
 int chunk_join(const octo_plan_s* p, const ChunkArgs& a, cudaStream_t s);
-
-#ifdef __CUDACC__
-// Slots [lo, hi) of a block that the row at own index i sees; w0: its first visible position
-// (INT32_MIN: no window).
-__device__ __forceinline__ void chunk_range(const ChunkBlock& b, int32_t i, int32_t w0, bool windowed, int& lo, int& hi) {
-  lo = b.lo;
-  if (windowed) lo = max(lo, w0 - b.kpos);
-  hi = min((int)b.hi, i - b.own0 + 1);
-}
-#endif
 
 }  // namespace octo

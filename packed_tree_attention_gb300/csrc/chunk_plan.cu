@@ -250,6 +250,8 @@ Cuts cut_into_runs(const std::vector<ChunkTile>& tiles, int heads, int sms) {
   return cuts;
 }
 
+constexpr int kPairBlocks = 6;
+
 // Two slots: a tile's partial result is up to 128 KB, so tiles go whole, longest first, to the
 // CTA with the least work, as long as that does not pass the average; what is left is cut to
 // fill the CTAs up.  (512 tiles of 35 blocks on 152 CTAs: three whole ones each, 56 cut.)
@@ -339,10 +341,21 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
   if (top >= kMaxPos) return OCTO_ENOTSUP;
   cp->window = window > top ? 0 : window;   // sees everything
 
-  // tiles have the rows of one 128-row tile, of two where a chunk is longer
+  // Tiles have the rows of one 128-row tile, or of two where a chunk is longer and, for the tensor
+  // cores, the work is more than kPairBlocks blocks an SM.  (Less of it is sooner done in twice as
+  // many pieces: four chunks of 80 tokens under a window of 1,000 take 15 us so and 20 in pairs;
+  // 22 either way at 160 tokens; four of 40 behind 4,096 tokens 22 and 18.)
+  const int sms = std::max(1, rows::sm_count()), heads = d.n_kv_heads;
   int32_t most_new = 0;
-  for (int32_t c = 0; c < n; c++) most_new = std::max(most_new, n_new[c]);
-  const int32_t cap = most_new > cp->tokens ? 2 * cp->tokens : cp->tokens;
+  int64_t pair_blocks = 0;
+  for (int32_t c = 0; c < n; c++) {
+    if (!n_new[c]) continue;
+    most_new = std::max(most_new, n_new[c]);
+    const int32_t seen = pool->segs[cursors[c]].pos.back() + 1;   // keys, about
+    pair_blocks += (int64_t)((n_new[c] + 2 * cp->tokens - 1) / (2 * cp->tokens)) *
+                   ((cp->window ? std::min(seen, cp->window + 2 * cp->tokens) : seen) / cp->width + 1) * heads;
+  }
+  const int32_t cap = most_new > cp->tokens && (!cp->tc || pair_blocks > (int64_t)kPairBlocks * sms) ? 2 * cp->tokens : cp->tokens;
   Builder b{pool, d.page_size, cp->width, cp->window ? n_sink : 0, {}};
   std::vector<ChunkBlock> blocks;
   std::vector<ChunkTile> tiles;
@@ -464,7 +477,6 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
   }
 
   // the work, in pieces of the tiles' blocks, and the joins of what has several
-  const int sms = std::max(1, rows::sm_count()), heads = d.n_kv_heads;
   for (const ChunkTile& t : tiles) cp->max_rows = std::max(cp->max_rows, t.rows);
   std::vector<int32_t> cta_work, refs;
   const Cuts cuts = !cp->tc ? cut_evenly(tiles, heads, sms)
@@ -515,6 +527,8 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
     work.swap(sorted);
   } else {
     std::stable_sort(work.begin(), work.end(), [](const ChunkWork& x, const ChunkWork& y) { return x.n > y.n; });
+    for (const ChunkWork& w : work)
+      for (int x = 1; x <= 8; x++) cp->simt_ctas[x] += ((int64_t)w.rows * cp->G + 16 * x - 1) / (16 * x);
   }
   if (work.size() > (size_t)INT32_MAX || joins.size() > (size_t)INT32_MAX) return OCTO_EINVAL;
   cp->n_work = (int32_t)work.size();

@@ -6,11 +6,15 @@
 //     l <- l 2^(m - m') + sum 2^(s - m'),   O <- O 2^(m - m') + P V.
 // A CTA has 16 RM rows (token * G + head), staged with 64 keys at a time in shared memory as
 // fp32.  Thread (ty, tx) of 16 x 16 holds rows ty + 16 i and keys tx + 16 j of the scores (RM x
-// 4 of them), then columns 4 tx + 64 c .. + 3 of O: 4 RM and RM D / 16 accumulators against RM +
-// 4 and RM / 4 + D / 64 vector loads for each four steps of the inner product, so that from RM =
-// 4 on the FMAs and not shared memory bound it.  Everything is fp32.
+// 4 of them, each as a pair of sums over even and odd places), then columns 4 tx + 64 c .. + 3 of
+// O, two fp32 operations an instruction: 4 RM and RM D / 16 accumulators against RM + 4 and RM / 4
+// + D / 64 vector loads for each four steps of the inner product, so that from RM = 4 on the FMAs
+// and not shared memory bound it.  fp32 pools are copied with cp.async, the next K while P V runs
+// and the next V while S does.  Everything is fp32.
 
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "chunk.h"
 #include "row_ring.cuh"
@@ -52,8 +56,17 @@ constexpr int simt_smem() {
   return (16 * RM * (D + 4) + kKeys * (D + 4) + kKeys * D + 16 * RM * (kKeys + 4)) * (int)sizeof(float);
 }
 
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
+
 template <typename T, int D, int RM>
 __global__ void __launch_bounds__(256) k_chunk_simt(const __grid_constant__ SimtParams p) {
+  using rows::f2;
   constexpr int M = 16 * RM, C = D / 64, LD = D + 4, LP = kKeys + 4;
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;
@@ -78,103 +91,141 @@ __global__ void __launch_bounds__(256) k_chunk_simt(const __grid_constant__ Simt
   }
   int own[RM];          // own index of the thread's rows
   float m[RM], l[RM];
-  float4 o[RM][C];
+  f2 o[RM][C][2];
 #pragma unroll
   for (int i = 0; i < RM; i++) {
     own[i] = t.t0 + min(r0 + ty + 16 * i, R - 1) / p.G;
     m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; c++) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < C; c++) o[i][c][0] = o[i][c][1] = 0;
   }
   const int first = t.t0 + r0 / p.G, last = t.t0 + (min(r0 + M, R) - 1) / p.G;
-  for (int b = 0; b < t.n; b++) {
-    const ChunkBlock k = p.blocks[t.blk + b];
-    int lo, hi, unused;   // what some row of the CTA sees
-    chunk_range(k, first, first + t.shift - p.window + 1, p.window > 0, lo, unused);
-    chunk_range(k, last, 0, false, unused, hi);
-    for (int j0 = lo / kKeys * kKeys; j0 < hi; j0 += kKeys) {
-      __syncthreads();
-      for (int i = tid; i < kKeys * (D / 4); i += 256) {
-        const int j = i / (D / 4), c = i % (D / 4) * 4, slot = j0 + j;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (slot >= lo && slot < hi) {
-          const size_t row = ((size_t)k.page[slot / p.span] * p.Hkv + g) * p.P + k.slot0 + slot % p.span;
-          x = load4(static_cast<const T*>(p.k) + row * D + c);
-          y = load4(static_cast<const T*>(p.v) + row * D + c);
-        }
-        *reinterpret_cast<float4*>(sk + j * LD + c) = x;
-        *reinterpret_cast<float4*>(sv + j * D + c) = y;
-      }
-      __syncthreads();
-      float s[RM][4];
+  // the steps: 64 slots of a block at a time, where some row of the CTA sees one
+  struct Step {
+    int b, j0, lo, hi;              // slots that some row sees
+    int own0, kpos, k_lo, k_hi;     // of the block
+  };
+  auto lowest = [&](const Step& s, int i) {   // slots [lowest, highest) that the row at own index i sees
+    return p.window > 0 ? max(s.k_lo, i + t.shift - p.window + 1 - s.kpos) : s.k_lo;
+  };
+  auto highest = [&](const Step& s, int i) { return min(s.k_hi, i - s.own0 + 1); };
+  auto enter = [&](Step& s) {   // at block s.b or the next one with such a slot
+    for (; s.b < t.n; s.b++) {
+      const int4 k = *reinterpret_cast<const int4*>(&p.blocks[t.blk + s.b].own0);
+      s.own0 = k.x, s.kpos = k.y, s.k_lo = k.z & 0xffff, s.k_hi = (uint32_t)k.z >> 16;
+      s.lo = lowest(s, first), s.hi = highest(s, last);
+      s.j0 = s.lo / kKeys * kKeys;
+      if (s.j0 < s.hi) return;
+    }
+  };
+  auto advance = [&](Step& s) {
+    s.j0 += kKeys;
+    if (s.j0 >= s.hi) s.b++, enter(s);
+  };
+  auto load = [&](const Step& s, const void* pool, float* dst, int ld) {
+    const ChunkBlock* k = p.blocks + t.blk + s.b;
+    const int slot0 = k->slot0;
+    for (int i = tid; i < kKeys * (D / 4); i += 256) {
+      const int j = i / (D / 4), c = i % (D / 4) * 4, slot = s.j0 + j;
+      const bool live = slot >= s.lo && slot < s.hi;
+      const int at = live ? slot : s.lo;
+      const T* src = static_cast<const T*>(pool) + (((size_t)k->page[at / p.span] * p.Hkv + g) * p.P + slot0 + at % p.span) * D + c;
+      if constexpr (sizeof(T) == 4) copy16(dst + j * ld + c, reinterpret_cast<const float*>(src), live);
+      else *reinterpret_cast<float4*>(dst + j * ld + c) = live ? load4(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    copies_issued();
+  };
+  Step s;
+  s.b = 0;
+  enter(s);
+  if (s.b < t.n) {
+    load(s, p.k, sk, LD);
+    load(s, p.v, sv, D);
+  }
+  while (s.b < t.n) {
+    Step next = s;
+    advance(next);
+    copies_wait<1>();   // K of this step
+    __syncthreads();
+    f2 a2[RM][4];
 #pragma unroll
-      for (int i = 0; i < RM; i++)
+    for (int i = 0; i < RM; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) s[i][j] = 0.f;
+      for (int j = 0; j < 4; j++) a2[i][j] = 0;
 #pragma unroll 4
-      for (int c = 0; c < D; c += 4) {
-        float4 x[RM], y[4];
+    for (int c = 0; c < D; c += 4) {
+      ulonglong2 y[4];
 #pragma unroll
-        for (int i = 0; i < RM; i++) x[i] = *reinterpret_cast<const float4*>(sq + (ty + 16 * i) * LD + c);
-#pragma unroll
-        for (int j = 0; j < 4; j++) y[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * LD + c);
-#pragma unroll
-        for (int i = 0; i < RM; i++)
-#pragma unroll
-          for (int j = 0; j < 4; j++)
-            s[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, s[i][j]))));
-      }
+      for (int j = 0; j < 4; j++) y[j] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * j) * LD + c);
 #pragma unroll
       for (int i = 0; i < RM; i++) {
-        int a, e;
-        chunk_range(k, own[i], own[i] + t.shift - p.window + 1, p.window > 0, a, e);
-        float mx = m[i];
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sq + (ty + 16 * i) * LD + c);
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const int slot = j0 + tx + 16 * j;
-          s[i][j] = slot >= a && slot < e ? s[i][j] * p.scale_log2 : -INFINITY;
-          mx = fmaxf(mx, s[i][j]);
-        }
-#pragma unroll
-        for (int w = 8; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-        const float base = mx == -INFINITY ? 0.f : mx;
-        const float f = ex2f(m[i] - base);
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const float e2 = ex2f(s[i][j] - base);
-          sum += e2;
-          sp[(ty + 16 * i) * LP + tx + 16 * j] = e2;
-        }
-        l[i] = l[i] * f + sum;   // the lane's own part of the row's sum
-        m[i] = mx;
-#pragma unroll
-        for (int c = 0; c < C; c++) o[i][c].x *= f, o[i][c].y *= f, o[i][c].z *= f, o[i][c].w *= f;
+        for (int j = 0; j < 4; j++) a2[i][j] = rows::fma2(x.y, y[j].y, rows::fma2(x.x, y[j].x, a2[i][j]));
       }
-      __syncwarp();   // a row's 16 lanes are in one warp
+    }
+    __syncthreads();    // K is read
+    if (next.b < t.n) load(next, p.k, sk, LD);
+    else copies_issued();
+#pragma unroll
+    for (int i = 0; i < RM; i++) {
+      const int lo = lowest(s, own[i]), hi = highest(s, own[i]);
+      float mx = m[i], x[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int slot = s.j0 + tx + 16 * j;
+        float e, f;
+        rows::unpack2(a2[i][j], e, f);
+        x[j] = slot >= lo && slot < hi ? (e + f) * p.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, x[j]);
+      }
+#pragma unroll
+      for (int w = 8; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+      const float base = mx == -INFINITY ? 0.f : mx;
+      const float f = ex2f(m[i] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const float e2 = ex2f(x[j] - base);
+        sum += e2;
+        sp[(ty + 16 * i) * LP + tx + 16 * j] = e2;
+      }
+      l[i] = l[i] * f + sum;   // the lane's own part of the row's sum
+      m[i] = mx;
+      const f2 ff = rows::pack2(f, f);
+#pragma unroll
+      for (int c = 0; c < C; c++) o[i][c][0] = rows::mul2(o[i][c][0], ff), o[i][c][1] = rows::mul2(o[i][c][1], ff);
+    }
+    copies_wait<1>();   // V of this step
+    __syncthreads();
 #pragma unroll 2
-      for (int j = 0; j < kKeys; j += 4) {
-        float4 w[RM];
+    for (int j = 0; j < kKeys; j += 4) {
+      float4 w[RM];
 #pragma unroll
-        for (int i = 0; i < RM; i++) w[i] = *reinterpret_cast<const float4*>(sp + (ty + 16 * i) * LP + j);
+      for (int i = 0; i < RM; i++) w[i] = *reinterpret_cast<const float4*>(sp + (ty + 16 * i) * LP + j);
 #pragma unroll
-        for (int jj = 0; jj < 4; jj++)
+      for (int jj = 0; jj < 4; jj++) {
+        ulonglong2 y[C];
+#pragma unroll
+        for (int c = 0; c < C; c++) y[c] = *reinterpret_cast<const ulonglong2*>(sv + (j + jj) * D + 64 * c + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < RM; i++) {
+          const float e2 = jj == 0 ? w[i].x : jj == 1 ? w[i].y : jj == 2 ? w[i].z : w[i].w;
+          const f2 ee = rows::pack2(e2, e2);
 #pragma unroll
           for (int c = 0; c < C; c++) {
-            const float4 y = *reinterpret_cast<const float4*>(sv + (j + jj) * D + 64 * c + 4 * tx);
-#pragma unroll
-            for (int i = 0; i < RM; i++) {
-              const float e2 = jj == 0 ? w[i].x : jj == 1 ? w[i].y : jj == 2 ? w[i].z : w[i].w;
-              o[i][c].x = fmaf(e2, y.x, o[i][c].x);
-              o[i][c].y = fmaf(e2, y.y, o[i][c].y);
-              o[i][c].z = fmaf(e2, y.z, o[i][c].z);
-              o[i][c].w = fmaf(e2, y.w, o[i][c].w);
-            }
+            o[i][c][0] = rows::fma2(ee, y[c].x, o[i][c][0]);
+            o[i][c][1] = rows::fma2(ee, y[c].y, o[i][c][1]);
           }
+        }
       }
-      __syncwarp();   // P is read before the next scores' replaces it
     }
+    __syncthreads();    // P and V are read
+    if (next.b < t.n) load(next, p.v, sv, D);
+    else copies_issued();
+    s = next;
   }
+  copies_wait<0>();
 #pragma unroll
   for (int i = 0; i < RM; i++) {
     const int r = r0 + ty + 16 * i;
@@ -182,18 +233,25 @@ __global__ void __launch_bounds__(256) k_chunk_simt(const __grid_constant__ Simt
 #pragma unroll
     for (int w = 8; w; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
     if (r >= R) continue;
+    auto columns = [&](int c) {
+      float4 v;
+      rows::unpack2(o[i][c][0], v.x, v.y);
+      rows::unpack2(o[i][c][1], v.z, v.w);
+      return v;
+    };
     if (t.part >= 0) {
       const int64_t at = (int64_t)t.part + r;
 #pragma unroll
-      for (int c = 0; c < C; c++) *reinterpret_cast<float4*>(p.part + at * D + 64 * c + 4 * tx) = o[i][c];
+      for (int c = 0; c < C; c++) *reinterpret_cast<float4*>(p.part + at * D + 64 * c + 4 * tx) = columns(c);
       if (tx == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * at) = make_float2(m[i], sum);
     } else {
       const size_t at = (size_t)(t.row0 + r / p.G) * p.Hq + g * p.G + r % p.G;
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-      for (int c = 0; c < C; c++)
-        store4(static_cast<T*>(p.out) + at * D + 64 * c + 4 * tx,
-               make_float4(o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv, o[i][c].w * inv));
+      for (int c = 0; c < C; c++) {
+        const float4 v = columns(c);
+        store4(static_cast<T*>(p.out) + at * D + 64 * c + 4 * tx, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+      }
       if (tx == 0 && p.lse) p.lse[at] = sum > 0.f ? (m[i] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
     }
   }
@@ -281,16 +339,25 @@ int launch(const SimtParams& p, int64_t ctas, cudaStream_t s) {
 
 template <typename T, int D>
 int run(SimtParams p, const octo_plan_s* plan, cudaStream_t s) {
-  // rows of a CTA: as many as the longest tile has, 128 at most
-  const int R = plan->chunk->max_rows * p.G;
-  const int rm = R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8;
+  // rows of a CTA, 16 rm: a step takes about rm + 1.5 units, and the SMs take the CTAs in turn
+  const int R = plan->chunk->max_rows * p.G, sms = std::max(1, rows::sm_count());
+  int rm = 1;
+  double best = 0;
+  for (int x : {1, 2, 3, 4, 5, 6, 8}) {
+    const int64_t ctas = plan->chunk->simt_ctas[x];
+    const double t = std::max((double)((ctas + sms - 1) / sms), ctas > 2 * sms ? (double)ctas / sms + 0.5 : 0.0) * (x + 1.5);
+    if (x == 1 || t <= best) rm = x, best = t;
+  }
   p.n_sub = (R + 16 * rm - 1) / (16 * rm);
   const int64_t ctas = (int64_t)plan->chunk->n_work * p.n_sub;
   if (ctas > INT32_MAX) return OCTO_EINVAL;
   switch (rm) {
     case 1: return launch<T, D, 1>(p, ctas, s);
     case 2: return launch<T, D, 2>(p, ctas, s);
+    case 3: return launch<T, D, 3>(p, ctas, s);
     case 4: return launch<T, D, 4>(p, ctas, s);
+    case 5: return launch<T, D, 5>(p, ctas, s);
+    case 6: return launch<T, D, 6>(p, ctas, s);
     default: return launch<T, D, 8>(p, ctas, s);
   }
 }
