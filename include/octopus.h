@@ -557,9 +557,10 @@ size_t octo_chunk_attn_workspace_size(octo_plan_t plan);
 /* Attention of a chunk plan's rows: out = softmax(scale q k^T) v over what each row sees; kv
  * head of query head h as in octo_attn_fwd.  q, out: [n_rows][n_q_heads][head_dim] of the pool
  * dtype; lse: fp32 [n_rows][n_q_heads], natural log (may be NULL).  k_pool / v_pool NULL = the
- * pool's arrays; every array 16-byte aligned.  ws: device workspace of the size above.  Long
- * contexts of few rows are split among CTAs and joined in a fixed order: the same bits on
- * every run.  Async on stream. */
+ * pool's arrays; every array 16-byte aligned; their slots that no row sees must hold finite
+ * values, as for octo_attn_fwd.  scale: finite, 1e-30 at least.  ws: device workspace of the size
+ * above, for one call at a time.  Long contexts of few rows are split among CTAs and joined in a
+ * fixed order: the same bits on every run.  Async on stream. */
 int octo_chunk_attn(octo_plan_t plan, const void* q, const void* k_pool, const void* v_pool, void* out,
                     float* lse, float scale, void* ws, size_t ws_bytes, void* stream);
 
@@ -592,7 +593,8 @@ int octo_verify_drafts_workspace_size(octo_plan_t plan, int32_t cur0, int32_t n_
  * drafts up to and including the first rejected one, 0 in these cursors' other rows).  A cursor
  * without rows has n_accept 0, next_id -1 and next_logp -inf, and so has one with no token
  * left to draw, besides its accepted ones.  An id outside [0, vocab) is rejected and, as
- * the first rejected one, gives OCTO_EINVAL at the next octo_sync.  The same results on every run.  Async on stream. */
+ * the first rejected one, gives OCTO_EINVAL at the next octo_sync.  The same results on every run.  ws: device workspace of the
+ * size above, 16-byte aligned, for one call at a time.  Async on stream. */
 int octo_verify_drafts(octo_plan_t plan, int32_t cur0, int32_t n_cur, const void* logits, int32_t dtype,
                        int64_t ld, int32_t vocab, float inv_temp, const int32_t* ids,
                        const void* draft_logits, int64_t draft_ld, float draft_inv_temp, const float* u,

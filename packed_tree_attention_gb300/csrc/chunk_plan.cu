@@ -12,6 +12,7 @@
 // every layer of a model, and its size is that of the contexts' page lists.
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <memory>
 #include <new>
@@ -654,6 +655,8 @@ int octo_chunk_attn(octo_plan_t plan, const void* q, const void* k_pool, const v
                     float scale, void* ws, size_t ws_bytes, void* stream) {
   octo::NvtxRange nv("octo_chunk_attn");
   if (!plan || !plan->chunk) return OCTO_EINVAL;
+  // the running maximum is that of the unscaled scores, and hidden ones are -inf times the scale
+  if (!(scale >= 1e-30f) || !std::isfinite(scale)) return OCTO_EINVAL;
   int dev = 0;
   OCTO_CUDA(cudaGetDevice(&dev));
   if (dev != plan->device) return OCTO_EINVAL;

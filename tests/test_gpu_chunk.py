@@ -65,12 +65,13 @@ class Case:
                 if window:
                     p = self.tok_pos[tok]
                     tok = tok[(p > self.plan.row_pos[row] - window) | (p < sink)]
-                for h in range(self.G * self.Hkv):
-                    g = h // self.G
-                    s = scale * (self.K[tok, g] @ q[r, h])
-                    lse[r, h] = np.logaddexp.reduce(s)
-                    p = np.exp(s - lse[r, h])
-                    o[r, h], a[r, h] = p @ self.V[tok, g], p @ np.abs(self.V[tok, g])
+                k, v = self.K[tok], self.V[tok]                      # [tokens][kv heads][d]
+                x = scale * np.einsum("ghd,ngd->ghn", q[r].reshape(self.Hkv, self.G, -1), k)
+                L = np.logaddexp.reduce(x, axis=2)
+                w = np.exp(x - L[:, :, None])
+                lse[r] = L.reshape(-1)
+                o[r] = np.einsum("ghn,ngd->ghd", w, v).reshape(o[r].shape)
+                a[r] = np.einsum("ghn,ngd->ghd", w, np.abs(v)).reshape(a[r].shape)
                 r += 1
         return o, lse, a
 
@@ -110,7 +111,7 @@ def live(case):
 SHAPES = [  # group, kv heads, head_dim, page, type
     (4, 4, 128, 64, "bf16"), (1, 2, 128, 64, "bf16"), (8, 1, 64, 32, "bf16"), (3, 2, 128, 16, "bf16"), (5, 1, 64, 128, "bf16"),
     (2, 2, 64, 24, "bf16"), (3, 2, 64, 16, "f32"), (4, 1, 128, 64, "f32"), (1, 1, 64, 128, "f32"), (2, 1, 128, 48, "f32"),
-    (16, 1, 64, 8, "f32"),
+    (16, 1, 64, 8, "f32"), (2, 1, 64, 100, "bf16"),
 ]
 
 
@@ -146,6 +147,15 @@ def test_chunk_lengths(lib, oracle_mod, dtype, P, n):
     Case(lib, oracle_mod, ep, 4, 2, 128, dtype).check([c], [n])
     ep, c = chain(P, 130, n)
     Case(lib, oracle_mod, ep, 4, 2, 128, dtype).check([c], [n], window=70, sink=3)
+
+
+@pytest.mark.parametrize("G,Hkv,d,P,dtype", [(128, 1, 128, 64, "bf16"), (127, 1, 64, 32, "bf16"), (65, 1, 128, 128, "bf16"), (33, 2, 64, 16, "f32")])
+def test_many_heads_a_kv_head(lib, oracle_mod, G, Hkv, d, P, dtype):
+    """Tiles of one, two or three tokens."""
+    ep, c = chain(P, 150, 9)
+    case = Case(lib, oracle_mod, ep, G, Hkv, d, dtype)
+    case.check([c, 0], [5, 3])
+    case.check([c], [9], window=70, sink=3)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -221,6 +231,36 @@ def test_shared_prefixes(lib, oracle_mod, dtype, P, G):
         case.check(cursors, n_new, window=700, sink=9)
 
 
+@pytest.mark.parametrize("G,Hkv,d,P", [(4, 8, 128, 64), (1, 8, 64, 32), (3, 8, 128, 16), (8, 8, 64, 128)])
+def test_long_chunks(lib, oracle_mod, G, Hkv, d, P):
+    """Work for every SM: tiles of twice 128 rows, chunks that end in either half of one beside short ones and empty ones, mounts inside
+    chunks, prefixes that short neighbours share, a window that ends inside tiles."""
+    T = 128 // G
+    ep = synth.Episode(P)
+    r = ep.root()
+    ep.append(r, 1500)
+    leaves = []
+    for i, n in enumerate((2 * T, 3 * T + 5, 7 * T - 1, 3, 4, 3 * T, 2 * T + 1, 5 * T)):
+        c = ep.fork(r, 1)[0]
+        ep.append(c, 40 + i)
+        if leaves and i % 3 == 2:
+            ep.append(c, n // 2)
+            ep.mount(c, leaves[-1], 10, 100 if ep.length[leaves[-1]] >= 100 else ep.length[leaves[-1]])
+            ep.append(c, n - n // 2)
+        else:
+            ep.append(c, n)
+        leaves.append(c)
+    case = Case(lib, oracle_mod, ep, G, Hkv, d, "bf16")
+    n_new = [ep.length[c] - 40 - i for i, c in enumerate(leaves)]
+    n_new[3] = 2
+    plan, q, out, lse = case.check(leaves, n_new)
+    assert plan.info["bm"] == 2 * T
+    again, lse2 = case.run(plan, q, 1 / math.sqrt(d))
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    case.check(leaves + [0], n_new + [3 * T], window=1300, sink=70)
+    case.check([0], [1500], window=T + 7)
+
+
 def test_same_cursor_twice_and_empty_plans(lib, oracle_mod):
     ep, c = chain(64, 100, 40)
     case = Case(lib, oracle_mod, ep, 2, 2, 128, "bf16")
@@ -287,12 +327,13 @@ def test_other_stream_other_arrays_and_capture(lib, oracle_mod):
 
 
 def test_refusals(lib, oracle_mod):
-    ep, c = chain(64, 300, 12)
+    ep, c = chain(64, 900, 12)
     case = Case(lib, oracle_mod, ep, 2, 2, 128, "bf16")
     plan = case.pool.chunk_plan([c], [12], 4)
     q = case.queries([c], [12], 3)
     out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
     need = plan.chunk_attn_workspace_size()
+    assert need > 0
     ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
     for bad in (None, ws[:need - 1].contiguous(), ws[1:]):
         with pytest.raises(lib.OctoError):
@@ -312,6 +353,9 @@ def test_refusals(lib, oracle_mod):
     shifted = torch.empty(q.numel() + 1, dtype=q.dtype, device="cuda")[1:].view(q.shape)
     with pytest.raises(lib.OctoError):
         plan.chunk_attn(shifted, out, lse, 1.0, ws)
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 1e-40):
+        with pytest.raises(lib.OctoError):
+            plan.chunk_attn(q, out, lse, scale, ws)
     # other plans and calls
     pack, dec = case.pool.pack_tree(ep.roots, 128), case.pool.decode_plan([c])
     assert pack.chunk_attn_workspace_size() == dec.chunk_attn_workspace_size() == 0
@@ -332,6 +376,132 @@ def test_refusals(lib, oracle_mod):
     assert np.array_equal(got["row_pos"], case.pool.seg_pos(c)) and got["tile_seg"].tolist() == [c] and got["tile_rows"].tolist() == [12]
     assert plan.recurrent_workspace_size(1, 128) == 0
     plan.sync()
+
+
+def test_nan_queries_stay_in_their_rows(lib, oracle_mod):
+    """A row of NaN beside others of its tile and a NaN key in one cursor's own tokens: the other rows are what they were."""
+    ep, leaves = forest(64)
+    case = Case(lib, oracle_mod, ep, 4, 1, 128, "bf16")
+    cur = leaves[:6]
+    n_new = [min(3, ep.length[c]) for c in cur]
+    scale = 1 / math.sqrt(128)
+    q = case.queries(cur, n_new, 7)
+    plan = case.pool.chunk_plan(cur, n_new, 4)
+    want, lse = case.run(plan, q, scale)
+    q[4] = float("nan")
+    out, lse2 = case.run(plan, q, scale)
+    keep = torch.arange(len(q), device="cuda") != 4
+    assert torch.isnan(out[4].float()).all() and torch.equal(out[keep], want[keep]) and torch.equal(lse2[keep], lse[keep])
+
+
+def test_layers_of_a_step_share_a_plan_on_two_streams(lib, oracle_mod):
+    """One plan, two calls under way at once on other arrays and workspaces."""
+    ep, c = chain(64, 3000, 40)
+    case = Case(lib, oracle_mod, ep, 4, 2, 128, "bf16")
+    scale = 1 / math.sqrt(128)
+    plan = case.pool.chunk_plan([c], [40], 8)
+    qs = [case.queries([c], [40], k) for k in (1, 2)]
+    want = [case.run(plan, q, scale)[0] for q in qs]
+    outs = [torch.empty_like(q) for q in qs]
+    ws = [torch.empty(max(1, plan.chunk_attn_workspace_size()), dtype=torch.uint8, device="cuda") for _ in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, o, w, s in zip(qs, outs, ws, streams):
+            plan.chunk_attn(q, o, None, scale, w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_scores_of_a_chunk(lib):
+    """octo_token_score on a chunk plan: row t leads to the token given for it."""
+    pool = lib.Pool(8, 16, 1, 64, lib.DTYPE_BF16)
+    r = pool.root()
+    pool.append(r, 30)
+    plan = pool.chunk_plan([r], [7], 1)
+    V = 500
+    x = torch.randn((7, 504), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    ids = torch.arange(7, dtype=torch.int32, device="cuda") * 60
+    stat, logp = torch.empty((7, 2), device="cuda"), torch.empty(7, device="cuda")
+    plan.token_score(0, 7, x, V, stat, ids=ids, logp=logp)
+    plan.sync()
+    ref = torch.log_softmax(x[:, :V].double(), 1)[torch.arange(7), ids.long()]
+    assert torch.all((logp.double() - ref).abs() <= 1e-5 * (1 + ref.abs()))
+
+
+def test_a_speculative_step(lib):
+    """Drafts of a forked child checked and the accepted ones kept: prefill of the prompt in parts, then the drafts appended to a child of
+    the cursor, attention of its rows, the target's tokens by greedy choice from a fixed read-out, the child released and the accepted
+    tokens appended to the cursor.  The tokens are those of decoding one by one."""
+    Hq, Hkv, d, P, V = 4, 2, 64, 32, 97
+    g = torch.Generator(device="cuda").manual_seed(5)
+    emb = torch.randn((V, Hkv * d * 2 + Hq * d), generator=g, device="cuda")
+    read = torch.randn((Hq * d, V), generator=g, device="cuda")
+    ld = 104
+    scale = 1 / math.sqrt(d)
+
+    def rows(ids):
+        e = emb[torch.as_tensor(ids, device="cuda")].bfloat16()
+        n = len(ids)
+        return e[:, :Hkv * d].reshape(n, Hkv, d).contiguous(), e[:, Hkv * d:2 * Hkv * d].reshape(n, Hkv, d).contiguous(), \
+            e[:, 2 * Hkv * d:].reshape(n, Hq, d).contiguous()
+
+    def new_pool():
+        kp = torch.zeros((64, Hkv, P, d), dtype=torch.bfloat16, device="cuda")
+        return lib.Pool(64, P, Hkv, d, lib.DTYPE_BF16, kp, torch.zeros_like(kp))
+
+    def attend(plan, q):
+        q = q.clone()
+        plan.rope_rows(Hq, q, 1e4)
+        out = torch.empty_like(q)
+        ws = torch.empty(max(1, plan.chunk_attn_workspace_size()), dtype=torch.uint8, device="cuda")
+        plan.chunk_attn(q, out, None, scale, ws)
+        x = torch.zeros((len(q), ld), device="cuda")
+        x[:, :V] = out.float().reshape(len(q), -1) @ read
+        return x
+
+    prompt = [(7 * i) % V for i in range(150)]
+    # one by one
+    pool = new_pool()
+    c = pool.root()
+    k, v, _ = rows(prompt[:-1])
+    pool.append_rope(c, len(prompt) - 1, k, v, 1e4)
+    slow, last = [], prompt[-1]
+    for _ in range(24):
+        k, v, q = rows([last])
+        pool.append_rope(c, 1, k, v, 1e4)
+        last = int(attend(pool.chunk_plan([c], [1], Hq), q)[0, :V].argmax())
+        slow.append(last)
+    # with drafts: right ones for a while, then a wrong one
+    pool = new_pool()
+    c = pool.root()
+    for part in (prompt[:100], prompt[100:-1]):        # read in in parts
+        k, v, q = rows(part)
+        pool.append_rope(c, len(part), k, v, 1e4)
+        attend(pool.chunk_plan([c], [len(part)], Hq), q)
+    fast, last, steps = [], prompt[-1], 0
+    while len(fast) < 24:
+        right = steps % 4
+        ahead = slow[len(fast):len(fast) + 4]
+        drafts = [t if i < right else (t + 1) % V for i, t in enumerate(ahead)] + [0] * (4 - len(ahead))
+        ids = [last] + drafts
+        child = pool.fork(c, 1)[0]
+        k, v, q = rows(ids)
+        pool.append_rope(child, len(ids), k, v, 1e4)
+        plan = pool.chunk_plan([child], [len(ids)], Hq)
+        x = attend(plan, q)
+        acc, nxt = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+        ws = torch.empty(plan.verify_drafts_workspace_size(0, 1), dtype=torch.uint8, device="cuda")
+        plan.verify_drafts(0, 1, x, V, torch.tensor(ids, dtype=torch.int32, device="cuda"), acc, nxt, ws)
+        plan.sync()
+        n = int(acc)
+        plan.close()
+        pool.release(child)
+        pool.append_rope(c, n + 1, k[:n + 1], v[:n + 1], 1e4)
+        fast += drafts[:n] + [int(nxt)]
+        last = int(nxt)
+        steps += 1
+    assert fast[:24] == slow and steps < 24
 
 
 def test_one_chunk_is_its_tokens_one_by_one(lib):

@@ -234,6 +234,55 @@ def test_some_of_the_cursors(lib):
     assert np.array_equal(whole[3][4:12], part[3][4:12]) and (part[3][:4] == -7).all() and (part[3][12:] == -7).all()
 
 
+def test_capture_and_replay(lib):
+    """A graph of a verification, replayed on other logits and draws with a dirty workspace; greedy and sampled."""
+    rng = np.random.default_rng(13)
+    rows, V = [5, 0, 3, 4], 3001
+    plan = chunk_plan(lib, rows)
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")
+    for greedy in (False, True):
+        sets = []
+        for _ in range(2):
+            x, y, ids, u, noise = inputs(rng, rows, V, 0, True)
+            sets.append((on_gpu(x, "bf16")[0], on_gpu(y, "bf16")[0], torch.tensor(ids, device="cuda"), torch.tensor(u, device="cuda"), on_gpu(noise, "f32")[0]))
+        xt, yt, it, ut, nt = (a.clone() for a in sets[0])
+        acc, nxt, ap, lp = i32(4), i32(4), torch.zeros(12, device="cuda"), torch.zeros(4, device="cuda")
+        ws = torch.full((plan.verify_drafts_workspace_size(0, 4),), 255, dtype=torch.uint8, device="cuda")
+        kw = {} if greedy else dict(u=ut, noise=nt, draft_logits=yt)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            plan.verify_drafts(0, 4, xt, V, it, acc, nxt, ws, accept_p=ap, next_logp=lp, **kw)
+        for s in (sets[1], sets[0]):
+            for a, b in zip((xt, yt, it, ut, nt), s):
+                a.copy_(b)
+            ws.fill_(77)
+            g.replay()
+            torch.cuda.synchronize()
+            got = [a.cpu().numpy() for a in (acc, nxt, lp, ap)]
+            want = run(plan, rows, V, s[0], s[2].cpu().numpy(), None if greedy else s[1], None if greedy else s[3].cpu().numpy(), None if greedy else s[4])
+            assert all(np.array_equal(a, b) for a, b in zip(got, want))
+    plan.sync()
+
+
+def test_nothing_left_of_the_target(lib):
+    """A rejected draft where the target is nowhere above the draft's distribution (equal rows, u = 1 - 2^-24 or the draft's own id masked):
+    the next token is drawn from the target itself."""
+    V, n = 1000, 6
+    rng = np.random.default_rng(14)
+    x = rng.standard_normal((2 * n, V))
+    noise = rng.exponential(size=(n, V)).astype(np.float32)
+    ids = np.zeros(2 * n, dtype=np.int32)
+    ids[1::2] = V + 5                      # rejected whatever u is
+    xt, xr = on_gpu(x, "f32")
+    nt, nr = on_gpu(noise, "f32")
+    plan = chunk_plan(lib, [2] * n)
+    acc, nxt, lp, ap = run(plan, [2] * n, V, xt, ids, xt.clone(), np.zeros(2 * n, dtype=np.float32), nt)
+    with pytest.raises(lib.OctoError):
+        plan.sync()
+    p = np.exp(log_softmax(xr, 1.0)[0])[::2]
+    assert acc.tolist() == [0] * n and nxt.tolist() == np.argmax(p / nr, axis=1).tolist() and (ap == 0).all()
+
+
 def test_distribution_of_the_emitted_token(lib):
     """Over many draws the first emitted token has the target's own distribution, whatever the draft's: frequencies of 40,000 within
     five standard deviations."""
