@@ -5,21 +5,18 @@
 // the cursor's shared pages.  The query heads of a kv head read the same K and V, so a tile's
 // 128 rows are T = 128 / G tokens times their G heads (row t G + h): a chunk of five tokens of
 // four heads fills 20 of them and reads its context once, a prefill chunk fills all.  Plans with
-// chunks of more than T tokens have tiles of twice as many (two slots of 128 rows that share
-// each block of K and V).
-// One CTA an SM, each with a run of the plan's work of equal length: pieces of tiles one after
-// another, through which the copies, the MMAs and the softmax run without a pause -- the ring
-// of K and V blocks fills across the pieces' ends, S of a piece's first blocks is computed
-// while the results of the one before are written.  Short chunks are bound by HBM, prefill
-// by the tensor cores (S and P V of a block of two slots: 0.66 us at their peak).
-// Warps: 0 copies K and V, 2 allocates TMEM and copies Q, 1 and 3 issue the MMAs of slots 0 and
-// 1 (S = Q K^T a block ahead, O += P V with P read from TMEM), 4-7 and 8-11 are the slots'
-// softmax, a row a thread: the running maximum stays until a block's probabilities relative to
-// it sum past 2^16, the sum is kept in fp32 of the unrounded probabilities, P is rounded to bf16
-// (half a step, as the inputs' type has it).  S has one buffer a slot, free again as soon as the
-// softmax has it in registers, and P two of its own: S of the next block then waits neither for
-// the softmax nor behind P V.  (P over S in two buffers, S two blocks ahead but behind P V:
-// prefill 13% slower.)  Warps whose rows a tile does not have only keep step.
+// long chunks have tiles of twice as many: two slots of 128 rows that share each block of K and V.
+// One CTA an SM, each with its share of the plan's work, pieces of tiles one after another; K and V
+// come through a ring of blocks, S = Q K^T and O += P V are issued by threads of their own, a row
+// of the softmax is a thread's.  Its running maximum stays until a block's probabilities relative
+// to it sum past 2^16; the sum is kept in fp32 of the unrounded probabilities, P is rounded to
+// bf16 (half a step, as the inputs' type has it).
+//   k_chunk_stream  one slot.  Bound by HBM (32 KB a block and SM in 0.8 us), so nothing pauses at
+//                   the end of a piece: the ring fills across it, S of the next one's first block
+//                   is computed while the results are written.
+//   k_chunk_pair    two slots.  Bound by the chain from S to S (0.82 us a block; the MMAs alone
+//                   0.5 at 2.07 GHz), in which every wait and every instruction of the issuing
+//                   threads counts: pieces start afresh, with the shortest loops.
 // Partial results are joined by k_chunk_join.
 
 #include <cuda_bf16.h>
@@ -166,20 +163,23 @@ __device__ __forceinline__ ChunkWork load_work(const ChunkWork* w) {
   return r;
 }
 
-// A run of work, one piece after another, its blocks' data fetched 32 at a time, a lane each, and
+// The copies' run of work, one piece after another, its blocks' pages fetched 32 at a time, a lane each, and
 // one such batch ahead (the next piece's first one at the last of this piece's): a load for each
 // block as it comes would make every block wait for memory, some 1 to 3 us in a streaming kernel.
 // All lanes call it alike.
-template <class Load>
 struct Feed {
-  using Data = decltype(Load{}(nullptr));
+  struct Pages {
+    int4 page;
+    int slot0;
+  };
   const ChunkWork* work;
   const ChunkBlock* blocks;
   int i, end;           // the piece at hand, the run's end
   ChunkWork w, w1;      // this piece and the next
-  Data cur, ahead;
-  __device__ __forceinline__ Data fetch(const ChunkWork& x, int j) const {
-    return Load{}(blocks + x.blk + min(j + (int)(threadIdx.x & 31), x.n - 1));
+  Pages cur, ahead;
+  __device__ __forceinline__ Pages fetch(const ChunkWork& x, int j) const {
+    const ChunkBlock* b = blocks + x.blk + min(j + (int)(threadIdx.x & 31), x.n - 1);
+    return {*reinterpret_cast<const int4*>(b->page), b->slot0};
   }
   __device__ __forceinline__ void start(const ChunkWork* wk, const ChunkBlock* b, int w0, int we) {
     work = wk, blocks = b, i = w0, end = we;
@@ -187,7 +187,7 @@ struct Feed {
     w1 = load_work(work + min(i + 1, end - 1));
     ahead = fetch(w, 0);
   }
-  // before block j of the piece: its data are in lane j % 32's `cur`
+  // before block j of the piece: its pages are in lane j % 32's `cur`
   __device__ __forceinline__ void at(int j) {
     if (j % 32 == 0) {
       cur = ahead;
@@ -201,15 +201,12 @@ struct Feed {
     w1 = load_work(work + min(i + 1, end - 1));
   }
 };
-struct LoadPages {   // pages and first slot
-  struct Data {
-    int4 page;
-    int slot0;
-  };
-  __device__ __forceinline__ Data operator()(const ChunkBlock* b) const {
-    return {*reinterpret_cast<const int4*>(b->page), b->slot0};
-  }
-};
+
+// Warps: 0 copies K and V, 2 allocates TMEM and copies Q, 1 issues the MMAs, 4-7 are the softmax.
+// S has one buffer, free again as soon as the softmax has it in registers, and P two of its own:
+// S of the next block waits neither for the softmax nor behind P V (P over S in two buffers, S two
+// blocks ahead but behind P V: 64 cursors' drafts 137 us where these take 128).  Warps whose rows
+// a tile does not have only keep step.
 template <int D>
 __global__ void __launch_bounds__(Shape<D, 1>::kThreads, 1)
     k_chunk_stream(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -267,7 +264,7 @@ __global__ void __launch_bounds__(Shape<D, 1>::kThreads, 1)
       prefetch_map(&tmK);
       prefetch_map(&tmV);
     }
-    Feed<LoadPages> f;
+    Feed f;
     f.start(p.work, p.blocks, w0, w1);
     rows::wait_for_predecessor();
     const uint32_t part = 8192u / p.loads;   // bytes of a load
@@ -518,8 +515,14 @@ __global__ void __launch_bounds__(Shape<D, 1>::kThreads, 1)
   if (warp == 2) tmem_dealloc(tbase, S::kCols);
 }
 
+// Warps: 0 copies Q, K and V, 2 allocates TMEM, 1 and 3 issue the MMAs of slots 0 and 1, 4-7 and
+// 8-11 are the slots' softmax.  S has two buffers a slot and is issued two blocks ahead; P goes
+// over the S that it came from, and S of the block after the next into that buffer behind P V, in
+// the order of the issuing thread.  Tried and slower at prefill: S a block ahead with P beside it
+// (872 us for 826), a thread for P V (1,110), the slots' exponentials in strict turns (979), every
+// fourth exponential by a polynomial on the FMA pipe (858 for 841), the scores in two halves (857).
 template <int D>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(Shape<D, 2>::kThreads, 1)
     k_chunk_pair(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcParams p) {
   using S = Shape<D, 2>;
@@ -613,10 +616,13 @@ __global__ void __launch_bounds__(384, 1)
           }
           issued = j + 1;
         }
-        // every copy this thread started has landed before the CTA may exit
+        // every copy that this thread started has landed, and every slot of the ring has been given
+        // back, before the barriers are made anew or the CTA ends
         mbar_wait(&B->q_full, 0, p.status, OCTO_ETIMEOUT);
-        for (int j = max(0, issued - kNS); j < issued; j++)
+        for (int j = max(0, issued - kNS); j < issued; j++) {
           mbar_wait(&B->kv_full[j % kNS], (j / kNS) & 1, p.status, OCTO_ETIMEOUT);
+          wait_or_abort(&B->kv_empty[j % kNS], (j / kNS) & 1, B, p.status);
+        }
       }
     } else if (warp == 1 || (warp == 3 && n_slots == 2)) {
       // ---------------- MMAs ----------------
