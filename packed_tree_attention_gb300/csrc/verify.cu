@@ -7,6 +7,7 @@
 // clocks of rates w_v), so that neither a sum of the weights nor an order of them is needed.
 
 #include <algorithm>
+#include <cmath>
 
 #include "chunk.h"
 #include "row_common.cuh"
@@ -35,7 +36,7 @@ struct VerifyParams {
   int64_t ld, yld, eld;
   int32_t V;
   float c, cy;                // inverse temperatures
-  float hi[2], lo[2];         // c log2 e and cy log2 e in two parts
+  float hi[2], lo[2];         // c log2 e and cy log2 e in two parts, lo > 0
   const int32_t* row0;        // [cursors + 1] first row of the plan's cursors, from cur0 on
   const int32_t* live;        // [cursors + 1] cursors with rows before each, from cur0 on
   const int32_t* drafted;     // rows of the plan that lead to a draft, from the first of these on
@@ -199,19 +200,25 @@ __device__ __forceinline__ unsigned long long row_best(const VerifyParams& p, in
   return warp_max(b);
 }
 
-// p = softmax of logits: 2^(d hi + (d lo - log2 S)), d = x - m, hi + lo = c log2 e to 48 bits: the
-// race compares probabilities of tokens, and one rounding of d c log2 e would be 2^-24 of it.
+// p = softmax of logits, two at a time: 2^(d hi + (d lo - log2 S)), d = x - m, hi + lo = c log2 e to
+// some 48 bits: the race compares probabilities of tokens, and one rounding of d c log2 e would be
+// 2^-24 of it.  hi is rounded down and lo positive, so that a masked entry's terms are both -inf.
+// A row without a logit above -inf gives NaN, which wins no race.
 struct Prob {
-  float m, hi, lo, l2;
-  __device__ __forceinline__ void set(float2 st, float h, float l) { m = st.x, l2 = st.y * kLog2e, hi = h, lo = l; }
-  __device__ __forceinline__ float operator()(float x) const {
-    const float d = max_nan(x - m, -1e30f);
-    return m == -INFINITY ? 0.f : ex2f(fmaf(d, hi, fmaf(d, lo, -l2)));
+  f2 minus_m, hi, lo, minus_l2;
+  __device__ __forceinline__ void set(float2 st, float h, float l) {
+    minus_m = pack2(-st.x, -st.x), hi = pack2(h, h), lo = pack2(l, l);
+    minus_l2 = pack2(-st.y * kLog2e, -st.y * kLog2e);
+  }
+  __device__ __forceinline__ f2 operator()(f2 x) const {
+    const f2 d = add2(x, minus_m);
+    float a, b;
+    unpack2(fma2(d, hi, fma2(d, lo, minus_l2)), a, b);
+    return pack2(ex2f(a), ex2f(b));
   }
 };
 
 // The race of one row: the largest w / e of this thread's entries and the lowest id that has it.
-// Two exponentials and a reciprocal an entry for the 8 to 12 bytes that it takes.
 template <typename T>
 struct Race {
   static constexpr int E = Vec<T>::E;
@@ -224,28 +231,50 @@ struct Race {
     pq.set(d.y_st, p.hi[1], p.lo[1]);
     out = d.out, top = 0.f, id = 0;
   }
-  __device__ __forceinline__ void one(float w, float e, int v) {
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(e));
-    if (v == out) w = 0.f;
-    const float s = w * inv;
-    if (s > top) top = s, id = v;
+  // E entries from id v on; s: their w / e
+  __device__ __forceinline__ void take(float (&s)[E], int v) {
+    if ((uint32_t)(out - v) < (uint32_t)E) {
+#pragma unroll
+      for (int k = 0; k < E; k++)
+        if (v + k == out) s[k] = 0.f;
+    }
+    float m = s[0];
+#pragma unroll
+    for (int k = 1; k < E; k++) m = fmaxf(m, s[k]);
+    if (m > top) {   // rare after the first few
+      top = m;
+#pragma unroll
+      for (int k = E - 1; k >= 0; k--)
+        if (s[k] == m) id = v + k;
+    }
   }
   template <bool kSub>
-  __device__ __forceinline__ void vec(const uint4& xr, const uint4& yr, const float4 (&er)[E / 4], int v) {
-    float x[E], y[E];
-    Vec<T>::cvt(xr, x);
-    if (kSub) Vec<T>::cvt(yr, y);
+  __device__ __forceinline__ void vec(const uint4& x, const uint4& y, const float4 (&er)[E / 4], int v) {
+    float s[E];
 #pragma unroll
-    for (int q = 0; q < E / 4; q++) {
-      const float e[4] = {er[q].x, er[q].y, er[q].z, er[q].w};
-#pragma unroll
-      for (int k = 0; k < 4; k++) one(kSub ? pp(x[4 * q + k]) - pq(y[4 * q + k]) : pp(x[4 * q + k]), e[k], v + 4 * q + k);
+    for (int k = 0; k < E / 2; k++) {
+      f2 w = pp(Raw<T>::pair(x, k));
+      if (kSub) {
+        float a, b;
+        unpack2(pq(Raw<T>::pair(y, k)), a, b);
+        w = add2(w, pack2(-a, -b));
+      }
+      const float4 f = er[k / 2];
+      float i0, i1;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i0) : "f"(k & 1 ? f.z : f.x));
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i1) : "f"(k & 1 ? f.w : f.y));
+      unpack2(mul2(w, pack2(i0, i1)), s[2 * k], s[2 * k + 1]);
     }
+    take(s, v);
   }
   // entry v of the row, past the last whole vector
   __device__ __forceinline__ void tail(const T* x, const T* y, const float* e, int v) {
-    one(y ? pp(Vec<T>::get(x + v)) - pq(Vec<T>::get(y + v)) : pp(Vec<T>::get(x + v)), e[v], v);
+    float s[E], w, unused, q = 0.f, i;
+    unpack2(pp(pack2(Vec<T>::get(x + v), 0.f)), w, unused);
+    if (y) unpack2(pq(pack2(Vec<T>::get(y + v), 0.f)), q, unused);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(i) : "f"(e[v]));
+    s[0] = v == out ? 0.f : (w - q) * i;
+    if (s[0] > top) top = s[0], id = v;
   }
   __device__ __forceinline__ unsigned long long key() const { return top > 0.f ? lowest_first(__float_as_uint(top), id) : 0; }
 };
@@ -293,6 +322,7 @@ __global__ void __launch_bounds__(kDecide) k_verify_decide(const __grid_constant
       const float u = draft ? p.u[row] : 0.f;
       d.st = row_stat(p, r, p.c);
       d.y_st = draft && y ? row_stat(p, y0 + r, p.cy) : make_float2(0.f, 0.f);
+      if (d.y_st.x == -INFINITY) d.y_row = -1;   // a draft of nothing takes nothing off
       const float lp = log_p(lx, d.st, p.c), lq = y ? log_p(ly, d.y_st, p.cy) : 0.f;
       if (known && lp == lp && lq == lq && lp != -INFINITY) a = lp >= lq ? 1.f : expf(lp - lq);
       taken = u < a;
@@ -544,7 +574,8 @@ int octo_verify_drafts(octo_plan_t plan, int32_t cur0, int32_t n_cur, const void
   for (int k = 0; k < 2; k++) {
     const double c2 = (double)(k ? draft_inv_temp : inv_temp) * 1.4426950408889634074;
     p.hi[k] = (float)c2;
-    p.lo[k] = c2 < 1e6 ? (float)(c2 - p.hi[k]) : 0.f;   // larger ones times far logits would be inf - inf
+    if (p.hi[k] > c2) p.hi[k] = std::nextafter(p.hi[k], 0.f);
+    p.lo[k] = std::max((float)(c2 - p.hi[k]), FLT_MIN);
   }
   p.row0 = plan->seg_row_base + cur0;
   p.first = first;
