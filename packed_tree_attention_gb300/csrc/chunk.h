@@ -7,16 +7,18 @@
 
 namespace octo {
 
-// Keys of one segment's tokens [c W, c W + W), W the plan's block width, at the positions and
-// visibility that these 32 bytes give.  Slot j is token c W + j.  The row with own index i at
-// position p sees it iff
-//     lo <= j < hi  &&  own0 + j <= i  &&  kpos + j > p - window.
-// own0 is kFarOwn where every row of the tiles that list the block sees it (an ancestor's or a
-// mounted token); kpos is kSinkPos where the tokens are sinks.  A run of tokens whose positions
-// jump, and one that the sinks end in, makes two blocks.
+// Keys of one segment's tokens [c W, c W + W), W the plan's block width, with the visibility that
+// these 32 bytes give.  Slot j is token c W + j.  The row with own index i (at position p) sees it
+// iff  lo <= j < hi  &&  own0 + j <= i  and
+//     without a window  seen <= i,
+//     under one         seen + j > p - window.
+// own0 is kFarOwn where no order between row and key counts (an ancestor's or a mounted token).
+// `seen` is the own index from which on rows see the block (a mount's point); under a window slot
+// 0's position, or kSinkPos where the tokens are sinks: there a run of tokens whose positions jump,
+// and one that the sinks end in, makes two blocks.
 struct ChunkBlock {
   int32_t page[4];   // pages of slots [0, s), [s, 2 s) ..., s = min(page_size, W)
-  int32_t own0, kpos;
+  int32_t own0, seen;
   uint16_t lo, hi;
   int32_t slot0;     // slot 0's place in its page (page 128: 0 or 64)
 };

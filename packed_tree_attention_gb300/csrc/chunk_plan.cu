@@ -25,7 +25,7 @@ namespace octo {
 namespace {
 
 // Rows [row0, row0 + rows) of the plan, and blocks that some of them sees.  Of one cursor: tokens
-// from own index t0 on, at positions own index + shift, no mount among them.  Or of several
+// from own index t0 on (under a window at positions own index + shift, no mount among them).  Or of several
 // cursors next to each other, with blocks of common ancestors, which all of them see (t0 = 0).
 struct ChunkTile {
   int32_t row0, rows, t0, shift;
@@ -45,25 +45,29 @@ struct Level {
 struct Builder {
   const octo_pool_s* pool;
   int32_t P, W, n_sink;
+  bool windowed;
   std::vector<ChunkBlock> out;
 
-  // tokens [a, b) of segment s; own: they are the cursor's own
-  void span(int32_t s, int32_t a, int32_t b, bool own) {
+  // tokens [a, b) of segment s; own: they are the cursor's own; from: see ChunkBlock
+  void span(int32_t s, int32_t a, int32_t b, bool own, int32_t from) {
     const Segment& g = pool->segs[s];
     for (int32_t c = a / W * W; c < b; c += W) {
       const int32_t end = std::min(b, c + W);
       for (int32_t t = std::max(a, c); t < end;) {
-        // the run from t on: positions rise by one, sinks or not
-        const bool sink = g.pos[t] < n_sink;
-        int32_t e = end;
-        if (g.pos[end - 1] - g.pos[t] != end - 1 - t || (sink && g.pos[end - 1] >= n_sink))
-          for (e = t + 1; e < end && g.pos[e] == g.pos[e - 1] + 1 && (g.pos[e] < n_sink) == sink;) e++;
+        int32_t e = end, seen = from;
+        if (windowed) {
+          // the run from t on: positions rise by one, sinks or not
+          const bool sink = g.pos[t] < n_sink;
+          if (g.pos[end - 1] - g.pos[t] != end - 1 - t || (sink && g.pos[end - 1] >= n_sink))
+            for (e = t + 1; e < end && g.pos[e] == g.pos[e - 1] + 1 && (g.pos[e] < n_sink) == sink;) e++;
+          seen = sink ? kSinkPos : g.pos[t] - (t - c);
+        }
         ChunkBlock k;
         const int32_t p0 = c / P;
         for (int i = 0; i < 4; i++) k.page[i] = g.pages[std::min<size_t>(p0 + i, g.pages.size() - 1)];
         k.slot0 = c % P;
         k.own0 = own ? c : kFarOwn;
-        k.kpos = sink ? kSinkPos : g.pos[t] - (t - c);
+        k.seen = seen;
         k.lo = (uint16_t)(t - c);
         k.hi = (uint16_t)(e - c);
         out.push_back(k);
@@ -77,9 +81,9 @@ struct Builder {
     const std::vector<int32_t>& mounts = pool->segs[l.seg].mounts;
     for (int32_t i = 0; i < l.n_mounts; i++) {
       const MountRec& m = pool->mounts[mounts[i]];
-      if (m.m <= l.fork) span(m.producer, m.a, m.b, false);
+      if (m.m <= l.fork) span(m.producer, m.a, m.b, false, 0);
     }
-    span(l.seg, 0, l.fork, false);
+    span(l.seg, 0, l.fork, false, 0);
   }
 };
 
@@ -141,9 +145,11 @@ constexpr int32_t kShareBlocks = 8;
 // Visible (row, key) pairs of a tile's block.
 int64_t block_pairs(const ChunkBlock& k, const ChunkTile& t, int32_t window) {
   const int32_t last = t.t0 + t.rows - 1;
-  auto lo = [&](int32_t i) { return window ? std::max<int32_t>(k.lo, i + t.shift - window + 1 - k.kpos) : (int32_t)k.lo; };
+  auto lo = [&](int32_t i) {
+    return window ? std::max<int32_t>(k.lo, i + t.shift - window + 1 - k.seen) : k.seen <= i ? (int32_t)k.lo : (int32_t)k.hi;
+  };
   auto hi = [&](int32_t i) { return std::min<int32_t>(k.hi, i - k.own0 + 1); };
-  if (hi(t.t0) == k.hi && lo(last) == k.lo) return (int64_t)t.rows * (k.hi - k.lo);
+  if (hi(t.t0) == k.hi && lo(t.t0) == k.lo && lo(last) == k.lo) return (int64_t)t.rows * (k.hi - k.lo);
   int64_t n = 0;
   for (int32_t i = t.t0; i <= last; i++) n += std::max(0, hi(i) - lo(i));
   return n;
@@ -367,7 +373,7 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
                    ((cp->window ? std::min(seen, cp->window + 2 * cp->tokens) : seen) / cp->width + 1) * heads;
   }
   const int32_t cap = most_new > cp->tokens && (!cp->tc || pair_blocks > (int64_t)kPairBlocks * sms) ? 2 * cp->tokens : cp->tokens;
-  Builder b{pool, d.page_size, cp->width, cp->window ? n_sink : 0, {}};
+  Builder b{pool, d.page_size, cp->width, cp->window ? n_sink : 0, cp->window > 0, {}};
   std::vector<ChunkBlock> blocks;
   std::vector<ChunkTile> tiles;
   std::vector<int32_t> row_pos((size_t)rows);
@@ -441,23 +447,25 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
     for (int32_t id : g.mounts) {
       const MountRec& m = pool->mounts[id];
       if (m.m > g.len - 1) continue;
-      // own blocks are cut at a mount, as their positions mostly are: what comes to be seen later
-      // is then listed later
-      if (m.m > next) {
-        b.span(cursors[c], next, m.m, true);
-        next = m.m;
+      // the own tokens before the mount go first: what comes to be seen later is listed later.  Under
+      // a window their block is cut there, where positions jump; without one it goes as a whole, the
+      // tokens behind the mount being hidden from the rows before them
+      const int32_t upto = cp->window ? m.m : std::min(g.len, (m.m + b.W - 1) / b.W * b.W);
+      if (upto > next) {
+        b.span(cursors[c], next, upto, true, 0);
+        next = upto;
       }
       own_from();
-      b.span(m.producer, m.a, m.b, false);
+      b.span(m.producer, m.a, m.b, false, m.m);
       from.resize(b.out.size(), m.m);
-      if (m.m > first) cut.push_back(m.m);
+      if (m.m > first && cp->window) cut.push_back(m.m);
     }
-    if (next < g.len) b.span(cursors[c], next, g.len, true);
+    if (next < g.len) b.span(cursors[c], next, g.len, true, 0);
     own_from();
     cut.push_back(g.len);
     const int32_t base = (int32_t)blocks.size();
     if (!cp->window) blocks.insert(blocks.end(), b.out.begin(), b.out.end());
-    // tiles: pieces without a mount inside
+    // tiles; under a window without a mount inside, so that their positions rise by one
     size_t seen = 0;
     for (int32_t t = first, k = 0; t < g.len;) {
       while (cut[k] <= t) k++;
@@ -472,7 +480,7 @@ int build(octo_pool_s* pool, const octo_cursor_t* cursors, const int32_t* n_new,
         tile.blk0 = (int32_t)blocks.size();
         for (size_t i = 0; i < seen; i++) {
           const ChunkBlock& x = b.out[i];
-          if (x.kpos + x.hi - 1 > g.pos[t] - cp->window) blocks.push_back(x);
+          if (x.seen + x.hi - 1 > g.pos[t] - cp->window) blocks.push_back(x);
         }
         tile.n_blk = (int32_t)blocks.size() - tile.blk0;
       } else {

@@ -103,17 +103,17 @@ __global__ void __launch_bounds__(256) k_chunk_simt(const __grid_constant__ Simt
   // the steps: 64 slots of a block at a time, where some row of the CTA sees one
   struct Step {
     int b, j0, lo, hi;              // slots that some row sees
-    int own0, kpos, k_lo, k_hi;     // of the block
+    int own0, seen, k_lo, k_hi;     // of the block
   };
   auto lowest = [&](const Step& s, int i) {   // slots [lowest, highest) that the row at own index i sees
-    return p.window > 0 ? max(s.k_lo, i + t.shift - p.window + 1 - s.kpos) : s.k_lo;
+    return p.window > 0 ? max(s.k_lo, i + t.shift - p.window + 1 - s.seen) : s.seen <= i ? s.k_lo : s.k_hi;
   };
   auto highest = [&](const Step& s, int i) { return min(s.k_hi, i - s.own0 + 1); };
   auto enter = [&](Step& s) {   // at block s.b or the next one with such a slot
     for (; s.b < t.n; s.b++) {
       const int4 k = *reinterpret_cast<const int4*>(&p.blocks[t.blk + s.b].own0);
-      s.own0 = k.x, s.kpos = k.y, s.k_lo = k.z & 0xffff, s.k_hi = (uint32_t)k.z >> 16;
-      s.lo = lowest(s, first), s.hi = highest(s, last);
+      s.own0 = k.x, s.seen = k.y, s.k_lo = k.z & 0xffff, s.k_hi = (uint32_t)k.z >> 16;
+      s.lo = lowest(s, p.window > 0 ? first : last), s.hi = highest(s, last);
       s.j0 = s.lo / kKeys * kKeys;
       if (s.j0 < s.hi) return;
     }

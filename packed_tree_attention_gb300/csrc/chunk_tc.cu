@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(Shape<D, 1>::kThreads, 1)
     const bool windowed = p.window > 0;
     const int tok_r = r / p.G, h_r = r - tok_r * p.G;
     ChunkWork w = load_work(p.work + w0), next = w;
-    // own0, kpos, lo | hi << 16 of this block, the next and the one after
+    // own0, seen, lo | hi << 16 of this block, the next and the one after
     auto fields = [&](const ChunkWork& x, int j) { return *reinterpret_cast<const int4*>(&p.blocks[x.blk + min(j, x.n - 1)].own0); };
     int4 e, e1, e2;
     int before = 0;   // blocks of the piece before
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(Shape<D, 1>::kThreads, 1)
         if (!(ok = warp_wait(&B->s_full, cnt & 1, B, p.status))) break;
         if (mine) {
           int lo = e.z & 0xffff, hi = (uint32_t)e.z >> 16;
-          const bool full = lo == 0 && hi == 64 && e.x + 63 <= own_first && (!windowed || own_last + w_shift <= e.y);
+          const bool full = lo == 0 && hi == 64 && e.x + 63 <= own_first && (windowed ? own_last + w_shift <= e.y : e.y <= own_first);
           tc_fence_after();
           uint32_t s0[32], s1[32];
           tmem_ld32(tS, s0);
@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(Shape<D, 1>::kThreads, 1)
           }
           if (!full) {
             if (windowed) lo = max(lo, own + w_shift - e.y);
+            else if (own < e.y) lo = 64;
             hi = min(hi, own - e.x + 1);
 #pragma unroll
             for (int k = 0; k < 64; k++)
@@ -687,14 +688,14 @@ __global__ void __launch_bounds__(Shape<D, 2>::kThreads, 1)
       const int w_shift = t.shift - p.window + 1;
       float m_used = -INFINITY, l = 0.f;
       bool ok = true;
-      auto fields = [&](int j) { return *reinterpret_cast<const int4*>(&blk[j].own0); };   // own0, kpos, lo | hi << 16, slot0
+      auto fields = [&](int j) { return *reinterpret_cast<const int4*>(&blk[j].own0); };   // own0, seen, lo | hi << 16, slot0
       int4 next = fields(0);
       for (int j = 0; j < n; j++) {
         const int4 e = next;
         if (j + 1 < n) next = fields(j + 1);
         const int b = j & 1;
         int lo = e.z & 0xffff, hi = (uint32_t)e.z >> 16;
-        const bool full = lo == 0 && hi == 64 && e.x + 63 <= own_first && (!windowed || own_last + w_shift <= e.y);
+        const bool full = lo == 0 && hi == 64 && e.x + 63 <= own_first && (windowed ? own_last + w_shift <= e.y : e.y <= own_first);
         if (!(ok = warp_wait(&B->s_full[hh][b], (j >> 1) & 1, B, p.status))) break;
         tc_fence_after();
         uint32_t s0[32], s1[32];
@@ -709,6 +710,7 @@ __global__ void __launch_bounds__(Shape<D, 2>::kThreads, 1)
         }
         if (!full) {
           if (windowed) lo = max(lo, own + w_shift - e.y);
+          else if (own < e.y) lo = 64;
           hi = min(hi, own - e.x + 1);
 #pragma unroll
           for (int i = 0; i < 64; i++)
