@@ -27,18 +27,10 @@ constexpr int32_t kFarOwn = -(1 << 30);
 constexpr int32_t kSinkPos = 1 << 30;
 constexpr int32_t kMaxPos = 1 << 29;   // positions of a chunk plan: their differences and the above fit 32 bits
 
-// Rows [row0, row0 + rows) of the plan, and blocks that some of them sees.  Of one cursor: tokens
-// from own index t0 on, at positions own index + shift, no mount among them.  Or of several
-// cursors next to each other, with blocks of common ancestors, which all of them see (t0 = 0).
-struct ChunkTile {
-  int32_t row0, rows, t0, shift;
-  int32_t blk0, n_blk;
-  int32_t pad[2];
-};
-
-// A piece of work: blocks [blk, blk + n) of kv head g for rows [row0, row0 + rows), which are as
-// the tile's that it is cut from.  part < 0: all that its rows see, the result is written; else
-// partial results from the part-th on (rows * G of them).
+// A piece of work: blocks [blk, blk + n) of kv head g for rows [row0, row0 + rows) of the plan.  Rows of
+// one cursor: tokens from own index t0 on, under a window at positions own index + shift.  Or of
+// several cursors next to each other, with blocks that all of them see (t0 = 0).  part < 0: all that
+// the rows see, the result is written; else partial results from the part-th on (rows * G of them).
 struct ChunkWork {
   int32_t row0, rows, t0, shift;
   int32_t blk, n, g, part;

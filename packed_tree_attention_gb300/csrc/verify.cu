@@ -5,6 +5,13 @@
 // first rejected one the next token is drawn from max(0, p_r - q_r) / sum, else from p.  A draw
 // from weights w is argmax_v w_v / e_v with e_v ~ Exp(1) independent (the first of exponential
 // clocks of rates w_v), so that neither a sum of the weights nor an order of them is needed.
+//
+//   k_verify_stats   softmax statistics of every row that is needed, in equal runs over all SMs
+//   k_verify_decide  a CTA a cursor: the first rejected draft
+//   k_verify_draw    the race over one row (pair) of each cursor
+// 256 cursors of five rows of 151,936 bf16 logits and four drafts' distributions: 107 us (6.5
+// TB/s), 4 and 48, in one stream 159.  The sums are fp32 of fp32 exponentials; a decision turns
+// where they are off by some 1e-7 of a probability.
 
 #include <algorithm>
 #include <cmath>
