@@ -309,7 +309,10 @@ __global__ void __launch_bounds__(kDecide) k_verify_decide(const __grid_constant
   __shared__ Decision s_dec[kWarps];   // what each warp would decide for the last row that it looked at
   if (tid == 0) s_acc = n - 1;
   __syncthreads();
-  for (int j = warp; j < n && j <= *(volatile int*)&s_acc; j += kWarps) {
+  for (int j = warp;; j += kWarps) {
+    // one reading a warp: lanes that read it apart could part here, before the shuffles of all 32
+    const int limit = __shfl_sync(0xffffffffu, *(volatile int*)&s_acc, 0);
+    if (j >= n || j > limit) break;
     const int r = r0 + j, row = p.first + r + 1;   // row: of the plan, the draft's (j < n - 1)
     const bool draft = j + 1 < n;
     const int id = draft ? p.ids[row] : -1;
@@ -334,6 +337,7 @@ __global__ void __launch_bounds__(kDecide) k_verify_decide(const __grid_constant
       if (known && lp == lp && lq == lq && lp != -INFINITY) a = lp >= lq ? 1.f : expf(lp - lq);
       taken = u < a;
     }
+    taken = __shfl_sync(0xffffffffu, taken, 0);
     if (lane == 0) {
       s_dec[warp] = d;
       if (draft && p.accept_p) p.accept_p[row] = a;
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(DrawShape<T>::kBlock, 1) k_verify_draw(const _
     for (int k = max(0, issued - S::kStages); k < issued; k++) ring_wait(&full[k % S::kStages], (k / S::kStages) & 1, p.status);
     return;
   }
-  auto sync = [] { tc::named_bar_sync(1, S::kConsumers); };
+  auto sync = [] { __syncwarp(), tc::named_bar_sync(1, S::kConsumers); };
   int st = 0, turn = 0;
   uint32_t round = 0;
   bool ok = true;
