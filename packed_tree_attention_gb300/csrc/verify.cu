@@ -7,11 +7,13 @@
 // clocks of rates w_v), so that neither a sum of the weights nor an order of them is needed.
 //
 //   k_verify_stats   softmax statistics of every row that is needed, in equal runs over all SMs
-//   k_verify_decide  a CTA a cursor: the first rejected draft
-//   k_verify_draw    the race over one row (pair) of each cursor
+//   k_verify_decide  greedy: a CTA a cursor, the first rejected draft and the next token
+//   k_verify_draw    sampled: the first rejected draft, then the race over one row (pair) of each
+//                    cursor
 // 256 cursors of five rows of 151,936 bf16 logits and four drafts' distributions: 107 us (6.5
-// TB/s), 4 and 48, in one stream 159.  The sums are fp32 of fp32 exponentials; a decision turns
-// where they are off by some 1e-7 of a probability.
+// TB/s) and 51, in one stream 161.  One cursor: 12.1, most of it the host's (the decision as a
+// kernel of its own: 14.8).  The sums are fp32 of fp32 exponentials; a decision turns where they
+// are off by some 1e-7 of a probability.
 
 #include <algorithm>
 #include <cmath>
@@ -54,7 +56,6 @@ struct VerifyParams {
   float *next_logp, *accept_p;
   float2* stat;               // [n_rows + n_drafted][slots] (m, S) of the target's and the draft's rows
   unsigned long long* best;   // [n_rows][slots] greedy: order_key of the largest logit, ~id
-  Decision* decision;         // [n_cur]
   unsigned long long* drawn;  // [n_cur] best score
   int32_t* done;              // [n_cur] CTAs that are through with the cursor's draw
   int32_t n_rows, n_drafted, n_cur;
@@ -113,6 +114,8 @@ __global__ void __launch_bounds__(kThreads, kHeld) k_verify_stats(const __grid_c
   };
   const T* x = data(row);
   wait_for_predecessor();
+  if (!kGreedy)
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < p.n_cur; i += (int64_t)p.ctas * kThreads) p.drawn[i] = 0, p.done[i] = 0;
   uint4 w[kPer], ahead[kPer];
   auto fetch = [&](const T* from, int ch) {
     const int v = ch * p.per_chunk + tid, end = min((ch + 1) * p.per_chunk, nv);
@@ -286,32 +289,19 @@ struct Race {
   __device__ __forceinline__ unsigned long long key() const { return top > 0.f ? lowest_first(__float_as_uint(top), id) : 0; }
 };
 
-// Which drafts of a cursor are accepted, a warp a draft (and one for the last row); greedy: the
-// next token too.  A chain of dependent loads: bound by latency.
+// One warp's share of a cursor's decision: its rows j = w, w + step, ..., of which all but the last
+// lead to a draft.  *acc: the first rejected draft so far (n - 1: none); dec: what this warp would
+// decide for the last row that it looked at; writes: whether accept_p is this CTA's to write.  A
+// chain of dependent loads: bound by latency.
 template <typename T, bool kGreedy>
-__global__ void __launch_bounds__(kDecide) k_verify_decide(const __grid_constant__ VerifyParams p) {
-  constexpr int kWarps = kDecide / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, i = blockIdx.x;
-  launch_dependents();
+__device__ __forceinline__ void judge(const VerifyParams& p, int i, int w, int step, int* acc, Decision* dec, bool writes) {
+  const int lane = threadIdx.x & 31;
   const int r0 = p.row0[i] - p.first, n = p.row0[i + 1] - p.row0[i];
   const int y0 = p.n_rows - (p.live[i] - p.live0);   // statistics of the draft's row r: y0 + r
-  wait_for_predecessor();
-  if (n == 0) {
-    if (tid == 0) {
-      p.n_accept[i] = 0, p.next_id[i] = -1;
-      if (p.next_logp) p.next_logp[i] = -INFINITY;
-      p.decision[i].row = -1;
-    }
-    return;
-  }
   const T *x = static_cast<const T*>(p.x), *y = static_cast<const T*>(p.y);
-  __shared__ int s_acc;
-  __shared__ Decision s_dec[kWarps];   // what each warp would decide for the last row that it looked at
-  if (tid == 0) s_acc = n - 1;
-  __syncthreads();
-  for (int j = warp;; j += kWarps) {
+  for (int j = w;; j += step) {
     // one reading a warp: lanes that read it apart could part here, before the shuffles of all 32
-    const int limit = __shfl_sync(0xffffffffu, *(volatile int*)&s_acc, 0);
+    const int limit = __shfl_sync(0xffffffffu, *(volatile int*)acc, 0);
     if (j >= n || j > limit) break;
     const int r = r0 + j, row = p.first + r + 1;   // row: of the plan, the draft's (j < n - 1)
     const bool draft = j + 1 < n;
@@ -339,39 +329,62 @@ __global__ void __launch_bounds__(kDecide) k_verify_decide(const __grid_constant
     }
     taken = __shfl_sync(0xffffffffu, taken, 0);
     if (lane == 0) {
-      s_dec[warp] = d;
-      if (draft && p.accept_p) p.accept_p[row] = a;
+      *dec = d;
+      if (draft && writes && p.accept_p) p.accept_p[row] = a;
     }
     if (draft && !taken) {
-      if (lane == 0) atomicMin(&s_acc, j);
+      if (lane == 0) atomicMin(acc, j);
       break;   // what comes after it does not count
     }
   }
-  __syncthreads();
-  const int acc = s_acc, r = r0 + acc;
-  if (p.accept_p) {   // 0 in the first row and behind the first rejected draft
-    if (tid == 0) p.accept_p[p.first + r0] = 0.f;
-    for (int j = acc + 2 + tid; j < n; j += kDecide) p.accept_p[p.first + r0 + j] = 0.f;
+  __syncwarp();
+}
+// Threads t of `step`, when a cursor is judged: accept_p of the first row and behind the first
+// rejected draft is 0; a rejected id out of range is an error.
+__device__ __forceinline__ void judged(const VerifyParams& p, int i, int acc, int t, int step) {
+  const int a = p.row0[i], n = p.row0[i + 1] - a;
+  if (p.accept_p) {
+    if (t == 0 && n > 0) p.accept_p[a] = 0.f;
+    for (int j = acc + 2 + t; j < n; j += step) p.accept_p[a + j] = 0.f;
   }
-  if (tid) return;
-  // row acc was the last that its warp looked at
-  const Decision d = s_dec[acc % kWarps];
-  if (acc + 1 < n) {
-    const int id = p.ids[p.first + r + 1];
+  if (t == 0 && acc + 1 < n) {
+    const int id = p.ids[a + acc + 1];
     if (id < 0 || id >= p.V) atomicExch(p.status, OCTO_EINVAL);
   }
-  if (kGreedy) {
-    p.n_accept[i] = acc, p.next_id[i] = d.out;
-    if (p.next_logp) p.next_logp[i] = d.out < 0 ? -INFINITY : log_p(Vec<T>::get(x + r * p.ld + d.out), d.st, p.c);
-  } else {
-    p.decision[i] = d, p.drawn[i] = 0, p.done[i] = 0;
-  }
+}
+// a cursor without rows, or whose next token is `id`
+template <typename T>
+__device__ __forceinline__ void result(const VerifyParams& p, int i, int acc, int id, int row, float2 st) {
+  p.n_accept[i] = acc, p.next_id[i] = id;
+  if (p.next_logp) p.next_logp[i] = id < 0 ? -INFINITY : log_p(Vec<T>::get(static_cast<const T*>(p.x) + row * p.ld + id), st, p.c);
+}
+
+// Greedy: a CTA a cursor, a warp a row.
+template <typename T>
+__global__ void __launch_bounds__(kDecide) k_verify_decide(const __grid_constant__ VerifyParams p) {
+  constexpr int kWarps = kDecide / 32;
+  const int tid = threadIdx.x, i = blockIdx.x;
+  __shared__ int s_acc;
+  __shared__ Decision s_dec[kWarps];
+  launch_dependents();
+  if (tid == 0) s_acc = p.row0[i + 1] - p.row0[i] - 1;
+  __syncthreads();
+  wait_for_predecessor();
+  judge<T, true>(p, i, tid / 32, kWarps, &s_acc, &s_dec[tid / 32], true);
+  __syncthreads();
+  const int acc = s_acc;   // its warp looked at row acc last
+  judged(p, i, acc, tid, kDecide);
+  if (tid) return;
+  if (acc < 0) result<T>(p, i, 0, -1, 0, make_float2(0.f, 0.f));
+  else result<T>(p, i, acc, s_dec[acc % kWarps].out, s_dec[acc % kWarps].row, s_dec[acc % kWarps].st);
 }
 
 // The draw of the cursors' next tokens: one CTA an SM, each with an equal run of chunks over the
-// cursors' ends.  One thread copies the chunks of logits, the draft's and the noise into a ring
-// (bulk copies, 190 KB under way); 16 warps race over them, a vector a thread, and take what they
-// have of a cursor to its best score; the last CTA of a cursor writes its results.  Bound by HBM.
+// cursors' ends.  First the CTA's cursors are judged, up to 16 at a time, a warp a row; a cursor of
+// several CTAs is judged in each, which takes no longer than a kernel of its own before this one.
+// Then one thread copies the chunks of logits, the draft's and the noise into a ring (bulk copies,
+// 190 KB under way); 16 warps race over them, a vector a thread, and take what they have of a
+// cursor to its best score; the last CTA of a cursor writes its results.  Bound by HBM.
 template <typename T>
 struct DrawShape {
   static constexpr int E = Vec<T>::E;
@@ -385,127 +398,135 @@ struct DrawShape {
 template <typename T>
 __global__ void __launch_bounds__(DrawShape<T>::kBlock, 1) k_verify_draw(const __grid_constant__ VerifyParams p) {
   using S = DrawShape<T>;
-  constexpr int E = S::E;
+  constexpr int E = S::E, kWarps = S::kConsumers / 32;
   extern __shared__ __align__(128) uint8_t sm[];
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::kStages * S::kStage);
   uint64_t* empty = full + S::kStages;
   __shared__ unsigned long long s_best[2], s_all, s_own;
   __shared__ bool s_last;
-  const int tid = threadIdx.x, lane = tid & 31;
+  __shared__ int s_acc[kWarps];
+  __shared__ Decision s_dec[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   launch_dependents();
   if (tid == 0) {
-    for (int k = 0; k < S::kStages; k++) tc::mbar_init(&full[k], 1), tc::mbar_init(&empty[k], S::kConsumers / 32);
+    for (int k = 0; k < S::kStages; k++) tc::mbar_init(&full[k], 1), tc::mbar_init(&empty[k], kWarps);
     tc::fence_mbar_init();
     s_best[0] = s_best[1] = 0;
   }
-  __syncthreads();
-  wait_for_predecessor();
   const int nv = p.V / E;
   const int64_t C = (int64_t)p.n_cur * p.draw_per_row;
   const int64_t x0 = blockIdx.x * C / p.draw_ctas, x1 = (blockIdx.x + 1) * C / p.draw_ctas;
   auto owner = [&](int64_t x) { return (int)(((x + 1) * p.draw_ctas - 1) / C); };
-  int i = (int)(x0 / p.draw_per_row), ch = (int)(x0 - (int64_t)i * p.draw_per_row);
-  if (tid >= S::kConsumers) {
-    if (lane) return;
-    int st = 0, issued = 0;
-    uint32_t round = 0;
-    bool ok = true;
-    Decision d = p.decision[i];
-    for (int64_t at = x0; ok && at < x1; at++) {
-      const int v0 = ch * p.draw_chunk, cnt = min(p.draw_chunk, nv - v0);
-      if (d.row >= 0 && cnt > 0) {
-        if (issued >= S::kStages && !(ok = ring_wait(&empty[st], round ^ 1, p.status))) break;
-        uint8_t* dst = sm + st * S::kStage;
-        const T* x = static_cast<const T*>(p.x) + d.row * p.ld;
-        tc::mbar_expect_tx(&full[st], (uint32_t)cnt * (d.y_row >= 0 ? 32 + 4 * E : 16 + 4 * E));
-        bulk_load(dst, x + (int64_t)v0 * E, cnt * 16, &full[st], true);
-        if (d.y_row >= 0) bulk_load(dst + S::kVec * 16, static_cast<const T*>(p.y) + d.y_row * p.yld + (int64_t)v0 * E, cnt * 16, &full[st], true);
-        bulk_load(dst + S::kVec * 32, p.noise + i * p.eld + (int64_t)v0 * E, cnt * 4 * E, &full[st], true);
-        issued++;
-        if (++st == S::kStages) st = 0, round ^= 1;
-      }
-      if (++ch == p.draw_per_row) {
-        ch = 0, i++;
-        if (at + 1 < x1) d = p.decision[i];
-      }
-    }
-    // what was started has landed before the CTA ends
-    for (int k = max(0, issued - S::kStages); k < issued; k++) ring_wait(&full[k % S::kStages], (k / S::kStages) & 1, p.status);
-    return;
-  }
+  const int first = (int)(x0 / p.draw_per_row), last = (int)((x1 - 1) / p.draw_per_row);
   auto sync = [] { __syncwarp(), tc::named_bar_sync(1, S::kConsumers); };
-  int st = 0, turn = 0;
+  int st = 0, issued = 0, turn = 0;
   uint32_t round = 0;
   bool ok = true;
-  for (int64_t at = x0; at < x1; i++, ch = 0) {
-    const int end = (int)min((int64_t)p.draw_per_row, ch + (x1 - at));
-    at += end - ch;
-    const Decision d = p.decision[i];
-    if (d.row < 0) continue;
-    const T* x = static_cast<const T*>(p.x) + d.row * p.ld;
-    const T* y = d.y_row >= 0 ? static_cast<const T*>(p.y) + d.y_row * p.yld : nullptr;
-    const float* e = p.noise + i * p.eld;
-    Race<T> race;
-    race.start(d, p);
-    for (int k = ch; k < end; k++) {
-      const int v0 = k * p.draw_chunk, cnt = min(p.draw_chunk, nv - v0);
-      if (cnt <= 0) break;
-      if (ok) ok = warp_wait(&full[st], round, p.status);
-      if (ok && tid < cnt) {
-        const uint8_t* src = sm + st * S::kStage;
-        const uint4 xr = reinterpret_cast<const uint4*>(src)[tid];
-        float4 er[E / 4];
-#pragma unroll
-        for (int q = 0; q < E / 4; q++) er[q] = reinterpret_cast<const float4*>(src + S::kVec * 32)[tid * (E / 4) + q];
-        if (y) race.template vec<true>(xr, reinterpret_cast<const uint4*>(src + S::kVec * 16)[tid], er, (v0 + tid) * E);
-        else race.template vec<false>(xr, xr, er, (v0 + tid) * E);
+  for (int i0 = first; i0 <= last; i0 += kWarps) {
+    const int i1 = min(i0 + kWarps, last + 1), each = kWarps / (i1 - i0);   // cursors [i0, i1), warps for each
+    if (tid < i1 - i0) s_acc[tid] = p.row0[i0 + tid + 1] - p.row0[i0 + tid] - 1;
+    __syncthreads();
+    if (i0 == first) wait_for_predecessor();
+    auto first_owner = [&](int i) { return (int64_t)i * p.draw_per_row >= x0; };
+    if (warp < each * (i1 - i0)) judge<T, false>(p, i0 + warp / each, warp % each, each, &s_acc[warp / each], &s_dec[warp], first_owner(i0 + warp / each));
+    __syncthreads();
+    // the chunks of cursor i that are this CTA's: [chunk0, chunk1)
+    auto chunk0 = [&](int i) { return (int)max((int64_t)0, x0 - (int64_t)i * p.draw_per_row); };
+    auto chunk1 = [&](int i) { return (int)min((int64_t)p.draw_per_row, x1 - (int64_t)i * p.draw_per_row); };
+    for (int i = i0; i < i1; i++) {
+      const int acc = s_acc[i - i0];   // its warp looked at row acc last
+      if (acc < 0) continue;
+      const Decision d = s_dec[(i - i0) * each + acc % each];
+      const T* x = static_cast<const T*>(p.x) + d.row * p.ld;
+      const T* y = d.y_row >= 0 ? static_cast<const T*>(p.y) + d.y_row * p.yld : nullptr;
+      const float* e = p.noise + i * p.eld;
+      if (warp == kWarps) {
+        if (lane) continue;
+        for (int ch = chunk0(i); ch < chunk1(i); ch++) {
+          const int v0 = ch * p.draw_chunk, cnt = min(p.draw_chunk, nv - v0);
+          if (cnt <= 0) break;
+          if (ok && issued >= S::kStages) ok = ring_wait(&empty[st], round ^ 1, p.status);
+          if (!ok) break;
+          uint8_t* dst = sm + st * S::kStage;
+          tc::mbar_expect_tx(&full[st], (uint32_t)cnt * (y ? 32 + 4 * E : 16 + 4 * E));
+          bulk_load(dst, x + (int64_t)v0 * E, cnt * 16, &full[st], true);
+          if (y) bulk_load(dst + S::kVec * 16, y + (int64_t)v0 * E, cnt * 16, &full[st], true);
+          bulk_load(dst + S::kVec * 32, e + (int64_t)v0 * E, cnt * 4 * E, &full[st], true);
+          issued++;
+          if (++st == S::kStages) st = 0, round ^= 1;
+        }
+        continue;
       }
-      give_back(&empty[st], race.top);
-      if (++st == S::kStages) st = 0, round ^= 1;
-    }
-    if (end == p.draw_per_row && tid < p.V - nv * E) race.tail(x, y, e, nv * E + tid);
-    unsigned long long best = warp_max(race.key());
-    if (lane == 0 && best) atomicMax(&s_best[turn], best);
-    sync();
-    turn ^= 1;
-    if (tid == 0) {
-      best = s_best[turn ^ 1];
-      s_best[turn] = 0;   // of the cursor before, read by then
-      if (best) atomicMax(&p.drawn[i], best);
-      const int n = owner((int64_t)(i + 1) * p.draw_per_row - 1) - owner((int64_t)i * p.draw_per_row) + 1;
-      __threadfence();
-      s_last = atomicAdd(&p.done[i], 1) == n - 1;
-      __threadfence();
-      s_all = atomicMax(&p.drawn[i], 0ull), s_own = 0;
-    }
-    sync();
-    if (!s_last) continue;
-    best = s_all;
-    if (best == 0 && (d.y_row >= 0 || d.out >= 0)) {
-      // nothing left of p: the target's own
+      Race<T> race;
       race.start(d, p);
-      race.out = -1;
-      for (int v = tid; v < nv; v += S::kConsumers) {
-        const uint4 xr = reinterpret_cast<const uint4*>(x)[v];
-        float4 er[E / 4];
+      const int end = chunk1(i);
+      for (int k = chunk0(i); k < end; k++) {
+        const int v0 = k * p.draw_chunk, cnt = min(p.draw_chunk, nv - v0);
+        if (cnt <= 0) break;
+        if (ok) ok = warp_wait(&full[st], round, p.status);
+        if (ok && tid < cnt) {
+          const uint8_t* src = sm + st * S::kStage;
+          const uint4 xr = reinterpret_cast<const uint4*>(src)[tid];
+          float4 er[E / 4];
 #pragma unroll
-        for (int q = 0; q < E / 4; q++) er[q] = reinterpret_cast<const float4*>(e)[(int64_t)v * (E / 4) + q];
-        race.template vec<false>(xr, xr, er, v * E);
+          for (int q = 0; q < E / 4; q++) er[q] = reinterpret_cast<const float4*>(src + S::kVec * 32)[tid * (E / 4) + q];
+          if (y) race.template vec<true>(xr, reinterpret_cast<const uint4*>(src + S::kVec * 16)[tid], er, (v0 + tid) * E);
+          else race.template vec<false>(xr, xr, er, (v0 + tid) * E);
+        }
+        give_back(&empty[st], race.top);
+        if (++st == S::kStages) st = 0, round ^= 1;
       }
-      if (tid < p.V - nv * E) race.tail(x, nullptr, e, nv * E + tid);
-      best = warp_max(race.key());
-      if (lane == 0 && best) atomicMax(&s_own, best);
+      if (end == p.draw_per_row && tid < p.V - nv * E) race.tail(x, y, e, nv * E + tid);
+      unsigned long long best = warp_max(race.key());
+      if (lane == 0 && best) atomicMax(&s_best[turn], best);
       sync();
-      best = s_own;
+      turn ^= 1;
+      if (tid == 0) {
+        best = s_best[turn ^ 1];
+        s_best[turn] = 0;   // of the cursor before, read by then
+        if (best) atomicMax(&p.drawn[i], best);
+        const int n = owner((int64_t)(i + 1) * p.draw_per_row - 1) - owner((int64_t)i * p.draw_per_row) + 1;
+        __threadfence();
+        s_last = atomicAdd(&p.done[i], 1) == n - 1;
+        __threadfence();
+        s_all = atomicMax(&p.drawn[i], 0ull), s_own = 0;
+      }
+      sync();
+      if (!s_last) continue;
+      best = s_all;
+      if (best == 0 && (d.y_row >= 0 || d.out >= 0)) {
+        // nothing left of p: the target's own
+        race.start(d, p);
+        race.out = -1;
+        for (int v = tid; v < nv; v += S::kConsumers) {
+          const uint4 xr = reinterpret_cast<const uint4*>(x)[v];
+          float4 er[E / 4];
+#pragma unroll
+          for (int q = 0; q < E / 4; q++) er[q] = reinterpret_cast<const float4*>(e)[(int64_t)v * (E / 4) + q];
+          race.template vec<false>(xr, xr, er, v * E);
+        }
+        if (tid < p.V - nv * E) race.tail(x, nullptr, e, nv * E + tid);
+        best = warp_max(race.key());
+        if (lane == 0 && best) atomicMax(&s_own, best);
+        sync();
+        best = s_own;
+      }
+      if (tid == 0) result<T>(p, i, d.acc, best ? id_of(best) : -1, d.row, d.st);
+      sync();   // the shared results are read before the next cursor's
     }
-    if (tid == 0) {
-      const int id = best ? id_of(best) : -1;
-      p.n_accept[i] = d.acc;
-      p.next_id[i] = id;
-      if (p.next_logp) p.next_logp[i] = id < 0 ? -INFINITY : log_p(Vec<T>::get(x + id), d.st, p.c);
-    }
-    sync();   // the shared results are read before the next cursor's
+    // what is left to write of the cursors that begin in this CTA
+    if (warp < kWarps)
+      for (int i = i0 + warp; i < i1; i += kWarps)
+        if (first_owner(i)) {
+          judged(p, i, s_acc[i - i0], lane, 32);
+          if (s_acc[i - i0] < 0 && lane == 0) result<T>(p, i, 0, -1, 0, make_float2(0.f, 0.f));
+        }
+    __syncwarp();
+    __syncthreads();   // the decisions are read before the next ones
   }
+  // what was started has landed before the CTA ends
+  if (tid == S::kConsumers)
+    for (int k = max(0, issued - S::kStages); k < issued; k++) ring_wait(&full[k % S::kStages], (k / S::kStages) & 1, p.status);
 }
 
 int held_ctas() { return kHeld * std::max(1, sm_count()); }
@@ -513,11 +534,10 @@ int held_ctas() { return kHeld * std::max(1, sm_count()); }
 size_t stat_count(int64_t rows) { return (size_t)(held_ctas() + 4 * rows); }
 
 struct Layout {   // of the workspace
-  size_t best, decision, drawn, done, bytes;
+  size_t best, drawn, done, bytes;
   Layout(int64_t rows, int64_t n_cur) {
     best = align_up(stat_count(rows) * sizeof(float2), 256);
-    decision = best + align_up(stat_count(rows) * 8, 256);
-    drawn = decision + align_up((size_t)n_cur * sizeof(Decision), 256);
+    drawn = best + align_up(stat_count(rows) * 8, 256);
     done = drawn + align_up((size_t)n_cur * 8, 256);
     bytes = done + (size_t)n_cur * 4;
   }
@@ -535,8 +555,7 @@ int run(VerifyParams& p, cudaStream_t s) {
     p.slots = (int)(p.ctas / rows + 2);
     if (int st = launch_overlapped((const void*)k_verify_stats<T, kGreedy>, &p, p.ctas, kThreads, 1, 0, s)) return st;
   }
-  if (int st = launch_overlapped((const void*)k_verify_decide<T, kGreedy>, &p, p.n_cur, kDecide, 1, 0, s)) return st;
-  if (kGreedy || rows == 0) return OCTO_OK;
+  if (kGreedy || rows == 0) return launch_overlapped((const void*)k_verify_decide<T>, &p, p.n_cur, kDecide, 1, 0, s);
   using S = DrawShape<T>;
   p.draw_per_row = std::max(1, (nv + S::kVec - 1) / S::kVec);
   p.draw_chunk = (nv + p.draw_per_row - 1) / p.draw_per_row;
@@ -596,7 +615,6 @@ int octo_verify_drafts(octo_plan_t plan, int32_t cur0, int32_t n_cur, const void
   char* w = static_cast<char*>(ws);
   p.stat = reinterpret_cast<float2*>(w);
   p.best = reinterpret_cast<unsigned long long*>(w + at.best);
-  p.decision = reinterpret_cast<octo::Decision*>(w + at.decision);
   p.drawn = reinterpret_cast<unsigned long long*>(w + at.drawn);
   p.done = reinterpret_cast<int32_t*>(w + at.done);
   const std::vector<int32_t>& live = plan->chunk->live;
