@@ -6,14 +6,17 @@
 // from weights w is argmax_v w_v / e_v with e_v ~ Exp(1) independent (the first of exponential
 // clocks of rates w_v), so that neither a sum of the weights nor an order of them is needed.
 //
-//   k_verify_stats   softmax statistics of every row that is needed, in equal runs over all SMs
+//   k_verify_stats   softmax statistics of all rows, in equal runs over all SMs
+//   k_verify_queue   the same where there are many cursors, but for most of what comes behind a
+//                    cursor's first rejected draft
 //   k_verify_decide  greedy: a CTA a cursor, the first rejected draft and the next token
 //   k_verify_draw    sampled: the first rejected draft, then the race over one row (pair) of each
 //                    cursor
-// 256 cursors of five rows of 151,936 bf16 logits and four drafts' distributions: 107 us (6.5
-// TB/s) and 51, in one stream 161.  One cursor: 12.1, most of it the host's (the decision as a
-// kernel of its own: 14.8).  The sums are fp32 of fp32 exponentials; a decision turns where they
-// are off by some 1e-7 of a probability.
+// 256 cursors of five rows of 151,936 bf16 logits and four drafts' distributions (700 MB), 1.36
+// drafts accepted on average: 137 us, of which the draw some 50; with k_verify_stats (106 us, 6.5
+// TB/s) 161.  One cursor: 12.0, most of it the host's (the decision as a kernel of its own: 14.5).
+// The sums are fp32 of fp32 exponentials; a decision turns where they are off by some 1e-7 of a
+// probability.
 
 #include <algorithm>
 #include <cmath>
@@ -31,6 +34,9 @@ constexpr int kThreads = 512;
 constexpr int kHeld = 2;              // CTAs of 512 threads that an SM holds
 constexpr int kChunk = kPer * kThreads;   // vectors that a CTA takes at once, at most
 constexpr int kDecide = 256;          // threads of a cursor's decision
+constexpr int kSummers = kThreads - 32;   // of a CTA of k_verify_queue; its last warp is in control
+constexpr int kAhead = 2;             // units that such a CTA holds
+constexpr int kNone = 0x7fffffff;
 
 // What is decided about a cursor: accepted drafts, the row (of the logits given) of the next
 // token's distribution with its statistics, and what a rejected draft takes off it: the draft's
@@ -58,8 +64,13 @@ struct VerifyParams {
   unsigned long long* best;   // [n_rows][slots] greedy: order_key of the largest logit, ~id
   unsigned long long* drawn;  // [n_cur] best score
   int32_t* done;              // [n_cur] CTAs that are through with the cursor's draw
+  int32_t* rejected;          // [n_cur] first rejected draft so far, kNone: none
+  int32_t* parts_done;        // [n_rows] units of the row, and of the draft's, that are summed
+  int32_t* ticket;            // the next unit but the first ones of all CTAs
   int32_t n_rows, n_drafted, n_cur;
   int32_t per_row, per_chunk, slots, ctas;   // chunks of a row, vectors of a chunk
+  int32_t longest;            // rows of the longest cursor
+  int32_t parts, units;       // queue: units of a row and its draft's (0: no queue), of all with the longest cursor's rows
   int32_t draw_chunk, draw_per_row, draw_ctas;   // vectors of a chunk of the draw, chunks of a row
   int32_t* status;
 
@@ -83,14 +94,44 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
   return v;
 }
 
-// largest entry of a vector, NaNs left out
-__device__ __forceinline__ float vec_max(const uint4& w, __nv_bfloat16) {
-  auto b = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
-  const __nv_bfloat162 m = __hmax2(__hmax2(b(w.x), b(w.y)), __hmax2(b(w.z), b(w.w)));
-  return fmaxf(__low2float(m), __high2float(m));
-}
-__device__ __forceinline__ float vec_max(const uint4& w, float) {
-  return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+// What a warp has of a row, st and the largest logit among its own whole vectors, with the entries
+// past the row's last one where `last`.  Greedy: returns the largest logit with its lowest id, from
+// the chunk that the thread first met it in (of kStride threads); the threads that have the warp's
+// read it again.
+template <typename T, bool kGreedy, int kStride>
+__device__ __forceinline__ unsigned long long warp_total(const VerifyParams& p, const T* x, float c2, bool last, float top, int top_chunk, Stat& st) {
+  constexpr int E = Vec<T>::E;
+  const int tid = threadIdx.x, nv = p.V / E;
+  int top_id = -1;
+  if (kGreedy) {
+    float all = top;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+    if (top_chunk >= 0 && top == all) {
+      const int v = top_chunk * p.per_chunk + tid, end = min((top_chunk + 1) * p.per_chunk, nv);
+      uint4 w[kPer];
+#pragma unroll
+      for (int q = 0; q < kPer; q++) w[q] = v + q * kStride < end ? reinterpret_cast<const uint4*>(x)[v + q * kStride] : Raw<T>::masked();
+#pragma unroll
+      for (int q = kPer - 1; q >= 0; q--) {
+        float f[E];
+        Vec<T>::cvt(w[q], f);
+#pragma unroll
+        for (int e = E - 1; e >= 0; e--)
+          if (f[e] == top) top_id = (v + q * kStride) * E + e;
+      }
+    }
+    __syncwarp();
+  }
+  if (last && tid < p.V - nv * E) {
+    const int i = nv * E + tid;
+    const float v = Vec<T>::get(x + i);
+    if (v > st.m) st.rebase(v, c2);
+    st.add(v, c2);
+    if (kGreedy && v > top) top = v, top_id = i;
+  }
+  warp_merge(st, c2);
+  return kGreedy ? warp_max(top_id >= 0 ? lowest_first(order_key(top), top_id) : 0) : 0;
 }
 
 // Softmax statistics (greedy: and the largest logits) of all rows that are needed: each CTA takes
@@ -132,53 +173,31 @@ __global__ void __launch_bounds__(kThreads, kHeld) k_verify_stats(const __grid_c
     const T* next_x = at + (end - chunk) < x1 ? data(row + 1) : x;
     StageStat<T, false> ss;
     ss.init();
-    float top = -INFINITY;     // largest logit so far, and (greedy) the first vector that has it
-    int top_vec = -1, top_id = -1;
+    float top = -INFINITY;     // largest logit so far, and (greedy) the first chunk that has it
+    int top_chunk = -1;
     for (int ch = chunk; ch < end; ch++) {
 #pragma unroll
       for (int q = 0; q < kPer; q++) w[q] = ahead[q];
       if (ch + 1 < end) fetch(x, ch + 1);
       else if (at + (end - chunk) < x1) fetch(next_x, 0);
       const float mx = Raw<T>::max(w);
-      if (kGreedy && mx > top) {
-#pragma unroll
-        for (int q = 0; q < kPer; q++) {
-          const float m = vec_max(w[q], T());
-          if (m > top) top = m, top_vec = ch * p.per_chunk + tid + q * kThreads;
-        }
-      }
+      if (kGreedy && mx > top) top_chunk = ch;
       top = fmaxf(top, mx);
       ss.add(w, INT_MAX, mx, c2);
     }
-    if (kGreedy && top_vec >= 0) {
-      float v[E];
-      Vec<T>::cvt(reinterpret_cast<const uint4*>(x)[top_vec], v);
-#pragma unroll
-      for (int e = E - 1; e >= 0; e--)
-        if (v[e] == top) top_id = top_vec * E + e;
-    }
     Stat st = ss.total(top, c2);
-    if (end == p.per_row && tid < p.V - nv * E) {   // the entries past the last whole vector
-      const int i = nv * E + tid;
-      const float v = Vec<T>::get(x + i);
-      if (v > st.m) st.rebase(v, c2);
-      st.add(v, c2);
-      if (kGreedy && v > top) top = v, top_id = i;
-    }
-    warp_merge(st, c2);
-    unsigned long long best = 0;
-    if (kGreedy) best = warp_max(top_id >= 0 ? lowest_first(order_key(top), top_id) : 0);
+    const unsigned long long best = warp_total<T, kGreedy, kThreads>(p, x, c2, end == p.per_row, top, top_chunk, st);
     if (lane == 0) part_st[turn][warp] = st, part_top[turn][warp] = best;
     __syncthreads();   // the arrays of the turn before are read by then
     if (warp == 0) {
       st.init();
       if (lane < kThreads / 32) st = part_st[turn][lane];
       warp_merge(st, c2);
-      if (kGreedy) best = warp_max(lane < kThreads / 32 ? part_top[turn][lane] : 0);
+      const unsigned long long all = kGreedy ? warp_max(lane < kThreads / 32 ? part_top[turn][lane] : 0) : 0;
       if (lane == 0) {
         const int64_t o = (int64_t)row * p.slots + (int)blockIdx.x - p.owner((int64_t)row * p.per_row);
         p.stat[o] = make_float2(st.m, st.s);
-        if (kGreedy) p.best[o] = best;
+        if (kGreedy) p.best[o] = all;
       }
     }
     at += end - chunk;
@@ -189,14 +208,18 @@ __global__ void __launch_bounds__(kThreads, kHeld) k_verify_stats(const __grid_c
 // ln p of a logit of a row with largest logit st.x and ln S = st.y (-inf, -inf: no logit above -inf)
 __device__ __forceinline__ float log_p(float x, float2 st, float c) { return st.x == -INFINITY ? -INFINITY : (x - st.x) * c - st.y; }
 
+// Slots of row t of the statistics that are written.
+__device__ __forceinline__ int slots_of(const VerifyParams& p, int t) {
+  return p.parts ? 2 : p.owner((int64_t)(t + 1) * p.per_row - 1) - p.owner((int64_t)t * p.per_row) + 1;
+}
 // One warp: (m, ln S) of row t of the statistics.
 __device__ __forceinline__ float2 row_stat(const VerifyParams& p, int t, float c) {
-  const int lane = threadIdx.x & 31, n = p.owner((int64_t)(t + 1) * p.per_row - 1) - p.owner((int64_t)t * p.per_row) + 1;
+  const int lane = threadIdx.x & 31, n = slots_of(p, t);
   const float c2 = c * kLog2e;
   Stat st;
   st.init();
   for (int i = lane; i < n; i += 32) {
-    const float2 s = p.stat[(int64_t)t * p.slots + i];
+    const float2 s = __ldcg(&p.stat[(int64_t)t * p.slots + i]);   // may be of another CTA of this kernel
     st.merge(s.x, s.y, 0.f, c2);
   }
   warp_merge(st, c2);
@@ -204,9 +227,9 @@ __device__ __forceinline__ float2 row_stat(const VerifyParams& p, int t, float c
 }
 // One warp: the largest logit of a target's row.
 __device__ __forceinline__ unsigned long long row_best(const VerifyParams& p, int t) {
-  const int lane = threadIdx.x & 31, n = p.owner((int64_t)(t + 1) * p.per_row - 1) - p.owner((int64_t)t * p.per_row) + 1;
+  const int lane = threadIdx.x & 31, n = slots_of(p, t);
   unsigned long long b = 0;
-  for (int i = lane; i < n; i += 32) b = max(b, p.best[(int64_t)t * p.slots + i]);
+  for (int i = lane; i < n; i += 32) b = max(b, __ldcg(&p.best[(int64_t)t * p.slots + i]));
   return warp_max(b);
 }
 
@@ -289,6 +312,201 @@ struct Race {
   __device__ __forceinline__ unsigned long long key() const { return top > 0.f ? lowest_first(__float_as_uint(top), id) : 0; }
 };
 
+// One warp: row r against the draft of the row after it (draft: there is one), with probability a;
+// statistics of the draft's row: y0 + r.  Returns whether it is accepted; d: the next token's
+// distribution if the cursor's drafts end here, but d.acc.
+template <typename T, bool kGreedy>
+__device__ __forceinline__ bool weigh(const VerifyParams& p, int r, int y0, bool draft, Decision& d, float& a) {
+  const T *x = static_cast<const T*>(p.x), *y = static_cast<const T*>(p.y);
+  const int row = p.first + r + 1, id = draft ? p.ids[row] : -1;
+  const bool known = id >= 0 && id < p.V;
+  d.row = r, d.y_row = draft && y ? r : -1, d.out = draft && !y ? id : -1;
+  bool taken;
+  a = 0.f;
+  if (kGreedy) {
+    const unsigned long long b = row_best(p, r);
+    d.out = b ? id_of(b) : -1;
+    taken = b && known && id_of(b) == id;
+    a = taken;
+    d.st = row_stat(p, r, p.c);
+  } else {
+    const float lx = known ? Vec<T>::get(x + r * p.ld + id) : 0.f, ly = known && y ? Vec<T>::get(y + r * p.yld + id) : 0.f;
+    const float u = draft ? p.u[row] : 0.f;
+    d.st = row_stat(p, r, p.c);
+    d.y_st = draft && y ? row_stat(p, y0 + r, p.cy) : make_float2(0.f, 0.f);
+    if (d.y_st.x == -INFINITY) d.y_row = -1;   // a draft of nothing takes nothing off
+    const float lp = log_p(lx, d.st, p.c), lq = y ? log_p(ly, d.y_st, p.cy) : 0.f;
+    if (known && lp == lp && lq == lq && lp != -INFINITY) a = lp >= lq ? 1.f : expf(lp - lq);
+    taken = u < a;
+  }
+  return __shfl_sync(0xffffffffu, taken, 0);
+}
+
+// What k_verify_queue counts in, and the draw.
+__global__ void __launch_bounds__(256) k_verify_clear(const __grid_constant__ VerifyParams p) {
+  launch_dependents();
+  wait_for_predecessor();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < p.n_cur) p.rejected[i] = kNone, p.drawn[i] = 0, p.done[i] = 0;
+  if (i < p.n_rows) p.parts_done[i] = 0;
+  if (i == 0) *p.ticket = p.ctas;
+}
+
+// Unit u: cursor, its row j, half of the target's row (half < 2) or of the draft's.
+struct Unit {
+  int i, j, half;
+  __device__ __forceinline__ Unit(const VerifyParams& p, int u) {
+    const int of_row = p.n_cur * p.parts;
+    j = u / of_row, i = (u - j * of_row) / p.parts, half = (u - j * of_row) % p.parts;
+  }
+};
+
+// The statistics where there are many cursors: what a cursor has behind its first rejected draft
+// need not be read.  Units of half a row, the cursors' first rows first, are handed out by a
+// counter; when those of a row and of its draft's distribution are summed, the draft is judged, and
+// the cursor's later units are passed over.  A CTA: 15 warps sum, the next chunk's loads under way;
+// one in control takes the units, joins the warps' results and judges, beside them.  Bound by HBM,
+// with 60 KB an SM under way where k_verify_stats has 64 (512 threads that sum and one warp more
+// leave 56 registers: 145 us where 137), and by what is taken before its cursor is judged.
+template <typename T, bool kGreedy>
+__global__ void __launch_bounds__(kThreads, kHeld) k_verify_queue(const __grid_constant__ VerifyParams p) {
+  constexpr int E = Vec<T>::E, kWarps = kSummers / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ Stat part_st[kAhead][kWarps];
+  __shared__ unsigned long long part_top[kAhead][kWarps];
+  __shared__ uint64_t given[kAhead], summed[kAhead];
+  __shared__ int s_unit[kAhead];   // -1: no more
+  launch_dependents();
+  if (tid == 0) {
+    for (int k = 0; k < kAhead; k++) tc::mbar_init(&given[k], 1), tc::mbar_init(&summed[k], kWarps);
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  wait_for_predecessor();
+  if (warp == kWarps) {
+    // the first unit from u on that has something to sum, or -1
+    auto take = [&](int u) {
+      int at = -1;
+      if (lane == 0)
+        for (; u < p.units; u = atomicAdd(p.ticket, 1)) {
+          const Unit w(p, u);
+          const int n = p.row0[w.i + 1] - p.row0[w.i];
+          if (w.j < n - (w.half >= 2) && w.j <= *(volatile int32_t*)&p.rejected[w.i]) {
+            at = u;
+            break;
+          }
+        }
+      return __shfl_sync(0xffffffffu, at, 0);
+    };
+    auto next = [&] { return take(lane == 0 ? atomicAdd(p.ticket, 1) : 0); };
+    auto give = [&](int k, int u) {
+      if (lane == 0) {
+        s_unit[k] = u;
+        tc::mbar_arrive(&given[k]);
+      }
+    };
+    int unit[kAhead];
+    unit[0] = take(blockIdx.x);
+    give(0, unit[0]);
+    unit[1] = unit[0] < 0 ? -1 : next();
+    give(1, unit[1]);
+    for (int k = 0;; k++) {
+      const int b = k & 1, u = b ? unit[1] : unit[0];
+      if (u < 0 || !warp_wait(&summed[b], (k >> 1) & 1, p.status)) return;
+      const Unit w(p, u);
+      const int r0 = p.row0[w.i] - p.first, n = p.row0[w.i + 1] - p.row0[w.i], y0 = p.n_rows - (p.live[w.i] - p.live0);
+      const float c2 = (w.half < 2 ? p.c : p.cy) * kLog2e;
+      Stat st;
+      st.init();
+      if (lane < kWarps) st = part_st[b][lane];
+      unsigned long long best = kGreedy && lane < kWarps ? part_top[b][lane] : 0;
+      __syncwarp();
+      const int after = (b ? unit[0] : unit[1]) < 0 ? -1 : next();
+      (b ? unit[1] : unit[0]) = after;
+      give(b, after);
+      warp_merge(st, c2);
+      if (kGreedy) best = warp_max(best);
+      const int r = r0 + w.j, t = w.half < 2 ? r : y0 + r;
+      int before = 0;
+      if (lane == 0) {
+        p.stat[(int64_t)t * 2 + (w.half & 1)] = make_float2(st.m, st.s);
+        if (kGreedy) p.best[(int64_t)t * 2 + (w.half & 1)] = best;
+        __threadfence();
+        if (w.j + 1 < n) before = atomicAdd(&p.parts_done[r], 1);
+        __threadfence();
+      }
+      before = __shfl_sync(0xffffffffu, before, 0);
+      __syncwarp();
+      if (w.j + 1 < n && before == p.parts - 1) {
+        Decision d;
+        float a;
+        if (!weigh<T, kGreedy>(p, r, y0, true, d, a) && lane == 0) atomicMin(&p.rejected[w.i], w.j);
+      }
+      __syncwarp();
+    }
+  }
+  const int nv = p.V / E;
+  uint4 w[kPer], ahead[kPer];
+  struct Row {
+    const T* x;
+    float c2;
+    int from, to;   // chunks
+  };
+  auto row_of = [&](int u) {
+    const Unit w(p, u);
+    const int r = p.row0[w.i] - p.first + w.j, h = w.half & 1;
+    Row o;
+    o.x = w.half < 2 ? static_cast<const T*>(p.x) + r * p.ld : static_cast<const T*>(p.y) + r * p.yld;
+    o.c2 = (w.half < 2 ? p.c : p.cy) * kLog2e;
+    o.from = h ? p.per_row / 2 : 0, o.to = h ? p.per_row : p.per_row / 2;
+    return o;
+  };
+  auto fetch = [&](const T* from, int ch) {
+    const int v = ch * p.per_chunk + tid, end = min((ch + 1) * p.per_chunk, nv);
+#pragma unroll
+    for (int q = 0; q < kPer; q++)
+      ahead[q] = v + q * kSummers < end ? __ldcs(reinterpret_cast<const uint4*>(from) + v + q * kSummers) : Raw<T>::masked();
+  };
+  if (!warp_wait(&given[0], 0, p.status) || s_unit[0] < 0) return;
+  Row row = row_of(s_unit[0]), next = row;
+  fetch(row.x, row.from);
+  for (int k = 0;; k++) {
+    const int b = k & 1;
+    bool more = false;
+    StageStat<T, false> ss;
+    ss.init();
+    float top = -INFINITY;
+    int top_chunk = -1;
+    for (int ch = row.from; ch < row.to; ch++) {
+#pragma unroll
+      for (int q = 0; q < kPer; q++) w[q] = ahead[q];
+      if (ch + 1 < row.to) fetch(row.x, ch + 1);
+      else {
+        if (!warp_wait(&given[b ^ 1], ((k + 1) >> 1) & 1, p.status)) return;
+        const int u = s_unit[b ^ 1];
+        more = u >= 0;
+        if (more) {
+          next = row_of(u);
+          fetch(next.x, next.from);
+        }
+      }
+      const float mx = Raw<T>::max(w);
+      if (kGreedy && mx > top) top_chunk = ch;
+      top = fmaxf(top, mx);
+      ss.add(w, INT_MAX, mx, row.c2);
+    }
+    Stat st = ss.total(top, row.c2);
+    const unsigned long long best = warp_total<T, kGreedy, kSummers>(p, row.x, row.c2, row.to == p.per_row, top, top_chunk, st);
+    if (lane == 0) {
+      part_st[b][warp] = st;
+      if (kGreedy) part_top[b][warp] = best;
+      tc::mbar_arrive(&summed[b]);
+    }
+    if (!more) return;
+    row = next;
+  }
+}
+
 // One warp's share of a cursor's decision: its rows j = w, w + step, ..., of which all but the last
 // lead to a draft.  *acc: the first rejected draft so far (n - 1: none); dec: what this warp would
 // decide for the last row that it looked at; writes: whether accept_p is this CTA's to write.  A
@@ -298,36 +516,16 @@ __device__ __forceinline__ void judge(const VerifyParams& p, int i, int w, int s
   const int lane = threadIdx.x & 31;
   const int r0 = p.row0[i] - p.first, n = p.row0[i + 1] - p.row0[i];
   const int y0 = p.n_rows - (p.live[i] - p.live0);   // statistics of the draft's row r: y0 + r
-  const T *x = static_cast<const T*>(p.x), *y = static_cast<const T*>(p.y);
   for (int j = w;; j += step) {
     // one reading a warp: lanes that read it apart could part here, before the shuffles of all 32
     const int limit = __shfl_sync(0xffffffffu, *(volatile int*)acc, 0);
     if (j >= n || j > limit) break;
     const int r = r0 + j, row = p.first + r + 1;   // row: of the plan, the draft's (j < n - 1)
     const bool draft = j + 1 < n;
-    const int id = draft ? p.ids[row] : -1;
-    const bool known = id >= 0 && id < p.V;
     Decision d;
-    d.acc = j, d.row = r, d.y_row = draft && y ? r : -1, d.out = draft && !y ? id : -1;
-    float a = 0.f;
-    bool taken = false;
-    if (kGreedy) {
-      const unsigned long long b = row_best(p, r);
-      d.out = b ? id_of(b) : -1;
-      taken = b && known && id_of(b) == id;
-      a = taken;
-      d.st = row_stat(p, r, p.c);
-    } else {
-      const float lx = known ? Vec<T>::get(x + r * p.ld + id) : 0.f, ly = known && y ? Vec<T>::get(y + r * p.yld + id) : 0.f;
-      const float u = draft ? p.u[row] : 0.f;
-      d.st = row_stat(p, r, p.c);
-      d.y_st = draft && y ? row_stat(p, y0 + r, p.cy) : make_float2(0.f, 0.f);
-      if (d.y_st.x == -INFINITY) d.y_row = -1;   // a draft of nothing takes nothing off
-      const float lp = log_p(lx, d.st, p.c), lq = y ? log_p(ly, d.y_st, p.cy) : 0.f;
-      if (known && lp == lp && lq == lq && lp != -INFINITY) a = lp >= lq ? 1.f : expf(lp - lq);
-      taken = u < a;
-    }
-    taken = __shfl_sync(0xffffffffu, taken, 0);
+    float a;
+    const bool taken = weigh<T, kGreedy>(p, r, y0, draft, d, a);
+    d.acc = j;
     if (lane == 0) {
       *dec = d;
       if (draft && writes && p.accept_p) p.accept_p[row] = a;
@@ -338,6 +536,11 @@ __device__ __forceinline__ void judge(const VerifyParams& p, int i, int w, int s
     }
   }
   __syncwarp();
+}
+// The cursor's row, from 0 on, that its drafts end at for all that is known.
+__device__ __forceinline__ int drafts_to_judge(const VerifyParams& p, int i) {
+  const int last = p.row0[i + 1] - p.row0[i] - 1;
+  return p.parts ? min(last, p.rejected[i]) : last;
 }
 // Threads t of `step`, when a cursor is judged: accept_p of the first row and behind the first
 // rejected draft is 0; a rejected id out of range is an error.
@@ -367,9 +570,9 @@ __global__ void __launch_bounds__(kDecide) k_verify_decide(const __grid_constant
   __shared__ int s_acc;
   __shared__ Decision s_dec[kWarps];
   launch_dependents();
-  if (tid == 0) s_acc = p.row0[i + 1] - p.row0[i] - 1;
-  __syncthreads();
   wait_for_predecessor();
+  if (tid == 0) s_acc = drafts_to_judge(p, i);
+  __syncthreads();
   judge<T, true>(p, i, tid / 32, kWarps, &s_acc, &s_dec[tid / 32], true);
   __syncthreads();
   const int acc = s_acc;   // its warp looked at row acc last
@@ -424,9 +627,9 @@ __global__ void __launch_bounds__(DrawShape<T>::kBlock, 1) k_verify_draw(const _
   bool ok = true;
   for (int i0 = first; i0 <= last; i0 += kWarps) {
     const int i1 = min(i0 + kWarps, last + 1), each = kWarps / (i1 - i0);   // cursors [i0, i1), warps for each
-    if (tid < i1 - i0) s_acc[tid] = p.row0[i0 + tid + 1] - p.row0[i0 + tid] - 1;
-    __syncthreads();
     if (i0 == first) wait_for_predecessor();
+    if (tid < i1 - i0) s_acc[tid] = drafts_to_judge(p, i0 + tid);
+    __syncthreads();
     auto first_owner = [&](int i) { return (int64_t)i * p.draw_per_row >= x0; };
     if (warp < each * (i1 - i0)) judge<T, false>(p, i0 + warp / each, warp % each, each, &s_acc[warp / each], &s_dec[warp], first_owner(i0 + warp / each));
     __syncthreads();
@@ -534,15 +737,24 @@ int held_ctas() { return kHeld * std::max(1, sm_count()); }
 size_t stat_count(int64_t rows) { return (size_t)(held_ctas() + 4 * rows); }
 
 struct Layout {   // of the workspace
-  size_t best, drawn, done, bytes;
+  size_t best, drawn, done, rejected, parts_done, bytes;
   Layout(int64_t rows, int64_t n_cur) {
     best = align_up(stat_count(rows) * sizeof(float2), 256);
     drawn = best + align_up(stat_count(rows) * 8, 256);
     done = drawn + align_up((size_t)n_cur * 8, 256);
-    bytes = done + (size_t)n_cur * 4;
+    rejected = done + (size_t)n_cur * 4;
+    parts_done = rejected + (size_t)n_cur * 4;
+    bytes = parts_done + (size_t)rows * 4 + 4;
   }
 };
 
+// The queue takes rows of four chunks at least (its units are half a row), cursors enough that a
+// row's units come three units' times after those of the row before, drafts enough, and cursors of
+// alike many rows, for the longest one's count of each is handed out.  256 cursors of five rows,
+// 0.5, 1.4 and 4 of four drafts accepted: 126, 137 and 163 us, else 161, 161 and 152; 512 cursors
+// 207, 229 and 306, else 309, 307 and 289; 512 greedily, without drafts' distributions, 1.8 and 4
+// accepted: 100 and 144, else 144.  256 cursors of two rows: 95 and 90, so three rows at least.
+constexpr int kQueueChunks = 4;
 template <typename T, bool kGreedy>
 int run(VerifyParams& p, cudaStream_t s) {
   const int nv = p.V / Vec<T>::E;
@@ -550,7 +762,20 @@ int run(VerifyParams& p, cudaStream_t s) {
   p.per_chunk = (nv + p.per_row - 1) / p.per_row;
   const int64_t rows = (int64_t)p.n_rows + p.n_drafted;
   if (rows > INT32_MAX / 4) return OCTO_EINVAL;
-  if (rows > 0) {
+  p.parts = 0;
+  const int32_t per_row = (nv + kPer * kSummers - 1) / (kPer * kSummers), parts = p.y ? 4 : 2;
+  // (the counter's steps past the end fit)
+  if (per_row >= kQueueChunks && (int64_t)p.n_cur * parts >= 3 * held_ctas() && p.longest > 2 &&
+      (int64_t)p.n_cur * p.longest <= 2LL * p.n_rows && p.n_rows < (1 << 26)) {
+    p.parts = parts;
+    p.units = p.n_cur * p.longest * parts;
+    p.per_row = per_row;
+    p.per_chunk = (nv + per_row - 1) / per_row;
+    p.ctas = held_ctas();
+    p.slots = 2;
+    if (int st = launch_overlapped((const void*)k_verify_clear, &p, (std::max(p.n_rows, p.n_cur) + 255) / 256, 256, 1, 0, s)) return st;
+    if (int st = launch_overlapped((const void*)k_verify_queue<T, kGreedy>, &p, p.ctas, kThreads, 1, 0, s)) return st;
+  } else if (rows > 0) {
     p.ctas = (int)std::min<int64_t>(held_ctas(), p.chunks());
     p.slots = (int)(p.ctas / rows + 2);
     if (int st = launch_overlapped((const void*)k_verify_stats<T, kGreedy>, &p, p.ctas, kThreads, 1, 0, s)) return st;
@@ -617,6 +842,11 @@ int octo_verify_drafts(octo_plan_t plan, int32_t cur0, int32_t n_cur, const void
   p.best = reinterpret_cast<unsigned long long*>(w + at.best);
   p.drawn = reinterpret_cast<unsigned long long*>(w + at.drawn);
   p.done = reinterpret_cast<int32_t*>(w + at.done);
+  p.rejected = reinterpret_cast<int32_t*>(w + at.rejected);
+  p.parts_done = reinterpret_cast<int32_t*>(w + at.parts_done);
+  p.ticket = p.parts_done + n;
+  p.longest = 0;
+  for (int32_t i = cur0; i < cur0 + n_cur; i++) p.longest = std::max(p.longest, plan->chunk->row0[i + 1] - plan->chunk->row0[i]);
   const std::vector<int32_t>& live = plan->chunk->live;
   p.live = plan->chunk->d_live + cur0, p.live0 = live[cur0];
   p.drafted = plan->chunk->drafted + (first - live[cur0]);

@@ -147,6 +147,28 @@ def test_many_cursors(lib):
     check(lib, [1] * 700, 64, "f32", seed=6)
 
 
+@pytest.mark.parametrize("dtype,V", [("f32", 31003), ("bf16", 62003)])
+@pytest.mark.parametrize("draft,near", [(True, 1.0), (True, 0.0), (True, 3.0), (False, 1.0)])
+def test_many_cursors_of_a_large_vocabulary(lib, dtype, V, draft, near):
+    """Enough of both that rows behind a rejected draft are passed over; all drafts accepted (near 0), few, ragged cursors."""
+    n = 230 if draft else 460
+    check(lib, [(1, 3, 2, 0, 3, 3, 2)[i % 7] for i in range(n)], V, dtype, masked=0.2 if near == 1 else 0, draft=draft, seed=15, near=near)
+
+
+def test_many_cursors_greedily(lib):
+    rng = np.random.default_rng(16)
+    V, rows = 31003, [(2, 3, 1, 3)[i % 4] for i in range(470)]
+    x = np.round(rng.standard_normal((sum(rows), V)) * 3)    # ties: the lowest id
+    xt, xr = on_gpu(x, "f32")
+    ids = np.where(rng.random(len(x)) < 0.7, np.roll(np.argmax(xr, axis=1), 1), 5)
+    plan = chunk_plan(lib, rows)
+    got = run(plan, rows, V, xt, ids, c=0.7)
+    plan.sync()
+    ref = ov.verify(xr, rows, ids, c=0.7)
+    assert np.array_equal(got[0], ref[0]) and np.array_equal(got[1], ref[1]) and np.array_equal(got[3], ref[3])
+    close(got[2], ref[2], "next_logp")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_greedy(lib, dtype):
     rng = np.random.default_rng(7)
