@@ -152,12 +152,12 @@ def test_many_cursors(lib):
 def test_many_cursors_of_a_large_vocabulary(lib, dtype, V, draft, near):
     """Enough of both that rows behind a rejected draft are passed over; all drafts accepted (near 0), few, ragged cursors."""
     n = 230 if draft else 460
-    check(lib, [(1, 3, 2, 0, 3, 3, 2)[i % 7] for i in range(n)], V, dtype, masked=0.2 if near == 1 else 0, draft=draft, seed=15, near=near)
+    check(lib, [(1, 4, 3, 0, 4, 4, 3)[i % 7] for i in range(n)], V, dtype, masked=0.2 if near == 1 else 0, draft=draft, seed=15, near=near)
 
 
 def test_many_cursors_greedily(lib):
     rng = np.random.default_rng(16)
-    V, rows = 31003, [(2, 3, 1, 3)[i % 4] for i in range(470)]
+    V, rows = 31003, [(3, 4, 1, 4)[i % 4] for i in range(470)]
     x = np.round(rng.standard_normal((sum(rows), V)) * 3)    # ties: the lowest id
     xt, xr = on_gpu(x, "f32")
     ids = np.where(rng.random(len(x)) < 0.7, np.roll(np.argmax(xr, axis=1), 1), 5)
