@@ -568,10 +568,10 @@ __global__ void __launch_bounds__(Shape<D, 2>::kThreads, 1)
         mbar_init(&B->kv_full[s], 1);
         mbar_init(&B->kv_empty[s], n_slots);   // released by the slots' P V
       }
-      for (int h = 0; h < n_slots; h++)
+      for (int h = 0; h < kSlots; h++)       // those of a slot without rows too: invalidate() takes all
         for (int b = 0; b < 2; b++) {
           mbar_init(&B->s_full[h][b], 1);
-          mbar_init(&B->p_full[h][b], (slot_rows(h) + 31) / 32 * 32);
+          mbar_init(&B->p_full[h][b], h < n_slots ? (slot_rows(h) + 31) / 32 * 32 : 1);
           mbar_init(&B->o_done[h][b], 1);
         }
       mbar_init(&B->drain, n_slots);
@@ -770,6 +770,8 @@ __global__ void __launch_bounds__(Shape<D, 2>::kThreads, 1)
         mbar_arrive(&B->p_full[hh][b]);
       }
       // ---------------- results ----------------
+      // both buffers' last commits: an arrival still to come may not meet the barriers made anew
+      if (ok && n > 1) ok = warp_wait(&B->o_done[hh][(n - 2) & 1], ((n - 2) >> 1) & 1, B, p.status);
       if (ok && warp_wait(&B->o_done[hh][(n - 1) & 1], ((n - 1) >> 1) & 1, B, p.status)) {
         tc_fence_after();
         const int tok = hh * p.T + min(r, R - 1) / p.G, h = min(r, R - 1) % p.G;

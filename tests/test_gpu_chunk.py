@@ -536,3 +536,26 @@ def test_one_chunk_is_its_tokens_one_by_one(lib):
     plan.sync()
     # both round P to at most bf16 and the output once: 2^-8 (|o| + A) each, A < 1 for means of randn
     assert torch.all((out.float() - one.float()).abs() <= 2.0 ** -7 * (one.float().abs() + 1))
+
+
+@pytest.mark.parametrize("G,Hkv,d,P", [(4, 8, 128, 64), (2, 8, 64, 16)])
+def test_pieces_of_one_and_two_slots_in_turn(lib, oracle_mod, G, Hkv, d, P):
+    """CTAs that take short chunks behind long contexts (one slot of 128 rows) and long chunks of few blocks (two slots, one to a
+    handful of blocks) one after the other, under a window in another order: each piece's barriers are made anew."""
+    T = 128 // G
+    ep = synth.Episode(P)
+    cur, n_new = [], []
+    for i in range(60):
+        r = ep.root()
+        long = i % 2
+        n = (2 * T, 3 * T + 1, 6 * T - 2, T + 1)[i // 2 % 4] if long else 1 + i % T
+        ep.append(r, n if long else 700 + 130 * (i % 5) + n)
+        cur.append(r), n_new.append(n)
+    case = Case(lib, oracle_mod, ep, G, Hkv, d, "bf16")
+    plan, q, out, lse = case.check(cur, n_new)
+    assert plan.info["bm"] == 2 * T and plan.info["max_tile_entries"] >= 19
+    for _ in range(20):
+        again, lse2 = case.run(plan, q, 1 / math.sqrt(d))
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+    case.check(cur, n_new, window=T + 3, sink=2)
+    case.check(cur[::-1], n_new[::-1], window=500)
