@@ -577,8 +577,9 @@ int octo_chunk_attn(octo_plan_t plan, const void* q, const void* k_pool, const v
  * the target's own.  draft_logits NULL: the drafts are certain (q = 1 at the drafted token), the
  * rejected one is left out.  u and noise NULL: greedy, a draft is accepted iff it is the
  * largest logit's lowest id, which is the next token too (inv_temp then only enters next_logp;
- * draft_logits must be NULL).  Masked logits are -inf.  A NaN in a row that is needed makes its draft
- * rejected and is never drawn. */
+ * draft_logits must be NULL).  Masked logits are -inf.  A NaN in a row that is needed,
+ * greedily too, makes its draft rejected, and no token is drawn from such a row of the target's.  So
+ * does a +inf, but not greedily: there it is the largest logit (next_logp is then NaN). */
 
 /* Workspace (bytes) for octo_verify_drafts over cursors [cur0, cur0 + n_cur). */
 int octo_verify_drafts_workspace_size(octo_plan_t plan, int32_t cur0, int32_t n_cur, size_t* bytes);

@@ -5,7 +5,8 @@ Row r of a cursor leads to the draft in row r + 1.  With p = softmax(c x_r), q =
     next token after the first rejected one: argmax max(0, p - q) / noise (without draft logits p
     with the rejected id left out), p / noise where nothing is left or all were accepted; the lowest
     id among equal ones.
-Greedy (u, noise None): accepted iff id is the largest logit's lowest id."""
+Greedy (u, noise None): accepted iff id is the largest logit's lowest id.  A row with a NaN has its draft
+rejected and gives no token."""
 from __future__ import annotations
 
 import numpy as np
@@ -16,6 +17,11 @@ from .token_score import log_softmax
 def _first(score):
     score = np.where(np.isnan(score), 0.0, score)
     return int(np.argmax(score)) if score.max() > 0 else -1
+
+
+def _largest(x):
+    """Lowest id of the largest logit; -1 where none is above -inf or one is NaN."""
+    return -1 if np.isnan(x).any() or not x.max(initial=-np.inf) > -np.inf else int(np.argmax(x))
 
 
 def verify(x, rows, ids, y=None, u=None, noise=None, c=1.0, cq=1.0):
@@ -37,7 +43,7 @@ def verify(x, rows, ids, y=None, u=None, noise=None, c=1.0, cq=1.0):
             if t < 0 or t >= x.shape[1]:
                 a, t = 0.0, -1
             elif greedy:
-                a = float(np.nanmax(x[r]) > -np.inf and int(np.argmax(np.where(np.isnan(x[r]), -np.inf, x[r]))) == t)
+                a = float(_largest(x[r]) == t)
             else:
                 with np.errstate(invalid="ignore", over="ignore"):
                     a = 0.0 if lp[r, t] == -np.inf else float(np.exp(min(0.0, lp[r, t] - (lq[r, t] if lq is not None else 0.0))))
@@ -59,7 +65,7 @@ def verify(x, rows, ids, y=None, u=None, noise=None, c=1.0, cq=1.0):
             break
         p = np.exp(lp[r])
         if greedy:
-            best = int(np.argmax(np.where(np.isnan(x[r]), -np.inf, x[r]))) if np.nanmax(x[r], initial=-np.inf) > -np.inf else -1
+            best = _largest(x[r])
         else:
             best = -1 if w is None else _first(w / noise[i])
             if best < 0:

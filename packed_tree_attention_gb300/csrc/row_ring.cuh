@@ -173,14 +173,16 @@ struct Raw<__nv_bfloat16> {
     const uint32_t u = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
     return pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   }
-  // largest entry, NaNs left out
+  // largest entry, NaNs left out, or NaN where one of them is (kNan)
+  template <bool kNan = false>
   __device__ __forceinline__ static float max(const uint4 (&w)[kPer]) {
     auto b = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
-    auto h = [&](const uint4& v) { return __hmax2(__hmax2(b(v.x), b(v.y)), __hmax2(b(v.z), b(v.w))); };
+    auto of = [](__nv_bfloat162 x, __nv_bfloat162 y) { return kNan ? __hmax2_nan(x, y) : __hmax2(x, y); };
+    auto h = [&](const uint4& v) { return of(of(b(v.x), b(v.y)), of(b(v.z), b(v.w))); };
     __nv_bfloat162 m = h(w[0]);
 #pragma unroll
-    for (int q = 1; q < kPer; q++) m = __hmax2(m, h(w[q]));
-    return fmaxf(__low2float(m), __high2float(m));
+    for (int q = 1; q < kPer; q++) m = of(m, h(w[q]));
+    return kNan ? max_nan(__low2float(m), __high2float(m)) : fmaxf(__low2float(m), __high2float(m));
   }
   // entries below -2^100 raised to it, NaNs kept
   __device__ __forceinline__ static uint4 floored(const uint4& w) {
@@ -199,12 +201,13 @@ struct Raw<float> {
   __device__ __forceinline__ static f2 pair(const uint4& w, int i) {
     return i == 0 ? pack2(__uint_as_float(w.x), __uint_as_float(w.y)) : pack2(__uint_as_float(w.z), __uint_as_float(w.w));
   }
+  template <bool kNan = false>
   __device__ __forceinline__ static float max(const uint4 (&w)[kPer]) {
+    auto of = [](float x, float y) { return kNan ? max_nan(x, y) : fmaxf(x, y); };
     float m = -INFINITY;
 #pragma unroll
     for (int q = 0; q < kPer; q++)
-      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(w[q].x), __uint_as_float(w[q].y)),
-                         fmaxf(__uint_as_float(w[q].z), __uint_as_float(w[q].w))));
+      m = of(m, of(of(__uint_as_float(w[q].x), __uint_as_float(w[q].y)), of(__uint_as_float(w[q].z), __uint_as_float(w[q].w))));
     return m;
   }
   __device__ __forceinline__ static uint4 floored(const uint4& w) {

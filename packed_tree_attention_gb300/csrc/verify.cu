@@ -87,6 +87,8 @@ struct VerifyParams {
 __device__ __forceinline__ unsigned long long lowest_first(uint32_t key, int v) {
   return (unsigned long long)key << 32 | (0xffffffffu - (uint32_t)v);
 }
+// Greedy: a row with a NaN, above every value's key.
+constexpr unsigned long long kNanRow = ~0ull;
 __device__ __forceinline__ int id_of(unsigned long long k) { return (int)(0xffffffffu - (uint32_t)k); }
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 #pragma unroll
@@ -97,9 +99,9 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 // What a warp has of a row, st and the largest logit among its own whole vectors, with the entries
 // past the row's last one where `last`.  Greedy: returns the largest logit with its lowest id, from
 // the chunk that the thread first met it in (of kStride threads); the threads that have the warp's
-// read it again.
+// read it again.  nan: the thread met one.
 template <typename T, bool kGreedy, int kStride>
-__device__ __forceinline__ unsigned long long warp_total(const VerifyParams& p, const T* x, float c2, bool last, float top, int top_chunk, Stat& st) {
+__device__ __forceinline__ unsigned long long warp_total(const VerifyParams& p, const T* x, float c2, bool last, float top, int top_chunk, bool nan, Stat& st) {
   constexpr int E = Vec<T>::E;
   const int tid = threadIdx.x, nv = p.V / E;
   int top_id = -1;
@@ -129,9 +131,10 @@ __device__ __forceinline__ unsigned long long warp_total(const VerifyParams& p, 
     if (v > st.m) st.rebase(v, c2);
     st.add(v, c2);
     if (kGreedy && v > top) top = v, top_id = i;
+    nan |= v != v;
   }
   warp_merge(st, c2);
-  return kGreedy ? warp_max(top_id >= 0 ? lowest_first(order_key(top), top_id) : 0) : 0;
+  return kGreedy ? warp_max(nan ? kNanRow : top_id >= 0 ? lowest_first(order_key(top), top_id) : 0) : 0;
 }
 
 // Softmax statistics (greedy: and the largest logits) of all rows that are needed: each CTA takes
@@ -175,18 +178,20 @@ __global__ void __launch_bounds__(kThreads, kHeld) k_verify_stats(const __grid_c
     ss.init();
     float top = -INFINITY;     // largest logit so far, and (greedy) the first chunk that has it
     int top_chunk = -1;
+    bool nan = false;          // (greedy) met one
     for (int ch = chunk; ch < end; ch++) {
 #pragma unroll
       for (int q = 0; q < kPer; q++) w[q] = ahead[q];
       if (ch + 1 < end) fetch(x, ch + 1);
       else if (at + (end - chunk) < x1) fetch(next_x, 0);
-      const float mx = Raw<T>::max(w);
+      const float mx = Raw<T>::template max<kGreedy>(w);
       if (kGreedy && mx > top) top_chunk = ch;
+      if (kGreedy) nan |= mx != mx;
       top = fmaxf(top, mx);
       ss.add(w, INT_MAX, mx, c2);
     }
     Stat st = ss.total(top, c2);
-    const unsigned long long best = warp_total<T, kGreedy, kThreads>(p, x, c2, end == p.per_row, top, top_chunk, st);
+    const unsigned long long best = warp_total<T, kGreedy, kThreads>(p, x, c2, end == p.per_row, top, top_chunk, nan, st);
     if (lane == 0) part_st[turn][warp] = st, part_top[turn][warp] = best;
     __syncthreads();   // the arrays of the turn before are read by then
     if (warp == 0) {
@@ -225,7 +230,7 @@ __device__ __forceinline__ float2 row_stat(const VerifyParams& p, int t, float c
   warp_merge(st, c2);
   return st.s == 0.f ? make_float2(-INFINITY, -INFINITY) : make_float2(st.m, logf(st.s));
 }
-// One warp: the largest logit of a target's row.
+// One warp: the largest logit of a target's row (0: none above -inf).
 __device__ __forceinline__ unsigned long long row_best(const VerifyParams& p, int t) {
   const int lane = threadIdx.x & 31, n = slots_of(p, t);
   unsigned long long b = 0;
@@ -325,8 +330,8 @@ __device__ __forceinline__ bool weigh(const VerifyParams& p, int r, int y0, bool
   a = 0.f;
   if (kGreedy) {
     const unsigned long long b = row_best(p, r);
-    d.out = b ? id_of(b) : -1;
-    taken = b && known && id_of(b) == id;
+    d.out = b && b != kNanRow ? id_of(b) : -1;
+    taken = known && d.out == id;
     a = taken;
     d.st = row_stat(p, r, p.c);
   } else {
@@ -477,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, kHeld) k_verify_queue(const __grid_c
     ss.init();
     float top = -INFINITY;
     int top_chunk = -1;
+    bool nan = false;          // (greedy) met one
     for (int ch = row.from; ch < row.to; ch++) {
 #pragma unroll
       for (int q = 0; q < kPer; q++) w[q] = ahead[q];
@@ -490,13 +496,14 @@ __global__ void __launch_bounds__(kThreads, kHeld) k_verify_queue(const __grid_c
           fetch(next.x, next.from);
         }
       }
-      const float mx = Raw<T>::max(w);
+      const float mx = Raw<T>::template max<kGreedy>(w);
       if (kGreedy && mx > top) top_chunk = ch;
+      if (kGreedy) nan |= mx != mx;
       top = fmaxf(top, mx);
       ss.add(w, INT_MAX, mx, row.c2);
     }
     Stat st = ss.total(top, row.c2);
-    const unsigned long long best = warp_total<T, kGreedy, kSummers>(p, row.x, row.c2, row.to == p.per_row, top, top_chunk, st);
+    const unsigned long long best = warp_total<T, kGreedy, kSummers>(p, row.x, row.c2, row.to == p.per_row, top, top_chunk, nan, st);
     if (lane == 0) {
       part_st[b][warp] = st;
       if (kGreedy) part_top[b][warp] = best;

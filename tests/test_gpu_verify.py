@@ -350,3 +350,40 @@ def test_refusals(lib):
     call(n_cur=0, x=xt[:0])
     call()
     plan.sync()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("many", [False, True])
+def test_greedy_rows_with_a_nan(lib, dtype, many):
+    """A NaN anywhere in a row that is needed, a +inf beside it or not: its draft is rejected and no token is drawn.  A +inf without one is
+    the largest logit.  Few cursors, and enough of a large vocabulary that rows behind a rejected draft are passed over."""
+    V = (24007 if dtype == "f32" else 48011) if many else 1003
+    n_cur, n = 480 if many else 40, 4
+    N = n_cur * n
+    g = torch.Generator(device="cuda").manual_seed(17)
+    x = torch.full((N, -(-V // 8) * 8 + 8), float("nan"), dtype=DT[dtype], device="cuda")
+    for r0 in range(0, N, 256):
+        x[r0:r0 + 256, :V] = torch.randn((min(256, N - r0), V), generator=g, device="cuda").to(DT[dtype])
+    rng = np.random.default_rng(18)
+    top = rng.integers(0, V - 1, N)
+    x[torch.arange(N), torch.from_numpy(top)] = 40.0
+    ids = np.concatenate([[0], top[:-1]]).astype(np.int32)
+    acc, nxt, ap, logp = [], [], np.zeros(N, dtype=np.float32), []
+    for i in range(n_cur):
+        j, kind = int(rng.integers(0, n)), i % 6
+        r = i * n + j
+        if kind in (3, 4):
+            x[r, top[r]] = float("inf")
+        if kind in (1, 2, 3, 5):
+            x[r, {1: int(rng.integers(0, V)), 2: V - 1, 3: top[r] ^ 1 if top[r] ^ 1 < V else top[r] - 1, 5: top[r]}[kind]] = float("nan")
+        k = j if kind in (1, 2, 3, 5) else n - 1
+        acc.append(k)
+        nxt.append(-1 if kind in (1, 2, 3, 5) else top[i * n + n - 1])
+        ap[i * n + 1:i * n + k + 1] = 1
+        logp.append(-np.inf if nxt[-1] < 0 else np.nan if kind == 4 and j == n - 1 else 0.0)
+    plan = chunk_plan(lib, [n] * n_cur)
+    got = run(plan, [n] * n_cur, V, x, ids)
+    plan.sync()
+    assert got[0].tolist() == acc and got[1].tolist() == nxt and np.array_equal(got[3], ap)
+    # the other V - 1 logits take less than V e^(5.5 - 40) of the mass
+    assert np.allclose(got[2], logp, rtol=0, atol=1e-6, equal_nan=True)
