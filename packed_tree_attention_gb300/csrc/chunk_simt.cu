@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(256) k_chunk_simt(const __grid_constant__ Simt
         const float4 v = columns(c);
         store4(static_cast<T*>(p.out) + at * D + 64 * c + 4 * tx, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
       }
-      if (tx == 0 && p.lse) p.lse[at] = sum > 0.f ? (m[i] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      if (tx == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (m[i] + log2f(sum)) * 0.69314718055994531f;   // NaN: NaN
     }
   }
 }
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(256) k_chunk_join(const ChunkJoin* joins, cons
     else
       *reinterpret_cast<float2*>(dst) = make_float2(o[e] * inv, o[e + 1] * inv);
   }
-  if (lane == 0 && lse) lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  if (lane == 0 && lse) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;   // NaN: NaN
 }
 
 template <typename T, int D, int RM>

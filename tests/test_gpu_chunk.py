@@ -559,3 +559,22 @@ def test_pieces_of_one_and_two_slots_in_turn(lib, oracle_mod, G, Hkv, d, P):
         assert torch.equal(out, again) and torch.equal(lse, lse2)
     case.check(cur, n_new, window=T + 3, sink=2)
     case.check(cur[::-1], n_new[::-1], window=500)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("lens,n", [((100, 5), 5), ((5000, 7), 7), ((900, 5), 1), ((1500,), 1500)], ids=str)
+def test_lse_of_a_nan_row(lib, oracle_mod, dtype, d, lens, n):
+    """NaN, as octo_decode gives it, whether the row's tile is cut and joined or not; the other rows are what they were."""
+    ep, c = chain(64, *lens)
+    case = Case(lib, oracle_mod, ep, 4, 1, d, dtype)
+    q = case.queries([c], [n], 8)
+    for window in (0, 150):
+        plan = case.pool.chunk_plan([c], [n], 4, window=window)
+        want, lse = case.run(plan, q, 1 / math.sqrt(d))
+        bad = q.clone()
+        bad[n // 2, 1:3] = float("nan")
+        out, lse2 = case.run(plan, bad, 1 / math.sqrt(d))
+        is_bad = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+        is_bad[n // 2, 1:3] = True
+        assert torch.isnan(out[is_bad]).all() and torch.isnan(lse2[is_bad]).all()
+        assert torch.equal(out[~is_bad], want[~is_bad]) and torch.equal(lse2[~is_bad], lse[~is_bad])
