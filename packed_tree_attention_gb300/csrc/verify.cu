@@ -16,7 +16,7 @@
 // drafts accepted on average: 136 us, of which the draw some 50; with k_verify_stats (106 us, 6.5
 // TB/s) 161.  One cursor: 12.0, most of it the host's (the decision as a kernel of its own: 14.5).
 // The sums are fp32 of fp32 exponentials; a decision turns where they are off by some 1e-7 of a
-// probability.
+// probability, for the exponents that its ratio is made of are kept in two parts.
 
 #include <algorithm>
 #include <cmath>
@@ -213,12 +213,28 @@ __global__ void __launch_bounds__(kThreads, kHeld) k_verify_stats(const __grid_c
 // ln p of a logit of a row with largest logit st.x and ln S = st.y (-inf, -inf: no logit above -inf)
 __device__ __forceinline__ float log_p(float x, float2 st, float c) { return st.x == -INFINITY ? -INFINITY : (x - st.x) * c - st.y; }
 
+// (x - m) c in two parts, to some 2^-46 of it: the difference and the product with their errors.
+__device__ __forceinline__ float2 scaled_difference(float x, float m, float c) {
+  const float d = __fsub_rn(x, m), b = __fsub_rn(d, x);
+  const float err = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(m, b));
+  const float h = __fmul_rn(d, c);
+  return make_float2(h, fmaf(err, c, fmaf(d, c, -h)));
+}
+// p / q = e^(ex - ey) sy / sx, ex and ey such differences: the difference of two fp32 logarithms at
+// -100 would leave 1e-5 of it.
+__device__ __forceinline__ float ratio(float2 ex, float sx, float2 ey, float sy) {
+  const float h = __fsub_rn(ex.x, ey.x), b = __fsub_rn(h, ex.x);
+  const float err = __fsub_rn(__fsub_rn(ex.x, __fsub_rn(h, b)), __fadd_rn(ey.x, b));
+  const float l = err + (ex.y - ey.y);
+  return expf(h) * (1.f + l) * (sy / sx);
+}
+
 // Slots of row t of the statistics that are written.
 __device__ __forceinline__ int slots_of(const VerifyParams& p, int t) {
   return p.parts ? 2 : p.owner((int64_t)(t + 1) * p.per_row - 1) - p.owner((int64_t)t * p.per_row) + 1;
 }
-// One warp: (m, ln S) of row t of the statistics.
-__device__ __forceinline__ float2 row_stat(const VerifyParams& p, int t, float c) {
+// One warp: (m, ln S) of row t of the statistics; sum: S.
+__device__ __forceinline__ float2 row_stat(const VerifyParams& p, int t, float c, float& sum) {
   const int lane = threadIdx.x & 31, n = slots_of(p, t);
   const float c2 = c * kLog2e;
   Stat st;
@@ -228,6 +244,7 @@ __device__ __forceinline__ float2 row_stat(const VerifyParams& p, int t, float c
     st.merge(s.x, s.y, 0.f, c2);
   }
   warp_merge(st, c2);
+  sum = st.s;
   return st.s == 0.f ? make_float2(-INFINITY, -INFINITY) : make_float2(st.m, logf(st.s));
 }
 // One warp: the largest logit of a target's row (0: none above -inf).
@@ -327,21 +344,27 @@ __device__ __forceinline__ bool weigh(const VerifyParams& p, int r, int y0, bool
   const bool known = id >= 0 && id < p.V;
   d.row = r, d.y_row = draft && y ? r : -1, d.out = draft && !y ? id : -1;
   bool taken;
+  float sx, sy = 1.f;
   a = 0.f;
   if (kGreedy) {
     const unsigned long long b = row_best(p, r);
     d.out = b && b != kNanRow ? id_of(b) : -1;
     taken = known && d.out == id;
     a = taken;
-    d.st = row_stat(p, r, p.c);
+    d.st = row_stat(p, r, p.c, sx);
   } else {
     const float lx = known ? Vec<T>::get(x + r * p.ld + id) : 0.f, ly = known && y ? Vec<T>::get(y + r * p.yld + id) : 0.f;
     const float u = draft ? p.u[row] : 0.f;
-    d.st = row_stat(p, r, p.c);
-    d.y_st = draft && y ? row_stat(p, y0 + r, p.cy) : make_float2(0.f, 0.f);
+    d.st = row_stat(p, r, p.c, sx);
+    d.y_st = draft && y ? row_stat(p, y0 + r, p.cy, sy) : make_float2(0.f, 0.f);
     if (d.y_st.x == -INFINITY) d.y_row = -1;   // a draft of nothing takes nothing off
     const float lp = log_p(lx, d.st, p.c), lq = y ? log_p(ly, d.y_st, p.cy) : 0.f;
-    if (known && lp == lp && lq == lq && lp != -INFINITY) a = lp >= lq ? 1.f : expf(lp - lq);
+    if (known && lp == lp && lq == lq && lp != -INFINITY) {
+      const float q = lq == -INFINITY ? 1.f
+                                      : ratio(scaled_difference(lx, d.st.x, p.c), sx,
+                                              y ? scaled_difference(ly, d.y_st.x, p.cy) : make_float2(0.f, 0.f), sy);
+      a = q >= 1.f ? 1.f : q;
+    }
     taken = u < a;
   }
   return __shfl_sync(0xffffffffu, taken, 0);

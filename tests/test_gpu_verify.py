@@ -387,3 +387,28 @@ def test_greedy_rows_with_a_nan(lib, dtype, many):
     assert got[0].tolist() == acc and got[1].tolist() == nxt and np.array_equal(got[3], ap)
     # the other V - 1 logits take less than V e^(5.5 - 40) of the mass
     assert np.allclose(got[2], logp, rtol=0, atol=1e-6, equal_nan=True)
+
+
+def test_acceptance_of_unlikely_drafts(lib):
+    """Ratios of probabilities far below the types' range: what is off is the two sums and one exponential, not the exponents.
+
+    Each sum: exponentials to 2^-22, exponents of at most 8 (those further down weigh less than 2^-24) times the rounded inverse
+    temperature and rounded once, 2 * 8 * 2^-24 ln 2, 64 terms in a tree of at most 9 roundings: 1.5e-6.  Two of them, the exponential
+    (2^-22), a quotient and two products: below 4e-6."""
+    V, n = 64, 400
+    rng = np.random.default_rng(19)
+    x, y = rng.standard_normal((2 * n, V)), rng.standard_normal((2 * n, V))
+    x[::2, 7] = -rng.uniform(20, 500, n)
+    y[::2, 7] = x[::2, 7] + rng.uniform(-0.5, 2.5, n)
+    xt, xr = on_gpu(x, "f32")
+    yt, yr = on_gpu(y, "f32")
+    nt, nr = on_gpu(rng.exponential(size=(n, V)).astype(np.float32), "f32")
+    ids = np.full(2 * n, 7, dtype=np.int32)
+    for c, cq in ((1.0, 1.0), (0.7, 0.7)):
+        c32, cq32 = float(np.float32(c)), float(np.float32(cq))
+        plan = chunk_plan(lib, [2] * n)
+        _, _, _, ap = run(plan, [2] * n, V, xt, ids, yt, np.ones(2 * n, dtype=np.float32), nt, c, cq)
+        plan.sync()
+        lp, lq = log_softmax(xr, c32)[0][::2, 7], log_softmax(yr, cq32)[0][::2, 7]
+        a = np.exp(np.minimum(lp - lq, 0))
+        assert (a < 1).mean() > 0.5 and np.all(np.abs(ap[1::2] - a) <= 4e-6 * a), np.abs(ap[1::2] / a - 1).max()
