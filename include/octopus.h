@@ -568,7 +568,7 @@ int octo_chunk_attn(octo_plan_t plan, const void* q, const void* k_pool, const v
  * Speculative sampling over a chunk plan's rows: of each cursor, the first row holds the token
  * agreed on last, the others (ids[r]) were drafted, row r from the draft's distribution
  * q_{r-1}.  With p_r = softmax(inv_temp x[r]), x the target's logits:
- *     a_r = min(1, p_{r-1}(ids r) / q_{r-1}(ids r)), 0 where p is 0;  accepted iff u[r] < a_r,
+ *     a_r = min(1, p_{r-1}(ids r) / q_{r-1}(ids r)), 0 where p is 0 (below e^-745);  accepted iff u[r] < a_r,
  * up to the first rejected draft.  The token after the last accepted one is drawn from
  *     max(0, p - q)   where a draft was rejected (p itself if that is 0 everywhere),
  *     p               where all were accepted,
@@ -577,7 +577,7 @@ int octo_chunk_attn(octo_plan_t plan, const void* q, const void* k_pool, const v
  * the target's own.  draft_logits NULL: the drafts are certain (q = 1 at the drafted token), the
  * rejected one is left out.  u and noise NULL: greedy, a draft is accepted iff it is the
  * largest logit's lowest id, which is the next token too (inv_temp then only enters next_logp;
- * draft_logits must be NULL).  Masked logits are -inf.  A NaN in a row that is needed,
+ * draft_logits must be NULL).  Masked logits are -inf or the type's lowest value.  A NaN in a row that is needed,
  * greedily too, makes its draft rejected, and no token is drawn from such a row of the target's.  So
  * does a +inf, but not greedily: there it is the largest logit (next_logp is then NaN). */
 

@@ -1,7 +1,7 @@
 """fp64 reference of the verification of drafted tokens -- TEST INFRASTRUCTURE ONLY.
 
 Row r of a cursor leads to the draft in row r + 1.  With p = softmax(c x_r), q = softmax(cq y_r):
-    a = min(1, p(id) / q(id)), 0 where p(id) is 0 (q = 1 without draft logits), accepted iff u < a;
+    a = min(1, p(id) / q(id)), 0 where p(id) is 0 in fp64 (q = 1 without draft logits), accepted iff u < a;
     next token after the first rejected one: argmax max(0, p - q) / noise (without draft logits p
     with the rejected id left out), p / noise where nothing is left or all were accepted; the lowest
     id among equal ones.
@@ -46,7 +46,7 @@ def verify(x, rows, ids, y=None, u=None, noise=None, c=1.0, cq=1.0):
                 a = float(_largest(x[r]) == t)
             else:
                 with np.errstate(invalid="ignore", over="ignore"):
-                    a = 0.0 if lp[r, t] == -np.inf else float(np.exp(min(0.0, lp[r, t] - (lq[r, t] if lq is not None else 0.0))))
+                    a = 0.0 if np.exp(lp[r, t]) == 0 else float(np.exp(min(0.0, lp[r, t] - (lq[r, t] if lq is not None else 0.0))))
                 if np.isnan(lp[r, t]) or (lq is not None and np.isnan(lq[r, t])):
                     a = 0.0
             accept[r + 1] = a

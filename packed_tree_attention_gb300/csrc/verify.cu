@@ -37,6 +37,9 @@ constexpr int kDecide = 256;          // threads of a cursor's decision
 constexpr int kSummers = kThreads - 32;   // of a CTA of k_verify_queue; its last warp is in control
 constexpr int kAhead = 2;             // units that such a CTA holds
 constexpr int kNone = 0x7fffffff;
+// Probabilities below e^-745 are 0, as they are in 64 bits: a draft that the target masks by its type's
+// lowest value is not taken because the draft's distribution masks it so too.
+constexpr float kLogZero = -745.f;
 
 // What is decided about a cursor: accepted drafts, the row (of the logits given) of the next
 // token's distribution with its statistics, and what a rejected draft takes off it: the draft's
@@ -359,8 +362,8 @@ __device__ __forceinline__ bool weigh(const VerifyParams& p, int r, int y0, bool
     d.y_st = draft && y ? row_stat(p, y0 + r, p.cy, sy) : make_float2(0.f, 0.f);
     if (d.y_st.x == -INFINITY) d.y_row = -1;   // a draft of nothing takes nothing off
     const float lp = log_p(lx, d.st, p.c), lq = y ? log_p(ly, d.y_st, p.cy) : 0.f;
-    if (known && lp == lp && lq == lq && lp != -INFINITY) {
-      const float q = lq == -INFINITY ? 1.f
+    if (known && lq == lq && lp >= kLogZero) {   // not where one is NaN
+      const float q = lq < kLogZero ? 1.f
                                       : ratio(scaled_difference(lx, d.st.x, p.c), sx,
                                               y ? scaled_difference(ly, d.y_st.x, p.cy) : make_float2(0.f, 0.f), sy);
       a = q >= 1.f ? 1.f : q;

@@ -412,3 +412,26 @@ def test_acceptance_of_unlikely_drafts(lib):
         lp, lq = log_softmax(xr, c32)[0][::2, 7], log_softmax(yr, cq32)[0][::2, 7]
         a = np.exp(np.minimum(lp - lq, 0))
         assert (a < 1).mean() > 0.5 and np.all(np.abs(ap[1::2] - a) <= 4e-6 * a), np.abs(ap[1::2] / a - 1).max()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_drafts_masked_by_the_lowest_value(lib, dtype):
+    """A drafted token that the target masks with its type's lowest value has no probability, whatever the draft's distribution has there
+    (the same value, -inf, a logit, or no distribution); one that only the draft masks so is taken."""
+    V = 40
+    low = float(torch.finfo(DT[dtype]).min)
+    rng = np.random.default_rng(20)
+    x, y = rng.standard_normal((8, V)), rng.standard_normal((8, V))
+    x[[0, 2, 4], 5] = low
+    y[0, 5], y[2, 5], y[6, 5] = low, -np.inf, low
+    ids = np.full(8, 5, dtype=np.int32)
+    xt, xr = on_gpu(x, dtype)
+    yt, yr = on_gpu(y, dtype)
+    nt, nr = on_gpu(rng.exponential(size=(4, V)).astype(np.float32), "f32")
+    for c in (1.0, 0.25, 2.0):
+        plan = chunk_plan(lib, [2] * 4)
+        acc, nxt, lp, ap = run(plan, [2] * 4, V, xt, ids, yt, np.zeros(8, dtype=np.float32), nt, c, c)
+        assert acc.tolist() == [0, 0, 0, 1] and ap[1::2].tolist() == [0, 0, 0, 1] and (nxt[:3] != 5).all()
+        acc, nxt, lp, ap = run(plan, [2] * 4, V, xt, ids, None, np.zeros(8, dtype=np.float32), nt, c, c)
+        assert acc.tolist() == [0, 0, 0, 1] and (ap[1:6] == 0).all() and ap[7] > 0 and (nxt[:3] != 5).all()
+        plan.sync()
