@@ -578,3 +578,43 @@ def test_lse_of_a_nan_row(lib, oracle_mod, dtype, d, lens, n):
         is_bad[n // 2, 1:3] = True
         assert torch.isnan(out[is_bad]).all() and torch.isnan(lse2[is_bad]).all()
         assert torch.equal(out[~is_bad], want[~is_bad]) and torch.equal(lse2[~is_bad], lse[~is_bad])
+
+
+@pytest.mark.parametrize("dtype,P,long", [("bf16", 64, False), ("bf16", 16, False), ("bf16", 64, True), ("f32", 64, False), ("f32", 16, False)])
+@pytest.mark.parametrize("window", [0, 300])
+def test_nan_keys_stay_with_who_sees_them(lib, oracle_mod, dtype, P, long, window):
+    """A NaN key among one cursor's own new tokens: its rows from there on are NaN, their lse too; the rows before it and the other
+    cursors', in shared tiles and two-slot ones as well, are what they were bit for bit."""
+    ep, leaves = forest(P)
+    cur = leaves[:8] + [leaves[0]]
+    Hkv = 8 if long else 2
+    if long:                                     # chunks of more than a tile beside them, work for every SM
+        for i in range(12):
+            r = ep.root()
+            ep.append(r, 600 + 30 * i)
+            cur.append(r)
+    case = Case(lib, oracle_mod, ep, 4, Hkv, 128, dtype)
+    n_new = [min(5, ep.length[c]) if c in leaves else ep.length[c] - 7 for c in cur]
+    q = case.queries(cur, n_new, 9)
+    plan = case.pool.chunk_plan(cur, n_new, 4 * Hkv, window=window)
+    if long and not window:
+        assert plan.info["bm"] == 64
+    want, lse = case.run(plan, q, 1 / math.sqrt(128))
+    row0 = np.concatenate([[0], np.cumsum(n_new)])
+    for victim in (2, len(cur) - 1):
+        c, n, L = cur[victim], n_new[victim], ep.length[cur[victim]]
+        t = L - n + n // 2                       # own index of the token with the NaN key
+        page = case.pool.seg_pages(c)[t // P]
+        before = case.kp[page, 1, t % P].clone()
+        case.kp[page, 1, t % P] = float("nan")
+        out, lse2 = case.run(plan, q, 1 / math.sqrt(128))
+        case.kp[page, 1, t % P] = before
+        bad = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+        for i, x in enumerate(cur):
+            if x == c:
+                first = L - n_new[i]
+                for k in range(n_new[i]):
+                    if first + k >= t and not (window and first + k >= t + window):
+                        bad[int(row0[i]) + k, 4:8] = True
+        assert bad.any() and torch.isnan(out[bad]).all() and torch.isnan(lse2[bad]).all()
+        assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse2[~bad], lse[~bad])

@@ -435,3 +435,140 @@ def test_drafts_masked_by_the_lowest_value(lib, dtype):
         acc, nxt, lp, ap = run(plan, [2] * 4, V, xt, ids, None, np.zeros(8, dtype=np.float32), nt, c, c)
         assert acc.tolist() == [0, 0, 0, 1] and (ap[1:6] == 0).all() and ap[7] > 0 and (nxt[:3] != 5).all()
         plan.sync()
+
+
+@pytest.mark.parametrize("dtype,V", [("f32", 24007), ("bf16", 48011)])
+@pytest.mark.parametrize("draft", [True, False])
+def test_many_cursors_with_broken_rows(lib, dtype, V, draft):
+    """Enough of a large vocabulary that rows behind a rejected draft are passed over: NaN in the target's rows and in the draft's, +inf,
+    rows without a token, ids out of range; a range of the plan's cursors gives what the whole gives."""
+    n_cur, n = 240 if draft else 470, 4
+    N = n_cur * n
+    rng = np.random.default_rng(21)
+    g = torch.Generator(device="cuda").manual_seed(22)
+
+    def rand():
+        t = torch.full((N, -(-V // 8) * 8), float("nan"), dtype=DT[dtype], device="cuda")
+        for r0 in range(0, N, 256):
+            t[r0:r0 + 256, :V] = (3 * torch.randn((min(256, N - r0), V), generator=g, device="cuda")).to(DT[dtype])
+        return t
+    x, y = rand(), rand() if draft else None
+    ids = np.zeros(N, dtype=np.int32)
+    best = x[:, :V].float().argmax(1).cpu().numpy()      # likely drafts, u = 0 below: taken
+    ids[1:] = best[:-1]
+    u = np.zeros(N, dtype=np.float32)
+    noise = torch.empty((n_cur, -(-V // 4) * 4), device="cuda").exponential_(generator=g)
+    acc, kinds = [], []
+    for i in range(n_cur):
+        j, kind = int(rng.integers(0, n - 1)), i % 8      # row r0 + j leads to a draft
+        r = i * n + j
+        if kind == 0:
+            u[r + 1] = 2                                  # rejected in the usual way
+        elif kind == 1:
+            x[r, int(rng.integers(0, V))] = float("nan")
+        elif kind == 2:
+            x[r, V - 1] = float("nan")
+        elif kind == 3:
+            x[r, int(rng.integers(0, V))] = float("inf")
+        elif kind == 4:
+            x[r, :V] = -float("inf")
+        elif kind == 5:
+            ids[r + 1] = V + i if i % 16 < 8 else -1 - i
+        elif kind == 6 and draft:
+            y[r, int(rng.integers(0, V))] = float("nan")
+        acc.append(j if kind < 6 or (kind == 6 and draft) else n - 1), kinds.append(kind)
+    plan = chunk_plan(lib, [n] * n_cur)
+    got = run(plan, [n] * n_cur, V, x, ids, y, u, noise)
+    with pytest.raises(lib.OctoError):
+        plan.sync()
+    assert got[0].tolist() == acc
+    ap = got[3].reshape(n_cur, n)
+    for i, (k, kind) in enumerate(zip(acc, kinds)):
+        assert (ap[i, 1:k + 1] > 0).all() and (ap[i, k + 2:] == 0).all() and (kind in (0, 7) or k == n - 1 or ap[i, k + 1] == 0)
+        if 1 <= kind <= 4:
+            assert got[1][i] == -1 and got[2][i] == -np.inf
+            continue
+        # the next token: p - q, p without the rejected draft, or p
+        r = i * n + k
+        lp = torch.log_softmax(x[r, :V].double(), 0)
+        p = lp.exp()
+        w, err = p, 1e-5 * p
+        if k < n - 1 and draft and kind != 6:
+            q = torch.softmax(y[r, :V].double(), 0)
+            w, err = (p - q).clamp_min(0), 1e-5 * (p + q)
+        elif k < n - 1 and not draft and kind != 5:
+            w = p.index_fill(0, torch.tensor([int(ids[r + 1])], device="cuda"), 0)
+        t = int(got[1][i])
+        lo, hi = (w - err) / noise[i, :V].double(), (w + err) / noise[i, :V].double()
+        assert hi[t] >= lo.max(), i
+        assert abs(got[2][i] - float(lp[t])) <= 1e-5 * (1 + abs(float(lp[t])))
+    part = run(plan, [n] * n_cur, V, x[3 * n:-2 * n], ids, None if y is None else y[3 * n:-2 * n], u, noise[3:-2], cur0=3, n_cur=n_cur - 5)
+    with pytest.raises(lib.OctoError):
+        plan.sync()
+    assert all(np.array_equal(a[3:-2], b) for a, b in zip(got[:3], part[:3]))
+    assert np.array_equal(got[3][3 * n:-2 * n], part[3][3 * n:-2 * n]) and (part[3][:3 * n] == -7).all() and (part[3][-2 * n:] == -7).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_nothing_left_of_the_target_over_several_ctas(lib, dtype, n):
+    """As above with a vocabulary that several CTAs draw from: whichever of them ends last draws from the target itself."""
+    V = 151936 if n < 40 else 20003
+    rng = np.random.default_rng(23)
+    x = rng.standard_normal((2 * n, V))
+    noise = rng.exponential(size=(n, V)).astype(np.float32)
+    ids = np.zeros(2 * n, dtype=np.int32)
+    ids[1::2] = V
+    xt, xr = on_gpu(x, dtype)
+    nt, nr = on_gpu(noise, "f32")
+    plan = chunk_plan(lib, [2] * n)
+    s = np.exp(log_softmax(xr, 1.0)[0])[::2] / nr
+    two = np.partition(s, V - 2, axis=1)[:, -2:]
+    sure = two[:, 0] < two[:, 1] * (1 - 2e-5)
+    assert sure.mean() > 0.9
+    want = np.argmax(s, axis=1)
+    for _ in range(5):
+        acc, nxt, lp, ap = run(plan, [2] * n, V, xt, ids, xt.clone(), np.zeros(2 * n, dtype=np.float32), nt)
+        with pytest.raises(lib.OctoError):
+            plan.sync()
+        assert acc.tolist() == [0] * n and (ap == 0).all()
+        same = np.abs(s[np.arange(n), nxt] - two[:, 1]) <= 2e-5 * two[:, 1]
+        assert np.array_equal(nxt[sure], want[sure]) and same.all()
+
+
+@pytest.mark.parametrize("n_cur,V,draft", [(3, 50001, True), (240, 24007, True), (470, 24007, None)])
+def test_two_verifications_at_once(lib, n_cur, V, draft):
+    """One plan, calls under way on two streams with logits, draws and workspaces of their own; greedily (draft None) too."""
+    n = 4
+    plan = chunk_plan(lib, [n] * n_cur)
+    g = torch.Generator(device="cuda").manual_seed(24)
+    ld = -(-V // 4) * 4
+    rnd = lambda rows: torch.randn((rows, ld), generator=g, device="cuda")
+    i32 = lambda k: torch.zeros(k, dtype=torch.int32, device="cuda")
+    sets, size = [], plan.verify_drafts_workspace_size(0, n_cur)
+    for _ in range(2):
+        x = rnd(n * n_cur)
+        kw = {}
+        if draft:
+            kw = dict(draft_logits=x + rnd(n * n_cur), u=torch.rand(n * n_cur, generator=g, device="cuda"),
+                      noise=torch.empty((n_cur, ld), device="cuda").exponential_(generator=g))
+        ids = i32(n * n_cur)
+        ids[1:] = x[:-1, :V].argmax(1).int()
+        ids[n // 2::n] = 1
+        out = (i32(n_cur), i32(n_cur), torch.zeros(n * n_cur, device="cuda"), torch.zeros(n_cur, device="cuda"))
+        sets.append((x, ids, kw, out, torch.full((size,), 255, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()))
+    call = lambda s, o, ws, st: plan.verify_drafts(0, n_cur, s[0], V, s[1], o[0], o[1], ws, accept_p=o[2], next_logp=o[3], stream=st, **s[2])
+    want = []
+    for s in sets:
+        o = tuple(t.clone() for t in s[3])
+        call(s, o, torch.empty(size, dtype=torch.uint8, device="cuda"), None)
+        want.append(o)
+    plan.sync()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s in sets:
+            call(s, s[3], s[4], s[5])
+    torch.cuda.synchronize()
+    for s, o in zip(sets, want):
+        assert all(torch.equal(a, b) for a, b in zip(s[3], o))
+    plan.sync()
