@@ -277,7 +277,7 @@ int octo_append_rope(octo_pool_t pool, octo_cursor_t cur, int32_t n, const void*
 
 /* Rotates in place x [n_rows][n_heads][head_dim] (dtype OCTO_DTYPE_BF16 or
  * OCTO_DTYPE_F32, device) in the plan's packed row order, each row at its position: a
- * pack plan's rows, or a decode plan's one row per cursor (its newest token).  inverse = 0
+ * pack plan's or a chunk plan's rows, or a decode plan's one row per cursor (its newest token).  inverse = 0
  * before attention (queries); inverse = 1 turns back, mapping the gradient with respect
  * to the rotated rows (octo_attn_bwd's dq) to the gradient with respect to the rows as
  * given.  Async on stream. */
@@ -333,7 +333,7 @@ int octo_token_logprob(octo_plan_t plan, int32_t row0, int32_t n_rows, const voi
  * logits, dtype, ld and vocab as in octo_token_logprob (columns past vocab are neither read
  * nor written).  Tokens t of row r:
  * on a pack plan the rows that continue r (pred t = r above); on a decode plan the token
- * that cursor r takes next, t = r.  ids, logp, g_logp: device arrays over ALL rows of the
+ * that cursor r takes next, t = r, and so on a chunk plan the token that follows row r.  ids, logp, g_logp: device arrays over ALL rows of the
  * plan; row_stat, entropy, g_entropy, top_ids, top_logp start at row row0.
  * With c = inv_temp (> 0, finite: 1 / temperature), m = max_v x[r][v]:
  *     S = sum_v exp(c (x[r][v] - m)),   row_stat[r] = (m, ln S),
@@ -389,7 +389,7 @@ int octo_token_score_bwd(octo_plan_t plan, int32_t row0, int32_t n_rows, const v
 /* Workspace (bytes) for octo_distill_topk's loss over n_rows rows. */
 int octo_distill_topk_workspace_size(int32_t n_rows, size_t* bytes);
 
-/* Rows [row0, row0 + n_rows) of a pack or decode plan; logits, dtype, ld, vocab as in
+/* Rows [row0, row0 + n_rows) of a pack, decode or chunk plan; logits, dtype, ld, vocab as in
  * octo_token_logprob.  1 <= k <= 128 (k may exceed vocab).  weight (NULL: ones) and row_kl:
  * device floats over ALL rows of the plan; row_kl[r] is written without the weight.
  * dlogits (optional): dtype, layout and alignment of logits; may be logits itself.  loss
@@ -545,9 +545,13 @@ int octo_decode_noalloc(octo_plan_t plan, int32_t n_q_heads, const void* q, cons
  * appends do not change it, a release of its segments ends it.  For chunk plans
  * octo_plan_info counts cursors as n_segments, has no entries (max_tile_entries is the most
  * blocks of up to 64 keys that a tile reads) and a tile's most tokens as bm; octo_plan_copy_out gives
- * the cursors, their first rows, positions and tiles.  octo_rope_rows, octo_token_score and
- * octo_distill_topk take them (row t leads to the token that follows it, as on a decode plan), the
- * other calls on plans refuse them.  Synchronises `stream` once. */
+ * the cursors, their first rows, positions and tiles.  octo_rope_rows, octo_token_score with its
+ * gradient and octo_distill_topk take them (row t leads to the token that follows it, as on a decode
+ * plan), the other calls that compute on plans refuse them.  Synchronises `stream` once.
+ * The order of the cursors changes no result but costs: without a window, a prefix that cursors
+ * share is read once for all of them only where they are listed next to each other and their new
+ * tokens fit a tile together (128 rows of tokens times query heads a kv head, 256 beside long
+ * chunks).  So list siblings side by side. */
 int octo_chunk_plan(octo_pool_t pool, const octo_cursor_t* cursors, const int32_t* n_new, int32_t n,
                     int32_t n_q_heads, int32_t window, int32_t n_sink, void* stream, octo_plan_t* out);
 
@@ -557,8 +561,9 @@ size_t octo_chunk_attn_workspace_size(octo_plan_t plan);
 /* Attention of a chunk plan's rows: out = softmax(scale q k^T) v over what each row sees; kv
  * head of query head h as in octo_attn_fwd.  q, out: [n_rows][n_q_heads][head_dim] of the pool
  * dtype; lse: fp32 [n_rows][n_q_heads], natural log (may be NULL).  k_pool / v_pool NULL = the
- * pool's arrays; every array 16-byte aligned; their slots that no row sees must hold finite
- * values, as for octo_attn_fwd.  scale: finite, 1e-30 at least.  ws: device workspace of the size
+ * pool's arrays; every array 16-byte aligned; the slots of V that some row does not see, in
+ * the pages that it reads, must hold finite values, as for octo_attn_fwd.  A row with NaN scores is
+ * NaN, its lse too, and no other row.  scale: finite, 1e-30 at least.  ws: device workspace of the size
  * above, for one call at a time.  Long contexts of few rows are split among CTAs and joined in a
  * fixed order: the same bits on every run.  Async on stream. */
 int octo_chunk_attn(octo_plan_t plan, const void* q, const void* k_pool, const void* v_pool, void* out,

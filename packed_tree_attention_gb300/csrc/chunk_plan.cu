@@ -140,7 +140,11 @@ template <typename F>
 Sharing(const octo_pool_s*, std::vector<Path>&, F) -> Sharing<F>;
 
 // Shared blocks that are worth tiles of their own: with fewer, the items and the partial results
-// that these cost take longer than reading the blocks again (from L2 mostly).
+// that these cost take longer than reading the blocks again (from L2 mostly).  At 4, 8 and 16, us, five
+// new tokens of each cursor: one tree of six cursors behind 256 shared tokens 10.3, 7.1 and 7.1, 384:
+// 11.9, 8.6 and 8.6, 512: 12.9, 13.5 and 10.1, 768: 10.0, 10.0 and 11.0; eight such trees, 256: 12.6, 16.1
+// and 16.1, 512: 15.1, 15.1 and 18.7, 768: 15.6, 15.6 and 22.8; 32 with 700 tokens of their own, 256: 94,
+// 78 and 78, 768: 90, 89 and 107.
 constexpr int32_t kShareBlocks = 8;
 
 // Visible (row, key) pairs of a tile's block.

@@ -8,11 +8,13 @@
 // fp32.  Thread (ty, tx) of 16 x 16 holds rows ty + 16 i and keys tx + 16 j of the scores (RM x
 // 4 of them, each as a pair of sums over even and odd places), then columns 4 tx + 64 c .. + 3 of
 // O, two fp32 operations an instruction: 4 RM and RM D / 16 accumulators against RM + 4 and RM / 4
-// + D / 64 vector loads for each four steps of the inner product, so that from RM = 4 on the FMAs
-// and not shared memory bound it.  fp32 pools are copied with cp.async, the next K while P V runs
-// and the next V while S does.  Everything is fp32.  (200 new tokens of two cursors behind 4,096,
-// 16 query heads: 500 us at d 128, 28 TFLOP/s, a third of the FMA peak; single tokens behind
-// 14,000 are bound by shared memory, 154 us at 1.2 TB/s.)
+// + D / 64 vector loads for each four steps of the inner product.  fp32 pools are copied with
+// cp.async, the next K while P V runs and the next V while S does.  Everything is fp32.
+// Bound by latency: at d 128 an SM holds one CTA from RM = 4 on, two warps a scheduler, which wait for
+// shared memory and for the instruction before.  200 new tokens of two cursors behind 4,096, 16 query
+// heads: 493 us, 28 TFLOP/s; the FMA pipe is busy 47% of the time, shared memory 60%, an
+// instruction is issued in 40% of the cycles, barriers are 3% of the warps' waiting.  Single tokens
+// behind 14,000: 154 us, 1.2 TB/s.
 
 #include <cuda_bf16.h>
 

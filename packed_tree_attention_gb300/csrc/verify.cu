@@ -12,7 +12,7 @@
 //   k_verify_decide  greedy: a CTA a cursor, the first rejected draft and the next token
 //   k_verify_draw    sampled: the first rejected draft, then the race over one row (pair) of each
 //                    cursor
-// 256 cursors of five rows of 151,936 bf16 logits and four drafts' distributions (700 MB), 1.6
+// 256 cursors of five rows of 151,936 bf16 logits and four drafts' distributions (700 MB), 1.3
 // drafts accepted on average: 136 us, of which the draw some 50; with k_verify_stats (106 us, 6.5
 // TB/s) 161.  One cursor: 12.0, most of it the host's (the decision as a kernel of its own: 14.5).
 // The sums are fp32 of fp32 exponentials; a decision turns where they are off by some 1e-7 of a
@@ -784,7 +784,7 @@ struct Layout {   // of the workspace
 // The queue takes rows of four chunks at least (its units are half a row), cursors enough that a
 // row's units come three units' times after those of the row before, drafts enough, and cursors of
 // alike many rows, for the longest one's count of each is handed out.  256 cursors of five rows,
-// 0.5, 1.4 and 4 of four drafts accepted: 126, 137 and 163 us, else 161, 161 and 152; 512 cursors
+// 0.5, 1.3 and 4 of four drafts accepted: 126, 137 and 163 us, else 161, 161 and 152; 512 cursors
 // 207, 229 and 306, else 309, 307 and 289; 512 greedily, without drafts' distributions, 1.8 and 4
 // accepted: 99 and 142, else 144.  256 cursors of three rows, 0.4, 1 and 2 of two accepted: 112, 112
 // and 115, else 115, 113 and 107, so four rows at least.  (Units of a quarter: 256 cursors of five
