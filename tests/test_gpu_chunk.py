@@ -618,3 +618,36 @@ def test_nan_keys_stay_with_who_sees_them(lib, oracle_mod, dtype, P, long, windo
                         bad[int(row0[i]) + k, 4:8] = True
         assert bad.any() and torch.isnan(out[bad]).all() and torch.isnan(lse2[bad]).all()
         assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse2[~bad], lse[~bad])
+
+
+def test_training_calls_on_a_chunk(lib):
+    """The gradient of the scores and a distillation over a chunk plan's rows, against autograd in 64 bits: terms of size at most 1 with a
+    dozen fp32 roundings of exponents of at most 20, 1e-5 (1 + |ref|)."""
+    pool = lib.Pool(16, 16, 1, 64, lib.DTYPE_BF16)
+    a, b = pool.root(), pool.root()
+    pool.append(a, 30), pool.append(b, 9)
+    plan = pool.chunk_plan([a, b], [7, 4], 1)
+    V, N, k = 500, 11, 8
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = 2 * torch.randn((N, 504), generator=g, device="cuda")
+    ids = (torch.arange(N, device="cuda") * 37 % V).int()
+    stat, logp, H = torch.empty((N, 2), device="cuda"), torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+    gl, gH = (torch.rand(N, generator=g, device="cuda") for _ in range(2))
+    dx = torch.empty_like(x)
+    plan.token_score(0, N, x, V, stat, entropy=H, ids=ids, logp=logp, inv_temp=0.8)
+    plan.token_score_bwd(0, N, x, V, stat, H, ids, gl, gH, dx, inv_temp=0.8)
+    plan.sync()
+    z = x[:, :V].double().requires_grad_()
+    lp = torch.log_softmax(0.8 * z, 1)
+    ref = (gl * lp[torch.arange(N), ids.long()] - gH * (lp.exp() * lp).sum(1)).sum()
+    want, = torch.autograd.grad(ref, z)
+    assert torch.all((dx[:, :V].double() - want).abs() <= 1e-5 * (1 + want.abs()))
+    val, top = (2 * torch.randn((N, V), generator=g, device="cuda")).topk(k)
+    w = torch.rand(N, generator=g, device="cuda")
+    kl, dx2 = torch.empty(N, device="cuda"), torch.empty_like(x)
+    plan.distill_topk(0, N, x, V, top.int().contiguous(), val.contiguous(), weight=w, row_kl=kl, dlogits=dx2)
+    plan.sync()
+    lq, P = torch.log_softmax(z, 1).gather(1, top), torch.softmax(val.double(), 1)
+    d = (P * (P.log() - lq)).sum(1)
+    want, = torch.autograd.grad((w * d).sum(), z)
+    assert torch.all((kl.double() - d).abs() <= 1e-5 * (1 + d.abs())) and torch.all((dx2[:, :V].double() - want).abs() <= 1e-5 * (1 + want.abs()))
